@@ -305,6 +305,122 @@ int mamba2_layer_decode_noalloc(const m2_dims* dims, const m2_layer* layer, uint
  * launch. */
 int m2_copy(void* dst, const void* src, size_t bytes, cudaStream_t stream);
 
+/* ------------------------------------------------ attention of hybrid stacks
+ *
+ * The operators of the attention layers that stand between the Mamba-2 layers
+ * of a hybrid stack.  Projections are w8a16_gemv / w8a8_gemm; between them:
+ *   m2_qk_norm_rope         RMS norm of the query and key heads and rotation
+ *   m2_kv4_append           new K/V rows into the paged 4-bit cache
+ *   m2_kv4_gather           cached rows back as bf16 (for a chunked prompt)
+ *   m2_attn_prefill_varlen  causal attention of a varlen batch of prompts
+ *   m2_attn_decode_kv4      one query token a sequence over the 4-bit cache
+ * head_dim is 64 or 128; H query heads share Hkv kv heads (H % Hkv == 0, query
+ * head h reads kv head h / (H / Hkv)).  Row pointers are 16-byte aligned and
+ * row strides (ld_*, in elements) multiples of 8 and at least the row's width,
+ * so that q, k and v may be column ranges of one projection's output rows.  A
+ * call without rows launches nothing and succeeds (their pointers may be NULL). */
+
+/* RMS norm of every query and key head and the rotation by position, in one
+ * pass over T rows: for each head x of a row
+ *   y = x * w / sqrt(mean(x^2) + eps)                   (w NULL: y = x)
+ *   pairs (a, b) of the first rot_dim channels of y at position p:
+ *     (a cos - b sin, b cos + a sin), angle = 2 pi * frac(p * rope_step[i] / 2^64)
+ * evaluated in fp32 and rounded to bf16 once.  Pair i is channels (i, i +
+ * rot_dim/2), or (2i, 2i+1) if interleaved != 0.
+ *   q [T][H*head_dim], k [T][Hkv*head_dim] bf16, ld_q / ld_k apart; q_out and
+ *   k_out the same shapes; the output may be the input itself (same pointer
+ *   and stride).
+ *   q_w, k_w    [head_dim] bf16 norm weights, or NULL.
+ *   pos         [T] int32 positions (device).
+ *   rope_step   [rot_dim/2] uint64 (device): turns a position, in units of
+ *               2^-64, so that a far position loses no accuracy
+ *               (m2_rope_steps).  rot_dim 0: no rotation (rope_step, pos NULL).
+ *   rot_dim     0, or a multiple of 16 up to head_dim. */
+int m2_qk_norm_rope(const uint16_t* q, int32_t ld_q, const uint16_t* k, int32_t ld_k, uint16_t* q_out, int32_t ld_qo,
+                    uint16_t* k_out, int32_t ld_ko, const uint16_t* q_w, const uint16_t* k_w, const int32_t* pos,
+                    const uint64_t* rope_step, int32_t T, int32_t H, int32_t Hkv, int32_t head_dim, int32_t rot_dim,
+                    int32_t interleaved, float eps, cudaStream_t stream);
+
+/* Host helper: steps[i] = 2^64 * theta^(-2i/rot_dim) / (2 pi) for i <
+ * rot_dim/2, into HOST memory (upload it once).  theta >= 1. */
+int m2_rope_steps(double theta, int32_t rot_dim, uint64_t* steps);
+
+/* The paged 4-bit cache of one attention layer.  A page holds 64 tokens of
+ * every kv head: n_kv_heads blocks of 72 * head_dim bytes, each (D = head_dim)
+ *   K codes  [64 tokens][c < 4][g < D/16][h < 2] bytes: low nibble channel
+ *            16g + 4c + 2h, high nibble the next channel
+ *   V codes  [8 blocks of 8 tokens][r < 8][c < 4][i < D/8] bytes: low nibble
+ *            channel 8i + r of the block's token 2c, high nibble of token 2c+1
+ *   K scales [64 tokens][g < D/16] bytes
+ *   V scales [32 token pairs][g/2][token of the pair][g%2] bytes
+ * (the orders in which the decode kernel's matrix operands want them).
+ * A group of 16 channels of one token shares a scale s: 5 exponent bits (bias
+ * 15) and 3 mantissa bits, no sign; s = max|x| / 6 rounded to nearest even, at
+ * most 10240.  A code is the E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ * sign) nearest to x / s, ties to even, saturated.  So magnitudes up to 61440
+ * are held (larger ones and infinities saturate), groups below about 2^-16
+ * become zero, and a NaN makes its group NaN.  4.5 bits a value. */
+#define M2_KV4_PAGE 64
+typedef struct m2_kv4_cache {
+  void* pages;                 /* [n_pages][n_kv_heads][72 * head_dim] bytes, 16-byte aligned        */
+  int32_t n_pages;
+  int32_t n_kv_heads, head_dim;
+  const int32_t* block_table;  /* device [nseq][ld_table]: page of tokens 64j .. 64j+63 of a sequence */
+  int32_t nseq, ld_table;
+} m2_kv4_cache;
+/* Bytes of one page; 0 for an unsupported head_dim. */
+size_t m2_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim);
+
+/* Quantizes new rows into the cache.  Rows cu_rows[i] .. cu_rows[i+1]-1 of k
+ * and v ([T][Hkv*head_dim] bf16) are tokens kv_pos[i], kv_pos[i]+1, ... of
+ * sequence i.
+ *   cu_rows  HOST array of nseq + 1 offsets, cu_rows[0] = 0, non-decreasing.
+ *   kv_pos   device [nseq] int32: tokens each sequence holds before the call.
+ *            Not advanced: every layer of a stack can share one array.
+ * Rows of a sequence must be appended in order; a page belongs to one
+ * sequence.  A row whose page index lies outside [0, n_pages), or whose
+ * position is negative or past the block table, is not stored, and
+ * m2_device_status reports M2_ERR_ARG. */
+int m2_kv4_append(const m2_kv4_cache* cache, const uint16_t* k, int32_t ld_k, const uint16_t* v, int32_t ld_v,
+                  const int32_t* cu_rows, const int32_t* kv_pos, cudaStream_t stream);
+
+/* Reads the first cu_rows[i+1] - cu_rows[i] tokens of every sequence back into
+ * rows cu_rows[i] .. of k and v (bf16; the conversion is exact).  Rows of pages
+ * outside the pool are left as they are and reported as above. */
+int m2_kv4_gather(const m2_kv4_cache* cache, uint16_t* k, int32_t ld_k, uint16_t* v, int32_t ld_v,
+                  const int32_t* cu_rows, cudaStream_t stream);
+
+/* Causal attention of nseq packed sequences.  Sequence i owns query rows cu_q[i]
+ * .. cu_q[i+1]-1 and key/value rows cu_k[i] .. cu_k[i+1]-1; its queries are the
+ * LAST tokens of its keys: with nq queries and nk keys, query j sees keys 0 ..
+ * j + nk - nq (the whole prompt when nq = nk, a chunk after cached tokens when
+ * nq < nk).  A query that sees no key (nq > nk) gives a row of zeros.
+ *   out[j] = sum_t softmax_t(scale * q[j] . k[t]) v[t]
+ * per head; scores and sums in fp32, probabilities rounded to bf16 for the
+ * second product.  Keys and values that a query does not see do not reach it,
+ * whatever they hold (NaN and infinities included).
+ *   cu_q, cu_k  HOST arrays of nseq + 1 offsets, read during the call only.
+ *   out         [T][H*head_dim] bf16; not the input. */
+int m2_attn_prefill_varlen(const uint16_t* q, int32_t ld_q, const uint16_t* k, int32_t ld_k, const uint16_t* v,
+                           int32_t ld_v, uint16_t* out, int32_t ld_o, int32_t H, int32_t Hkv, int32_t head_dim,
+                           int32_t nseq, const int32_t* cu_q, const int32_t* cu_k, float scale, cudaStream_t stream);
+
+/* Attention of one query token a sequence over the cache: q and out
+ * [cache->nseq][H*head_dim] bf16.
+ *   kv_len  device [nseq] int32: tokens each sequence sees (its own, appended
+ *           before the call, included).  A length of 0 gives a row of zeros;
+ *           one past the block table is cut to it and reported by
+ *           m2_device_status as M2_ERR_ARG, as is a page outside the pool,
+ *           whose tokens are left out.
+ *   ws      m2_attn_decode_kv4_workspace_bytes(nseq, H, Hkv, head_dim) bytes,
+ *           256-byte aligned, scratch.
+ * The cache is read once for all H / Hkv query heads of a kv head (up to 16 of
+ * them at a time).  Nothing depends on host copies of the lengths: a captured
+ * step can be replayed while kv_len grows. */
+size_t m2_attn_decode_kv4_workspace_bytes(int32_t nseq, int32_t H, int32_t Hkv, int32_t head_dim);
+int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q, uint16_t* out, int32_t ld_o,
+                       int32_t H, const int32_t* kv_len, float scale, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------ diagnostics */
 
 /* Where a call keeps its intermediate values in the workspace, for reading
@@ -334,8 +450,9 @@ enum { M2_WS_XN = 0, M2_WS_ZX, M2_WS_U, M2_WS_Y, M2_WS_G, M2_WS_Q8, M2_WS_SQ, M2
 int m2_workspace_map(const m2_dims* dims, int32_t kind, int32_t n, const int32_t* cu_seqlens, size_t* offsets,
                      int32_t n_offsets);
 
-/* Device status word: M2_OK, or the first M2_ERR_TIMEOUT a kernel recorded on
- * the current device.  Synchronises the device.  clear != 0 resets it. */
+/* Device status word: M2_OK, or the first failure a kernel recorded on the
+ * current device (M2_ERR_TIMEOUT; M2_ERR_ARG for a page index or length that the
+ * 4-bit cache's kernels left out).  Synchronises the device.  clear != 0 resets it. */
 int m2_device_status(int clear);
 
 /* Limit of the library's in-kernel pipeline waits on the current device, in

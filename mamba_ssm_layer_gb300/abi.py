@@ -37,7 +37,9 @@ EXPORTS = ("m2_strerror", "m2_validate", "m2_workspace_bytes", "mamba2_layer_dec
            "mamba2_layer_prefill_varlen_w8a8", "w8a8_gemm", "m2_w8a8_workspace_bytes",
            "w8a16_gemv", "conv1d_update", "mamba2_ssm_step", "m2_device_status", "m2_launch_count",
            "m2_trace_begin", "m2_trace_end", "m2_kernel_name", "m2_kernel_count", "m2_set_fused_decode", "m2_copy",
-           "m2_set_wait_limit", "m2_wait_check", "m2_workspace_map")
+           "m2_set_wait_limit", "m2_wait_check", "m2_workspace_map",
+           "m2_qk_norm_rope", "m2_rope_steps", "m2_kv4_page_bytes", "m2_kv4_append", "m2_kv4_gather",
+           "m2_attn_prefill_varlen", "m2_attn_decode_kv4_workspace_bytes", "m2_attn_decode_kv4")
 
 
 class M2Dims(C.Structure):
@@ -54,6 +56,11 @@ class M2Layer(C.Structure):
     _fields_ = [("norm_w", C.c_void_p), ("in_proj", M2Weight), ("conv_w", C.c_void_p), ("conv_b", C.c_void_p),
                 ("A_log", C.c_void_p), ("D", C.c_void_p), ("dt_bias", C.c_void_p), ("gnorm_w", C.c_void_p),
                 ("out_proj", M2Weight)]
+
+
+class M2Kv4Cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("n_pages", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("block_table", C.c_void_p), ("nseq", C.c_int32), ("ld_table", C.c_int32)]
 
 
 class M2Error(RuntimeError):
@@ -118,6 +125,19 @@ def lib():
             l.m2_wait_check.argtypes = [P, P, P]; l.m2_wait_check.restype = C.c_int
             l.m2_workspace_map.argtypes = [C.POINTER(M2Dims), I32, I32, C.POINTER(C.c_int32), C.POINTER(SZ), I32]
             l.m2_workspace_map.restype = C.c_int
+            F, CACHE, CU = C.c_float, C.POINTER(M2Kv4Cache), C.POINTER(I32)
+            l.m2_qk_norm_rope.argtypes = [P, I32, P, I32, P, I32, P, I32, P, P, P, P, I32, I32, I32, I32, I32, I32, F, P]
+            l.m2_qk_norm_rope.restype = C.c_int
+            l.m2_rope_steps.argtypes = [C.c_double, I32, C.POINTER(C.c_uint64)]; l.m2_rope_steps.restype = C.c_int
+            l.m2_kv4_page_bytes.argtypes = [I32, I32]; l.m2_kv4_page_bytes.restype = SZ
+            l.m2_kv4_append.argtypes = [CACHE, P, I32, P, I32, CU, P, P]; l.m2_kv4_append.restype = C.c_int
+            l.m2_kv4_gather.argtypes = [CACHE, P, I32, P, I32, CU, P]; l.m2_kv4_gather.restype = C.c_int
+            l.m2_attn_prefill_varlen.argtypes = [P, I32, P, I32, P, I32, P, I32, I32, I32, I32, I32, CU, CU, F, P]
+            l.m2_attn_prefill_varlen.restype = C.c_int
+            l.m2_attn_decode_kv4_workspace_bytes.argtypes = [I32, I32, I32, I32]
+            l.m2_attn_decode_kv4_workspace_bytes.restype = SZ
+            l.m2_attn_decode_kv4.argtypes = [CACHE, P, I32, P, I32, I32, P, F, P, SZ, P]
+            l.m2_attn_decode_kv4.restype = C.c_int
             _lib = l
     return _lib
 
@@ -262,6 +282,78 @@ def m2_copy(dst, src, nbytes: int, stream=None, check=True) -> int:
     """Kernel copy between device tensors and/or pinned host tensors (stays in the PDL launch chain)."""
     st = lib().m2_copy(_ptr(dst), _ptr(src), nbytes, _stream(stream))
     return _check("m2_copy", st) if check else st
+
+
+# ------------------------------------------------------------------ attention of hybrid stacks
+
+M2_KV4_PAGE = 64
+
+
+def _offsets(cu):
+    return (C.c_int32 * len(cu))(*map(int, cu))
+
+
+def kv4_cache(pages, n_pages: int, n_kv_heads: int, head_dim: int, block_table, nseq: int, ld_table: int) -> M2Kv4Cache:
+    """The 4-bit cache of one layer: a pool of pages and the sequences' page table (both on the device)."""
+    return M2Kv4Cache(_ptr(pages), n_pages, n_kv_heads, head_dim, _ptr(block_table), nseq, ld_table)
+
+
+def m2_kv4_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    return lib().m2_kv4_page_bytes(n_kv_heads, head_dim)
+
+
+def m2_rope_steps(theta: float, rot_dim: int) -> list:
+    """Turns a position of each channel pair, in units of 2^-64 (upload as 64-bit integers)."""
+    out = (C.c_uint64 * max(rot_dim // 2, 1))()
+    _check("m2_rope_steps", lib().m2_rope_steps(theta, rot_dim, out))
+    return list(out)
+
+
+def m2_qk_norm_rope(q, ld_q, k, ld_k, q_out, ld_qo, k_out, ld_ko, q_w, k_w, pos, rope_step, T, H, Hkv, head_dim,
+                    rot_dim, interleaved, eps, stream=None, check=True) -> int:
+    st = lib().m2_qk_norm_rope(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(q_out), ld_qo, _ptr(k_out), ld_ko, _ptr(q_w),
+                               _ptr(k_w), _ptr(pos), _ptr(rope_step), T, H, Hkv, head_dim, rot_dim,
+                               1 if interleaved else 0, eps, _stream(stream))
+    return _check("m2_qk_norm_rope", st) if check else st
+
+
+def m2_kv4_append(cache, k, ld_k, v, ld_v, cu_rows, kv_pos, stream=None, check=True) -> int:
+    """cu_rows: host sequence of nseq + 1 row offsets; kv_pos: device int32, tokens held before the call."""
+    _need_offsets("m2_kv4_append", cu_rows, cache.nseq)
+    st = lib().m2_kv4_append(C.byref(cache), _ptr(k), ld_k, _ptr(v), ld_v, _offsets(cu_rows), _ptr(kv_pos),
+                             _stream(stream))
+    return _check("m2_kv4_append", st) if check else st
+
+
+def m2_kv4_gather(cache, k, ld_k, v, ld_v, cu_rows, stream=None, check=True) -> int:
+    """cu_rows: host sequence of nseq + 1 row offsets of the output."""
+    _need_offsets("m2_kv4_gather", cu_rows, cache.nseq)
+    st = lib().m2_kv4_gather(C.byref(cache), _ptr(k), ld_k, _ptr(v), ld_v, _offsets(cu_rows), _stream(stream))
+    return _check("m2_kv4_gather", st) if check else st
+
+
+def _need_offsets(fn: str, cu, nseq: int) -> None:
+    if len(cu) != nseq + 1:  # the C side reads nseq + 1 entries
+        raise M2Error(fn, M2_ERR_ARG)
+
+
+def m2_attn_prefill_varlen(q, ld_q, k, ld_k, v, ld_v, out, ld_o, H, Hkv, head_dim, cu_q, cu_k, scale, stream=None,
+                           check=True) -> int:
+    """cu_q, cu_k: host sequences of nseq + 1 row offsets."""
+    _need_offsets("m2_attn_prefill_varlen", cu_k, len(cu_q) - 1)
+    st = lib().m2_attn_prefill_varlen(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(out), ld_o, H, Hkv, head_dim,
+                                      len(cu_q) - 1, _offsets(cu_q), _offsets(cu_k), scale, _stream(stream))
+    return _check("m2_attn_prefill_varlen", st) if check else st
+
+
+def m2_attn_decode_kv4_workspace_bytes(nseq: int, H: int, Hkv: int, head_dim: int) -> int:
+    return lib().m2_attn_decode_kv4_workspace_bytes(nseq, H, Hkv, head_dim)
+
+
+def m2_attn_decode_kv4(cache, q, ld_q, out, ld_o, H, kv_len, scale, ws, ws_bytes, stream=None, check=True) -> int:
+    st = lib().m2_attn_decode_kv4(C.byref(cache), _ptr(q), ld_q, _ptr(out), ld_o, H, _ptr(kv_len), scale, _ptr(ws),
+                                  ws_bytes, _stream(stream))
+    return _check("m2_attn_decode_kv4", st) if check else st
 
 
 def m2_device_status(clear: bool = False) -> int:

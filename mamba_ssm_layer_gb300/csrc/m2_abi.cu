@@ -78,7 +78,8 @@ static const char* kNames[K_COUNT] = {
     "gemv_bf16",     "gemv_bf16_inproj_conv", "gemv_bf16_outproj_resid", "conv_update",
     "conv_pos",      "ssm_step",        "conv_prefill",    "ssm_scan_seq",
     "gemm_tc",       "ssd_chunk_state", "ssd_state_pass",  "ssd_chunk_out",   "gemm_tc_reduce",
-    "conv_ring_store", "decode_step_fused", "copy", "wait_check"};
+    "conv_ring_store", "decode_step_fused", "copy", "wait_check", "qk_norm_rope", "kv4_append", "kv4_gather",
+    "attn_prefill",  "attn_decode_kv4", "attn_decode_combine"};
 
 // ------------------------------------------------------------------ helpers
 
@@ -893,7 +894,8 @@ int mamba2_layer_decode_noalloc(const m2_dims* dims, const m2_layer* layer, uint
 
 int m2_device_status(int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return M2_ERR_LAUNCH;
-  const int parts[] = {status_gemv(clear), status_gemv_mma(clear), status_gemm_tc(clear), status_mixer(clear)};
+  const int parts[] = {status_gemv(clear), status_gemv_mma(clear), status_gemm_tc(clear), status_mixer(clear),
+                       status_kv4(clear), status_attn(clear), status_attn_decode(clear)};
   for (int v : parts)
     if (v != 0) return v;
   return M2_OK;
@@ -937,7 +939,8 @@ int m2_workspace_map(const m2_dims* dims, int32_t kind, int32_t n, const int32_t
 int m2_set_wait_limit(int64_t cycles) {
   const long long v = cycles > 0 ? (long long)cycles : 4000000000LL;
   if (wait_limit_gemv(v) != cudaSuccess || wait_limit_gemv_mma(v) != cudaSuccess ||
-      wait_limit_gemm_tc(v) != cudaSuccess || wait_limit_mixer(v) != cudaSuccess) {
+      wait_limit_gemm_tc(v) != cudaSuccess || wait_limit_mixer(v) != cudaSuccess ||
+      wait_limit_attn(v) != cudaSuccess || wait_limit_attn_decode(v) != cudaSuccess) {
     cudaGetLastError();
     return M2_ERR_DEVICE;
   }

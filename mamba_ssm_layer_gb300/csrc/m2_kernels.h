@@ -33,6 +33,12 @@ enum KernelId : int32_t {
   K_DECODE_FUSED,
   K_COPY,
   K_WAIT_CHECK,
+  K_QK_NORM_ROPE,
+  K_KV4_APPEND,
+  K_KV4_GATHER,
+  K_ATTN_PREFILL,
+  K_ATTN_DECODE,
+  K_ATTN_COMBINE,
   K_COUNT
 };
 
@@ -46,11 +52,16 @@ int status_gemv(int clear);
 int status_gemv_mma(int clear);
 int status_gemm_tc(int clear);
 int status_mixer(int clear);
+int status_kv4(int clear);
+int status_attn(int clear);
+int status_attn_decode(int clear);
 // Setters of each translation unit's pipeline wait limit (SM clock cycles).
 cudaError_t wait_limit_gemv(long long cycles);
 cudaError_t wait_limit_gemv_mma(long long cycles);
 cudaError_t wait_limit_gemm_tc(long long cycles);
 cudaError_t wait_limit_mixer(long long cycles);
+cudaError_t wait_limit_attn(long long cycles);
+cudaError_t wait_limit_attn_decode(long long cycles);
 
 // Number of SMs of the current device (cached).
 int num_sms();
@@ -313,5 +324,75 @@ int32_t ssd_chunk_table(const int32_t* cu_host, int32_t nseq, int32_t* table_out
 bool ssd_supported(int H, int P, int N, int G);
 size_t ssd_workspace_bytes(int nchunks, int H, int P, int N);  // dH then decay, each 256-aligned
 cudaError_t launch_ssd(const SsdArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ attention
+
+// Head norm and rotation (k_kv4.cu).
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int32_t ld_q, ld_k, ld_qo, ld_ko;
+  const uint16_t* q_w;
+  const uint16_t* k_w;
+  const int32_t* pos;
+  const uint64_t* step;
+  int32_t T, H, Hkv, D, rot, interleaved;
+  float eps;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t s);
+
+// Host offsets of a varlen batch travel in the launch's parameters (no copy,
+// nothing to keep alive for a captured launch), kSeqs sequences a launch.
+constexpr int kSeqs = 128;
+
+// Paged 4-bit cache (k_kv4.cu).
+struct Kv4 {
+  uint8_t* pages;
+  const int32_t* table;  // [nseq][ld_table]
+  int32_t n_pages, Hkv, D, ld_table;
+};
+struct Kv4RowsArgs {
+  Kv4 c;             // table: of the launch's first sequence
+  uint16_t* k;       // rows of the launch's first sequence
+  uint16_t* v;
+  int32_t ld_k, ld_v;
+  const int32_t* pos;  // append: first position of each sequence; gather: null (0)
+  int32_t nseq;
+  int32_t cu[kSeqs + 1];  // row offsets, cu[0] = 0
+};
+cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv4_gather(const Kv4RowsArgs& a, cudaStream_t s);
+
+// Causal attention of packed sequences (k_attn.cu).
+struct AttnArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  int32_t ld_q, ld_k, ld_v, ld_o;
+  int32_t H, Hkv, D;
+  int32_t Tq, Tk;          // rows of q and k of the whole call
+  float scale;
+  int32_t nseq;
+  int32_t cu_q[kSeqs + 1];  // absolute row offsets
+  int32_t cu_k[kSeqs + 1];
+};
+cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
+
+// Decode attention over the 4-bit cache (k_attn_decode.cu).
+struct AttnDecodeArgs {
+  Kv4 c;
+  const uint16_t* q;
+  uint16_t* out;
+  int32_t ld_q, ld_o;
+  int32_t B, H;
+  const int32_t* len;
+  float scale;
+  void* ws;
+};
+size_t attn_decode_ws_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t D);
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t s);
 
 }  // namespace m2
