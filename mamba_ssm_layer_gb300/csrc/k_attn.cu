@@ -1,54 +1,512 @@
-// k_attn.cu -- causal attention of packed sequences.
+// k_attn.cu -- causal attention of packed sequences on the tensor cores.
+//
+// A tile is 128 query rows: 128 / PK consecutive tokens x PK query heads that
+// share a kv head (PK: the largest power of two that divides H / Hkv), so that
+// short prompts fill it and one K/V tile serves all of them.  A CTA takes two
+// neighbouring tiles of one sequence through the keys, 128 at a time:
+//   S = Q K^T   (tcgen05, 128 x 128 fp32 in tensor memory)
+//   P = exp2(c S - c m) as bf16, written over S; l += sum P   (one thread a row)
+//   O += P V    (P read from tensor memory, V as an MN-major operand)
+// m is the row's reference maximum.  It follows the running maximum only when
+// that has grown by more than 2^8 in the exponential: until then P stays below
+// 2^8, which bf16 and fp32 hold as well, and O needs no rescaling.
+// Bound: the tensor cores (4 * 128 * 128 * D operations a tile pair) and the
+// exponentials (one a score); while one tile's scores are in the softmax
+// warps, the other tile's products run.
+//
+// Roles: warps 0-3 softmax and output of tile 0, warps 4-7 of tile 1, warp 8
+// issues the products, warp 9 the TMA copies; warps 10 and 11 only complete the
+// warpgroup that hands its registers to the softmax (a score row is 128 of them).
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "m2_common.cuh"
 #include "m2_kernels.h"
+#include "m2_tc.cuh"
 
 namespace m2 {
 
-// One warp per (query row, head): online softmax over the keys it sees, lane l
-// holding channels l * D/32 ..  The simplest form; scores and sums in fp32.
+constexpr int kAtThreads = 384;
+// Registers a thread after the hand-over; launched with 168 (65536 / 384, in
+// steps of 8): 2 * 216 + 72 = 3 * 168.
+constexpr int kAtRegsSoftmax = 216, kAtRegsOther = 72;
+constexpr int kAtRows = 128;      // query rows of a tile, keys of a block
+constexpr int kAtMaskBlocks = 4;  // key blocks that some row of the two tiles sees only in part: at most 3
+
 template <int D>
-__global__ void __launch_bounds__(256) attn_rows_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;
+struct AtCfg {
+  static constexpr int kTile = kAtRows * D * 2;            // bytes of a Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;        // K and V tiles in turn
+  static constexpr int kQ = 0;
+  static constexpr int kKV = 2 * kTile;
+  static constexpr int kBars = kKV + kStages * kTile;
+  static constexpr uint32_t kTmS = 0, kTmO = 256;          // tensor-memory columns: S 2 x 128, O 2 x D
+};
+struct AtBars {
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], fin;
+  uint64_t full[10], empty[10];
+  uint32_t bad[kAtMaskBlocks][4];  // keys of a masked block whose values are not finite
+  uint32_t tmem;
+};
+template <int D>
+constexpr int at_smem_bytes() {
+  static_assert(AtCfg<D>::kBars + (int)sizeof(AtBars) + 1024 <= 232448, "shared memory");
+  return AtCfg<D>::kBars + (int)sizeof(AtBars) + 1024;
+}
+
+struct AtArgs {
+  uint16_t* out;
+  const uint16_t* v;
+  int32_t ld_o, ld_v;
+  int32_t groups;   // H / PK
+  int32_t pk_log;
+  int32_t gqa;      // H / Hkv
+  float scale_log2; // scale * log2(e)
+  int32_t nseq;
+  int32_t cu_q[kSeqs + 1], cu_k[kSeqs + 1];
+  int32_t tile[kSeqs + 1];  // first tile pair of each sequence
+};
+
+// MN-major operand descriptor, 128-byte swizzle: 64 elements (128 bytes) of the
+// M/N dimension per row, rows along K; 8-row atoms 1024 bytes apart (stride
+// byte offset), the next 64 elements `lbo` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdescBMn = 1u << 16;  // B is MN-major
+
+// 32 columns of this warp's 32 lanes, without waiting.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+// The loads above have arrived; n values may be used after this.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // no use moves above the wait
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// mbar_wait without a call: a kernel that hands registers between its warps
+// has to be one function.
+__device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
+  const long long t0 = clock64();
+  const bool suspend = limit >= 1000000;
+  while (!(suspend ? mbar_try_wait(bar, parity, 1000u) : mbar_test_wait(bar, parity))) {
+    if (clock64() - t0 > limit) {
+      record_timeout();
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_test_wait(bar, parity) ||
+         at_wait_until(bar, parity, *reinterpret_cast<volatile long long*>(&g_wait_limit));
+}
+__device__ __forceinline__ bool at_drain(uint64_t* bar, uint32_t parity) {
+  return mbar_test_wait(bar, parity) || at_wait_until(bar, parity, kWaitCycles);
+}
+
+// What a CTA works on.
+struct AtItem {
+  int seq, hg;       // sequence; group of PK query heads
+  int q0, nq, nk;    // first token of tile 0 (in the sequence), the sequence's queries and keys
+  int n0, n1;        // key blocks of each tile
+  int jm;            // first key block that some row of tile 0 sees only in part
+};
+__device__ __forceinline__ AtItem at_item(const AtArgs& a) {
+  AtItem it;
+  const int tokens = kAtRows >> a.pk_log;  // of one tile
+  const int total = a.tile[a.nseq];
+  const int p = total - 1 - (int)(blockIdx.x / a.groups);  // late tiles (the most keys) first
+  it.hg = blockIdx.x % a.groups;
+  int lo = 0, hi = a.nseq;  // the last sequence whose first pair is <= p
+  while (hi - lo > 1) {
+    const int m = (lo + hi) / 2;
+    if (a.tile[m] <= p)
+      lo = m;
+    else
+      hi = m;
+  }
+  it.seq = lo;
+  it.nq = a.cu_q[lo + 1] - a.cu_q[lo];
+  it.nk = a.cu_k[lo + 1] - a.cu_k[lo];
+  it.q0 = (p - a.tile[lo]) * 2 * tokens;
+  const int off = it.nk - it.nq;
+  auto blocks = [&](int first) {
+    const int last = min(first + tokens, it.nq) - 1 + off;  // the last key seen
+    return first < it.nq && last >= 0 ? last / kAtRows + 1 : 0;
+  };
+  it.n0 = blocks(it.q0);
+  it.n1 = blocks(it.q0 + tokens);
+  it.jm = max(0, (it.q0 + off + 1) >> 7);
+  return it;
+}
+
+// Looks through row r of a value tile for numbers that are not finite: a
+// probability of zero does not keep them out of the product.  They are set to
+// zero in shared memory and their key is marked; rows that do see the key add
+// them at the end.
+template <int D>
+__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, uint32_t* bad) {
+  bool any = false;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + sw128_chunk(kAtRows, r, c));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      any |= (u[i] & 0x7F80u) == 0x7F80u || (u[i] & 0x7F800000u) == 0x7F800000u;
+  }
+  if (!any) return;
+  atomicOr(&bad[r >> 5], 1u << (r & 31));
+  __threadfence_block();  // marked before it is gone
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(tile + sw128_chunk(kAtRows, r, c));
+    for (int i = 0; i < 4; ++i) {
+      uint32_t u = p[i];
+      if ((u & 0x7F80u) == 0x7F80u) u &= 0xFFFF0000u;
+      if ((u & 0x7F800000u) == 0x7F800000u) u &= 0xFFFFu;
+      p[i] = u;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AtArgs a) {
+  using C = AtCfg<D>;
+  constexpr int NS = C::kStages, HALVES = D / 64, HB = kAtRows * 128;  // 64-channel halves of a tile, bytes of one
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  AtBars* bars = reinterpret_cast<AtBars*>(smem + C::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->o_done[t], 1);
+    }
+    mbar_init(&bars->fin, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int i = 0; i < kAtMaskBlocks * 4; ++i) (&bars->bad[0][0])[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&bars->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const AtItem it = at_item(a);
+  const int n = max(it.n0, it.n1);
+  const int tokens = kAtRows >> a.pk_log;
+  const int hk = (it.hg << a.pk_log) / a.gqa;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t rows = a.cu_q[a.nseq] - a.cu_q[0];
-  if (id >= rows * a.H) return;
-  const int row = a.cu_q[0] + (int)(id / a.H), h = (int)(id % a.H), hk = h / (a.H / a.Hkv);
-  int seq = 0;
-  while (row >= a.cu_q[seq + 1]) ++seq;
-  const int nk = a.cu_k[seq + 1] - a.cu_k[seq], nq = a.cu_q[seq + 1] - a.cu_q[seq];
-  const int last = row - a.cu_q[seq] + nk - nq;  // the last key seen
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  for (int i = 0; i < E; ++i) {
-    q[i] = bf16_to_f32(a.q[(size_t)row * a.ld_q + h * D + lane * E + i]) * a.scale;
-    o[i] = 0.0f;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsOther));
+    if (warp == 9 && lane == 0) {
+      // ------------------------------------------------------ copies
+      const uint64_t keep = policy_evict_normal();
+      int issued = 0, qs = 0;
+      const int h0 = it.hg << a.pk_log;
+      auto load_q = [&](int t) {
+        if (!(t ? it.n1 : it.n0)) return;
+        mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
+        for (int hf = 0; hf < HALVES; ++hf)
+          tma_load_3d(smem + C::kQ + t * C::kTile + hf * HB, &tmQ, hf * 64, h0, a.cu_q[it.seq] + it.q0 + t * tokens,
+                      &bars->q_full[t], keep);
+        qs |= 1 << t;
+      };
+      bool dead = false;
+      load_q(0);
+      for (int i = 0; i < 2 * n && !dead; ++i) {
+        const int s = i % NS;
+        if (i >= NS && !at_wait(&bars->empty[s], ((i / NS) - 1) & 1)) {
+          dead = true;
+          break;
+        }
+        mbar_arrive_expect_tx(&bars->full[s], C::kTile);
+        const CUtensorMap* m = i & 1 ? &tmV : &tmK;
+        for (int hf = 0; hf < HALVES; ++hf)
+          tma_load_3d(smem + C::kKV + s * C::kTile + hf * HB, m, hf * 64, hk, a.cu_k[it.seq] + (i >> 1) * kAtRows,
+                      &bars->full[s], keep);
+        issued = i + 1;
+        if (i == 0) load_q(1);
+      }
+      // every copy this thread issued has landed
+      for (int t = 0; t < 2; ++t)
+        if (qs >> t & 1) at_drain(&bars->q_full[t], 0);
+      for (int i = max(0, issued - NS); i < issued; ++i)
+        if (!at_drain(&bars->full[i % NS], (i / NS) & 1)) break;
+    } else if (warp == 8 && lane == 0 && n > 0) {
+      // ------------------------------------------------------ products
+      constexpr uint32_t idS = tc_idesc(kAtRows, kAtRows), idO = tc_idesc(kAtRows, D) | kIdescBMn;
+      bool dead = false;
+      auto full = [&](int i) { return at_wait(&bars->full[i % NS], (i / NS) & 1); };
+      auto scores = [&](int t, int i) {  // S of tile t with K tile i
+        const uint32_t qb = smem_addr(smem + C::kQ + t * C::kTile), kb = smem_addr(smem + C::kKV + (i % NS) * C::kTile);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma(tmem + C::kTmS + t * kAtRows, sw128_desc(qb + (k >> 2) * HB + (k & 3) * 32),
+                 sw128_desc(kb + (k >> 2) * HB + (k & 3) * 32), idS, k > 0 ? 1 : 0);
+        tc_commit(&bars->s_full[t]);
+      };
+      dead = !full(0);
+      for (int t = 0; t < 2 && !dead; ++t) {
+        if (!(t ? it.n1 : it.n0)) continue;
+        if (!at_wait(&bars->q_full[t], 0)) {
+          dead = true;
+          break;
+        }
+        scores(t, 0);
+      }
+      if (!dead) tc_commit(&bars->empty[0]);
+      for (int j = 0; j < n && !dead; ++j) {
+        const int vi = 2 * j + 1, kn = 2 * j + 2;
+        const uint32_t vb = smem_addr(smem + C::kKV + (vi % NS) * C::kTile);
+        const int tl = j < it.n1 ? 1 : 0;  // the last tile that uses this block
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? it.n1 : it.n0;
+          if (j >= nt) continue;
+          if (!full(vi) || !at_wait(&bars->p_full[t], j & 1)) {
+            dead = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kAtRows / 16; ++k)
+            tc_mma_ts(tmem + C::kTmO + t * D, tmem + C::kTmS + t * kAtRows + k * 8, sw128_mn_desc(vb + k * 2048, HB), idO,
+                      j > 0 || k > 0 ? 1 : 0);
+          if (t == tl) tc_commit(&bars->empty[vi % NS]);
+          if (j + 1 == nt) {
+            tc_commit(&bars->o_done[t]);
+          } else {
+            if (!full(kn)) {
+              dead = true;
+              break;
+            }
+            scores(t, kn);
+          }
+        }
+        if (!dead && j + 1 < n) tc_commit(&bars->empty[kn % NS]);
+      }
+      tc_commit(&bars->fin);  // everything issued here is done before tensor memory is freed
+      at_drain(&bars->fin, 0);
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtRegsSoftmax));
+    // -------------------------------------------------------- softmax and output
+    const int t = warp >> 2, r = 32 * (warp & 3) + lane;
+    const int nt = t ? it.n1 : it.n0, first = it.q0 + t * tokens;
+    const int tok = first + (r >> a.pk_log), off = it.nk - it.nq;
+    const int limit = tok + off;                // the last key this row sees
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + C::kTmS + t * kAtRows, to = tmem + lanes + C::kTmO + t * D;
+    const bool pos = a.scale_log2 > 0.0f;
+    const float c = pos ? a.scale_log2 : 1.0f;  // a scale <= 0 is applied to the scores first
+    float m = -INFINITY, l = 0.0f;
+    bool dead = false;
+    for (int j = 0; j < nt; ++j) {
+      if (j >= it.jm) {
+        const int vi = 2 * j + 1;
+        if (!__all_sync(0xffffffffu, at_wait(&bars->full[vi % NS], (vi / NS) & 1))) {
+          dead = true;
+          break;
+        }
+        at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[j - it.jm]);
+        fence_proxy_async();
+      }
+      if (!__all_sync(0xffffffffu, at_wait(&bars->s_full[t], j & 1))) {
+        dead = true;
+        break;
+      }
+      tc_fence_after();
+      float s[kAtRows];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, s + 32 * i);
+      tmem_ld_wait<kAtRows>(s);
+      if (!pos) {
+#pragma unroll
+        for (int i = 0; i < kAtRows; ++i) s[i] *= a.scale_log2;
+      }
+      if (j * kAtRows + kAtRows - 1 > first + off) {  // some row of the tile does not see the whole block
+        const int seen = limit - j * kAtRows;
+#pragma unroll
+        for (int i = 0; i < kAtRows; ++i) s[i] = i <= seen ? s[i] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i < kAtRows; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+      const float mn = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
+      if (j == 0) {
+        m = mn;
+      } else {
+        const bool grow = (mn - m) * c > 8.0f;
+        if (__any_sync(0xffffffffu, grow)) {  // rescale what was summed so far (its products are complete)
+          const float f = grow ? ex2((m - mn) * c) : 1.0f;
+          if (grow) m = mn;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < D; i += 16) {
+            float o[16];
+            uint32_t u[16];
+            tmem_ld16(to + i, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * f);
+            tmem_st16(to + i, u);
+          }
+        }
+      }
+      const float b = m == -INFINITY ? 0.0f : -m * c;  // nothing seen yet: every exponential is 0
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kAtRows; i += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float x = ex2(fmaf(s[i + 2 * k], c, b)), y = ex2(fmaf(s[i + 2 * k + 1], c, b));
+          sum[k & 3] += x + y;
+          p[k] = pack_bf16x2(x, y);
+        }
+        tmem_st16(ts + i / 2, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->p_full[t]);
+    }
+    if (!dead && nt > 0) dead = !__all_sync(0xffffffffu, at_wait(&bars->o_done[t], 0));
+    if (!dead) {
+      tc_fence_after();
+      const float inv = limit >= 0 ? 1.0f / l : 0.0f;
+      uint16_t* dst = a.out + (size_t)(a.cu_q[it.seq] + tok) * a.ld_o +
+                      (size_t)((it.hg << a.pk_log) + (r & ((1 << a.pk_log) - 1))) * D;
+      uint32_t marks = 0;
+      for (int i = 0; i < kAtMaskBlocks * 4; ++i) marks |= (&bars->bad[0][0])[i];
+#pragma unroll
+      for (int i = 0; i < D; i += 32) {
+        float o[32];
+        if (nt > 0) {
+          tmem_ld32_async(to + i, o);
+          tmem_ld_wait<32>(o);
+        }
+        if (marks) {  // add the values that were kept out of the products, where they are seen
+          for (int w = 0; w < kAtMaskBlocks * 4; ++w) {
+            const int j = it.jm + (w >> 2);
+            for (uint32_t bits = j < nt ? (&bars->bad[0][0])[w] : 0; bits; bits &= bits - 1) {
+              const int key = j * kAtRows + (w & 3) * 32 + __ffs(bits) - 1;
+              if (key > limit || tok >= it.nq) continue;
+              const uint16_t* vr = a.v + (size_t)(a.cu_k[it.seq] + key) * a.ld_v + (size_t)hk * D + i;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float x = bf16_to_f32(vr[k]);
+                if (!(fabsf(x) < INFINITY)) o[k] += x;
+              }
+            }
+          }
+        }
+        if (tok < it.nq) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (limit >= 0)
+              w = make_uint4(pack_bf16x2(o[k] * inv, o[k + 1] * inv), pack_bf16x2(o[k + 2] * inv, o[k + 3] * inv),
+                             pack_bf16x2(o[k + 4] * inv, o[k + 5] * inv), pack_bf16x2(o[k + 6] * inv, o[k + 7] * inv));
+            *reinterpret_cast<uint4*>(dst + i + k) = w;
+          }
+        }
+      }
+    }
   }
-  for (int j = 0; j <= last; ++j) {
-    const size_t kr = a.cu_k[seq] + j;
-    float s = 0.0f;
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], bf16_to_f32(a.k[kr * a.ld_k + hk * D + lane * E + i]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), f = expf(m - mn), p = expf(s - mn);
-    m = mn;
-    l = l * f + p;
-    for (int i = 0; i < E; ++i) o[i] = o[i] * f + p * bf16_to_f32(a.v[kr * a.ld_v + hk * D + lane * E + i]);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
   }
-  for (int i = 0; i < E; ++i)
-    a.out[(size_t)row * a.ld_o + h * D + lane * E + i] = f32_to_bf16(last >= 0 ? o[i] / l : 0.0f);
+}
+
+// ------------------------------------------------------------------ host
+
+// Rows of `heads` heads of D channels, as {channel, head, row}; boxes of 64
+// channels x box_heads x box_rows land as 128-byte rows, swizzled.
+static bool encode_heads(CUtensorMap* map, const uint16_t* base, int D, int heads, int64_t rows, int64_t ld,
+                         int box_heads, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+static cudaError_t launch_attn(const AttnArgs& g, cudaStream_t s) {
+  static int done_mask[64] = {0};
+  AtArgs a;
+  a.out = g.out;
+  a.v = g.v;
+  a.ld_o = g.ld_o;
+  a.ld_v = g.ld_v;
+  a.gqa = g.H / g.Hkv;
+  a.pk_log = 0;
+  while (a.pk_log < 7 && a.gqa % (2 << a.pk_log) == 0) ++a.pk_log;
+  const int pk = 1 << a.pk_log, tokens = kAtRows / pk;
+  a.groups = g.H / pk;
+  a.scale_log2 = g.scale * 1.4426950408889634f;
+  a.nseq = g.nseq;
+  a.tile[0] = 0;
+  for (int i = 0; i <= kSeqs; ++i) {
+    a.cu_q[i] = g.cu_q[i];
+    a.cu_k[i] = g.cu_k[i];
+    if (i < kSeqs) a.tile[i + 1] = a.tile[i] + (g.cu_q[i + 1] - g.cu_q[i] + 2 * tokens - 1) / (2 * tokens);
+  }
+  CUtensorMap q, k, v;
+  // without keys no copy of them is issued: any rows do for the maps
+  const bool keys = g.Tk > 0;
+  if (!encode_heads(&q, g.q, D, g.H, g.Tq, g.ld_q, pk, tokens) ||
+      !encode_heads(&k, keys ? g.k : g.q, D, keys ? g.Hkv : 1, keys ? g.Tk : 1, keys ? g.ld_k : g.ld_q, 1, kAtRows) ||
+      !encode_heads(&v, keys ? g.v : g.q, D, keys ? g.Hkv : 1, keys ? g.Tk : 1, keys ? g.ld_v : g.ld_q, 1, kAtRows))
+    return cudaErrorInvalidValue;
+  auto kern = attn_prefill_kernel<D>;
+  constexpr int smem = at_smem_bytes<D>();
+  cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
+  if (e != cudaSuccess) return e;
+  trace_pre(K_ATTN_PREFILL, s);
+  e = launch_k(kern, dim3((unsigned)a.tile[g.nseq] * a.groups), dim3(kAtThreads), smem, s, true, q, k, v, a);
+  trace_post(K_ATTN_PREFILL, s);
+  return e;
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
-  const int64_t tasks = (int64_t)(a.cu_q[a.nseq] - a.cu_q[0]) * a.H;
-  const dim3 grid((unsigned)((tasks + 7) / 8)), block(256);
-  trace_pre(K_ATTN_PREFILL, s);
-  const cudaError_t e = launch_k(a.D == 128 ? attn_rows_kernel<128> : attn_rows_kernel<64>, grid, block, 0, s, true, a);
-  trace_post(K_ATTN_PREFILL, s);
-  return e;
+  return a.D == 128 ? launch_attn<128>(a, s) : launch_attn<64>(a, s);
 }
 
 int status_attn(int clear) { return tu_status(clear); }
