@@ -1,5 +1,20 @@
 // k_attn_decode.cu -- attention of one query token a sequence over the paged
 // 4-bit cache.
+//
+// A unit is one page (64 tokens) of one kv head: 72 * D contiguous bytes.  The
+// units of all sequences, in the order (sequence, head chunk, page), are cut
+// into equal spans, one a CTA, and each span into equal runs, one a warp, so
+// that ragged lengths, few sequences and single long ones all load every SM
+// alike.  A warp streams its units through its own ring of bulk copies and
+// keeps the running softmax of up to 16 query heads (HN = 8 or 16) on warp MMA:
+//   S^T [64 tokens x HN] = K Q^T    K codes become f16 and take their scale,
+//                                   exactly (6 significant bits)
+//   O^T [D x HN] += V^T P^T         likewise V; P rounded to f16 (2^-11)
+// Queries enter as f16 rows prescaled by an exact power of two.  Scores, sums and
+// outputs are fp32.  Rows that a warp, then a CTA, holds only in part are
+// joined: warps through shared memory, CTAs by attn_decode_combine.
+// Bound: HBM (4.5 bits a value); per unit 256 4-bit conversions, 256 f16x2
+// multiplications and 64 HN/8 MMAs a warp keep the other pipes close behind.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -9,86 +24,620 @@
 
 namespace m2 {
 
-// One CTA per (sequence, query head): 8 warps take the tokens in turn, lane l
-// holding channels 4l .. 4l+3 (D = 128) or 2l, 2l+1; the warps' running
-// maxima, sums and outputs are joined at the end.  The simplest form.
+constexpr int kAdWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(256) attn_decode_rows_kernel(const AttnDecodeArgs a) {
-  using L = Kv4Block<D>;
-  constexpr int E = D / 32, W = 8;
-  __shared__ float sm[W], sl[W], so[W][D];
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, hk = h / (a.H / a.c.Hkv);
-  int64_t n = a.len[b];
-  if (n > (int64_t)a.c.ld_table * kPage) {
-    n = (int64_t)a.c.ld_table * kPage;
-    M2_RECORD_ARG(g_status);
-  }
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  const int d0 = lane * E, g = d0 / 16;
-  for (int i = 0; i < E; ++i) {
-    q[i] = bf16_to_f32(a.q[(size_t)b * a.ld_q + h * D + d0 + i]) * a.scale;
-    o[i] = 0.0f;
-  }
-  for (int64_t j = warp; j < n; j += W) {
-    const int page = a.c.table[(size_t)b * a.c.ld_table + j / kPage], t = (int)(j % kPage);
-    if (page < 0 || page >= a.c.n_pages) {
-      M2_RECORD_ARG(g_status);
-      continue;
-    }
-    const uint8_t* blk = a.c.pages + ((size_t)page * a.c.Hkv + hk) * L::kBytes;
-    const float sk = kv4_scale(blk[L::ks(t, g)]), sv = kv4_scale(blk[L::vs(t, g)]);
-    float s = 0.0f;
-    for (int i = 0; i < E; i += 2) {
-      const int d = d0 + i;
-      const float2 f = kv4_f32x2(blk[L::k(t, g, d % 16 / 4) + d % 4 / 2]);
-      s += (q[i] * f.x + q[i + 1] * f.y) * sk;
-    }
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), f = expf(m - mn), p = expf(s - mn);
-    m = mn;
-    l = l * f + p;
-    for (int i = 0; i < E; ++i) {
-      const uint32_t c = blk[L::v(t, (d0 + i) / 8, (d0 + i) % 8)] >> (4 * (t & 1));
-      o[i] = o[i] * f + p * (kv4_f32x2(c & 15u).x * sv);
-    }
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int i = 0; i < E; ++i) so[warp][d0 + i] = o[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-    for (int w = 0; w < W; ++w)
-      if (sl[w] != 0.0f) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < W; ++w) {
-      if (sl[w] == 0.0f) continue;
-      const float f = expf(sm[w] - top);
-      sum += sl[w] * f;
-      acc += so[w][threadIdx.x] * f;
-    }
-    a.out[(size_t)b * a.ld_o + h * D + threadIdx.x] = f32_to_bf16(sum != 0.0f ? acc / sum : 0.0f);
+struct AdCfg {
+  static constexpr int kUnit = Kv4Block<D>::kBytes;
+  static constexpr int kStages = D == 128 ? 3 : 6;  // 8 warps * stages * unit = 216 KB
+  static constexpr int kRing = kStages * kUnit;     // of one warp
+  static constexpr int kStride = D + 4;             // floats between the heads of a record: no bank conflicts
+};
+// A partial result: running maxima and sums of HN heads, then their outputs.
+template <int D, int HN>
+constexpr int ad_record() {
+  return 2 * HN + HN * AdCfg<D>::kStride;
+}
+// Which row (sequence, head chunk) a partial belongs to, and whether the row
+// starts before / ends after the CTA's span.
+struct AdMeta {
+  int32_t seg, before, after;
+};
+struct AdShared {
+  uint64_t full[kAdWarps][6];
+  int32_t ok[kAdWarps][6];
+  AdMeta meta[kAdWarps][2];
+  int64_t scan[kAdWarps];
+  int64_t run0[kAdWarps + 1];           // first unit of each warp's run, then the span's end
+  int32_t run_b[kAdWarps];              // sequence of the run's first unit
+  int64_t run_base[kAdWarps];           // units before that sequence
+};
+
+struct AdArgs {
+  AttnDecodeArgs g;
+  int32_t G, chunks, rows;  // query heads a kv head; chunks of HN heads; rows = Hkv * chunks a sequence
+  int32_t nc;               // CTAs
+  int32_t by_row;           // one CTA a row: no row is cut
+  float* warp_part;         // [nc][8] records
+  float* cta_part;          // [nc][2] records: a row that began earlier, a row that goes on
+  int32_t* cta_seg;         // [nc][2] rows of those, -1 where there is none
+};
+
+__device__ __forceinline__ int ad_len(const AttnDecodeArgs& g, int b) {
+  const int n = g.len[b], most = g.c.ld_table * kPage;
+  if (n > most) M2_RECORD_ARG(g_status);
+  return max(0, min(n, most));
+}
+__device__ __forceinline__ int ad_pages(const AttnDecodeArgs& g, int b) { return (ad_len(g, b) + kPage - 1) / kPage; }
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t dup_lo(uint32_t a) { return __byte_perm(a, a, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t a) { return __byte_perm(a, a, 0x3232); }
+__device__ __forceinline__ uint32_t trans8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ad_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 4-byte words of a lane's codes or scales.
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
+// Two scale bytes of a word (0 and 2, or 1 and 3) as f16x2.
+constexpr uint32_t kScaleBits = 0x7F807F80u;
+__device__ __forceinline__ uint32_t scales02(uint32_t w, uint32_t mask) { return (w << 7) & mask; }
+__device__ __forceinline__ uint32_t scales13(uint32_t w, uint32_t mask) { return (w >> 1) & mask; }
+
+// The running softmax of one row (sequence, head chunk) in a warp.  Lane (r, c) =
+// (lane / 4, lane % 4) owns heads 2c and 2c + 1 of each tile of 8.
+template <int D, int NT>
+struct AdRow {
+  uint32_t q[NT][D / 16][2];  // B operand: head r, channels 16g + 4c .. + 3
+  float qs[NT][2];            // score factor (log2 units) of heads 2c, 2c + 1
+  float m[NT][2], l[NT][2];   // reference maximum; this lane's share of the sum
+  float o[NT][D / 16][4];     // channels 16i + r and 16i + 8 + r of heads 2c, 2c + 1
+
+  __device__ __forceinline__ void start(const AdArgs& a, int b, int row, int lane) {
+    const int r = lane >> 2, c = lane & 3, hk = row / a.chunks, ch = row - hk * a.chunks;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int h = ch * 8 * NT + t * 8 + r;  // within the group
+      uint2 w[D / 16];
+      float top = 0.0f;
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) {
+        w[g] = make_uint2(0u, 0u);
+        if (h < a.G)
+          w[g] = *reinterpret_cast<const uint2*>(a.g.q + (size_t)b * a.g.ld_q + (size_t)(hk * a.G + h) * D + 16 * g + 4 * c);
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w[g].x)), fabsf(bf16hi(w[g].x))),
+                               fmaxf(fabsf(bf16lo(w[g].y)), fabsf(bf16hi(w[g].y)))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^-e for a largest magnitude of 2^e ..: exact in f16 except far below the largest
+      int e = (int)(__float_as_uint(top) >> 23);
+      e = e == 255 ? 127 : max(1, min(e, 253));
+      const float f = __uint_as_float((uint32_t)(254 - e) << 23), u = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) {
+        q[t][g][0] = pack_f16x2(bf16lo(w[g].x) * f, bf16hi(w[g].x) * f);
+        q[t][g][1] = pack_f16x2(bf16lo(w[g].y) * f, bf16hi(w[g].y) * f);
+      }
+      const float k = u * (a.g.scale * 1.4426950408889634f);
+      qs[t][0] = __shfl_sync(0xffffffffu, k, 8 * c);
+      qs[t][1] = __shfl_sync(0xffffffffu, k, 8 * c + 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[t][i][j] = 0.0f;
+    }
+  }
+
+  // One unit in shared memory, of which the first `seen` tokens count.
+  __device__ __forceinline__ void unit(const uint8_t* u, int seen, int lane) {
+    using L = Kv4Block<D>;
+    constexpr int GW = D / 32;  // words of a lane's codes: 2 groups each
+    const int r = lane >> 2, c = lane & 3;
+    float s[4][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      uint32_t k0[GW], k1[GW], s0[GW / 2], s1[GW / 2];
+      const int t0 = 16 * mt + r;
+      lds_words<GW>(u + L::kK + t0 * (D / 2) + c * (D / 8), k0);
+      lds_words<GW>(u + L::kK + (t0 + 8) * (D / 2) + c * (D / 8), k1);
+      lds_words<GW / 2>(u + L::kKs + t0 * (D / 16), s0);
+      lds_words<GW / 2>(u + L::kKs + (t0 + 8) * (D / 16), s1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[mt][t][j] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        // scale word w / 2 holds groups 4(w/2) .. + 3: this code word's are (0, 1) or (2, 3) of them
+        const uint32_t e0 = scales02(s0[w / 2], kScaleBits), f0 = scales13(s0[w / 2], kScaleBits);
+        const uint32_t e1 = scales02(s1[w / 2], kScaleBits), f1 = scales13(s1[w / 2], kScaleBits);
+        const uint32_t g00 = w & 1 ? dup_hi(e0) : dup_lo(e0), g01 = w & 1 ? dup_hi(f0) : dup_lo(f0);
+        const uint32_t g10 = w & 1 ? dup_hi(e1) : dup_lo(e1), g11 = w & 1 ? dup_hi(f1) : dup_lo(f1);
+        const uint32_t a0 = hmul2(kv4_f16x2(k0[w]), g00), a2 = hmul2(kv4_f16x2(k0[w] >> 8), g00);
+        const uint32_t a1 = hmul2(kv4_f16x2(k1[w]), g10), a3 = hmul2(kv4_f16x2(k1[w] >> 8), g10);
+        const uint32_t b0 = hmul2(kv4_f16x2(k0[w] >> 16), g01), b2 = hmul2(kv4_f16x2(k0[w] >> 24), g01);
+        const uint32_t b1 = hmul2(kv4_f16x2(k1[w] >> 16), g11), b3 = hmul2(kv4_f16x2(k1[w] >> 24), g11);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mma_f16(s[mt][t], a0, a1, a2, a3, q[t][2 * w][0], q[t][2 * w][1]);
+          mma_f16(s[mt][t], b0, b1, b2, b3, q[t][2 * w + 1][0], q[t][2 * w + 1][1]);
+        }
+      }
+    }
+    // softmax: P as the second product's B operand
+    uint32_t p[4][NT][2];
+    bool grow = false;
+    float mx[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      mx[t][0] = mx[t][1] = -INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[mt][t][j] *= qs[t][j & 1];
+          if (seen < kPage && 16 * mt + r + (j & 2) * 4 >= seen) s[mt][t][j] = -INFINITY;
+          mx[t][j & 1] = fmaxf(mx[t][j & 1], s[mt][t][j]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mx[t][i] = fmaxf(mx[t][i], __shfl_xor_sync(0xffffffffu, mx[t][i], x));
+        grow |= mx[t][i] - m[t][i] > 8.0f;
+      }
+    }
+    // the reference follows the maximum once it has grown 2^8: until then P (with its
+    // factor 2^7, which keeps small ones out of f16's subnormals) stays below 2^15
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool up = mx[t][i] - m[t][i] > 8.0f;
+          f[i] = up ? ad_ex2(m[t][i] - mx[t][i]) : 1.0f;
+          if (up) m[t][i] = mx[t][i];
+          l[t][i] *= f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[t][i][j] *= f[j & 1];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float b0 = m[t][0] == -INFINITY ? 0.0f : 7.0f - m[t][0], b1 = m[t][1] == -INFINITY ? 0.0f : 7.0f - m[t][1];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const float x0 = ad_ex2(s[mt][t][0] + b0), x1 = ad_ex2(s[mt][t][1] + b1);
+        const float x2 = ad_ex2(s[mt][t][2] + b0), x3 = ad_ex2(s[mt][t][3] + b1);
+        l[t][0] += x0 + x2;
+        l[t][1] += x1 + x3;
+        p[mt][t][0] = trans8x8(pack_f16x2(x0, x1));
+        p[mt][t][1] = trans8x8(pack_f16x2(x2, x3));
+      }
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint32_t v0[GW], v1[GW], s0[GW], s1[GW];
+      lds_words<GW>(u + L::kV + (2 * ks) * (4 * D) + r * (D / 2) + c * (D / 8), v0);
+      lds_words<GW>(u + L::kV + (2 * ks + 1) * (4 * D) + r * (D / 2) + c * (D / 8), v1);
+      lds_words<GW>(u + L::kVs + (8 * ks + c) * (D / 8), s0);
+      lds_words<GW>(u + L::kVs + (8 * ks + 4 + c) * (D / 8), s1);
+      // slots past the last token may hold any scale: theirs become 0
+      uint32_t m0 = kScaleBits, m1 = kScaleBits;
+      if (seen < kPage) {
+        const int t0 = 16 * ks + 2 * c;
+        m0 = (t0 < seen ? 0x7F80u : 0u) | (t0 + 1 < seen ? 0x7F800000u : 0u);
+        m1 = (t0 + 8 < seen ? 0x7F80u : 0u) | (t0 + 9 < seen ? 0x7F800000u : 0u);
+      }
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        const uint32_t e0 = scales02(s0[w], m0), e1 = scales02(s1[w], m1);
+        const uint32_t f0 = scales13(s0[w], m0), f1 = scales13(s1[w], m1);
+        const uint32_t a0 = hmul2(kv4_f16x2(v0[w]), e0), a1 = hmul2(kv4_f16x2(v0[w] >> 8), e0);
+        const uint32_t a2 = hmul2(kv4_f16x2(v1[w]), e1), a3 = hmul2(kv4_f16x2(v1[w] >> 8), e1);
+        const uint32_t b0 = hmul2(kv4_f16x2(v0[w] >> 16), f0), b1 = hmul2(kv4_f16x2(v0[w] >> 24), f0);
+        const uint32_t b2 = hmul2(kv4_f16x2(v1[w] >> 16), f1), b3 = hmul2(kv4_f16x2(v1[w] >> 24), f1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mma_f16(o[t][2 * w], a0, a1, a2, a3, p[ks][t][0], p[ks][t][1]);
+          mma_f16(o[t][2 * w + 1], b0, b1, b2, b3, p[ks][t][0], p[ks][t][1]);
+        }
+      }
+    }
+  }
+
+  // The sums over the lanes of a head.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
+  }
+  __device__ __forceinline__ void store_record(float* rec, int lane) const {
+    constexpr int HN = 8 * NT;
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int h = 8 * t + 2 * c;
+      if (r == 0) {
+        rec[h] = m[t][0], rec[h + 1] = m[t][1];
+        rec[HN + h] = l[t][0], rec[HN + h + 1] = l[t][1];
+      }
+      float* d0 = rec + 2 * HN + h * AdCfg<D>::kStride + r;
+      float* d1 = d0 + AdCfg<D>::kStride;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        d0[16 * i] = o[t][i][0], d1[16 * i] = o[t][i][1];
+        d0[16 * i + 8] = o[t][i][2], d1[16 * i + 8] = o[t][i][3];
+      }
+    }
+  }
+  __device__ __forceinline__ void store_out(const AdArgs& a, int b, int row, int lane) const {
+    const int r = lane >> 2, c = lane & 3, hk = row / a.chunks, ch = row - hk * a.chunks;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = ch * 8 * NT + t * 8 + 2 * c + k;
+        if (h >= a.G) continue;
+        const float inv = l[t][k] != 0.0f ? 1.0f / l[t][k] : 0.0f;  // nothing seen: zeros
+        uint16_t* dst = a.g.out + (size_t)b * a.g.ld_o + (size_t)(hk * a.G + h) * D + r;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          dst[16 * i] = f32_to_bf16(o[t][i][k] * inv);
+          dst[16 * i + 8] = f32_to_bf16(o[t][i][2 + k] * inv);
+        }
+      }
+  }
+};
+
+// A position in the order of units.
+struct AdCursor {
+  int b, row, page, pages, len;
+  __device__ __forceinline__ void load(const AdArgs& a) {
+    len = ad_len(a.g, b);
+    pages = (len + kPage - 1) / kPage;
+  }
+  // to the next unit; b == B past the last one
+  __device__ __forceinline__ void next(const AdArgs& a) {
+    if (++page < pages) return;
+    page = 0;
+    if (++row < a.rows) return;
+    row = 0;
+    do {
+      if (++b >= a.g.B) return;
+      load(a);
+    } while (pages == 0);
+  }
+};
+
+// Joins `members` records of one row: `at(i)` gives the i-th.  Writes the output
+// (rec null) or another record.
+template <int D, int NT, typename At>
+__device__ __forceinline__ void ad_join(const AdArgs& a, int members, At at, int seg, float* rec) {
+  constexpr int HN = 8 * NT;
+  const int b = seg / a.rows, row = seg - b * a.rows, hk = row / a.chunks, ch = row - hk * a.chunks;
+  for (int i = threadIdx.x; i < HN * D; i += blockDim.x) {
+    const int h = i / D, d = i - h * D, head = ch * HN + h;
+    if (head >= a.G) break;
+    float m = -INFINITY, l = 0.0f, o = 0.0f;
+    for (int k = 0; k < members; ++k) m = fmaxf(m, at(k)[h]);
+    for (int k = 0; k < members; ++k) {
+      const float* p = at(k);
+      const float f = p[h] == -INFINITY ? (p[HN + h] == 0.0f ? 0.0f : 1.0f) : ad_ex2(p[h] - m);
+      l += p[HN + h] * f;
+      o += p[2 * HN + h * AdCfg<D>::kStride + d] * f;
+    }
+    if (rec) {
+      if (d == 0) rec[h] = m, rec[HN + h] = l;
+      rec[2 * HN + h * AdCfg<D>::kStride + d] = o;
+    } else {
+      a.g.out[(size_t)b * a.g.ld_o + (size_t)(hk * a.G + head) * D + d] = f32_to_bf16(l != 0.0f ? o / l : 0.0f);
+    }
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdArgs a) {
+  using C = AdCfg<D>;
+  constexpr int S = C::kStages, REC = ad_record<D, 8 * NT>();
+  static_assert(REC * 4 <= C::kRing, "a record lies in its warp's ring");
+  extern __shared__ __align__(128) uint8_t smem[];
+  AdShared* sh = reinterpret_cast<AdShared*>(smem + kAdWarps * C::kRing);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&sh->full[warp][s], 1);
+    sh->meta[warp][0].seg = sh->meta[warp][1].seg = -1;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  const int B = a.g.B;
+  // ---- the span and its runs: prefix sums of the sequences' units
+  const int per = (B + kAdWarps * 32 - 1) / (kAdWarps * 32), b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += ad_pages(a.g, b);
+  int64_t pre = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) sh->scan[warp] = pre;
+  __syncthreads();
+  int64_t total = 0;
+  pre -= mine;
+#pragma unroll
+  for (int w = 0; w < kAdWarps; ++w) {
+    if (w < warp) pre += sh->scan[w];
+    total += sh->scan[w];
+  }
+  pre *= a.rows;
+  total *= a.rows;
+  int64_t s0, s1;
+  if (a.by_row) {  // row cta of sequence cta / rows
+    const int b = cta / a.rows;
+    if (tid == b / per) {
+      int64_t at = pre;
+      for (int k = b0; k < b; ++k) at += (int64_t)ad_pages(a.g, k) * a.rows;
+      const int64_t n = ad_pages(a.g, b);
+      sh->run0[0] = at + (cta - b * a.rows) * n;
+      sh->run0[1] = sh->run0[0] + n;
+    }
+    __syncthreads();
+    s0 = sh->run0[0];
+    s1 = sh->run0[1];
+    __syncthreads();
+  } else {
+    // at least a unit for every warp: the CTAs without work are the last ones
+    const int64_t nc = min((int64_t)a.nc, (total + kAdWarps - 1) / kAdWarps);
+    s0 = cta < nc ? total * cta / nc : total;
+    s1 = cta < nc ? total * (cta + 1) / nc : total;
+  }
+  if (tid <= kAdWarps) sh->run0[tid] = s0 + (s1 - s0) * tid / kAdWarps;
+  __syncthreads();
+  {
+    int64_t at = pre;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t n = (int64_t)ad_pages(a.g, b) * a.rows;
+      for (int w = 0; w < kAdWarps; ++w)
+        if (sh->run0[w] >= at && sh->run0[w] < at + n) {
+          sh->run_b[w] = b;
+          sh->run_base[w] = at;
+        }
+      at += n;
+    }
+  }
+  // rows of sequences without tokens
+  for (int b = cta; b < B; b += gridDim.x)
+    if (ad_len(a.g, b) == 0)
+      for (int i = tid; i < a.g.H * D / 8; i += kAdWarps * 32)
+        *reinterpret_cast<uint4*>(a.g.out + (size_t)b * a.g.ld_o + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+
+  // ---- this warp's run
+  uint8_t* ring = smem + warp * C::kRing;
+  const int64_t u0 = sh->run0[warp], u1 = sh->run0[warp + 1];
+  const int n = (int)(u1 - u0);
+  if (n > 0) {
+    AdCursor cur;
+    cur.b = sh->run_b[warp];
+    cur.load(a);
+    const int64_t in = u0 - sh->run_base[warp];
+    cur.row = (int)(in / cur.pages);
+    cur.page = (int)(in - (int64_t)cur.row * cur.pages);
+    AdCursor ahead = cur;
+    const uint64_t pol = a.chunks > 1 ? policy_evict_normal() : policy_evict_first();
+    auto fetch = [&](int i) {  // unit i of the run into its stage
+      const int st = i % S;
+      if (lane == 0) {
+        const int page = a.g.c.table[(size_t)ahead.b * a.g.c.ld_table + ahead.page];
+        const bool ok = page >= 0 && page < a.g.c.n_pages;
+        sh->ok[warp][st] = ok;
+        if (ok) {
+          mbar_arrive_expect_tx(&sh->full[warp][st], C::kUnit);
+          bulk_g2s(ring + st * C::kUnit, a.g.c.pages + ((size_t)page * a.g.c.Hkv + ahead.row / a.chunks) * C::kUnit,
+                   C::kUnit, &sh->full[warp][st], pol);
+        } else {
+          M2_RECORD_ARG(g_status);
+          mbar_arrive(&sh->full[warp][st]);
+        }
+      }
+      ahead.next(a);
+    };
+    int fetched = 0;
+    for (; fetched < S && fetched < n; ++fetched) fetch(fetched);
+    AdRow<D, NT> row;
+    row.start(a, cur.b, cur.row, lane);
+    int first_page = cur.page;  // of the row's part in this run
+    int64_t row_at = u0 - cur.page;  // the row's first unit
+    bool dead = false;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % S;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[warp][st], (i / S) & 1))) {
+        dead = true;
+        break;
+      }
+      if (sh->ok[warp][st]) row.unit(ring + st * C::kUnit, min(kPage, cur.len - cur.page * kPage), lane);
+      __syncwarp();  // the stage is read
+      if (fetched < n) fetch(fetched++);
+      const bool ends = cur.page + 1 == cur.pages;
+      if (ends || i + 1 == n) {  // the row leaves this warp
+        row.finish();
+        if (ends && first_page == 0) {
+          row.store_out(a, cur.b, cur.row, lane);
+        } else {
+          const int slot = i + 1 == n ? 1 : 0;
+          // the last part goes into the ring (free by now), an earlier one through L2
+          row.store_record(slot ? reinterpret_cast<float*>(ring) : a.warp_part + (size_t)(cta * kAdWarps + warp) * REC,
+                           lane);
+          if (lane == 0) {
+            AdMeta& mt = sh->meta[warp][slot];
+            mt.seg = cur.b * a.rows + cur.row;
+            mt.before = row_at < s0;
+            mt.after = row_at + cur.pages > s1;
+          }
+        }
+        if (i + 1 < n) {
+          cur.next(a);
+          first_page = 0;
+          row_at = u0 + i + 1;
+          row.start(a, cur.b, cur.row, lane);
+        }
+      } else {
+        ++cur.page;
+      }
+    }
+    if (dead) {  // every copy of this warp has landed before the CTA goes on
+      for (int i = max(0, fetched - S); i < fetched; ++i)
+        if (!mbar_drain(&sh->full[warp][i % S], (i / S) & 1)) break;
+    }
+  }
+  __syncthreads();
+
+  // ---- rows cut between warps
+  int32_t seg_first = -1, seg_last = -1;
+  for (int e = 0; e < 2 * kAdWarps;) {
+    const AdMeta& mt = sh->meta[e >> 1][e & 1];
+    if (mt.seg < 0) {
+      ++e;
+      continue;
+    }
+    // members: the entries from e on with this row; a row passes from a warp's last part to the next warp's
+    // first or only one, and warps without work lie at the end or hold nothing
+    int list[kAdWarps + 1], k = 0;
+    int x = e;
+    for (; x < 2 * kAdWarps; ++x) {
+      const int sg = sh->meta[x >> 1][x & 1].seg;
+      if (sg < 0) continue;
+      if (sg != mt.seg) break;
+      if (k <= kAdWarps) list[k++] = x;
+    }
+    auto at = [&](int i) -> const float* {
+      const int y = list[i];
+      return y & 1 ? reinterpret_cast<const float*>(smem + (y >> 1) * C::kRing)
+                   : a.warp_part + (size_t)(cta * kAdWarps + (y >> 1)) * REC;
+    };
+    float* rec = nullptr;
+    if (mt.before) {
+      rec = a.cta_part + (size_t)(2 * cta) * REC;
+      seg_first = mt.seg;
+    } else if (mt.after) {
+      rec = a.cta_part + (size_t)(2 * cta + 1) * REC;
+      seg_last = mt.seg;
+    }
+    ad_join<D, NT>(a, k, at, mt.seg, rec);
+    e = x;
+  }
+  if (tid == 0 && !a.by_row) {
+    a.cta_seg[2 * cta] = seg_first;
+    a.cta_seg[2 * cta + 1] = seg_last;
+  }
+}
+
+// Rows cut between CTAs: CTA c joins the row that began in span c and goes on.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) attn_decode_combine_kernel(const AdArgs a) {
+  constexpr int REC = ad_record<D, 8 * NT>();
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, seg = a.cta_seg[2 * c + 1];
+  if (seg < 0) return;
+  int k = 1;
+  while (c + k < a.nc && a.cta_seg[2 * (c + k)] == seg) ++k;
+  ad_join<D, NT>(
+      a, k,
+      [&](int i) -> const float* { return a.cta_part + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * REC; }, seg,
+      nullptr);
+}
+
+// ------------------------------------------------------------------ host
+
+static int ad_tiles(int G) { return G <= 8 ? 1 : 2; }
+static size_t ad_record_bytes(int D, int nt) { return (size_t)(2 * 8 * nt + 8 * nt * (D + 4)) * 4; }
 
 size_t attn_decode_ws_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t D) {
   (void)B;
-  (void)H;
-  (void)Hkv;
-  (void)D;
-  return 256;
+  const size_t n = num_sms();
+  return n * (kAdWarps + 2) * ad_record_bytes(D, ad_tiles(H / Hkv)) + (n * 2 * 4 + 255) / 256 * 256;
+}
+
+template <int D, int NT>
+static cudaError_t launch_ad(const AttnDecodeArgs& g, cudaStream_t s) {
+  static int done_mask[64] = {0};
+  constexpr int smem = kAdWarps * AdCfg<D>::kRing + (int)sizeof(AdShared);
+  static_assert(smem <= 232448, "shared memory");
+  AdArgs a;
+  a.g = g;
+  a.G = g.H / g.c.Hkv;
+  a.chunks = (a.G + 8 * NT - 1) / (8 * NT);
+  a.rows = g.c.Hkv * a.chunks;
+  // Few rows of few pages: a CTA takes a whole row, and nothing is left to combine.
+  a.by_row = (int64_t)g.B * a.rows <= num_sms() && g.c.ld_table <= 32;
+  a.nc = a.by_row ? g.B * a.rows : num_sms();
+  const size_t rec = ad_record<D, 8 * NT>(), n = num_sms();
+  a.cta_seg = static_cast<int32_t*>(g.ws);
+  a.warp_part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.ws) + (n * 2 * 4 + 255) / 256 * 256);
+  a.cta_part = a.warp_part + n * kAdWarps * rec;
+  auto kern = attn_decode_kernel<D, NT>;
+  cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
+  if (e != cudaSuccess) return e;
+  trace_pre(K_ATTN_DECODE, s);
+  e = launch_k(kern, dim3(a.nc), dim3(kAdWarps * 32), smem, s, true, a);
+  trace_post(K_ATTN_DECODE, s);
+  if (e != cudaSuccess || a.by_row) return e;
+  trace_pre(K_ATTN_COMBINE, s);
+  e = launch_k(attn_decode_combine_kernel<D, NT>, dim3(a.nc), dim3(256), 0, s, true, a);
+  trace_post(K_ATTN_COMBINE, s);
+  return e;
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t s) {
-  trace_pre(K_ATTN_DECODE, s);
-  const cudaError_t e = launch_k(a.c.D == 128 ? attn_decode_rows_kernel<128> : attn_decode_rows_kernel<64>,
-                                 dim3(a.B * a.H), dim3(256), 0, s, true, a);
-  trace_post(K_ATTN_DECODE, s);
-  return e;
+  const int nt = ad_tiles(a.H / a.c.Hkv);
+  if (a.c.D == 128) return nt == 1 ? launch_ad<128, 1>(a, s) : launch_ad<128, 2>(a, s);
+  return nt == 1 ? launch_ad<64, 1>(a, s) : launch_ad<64, 2>(a, s);
 }
 
 int status_attn_decode(int clear) { return tu_status(clear); }
