@@ -416,7 +416,8 @@ int m2_attn_prefill_varlen(const uint16_t* q, int32_t ld_q, const uint16_t* k, i
  *           256-byte aligned, scratch.
  * The cache is read once for all H / Hkv query heads of a kv head (up to 16 of
  * them at a time).  Nothing depends on host copies of the lengths: a captured
- * step can be replayed while kv_len grows. */
+ * step can be replayed while kv_len grows.  nseq * ld_table * H is at most
+ * 2^31 - 1 (M2_ERR_UNSUPPORTED otherwise). */
 size_t m2_attn_decode_kv4_workspace_bytes(int32_t nseq, int32_t H, int32_t Hkv, int32_t head_dim);
 int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q, uint16_t* out, int32_t ld_o,
                        int32_t H, const int32_t* kv_len, float scale, void* ws, size_t ws_bytes, cudaStream_t stream);

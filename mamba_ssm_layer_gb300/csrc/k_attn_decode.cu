@@ -24,12 +24,12 @@
 
 namespace m2 {
 
-constexpr int kAdWarps = 8;
+constexpr int kAdWarps = 12;
 
 template <int D>
 struct AdCfg {
   static constexpr int kUnit = Kv4Block<D>::kBytes;
-  static constexpr int kStages = D == 128 ? 3 : 6;  // 8 warps * stages * unit = 216 KB
+  static constexpr int kStages = D == 128 ? 2 : 4;  // 12 warps * stages * unit = 216 KB
   static constexpr int kRing = kStages * kUnit;     // of one warp
   static constexpr int kStride = D + 4;             // floats between the heads of a record: no bank conflicts
 };
@@ -38,6 +38,7 @@ template <int D, int HN>
 constexpr int ad_record() {
   return 2 * HN + HN * AdCfg<D>::kStride;
 }
+constexpr int kAdParts = 2 * kAdWarps;  // a warp leaves a first and a last part at most
 // Which row (sequence, head chunk) a partial belongs to, and whether the row
 // starts before / ends after the CTA's span.
 struct AdMeta {
@@ -46,11 +47,15 @@ struct AdMeta {
 struct AdShared {
   uint64_t full[kAdWarps][6];
   int32_t ok[kAdWarps][6];
-  AdMeta meta[kAdWarps][2];
-  int64_t scan[kAdWarps];
-  int64_t run0[kAdWarps + 1];           // first unit of each warp's run, then the span's end
+  AdMeta meta[kAdParts];
+  float part_m[kAdParts][16], part_l[kAdParts][16];  // the parts' maxima (then their weights) and sums
+  float row_l[kAdParts][16];                         // sums of the cut rows
+  uint32_t row_parts[kAdParts];                      // their parts, as bits
+  int32_t cta_seg[2];
+  int32_t scan[kAdWarps];
+  int32_t run0[kAdWarps + 1];           // first unit of each warp's run, then the span's end
   int32_t run_b[kAdWarps];              // sequence of the run's first unit
-  int64_t run_base[kAdWarps];           // units before that sequence
+  int32_t run_base[kAdWarps];           // units before that sequence
 };
 
 struct AdArgs {
@@ -58,7 +63,7 @@ struct AdArgs {
   int32_t G, chunks, rows;  // query heads a kv head; chunks of HN heads; rows = Hkv * chunks a sequence
   int32_t nc;               // CTAs
   int32_t by_row;           // one CTA a row: no row is cut
-  float* warp_part;         // [nc][8] records
+  float* warp_part;         // [nc][kAdWarps] records
   float* cta_part;          // [nc][2] records: a row that began earlier, a row that goes on
   int32_t* cta_seg;         // [nc][2] rows of those, -1 where there is none
 };
@@ -78,12 +83,36 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+      "%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t dup_lo(uint32_t a) { return __byte_perm(a, a, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t a) { return __byte_perm(a, a, 0x3232); }
+// a times one half of s: the instruction broadcasts it.
+__device__ __forceinline__ uint32_t hmul2_lo(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __low2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmul2_hi(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The four bytes of a code word as f16x2.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t trans8x8(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -146,13 +175,15 @@ struct AdRow {
       // 2^-e for a largest magnitude of 2^e ..: exact in f16 except far below the largest
       int e = (int)(__float_as_uint(top) >> 23);
       e = e == 255 ? 127 : max(1, min(e, 253));
-      const float f = __uint_as_float((uint32_t)(254 - e) << 23), u = __uint_as_float((uint32_t)e << 23);
+      // the factor's sign goes into the queries, and a factor of 0 makes them 0: qs > 0
+      const float sc = a.g.scale * 1.4426950408889634f, u = __uint_as_float((uint32_t)e << 23);
+      const float f = sc == 0.0f ? 0.0f : copysignf(__uint_as_float((uint32_t)(254 - e) << 23), sc);
 #pragma unroll
       for (int g = 0; g < D / 16; ++g) {
         q[t][g][0] = pack_f16x2(bf16lo(w[g].x) * f, bf16hi(w[g].x) * f);
         q[t][g][1] = pack_f16x2(bf16lo(w[g].y) * f, bf16hi(w[g].y) * f);
       }
-      const float k = u * (a.g.scale * 1.4426950408889634f);
+      const float k = sc == 0.0f ? 1.0f : fmaxf(u * fabsf(sc), 1.17549435e-38f);
       qs[t][0] = __shfl_sync(0xffffffffu, k, 8 * c);
       qs[t][1] = __shfl_sync(0xffffffffu, k, 8 * c + 4);
 #pragma unroll
@@ -179,47 +210,51 @@ struct AdRow {
       lds_words<GW / 2>(u + L::kKs + t0 * (D / 16), s0);
       lds_words<GW / 2>(u + L::kKs + (t0 + 8) * (D / 16), s1);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[mt][t][j] = 0.0f;
-#pragma unroll
       for (int w = 0; w < GW; ++w) {
         // scale word w / 2 holds groups 4(w/2) .. + 3: this code word's are (0, 1) or (2, 3) of them
         const uint32_t e0 = scales02(s0[w / 2], kScaleBits), f0 = scales13(s0[w / 2], kScaleBits);
         const uint32_t e1 = scales02(s1[w / 2], kScaleBits), f1 = scales13(s1[w / 2], kScaleBits);
-        const uint32_t g00 = w & 1 ? dup_hi(e0) : dup_lo(e0), g01 = w & 1 ? dup_hi(f0) : dup_lo(f0);
-        const uint32_t g10 = w & 1 ? dup_hi(e1) : dup_lo(e1), g11 = w & 1 ? dup_hi(f1) : dup_lo(f1);
-        const uint32_t a0 = hmul2(kv4_f16x2(k0[w]), g00), a2 = hmul2(kv4_f16x2(k0[w] >> 8), g00);
-        const uint32_t a1 = hmul2(kv4_f16x2(k1[w]), g10), a3 = hmul2(kv4_f16x2(k1[w] >> 8), g10);
-        const uint32_t b0 = hmul2(kv4_f16x2(k0[w] >> 16), g01), b2 = hmul2(kv4_f16x2(k0[w] >> 24), g01);
-        const uint32_t b1 = hmul2(kv4_f16x2(k1[w] >> 16), g11), b3 = hmul2(kv4_f16x2(k1[w] >> 24), g11);
+        uint32_t x[4], y[4];
+        codes4(k0[w], x);
+        codes4(k1[w], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t sx = i < 2 ? e0 : f0, sy = i < 2 ? e1 : f1;
+          x[i] = w & 1 ? hmul2_hi(x[i], sx) : hmul2_lo(x[i], sx);
+          y[i] = w & 1 ? hmul2_hi(y[i], sy) : hmul2_lo(y[i], sy);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_f16(s[mt][t], a0, a1, a2, a3, q[t][2 * w][0], q[t][2 * w][1]);
-          mma_f16(s[mt][t], b0, b1, b2, b3, q[t][2 * w + 1][0], q[t][2 * w + 1][1]);
+          if (w == 0)
+            mma_f16_first(s[mt][t], x[0], y[0], x[1], y[1], q[t][0][0], q[t][0][1]);
+          else
+            mma_f16(s[mt][t], x[0], y[0], x[1], y[1], q[t][2 * w][0], q[t][2 * w][1]);
+          mma_f16(s[mt][t], x[2], y[2], x[3], y[3], q[t][2 * w + 1][0], q[t][2 * w + 1][1]);
         }
       }
     }
-    // softmax: P as the second product's B operand
+    // softmax: P as the second product's B operand.  qs > 0: maxima are taken before it is applied.
+    if (seen < kPage) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (16 * mt + r + (j & 2) * 4 >= seen)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[mt][t][j] = -INFINITY;
+    }
     uint32_t p[4][NT][2];
     bool grow = false;
     float mx[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      mx[t][0] = mx[t][1] = -INFINITY;
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[mt][t][j] *= qs[t][j & 1];
-          if (seen < kPage && 16 * mt + r + (j & 2) * 4 >= seen) s[mt][t][j] = -INFINITY;
-          mx[t][j & 1] = fmaxf(mx[t][j & 1], s[mt][t][j]);
-        }
-      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        mx[t][i] = fmaxf(fmaxf(fmaxf(s[0][t][i], s[0][t][i + 2]), fmaxf(s[1][t][i], s[1][t][i + 2])),
+                         fmaxf(fmaxf(s[2][t][i], s[2][t][i + 2]), fmaxf(s[3][t][i], s[3][t][i + 2])));
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx[t][i] = fmaxf(mx[t][i], __shfl_xor_sync(0xffffffffu, mx[t][i], x));
+        mx[t][i] *= qs[t][i];
         grow |= mx[t][i] - m[t][i] > 8.0f;
       }
     }
@@ -247,8 +282,8 @@ struct AdRow {
       const float b0 = m[t][0] == -INFINITY ? 0.0f : 7.0f - m[t][0], b1 = m[t][1] == -INFINITY ? 0.0f : 7.0f - m[t][1];
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        const float x0 = ad_ex2(s[mt][t][0] + b0), x1 = ad_ex2(s[mt][t][1] + b1);
-        const float x2 = ad_ex2(s[mt][t][2] + b0), x3 = ad_ex2(s[mt][t][3] + b1);
+        const float x0 = ad_ex2(fmaf(s[mt][t][0], qs[t][0], b0)), x1 = ad_ex2(fmaf(s[mt][t][1], qs[t][1], b1));
+        const float x2 = ad_ex2(fmaf(s[mt][t][2], qs[t][0], b0)), x3 = ad_ex2(fmaf(s[mt][t][3], qs[t][1], b1));
         l[t][0] += x0 + x2;
         l[t][1] += x1 + x3;
         p[mt][t][0] = trans8x8(pack_f16x2(x0, x1));
@@ -273,14 +308,18 @@ struct AdRow {
       for (int w = 0; w < GW; ++w) {
         const uint32_t e0 = scales02(s0[w], m0), e1 = scales02(s1[w], m1);
         const uint32_t f0 = scales13(s0[w], m0), f1 = scales13(s1[w], m1);
-        const uint32_t a0 = hmul2(kv4_f16x2(v0[w]), e0), a1 = hmul2(kv4_f16x2(v0[w] >> 8), e0);
-        const uint32_t a2 = hmul2(kv4_f16x2(v1[w]), e1), a3 = hmul2(kv4_f16x2(v1[w] >> 8), e1);
-        const uint32_t b0 = hmul2(kv4_f16x2(v0[w] >> 16), f0), b1 = hmul2(kv4_f16x2(v0[w] >> 24), f0);
-        const uint32_t b2 = hmul2(kv4_f16x2(v1[w] >> 16), f1), b3 = hmul2(kv4_f16x2(v1[w] >> 24), f1);
+        uint32_t x[4], y[4];
+        codes4(v0[w], x);
+        codes4(v1[w], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = hmul2(x[i], i < 2 ? e0 : f0);
+          y[i] = hmul2(y[i], i < 2 ? e1 : f1);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_f16(o[t][2 * w], a0, a1, a2, a3, p[ks][t][0], p[ks][t][1]);
-          mma_f16(o[t][2 * w + 1], b0, b1, b2, b3, p[ks][t][0], p[ks][t][1]);
+          mma_f16(o[t][2 * w], x[0], x[1], y[0], y[1], p[ks][t][0], p[ks][t][1]);
+          mma_f16(o[t][2 * w + 1], x[2], x[3], y[2], y[3], p[ks][t][0], p[ks][t][1]);
         }
       }
     }
@@ -295,17 +334,16 @@ struct AdRow {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
   }
-  __device__ __forceinline__ void store_record(float* rec, int lane) const {
-    constexpr int HN = 8 * NT;
+  __device__ __forceinline__ void store_part(float* out, float* pm, float* pl, int lane) const {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int h = 8 * t + 2 * c;
       if (r == 0) {
-        rec[h] = m[t][0], rec[h + 1] = m[t][1];
-        rec[HN + h] = l[t][0], rec[HN + h + 1] = l[t][1];
+        pm[h] = m[t][0], pm[h + 1] = m[t][1];
+        pl[h] = l[t][0], pl[h + 1] = l[t][1];
       }
-      float* d0 = rec + 2 * HN + h * AdCfg<D>::kStride + r;
+      float* d0 = out + h * AdCfg<D>::kStride + r;
       float* d1 = d0 + AdCfg<D>::kStride;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -353,61 +391,54 @@ struct AdCursor {
   }
 };
 
-// Joins `members` records of one row: `at(i)` gives the i-th.  Writes the output
-// (rec null) or another record.
-template <int D, int NT, typename At>
-__device__ __forceinline__ void ad_join(const AdArgs& a, int members, At at, int seg, float* rec) {
-  constexpr int HN = 8 * NT;
-  const int b = seg / a.rows, row = seg - b * a.rows, hk = row / a.chunks, ch = row - hk * a.chunks;
-  for (int i = threadIdx.x; i < HN * D; i += blockDim.x) {
-    const int h = i / D, d = i - h * D, head = ch * HN + h;
-    if (head >= a.G) break;
-    float m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int k = 0; k < members; ++k) m = fmaxf(m, at(k)[h]);
-    for (int k = 0; k < members; ++k) {
-      const float* p = at(k);
-      const float f = p[h] == -INFINITY ? (p[HN + h] == 0.0f ? 0.0f : 1.0f) : ad_ex2(p[h] - m);
-      l += p[HN + h] * f;
-      o += p[2 * HN + h * AdCfg<D>::kStride + d] * f;
-    }
-    if (rec) {
-      if (d == 0) rec[h] = m, rec[HN + h] = l;
-      rec[2 * HN + h * AdCfg<D>::kStride + d] = o;
-    } else {
-      a.g.out[(size_t)b * a.g.ld_o + (size_t)(hk * a.G + head) * D + d] = f32_to_bf16(l != 0.0f ? o / l : 0.0f);
-    }
-  }
+// A part's weight against the joined maximum; a part that saw nothing has none
+// (its sum is 0), and one of NaN scores passes its NaN on.
+__device__ __forceinline__ float ad_weight(float m, float l, float top) {
+  return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ad_ex2(m - top);
+}
+// Four channels of a row's output.
+__device__ __forceinline__ void ad_store4(const AdArgs& a, int seg, int hn, int h, int d, int D, float4 o, float l) {
+  const int b = seg / a.rows, row = seg - b * a.rows, hk = row / a.chunks, head = (row - hk * a.chunks) * hn + h;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
+  *reinterpret_cast<uint2*>(a.g.out + (size_t)b * a.g.ld_o + (size_t)(hk * a.G + head) * D + d) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+// Heads of a row that exist.
+__device__ __forceinline__ int ad_heads(const AdArgs& a, int seg, int hn) {
+  return min(hn, a.G - (seg % a.rows) % a.chunks * hn);
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdArgs a) {
   using C = AdCfg<D>;
-  constexpr int S = C::kStages, REC = ad_record<D, 8 * NT>();
-  static_assert(REC * 4 <= C::kRing, "a record lies in its warp's ring");
+  constexpr int S = C::kStages, HN = 8 * NT, REC = ad_record<D, HN>();
+  static_assert(kAdParts * HN <= kAdWarps * 32 && kAdParts <= 32, "a thread per part and head, a lane per part");
+  static_assert(REC * 4 <= C::kRing && S <= 6, "a record lies in its warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
   AdShared* sh = reinterpret_cast<AdShared*>(smem + kAdWarps * C::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   if (lane == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&sh->full[warp][s], 1);
-    sh->meta[warp][0].seg = sh->meta[warp][1].seg = -1;
+    sh->meta[2 * warp].seg = sh->meta[2 * warp + 1].seg = -1;
     fence_mbar_init();
   }
+  if (tid < 2) sh->cta_seg[tid] = -1;
   pdl_wait();
   pdl_trigger();
   const int B = a.g.B;
-  // ---- the span and its runs: prefix sums of the sequences' units
+  // ---- the span and its runs: prefix sums of the sequences' units (the host made sure that 32 bits hold them)
   const int per = (B + kAdWarps * 32 - 1) / (kAdWarps * 32), b0 = min(B, tid * per), b1 = min(B, b0 + per);
-  int64_t mine = 0;
+  int mine = 0;
   for (int b = b0; b < b1; ++b) mine += ad_pages(a.g, b);
-  int64_t pre = mine;
+  int pre = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+    const int v = __shfl_up_sync(0xffffffffu, pre, o);
     if (lane >= o) pre += v;
   }
   if (lane == 31) sh->scan[warp] = pre;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
   pre -= mine;
 #pragma unroll
   for (int w = 0; w < kAdWarps; ++w) {
@@ -416,13 +447,13 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
   }
   pre *= a.rows;
   total *= a.rows;
-  int64_t s0, s1;
-  if (a.by_row) {  // row cta of sequence cta / rows
+  int s0, s1;
+  if (a.by_row) {  // row cta % rows of sequence cta / rows
     const int b = cta / a.rows;
     if (tid == b / per) {
-      int64_t at = pre;
-      for (int k = b0; k < b; ++k) at += (int64_t)ad_pages(a.g, k) * a.rows;
-      const int64_t n = ad_pages(a.g, b);
+      int at = pre;
+      for (int k = b0; k < b; ++k) at += ad_pages(a.g, k) * a.rows;
+      const int n = ad_pages(a.g, b);
       sh->run0[0] = at + (cta - b * a.rows) * n;
       sh->run0[1] = sh->run0[0] + n;
     }
@@ -432,20 +463,24 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
     __syncthreads();
   } else {
     // at least a unit for every warp: the CTAs without work are the last ones
-    const int64_t nc = min((int64_t)a.nc, (total + kAdWarps - 1) / kAdWarps);
-    s0 = cta < nc ? total * cta / nc : total;
-    s1 = cta < nc ? total * (cta + 1) / nc : total;
+    const int nc = min(a.nc, (total + kAdWarps - 1) / kAdWarps), q = nc ? total / nc : 0, extra = total - q * nc;
+    s0 = cta < nc ? q * cta + min(cta, extra) : total;
+    s1 = cta < nc ? s0 + q + (cta < extra ? 1 : 0) : total;
   }
-  if (tid <= kAdWarps) sh->run0[tid] = s0 + (s1 - s0) * tid / kAdWarps;
-  __syncthreads();
   {
-    int64_t at = pre;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t n = (int64_t)ad_pages(a.g, b) * a.rows;
-      for (int w = 0; w < kAdWarps; ++w)
-        if (sh->run0[w] >= at && sh->run0[w] < at + n) {
-          sh->run_b[w] = b;
-          sh->run_base[w] = at;
+    // run w: its share of the span, the first ones a unit longer
+    const int q = (s1 - s0) / kAdWarps, extra = s1 - s0 - q * kAdWarps;
+    if (tid <= kAdWarps) sh->run0[tid] = s0 + q * tid + min(tid, extra);
+    int at = pre;
+    for (int b = b0; b < b1 && at < s1; ++b) {
+      const int n = ad_pages(a.g, b) * a.rows;
+      if (at + n > s0)
+        for (int w = 0; w < kAdWarps; ++w) {
+          const int u = s0 + q * w + min(w, extra);
+          if (u >= at && u < at + n) {
+            sh->run_b[w] = b;
+            sh->run_base[w] = at;
+          }
         }
       at += n;
     }
@@ -459,15 +494,14 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
 
   // ---- this warp's run
   uint8_t* ring = smem + warp * C::kRing;
-  const int64_t u0 = sh->run0[warp], u1 = sh->run0[warp + 1];
-  const int n = (int)(u1 - u0);
+  const int u0 = sh->run0[warp], u1 = sh->run0[warp + 1], n = u1 - u0;
   if (n > 0) {
     AdCursor cur;
     cur.b = sh->run_b[warp];
     cur.load(a);
-    const int64_t in = u0 - sh->run_base[warp];
-    cur.row = (int)(in / cur.pages);
-    cur.page = (int)(in - (int64_t)cur.row * cur.pages);
+    const int in = u0 - sh->run_base[warp];
+    cur.row = in / cur.pages;
+    cur.page = in - cur.row * cur.pages;
     AdCursor ahead = cur;
     const uint64_t pol = a.chunks > 1 ? policy_evict_normal() : policy_evict_first();
     auto fetch = [&](int i) {  // unit i of the run into its stage
@@ -492,7 +526,7 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
     AdRow<D, NT> row;
     row.start(a, cur.b, cur.row, lane);
     int first_page = cur.page;  // of the row's part in this run
-    int64_t row_at = u0 - cur.page;  // the row's first unit
+    int row_at = u0 - cur.page;      // the row's first unit
     bool dead = false;
     for (int i = 0; i < n; ++i) {
       const int st = i % S;
@@ -511,10 +545,10 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
         } else {
           const int slot = i + 1 == n ? 1 : 0;
           // the last part goes into the ring (free by now), an earlier one through L2
-          row.store_record(slot ? reinterpret_cast<float*>(ring) : a.warp_part + (size_t)(cta * kAdWarps + warp) * REC,
-                           lane);
+          row.store_part(slot ? reinterpret_cast<float*>(ring) : a.warp_part + (size_t)(cta * kAdWarps + warp) * REC,
+                         sh->part_m[2 * warp + slot], sh->part_l[2 * warp + slot], lane);
           if (lane == 0) {
-            AdMeta& mt = sh->meta[warp][slot];
+            AdMeta& mt = sh->meta[2 * warp + slot];
             mt.seg = cur.b * a.rows + cur.row;
             mt.before = row_at < s0;
             mt.after = row_at + cur.pages > s1;
@@ -538,59 +572,143 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
   __syncthreads();
 
   // ---- rows cut between warps
-  int32_t seg_first = -1, seg_last = -1;
-  for (int e = 0; e < 2 * kAdWarps;) {
-    const AdMeta& mt = sh->meta[e >> 1][e & 1];
-    if (mt.seg < 0) {
-      ++e;
-      continue;
+  const int seg_e = lane < kAdParts ? sh->meta[lane].seg : -1;
+  const uint32_t same = __match_any_sync(0xffffffffu, seg_e);  // entry `lane`: all parts of its row
+  const uint32_t lead = __ballot_sync(0xffffffffu, seg_e >= 0 && (same & ((1u << lane) - 1)) == 0);
+  const int nrows = __popc(lead);
+  {
+    // a thread per (part, head): those of a row's first part weigh its parts
+    const int e = tid / HN, h = tid - e * HN;
+    const uint32_t parts = __shfl_sync(0xffffffffu, same, e & 31);
+    if (e < kAdParts && (lead >> e & 1)) {
+      float top = -INFINITY, l = 0.0f;
+      for (uint32_t y = parts; y; y &= y - 1) top = fmaxf(top, sh->part_m[__ffs(y) - 1][h]);
+      for (uint32_t y = parts; y; y &= y - 1) {
+        const int x = __ffs(y) - 1;
+        const float w = ad_weight(sh->part_m[x][h], sh->part_l[x][h], top);
+        l += sh->part_l[x][h] * w;
+        sh->part_m[x][h] = w;
+      }
+      const int k = __popc(lead & ((1u << e) - 1));
+      sh->row_l[k][h] = l;
+      sh->row_parts[k] = parts;
+      const AdMeta& mt = sh->meta[e];
+      if (mt.before || mt.after) {  // cut between CTAs too
+        float* rec = a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * REC;
+        rec[h] = top;
+        rec[HN + h] = l;
+        if (h == 0) sh->cta_seg[mt.before ? 0 : 1] = mt.seg;
+      }
     }
-    // members: the entries from e on with this row; a row passes from a warp's last part to the next warp's
-    // first or only one, and warps without work lie at the end or hold nothing
-    int list[kAdWarps + 1], k = 0;
-    int x = e;
-    for (; x < 2 * kAdWarps; ++x) {
-      const int sg = sh->meta[x >> 1][x & 1].seg;
-      if (sg < 0) continue;
-      if (sg != mt.seg) break;
-      if (k <= kAdWarps) list[k++] = x;
-    }
-    auto at = [&](int i) -> const float* {
-      const int y = list[i];
-      return y & 1 ? reinterpret_cast<const float*>(smem + (y >> 1) * C::kRing)
-                   : a.warp_part + (size_t)(cta * kAdWarps + (y >> 1)) * REC;
-    };
-    float* rec = nullptr;
-    if (mt.before) {
-      rec = a.cta_part + (size_t)(2 * cta) * REC;
-      seg_first = mt.seg;
-    } else if (mt.after) {
-      rec = a.cta_part + (size_t)(2 * cta + 1) * REC;
-      seg_last = mt.seg;
-    }
-    ad_join<D, NT>(a, k, at, mt.seg, rec);
-    e = x;
   }
-  if (tid == 0 && !a.by_row) {
-    a.cta_seg[2 * cta] = seg_first;
-    a.cta_seg[2 * cta + 1] = seg_last;
+  __syncthreads();
+  for (int i = tid; i < nrows * (HN * D / 4); i += kAdWarps * 32) {
+    const int k = i / (HN * D / 4), h = i / (D / 4) % HN, d = i % (D / 4) * 4;
+    uint32_t parts = sh->row_parts[k];
+    const AdMeta& mt = sh->meta[__ffs(parts) - 1];
+    if (h >= ad_heads(a, mt.seg, HN)) continue;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    while (parts) {
+      // four parts at a time, their loads together
+      float4 v[4];
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = parts ? __ffs(parts) - 1 : -1;
+        parts &= parts - 1;
+        w[j] = 0.0f;
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (x >= 0) {
+          w[j] = sh->part_m[x][h];
+          v[j] = x & 1 ? *reinterpret_cast<const float4*>(smem + (x >> 1) * C::kRing + (h * C::kStride + d) * 4)
+                       : *reinterpret_cast<const float4*>(a.warp_part + (size_t)(cta * kAdWarps + (x >> 1)) * REC +
+                                                          h * C::kStride + d);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o.x = fmaf(v[j].x, w[j], o.x), o.y = fmaf(v[j].y, w[j], o.y), o.z = fmaf(v[j].z, w[j], o.z),
+        o.w = fmaf(v[j].w, w[j], o.w);
+    }
+    if (mt.before || mt.after)
+      *reinterpret_cast<float4*>(a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * REC + 2 * HN + h * C::kStride +
+                                 d) = o;
+    else
+      ad_store4(a, mt.seg, HN, h, d, D, o, sh->row_l[k][h]);
   }
+  if (tid < 2 && !a.by_row) a.cta_seg[2 * cta + tid] = sh->cta_seg[tid];
 }
 
 // Rows cut between CTAs: CTA c joins the row that began in span c and goes on.
+// A thread holds four channels of a head; the parts are dealt out over thread
+// groups, so that each loads its few parts at once, and joined through shared
+// memory.
+constexpr int kAcThreads = 1024;
 template <int D, int NT>
-__global__ void __launch_bounds__(256) attn_decode_combine_kernel(const AdArgs a) {
-  constexpr int REC = ad_record<D, 8 * NT>();
+__global__ void __launch_bounds__(kAcThreads) attn_decode_combine_kernel(const AdArgs a) {
+  constexpr int HN = 8 * NT, REC = ad_record<D, HN>(), ST = AdCfg<D>::kStride;
+  struct Sum {
+    float m, l;
+    float4 o;
+  };
+  __shared__ Sum part[kAcThreads];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x, seg = a.cta_seg[2 * c + 1];
+  const int c = blockIdx.x, tid = threadIdx.x;
+  const int seg = a.cta_seg[2 * c + 1];
+  int k = 1;  // parts: this span's, then those of the spans that the row goes on through
+  for (int x = c + 1; x < a.nc; x += kAcThreads) {
+    const int n = __syncthreads_count(x + tid < a.nc && a.cta_seg[2 * (x + tid)] == seg);
+    k += n;
+    if (n < kAcThreads) break;
+  }
   if (seg < 0) return;
-  int k = 1;
-  while (c + k < a.nc && a.cta_seg[2 * (c + k)] == seg) ++k;
-  ad_join<D, NT>(
-      a, k,
-      [&](int i) -> const float* { return a.cta_part + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * REC; }, seg,
-      nullptr);
+  const int pos = ad_heads(a, seg, HN) * (D / 4), groups = min(16, kAcThreads / pos), g = tid / pos, i = tid - g * pos;
+  const int h = i / (D / 4), d = i % (D / 4) * 4;
+  Sum s;
+  s.m = -INFINITY, s.l = 0.0f, s.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (g < groups) {
+    for (int y0 = g; y0 < k; y0 += 4 * groups) {
+      Sum v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int y = y0 + j * groups;
+        v[j].m = -INFINITY, v[j].l = 0.0f, v[j].o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (y < k) {
+          const float* r = a.cta_part + (size_t)(y == 0 ? 2 * c + 1 : 2 * (c + y)) * REC;
+          v[j].m = r[h], v[j].l = r[HN + h];
+          v[j].o = *reinterpret_cast<const float4*>(r + 2 * HN + h * ST + d);
+        }
+      }
+      const float top = fmaxf(fmaxf(fmaxf(s.m, v[0].m), fmaxf(v[1].m, v[2].m)), v[3].m);
+      const float f = ad_weight(s.m, s.l, top);
+      s.m = top;
+      s.l *= f, s.o.x *= f, s.o.y *= f, s.o.z *= f, s.o.w *= f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = ad_weight(v[j].m, v[j].l, top);
+        s.l = fmaf(v[j].l, w, s.l);
+        s.o.x = fmaf(v[j].o.x, w, s.o.x), s.o.y = fmaf(v[j].o.y, w, s.o.y), s.o.z = fmaf(v[j].o.z, w, s.o.z),
+        s.o.w = fmaf(v[j].o.w, w, s.o.w);
+      }
+    }
+    part[tid] = s;
+  }
+  __syncthreads();
+  if (g == 0) {
+    float top = s.m;
+    for (int y = 1; y < groups; ++y) top = fmaxf(top, part[y * pos + i].m);
+    Sum t;
+    t.l = 0.0f, t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int y = 0; y < groups; ++y) {
+      const Sum& v = part[y * pos + i];
+      const float w = ad_weight(v.m, v.l, top);
+      t.l = fmaf(v.l, w, t.l);
+      t.o.x = fmaf(v.o.x, w, t.o.x), t.o.y = fmaf(v.o.y, w, t.o.y), t.o.z = fmaf(v.o.z, w, t.o.z),
+      t.o.w = fmaf(v.o.w, w, t.o.w);
+    }
+    ad_store4(a, seg, HN, h, d, D, t.o, t.l);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -629,7 +747,7 @@ static cudaError_t launch_ad(const AttnDecodeArgs& g, cudaStream_t s) {
   trace_post(K_ATTN_DECODE, s);
   if (e != cudaSuccess || a.by_row) return e;
   trace_pre(K_ATTN_COMBINE, s);
-  e = launch_k(attn_decode_combine_kernel<D, NT>, dim3(a.nc), dim3(256), 0, s, true, a);
+  e = launch_k(attn_decode_combine_kernel<D, NT>, dim3(a.nc), dim3(kAcThreads), 0, s, true, a);
   trace_post(K_ATTN_COMBINE, s);
   return e;
 }

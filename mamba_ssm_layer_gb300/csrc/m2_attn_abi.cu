@@ -212,7 +212,7 @@ int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_
   if ((st = check_cache(cache))) return st;
   if ((st = check_heads(H, cache->n_kv_heads, cache->head_dim))) return st;
   if (!kv_len || !isfinite(scale)) return M2_ERR_ARG;
-  if ((int64_t)cache->nseq * H > INT32_MAX) return M2_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+  if ((int64_t)cache->nseq * cache->ld_table > INT32_MAX / H) return M2_ERR_UNSUPPORTED;  // counted in 32 bits
   const int32_t w = H * cache->head_dim;
   if ((st = check_rows(q, ld_q, w)) || (st = check_rows(out, ld_o, w))) return st;
   if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return M2_ERR_ALIGN;
