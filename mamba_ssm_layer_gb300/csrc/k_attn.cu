@@ -10,13 +10,17 @@
 // m is the row's reference maximum.  It follows the running maximum only when
 // that has grown by more than 2^8 in the exponential: until then P stays below
 // 2^8, which bf16 and fp32 hold as well, and O needs no rescaling.
+// CTAs are persistent: the copies and the first scores of a CTA's next item (a
+// tile pair of one head group) run under the last softmax and the output of the
+// current one.
 // Bound: the tensor cores (4 * 128 * 128 * D operations a tile pair) and the
 // exponentials (one a score); while one tile's scores are in the softmax
 // warps, the other tile's products run.
 //
 // Roles: warps 0-3 softmax and output of tile 0, warps 4-7 of tile 1, warp 8
-// issues the products, warp 9 the TMA copies; warps 10 and 11 only complete the
-// warpgroup that hands its registers to the softmax (a score row is 128 of them).
+// issues the products, warp 9 the TMA copies, warps 10 and 11 look through the
+// values of blocks that some row sees only in part.  Warps 8-11 hand registers
+// to the softmax (a score row is 128 of them).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -44,9 +48,13 @@ struct AtCfg {
   static constexpr uint32_t kTmS = 0, kTmO = 256;          // tensor-memory columns: S 2 x 128, O 2 x D
 };
 struct AtBars {
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], fin;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2], fin;
   uint64_t full[10], empty[10];
-  uint32_t bad[kAtMaskBlocks][4];  // keys of a masked block whose values are not finite
+  uint64_t look, clean;  // a masked block's values may be looked through; they are
+  // Keys of a masked block whose values are not finite: (item << 32) | bits, by the
+  // CTA's item.  A block is looked through after its first scores were issued, when
+  // the tiles have at most the output of the item before last ahead of them.
+  unsigned long long bad[4][kAtMaskBlocks * 4];
   uint32_t tmem;
 };
 template <int D>
@@ -64,18 +72,10 @@ struct AtArgs {
   int32_t gqa;      // H / Hkv
   float scale_log2; // scale * log2(e)
   int32_t nseq;
+  int32_t items;    // tile pairs * groups
   int32_t cu_q[kSeqs + 1], cu_k[kSeqs + 1];
   int32_t tile[kSeqs + 1];  // first tile pair of each sequence
 };
-
-// MN-major operand descriptor, 128-byte swizzle: 64 elements (128 bytes) of the
-// M/N dimension per row, rows along K; 8-row atoms 1024 bytes apart (stride
-// byte offset), the next 64 elements `lbo` bytes on (leading byte offset).
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-constexpr uint32_t kIdescBMn = 1u << 16;  // B is MN-major
 
 // 32 columns of this warp's 32 lanes, without waiting.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
@@ -101,6 +101,55 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Operands are 128-byte swizzled: Q and K K-major (leading offset unused: 1), V
+// MN-major (64 channels a row, rows along the keys; the next 64 channels at the
+// leading offset); 8-row atoms 1024 bytes apart (stride offset).
+// The products of one tile, operand addresses in units of 16 bytes: the
+// descriptors' upper words are constants, steps along K add to the lower ones.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t at_desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+template <int D>
+__device__ __forceinline__ void at_issue_scores(uint32_t d, uint32_t q, uint32_t k) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint32_t step = (i >> 2) * (kAtRows * 128 >> 4) + (i & 3) * 2;
+    tc_mma(d, at_desc((q + step) | (1u << 16)), at_desc((k + step) | (1u << 16)), tc_idesc(kAtRows, kAtRows), i > 0);
+  }
+}
+// 64 keys of O += P V; the values' second 64 channels lie kAtRows * 128 bytes on.
+template <int D>
+__device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t v, bool acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    tc_mma_ts(d, p + 8 * i, at_desc((v + i * (2048 >> 4)) | ((kAtRows * 128 >> 4) << 16)), tc_idesc(kAtRows, D) | (1u << 16),
+              acc || i > 0);
+}
+
+// Four lanes (aligned) with four pieces each: lane q's piece j becomes lane j's piece q.
+__device__ __forceinline__ void swap_pieces(uint4& lo, uint4& hi, int mask, bool up) {
+  uint4 s = up ? lo : hi;
+  s.x = __shfl_xor_sync(0xffffffffu, s.x, mask);
+  s.y = __shfl_xor_sync(0xffffffffu, s.y, mask);
+  s.z = __shfl_xor_sync(0xffffffffu, s.z, mask);
+  s.w = __shfl_xor_sync(0xffffffffu, s.w, mask);
+  if (up)
+    lo = s;
+  else
+    hi = s;
+}
+__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
+  swap_pieces(w[0], w[1], 1, lane & 1);
+  swap_pieces(w[2], w[3], 1, lane & 1);
+  swap_pieces(w[0], w[2], 2, lane & 2);
+  swap_pieces(w[1], w[3], 2, lane & 2);
+}
+
 // mbar_wait without a call: a kernel that hands registers between its warps
 // has to be one function.
 __device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
@@ -122,6 +171,13 @@ __device__ __forceinline__ bool at_drain(uint64_t* bar, uint32_t parity) {
   return mbar_test_wait(bar, parity) || at_wait_until(bar, parity, kWaitCycles);
 }
 
+// A CTA's k-th item: every other round backwards, so that each CTA gets late
+// (long) and early (short) tiles alike.
+__device__ __forceinline__ int at_pick(int k, int items) {
+  const int g = gridDim.x, id = k * g + (k & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+  return id < items ? id : -1;
+}
+
 // What a CTA works on.
 struct AtItem {
   int seq, hg;       // sequence; group of PK query heads
@@ -129,12 +185,12 @@ struct AtItem {
   int n0, n1;        // key blocks of each tile
   int jm;            // first key block that some row of tile 0 sees only in part
 };
-__device__ __forceinline__ AtItem at_item(const AtArgs& a) {
+__device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
   AtItem it;
   const int tokens = kAtRows >> a.pk_log;  // of one tile
   const int total = a.tile[a.nseq];
-  const int p = total - 1 - (int)(blockIdx.x / a.groups);  // late tiles (the most keys) first
-  it.hg = blockIdx.x % a.groups;
+  const int p = total - 1 - id / a.groups;  // late tiles (the most keys) first
+  it.hg = id % a.groups;
   int lo = 0, hi = a.nseq;  // the last sequence whose first pair is <= p
   while (hi - lo > 1) {
     const int m = (lo + hi) / 2;
@@ -163,7 +219,7 @@ __device__ __forceinline__ AtItem at_item(const AtArgs& a) {
 // zero in shared memory and their key is marked; rows that do see the key add
 // them at the end.
 template <int D>
-__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, uint32_t* bad) {
+__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long long* bad, uint32_t item) {
   bool any = false;
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
@@ -174,8 +230,14 @@ __device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, uint32_t* bad
       any |= (u[i] & 0x7F80u) == 0x7F80u || (u[i] & 0x7F800000u) == 0x7F800000u;
   }
   if (!any) return;
-  atomicOr(&bad[r >> 5], 1u << (r & 31));
-  __threadfence_block();  // marked before it is gone
+  unsigned long long old = bad[r >> 5];
+  for (;;) {
+    const unsigned long long want =
+        ((unsigned long long)item << 32) | (old >> 32 == item ? (uint32_t)old : 0u) | 1u << (r & 31);
+    const unsigned long long seen = atomicCAS(&bad[r >> 5], old, want);
+    if (seen == old) break;
+    old = seen;
+  }
   for (int c = 0; c < D / 8; ++c) {
     uint32_t* p = reinterpret_cast<uint32_t*>(tile + sw128_chunk(kAtRows, r, c));
     for (int i = 0; i < 4; ++i) {
@@ -200,16 +262,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->p_full[t][0], 4);
+      mbar_init(&bars->p_full[t][1], 4);
       mbar_init(&bars->o_done[t], 1);
     }
     mbar_init(&bars->fin, 1);
+    mbar_init(&bars->look, 1);
+    mbar_init(&bars->clean, 2);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
-    for (int i = 0; i < kAtMaskBlocks * 4; ++i) (&bars->bad[0][0])[i] = 0;
+    for (int i = 0; i < 4 * kAtMaskBlocks * 4; ++i) (&bars->bad[0][0])[i] = ~0ull;
     fence_mbar_init();
   }
   if (warp == 8) tmem_alloc(&bars->tmem, 512);
@@ -217,196 +283,260 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
-  const AtItem it = at_item(a);
-  const int n = max(it.n0, it.n1);
   const int tokens = kAtRows >> a.pk_log;
-  const int hk = (it.hg << a.pk_log) / a.gqa;
   pdl_wait();
   pdl_trigger();
 
+  // Every role walks the same items; a key block j of an item is copies kv + 2j
+  // (K) and kv + 2j + 1 (V) of the CTA, and barrier phases are counted through.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsOther));
     if (warp == 9 && lane == 0) {
       // ------------------------------------------------------ copies
       const uint64_t keep = policy_evict_normal();
-      int issued = 0, qs = 0;
-      const int h0 = it.hg << a.pk_log;
-      auto load_q = [&](int t) {
-        if (!(t ? it.n1 : it.n0)) return;
-        mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
-        for (int hf = 0; hf < HALVES; ++hf)
-          tma_load_3d(smem + C::kQ + t * C::kTile + hf * HB, &tmQ, hf * 64, h0, a.cu_q[it.seq] + it.q0 + t * tokens,
-                      &bars->q_full[t], keep);
-        qs |= 1 << t;
-      };
+      int kv = 0, nq0 = 0, nq1 = 0;  // copies and Q tiles issued
       bool dead = false;
-      load_q(0);
-      for (int i = 0; i < 2 * n && !dead; ++i) {
-        const int s = i % NS;
-        if (i >= NS && !at_wait(&bars->empty[s], ((i / NS) - 1) & 1)) {
-          dead = true;
-          break;
-        }
-        mbar_arrive_expect_tx(&bars->full[s], C::kTile);
-        const CUtensorMap* m = i & 1 ? &tmV : &tmK;
-        for (int hf = 0; hf < HALVES; ++hf)
-          tma_load_3d(smem + C::kKV + s * C::kTile + hf * HB, m, hf * 64, hk, a.cu_k[it.seq] + (i >> 1) * kAtRows,
-                      &bars->full[s], keep);
-        issued = i + 1;
-        if (i == 0) load_q(1);
-      }
-      // every copy this thread issued has landed
-      for (int t = 0; t < 2; ++t)
-        if (qs >> t & 1) at_drain(&bars->q_full[t], 0);
-      for (int i = max(0, issued - NS); i < issued; ++i)
-        if (!at_drain(&bars->full[i % NS], (i / NS) & 1)) break;
-    } else if (warp == 8 && lane == 0 && n > 0) {
-      // ------------------------------------------------------ products
-      constexpr uint32_t idS = tc_idesc(kAtRows, kAtRows), idO = tc_idesc(kAtRows, D) | kIdescBMn;
-      bool dead = false;
-      auto full = [&](int i) { return at_wait(&bars->full[i % NS], (i / NS) & 1); };
-      auto scores = [&](int t, int i) {  // S of tile t with K tile i
-        const uint32_t qb = smem_addr(smem + C::kQ + t * C::kTile), kb = smem_addr(smem + C::kKV + (i % NS) * C::kTile);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma(tmem + C::kTmS + t * kAtRows, sw128_desc(qb + (k >> 2) * HB + (k & 3) * 32),
-                 sw128_desc(kb + (k >> 2) * HB + (k & 3) * 32), idS, k > 0 ? 1 : 0);
-        tc_commit(&bars->s_full[t]);
-      };
-      dead = !full(0);
-      for (int t = 0; t < 2 && !dead; ++t) {
-        if (!(t ? it.n1 : it.n0)) continue;
-        if (!at_wait(&bars->q_full[t], 0)) {
-          dead = true;
-          break;
-        }
-        scores(t, 0);
-      }
-      if (!dead) tc_commit(&bars->empty[0]);
-      for (int j = 0; j < n && !dead; ++j) {
-        const int vi = 2 * j + 1, kn = 2 * j + 2;
-        const uint32_t vb = smem_addr(smem + C::kKV + (vi % NS) * C::kTile);
-        const int tl = j < it.n1 ? 1 : 0;  // the last tile that uses this block
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? it.n1 : it.n0;
-          if (j >= nt) continue;
-          if (!full(vi) || !at_wait(&bars->p_full[t], j & 1)) {
+      for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
+        const AtItem it = at_item(a, id);
+        const int n = max(it.n0, it.n1), h0 = it.hg << a.pk_log, hk = h0 / a.gqa;
+        auto load_q = [&](int t) {
+          if (!(t ? it.n1 : it.n0) || dead) return;
+          int& nq = t ? nq1 : nq0;
+          if (nq > 0 && !at_wait(&bars->q_empty[t], (nq - 1) & 1)) {
+            dead = true;
+            return;
+          }
+          mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_3d(smem + C::kQ + t * C::kTile + hf * HB, &tmQ, hf * 64, h0, a.cu_q[it.seq] + it.q0 + t * tokens,
+                        &bars->q_full[t], keep);
+          ++nq;
+        };
+        for (int i = 0; i < 2 * n && !dead; ++i, ++kv) {
+          const int s = kv % NS;
+          if (kv >= NS && !at_wait(&bars->empty[s], ((kv / NS) - 1) & 1)) {
             dead = true;
             break;
           }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < kAtRows / 16; ++k)
-            tc_mma_ts(tmem + C::kTmO + t * D, tmem + C::kTmS + t * kAtRows + k * 8, sw128_mn_desc(vb + k * 2048, HB), idO,
-                      j > 0 || k > 0 ? 1 : 0);
-          if (t == tl) tc_commit(&bars->empty[vi % NS]);
-          if (j + 1 == nt) {
-            tc_commit(&bars->o_done[t]);
-          } else {
-            if (!full(kn)) {
-              dead = true;
-              break;
-            }
-            scores(t, kn);
+          mbar_arrive_expect_tx(&bars->full[s], C::kTile);
+          const CUtensorMap* m = i & 1 ? &tmV : &tmK;
+          for (int hf = 0; hf < HALVES; ++hf)
+            tma_load_3d(smem + C::kKV + s * C::kTile + hf * HB, m, hf * 64, hk, a.cu_k[it.seq] + (i >> 1) * kAtRows,
+                        &bars->full[s], keep);
+          if (i == 0) {
+            load_q(0);
+            load_q(1);
           }
         }
-        if (!dead && j + 1 < n) tc_commit(&bars->empty[kn % NS]);
       }
-      tc_commit(&bars->fin);  // everything issued here is done before tensor memory is freed
-      at_drain(&bars->fin, 0);
+      // every copy this thread issued has landed
+      if (nq0) at_drain(&bars->q_full[0], (nq0 - 1) & 1);
+      if (nq1) at_drain(&bars->q_full[1], (nq1 - 1) & 1);
+      for (int i = max(0, kv - NS); i < kv; ++i)
+        if (!at_drain(&bars->full[i % NS], (i / NS) & 1)) break;
+    } else if (warp == 8) {
+      // ------------------------------------------------------ products
+      // The whole warp walks the blocks, so that addresses and descriptors stay
+      // warp-uniform; one elected lane issues.
+      const bool leader = elect_one();
+      int kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // copies, Q tiles and probability tiles used
+      int cleaned = 0;                             // masked blocks looked through
+      bool dead = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !__all_sync(0xffffffffu, at_wait(bar, parity));
+        return !dead;
+      };
+      auto full = [&](int i) { return wait(&bars->full[i % NS], (i / NS) & 1); };
+      const uint32_t q0 = (smem_addr(smem + C::kQ) & 0x3FFFFu) >> 4, kv0 = (smem_addr(smem + C::kKV) & 0x3FFFFu) >> 4;
+      // S of tile t with K copy i
+      auto scores = [&](int t, int i, bool last, bool look) {
+        if (!leader) return;
+        at_issue_scores<D>(tmem + C::kTmS + t * kAtRows, q0 + t * (C::kTile >> 4), kv0 + (i % NS) * (C::kTile >> 4));
+        tc_commit(&bars->s_full[t]);
+        if (last) tc_commit(&bars->q_empty[t]);  // the tile's last scores
+        if (look) mbar_arrive(&bars->look);
+      };
+      for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
+        const AtItem it = at_item(a, id);
+        const int n = max(it.n0, it.n1), lead = it.n0 ? 0 : 1;
+        if (n == 0) continue;
+        if (!full(kv)) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? it.n1 : it.n0;
+          if (!nt || !wait(&bars->q_full[t], nq[t] & 1)) continue;
+          ++nq[t];
+          scores(t, kv, nt == 1, it.jm == 0 && t == lead);
+        }
+        if (dead) break;
+        if (leader) tc_commit(&bars->empty[kv % NS]);
+        for (int j = 0; j < n && !dead; ++j) {
+          const int vi = kv + 2 * j + 1, kn = vi + 1;
+          if (!full(vi)) break;
+          if (j >= it.jm && !wait(&bars->clean, cleaned++ & 1)) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? it.n1 : it.n0;
+            if (j >= nt || dead) continue;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {  // the first 64 keys' probabilities come before the others'
+              if (!wait(&bars->p_full[t][hf], np[t] & 1)) break;
+              tc_fence_after();
+              if (leader)
+                at_issue_values<D>(tmem + C::kTmO + t * D, tmem + C::kTmS + t * kAtRows + 32 * hf,
+                                   kv0 + (vi % NS) * (C::kTile >> 4) + hf * (8192 >> 4), j > 0 || hf > 0);
+            }
+            if (dead) continue;
+            ++np[t];
+            if (leader) {
+              if (t == (j < it.n1 ? 1 : 0)) tc_commit(&bars->empty[vi % NS]);  // the last tile that uses this block
+              if (j + 1 == nt) tc_commit(&bars->o_done[t]);
+            }
+            if (j + 1 < nt && full(kn)) scores(t, kn, j + 2 == nt, j + 1 >= it.jm && t == (j + 1 < it.n0 ? 0 : 1));
+          }
+          if (!dead && j + 1 < n && leader) tc_commit(&bars->empty[kn % NS]);
+        }
+        kv += 2 * n;
+      }
+      if (leader) {
+        tc_commit(&bars->fin);  // everything issued here is done before tensor memory is freed
+        at_drain(&bars->fin, 0);
+      }
+    } else if (warp >= 10) {
+      // ------------------------------------------------------ values of masked blocks
+      // The products' warp calls for a block once it has issued the block's first
+      // scores: only then is the phase of the values' ring slot the block's own or
+      // the one before, and it stays so until the block is declared clean.
+      int kv = 0, looked = 0;
+      uint32_t item = 0;
+      bool dead = false;
+      for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
+        const AtItem it = at_item(a, id);
+        const int n = max(it.n0, it.n1);
+        if (n == 0) continue;
+        for (int j = it.jm; j < n; ++j) {
+          const int vi = kv + 2 * j + 1;
+          if (!__all_sync(0xffffffffu, at_wait(&bars->look, looked++ & 1) &&
+                                           at_wait(&bars->full[vi % NS], (vi / NS) & 1))) {
+            dead = true;
+            break;
+          }
+          for (int r = (warp - 10) * 32 + lane; r < kAtRows; r += 64)
+            at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[item & 3] + 4 * (j - it.jm), item);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->clean);
+        }
+        kv += 2 * n;
+        ++item;
+      }
     }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtRegsSoftmax));
     // -------------------------------------------------------- softmax and output
     const int t = warp >> 2, r = 32 * (warp & 3) + lane;
-    const int nt = t ? it.n1 : it.n0, first = it.q0 + t * tokens;
-    const int tok = first + (r >> a.pk_log), off = it.nk - it.nq;
-    const int limit = tok + off;                // the last key this row sees
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + C::kTmS + t * kAtRows, to = tmem + lanes + C::kTmO + t * D;
     const bool pos = a.scale_log2 > 0.0f;
     const float c = pos ? a.scale_log2 : 1.0f;  // a scale <= 0 is applied to the scores first
-    float m = -INFINITY, l = 0.0f;
+    int ns = 0, no = 0;                         // score tiles and outputs before this item
+    uint32_t item = 0;                          // items with keys before this one
     bool dead = false;
-    for (int j = 0; j < nt; ++j) {
-      if (j >= it.jm) {
-        const int vi = 2 * j + 1;
-        if (!__all_sync(0xffffffffu, at_wait(&bars->full[vi % NS], (vi / NS) & 1))) {
+    for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
+      const AtItem it = at_item(a, id);
+      const int nt = t ? it.n1 : it.n0, first = it.q0 + t * tokens;
+      const int tok = first + (r >> a.pk_log), off = it.nk - it.nq;
+      const int limit = tok + off;  // the last key this row sees
+      unsigned long long* bad = bars->bad[item & 3];
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < nt; ++j) {
+        if (!__all_sync(0xffffffffu, at_wait(&bars->s_full[t], (ns + j) & 1))) {
           dead = true;
           break;
         }
-        at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[j - it.jm]);
-        fence_proxy_async();
+        tc_fence_after();
+        float s[kAtRows];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, s + 32 * i);
+        tmem_ld_wait<kAtRows>(s);
+        if (!pos) {
+#pragma unroll
+          for (int i = 0; i < kAtRows; ++i) s[i] *= a.scale_log2;
+        }
+        if (j * kAtRows + kAtRows - 1 > first + off) {  // some row of the tile does not see the whole block
+          const int seen = limit - j * kAtRows;
+#pragma unroll
+          for (int i = 0; i < kAtRows; ++i) s[i] = i <= seen ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kAtRows; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        const float mn = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = mn;
+        } else {
+          const bool grow = (mn - m) * c > 8.0f;
+          if (__any_sync(0xffffffffu, grow)) {  // rescale what was summed so far (its products are complete)
+            const float f = grow ? ex2((m - mn) * c) : 1.0f;
+            if (grow) m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              uint32_t u[16];
+              tmem_ld16(to + i, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * f);
+              tmem_st16(to + i, u);
+            }
+          }
+        }
+        const float b = m == -INFINITY ? 0.0f : -m * c;  // nothing seen yet: every exponential is 0
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kAtRows; i += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float x = ex2(fmaf(s[i + 2 * k], c, b)), y = ex2(fmaf(s[i + 2 * k + 1], c, b));
+            sum[k & 3] += x + y;
+            p[k] = pack_bf16x2(x, y);
+          }
+          tmem_st16(ts + i / 2, p);
+          if (i % 64 == 32) {  // 64 keys' probabilities are there
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[t][i / 64]);
+          }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
-      if (!__all_sync(0xffffffffu, at_wait(&bars->s_full[t], j & 1))) {
+      if (dead) break;
+      if (nt > 0 && !__all_sync(0xffffffffu, at_wait(&bars->o_done[t], no & 1))) {
         dead = true;
         break;
       }
       tc_fence_after();
-      float s[kAtRows];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, s + 32 * i);
-      tmem_ld_wait<kAtRows>(s);
-      if (!pos) {
-#pragma unroll
-        for (int i = 0; i < kAtRows; ++i) s[i] *= a.scale_log2;
-      }
-      if (j * kAtRows + kAtRows - 1 > first + off) {  // some row of the tile does not see the whole block
-        const int seen = limit - j * kAtRows;
-#pragma unroll
-        for (int i = 0; i < kAtRows; ++i) s[i] = i <= seen ? s[i] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int i = 4; i < kAtRows; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-      const float mn = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
-      if (j == 0) {
-        m = mn;
-      } else {
-        const bool grow = (mn - m) * c > 8.0f;
-        if (__any_sync(0xffffffffu, grow)) {  // rescale what was summed so far (its products are complete)
-          const float f = grow ? ex2((m - mn) * c) : 1.0f;
-          if (grow) m = mn;
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < D; i += 16) {
-            float o[16];
-            uint32_t u[16];
-            tmem_ld16(to + i, o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * f);
-            tmem_st16(to + i, u);
-          }
-        }
-      }
-      const float b = m == -INFINITY ? 0.0f : -m * c;  // nothing seen yet: every exponential is 0
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < kAtRows; i += 32) {
-        uint32_t p[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float x = ex2(fmaf(s[i + 2 * k], c, b)), y = ex2(fmaf(s[i + 2 * k + 1], c, b));
-          sum[k & 3] += x + y;
-          p[k] = pack_bf16x2(x, y);
-        }
-        tmem_st16(ts + i / 2, p);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full[t]);
-    }
-    if (!dead && nt > 0) dead = !__all_sync(0xffffffffu, at_wait(&bars->o_done[t], 0));
-    if (!dead) {
-      tc_fence_after();
       const float inv = limit >= 0 ? 1.0f / l : 0.0f;
-      uint16_t* dst = a.out + (size_t)(a.cu_q[it.seq] + tok) * a.ld_o +
-                      (size_t)((it.hg << a.pk_log) + (r & ((1 << a.pk_log) - 1))) * D;
-      uint32_t marks = 0;
-      for (int i = 0; i < kAtMaskBlocks * 4; ++i) marks |= (&bars->bad[0][0])[i];
+      // Four neighbouring rows' lanes exchange 16-byte pieces, so that a store covers
+      // 64 bytes of a row: dst[i] is row (r & ~3) + i, piece r & 3.
+      uint16_t* dst[4];
+      {
+        const int hl = r & ((1 << a.pk_log) - 1);
+        const uint64_t mine = tok < it.nq ? reinterpret_cast<uint64_t>(a.out + (size_t)(a.cu_q[it.seq] + tok) * a.ld_o +
+                                                                       (size_t)((it.hg << a.pk_log) + hl) * D)
+                                          : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t p = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
+          dst[i] = p ? reinterpret_cast<uint16_t*>(p) + 8 * (lane & 3) : nullptr;
+        }
+      }
+      bool marks = false;
+      if (nt > 0)
+        for (int w = 0; w < kAtMaskBlocks * 4; ++w) marks |= (uint32_t)(bad[w] >> 32) == item;
 #pragma unroll
       for (int i = 0; i < D; i += 32) {
         float o[32];
@@ -417,10 +547,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (marks) {  // add the values that were kept out of the products, where they are seen
           for (int w = 0; w < kAtMaskBlocks * 4; ++w) {
             const int j = it.jm + (w >> 2);
-            for (uint32_t bits = j < nt ? (&bars->bad[0][0])[w] : 0; bits; bits &= bits - 1) {
+            const unsigned long long e = bad[w];
+            for (uint32_t bits = j < nt && (uint32_t)(e >> 32) == item ? (uint32_t)e : 0; bits; bits &= bits - 1) {
               const int key = j * kAtRows + (w & 3) * 32 + __ffs(bits) - 1;
               if (key > limit || tok >= it.nq) continue;
-              const uint16_t* vr = a.v + (size_t)(a.cu_k[it.seq] + key) * a.ld_v + (size_t)hk * D + i;
+              const uint16_t* vr = a.v + (size_t)(a.cu_k[it.seq] + key) * a.ld_v +
+                                   (size_t)((it.hg << a.pk_log) / a.gqa) * D + i;
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
                 const float x = bf16_to_f32(vr[k]);
@@ -429,17 +561,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
           }
         }
-        if (tok < it.nq) {
+        uint4 w[4];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (limit >= 0)
-              w = make_uint4(pack_bf16x2(o[k] * inv, o[k + 1] * inv), pack_bf16x2(o[k + 2] * inv, o[k + 3] * inv),
-                             pack_bf16x2(o[k + 4] * inv, o[k + 5] * inv), pack_bf16x2(o[k + 6] * inv, o[k + 7] * inv));
-            *reinterpret_cast<uint4*>(dst + i + k) = w;
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float* x = o + 8 * k;
+          w[k] = limit >= 0 ? make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                                         pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv))
+                            : make_uint4(0u, 0u, 0u, 0u);
         }
+        transpose4(w, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + i) = w[k];
       }
+      tc_fence_before();  // O is read before the next item's products, which wait for this warp's probabilities
+      ns += nt;
+      no += nt > 0 ? 1 : 0;
+      item += max(it.n0, it.n1) > 0 ? 1 : 0;
     }
   }
   tc_fence_before();
@@ -499,8 +637,9 @@ static cudaError_t launch_attn(const AttnArgs& g, cudaStream_t s) {
   constexpr int smem = at_smem_bytes<D>();
   cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
   if (e != cudaSuccess) return e;
+  a.items = a.tile[g.nseq] * a.groups;
   trace_pre(K_ATTN_PREFILL, s);
-  e = launch_k(kern, dim3((unsigned)a.tile[g.nseq] * a.groups), dim3(kAtThreads), smem, s, true, q, k, v, a);
+  e = launch_k(kern, dim3(a.items < num_sms() ? a.items : num_sms()), dim3(kAtThreads), smem, s, true, q, k, v, a);
   trace_post(K_ATTN_PREFILL, s);
   return e;
 }
