@@ -33,9 +33,10 @@ namespace m2 {
 
 constexpr int kAtThreads = 384;
 // Registers a thread after the hand-over; launched with 168 (65536 / 384, in
-// steps of 8): 2 * 216 + 72 = 3 * 168.
-constexpr int kAtRegsSoftmax = 216, kAtRegsOther = 72;
+// steps of 8): 2 * 224 + 56 = 3 * 168.
+constexpr int kAtRegsSoftmax = 224, kAtRegsOther = 56;
 constexpr int kAtRows = 128;      // query rows of a tile, keys of a block
+constexpr int kAtItems = 4;       // items handed on ahead of their use
 constexpr int kAtMaskBlocks = 4;  // key blocks that some row of the two tiles sees only in part: at most 3
 
 template <int D>
@@ -47,10 +48,22 @@ struct AtCfg {
   static constexpr int kBars = kKV + kStages * kTile;
   static constexpr uint32_t kTmS = 0, kTmO = 256;          // tensor-memory columns: S 2 x 128, O 2 x D
 };
+// What a CTA works on: the copies' thread works it out and hands it on through
+// shared memory.
+struct __align__(16) AtItem {
+  int row_q, left;  // row of tile 0's first token; the sequence's tokens from it on
+  int see;          // the last key that this token sees (of the sequence; below 0: none)
+  int row_k;        // row of the sequence's first key
+  int hg;           // group of PK query heads; below 0: no more items
+  int n0, n1;       // key blocks of each tile
+  int jm;           // first key block that some row of tile 0 sees only in part
+};
 struct AtBars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2], fin;
   uint64_t full[10], empty[10];
   uint64_t look, clean;  // a masked block's values may be looked through; they are
+  uint64_t item_full[kAtItems], item_empty[kAtItems];
+  AtItem item[kAtItems];
   // Keys of a masked block whose values are not finite: (item << 32) | bits, by the
   // CTA's item.  A block is looked through after its first scores were issued, when
   // the tiles have at most the output of the item before last ahead of them.
@@ -98,6 +111,21 @@ __device__ __forceinline__ void tmem_ld_wait(float* v) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%1, %2};\n\tmov.b64 rb, {%3, %4};\n\tadd.rn.f32x2 %0, ra, rb;\n\t}"
+      : "=l"(d)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
   return r;
 }
 
@@ -178,13 +206,6 @@ __device__ __forceinline__ int at_pick(int k, int items) {
   return id < items ? id : -1;
 }
 
-// What a CTA works on.
-struct AtItem {
-  int seq, hg;       // sequence; group of PK query heads
-  int q0, nq, nk;    // first token of tile 0 (in the sequence), the sequence's queries and keys
-  int n0, n1;        // key blocks of each tile
-  int jm;            // first key block that some row of tile 0 sees only in part
-};
 __device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
   AtItem it;
   const int tokens = kAtRows >> a.pk_log;  // of one tile
@@ -199,18 +220,19 @@ __device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
     else
       hi = m;
   }
-  it.seq = lo;
-  it.nq = a.cu_q[lo + 1] - a.cu_q[lo];
-  it.nk = a.cu_k[lo + 1] - a.cu_k[lo];
-  it.q0 = (p - a.tile[lo]) * 2 * tokens;
-  const int off = it.nk - it.nq;
+  const int nq = a.cu_q[lo + 1] - a.cu_q[lo], nk = a.cu_k[lo + 1] - a.cu_k[lo];
+  const int q0 = (p - a.tile[lo]) * 2 * tokens;
+  it.row_q = a.cu_q[lo] + q0;
+  it.left = nq - q0;
+  it.see = q0 + nk - nq;
+  it.row_k = a.cu_k[lo];
   auto blocks = [&](int first) {
-    const int last = min(first + tokens, it.nq) - 1 + off;  // the last key seen
-    return first < it.nq && last >= 0 ? last / kAtRows + 1 : 0;
+    const int last = it.see + min(first + tokens, it.left) - 1;  // the last key seen
+    return first < it.left && last >= 0 ? last / kAtRows + 1 : 0;
   };
-  it.n0 = blocks(it.q0);
-  it.n1 = blocks(it.q0 + tokens);
-  it.jm = max(0, (it.q0 + off + 1) >> 7);
+  it.n0 = blocks(0);
+  it.n1 = blocks(tokens);
+  it.jm = max(0, (it.see + 1) >> 7);
   return it;
 }
 
@@ -249,6 +271,16 @@ __device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long
   }
 }
 
+// A consuming warp's next item; false when there is none (or a wait gave up).
+__device__ __forceinline__ bool at_next(AtBars* bars, int pick, int lane, AtItem& it) {
+  const int sl = pick % kAtItems;
+  if (!__all_sync(0xffffffffu, at_wait(&bars->item_full[sl], (pick / kAtItems) & 1))) return false;
+  it = bars->item[sl];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
+  return it.hg >= 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -269,6 +301,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bars->o_done[t], 1);
     }
     mbar_init(&bars->fin, 1);
+    for (int i = 0; i < kAtItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], 11);  // softmax, products and look-through warps
+    }
     mbar_init(&bars->look, 1);
     mbar_init(&bars->clean, 2);
     for (int s = 0; s < NS; ++s) {
@@ -287,7 +323,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // Every role walks the same items; a key block j of an item is copies kv + 2j
+  // Every role walks the same items, which the copies' thread picks; a key block j of an item is copies kv + 2j
   // (K) and kv + 2j + 1 (V) of the CTA, and barrier phases are counted through.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsOther));
@@ -296,8 +332,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const uint64_t keep = policy_evict_normal();
       int kv = 0, nq0 = 0, nq1 = 0;  // copies and Q tiles issued
       bool dead = false;
-      for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
-        const AtItem it = at_item(a, id);
+      for (int pick = 0; !dead; ++pick) {
+        const int id = at_pick(pick, a.items), sl = pick % kAtItems;
+        AtItem it;
+        it.hg = -1;
+        if (id >= 0) it = at_item(a, id);
+        if (pick >= kAtItems && !at_wait(&bars->item_empty[sl], ((pick / kAtItems) - 1) & 1)) break;
+        bars->item[sl] = it;
+        mbar_arrive(&bars->item_full[sl]);
+        if (id < 0) break;
         const int n = max(it.n0, it.n1), h0 = it.hg << a.pk_log, hk = h0 / a.gqa;
         auto load_q = [&](int t) {
           if (!(t ? it.n1 : it.n0) || dead) return;
@@ -308,7 +351,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           mbar_arrive_expect_tx(&bars->q_full[t], C::kTile);
           for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_3d(smem + C::kQ + t * C::kTile + hf * HB, &tmQ, hf * 64, h0, a.cu_q[it.seq] + it.q0 + t * tokens,
+            tma_load_3d(smem + C::kQ + t * C::kTile + hf * HB, &tmQ, hf * 64, h0, it.row_q + t * tokens,
                         &bars->q_full[t], keep);
           ++nq;
         };
@@ -321,7 +364,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           mbar_arrive_expect_tx(&bars->full[s], C::kTile);
           const CUtensorMap* m = i & 1 ? &tmV : &tmK;
           for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_3d(smem + C::kKV + s * C::kTile + hf * HB, m, hf * 64, hk, a.cu_k[it.seq] + (i >> 1) * kAtRows,
+            tma_load_3d(smem + C::kKV + s * C::kTile + hf * HB, m, hf * 64, hk, it.row_k + (i >> 1) * kAtRows,
                         &bars->full[s], keep);
           if (i == 0) {
             load_q(0);
@@ -356,8 +399,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (last) tc_commit(&bars->q_empty[t]);  // the tile's last scores
         if (look) mbar_arrive(&bars->look);
       };
-      for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
-        const AtItem it = at_item(a, id);
+      for (int pick = 0; !dead; ++pick) {
+        AtItem it;
+        if (!at_next(bars, pick, lane, it)) break;
         const int n = max(it.n0, it.n1), lead = it.n0 ? 0 : 1;
         if (n == 0) continue;
         if (!full(kv)) break;
@@ -410,8 +454,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       int kv = 0, looked = 0;
       uint32_t item = 0;
       bool dead = false;
-      for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
-        const AtItem it = at_item(a, id);
+      for (int pick = 0; !dead; ++pick) {
+        AtItem it;
+        if (!at_next(bars, pick, lane, it)) break;
         const int n = max(it.n0, it.n1);
         if (n == 0) continue;
         for (int j = it.jm; j < n; ++j) {
@@ -443,11 +488,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     int ns = 0, no = 0;                         // score tiles and outputs before this item
     uint32_t item = 0;                          // items with keys before this one
     bool dead = false;
-    for (int pick = 0, id; (id = at_pick(pick, a.items)) >= 0 && !dead; ++pick) {
-      const AtItem it = at_item(a, id);
-      const int nt = t ? it.n1 : it.n0, first = it.q0 + t * tokens;
-      const int tok = first + (r >> a.pk_log), off = it.nk - it.nq;
-      const int limit = tok + off;  // the last key this row sees
+    for (int pick = 0;; ++pick) {
+      AtItem it;
+      if (!at_next(bars, pick, lane, it)) break;
+      const int nt = t ? it.n1 : it.n0;
+      const int tok = t * tokens + (r >> a.pk_log);
+      const int limit = it.see + tok;  // the last key this row sees
+      const int warp_limit = it.see + t * tokens + ((r & ~31) >> a.pk_log);  // the warp's first row
       unsigned long long* bad = bars->bad[item & 3];
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < nt; ++j) {
@@ -464,15 +511,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int i = 0; i < kAtRows; ++i) s[i] *= a.scale_log2;
         }
-        if (j * kAtRows + kAtRows - 1 > first + off) {  // some row of the tile does not see the whole block
-          const int seen = limit - j * kAtRows;
+        // How many of the block's keys this row sees, and the warp's first row, which sees the fewest.
+        const int seen = limit - j * kAtRows + 1, least = warp_limit - j * kAtRows + 1;
+        if (least < kAtRows) {
 #pragma unroll
-          for (int i = 0; i < kAtRows; ++i) s[i] = i <= seen ? s[i] : -INFINITY;
+          for (int i = 0; i < kAtRows; i += 32) {
+            if (least >= i + 32) continue;  // the warp's rows see all 32
+#pragma unroll
+            for (int k = i; k < i + 32; ++k) s[k] = k < seen ? s[k] : -INFINITY;
+          }
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float mx[4] = {m, s[0], s[1], s[2]};
 #pragma unroll
-        for (int i = 4; i < kAtRows; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        const float mn = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
+        for (int i = 3; i + 1 < kAtRows; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
+        const float mn = max3(fmaxf(mx[0], s[kAtRows - 1]), mx[1], fmaxf(mx[2], mx[3]));
         if (j == 0) {
           m = mn;
         } else {
@@ -493,15 +545,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
         }
         const float b = m == -INFINITY ? 0.0f : -m * c;  // nothing seen yet: every exponential is 0
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 c2 = make_float2(c, c), b2 = make_float2(b, b);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int i = 0; i < kAtRows; i += 32) {
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float x = ex2(fmaf(s[i + 2 * k], c, b)), y = ex2(fmaf(s[i + 2 * k + 1], c, b));
-            sum[k & 3] += x + y;
-            p[k] = pack_bf16x2(x, y);
+            const float2 z = ffma2(c2, make_float2(s[i + 2 * k], s[i + 2 * k + 1]), b2);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+            sum[k & 1] = fadd2(sum[k & 1], e);
+            p[k] = pack_bf16x2(e.x, e.y);
           }
           tmem_st16(ts + i / 2, p);
           if (i % 64 == 32) {  // 64 keys' probabilities are there
@@ -511,7 +565,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (lane == 0) mbar_arrive(&bars->p_full[t][i / 64]);
           }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (dead) break;
       if (nt > 0 && !__all_sync(0xffffffffu, at_wait(&bars->o_done[t], no & 1))) {
@@ -525,7 +579,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       uint16_t* dst[4];
       {
         const int hl = r & ((1 << a.pk_log) - 1);
-        const uint64_t mine = tok < it.nq ? reinterpret_cast<uint64_t>(a.out + (size_t)(a.cu_q[it.seq] + tok) * a.ld_o +
+        const uint64_t mine = tok < it.left ? reinterpret_cast<uint64_t>(a.out + (size_t)(it.row_q + tok) * a.ld_o +
                                                                        (size_t)((it.hg << a.pk_log) + hl) * D)
                                           : 0;
 #pragma unroll
@@ -550,8 +604,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const unsigned long long e = bad[w];
             for (uint32_t bits = j < nt && (uint32_t)(e >> 32) == item ? (uint32_t)e : 0; bits; bits &= bits - 1) {
               const int key = j * kAtRows + (w & 3) * 32 + __ffs(bits) - 1;
-              if (key > limit || tok >= it.nq) continue;
-              const uint16_t* vr = a.v + (size_t)(a.cu_k[it.seq] + key) * a.ld_v +
+              if (key > limit || tok >= it.left) continue;
+              const uint16_t* vr = a.v + (size_t)(it.row_k + key) * a.ld_v +
                                    (size_t)((it.hg << a.pk_log) / a.gqa) * D + i;
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
