@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import threading
+from array import array
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmamba2_gb300.so")
@@ -125,7 +126,7 @@ def lib():
             l.m2_wait_check.argtypes = [P, P, P]; l.m2_wait_check.restype = C.c_int
             l.m2_workspace_map.argtypes = [C.POINTER(M2Dims), I32, I32, C.POINTER(C.c_int32), C.POINTER(SZ), I32]
             l.m2_workspace_map.restype = C.c_int
-            F, CACHE, CU = C.c_float, C.POINTER(M2Kv4Cache), C.POINTER(I32)
+            F, CACHE, CU = C.c_float, C.POINTER(M2Kv4Cache), P  # CU: the address of int32 offsets
             l.m2_qk_norm_rope.argtypes = [P, I32, P, I32, P, I32, P, I32, P, P, P, P, I32, I32, I32, I32, I32, I32, F, P]
             l.m2_qk_norm_rope.restype = C.c_int
             l.m2_rope_steps.argtypes = [C.c_double, I32, C.POINTER(C.c_uint64)]; l.m2_rope_steps.restype = C.c_int
@@ -289,8 +290,12 @@ def m2_copy(dst, src, nbytes: int, stream=None, check=True) -> int:
 M2_KV4_PAGE = 64
 
 
-def _offsets(cu):
-    return (C.c_int32 * len(cu))(*map(int, cu))
+def _offsets(fn: str, cu, nseq: int):
+    """Host offsets as a C array (an array object; its address is passed while it lives)."""
+    a = array("i", cu)
+    if len(a) != nseq + 1:  # the C side reads nseq + 1 entries
+        raise M2Error(fn, M2_ERR_ARG)
+    return a
 
 
 def kv4_cache(pages, n_pages: int, n_kv_heads: int, head_dim: int, block_table, nseq: int, ld_table: int) -> M2Kv4Cache:
@@ -311,38 +316,36 @@ def m2_rope_steps(theta: float, rot_dim: int) -> list:
 
 def m2_qk_norm_rope(q, ld_q, k, ld_k, q_out, ld_qo, k_out, ld_ko, q_w, k_w, pos, rope_step, T, H, Hkv, head_dim,
                     rot_dim, interleaved, eps, stream=None, check=True) -> int:
-    st = lib().m2_qk_norm_rope(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(q_out), ld_qo, _ptr(k_out), ld_ko, _ptr(q_w),
-                               _ptr(k_w), _ptr(pos), _ptr(rope_step), T, H, Hkv, head_dim, rot_dim,
-                               1 if interleaved else 0, eps, _stream(stream))
+    st = (_lib or lib()).m2_qk_norm_rope(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(q_out), ld_qo, _ptr(k_out), ld_ko,
+                                         _ptr(q_w), _ptr(k_w), _ptr(pos), _ptr(rope_step), T, H, Hkv, head_dim,
+                                         rot_dim, 1 if interleaved else 0, eps, _stream(stream))
     return _check("m2_qk_norm_rope", st) if check else st
 
 
 def m2_kv4_append(cache, k, ld_k, v, ld_v, cu_rows, kv_pos, stream=None, check=True) -> int:
     """cu_rows: host sequence of nseq + 1 row offsets; kv_pos: device int32, tokens held before the call."""
-    _need_offsets("m2_kv4_append", cu_rows, cache.nseq)
-    st = lib().m2_kv4_append(C.byref(cache), _ptr(k), ld_k, _ptr(v), ld_v, _offsets(cu_rows), _ptr(kv_pos),
-                             _stream(stream))
+    cu = _offsets("m2_kv4_append", cu_rows, cache.nseq)
+    st = (_lib or lib()).m2_kv4_append(C.byref(cache), _ptr(k), ld_k, _ptr(v), ld_v, cu.buffer_info()[0],
+                                       _ptr(kv_pos), _stream(stream))
     return _check("m2_kv4_append", st) if check else st
 
 
 def m2_kv4_gather(cache, k, ld_k, v, ld_v, cu_rows, stream=None, check=True) -> int:
     """cu_rows: host sequence of nseq + 1 row offsets of the output."""
-    _need_offsets("m2_kv4_gather", cu_rows, cache.nseq)
-    st = lib().m2_kv4_gather(C.byref(cache), _ptr(k), ld_k, _ptr(v), ld_v, _offsets(cu_rows), _stream(stream))
+    cu = _offsets("m2_kv4_gather", cu_rows, cache.nseq)
+    st = (_lib or lib()).m2_kv4_gather(C.byref(cache), _ptr(k), ld_k, _ptr(v), ld_v, cu.buffer_info()[0],
+                                       _stream(stream))
     return _check("m2_kv4_gather", st) if check else st
-
-
-def _need_offsets(fn: str, cu, nseq: int) -> None:
-    if len(cu) != nseq + 1:  # the C side reads nseq + 1 entries
-        raise M2Error(fn, M2_ERR_ARG)
 
 
 def m2_attn_prefill_varlen(q, ld_q, k, ld_k, v, ld_v, out, ld_o, H, Hkv, head_dim, cu_q, cu_k, scale, stream=None,
                            check=True) -> int:
     """cu_q, cu_k: host sequences of nseq + 1 row offsets."""
-    _need_offsets("m2_attn_prefill_varlen", cu_k, len(cu_q) - 1)
-    st = lib().m2_attn_prefill_varlen(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(out), ld_o, H, Hkv, head_dim,
-                                      len(cu_q) - 1, _offsets(cu_q), _offsets(cu_k), scale, _stream(stream))
+    nseq = len(cu_q) - 1
+    cq, ck = _offsets("m2_attn_prefill_varlen", cu_q, nseq), _offsets("m2_attn_prefill_varlen", cu_k, nseq)
+    st = (_lib or lib()).m2_attn_prefill_varlen(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(out), ld_o, H, Hkv,
+                                                head_dim, nseq, cq.buffer_info()[0], ck.buffer_info()[0], scale,
+                                                _stream(stream))
     return _check("m2_attn_prefill_varlen", st) if check else st
 
 
@@ -351,8 +354,8 @@ def m2_attn_decode_kv4_workspace_bytes(nseq: int, H: int, Hkv: int, head_dim: in
 
 
 def m2_attn_decode_kv4(cache, q, ld_q, out, ld_o, H, kv_len, scale, ws, ws_bytes, stream=None, check=True) -> int:
-    st = lib().m2_attn_decode_kv4(C.byref(cache), _ptr(q), ld_q, _ptr(out), ld_o, H, _ptr(kv_len), scale, _ptr(ws),
-                                  ws_bytes, _stream(stream))
+    st = (_lib or lib()).m2_attn_decode_kv4(C.byref(cache), _ptr(q), ld_q, _ptr(out), ld_o, H, _ptr(kv_len), scale,
+                                            _ptr(ws), ws_bytes, _stream(stream))
     return _check("m2_attn_decode_kv4", st) if check else st
 
 

@@ -11,279 +11,450 @@ namespace m2 {
 
 // ------------------------------------------------------------------ head norm and rotation
 //
-// A head is D/8 lanes of 8 channels (16-byte loads and stores), so that a
-// warp holds 256/D heads of a row.  The angles of a row are shared by all its
-// heads: one thread per (row, frequency) evaluates sin and cos into shared
-// memory.  p * step mod 2^64 is the angle in turns, exactly; only its top 32
-// bits (as a signed fraction of a half turn) enter the fp32 functions.
-constexpr int kRopeThreads = 256;
+// A warp takes a row, or a part of its heads when there are few rows: a head is
+// D/8 lanes of 8 channels, so that the warp holds 256/D heads (a group) at a
+// time.  The angles of the row are worked out once, by the warp's lanes, into
+// shared memory: p * step mod 2^64 is the angle in turns, exactly, and only its
+// top 32 bits (a signed fraction of a half turn) enter the fp32 functions.
+// Bound: HBM, one read and one write of every row; the kernel for the usual
+// rotation of all channels is also close to the issue rate.
+constexpr int kRopeWarps = 8, kRopeBatch = 4;
 
+// Cosines and sines of the row's angles.
+__device__ __forceinline__ void rope_angles(const RopeArgs& a, int64_t row, int lane, float2* cs) {
+  const int64_t pos = a.pos[row];
+  for (int f = lane; f < a.rot / 2; f += 32) {
+    const uint64_t t = (uint64_t)pos * a.step[f];
+    float s, c;
+    sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+    cs[f] = make_float2(c, s);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%1, %2};\n\tmov.b64 rb, {%3, %4};\n\tmul.rn.f32x2 %0, ra, rb;\n\t}"
+      : "=l"(d)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%1, %2};\n\tmov.b64 rb, {%3, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
+      "fma.rn.f32x2 %0, ra, rb, rc;\n\t}"
+      : "=l"(d)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+
+// Rotation of all channels, pair i = (i, i + D/2): a lane's 8 channels are 4 l .. 4 l + 3
+// and those D/2 on, so that nothing but the sum of squares crosses lanes.  Weights
+// and angles meet once a row: with w' = w cos, w" = w sin of the pair,
+//   y_a = r (a w'_a - b w"_b),  y_b = r (b w'_b + a w"_a),  r = 1 / sqrt(mean + eps).
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a, int rows_per_cta) {
-  constexpr int LH = D / 8, HW = 32 / LH;  // lanes a head, heads a warp
-  extern __shared__ float2 cs[];           // [rows][rot / 2] (cos, sin)
-  const int r0 = blockIdx.x * rows_per_cta;
-  const int rows = min(rows_per_cta, a.T - r0), half = a.rot / 2;
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(const RopeArgs a, int parts) {
+  constexpr int LH = D / 8, HW = 32 / LH;  // lanes a head, heads a group
+  __shared__ float2 turn[kRopeWarps][D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LH, sub = lane / LH;
+  const int64_t id = (int64_t)blockIdx.x * kRopeWarps + warp, row = id / parts;
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x; i < rows * half; i += kRopeThreads) {
-    const int r = i / half, f = i - r * half;
-    const uint64_t turn = (uint64_t)(int64_t)a.pos[r0 + r] * a.step[f];
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    cs[i] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = (lane % LH) * 8;  // this lane's first channel
+  if (row >= a.T) return;
+  rope_angles(a, row, lane, turn[warp]);
+  float2 cs[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) cs[i] = turn[warp][4 * l + i];
+  const int gq = (a.H + HW - 1) / HW, groups = gq + (a.Hkv + HW - 1) / HW;
+  const int per = (groups + parts - 1) / parts, g0 = (int)(id - row * parts) * per, g1 = min(groups, g0 + per);
+  // the groups from `from` to `to` of n heads at in -> out
+  auto run = [&](const uint16_t* in, uint16_t* out, const uint16_t* w, int n, int from, int to) {
+    if (from >= to) return;
+    float2 ca[2], sb[2], cb[2], sa[2];  // of channel pairs (0, 1), (2, 3): w'_a, -w"_b, w'_b, w"_a
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 wa = make_float2(1.0f, 1.0f), wb = wa;
+      if (w) {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(w + 4 * l + 2 * i);
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(w + D / 2 + 4 * l + 2 * i);
+        wa = make_float2(bf16lo(u), bf16hi(u)), wb = make_float2(bf16lo(v), bf16hi(v));
+      }
+      const float2 c = make_float2(cs[2 * i].x, cs[2 * i + 1].x), s = make_float2(cs[2 * i].y, cs[2 * i + 1].y);
+      ca[i] = mul2(wa, c), cb[i] = mul2(wb, c), sa[i] = mul2(wa, s), sb[i] = mul2(wb, make_float2(-s.x, -s.y));
+    }
+    const int64_t lane_at = (int64_t)sub * D + 4 * l;
+    in += lane_at, out += lane_at;
+    for (int gb = from; gb < to; gb += kRopeBatch) {
+      uint2 u[kRopeBatch], v[kRopeBatch];
+#pragma unroll
+      for (int k = 0; k < kRopeBatch; ++k) {
+        u[k] = v[k] = make_uint2(0u, 0u);
+        if (gb + k < to && (gb + k) * HW + sub < n) {
+          u[k] = *reinterpret_cast<const uint2*>(in + (gb + k) * (HW * D));
+          v[k] = *reinterpret_cast<const uint2*>(in + (gb + k) * (HW * D) + D / 2);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRopeBatch; ++k) {
+        float2 xa[2] = {make_float2(bf16lo(u[k].x), bf16hi(u[k].x)), make_float2(bf16lo(u[k].y), bf16hi(u[k].y))};
+        float2 xb[2] = {make_float2(bf16lo(v[k].x), bf16hi(v[k].x)), make_float2(bf16lo(v[k].y), bf16hi(v[k].y))};
+        float r = 1.0f;
+        if (w) {
+          const float2 q = fma2(xa[0], xa[0], fma2(xa[1], xa[1], fma2(xb[0], xb[0], mul2(xb[1], xb[1]))));
+          float ss = q.x + q.y;
+#pragma unroll
+          for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          r = rsqrtf(ss * (1.0f / D) + a.eps);
+        }
+        const float2 r2 = make_float2(r, r);
+        float2 ya[2], yb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ya[i] = mul2(fma2(xa[i], ca[i], mul2(xb[i], sb[i])), r2);
+          yb[i] = mul2(fma2(xb[i], cb[i], mul2(xa[i], sa[i])), r2);
+        }
+        if (gb + k < to && (gb + k) * HW + sub < n) {
+          uint16_t* d = out + (gb + k) * (HW * D);
+          *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(ya[0].x, ya[0].y), pack_bf16x2(ya[1].x, ya[1].y));
+          *reinterpret_cast<uint2*>(d + D / 2) = make_uint2(pack_bf16x2(yb[0].x, yb[0].y), pack_bf16x2(yb[1].x, yb[1].y));
+        }
+      }
+    }
+  };
+  run(a.q + row * a.ld_q, a.q_out + row * a.ld_qo, a.q_w, a.H, min(g0, gq), min(g1, gq));
+  run(a.k + row * a.ld_k, a.k_out + row * a.ld_ko, a.k_w, a.Hkv, max(g0, gq) - gq, max(g1, gq) - gq);
+}
+
+// Every other form: part of the channels rotated, neighbouring pairs, none.  A
+// lane's 8 channels lie together.
+template <int D>
+__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const RopeArgs a, int parts) {
+  constexpr int LH = D / 8, HW = 32 / LH;
+  __shared__ float2 turn[kRopeWarps][D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LH, half = a.rot / 2, c0 = 8 * l;
+  const int64_t id = (int64_t)blockIdx.x * kRopeWarps + warp, row = id / parts;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.T) return;
+  const float2* cs = turn[warp];
+  if (half) rope_angles(a, row, lane, turn[warp]);
   const int heads = a.H + a.Hkv, groups = (heads + HW - 1) / HW;
-  for (int t = warp; t < rows * groups; t += kRopeThreads / 32) {
-    const int r = t / groups, h = (t - r * groups) * HW + lane / LH;
-    const bool on = h < heads, isq = h < a.H;
-    const size_t row = r0 + r;
-    float x[8];
-    if (on) {
-      const uint16_t* src = isq ? a.q + row * a.ld_q + (size_t)h * D : a.k + row * a.ld_k + (size_t)(h - a.H) * D;
-      const uint4 v = *reinterpret_cast<const uint4*>(src + c0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int per = (groups + parts - 1) / parts, g0 = (int)(id - row * parts) * per, g1 = min(groups, g0 + per);
+  for (int gb = g0; gb < g1; gb += kRopeBatch) {
+    uint4 in[kRopeBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16lo(w[i]);
-        x[2 * i + 1] = bf16hi(w[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int h = (gb + k) * HW + lane / LH;
+      in[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (gb + k < g1 && h < heads)
+        in[k] = *reinterpret_cast<const uint4*>((h < a.H ? a.q + row * a.ld_q + h * D : a.k + row * a.ld_k + (h - a.H) * D) + c0);
     }
-    float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int k = 0; k < kRopeBatch; ++k) {
+      if (gb + k >= g1) break;
+      const int h = (gb + k) * HW + lane / LH;
+      const bool isq = h < a.H;
+      const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+      float x[8], ss = 0.0f;
 #pragma unroll
-    for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const uint16_t* nw = isq ? a.q_w : a.k_w;
-    if (nw) {
-      const float rr = rsqrtf(ss * (1.0f / D) + a.eps);
-      const uint4 v = *reinterpret_cast<const uint4*>(nw + c0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] *= rr * bf16lo(w[i]);
-        x[2 * i + 1] *= rr * bf16hi(w[i]);
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const uint16_t* nw = isq ? a.q_w : a.k_w;
+      if (nw) {
+        const float rr = rsqrtf(ss * (1.0f / D) + a.eps);
+        const uint4 v = *reinterpret_cast<const uint4*>(nw + c0);
+        const uint32_t n[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] *= rr * bf16lo(n[i]), x[2 * i + 1] *= rr * bf16hi(n[i]);
       }
-    }
-    if (half) {
-      const float2* rc = cs + r * half;
-      if (a.interleaved) {
+      if (half && a.interleaved) {
         if (c0 < a.rot) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 t2 = rc[c0 / 2 + i];
-            const float u = x[2 * i], w = x[2 * i + 1];
-            x[2 * i] = u * t2.x - w * t2.y;
-            x[2 * i + 1] = w * t2.x + u * t2.y;
+            const float2 t = cs[c0 / 2 + i];
+            const float u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = u * t.x - v * t.y;
+            x[2 * i + 1] = v * t.x + u * t.y;
           }
         }
-      } else {
+      } else if (half) {
         // the partner channel is rot/2 away: rot/16 lanes
-        const int dl = a.rot / 16, l = lane % LH;
-        const bool first = l < dl, in = l < 2 * dl;
-        const int src = in ? (first ? lane + dl : lane - dl) : lane;
+        __syncwarp();
+        const int dl = a.rot / 16;
+        const bool first = l < dl, in_rot = l < 2 * dl;
+        const int src = in_rot ? (first ? lane + dl : lane - dl) : lane;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float o = __shfl_sync(0xffffffffu, x[i], src);
-          if (in) {
-            const float2 t2 = rc[(first ? c0 : c0 - half) + i];
-            x[i] = x[i] * t2.x + (first ? -o : o) * t2.y;
+          if (in_rot) {
+            const float2 t = cs[(first ? c0 : c0 - half) + i];
+            x[i] = x[i] * t.x + (first ? -o : o) * t.y;
           }
         }
       }
-    }
-    if (on) {
-      uint16_t* dst =
-          isq ? a.q_out + row * a.ld_qo + (size_t)h * D : a.k_out + row * a.ld_ko + (size_t)(h - a.H) * D;
-      *reinterpret_cast<uint4*>(dst + c0) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      if (h < heads)
+        *reinterpret_cast<uint4*>((isq ? a.q_out + row * a.ld_qo + h * D : a.k_out + row * a.ld_ko + (h - a.H) * D) + c0) =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                       pack_bf16x2(x[6], x[7]));
     }
   }
 }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t s) {
-  const int rows = a.T > 4 * num_sms() ? 4 : 1;
-  const dim3 grid((a.T + rows - 1) / rows), block(kRopeThreads);
-  const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);
+  const bool all = a.rot == a.D && !a.interleaved;
+  // Few rows: a row's heads are dealt out over several warps, until every SM has
+  // 16 (64 rows of 32 + 8 heads of 128: one batch of loads a warp).
+  int parts = 1;
+  while (parts < 8 && (int64_t)a.T * parts < 16ll * num_sms()) parts *= 2;
+  const dim3 grid((unsigned)(((int64_t)a.T * parts + kRopeWarps - 1) / kRopeWarps)), block(kRopeWarps * 32);
+  auto k = a.D == 128 ? (all ? qk_norm_rope_all_kernel<128> : qk_norm_rope_kernel<128>)
+                      : (all ? qk_norm_rope_all_kernel<64> : qk_norm_rope_kernel<64>);
   trace_pre(K_QK_NORM_ROPE, s);
-  const cudaError_t e = a.D == 128 ? launch_k(qk_norm_rope_kernel<128>, grid, block, smem, s, true, a, rows)
-                                   : launch_k(qk_norm_rope_kernel<64>, grid, block, smem, s, true, a, rows);
+  const cudaError_t e = launch_k(k, grid, block, 0, s, true, a, parts);
   trace_post(K_QK_NORM_ROPE, s);
   return e;
 }
 
 // ------------------------------------------------------------------ cache rows
 //
-// A task is one token pair (positions 2p and 2p + 1: they share V's bytes) of
-// one kv head, on D/4 lanes: lane l of it holds 8 channels of token l / (D/8).
-// The pair's two tokens always lie in one page.  Sequence i's tasks start at
-// pair_base(i): a closed form that leaves room for a pair cut at both ends.
-__device__ __forceinline__ int64_t pair_base(const Kv4RowsArgs& a, int i) { return a.cu[i] / 2 + 2ll * i; }
-static int64_t pair_count(const Kv4RowsArgs& a) { return a.cu[a.nseq] / 2 + 2ll * a.nseq; }
+// A warp's task is 8 tokens (positions 8b .. 8b+7) of one kv head: there the
+// codes of K (8 rows) and of V (one block of the layout), and both kinds of
+// scales, are four contiguous runs of a page.  Codes pass through shared memory
+// between the layout's order and that of the rows, so that rows and runs are
+// both read and written 16 bytes a lane.  Sequence i's tasks start at
+// block_base(i): a closed form that leaves room for blocks cut at both ends.
+// Bound: HBM (2 bytes a value of the rows, 0.56 of the cache).
+__device__ __forceinline__ int64_t block_base(const Kv4RowsArgs& a, int i) { return a.cu[i] / 8 + 2ll * i; }
+static int64_t block_count(const Kv4RowsArgs& a) { return a.cu[a.nseq] / 8 + 2ll * a.nseq; }
 
-struct PairTask {
-  bool any;        // a token of the pair belongs to the call
+constexpr int kRowWarps = 8;
+struct RowTask {
   int seq, h;
-  int64_t tok;     // position of this lane's token
-  bool have;       // it belongs to the call
-  uint8_t* block;  // its page's block, null if the table does not give one
+  int64_t first, end;  // positions of the call's tokens of the sequence
+  int64_t tok;         // the block's first position
+  int page;            // the table's entry: loaded here, looked at when it is needed
+  bool any;            // a token of the block belongs to the call
 };
-
-template <int D>
-__device__ __forceinline__ PairTask pair_task(const Kv4RowsArgs& a, int64_t tasks) {
-  constexpr int LT = D / 4;
-  PairTask t;
-  const int64_t id = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LT;
-  t.any = t.have = false;
-  t.block = nullptr;
-  t.seq = 0;
-  t.tok = 0;
+__device__ __forceinline__ RowTask row_task(const Kv4RowsArgs& a, int64_t tasks) {
+  RowTask t;
+  t.any = false;
+  const int64_t id = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (id >= tasks) return t;
   const int64_t p = id / a.c.Hkv;
   t.h = (int)(id - p * a.c.Hkv);
-  int lo = 0, hi = a.nseq;  // the last i with pair_base(i) <= p
+  int lo = 0, hi = a.nseq;  // the last i with block_base(i) <= p
   while (hi - lo > 1) {
     const int m = (lo + hi) / 2;
-    if (pair_base(a, m) <= p)
+    if (block_base(a, m) <= p)
       lo = m;
     else
       hi = m;
   }
   t.seq = lo;
-  const int64_t first = a.pos ? a.pos[lo] : 0, end = first + a.cu[lo + 1] - a.cu[lo];
-  // pairs from that of `first` (rounded down, also below zero) on
-  const int64_t pr = (first >> 1) + (p - pair_base(a, lo));
-  t.tok = 2 * pr + (threadIdx.x % LT) / (D / 8);
-  t.have = t.tok >= first && t.tok < end;
-  t.any = 2 * pr + 1 >= first && 2 * pr < end;
-  if (!t.any) return t;
-  const int64_t page = pr >= 0 ? pr / (kPage / 2) : a.c.ld_table;
-  const int id_page = page < a.c.ld_table ? a.c.table[(size_t)lo * a.c.ld_table + page] : -1;
-  if (id_page >= 0 && id_page < a.c.n_pages)
-    t.block = a.c.pages + ((size_t)id_page * a.c.Hkv + t.h) * (72 * D);
-  else
-    M2_RECORD_ARG(g_status);
-  t.have = t.have && t.block;
+  t.first = a.pos ? a.pos[lo] : 0;
+  t.end = t.first + a.cu[lo + 1] - a.cu[lo];
+  const int64_t blk = (t.first >> 3) + (p - block_base(a, lo));  // from the block of `first` (also below zero) on
+  t.tok = 8 * blk;
+  if (t.tok >= t.end || t.end == t.first) return t;
+  t.any = true;
+  const int64_t pg = blk >= 0 ? blk / (kPage / 8) : a.c.ld_table;
+  t.page = pg < a.c.ld_table ? a.c.table[(size_t)lo * a.c.ld_table + pg] : -1;
   return t;
 }
-
-// 8 channels of a row as fp32.
-__device__ __forceinline__ void row8(const uint16_t* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16lo(w[i]);
-    x[2 * i + 1] = bf16hi(w[i]);
-  }
+// The bytes of the task's page and head; null, and the device status, if the table does not give one.
+__device__ __forceinline__ uint8_t* row_page(const Kv4RowsArgs& a, const RowTask& t, int unit) {
+  if (t.page >= 0 && t.page < a.c.n_pages) return a.c.pages + ((size_t)t.page * a.c.Hkv + t.h) * unit;
+  M2_RECORD_ARG(g_status);
+  return nullptr;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Scale byte and codes (8 nibbles, channel order) of this lane's half group;
 // the group's other half is on the neighbouring lane.
-__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& byte) {
-  float m = 0.0f;
-  bool nan = false;
+__device__ __forceinline__ uint32_t quantize8(const uint4& v, uint32_t& byte) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // bf16 magnitudes compare as integers, and a NaN is above everything
+  uint32_t m2 = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                          max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m2 = max_u16x2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+  const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+  const bool nan = m > 0x7F80u;
+  byte = nan ? 0xFFu : kv4_scale_byte(__uint_as_float(m << 16));
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(kv4_scale(byte)));
+  if (nan || byte == 0) inv = 0.0f;
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m = fmaxf(m, fabsf(x[i]));
-    nan |= x[i] != x[i];
-  }
-  if (nan) m = __int_as_float(0x7fffffff);
-  const float o = __shfl_xor_sync(0xffffffffu, m, 1);
-  nan = m != m || o != o;
-  m = fmaxf(m, o);
-  byte = nan ? 0xFFu : kv4_scale_byte(m);
-  const float s = nan ? 0.0f : kv4_scale(byte);
-  uint32_t c = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c |= kv4_codes(x[2 * i], x[2 * i + 1], s) << (8 * i);
-  return c;
+  for (int i = 0; i < 4; ++i) c[i] = kv4_codes(make_float2(bf16lo(w[i]), bf16hi(w[i])), inv);
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
+
+// The low 4 nibbles, one a byte.
+__device__ __forceinline__ uint32_t spread4(uint32_t x) {
+  x = (x & 0xFFu) | (x & 0xFF00u) << 8;
+  return (x | x << 4) & 0x0F0F0F0Fu;
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsArgs a, int64_t tasks) {
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4RowsArgs a, int64_t tasks) {
   using L = Kv4Block<D>;
+  constexpr int LT = D / 8, TI = 32 / LT, RUN = 4 * D;  // lanes a token, tokens at a time, bytes of 8 tokens' codes
+  __shared__ __align__(16) uint8_t buf[kRowWarps][2 * RUN + D];  // K codes, V codes, K scales, V scales
   pdl_wait();
   pdl_trigger();
-  const PairTask t = pair_task<D>(a, tasks);
-  const int lt = threadIdx.x % (D / 4), l = lt % (D / 8);
-  const int c0 = 8 * l, g = c0 / 16, c = (c0 % 16) / 4;
-  float x[8] = {}, y[8] = {};
-  if (t.have) {
-    const size_t row = a.cu[t.seq] + (t.tok - a.pos[t.seq]);
-    row8(a.k + row * a.ld_k + t.h * D + c0, x);
-    row8(a.v + row * a.ld_v + t.h * D + c0, y);
-  }
-  uint32_t kb, vb;
-  const uint32_t kc = quantize8(x, kb), vc = quantize8(y, vb);
-  // the other token's V codes and whether it is new
-  const uint32_t vo = __shfl_xor_sync(0xffffffffu, vc, D / 8);
-  const bool other = __shfl_xor_sync(0xffffffffu, t.have ? 1 : 0, D / 8) != 0;
-  if (!t.block) return;
-  const int tk = (int)(t.tok % kPage);
-  if (t.have) {
-    *reinterpret_cast<uint16_t*>(t.block + L::k(tk, g, c)) = (uint16_t)kc;
-    *reinterpret_cast<uint16_t*>(t.block + L::k(tk, g, c + 1)) = (uint16_t)(kc >> 16);
-    if (l % 2 == 0) {
-      t.block[L::ks(tk, g)] = (uint8_t)kb;
-      t.block[L::vs(tk, g)] = (uint8_t)vb;
+  const RowTask t = row_task(a, tasks);
+  if (!t.any) return;
+  const int lane = threadIdx.x & 31, l = lane % LT;
+  uint8_t* kc = buf[threadIdx.x >> 5];
+  uint8_t* vc = kc + RUN;
+  uint8_t* ks = vc + RUN;
+  uint8_t* vs = ks + D / 2;
+  const int t0 = (int)max((int64_t)0, t.first - t.tok), t1 = (int)min((int64_t)8, t.end - t.tok);  // new tokens of the block
+  uint4 x[8 / TI], y[8 / TI];
+#pragma unroll
+  for (int i = 0; i < 8 / TI; ++i) {
+    const int n = i * TI + lane / LT;
+    x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (n >= t0 && n < t1) {
+      const size_t row = a.cu[t.seq] + (t.tok + n - t.first);
+      x[i] = *reinterpret_cast<const uint4*>(a.k + row * a.ld_k + t.h * D + 8 * l);
+      y[i] = *reinterpret_cast<const uint4*>(a.v + row * a.ld_v + t.h * D + 8 * l);
     }
   }
-  // V: channel 8l + r is byte r of the two tokens' codes; the even token's
-  // lane writes r = 0..3, the odd one's r = 4..7
-  const bool odd = lt >= D / 8;
-  const uint32_t ve = odd ? vo : vc, vd = odd ? vc : vo;
-  const bool he = odd ? other : t.have, hd = odd ? t.have : other;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = odd ? 4 + i : i;
-    uint8_t* p = t.block + L::v(tk, l, r);
-    const uint32_t lo = (ve >> (4 * r)) & 15u, hi = (vd >> (4 * r)) & 15u;
-    uint32_t b = lo | (hi << 4);
-    if (!he)
-      b = (*p & 15u) | (hi << 4);  // stored by an earlier call
-    else if (!hd)
-      b = lo;
-    *p = (uint8_t)b;
+  for (int i = 0; i < 8 / TI; ++i) {
+    const int n = i * TI + lane / LT, g = l / 2, c = 2 * (l & 1);
+    uint32_t kb, vb;
+    const uint32_t k8 = quantize8(x[i], kb), v8 = quantize8(y[i], vb);
+    *reinterpret_cast<uint16_t*>(kc + L::k(n, g, c) - L::kK) = (uint16_t)k8;
+    *reinterpret_cast<uint16_t*>(kc + L::k(n, g, c + 1) - L::kK) = (uint16_t)(k8 >> 16);
+    if (l % 2 == 0) {
+      ks[L::ks(n, g) - L::kKs] = (uint8_t)kb;
+      vs[L::vs(n, g) - L::kVs] = (uint8_t)vb;
+    }
+    // channel 8l + r is nibble r: the even token's lane writes r = 0..3 of the pair's bytes, the odd one's 4..7
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, v8, LT);
+    const uint32_t even = n & 1 ? other >> 16 : v8, odd = n & 1 ? v8 >> 16 : other;
+    const uint32_t b = spread4(even) | spread4(odd) << 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vc[L::v(n, l, (n & 1) * 4 + j) - L::kV] = (uint8_t)(b >> (8 * j));
+  }
+  __syncwarp();
+  uint8_t* page = row_page(a, t, L::kBytes);
+  if (!page) return;
+  const int tk = (int)(t.tok % kPage);
+  if (lane < RUN / 16) {
+    const uint4 k = *reinterpret_cast<const uint4*>(kc + 16 * lane);
+    uint4 v = *reinterpret_cast<const uint4*>(vc + 16 * lane);
+    uint8_t* kd = page + L::k(tk, 0, 0) + 16 * lane;
+    uint8_t* vd = page + L::v(tk, 0, 0) + 16 * lane;
+    const int n = 16 * lane / (D / 2);
+    if (n >= t0 && n < t1) *reinterpret_cast<uint4*>(kd) = k;
+    // V bytes hold two tokens: the other's nibbles stay when only one is new.  16 bytes are one pair's (D = 128)
+    // or two pairs' (D = 64).
+    uint32_t keep[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int p = (16 * lane + 8 * q) / (D / 8) % 4;
+      keep[q] = (2 * p >= t0 && 2 * p < t1 ? 0u : 0x0F0F0F0Fu) | (2 * p + 1 >= t0 && 2 * p + 1 < t1 ? 0u : 0xF0F0F0F0u);
+    }
+    if ((keep[0] & keep[1]) != 0xFFFFFFFFu) {
+      if (keep[0] | keep[1]) {
+        const uint4 o = *reinterpret_cast<const uint4*>(vd);
+        v.x = (o.x & keep[0]) | (v.x & ~keep[0]);
+        v.y = (o.y & keep[0]) | (v.y & ~keep[0]);
+        v.z = (o.z & keep[1]) | (v.z & ~keep[1]);
+        v.w = (o.w & keep[1]) | (v.w & ~keep[1]);
+      }
+      *reinterpret_cast<uint4*>(vd) = v;
+    }
+  }
+  // scales, 4 bytes a lane: of one token (K), of a pair (V: bytes 0, 1 of the even token, 2, 3 of the odd one)
+  if (lane < D / 8) {
+    const int n = 4 * lane / (D / 16), p = 4 * lane / (D / 8);
+    if (n >= t0 && n < t1)
+      *reinterpret_cast<uint32_t*>(page + L::ks(tk, 0) + 4 * lane) = *reinterpret_cast<const uint32_t*>(ks + 4 * lane);
+    const bool e = 2 * p >= t0 && 2 * p < t1, o = 2 * p + 1 >= t0 && 2 * p + 1 < t1;
+    uint8_t* d = page + L::vs(tk, 0) + 4 * lane;
+    if (e) *reinterpret_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(vs + 4 * lane);
+    if (o) *reinterpret_cast<uint16_t*>(d + 2) = *reinterpret_cast<const uint16_t*>(vs + 4 * lane + 2);
   }
 }
 
+// Two codes times their scale, both f16, as bf16x2: exact (6 significant bits).
+__device__ __forceinline__ uint32_t kv4_bf16x2(uint32_t codes, uint32_t scale2) {
+  const uint32_t h = kv4_f16x2(codes);
+  const float2 f = __half22float2(
+      __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&scale2)));
+  return pack_bf16x2(f.x, f.y);
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4RowsArgs a, int64_t tasks) {
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_gather_kernel(const Kv4RowsArgs a, int64_t tasks) {
   using L = Kv4Block<D>;
+  constexpr int LT = D / 8, TI = 32 / LT, RUN = 4 * D;
+  __shared__ __align__(16) uint8_t buf[kRowWarps][2 * RUN + D];
   pdl_wait();
   pdl_trigger();
-  const PairTask t = pair_task<D>(a, tasks);
-  if (!t.have) return;
-  const int lt = threadIdx.x % (D / 4), l = lt % (D / 8);
-  const int c0 = 8 * l, g = c0 / 16, c = (c0 % 16) / 4, tk = (int)(t.tok % kPage);
-  const float sk = kv4_scale(t.block[L::ks(tk, g)]), sv = kv4_scale(t.block[L::vs(tk, g)]);
-  uint32_t k[4], v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = kv4_f32x2(t.block[L::k(tk, g, c + i / 2) + i % 2]);
-    k[i] = pack_bf16x2(f.x * sk, f.y * sk);
-    const uint32_t b0 = t.block[L::v(tk, l, 2 * i)] >> (4 * (tk & 1)),
-                   b1 = t.block[L::v(tk, l, 2 * i + 1)] >> (4 * (tk & 1));
-    const float2 w = kv4_f32x2((b0 & 15u) | ((b1 & 15u) << 4));
-    v[i] = pack_bf16x2(w.x * sv, w.y * sv);
+  const RowTask t = row_task(a, tasks);
+  uint8_t* page = t.any ? row_page(a, t, L::kBytes) : nullptr;
+  if (!page) return;
+  const int lane = threadIdx.x & 31, l = lane % LT;
+  uint8_t* kc = buf[threadIdx.x >> 5];
+  uint8_t* vc = kc + RUN;
+  uint8_t* ks = vc + RUN;
+  uint8_t* vs = ks + D / 2;
+  const int tk = (int)(t.tok % kPage);
+  if (lane < RUN / 16) {
+    *reinterpret_cast<uint4*>(kc + 16 * lane) = *reinterpret_cast<const uint4*>(page + L::k(tk, 0, 0) + 16 * lane);
+    *reinterpret_cast<uint4*>(vc + 16 * lane) = *reinterpret_cast<const uint4*>(page + L::v(tk, 0, 0) + 16 * lane);
   }
-  const size_t row = a.cu[t.seq] + t.tok;
-  *reinterpret_cast<uint4*>(a.k + row * a.ld_k + t.h * D + c0) = make_uint4(k[0], k[1], k[2], k[3]);
-  *reinterpret_cast<uint4*>(a.v + row * a.ld_v + t.h * D + c0) = make_uint4(v[0], v[1], v[2], v[3]);
+  if (lane < D / 8) {
+    *reinterpret_cast<uint32_t*>(ks + 4 * lane) = *reinterpret_cast<const uint32_t*>(page + L::ks(tk, 0) + 4 * lane);
+    *reinterpret_cast<uint32_t*>(vs + 4 * lane) = *reinterpret_cast<const uint32_t*>(page + L::vs(tk, 0) + 4 * lane);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8 / TI; ++i) {
+    const int n = i * TI + lane / LT, g = l / 2, c = 2 * (l & 1);
+    if (t.tok + n >= t.end) continue;
+    const size_t row = a.cu[t.seq] + t.tok + n;
+    const uint32_t sk = (uint32_t)ks[L::ks(n, g) - L::kKs] * 0x00800080u;  // f16 bits, twice
+    const uint32_t sv = (uint32_t)vs[L::vs(n, g) - L::kVs] * 0x00800080u;
+    const uint32_t k0 = *reinterpret_cast<const uint16_t*>(kc + L::k(n, g, c) - L::kK);
+    const uint32_t k1 = *reinterpret_cast<const uint16_t*>(kc + L::k(n, g, c + 1) - L::kK);
+    *reinterpret_cast<uint4*>(a.k + row * a.ld_k + t.h * D + 8 * l) = make_uint4(
+        kv4_bf16x2(k0, sk), kv4_bf16x2(k0 >> 8, sk), kv4_bf16x2(k1, sk), kv4_bf16x2(k1 >> 8, sk));
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // channels 8l + 2j and + 1: this token's nibbles of two bytes
+      uint32_t b0 = vc[L::v(n, l, 2 * j) - L::kV], b1 = vc[L::v(n, l, 2 * j + 1) - L::kV];
+      if (n & 1)
+        b0 = b0 >> 4 | (b1 & 0xF0u);
+      else
+        b0 = (b0 & 15u) | b1 << 4;
+      v[j] = kv4_bf16x2(b0, sv);
+    }
+    *reinterpret_cast<uint4*>(a.v + row * a.ld_v + t.h * D + 8 * l) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
 }
 
 static cudaError_t launch_rows(void (*k128)(Kv4RowsArgs, int64_t), void (*k64)(Kv4RowsArgs, int64_t), int id,
                                const Kv4RowsArgs& a, cudaStream_t s) {
-  const int64_t tasks = pair_count(a) * a.c.Hkv;
-  const int per = 256 / (a.c.D / 4);
-  const dim3 grid((unsigned)((tasks + per - 1) / per)), block(256);
+  const int64_t tasks = block_count(a) * a.c.Hkv;
+  const dim3 grid((unsigned)((tasks + kRowWarps - 1) / kRowWarps)), block(kRowWarps * 32);
   trace_pre(id, s);
   const cudaError_t e = launch_k(a.c.D == 128 ? k128 : k64, grid, block, 0, s, true, a, tasks);
   trace_post(id, s);
