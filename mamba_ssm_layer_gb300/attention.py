@@ -1,0 +1,141 @@
+"""Device-side holders for the attention mixers of a hybrid stack and their 4-bit cache.
+
+PyTorch provides the device memory and the stream; every computation is one of
+the C entry points in ``abi``: the projections (``w8a16_gemv``), the head norm
+and rotation, the cache's writes and reads, and attention over a whole prompt or
+over the cache.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import abi
+from .layer import _empty, _zeros, to_dev
+
+PAGE = abi.M2_KV4_PAGE
+
+
+class Kv4Cache:
+    """The paged 4-bit K/V cache of ``n_layers`` attention layers for ``nseq`` sequences.
+
+    The layers share one page table and one token count per sequence (page p of
+    every layer's pool belongs to the same tokens).  ``reserve`` hands out pages
+    on the host; appending, reading and attending are the layers' calls; then
+    ``advance`` counts the new tokens.  A captured decode loop reserves ahead and
+    advances with ``pos.add_(1)`` inside the capture.
+    """
+
+    def __init__(self, n_layers: int, nseq: int, n_pages: int, max_tokens: int, n_kv_heads: int, head_dim: int,
+                 device="cuda"):
+        self.nseq, self.n_kv_heads, self.head_dim = nseq, n_kv_heads, head_dim
+        self.max_pages = -(-max_tokens // PAGE)
+        block = abi.m2_kv4_page_bytes(n_kv_heads, head_dim)
+        if not block or self.max_pages <= 0:
+            raise abi.M2Error("Kv4Cache", abi.M2_ERR_UNSUPPORTED)
+        self.pages = [_empty((n_pages, block), torch.uint8, device) for _ in range(n_layers)]
+        self.table = _empty((nseq, self.max_pages), torch.int32, device)
+        self.table.fill_(-1)
+        self.pos = _zeros((nseq,), torch.int32, device)  # tokens held, for the kernels
+        self.tokens = [0] * nseq                         # the same, on the host
+        self._owned = [[] for _ in range(nseq)]
+        self._free = list(range(n_pages - 1, -1, -1))
+        self.struct = [abi.kv4_cache(p, n_pages, n_kv_heads, head_dim, self.table, nseq, self.max_pages)
+                       for p in self.pages]
+
+    def reserve(self, new) -> None:
+        """Pages for new[i] more tokens of each sequence."""
+        need = [-(-(t + n) // PAGE) - len(o) for t, n, o in zip(self.tokens, new, self._owned)]
+        if sum(max(0, n) for n in need) > len(self._free):
+            raise RuntimeError("Kv4Cache: out of pages")
+        for i, n in enumerate(need):
+            if n <= 0:
+                continue
+            have = len(self._owned[i])
+            if have + n > self.max_pages:
+                raise RuntimeError(f"Kv4Cache: sequence {i} would pass max_tokens")
+            got = [self._free.pop() for _ in range(n)]
+            self._owned[i] += got
+            self.table[i, have:have + n].copy_(torch.tensor(got, dtype=torch.int32))
+
+    def advance(self, new) -> None:
+        """Counts new[i] appended tokens of each sequence (on the device unless the capture did it)."""
+        self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
+        self.tokens = [t + n for t, n in zip(self.tokens, new)]
+
+    def release(self, seq: int) -> None:
+        """Gives a finished sequence's pages back."""
+        self._free += reversed(self._owned[seq])
+        self._owned[seq] = []
+        self.tokens[seq] = 0
+        self.pos[seq] = 0
+        self.table[seq].fill_(-1)
+
+
+class DeviceAttention:
+    """One attention mixer: rows of hidden -> q, k, v projection -> head norm and rotation ->
+    attention -> output projection.  ``p``: ``synth.make_attention`` or the like."""
+
+    def __init__(self, p: dict, device="cuda"):
+        d = p["dims"]
+        self.hidden, self.H, self.Hkv, self.D = d["hidden"], d["heads"], d["kv_heads"], d["head_dim"]
+        self.rot, self.eps = d["rot_dim"], d["eps"]
+        self.scale = self.D ** -0.5
+        self.n_qkv = (self.H + 2 * self.Hkv) * self.D
+        self.t = {k: to_dev(p[k], device) for k in ("qkv_w", "qkv_s", "o_w", "o_s")}
+        for k in ("q_w", "k_w"):  # head norms, optional
+            self.t[k] = None if p.get(k) is None else to_dev(p[k], device)
+        self.steps = None
+        if self.rot:
+            self.steps = torch.tensor(abi.m2_rope_steps(d["theta"], self.rot), dtype=torch.int64).to(device)
+        self.device = device
+
+    def buffers(self, max_rows: int, max_keys: int = 0, nseq: int = 1) -> dict:
+        """Scratch for calls of up to max_rows token rows (prompts over cached tokens: max_keys cached and new
+        tokens of all sequences).  Layers run one after the other can share it."""
+        bf, dev = torch.bfloat16, self.device
+        return dict(qkv=_empty((max_rows, self.n_qkv), bf, dev), q=_empty((max_rows, self.H * self.D), bf, dev),
+                    k=_empty((max_rows, self.Hkv * self.D), bf, dev),
+                    attn=_empty((max_rows, self.H * self.D), bf, dev),
+                    keys=_empty((max(max_keys, 1), 2 * self.Hkv * self.D), bf, dev),
+                    ws=_empty((abi.m2_attn_decode_kv4_workspace_bytes(nseq, self.H, self.Hkv, self.D),), torch.uint8, dev))
+
+    def _project(self, x, b, row_pos, stream):
+        T, H, Hkv, D, n = x.shape[0], self.H, self.Hkv, self.D, self.n_qkv
+        qkv = b["qkv"]
+        abi.w8a16_gemv(x, self.t["qkv_w"], self.t["qkv_s"], qkv, T, n, self.hidden, stream)
+        abi.m2_qk_norm_rope(qkv, n, qkv[:, H * D:], n, b["q"], H * D, b["k"], Hkv * D, self.t["q_w"], self.t["k_w"],
+                            row_pos, self.steps, T, H, Hkv, D, self.rot, False, self.eps, stream)
+        return b["q"], b["k"], qkv[:, (H + Hkv) * D:]
+
+    def _output(self, b, out, stream):
+        abi.w8a16_gemv(b["attn"], self.t["o_w"], self.t["o_s"], out, out.shape[0], self.hidden, self.H * self.D, stream)
+
+    def prefill(self, x, new, row_pos, cache: Kv4Cache, layer: int, b: dict, out, stream=None) -> None:
+        """x, out [sum(new)][hidden] bf16: new[i] tokens of each sequence, after those that the cache holds.
+        row_pos: device int32, each row's position.  Appends to the cache (reserved before); the caller advances."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        H, Hkv, D = self.H, self.Hkv, self.D
+        q, k, v = self._project(x, b, row_pos, s)
+        cu, all_ = [0], [0]
+        for n, t in zip(new, cache.tokens):
+            cu.append(cu[-1] + n)
+            all_.append(all_[-1] + n + t)
+        abi.m2_kv4_append(cache.struct[layer], k, Hkv * D, v, self.n_qkv, cu, cache.pos, s)
+        ld_k, ld_v = Hkv * D, self.n_qkv
+        if all_[-1] > cu[-1]:
+            # earlier tokens: attend to the cache's rows, as the single tokens after this will
+            k, v, ld_k, ld_v = b["keys"], b["keys"][:, Hkv * D:], 2 * Hkv * D, 2 * Hkv * D
+            abi.m2_kv4_gather(cache.struct[layer], k, ld_k, v, ld_v, all_, s)
+        abi.m2_attn_prefill_varlen(q, H * D, k, ld_k, v, ld_v, b["attn"], H * D, H, Hkv, D, cu, all_, self.scale, s)
+        self._output(b, out, s)
+
+    def decode(self, x, cache: Kv4Cache, layer: int, b: dict, kv_len, out, stream=None) -> None:
+        """x, out [nseq][hidden] bf16: one token of every sequence; kv_len = cache.pos + 1 (device int32).
+        Appends and attends; the caller advances.  Can be captured."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        H, Hkv, D = self.H, self.Hkv, self.D
+        q, k, v = self._project(x, b, cache.pos, s)
+        abi.m2_kv4_append(cache.struct[layer], k, Hkv * D, v, self.n_qkv, range(cache.nseq + 1), cache.pos, s)
+        abi.m2_attn_decode_kv4(cache.struct[layer], q, H * D, b["attn"], H * D, H, kv_len, self.scale, b["ws"],
+                               b["ws"].numel(), s)
+        self._output(b, out, s)

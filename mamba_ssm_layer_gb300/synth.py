@@ -102,6 +102,24 @@ def make_layer(dims: dict, workload: int, layer: int = 0, in_fmt: str = "fp8", o
     return out
 
 
+# Attention mixers of a hybrid stack beside the two layer sizes.
+TINY_ATTENTION = dict(hidden=256, heads=4, kv_heads=2, head_dim=64, rot_dim=64, theta=10000.0, eps=1e-5)
+ATTENTION_4096 = dict(hidden=4096, heads=32, kv_heads=8, head_dim=128, rot_dim=128, theta=10000.0, eps=1e-5)
+_T_QKV, _T_O, _T_QN, _T_KN = 20, 21, 22, 23
+
+
+def make_attention(dims: dict, workload: int, layer: int = 0) -> dict:
+    """Parameters of one attention mixer as numpy arrays: E4M3 projections, bf16 head norm weights."""
+    H, K, D, hid = dims["heads"], dims["kv_heads"], dims["head_dim"], dims["hidden"]
+    key = (workload, layer)
+    out = dict(dims=dict(dims))
+    out["qkv_w"], out["qkv_s"] = make_weight((H + 2 * K) * D, hid, "fp8", *key, _T_QKV)
+    out["o_w"], out["o_s"] = make_weight(hid, H * D, "fp8", *key, _T_O)
+    out["q_w"] = to_bf16_bits(1.0 + 0.1 * _rng(*key, _T_QN).standard_normal(D))
+    out["k_w"] = to_bf16_bits(1.0 + 0.1 * _rng(*key, _T_KN).standard_normal(D))
+    return out
+
+
 def make_hidden(rows: int, hidden: int, *key) -> np.ndarray:
     """N(0,1) bf16 hidden rows [rows][hidden]; key = (workload, stream id, step)."""
     return to_bf16_bits(_rng(*key, _T_HIDDEN).standard_normal((rows, hidden)))
