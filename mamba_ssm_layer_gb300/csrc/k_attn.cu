@@ -36,6 +36,12 @@ constexpr int kAtThreads = 384;
 // steps of 8): 2 * 224 + 56 = 3 * 168.
 constexpr int kAtRegsSoftmax = 224, kAtRegsOther = 56;
 constexpr int kAtRows = 128;      // query rows of a tile, keys of a block
+// Up to so many tile pairs are handed out longest first; with more of them, later
+// ones first (a sequence's longest) spreads the work as well.  Measured by the
+// blocks of the busiest CTA against the mean: four chunks over up to 6000 tokens
+// (33 pairs x 8 groups) 95 to 79 sorted, 113 to 79 unsorted; one prompt of 8192
+// (128 pairs) 237 to 232 both ways.
+constexpr int kAtSorted = 512;
 constexpr int kAtItems = 4;       // items handed on ahead of their use
 constexpr int kAtMaskBlocks = 4;  // key blocks that some row of the two tiles sees only in part: at most 3
 
@@ -46,7 +52,11 @@ struct AtCfg {
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kTile;
   static constexpr int kBars = kKV + kStages * kTile;
-  static constexpr uint32_t kTmS = 0, kTmO = 256;          // tensor-memory columns: S 2 x 128, O 2 x D
+  // Tensor-memory columns: S 2 x 128, O 2 x D, and P over S, or with D = 64 next to
+  // O: then the next scores are computed as soon as S has been read, under the
+  // softmax, and a block takes what the softmax takes.
+  static constexpr bool kApart = D == 64;
+  static constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = kApart ? 256 + 2 * D : 0, kTmPStep = kApart ? 64 : 128;
 };
 // What a CTA works on: the copies' thread works it out and hands it on through
 // shared memory.
@@ -60,6 +70,7 @@ struct __align__(16) AtItem {
 };
 struct AtBars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2], fin;
+  uint64_t s_free[2], pv_done[2];  // kApart: S has been read; the block's values product is complete
   uint64_t full[10], empty[10];
   uint64_t look, clean;  // a masked block's values may be looked through; they are
   uint64_t item_full[kAtItems], item_empty[kAtItems];
@@ -86,8 +97,10 @@ struct AtArgs {
   float scale_log2; // scale * log2(e)
   int32_t nseq;
   int32_t items;    // tile pairs * groups
+  int32_t sorted;   // order[] holds the pairs, most key blocks first
   int32_t cu_q[kSeqs + 1], cu_k[kSeqs + 1];
   int32_t tile[kSeqs + 1];  // first tile pair of each sequence
+  uint16_t order[kAtSorted];
 };
 
 // 32 columns of this warp's 32 lanes, without waiting.
@@ -209,8 +222,7 @@ __device__ __forceinline__ int at_pick(int k, int items) {
 __device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
   AtItem it;
   const int tokens = kAtRows >> a.pk_log;  // of one tile
-  const int total = a.tile[a.nseq];
-  const int p = total - 1 - id / a.groups;  // late tiles (the most keys) first
+  const int k = id / a.groups, p = a.sorted ? a.order[k] : a.tile[a.nseq] - 1 - k;
   it.hg = id % a.groups;
   int lo = 0, hi = a.nseq;  // the last sequence whose first pair is <= p
   while (hi - lo > 1) {
@@ -296,6 +308,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->s_free[t], 4);
+      mbar_init(&bars->pv_done[t], 1);
       mbar_init(&bars->p_full[t][0], 4);
       mbar_init(&bars->p_full[t][1], 4);
       mbar_init(&bars->o_done[t], 1);
@@ -391,18 +405,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       };
       auto full = [&](int i) { return wait(&bars->full[i % NS], (i / NS) & 1); };
       const uint32_t q0 = (smem_addr(smem + C::kQ) & 0x3FFFFu) >> 4, kv0 = (smem_addr(smem + C::kKV) & 0x3FFFFu) >> 4;
+      int ns[2] = {0, 0};  // score tiles issued
       // S of tile t with K copy i
-      auto scores = [&](int t, int i, bool last, bool look) {
+      auto scores = [&](int t, int i, bool last) {
+        if (C::kApart && ns[t] > 0 && !wait(&bars->s_free[t], (ns[t] - 1) & 1)) return;
+        ++ns[t];
         if (!leader) return;
+        if (C::kApart) tc_fence_after();
         at_issue_scores<D>(tmem + C::kTmS + t * kAtRows, q0 + t * (C::kTile >> 4), kv0 + (i % NS) * (C::kTile >> 4));
         tc_commit(&bars->s_full[t]);
         if (last) tc_commit(&bars->q_empty[t]);  // the tile's last scores
-        if (look) mbar_arrive(&bars->look);
       };
       for (int pick = 0; !dead; ++pick) {
         AtItem it;
         if (!at_next(bars, pick, lane, it)) break;
-        const int n = max(it.n0, it.n1), lead = it.n0 ? 0 : 1;
+        const int n = max(it.n0, it.n1);
         if (n == 0) continue;
         if (!full(kv)) break;
 #pragma unroll
@@ -410,14 +427,27 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           const int nt = t ? it.n1 : it.n0;
           if (!nt || !wait(&bars->q_full[t], nq[t] & 1)) continue;
           ++nq[t];
-          scores(t, kv, nt == 1, it.jm == 0 && t == lead);
+          scores(t, kv, nt == 1);
         }
         if (dead) break;
-        if (leader) tc_commit(&bars->empty[kv % NS]);
+        if (leader) {
+          tc_commit(&bars->empty[kv % NS]);
+          if (it.jm == 0) mbar_arrive(&bars->look);
+        }
         for (int j = 0; j < n && !dead; ++j) {
           const int vi = kv + 2 * j + 1, kn = vi + 1;
+          if (C::kApart && j + 1 < n) {
+            if (!full(kn)) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (!dead && j + 1 < (t ? it.n1 : it.n0)) scores(t, kn, j + 2 == (t ? it.n1 : it.n0));
+            if (dead) break;
+            if (leader) tc_commit(&bars->empty[kn % NS]);
+          }
           if (!full(vi)) break;
           if (j >= it.jm && !wait(&bars->clean, cleaned++ & 1)) break;
+          // the next block's values may be looked through (its first scores are issued, or follow at once)
+          if (leader && j + 1 < n && j + 1 >= it.jm && C::kApart) mbar_arrive(&bars->look);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int nt = t ? it.n1 : it.n0;
@@ -427,18 +457,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               if (!wait(&bars->p_full[t][hf], np[t] & 1)) break;
               tc_fence_after();
               if (leader)
-                at_issue_values<D>(tmem + C::kTmO + t * D, tmem + C::kTmS + t * kAtRows + 32 * hf,
+                at_issue_values<D>(tmem + C::kTmO + t * D, tmem + C::kTmP + t * C::kTmPStep + 32 * hf,
                                    kv0 + (vi % NS) * (C::kTile >> 4) + hf * (8192 >> 4), j > 0 || hf > 0);
             }
             if (dead) continue;
             ++np[t];
             if (leader) {
+              if (C::kApart) tc_commit(&bars->pv_done[t]);
               if (t == (j < it.n1 ? 1 : 0)) tc_commit(&bars->empty[vi % NS]);  // the last tile that uses this block
               if (j + 1 == nt) tc_commit(&bars->o_done[t]);
             }
-            if (j + 1 < nt && full(kn)) scores(t, kn, j + 2 == nt, j + 1 >= it.jm && t == (j + 1 < it.n0 ? 0 : 1));
+            if (!C::kApart && j + 1 < nt && full(kn)) {
+              scores(t, kn, j + 2 == nt);
+              if (leader && j + 1 >= it.jm && t == (j + 1 < it.n0 ? 0 : 1)) mbar_arrive(&bars->look);
+            }
           }
-          if (!dead && j + 1 < n && leader) tc_commit(&bars->empty[kn % NS]);
+          if (!C::kApart && !dead && j + 1 < n && leader) tc_commit(&bars->empty[kn % NS]);
         }
         kv += 2 * n;
       }
@@ -483,6 +517,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int t = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + C::kTmS + t * kAtRows, to = tmem + lanes + C::kTmO + t * D;
+    const uint32_t tp = tmem + lanes + C::kTmP + t * C::kTmPStep;
     const bool pos = a.scale_log2 > 0.0f;
     const float c = pos ? a.scale_log2 : 1.0f;  // a scale <= 0 is applied to the scores first
     int ns = 0, no = 0;                         // score tiles and outputs before this item
@@ -507,6 +542,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, s + 32 * i);
         tmem_ld_wait<kAtRows>(s);
+        if (C::kApart) {  // S may be computed anew
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->s_free[t]);
+        }
         if (!pos) {
 #pragma unroll
           for (int i = 0; i < kAtRows; ++i) s[i] *= a.scale_log2;
@@ -528,6 +568,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (j == 0) {
           m = mn;
         } else {
+          if (C::kApart) {  // P may be written and O rescaled: the last block's product is complete
+            if (!__all_sync(0xffffffffu, at_wait(&bars->pv_done[t], (ns + j - 1) & 1))) {
+              dead = true;
+              break;
+            }
+            tc_fence_after();
+          }
           const bool grow = (mn - m) * c > 8.0f;
           if (__any_sync(0xffffffffu, grow)) {  // rescale what was summed so far (its products are complete)
             const float f = grow ? ex2((m - mn) * c) : 1.0f;
@@ -557,7 +604,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             sum[k & 1] = fadd2(sum[k & 1], e);
             p[k] = pack_bf16x2(e.x, e.y);
           }
-          tmem_st16(ts + i / 2, p);
+          tmem_st16(tp + i / 2, p);
           if (i % 64 == 32) {  // 64 keys' probabilities are there
             tmem_st_wait();
             tc_fence_before();
@@ -692,6 +739,22 @@ static cudaError_t launch_attn(const AttnArgs& g, cudaStream_t s) {
   cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
   if (e != cudaSuccess) return e;
   a.items = a.tile[g.nseq] * a.groups;
+  a.sorted = a.tile[g.nseq] <= kAtSorted ? 1 : 0;
+  if (a.sorted) {  // counting sort by key blocks (longer than the last bucket: any order)
+    constexpr int kBuckets = 256;
+    uint16_t first[kBuckets + 1] = {0}, len[kAtSorted];
+    for (int i = 0; i < g.nseq; ++i) {
+      const int nq = a.cu_q[i + 1] - a.cu_q[i], nk = a.cu_k[i + 1] - a.cu_k[i];
+      for (int t = a.tile[i]; t < a.tile[i + 1]; ++t) {
+        const int64_t end = (int64_t)(t - a.tile[i] + 1) * 2 * tokens;
+        const int64_t last = (end < nq ? end : nq) - 1 + nk - nq, n = last < 0 ? 0 : last / kAtRows + 1;
+        len[t] = (uint16_t)(kBuckets - 1 - (n < kBuckets ? n : kBuckets - 1));
+        ++first[len[t] + 1];
+      }
+    }
+    for (int b = 0; b < kBuckets; ++b) first[b + 1] += first[b];
+    for (int t = 0; t < a.tile[g.nseq]; ++t) a.order[first[len[t]]++] = (uint16_t)t;
+  }
   trace_pre(K_ATTN_PREFILL, s);
   e = launch_k(kern, dim3(a.items < num_sms() ? a.items : num_sms()), dim3(kAtThreads), smem, s, true, q, k, v, a);
   trace_post(K_ATTN_PREFILL, s);
