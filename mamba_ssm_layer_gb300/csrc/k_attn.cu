@@ -25,6 +25,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "m2_common.cuh"
 #include "m2_kernels.h"
 #include "m2_tc.cuh"
@@ -52,11 +54,11 @@ struct AtCfg {
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kTile;
   static constexpr int kBars = kKV + kStages * kTile;
-  // Tensor-memory columns: S 2 x 128, O 2 x D, and P over S, or with D = 64 next to
-  // O: then the next scores are computed as soon as S has been read, under the
-  // softmax, and a block takes what the softmax takes.
-  static constexpr bool kApart = D == 64;
-  static constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = kApart ? 256 + 2 * D : 0, kTmPStep = kApart ? 64 : 128;
+  // Tensor-memory columns: S 2 x 128 (P over it), O 2 x D.  (With D = 64 there is
+  // room for P of its own, so that the next scores run under the softmax; the two
+  // tiles' softmax phases then run in step, and four chunks over cached tokens took
+  // 138 us instead of 128.)
+  static constexpr uint32_t kTmS = 0, kTmO = 256;
 };
 // What a CTA works on: the copies' thread works it out and hands it on through
 // shared memory.
@@ -70,7 +72,6 @@ struct __align__(16) AtItem {
 };
 struct AtBars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_done[2], fin;
-  uint64_t s_free[2], pv_done[2];  // kApart: S has been read; the block's values product is complete
   uint64_t full[10], empty[10];
   uint64_t look, clean;  // a masked block's values may be looked through; they are
   uint64_t item_full[kAtItems], item_empty[kAtItems];
@@ -308,8 +309,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->s_free[t], 4);
-      mbar_init(&bars->pv_done[t], 1);
       mbar_init(&bars->p_full[t][0], 4);
       mbar_init(&bars->p_full[t][1], 4);
       mbar_init(&bars->o_done[t], 1);
@@ -396,85 +395,102 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       // The whole warp walks the blocks, so that addresses and descriptors stay
       // warp-uniform; one elected lane issues.
       const bool leader = elect_one();
-      int kv = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // copies, Q tiles and probability tiles used
-      int cleaned = 0;                             // masked blocks looked through
-      bool dead = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead) dead = !__all_sync(0xffffffffu, at_wait(bar, parity));
-        return !dead;
-      };
-      auto full = [&](int i) { return wait(&bars->full[i % NS], (i / NS) & 1); };
+      using T0 = std::integral_constant<int, 0>;
+      using T1 = std::integral_constant<int, 1>;
+      int nq[2] = {0, 0}, np[2] = {0, 0};  // Q and probability tiles used
+      int cleaned = 0;                     // masked blocks looked through
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, at_wait(bar, parity)); };
       const uint32_t q0 = (smem_addr(smem + C::kQ) & 0x3FFFFu) >> 4, kv0 = (smem_addr(smem + C::kKV) & 0x3FFFFu) >> 4;
-      int ns[2] = {0, 0};  // score tiles issued
-      // S of tile t with K copy i
-      auto scores = [&](int t, int i, bool last) {
-        if (C::kApart && ns[t] > 0 && !wait(&bars->s_free[t], (ns[t] - 1) & 1)) return;
-        ++ns[t];
-        if (!leader) return;
-        if (C::kApart) tc_fence_after();
-        at_issue_scores<D>(tmem + C::kTmS + t * kAtRows, q0 + t * (C::kTile >> 4), kv0 + (i % NS) * (C::kTile >> 4));
-        tc_commit(&bars->s_full[t]);
-        if (last) tc_commit(&bars->q_empty[t]);  // the tile's last scores
+      // S of a tile with the K tile of ring slot `sl`
+      auto scores = [&](auto tile, int sl, bool last) {
+        constexpr int t = decltype(tile)::value;
+        if (leader) {
+          at_issue_scores<D>(tmem + C::kTmS + t * kAtRows, q0 + t * (C::kTile >> 4), kv0 + sl * (C::kTile >> 4));
+          tc_commit(&bars->s_full[t]);
+          if (last) tc_commit(&bars->q_empty[t]);  // the tile's last scores
+        }
       };
+      // O += P V of a tile with the V tile of ring slot `sl`; free: no other tile needs it, last: the tile's last block
+      auto values = [&](auto tile, int sl, bool add, bool free, bool last) {
+        constexpr int t = decltype(tile)::value;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {  // the first 64 keys' probabilities come before the others'
+          if (!wait(&bars->p_full[t][hf], np[t] & 1)) return false;
+          tc_fence_after();
+          if (leader)
+            at_issue_values<D>(tmem + C::kTmO + t * D, tmem + C::kTmS + t * kAtRows + 32 * hf,
+                               kv0 + sl * (C::kTile >> 4) + hf * (8192 >> 4), add || hf > 0);
+        }
+        ++np[t];
+        if (leader) {
+          if (free) tc_commit(&bars->empty[sl]);
+          if (last) tc_commit(&bars->o_done[t]);
+        }
+        return true;
+      };
+      int sl = 0, ph = 0;  // ring slot and phase of the item's next copy
+      auto step = [&](int& slot, int& phase, int k) {
+        slot += k;
+        if (slot >= NS) slot -= NS, phase ^= 1;
+      };
+      bool dead = false;
       for (int pick = 0; !dead; ++pick) {
         AtItem it;
         if (!at_next(bars, pick, lane, it)) break;
-        const int n = max(it.n0, it.n1);
+        const int n0 = it.n0, n1 = it.n1, n = max(n0, n1);
         if (n == 0) continue;
-        if (!full(kv)) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? it.n1 : it.n0;
-          if (!nt || !wait(&bars->q_full[t], nq[t] & 1)) continue;
-          ++nq[t];
-          scores(t, kv, nt == 1);
+        dead = true;  // until the item is through
+        if (!wait(&bars->full[sl], ph)) break;
+        if (n0) {
+          if (!wait(&bars->q_full[0], nq[0]++ & 1)) break;
+          scores(T0(), sl, n0 == 1);
         }
-        if (dead) break;
+        if (n1) {
+          if (!wait(&bars->q_full[1], nq[1]++ & 1)) break;
+          scores(T1(), sl, n1 == 1);
+        }
         if (leader) {
-          tc_commit(&bars->empty[kv % NS]);
+          tc_commit(&bars->empty[sl]);
           if (it.jm == 0) mbar_arrive(&bars->look);
         }
-        for (int j = 0; j < n && !dead; ++j) {
-          const int vi = kv + 2 * j + 1, kn = vi + 1;
-          if (C::kApart && j + 1 < n) {
-            if (!full(kn)) break;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (!dead && j + 1 < (t ? it.n1 : it.n0)) scores(t, kn, j + 2 == (t ? it.n1 : it.n0));
-            if (dead) break;
-            if (leader) tc_commit(&bars->empty[kn % NS]);
+        int vs = sl, vph = ph, ks, kph, j = 0;  // slots of V_j and K_j+1
+        step(vs, vph, 1);
+        for (;; ++j) {
+          if (j == n) {
+            dead = false;
+            break;
           }
-          if (!full(vi)) break;
-          if (j >= it.jm && !wait(&bars->clean, cleaned++ & 1)) break;
-          // the next block's values may be looked through (its first scores are issued, or follow at once)
-          if (leader && j + 1 < n && j + 1 >= it.jm && C::kApart) mbar_arrive(&bars->look);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nt = t ? it.n1 : it.n0;
-            if (j >= nt || dead) continue;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {  // the first 64 keys' probabilities come before the others'
-              if (!wait(&bars->p_full[t][hf], np[t] & 1)) break;
-              tc_fence_after();
-              if (leader)
-                at_issue_values<D>(tmem + C::kTmO + t * D, tmem + C::kTmP + t * C::kTmPStep + 32 * hf,
-                                   kv0 + (vi % NS) * (C::kTile >> 4) + hf * (8192 >> 4), j > 0 || hf > 0);
-            }
-            if (dead) continue;
-            ++np[t];
-            if (leader) {
-              if (C::kApart) tc_commit(&bars->pv_done[t]);
-              if (t == (j < it.n1 ? 1 : 0)) tc_commit(&bars->empty[vi % NS]);  // the last tile that uses this block
-              if (j + 1 == nt) tc_commit(&bars->o_done[t]);
-            }
-            if (!C::kApart && j + 1 < nt && full(kn)) {
-              scores(t, kn, j + 2 == nt);
-              if (leader && j + 1 >= it.jm && t == (j + 1 < it.n0 ? 0 : 1)) mbar_arrive(&bars->look);
+          ks = vs, kph = vph;
+          step(ks, kph, 1);
+          // V_j is there, and looked through if some row must not see all of it
+          if (!wait(&bars->full[vs], vph) || (j >= it.jm && !wait(&bars->clean, cleaned++ & 1))) break;
+          const bool more = j + 1 < n, look = leader && more && j + 1 >= it.jm;
+          if (j < n0) {
+            if (!values(T0(), vs, j > 0, j >= n1, j + 1 == n0)) break;
+            if (j + 1 < n0) {
+              if (!wait(&bars->full[ks], kph)) break;
+              scores(T0(), ks, j + 2 == n0);
+              if (look) mbar_arrive(&bars->look);
             }
           }
-          if (!C::kApart && !dead && j + 1 < n && leader) tc_commit(&bars->empty[kn % NS]);
+          if (j < n1) {
+            if (!values(T1(), vs, j > 0, true, j + 1 == n1)) break;
+            if (j + 1 < n1) {
+              if (j + 1 >= n0) {
+                if (!wait(&bars->full[ks], kph)) break;
+                if (look) mbar_arrive(&bars->look);
+              }
+              scores(T1(), ks, j + 2 == n1);
+            }
+          }
+          if (more && leader) tc_commit(&bars->empty[ks]);
+          vs = ks, vph = kph;
+          step(vs, vph, 1);
         }
-        kv += 2 * n;
+        // past the item's 2 n copies
+        const int past = sl + 2 * n;
+        ph ^= past / NS & 1;
+        sl = past % NS;
       }
       if (leader) {
         tc_commit(&bars->fin);  // everything issued here is done before tensor memory is freed
@@ -517,7 +533,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int t = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + C::kTmS + t * kAtRows, to = tmem + lanes + C::kTmO + t * D;
-    const uint32_t tp = tmem + lanes + C::kTmP + t * C::kTmPStep;
     const bool pos = a.scale_log2 > 0.0f;
     const float c = pos ? a.scale_log2 : 1.0f;  // a scale <= 0 is applied to the scores first
     int ns = 0, no = 0;                         // score tiles and outputs before this item
@@ -542,11 +557,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32_async(ts + 32 * i, s + 32 * i);
         tmem_ld_wait<kAtRows>(s);
-        if (C::kApart) {  // S may be computed anew
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->s_free[t]);
-        }
         if (!pos) {
 #pragma unroll
           for (int i = 0; i < kAtRows; ++i) s[i] *= a.scale_log2;
@@ -568,13 +578,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (j == 0) {
           m = mn;
         } else {
-          if (C::kApart) {  // P may be written and O rescaled: the last block's product is complete
-            if (!__all_sync(0xffffffffu, at_wait(&bars->pv_done[t], (ns + j - 1) & 1))) {
-              dead = true;
-              break;
-            }
-            tc_fence_after();
-          }
           const bool grow = (mn - m) * c > 8.0f;
           if (__any_sync(0xffffffffu, grow)) {  // rescale what was summed so far (its products are complete)
             const float f = grow ? ex2((m - mn) * c) : 1.0f;
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             sum[k & 1] = fadd2(sum[k & 1], e);
             p[k] = pack_bf16x2(e.x, e.y);
           }
-          tmem_st16(tp + i / 2, p);
+          tmem_st16(ts + i / 2, p);
           if (i % 64 == 32) {  // 64 keys' probabilities are there
             tmem_st_wait();
             tc_fence_before();

@@ -91,7 +91,7 @@ def test_example_runs():
 
 def test_kernels_time_out_cleanly():
     """Pipeline waits that give up at once: the kernels record it, wait for their own copies and products, return,
-    and compute correctly afterwards.  The decode reads enough (80 MB) for copies to be waited for."""
+    and compute correctly afterwards.  The decode reads 80 MB that L2 does not hold, so that copies are waited for."""
     g = torch.Generator(device="cuda").manual_seed(1)
     H, K, D, T, n_q = 32, 8, 128, 70000, 2000
     q, k, v = (torch.randn(r, w * D, device="cuda", generator=g).to(torch.bfloat16) for r, w in ((n_q, H), (T, K), (T, K)))
@@ -106,6 +106,7 @@ def test_kernels_time_out_cleanly():
         o2 = torch.zeros(1, H * D, dtype=torch.bfloat16, device="cuda")
         abi.m2_attn_prefill_varlen(q, H * D, k, K * D, v, K * D, o1, H * D, H, K, D, [0, n_q], [0, n_q], 0.1)
         s1 = abi.m2_device_status(clear=True)
+        torch.zeros(512 << 20, dtype=torch.uint8, device="cuda")  # through L2
         abi.m2_attn_decode_kv4(c.struct[0], q, H * D, o2, H * D, H, n, 0.1, ws, ws.numel())
         return o1, o2, s1, abi.m2_device_status(clear=True)
 
