@@ -13,8 +13,13 @@
 // Queries enter as f16 rows prescaled by an exact power of two.  Scores, sums and
 // outputs are fp32.  Rows that a warp, then a CTA, holds only in part are
 // joined: warps through shared memory, CTAs by attn_decode_combine.
-// Bound: HBM (4.5 bits a value); per unit 256 4-bit conversions, 256 f16x2
-// multiplications and 64 HN/8 MMAs a warp keep the other pipes close behind.
+// Bound: HBM (4.5 bits a value) and, as close, the issue rate: a unit is about
+// 1160 instructions of a warp (256 conversions of two codes, 256 multiplications by
+// scales, 64 MMAs at HN = 8), 82% of the issue slots while a span is streamed.
+// Measured at 32 + 8 heads of 128: 131000 tokens of one sequence 37 us (4.1 TB/s),
+// 64 sequences of 64..4096 tokens 43 us (4.0 TB/s); 6 to 7 us of that are the way to
+// the first data, 4 to 5 the joining.  8 warps with 3 stages took 48 us instead of 37
+// in the kernel itself, 12 warps with 128 registers the same.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -639,75 +644,62 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
   if (tid < 2 && !a.by_row) a.cta_seg[2 * cta + tid] = sh->cta_seg[tid];
 }
 
-// Rows cut between CTAs: CTA c joins the row that began in span c and goes on.
-// A thread holds four channels of a head; the parts are dealt out over thread
-// groups, so that each loads its few parts at once, and joined through shared
-// memory.
-constexpr int kAcThreads = 1024;
+// Rows cut between CTAs: block (c, h) joins head h of the row that began in span
+// c and goes on.  D/4 threads hold four channels each; the parts are dealt out
+// over groups of them and joined through shared memory.  The first parts are
+// loaded before it is known how many there are (any span's record may be read),
+// and the blocks are small enough to wait on the SMs for the spans' end.
+constexpr int kAcThreads = 128;
 template <int D, int NT>
-__global__ void __launch_bounds__(kAcThreads) attn_decode_combine_kernel(const AdArgs a) {
-  constexpr int HN = 8 * NT, REC = ad_record<D, HN>(), ST = AdCfg<D>::kStride;
-  struct Sum {
-    float m, l;
-    float4 o;
-  };
-  __shared__ Sum part[kAcThreads];
+__global__ void __launch_bounds__(kAcThreads, 16) attn_decode_combine_kernel(const AdArgs a) {
+  constexpr int HN = 8 * NT, REC = ad_record<D, HN>(), ST = AdCfg<D>::kStride, P = D / 4, GR = kAcThreads / P;
+  __shared__ float pm[GR], pl[GR];
+  __shared__ float4 po[kAcThreads];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x, tid = threadIdx.x;
+  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, g = tid / P, d = tid % P * 4;
   const int seg = a.cta_seg[2 * c + 1];
+  auto load = [&](int y, float& m, float& l, float4& o) {
+    const float* r = a.cta_part + (size_t)(y == 0 ? 2 * c + 1 : 2 * min(c + y, a.nc - 1)) * REC;
+    m = r[h], l = r[HN + h];
+    o = *reinterpret_cast<const float4*>(r + 2 * HN + h * ST + d);
+  };
+  float m, l;
+  float4 o;
+  load(g, m, l, o);
   int k = 1;  // parts: this span's, then those of the spans that the row goes on through
   for (int x = c + 1; x < a.nc; x += kAcThreads) {
     const int n = __syncthreads_count(x + tid < a.nc && a.cta_seg[2 * (x + tid)] == seg);
     k += n;
     if (n < kAcThreads) break;
   }
-  if (seg < 0) return;
-  const int pos = ad_heads(a, seg, HN) * (D / 4), groups = min(16, kAcThreads / pos), g = tid / pos, i = tid - g * pos;
-  const int h = i / (D / 4), d = i % (D / 4) * 4;
-  Sum s;
-  s.m = -INFINITY, s.l = 0.0f, s.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (g < groups) {
-    for (int y0 = g; y0 < k; y0 += 4 * groups) {
-      Sum v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int y = y0 + j * groups;
-        v[j].m = -INFINITY, v[j].l = 0.0f, v[j].o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (y < k) {
-          const float* r = a.cta_part + (size_t)(y == 0 ? 2 * c + 1 : 2 * (c + y)) * REC;
-          v[j].m = r[h], v[j].l = r[HN + h];
-          v[j].o = *reinterpret_cast<const float4*>(r + 2 * HN + h * ST + d);
-        }
-      }
-      const float top = fmaxf(fmaxf(fmaxf(s.m, v[0].m), fmaxf(v[1].m, v[2].m)), v[3].m);
-      const float f = ad_weight(s.m, s.l, top);
-      s.m = top;
-      s.l *= f, s.o.x *= f, s.o.y *= f, s.o.z *= f, s.o.w *= f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float w = ad_weight(v[j].m, v[j].l, top);
-        s.l = fmaf(v[j].l, w, s.l);
-        s.o.x = fmaf(v[j].o.x, w, s.o.x), s.o.y = fmaf(v[j].o.y, w, s.o.y), s.o.z = fmaf(v[j].o.z, w, s.o.z),
-        s.o.w = fmaf(v[j].o.w, w, s.o.w);
-      }
-    }
-    part[tid] = s;
+  if (seg < 0 || h >= ad_heads(a, seg, HN)) return;
+  if (g >= k) m = -INFINITY, l = 0.0f, o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int y = g + GR; y < k; y += GR) {
+    float m1, l1;
+    float4 v;
+    load(y, m1, l1, v);
+    const float top = fmaxf(m, m1), f = ad_weight(m, l, top), w = ad_weight(m1, l1, top);
+    m = top;
+    l = l * f + l1 * w;
+    o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
   }
+  po[tid] = o;
+  if (d == 0) pm[g] = m, pl[g] = l;
   __syncthreads();
   if (g == 0) {
-    float top = s.m;
-    for (int y = 1; y < groups; ++y) top = fmaxf(top, part[y * pos + i].m);
-    Sum t;
-    t.l = 0.0f, t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int y = 0; y < groups; ++y) {
-      const Sum& v = part[y * pos + i];
-      const float w = ad_weight(v.m, v.l, top);
-      t.l = fmaf(v.l, w, t.l);
-      t.o.x = fmaf(v.o.x, w, t.o.x), t.o.y = fmaf(v.o.y, w, t.o.y), t.o.z = fmaf(v.o.z, w, t.o.z),
-      t.o.w = fmaf(v.o.w, w, t.o.w);
+    float top = m, sum = 0.0f;
+#pragma unroll
+    for (int y = 1; y < GR; ++y) top = fmaxf(top, pm[y]);
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int y = 0; y < GR; ++y) {
+      const float w = ad_weight(pm[y], pl[y], top);
+      const float4 v = po[y * P + tid];
+      sum = fmaf(pl[y], w, sum);
+      t = make_float4(fmaf(v.x, w, t.x), fmaf(v.y, w, t.y), fmaf(v.z, w, t.z), fmaf(v.w, w, t.w));
     }
-    ad_store4(a, seg, HN, h, d, D, t.o, t.l);
+    ad_store4(a, seg, HN, h, d, D, t, sum);
   }
 }
 
@@ -747,7 +739,8 @@ static cudaError_t launch_ad(const AttnDecodeArgs& g, cudaStream_t s) {
   trace_post(K_ATTN_DECODE, s);
   if (e != cudaSuccess || a.by_row) return e;
   trace_pre(K_ATTN_COMBINE, s);
-  e = launch_k(attn_decode_combine_kernel<D, NT>, dim3(a.nc), dim3(kAcThreads), 0, s, true, a);
+  e = launch_k(attn_decode_combine_kernel<D, NT>, dim3(a.nc, a.G < 8 * NT ? a.G : 8 * NT), dim3(kAcThreads), 0, s,
+               true, a);
   trace_post(K_ATTN_COMBINE, s);
   return e;
 }
