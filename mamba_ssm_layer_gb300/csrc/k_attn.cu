@@ -25,6 +25,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "m2_common.cuh"
@@ -99,6 +100,7 @@ struct AtArgs {
   int32_t nseq;
   int32_t items;    // tile pairs * groups
   int32_t sorted;   // order[] holds the pairs, most key blocks first
+  int64_t limit;    // of the pipeline's waits, SM clock cycles
   int32_t cu_q[kSeqs + 1], cu_k[kSeqs + 1];
   int32_t tile[kSeqs + 1];  // first tile pair of each sequence
   uint16_t order[kAtSorted];
@@ -192,12 +194,16 @@ __device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
   swap_pieces(w[1], w[3], 2, lane & 2);
 }
 
-// mbar_wait without a call: a kernel that hands registers between its warps
-// has to be one function.
+// mbar_wait without a call (a kernel that hands registers between its warps has to
+// be one function), its limit from the launch's parameters.  The hardware may hold a
+// suspended wait longer than asked, so that a short limit takes waits that only test
+// (TEST), in a kernel of their own: the waits' own instructions matter.  With both
+// forms in one kernel and the limit read from global memory, every case took 3 to 4%
+// longer.
+template <bool TEST>
 __device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
   const long long t0 = clock64();
-  const bool suspend = limit >= 1000000;
-  while (!(suspend ? mbar_try_wait(bar, parity, 1000u) : mbar_test_wait(bar, parity))) {
+  while (!(TEST ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity, 1000u))) {
     if (clock64() - t0 > limit) {
       record_timeout();
       return false;
@@ -205,12 +211,12 @@ __device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, lo
   }
   return true;
 }
-__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity) {
-  return mbar_test_wait(bar, parity) ||
-         at_wait_until(bar, parity, *reinterpret_cast<volatile long long*>(&g_wait_limit));
+template <bool TEST>
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, const AtArgs& a) {
+  return mbar_test_wait(bar, parity) || at_wait_until<TEST>(bar, parity, a.limit);
 }
 __device__ __forceinline__ bool at_drain(uint64_t* bar, uint32_t parity) {
-  return mbar_test_wait(bar, parity) || at_wait_until(bar, parity, kWaitCycles);
+  return mbar_test_wait(bar, parity) || at_wait_until<false>(bar, parity, kWaitCycles);
 }
 
 // A CTA's k-th item: every other round backwards, so that each CTA gets late
@@ -285,16 +291,17 @@ __device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long
 }
 
 // A consuming warp's next item; false when there is none (or a wait gave up).
-__device__ __forceinline__ bool at_next(AtBars* bars, int pick, int lane, AtItem& it) {
+template <bool TEST>
+__device__ __forceinline__ bool at_next(const AtArgs& a, AtBars* bars, int pick, int lane, AtItem& it) {
   const int sl = pick % kAtItems;
-  if (!__all_sync(0xffffffffu, at_wait(&bars->item_full[sl], (pick / kAtItems) & 1))) return false;
+  if (!__all_sync(0xffffffffu, at_wait<TEST>(&bars->item_full[sl], (pick / kAtItems) & 1, a))) return false;
   it = bars->item[sl];
   __syncwarp();
   if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
   return it.hg >= 0;
 }
 
-template <int D>
+template <int D, bool TEST>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AtArgs a) {
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         AtItem it;
         it.hg = -1;
         if (id >= 0) it = at_item(a, id);
-        if (pick >= kAtItems && !at_wait(&bars->item_empty[sl], ((pick / kAtItems) - 1) & 1)) break;
+        if (pick >= kAtItems && !at_wait<TEST>(&bars->item_empty[sl], ((pick / kAtItems) - 1) & 1, a)) break;
         bars->item[sl] = it;
         mbar_arrive(&bars->item_full[sl]);
         if (id < 0) break;
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         auto load_q = [&](int t) {
           if (!(t ? it.n1 : it.n0) || dead) return;
           int& nq = t ? nq1 : nq0;
-          if (nq > 0 && !at_wait(&bars->q_empty[t], (nq - 1) & 1)) {
+          if (nq > 0 && !at_wait<TEST>(&bars->q_empty[t], (nq - 1) & 1, a)) {
             dead = true;
             return;
           }
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         };
         for (int i = 0; i < 2 * n && !dead; ++i, ++kv) {
           const int s = kv % NS;
-          if (kv >= NS && !at_wait(&bars->empty[s], ((kv / NS) - 1) & 1)) {
+          if (kv >= NS && !at_wait<TEST>(&bars->empty[s], ((kv / NS) - 1) & 1, a)) {
             dead = true;
             break;
           }
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       using T1 = std::integral_constant<int, 1>;
       int nq[2] = {0, 0}, np[2] = {0, 0};  // Q and probability tiles used
       int cleaned = 0;                     // masked blocks looked through
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, at_wait(bar, parity)); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, at_wait<TEST>(bar, parity, a)); };
       const uint32_t q0 = (smem_addr(smem + C::kQ) & 0x3FFFFu) >> 4, kv0 = (smem_addr(smem + C::kKV) & 0x3FFFFu) >> 4;
       // S of a tile with the K tile of ring slot `sl`
       auto scores = [&](auto tile, int sl, bool last) {
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       bool dead = false;
       for (int pick = 0; !dead; ++pick) {
         AtItem it;
-        if (!at_next(bars, pick, lane, it)) break;
+        if (!at_next<TEST>(a, bars, pick, lane, it)) break;
         const int n0 = it.n0, n1 = it.n1, n = max(n0, n1);
         if (n == 0) continue;
         dead = true;  // until the item is through
@@ -506,13 +513,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       bool dead = false;
       for (int pick = 0; !dead; ++pick) {
         AtItem it;
-        if (!at_next(bars, pick, lane, it)) break;
+        if (!at_next<TEST>(a, bars, pick, lane, it)) break;
         const int n = max(it.n0, it.n1);
         if (n == 0) continue;
         for (int j = it.jm; j < n; ++j) {
           const int vi = kv + 2 * j + 1;
-          if (!__all_sync(0xffffffffu, at_wait(&bars->look, looked++ & 1) &&
-                                           at_wait(&bars->full[vi % NS], (vi / NS) & 1))) {
+          if (!__all_sync(0xffffffffu, at_wait<TEST>(&bars->look, looked++ & 1, a) &&
+                                           at_wait<TEST>(&bars->full[vi % NS], (vi / NS) & 1, a))) {
             dead = true;
             break;
           }
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     bool dead = false;
     for (int pick = 0;; ++pick) {
       AtItem it;
-      if (!at_next(bars, pick, lane, it)) break;
+      if (!at_next<TEST>(a, bars, pick, lane, it)) break;
       const int nt = t ? it.n1 : it.n0;
       const int tok = t * tokens + (r >> a.pk_log);
       const int limit = it.see + tok;  // the last key this row sees
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       unsigned long long* bad = bars->bad[item & 3];
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < nt; ++j) {
-        if (!__all_sync(0xffffffffu, at_wait(&bars->s_full[t], (ns + j) & 1))) {
+        if (!__all_sync(0xffffffffu, at_wait<TEST>(&bars->s_full[t], (ns + j) & 1, a))) {
           dead = true;
           break;
         }
@@ -597,8 +604,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const float b = m == -INFINITY ? 0.0f : -m * c;  // nothing seen yet: every exponential is 0
         const float2 c2 = make_float2(c, c), b2 = make_float2(b, b);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-        for (int i = 0; i < kAtRows; i += 32) {
+        auto quarter = [&](int i) {  // 32 keys' probabilities
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -608,17 +614,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             p[k] = pack_bf16x2(e.x, e.y);
           }
           tmem_st16(ts + i / 2, p);
-          if (i % 64 == 32) {  // 64 keys' probabilities are there
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[t][i / 64]);
-          }
-        }
+        };
+        auto half_done = [&](int h) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[t][h]);
+        };
+        quarter(0);
+        quarter(32);
+        half_done(0);
+        quarter(64);
+        quarter(96);
+        half_done(1);
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (dead) break;
-      if (nt > 0 && !__all_sync(0xffffffffu, at_wait(&bars->o_done[t], no & 1))) {
+      if (nt > 0 && !__all_sync(0xffffffffu, at_wait<TEST>(&bars->o_done[t], no & 1, a))) {
         dead = true;
         break;
       }
@@ -641,14 +653,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       bool marks = false;
       if (nt > 0)
         for (int w = 0; w < kAtMaskBlocks * 4; ++w) marks |= (uint32_t)(bad[w] >> 32) == item;
-#pragma unroll
-      for (int i = 0; i < D; i += 32) {
-        float o[32];
-        if (nt > 0) {
-          tmem_ld32_async(to + i, o);
-          tmem_ld_wait<32>(o);
-        }
-        if (marks) {  // add the values that were kept out of the products, where they are seen
+      if (marks) {  // add the values that were kept out of the products, where they are seen
+        for (int i = 0; i < D; i += 16) {
+          float o[16];
+          uint32_t u[16];
+          tmem_ld16(to + i, o);
           for (int w = 0; w < kAtMaskBlocks * 4; ++w) {
             const int j = it.jm + (w >> 2);
             const unsigned long long e = bad[w];
@@ -658,12 +667,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               const uint16_t* vr = a.v + (size_t)(it.row_k + key) * a.ld_v +
                                    (size_t)((it.hg << a.pk_log) / a.gqa) * D + i;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
+              for (int k = 0; k < 16; ++k) {
                 const float x = bf16_to_f32(vr[k]);
                 if (!(fabsf(x) < INFINITY)) o[k] += x;
               }
             }
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k]);
+          tmem_st16(to + i, u);
+        }
+        tmem_st_wait();
+      }
+#pragma unroll
+      for (int i = 0; i < D; i += 32) {
+        float o[32];
+        if (nt > 0) {
+          tmem_ld32_async(to + i, o);
+          tmem_ld_wait<32>(o);
         }
         uint4 w[4];
 #pragma unroll
@@ -709,10 +731,14 @@ static bool encode_heads(CUtensorMap* map, const uint16_t* base, int D, int head
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-static cudaError_t launch_attn(const AttnArgs& g, cudaStream_t s) {
+// Limit of the pipeline's waits of each device (0: the default), for later launches.
+static std::atomic<long long> g_limit[64];
+
+template <int D, bool TEST>
+static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s) {
   static int done_mask[64] = {0};
   AtArgs a;
+  a.limit = limit;
   a.out = g.out;
   a.v = g.v;
   a.ld_o = g.ld_o;
@@ -737,7 +763,7 @@ static cudaError_t launch_attn(const AttnArgs& g, cudaStream_t s) {
       !encode_heads(&k, keys ? g.k : g.q, D, keys ? g.Hkv : 1, keys ? g.Tk : 1, keys ? g.ld_k : g.ld_q, 1, kAtRows) ||
       !encode_heads(&v, keys ? g.v : g.q, D, keys ? g.Hkv : 1, keys ? g.Tk : 1, keys ? g.ld_v : g.ld_q, 1, kAtRows))
     return cudaErrorInvalidValue;
-  auto kern = attn_prefill_kernel<D>;
+  auto kern = attn_prefill_kernel<D, TEST>;
   constexpr int smem = at_smem_bytes<D>();
   cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
   if (e != cudaSuccess) return e;
@@ -765,10 +791,20 @@ static cudaError_t launch_attn(const AttnArgs& g, cudaStream_t s) {
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
-  return a.D == 128 ? launch_attn<128>(a, s) : launch_attn<64>(a, s);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int64_t limit = dev >= 0 && dev < 64 ? g_limit[dev].load(std::memory_order_relaxed) : 0;
+  if (limit <= 0) limit = kWaitCycles;
+  if (limit < 1000000) return a.D == 128 ? launch_attn<128, true>(a, limit, s) : launch_attn<64, true>(a, limit, s);
+  return a.D == 128 ? launch_attn<128, false>(a, limit, s) : launch_attn<64, false>(a, limit, s);
 }
 
 int status_attn(int clear) { return tu_status(clear); }
-cudaError_t wait_limit_attn(long long cycles) { return tu_set_wait_limit(cycles); }
+cudaError_t wait_limit_attn(long long cycles) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) g_limit[dev].store(cycles, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace m2
