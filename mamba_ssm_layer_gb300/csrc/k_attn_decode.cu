@@ -26,6 +26,7 @@
 #include "m2_common.cuh"
 #include "m2_kernels.h"
 #include "m2_kv4.cuh"
+#include "m2_tc.cuh"
 
 namespace m2 {
 
@@ -136,14 +137,16 @@ __device__ __forceinline__ float ad_ex2(float x) {
 // 4-byte words of a lane's codes or scales.
 template <int N>
 __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
+  if constexpr (N == 8) {
+    const uint4 v = reinterpret_cast<const uint4*>(p)[0], x = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w, w[4] = x.x, w[5] = x.y, w[6] = x.z, w[7] = x.w;
+  } else if constexpr (N == 4) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else if constexpr (N == 2) {
+  } else {
+    static_assert(N == 2, "words");
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x, w[1] = v.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 // Two scale bytes of a word (0 and 2, or 1 and 3) as f16x2.
@@ -200,25 +203,41 @@ struct AdRow {
     }
   }
 
-  // One unit in shared memory, of which the first `seen` tokens count.
-  __device__ __forceinline__ void unit(const uint8_t* u, int seen, int lane) {
+  // One unit in shared memory, of which the first `seen` tokens count.  Its scale
+  // bytes become f16 once (a token or token pair a lane) in the place where both
+  // kinds lay, first K's, after the scores V's: done by every lane for itself, the
+  // conversion was an eighth of the unit's instructions.
+  __device__ __forceinline__ void unit(uint8_t* u, int seen, int lane) {
     using L = Kv4Block<D>;
     constexpr int GW = D / 32;  // words of a lane's codes: 2 groups each
     const int r = lane >> 2, c = lane & 3;
+    uint8_t* sc = u + L::kKs;
+    uint32_t vs[GW];  // of token pair `lane`
+    {
+      uint32_t ks[GW];  // of tokens 2 lane and 2 lane + 1
+      lds_words<GW>(sc + lane * (D / 8), ks);
+      lds_words<GW>(u + L::kVs + lane * (D / 8), vs);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < GW; i += 2)
+        *reinterpret_cast<uint4*>(sc + lane * (D / 4) + 8 * i) =
+            make_uint4(scales02(ks[i], kScaleBits), scales13(ks[i], kScaleBits), scales02(ks[i + 1], kScaleBits),
+                       scales13(ks[i + 1], kScaleBits));
+      __syncwarp();
+    }
     float s[4][NT][4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      uint32_t k0[GW], k1[GW], s0[GW / 2], s1[GW / 2];
+      uint32_t k0[GW], k1[GW], s0[GW], s1[GW];
       const int t0 = 16 * mt + r;
       lds_words<GW>(u + L::kK + t0 * (D / 2) + c * (D / 8), k0);
       lds_words<GW>(u + L::kK + (t0 + 8) * (D / 2) + c * (D / 8), k1);
-      lds_words<GW / 2>(u + L::kKs + t0 * (D / 16), s0);
-      lds_words<GW / 2>(u + L::kKs + (t0 + 8) * (D / 16), s1);
+      lds_words<GW>(sc + t0 * (D / 8), s0);
+      lds_words<GW>(sc + (t0 + 8) * (D / 8), s1);
 #pragma unroll
       for (int w = 0; w < GW; ++w) {
-        // scale word w / 2 holds groups 4(w/2) .. + 3: this code word's are (0, 1) or (2, 3) of them
-        const uint32_t e0 = scales02(s0[w / 2], kScaleBits), f0 = scales13(s0[w / 2], kScaleBits);
-        const uint32_t e1 = scales02(s1[w / 2], kScaleBits), f1 = scales13(s1[w / 2], kScaleBits);
+        // scales of groups 4(w/2) .. + 3 lie as (0, 2), (1, 3): this code word's groups are (0, 1) or (2, 3) of them
+        const uint32_t e0 = s0[w & ~1], f0 = s0[w | 1], e1 = s1[w & ~1], f1 = s1[w | 1];
         uint32_t x[4], y[4];
         codes4(k0[w], x);
         codes4(k1[w], y);
@@ -295,24 +314,26 @@ struct AdRow {
         p[mt][t][1] = trans8x8(pack_f16x2(x2, x3));
       }
     }
+    {
+      // slots past the last token may hold any scale: theirs become 0
+      const uint32_t m = (2 * lane < seen ? 0x7F80u : 0u) | (2 * lane + 1 < seen ? 0x7F800000u : 0u);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < GW; i += 2)
+        *reinterpret_cast<uint4*>(sc + lane * (D / 4) + 8 * i) =
+            make_uint4(scales02(vs[i], m), scales13(vs[i], m), scales02(vs[i + 1], m), scales13(vs[i + 1], m));
+      __syncwarp();
+    }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      uint32_t v0[GW], v1[GW], s0[GW], s1[GW];
+      uint32_t v0[GW], v1[GW], s0[2 * GW], s1[2 * GW];
       lds_words<GW>(u + L::kV + (2 * ks) * (4 * D) + r * (D / 2) + c * (D / 8), v0);
       lds_words<GW>(u + L::kV + (2 * ks + 1) * (4 * D) + r * (D / 2) + c * (D / 8), v1);
-      lds_words<GW>(u + L::kVs + (8 * ks + c) * (D / 8), s0);
-      lds_words<GW>(u + L::kVs + (8 * ks + 4 + c) * (D / 8), s1);
-      // slots past the last token may hold any scale: theirs become 0
-      uint32_t m0 = kScaleBits, m1 = kScaleBits;
-      if (seen < kPage) {
-        const int t0 = 16 * ks + 2 * c;
-        m0 = (t0 < seen ? 0x7F80u : 0u) | (t0 + 1 < seen ? 0x7F800000u : 0u);
-        m1 = (t0 + 8 < seen ? 0x7F80u : 0u) | (t0 + 9 < seen ? 0x7F800000u : 0u);
-      }
+      lds_words<2 * GW>(sc + (8 * ks + c) * (D / 4), s0);
+      lds_words<2 * GW>(sc + (8 * ks + 4 + c) * (D / 4), s1);
 #pragma unroll
       for (int w = 0; w < GW; ++w) {
-        const uint32_t e0 = scales02(s0[w], m0), e1 = scales02(s1[w], m1);
-        const uint32_t f0 = scales13(s0[w], m0), f1 = scales13(s1[w], m1);
+        const uint32_t e0 = s0[2 * w], f0 = s0[2 * w + 1], e1 = s1[2 * w], f1 = s1[2 * w + 1];
         uint32_t x[4], y[4];
         codes4(v0[w], x);
         codes4(v1[w], y);
@@ -540,7 +561,8 @@ __global__ void __launch_bounds__(kAdWarps * 32, 1) attn_decode_kernel(const AdA
         break;
       }
       if (sh->ok[warp][st]) row.unit(ring + st * C::kUnit, min(kPage, cur.len - cur.page * kPage), lane);
-      __syncwarp();  // the stage is read
+      fence_proxy_async();  // the scales' place is written anew by the next copy
+      __syncwarp();         // the stage is read
       if (fetched < n) fetch(fetched++);
       const bool ends = cur.page + 1 == cur.pages;
       if (ends || i + 1 == n) {  // the row leaves this warp
