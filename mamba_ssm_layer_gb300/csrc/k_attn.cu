@@ -156,23 +156,45 @@ __device__ __forceinline__ bool elect_one() {
 // leading offset); 8-row atoms 1024 bytes apart (stride offset).
 // The products of one tile, operand addresses in units of 16 bytes: the
 // descriptors' upper words are constants, steps along K add to the lower ones.
+// Every lane comes here and only the leader's product takes place: with a branch
+// around them, operands would pass through vector registers.
 constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t at_desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+__device__ __forceinline__ void at_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc, int leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc, int leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void at_commit(uint64_t* bar, int leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(leader)
+      : "memory");
+}
 template <int D>
-__device__ __forceinline__ void at_issue_scores(uint32_t d, uint32_t q, uint32_t k) {
+__device__ __forceinline__ void at_issue_scores(uint32_t d, uint32_t q, uint32_t k, int leader) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const uint32_t step = (i >> 2) * (kAtRows * 128 >> 4) + (i & 3) * 2;
-    tc_mma(d, at_desc((q + step) | (1u << 16)), at_desc((k + step) | (1u << 16)), tc_idesc(kAtRows, kAtRows), i > 0);
+    at_mma(d, at_desc((q + step) | (1u << 16)), at_desc((k + step) | (1u << 16)), tc_idesc(kAtRows, kAtRows), i > 0,
+           leader);
   }
 }
 // 64 keys of O += P V; the values' second 64 channels lie kAtRows * 128 bytes on.
 template <int D>
-__device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t v, bool acc) {
+__device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t v, bool acc, int leader) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    tc_mma_ts(d, p + 8 * i, at_desc((v + i * (2048 >> 4)) | ((kAtRows * 128 >> 4) << 16)), tc_idesc(kAtRows, D) | (1u << 16),
-              acc || i > 0);
+    at_mma_ts(d, p + 8 * i, at_desc((v + i * (2048 >> 4)) | ((kAtRows * 128 >> 4) << 16)),
+              tc_idesc(kAtRows, D) | (1u << 16), acc || i > 0, leader);
 }
 
 // Four lanes (aligned) with four pieces each: lane q's piece j becomes lane j's piece q.
@@ -214,6 +236,19 @@ __device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, lo
 template <bool TEST>
 __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, const AtArgs& a) {
   return mbar_test_wait(bar, parity) || at_wait_until<TEST>(bar, parity, a.limit);
+}
+// The same for a whole warp, which stays together.
+template <bool TEST>
+__device__ __forceinline__ bool at_wait_warp(uint64_t* bar, uint32_t parity, const AtArgs& a) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, TEST ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity, 1000u))) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > a.limit)) {
+      record_timeout();
+      return false;
+    }
+  }
+  return true;
 }
 __device__ __forceinline__ bool at_drain(uint64_t* bar, uint32_t parity) {
   return mbar_test_wait(bar, parity) || at_wait_until<false>(bar, parity, kWaitCycles);
@@ -401,21 +436,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       // ------------------------------------------------------ products
       // The whole warp walks the blocks, so that addresses and descriptors stay
       // warp-uniform; one elected lane issues.
-      const bool leader = elect_one();
+      const int leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       using T0 = std::integral_constant<int, 0>;
       using T1 = std::integral_constant<int, 1>;
       int nq[2] = {0, 0}, np[2] = {0, 0};  // Q and probability tiles used
       int cleaned = 0;                     // masked blocks looked through
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, at_wait<TEST>(bar, parity, a)); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return at_wait_warp<TEST>(bar, parity, a); };
       const uint32_t q0 = (smem_addr(smem + C::kQ) & 0x3FFFFu) >> 4, kv0 = (smem_addr(smem + C::kKV) & 0x3FFFFu) >> 4;
       // S of a tile with the K tile of ring slot `sl`
       auto scores = [&](auto tile, int sl, bool last) {
         constexpr int t = decltype(tile)::value;
-        if (leader) {
-          at_issue_scores<D>(tmem + C::kTmS + t * kAtRows, q0 + t * (C::kTile >> 4), kv0 + sl * (C::kTile >> 4));
-          tc_commit(&bars->s_full[t]);
-          if (last) tc_commit(&bars->q_empty[t]);  // the tile's last scores
-        }
+        at_issue_scores<D>(tm + C::kTmS + t * kAtRows, q0 + t * (C::kTile >> 4), kv0 + sl * (C::kTile >> 4), leader);
+        at_commit(&bars->s_full[t], leader);
+        if (last) at_commit(&bars->q_empty[t], leader);  // the tile's last scores
       };
       // O += P V of a tile with the V tile of ring slot `sl`; free: no other tile needs it, last: the tile's last block
       auto values = [&](auto tile, int sl, bool add, bool free, bool last) {
@@ -424,15 +458,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         for (int hf = 0; hf < 2; ++hf) {  // the first 64 keys' probabilities come before the others'
           if (!wait(&bars->p_full[t][hf], np[t] & 1)) return false;
           tc_fence_after();
-          if (leader)
-            at_issue_values<D>(tmem + C::kTmO + t * D, tmem + C::kTmS + t * kAtRows + 32 * hf,
-                               kv0 + sl * (C::kTile >> 4) + hf * (8192 >> 4), add || hf > 0);
+          at_issue_values<D>(tm + C::kTmO + t * D, tm + C::kTmS + t * kAtRows + 32 * hf,
+                             kv0 + sl * (C::kTile >> 4) + hf * (8192 >> 4), add || hf > 0, leader);
         }
         ++np[t];
-        if (leader) {
-          if (free) tc_commit(&bars->empty[sl]);
-          if (last) tc_commit(&bars->o_done[t]);
-        }
+        if (free) at_commit(&bars->empty[sl], leader);
+        if (last) at_commit(&bars->o_done[t], leader);
         return true;
       };
       int sl = 0, ph = 0;  // ring slot and phase of the item's next copy
@@ -444,7 +475,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int pick = 0; !dead; ++pick) {
         AtItem it;
         if (!at_next<TEST>(a, bars, pick, lane, it)) break;
-        const int n0 = it.n0, n1 = it.n1, n = max(n0, n1);
+        // (one value of the warp, for the compiler too)
+        const int n0 = __shfl_sync(0xffffffffu, it.n0, 0), n1 = __shfl_sync(0xffffffffu, it.n1, 0);
+        const int jm = __shfl_sync(0xffffffffu, it.jm, 0), n = max(n0, n1);
         if (n == 0) continue;
         dead = true;  // until the item is through
         if (!wait(&bars->full[sl], ph)) break;
@@ -456,10 +489,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!wait(&bars->q_full[1], nq[1]++ & 1)) break;
           scores(T1(), sl, n1 == 1);
         }
-        if (leader) {
-          tc_commit(&bars->empty[sl]);
-          if (it.jm == 0) mbar_arrive(&bars->look);
-        }
+        at_commit(&bars->empty[sl], leader);
+        if (jm == 0 && leader) mbar_arrive(&bars->look);
         int vs = sl, vph = ph, ks, kph, j = 0;  // slots of V_j and K_j+1
         step(vs, vph, 1);
         for (;; ++j) {
@@ -470,8 +501,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           ks = vs, kph = vph;
           step(ks, kph, 1);
           // V_j is there, and looked through if some row must not see all of it
-          if (!wait(&bars->full[vs], vph) || (j >= it.jm && !wait(&bars->clean, cleaned++ & 1))) break;
-          const bool more = j + 1 < n, look = leader && more && j + 1 >= it.jm;
+          if (!wait(&bars->full[vs], vph) || (j >= jm && !wait(&bars->clean, cleaned++ & 1))) break;
+          const bool more = j + 1 < n, look = leader && more && j + 1 >= jm;
           if (j < n0) {
             if (!values(T0(), vs, j > 0, j >= n1, j + 1 == n0)) break;
             if (j + 1 < n0) {
@@ -490,7 +521,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               scores(T1(), ks, j + 2 == n1);
             }
           }
-          if (more && leader) tc_commit(&bars->empty[ks]);
+          if (more) at_commit(&bars->empty[ks], leader);
           vs = ks, vph = kph;
           step(vs, vph, 1);
         }
