@@ -16,6 +16,15 @@
 // Bound: the tensor cores (4 * 128 * 128 * D operations a tile pair) and the
 // exponentials (one a score); while one tile's scores are in the softmax
 // warps, the other tile's products run.
+// Measured at 32 + 8 heads: one prompt of 8192 tokens, D = 128, 340 us (1.6
+// PFLOP/s; a step of both tiles is 2900 cycles for 2048 of products: 1850 of
+// softmax, 950 of them exponentials, which a warp alone on its quarter of the SM
+// issues at half the rate of two, then the products that the next scores wait
+// for); four chunks of 200..1000 tokens over up to 6000, D = 64, 112 us (0.8
+// PFLOP/s); 16 prompts of 64..512 tokens 38 us, of which an item's first block
+// and output take more than its products.  Two threads a row (16 softmax warps of
+// 104 registers) took 418 us instead of 371: what a warp does once a block
+// (waits, votes, the exchange of maxima) counts twice.
 //
 // Roles: warps 0-3 softmax and output of tile 0, warps 4-7 of tile 1, warp 8
 // issues the products, warp 9 the TMA copies, warps 10 and 11 look through the
@@ -56,9 +65,9 @@ struct AtCfg {
   static constexpr int kKV = 2 * kTile;
   static constexpr int kBars = kKV + kStages * kTile;
   // Tensor-memory columns: S 2 x 128 (P over it), O 2 x D.  (With D = 64 there is
-  // room for P of its own, so that the next scores run under the softmax; the two
-  // tiles' softmax phases then run in step, and four chunks over cached tokens took
-  // 138 us instead of 128.)
+  // room for P of its own, so that the next scores run under the softmax; scores are
+  // then read while products run, which takes twice as long, and four chunks over
+  // cached tokens took 123 us instead of 115.)
   static constexpr uint32_t kTmS = 0, kTmO = 256;
 };
 // What a CTA works on: the copies' thread works it out and hands it on through
@@ -81,6 +90,7 @@ struct AtBars {
   // CTA's item.  A block is looked through after its first scores were issued, when
   // the tiles have at most the output of the item before last ahead of them.
   unsigned long long bad[4][kAtMaskBlocks * 4];
+  uint32_t marked[4];  // the last item with such keys
   uint32_t tmem;
 };
 template <int D>
@@ -99,6 +109,7 @@ struct AtArgs {
   float scale_log2; // scale * log2(e)
   int32_t nseq;
   int32_t items;    // tile pairs * groups
+  int32_t wide;     // output rows start on 32 bytes
   int32_t sorted;   // order[] holds the pairs, most key blocks first
   int64_t limit;    // of the pipeline's waits, SM clock cycles
   int32_t cu_q[kSeqs + 1], cu_k[kSeqs + 1];
@@ -157,7 +168,8 @@ __device__ __forceinline__ bool elect_one() {
 // The products of one tile, operand addresses in units of 16 bytes: the
 // descriptors' upper words are constants, steps along K add to the lower ones.
 // Every lane comes here and only the leader's product takes place: with a branch
-// around them, operands would pass through vector registers.
+// around them operands pass through vector registers, and a prompt of 8192 tokens
+// took 370 us instead of 349.
 constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t at_desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 __device__ __forceinline__ void at_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc, int leader) {
@@ -197,23 +209,11 @@ __device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t
               tc_idesc(kAtRows, D) | (1u << 16), acc || i > 0, leader);
 }
 
-// Four lanes (aligned) with four pieces each: lane q's piece j becomes lane j's piece q.
-__device__ __forceinline__ void swap_pieces(uint4& lo, uint4& hi, int mask, bool up) {
-  uint4 s = up ? lo : hi;
-  s.x = __shfl_xor_sync(0xffffffffu, s.x, mask);
-  s.y = __shfl_xor_sync(0xffffffffu, s.y, mask);
-  s.z = __shfl_xor_sync(0xffffffffu, s.z, mask);
-  s.w = __shfl_xor_sync(0xffffffffu, s.w, mask);
-  if (up)
-    lo = s;
-  else
-    hi = s;
-}
-__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
-  swap_pieces(w[0], w[1], 1, lane & 1);
-  swap_pieces(w[2], w[3], 1, lane & 1);
-  swap_pieces(w[0], w[2], 2, lane & 2);
-  swap_pieces(w[1], w[3], 2, lane & 2);
+// 32 bytes, aligned: a whole sector.
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // mbar_wait without a call (a kernel that hands registers between its warps has to
@@ -290,22 +290,30 @@ __device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
   return it;
 }
 
+// Two bf16 of the larger magnitudes (their signs mean nothing).
+__device__ __forceinline__ void max_abs(uint32_t& a, uint32_t b) {
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+}
+
 // Looks through row r of a value tile for numbers that are not finite: a
 // probability of zero does not keep them out of the product.  They are set to
 // zero in shared memory and their key is marked; rows that do see the key add
 // them at the end.
 template <int D>
-__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long long* bad, uint32_t item) {
-  bool any = false;
+__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long long* bad, volatile uint32_t* marked,
+                                             uint32_t item) {
+  uint32_t top[2] = {0u, 0u};  // largest magnitudes, NaN above all
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
     const uint4 w = *reinterpret_cast<const uint4*>(tile + sw128_chunk(kAtRows, r, c));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      any |= (u[i] & 0x7F80u) == 0x7F80u || (u[i] & 0x7F800000u) == 0x7F800000u;
+    max_abs(top[0], w.x);
+    max_abs(top[1], w.y);
+    max_abs(top[0], w.z);
+    max_abs(top[1], w.w);
   }
-  if (!any) return;
+  max_abs(top[0], top[1]);
+  if ((top[0] & 0x7F80u) != 0x7F80u && (top[0] & 0x7F800000u) != 0x7F800000u) return;
+  *marked = item;
   unsigned long long old = bad[r >> 5];
   for (;;) {
     const unsigned long long want =
@@ -367,6 +375,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bars->empty[s], 1);
     }
     for (int i = 0; i < 4 * kAtMaskBlocks * 4; ++i) (&bars->bad[0][0])[i] = ~0ull;
+    for (int i = 0; i < 4; ++i) bars->marked[i] = ~0u;
     fence_mbar_init();
   }
   if (warp == 8) tmem_alloc(&bars->tmem, 512);
@@ -555,7 +564,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             break;
           }
           for (int r = (warp - 10) * 32 + lane; r < kAtRows; r += 64)
-            at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[item & 3] + 4 * (j - it.jm), item);
+            at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[item & 3] + 4 * (j - it.jm),
+                            &bars->marked[item & 3], item);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->clean);
@@ -576,9 +586,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     int ns = 0, no = 0;                         // score tiles and outputs before this item
     uint32_t item = 0;                          // items with keys before this one
     bool dead = false;
-    for (int pick = 0;; ++pick) {
-      AtItem it;
-      if (!at_next<TEST>(a, bars, pick, lane, it)) break;
+    AtItem it;
+    bool more = at_next<TEST>(a, bars, 0, lane, it);
+    for (int pick = 0; more; ++pick) {
       const int nt = t ? it.n1 : it.n0;
       const int tok = t * tokens + (r >> a.pk_log);
       const int limit = it.see + tok;  // the last key this row sees
@@ -605,8 +615,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int i = 0; i < kAtRows; i += 32) {
             if (least >= i + 32) continue;  // the warp's rows see all 32
+            const uint32_t bits = seen >= i + 32 ? ~0u : (1u << max(seen - i, 0)) - 1u;
 #pragma unroll
-            for (int k = i; k < i + 32; ++k) s[k] = k < seen ? s[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) s[i + k] = bits >> k & 1u ? s[i + k] : -INFINITY;
           }
         }
         float mx[4] = {m, s[0], s[1], s[2]};
@@ -661,30 +672,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (dead) break;
+      const float inv = limit >= 0 ? 1.0f / l : 0.0f;
+      uint16_t* dst = a.out + (size_t)(it.row_q + min(tok, it.left - 1)) * a.ld_o +
+                      (size_t)((it.hg << a.pk_log) + (r & ((1 << a.pk_log) - 1))) * D;
+      // The next item is taken now: behind the stores, the slot's release would wait for them.
+      AtItem next;
+      more = at_next<TEST>(a, bars, pick + 1, lane, next);
       if (nt > 0 && !__all_sync(0xffffffffu, at_wait<TEST>(&bars->o_done[t], no & 1, a))) {
         dead = true;
         break;
       }
       tc_fence_after();
-      const float inv = limit >= 0 ? 1.0f / l : 0.0f;
-      // Four neighbouring rows' lanes exchange 16-byte pieces, so that a store covers
-      // 64 bytes of a row: dst[i] is row (r & ~3) + i, piece r & 3.
-      uint16_t* dst[4];
-      {
-        const int hl = r & ((1 << a.pk_log) - 1);
-        const uint64_t mine = tok < it.left ? reinterpret_cast<uint64_t>(a.out + (size_t)(it.row_q + tok) * a.ld_o +
-                                                                       (size_t)((it.hg << a.pk_log) + hl) * D)
-                                          : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t p = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
-          dst[i] = p ? reinterpret_cast<uint16_t*>(p) + 8 * (lane & 3) : nullptr;
-        }
-      }
-      bool marks = false;
-      if (nt > 0)
-        for (int w = 0; w < kAtMaskBlocks * 4; ++w) marks |= (uint32_t)(bad[w] >> 32) == item;
-      if (marks) {  // add the values that were kept out of the products, where they are seen
+      if (nt > 0 && bars->marked[item & 3] == item) {  // add the values that were kept out of the products, where they are seen
         for (int i = 0; i < D; i += 16) {
           float o[16];
           uint32_t u[16];
@@ -718,23 +717,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           tmem_ld32_async(to + i, o);
           tmem_ld_wait<32>(o);
         }
-        uint4 w[4];
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float* x = o + 8 * k;
-          w[k] = limit >= 0 ? make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
-                                         pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv))
-                            : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 16; ++k) w[k] = limit >= 0 ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+        if (tok < it.left) {
+          if (a.wide) {
+            store32(dst + i, w);
+            store32(dst + i + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(dst + i + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+          }
         }
-        transpose4(w, lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + i) = w[k];
       }
       tc_fence_before();  // O is read before the next item's products, which wait for this warp's probabilities
       ns += nt;
       no += nt > 0 ? 1 : 0;
       item += max(it.n0, it.n1) > 0 ? 1 : 0;
+      it = next;
     }
   }
   tc_fence_before();
@@ -781,6 +782,7 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
   a.groups = g.H / pk;
   a.scale_log2 = g.scale * 1.4426950408889634f;
   a.nseq = g.nseq;
+  a.wide = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.ld_o % 16 == 0;
   a.tile[0] = 0;
   for (int i = 0; i <= kSeqs; ++i) {
     a.cu_q[i] = g.cu_q[i];
