@@ -16,14 +16,14 @@
 // Bound: the tensor cores (4 * 128 * 128 * D operations a tile pair) and the
 // exponentials (one a score); while one tile's scores are in the softmax
 // warps, the other tile's products run.
-// Measured at 32 + 8 heads: one prompt of 8192 tokens, D = 128, 340 us (1.6
-// PFLOP/s; a step of both tiles is 2900 cycles for 2048 of products: 1850 of
+// Measured at 32 + 8 heads: one prompt of 8192 tokens, D = 128, 330 us (1.7
+// PFLOP/s; a step of both tiles is 2800 cycles for 2048 of products: 1800 of
 // softmax, 950 of them exponentials, which a warp alone on its quarter of the SM
 // issues at half the rate of two, then the products that the next scores wait
-// for); four chunks of 200..1000 tokens over up to 6000, D = 64, 112 us (0.8
-// PFLOP/s); 16 prompts of 64..512 tokens 38 us, of which an item's first block
-// and output take more than its products.  Two threads a row (16 softmax warps of
-// 104 registers) took 418 us instead of 371: what a warp does once a block
+// for); four chunks of 200..1000 tokens over up to 6000, D = 64, 107 us (0.8
+// PFLOP/s); 16 prompts of 64..512 tokens 32 us, of which an item's first block
+// and output take as long as its products.  Two threads a row (16 softmax warps of
+// 104 registers) took 418 us where one took 371: what a warp does once a block
 // (waits, votes, the exchange of maxima) counts twice.
 //
 // Roles: warps 0-3 softmax and output of tile 0, warps 4-7 of tile 1, warp 8
@@ -45,8 +45,8 @@ namespace m2 {
 
 constexpr int kAtThreads = 384;
 // Registers a thread after the hand-over; launched with 168 (65536 / 384, in
-// steps of 8): 2 * 224 + 56 = 3 * 168.
-constexpr int kAtRegsSoftmax = 224, kAtRegsOther = 56;
+// steps of 8): 2 * 216 + 72 = 3 * 168.
+constexpr int kAtRegsSoftmax = 216, kAtRegsOther = 72;
 constexpr int kAtRows = 128;      // query rows of a tile, keys of a block
 // Up to so many tile pairs are handed out longest first; with more of them, later
 // ones first (a sequence's longest) spreads the work as well.  Measured by the
@@ -216,6 +216,19 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* w) {
                : "memory");
 }
 
+// A potentially blocking test, for as long as the hardware likes.  (A time asked for
+// becomes sleeping in steps, which took 1 to 2% longer.)
+__device__ __forceinline__ bool at_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // mbar_wait without a call (a kernel that hands registers between its warps has to
 // be one function), its limit from the launch's parameters.  The hardware may hold a
 // suspended wait longer than asked, so that a short limit takes waits that only test
@@ -225,7 +238,7 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* w) {
 template <bool TEST>
 __device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
   const long long t0 = clock64();
-  while (!(TEST ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity, 1000u))) {
+  while (!(TEST ? mbar_test_wait(bar, parity) : at_try(bar, parity))) {
     if (clock64() - t0 > limit) {
       record_timeout();
       return false;
@@ -242,7 +255,7 @@ template <bool TEST>
 __device__ __forceinline__ bool at_wait_warp(uint64_t* bar, uint32_t parity, const AtArgs& a) {
   if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, TEST ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity, 1000u))) {
+  while (!__all_sync(0xffffffffu, TEST ? mbar_test_wait(bar, parity) : at_try(bar, parity))) {
     if (__any_sync(0xffffffffu, clock64() - t0 > a.limit)) {
       record_timeout();
       return false;
@@ -337,7 +350,7 @@ __device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long
 template <bool TEST>
 __device__ __forceinline__ bool at_next(const AtArgs& a, AtBars* bars, int pick, int lane, AtItem& it) {
   const int sl = pick % kAtItems;
-  if (!__all_sync(0xffffffffu, at_wait<TEST>(&bars->item_full[sl], (pick / kAtItems) & 1, a))) return false;
+  if (!at_wait_warp<TEST>(&bars->item_full[sl], (pick / kAtItems) & 1, a)) return false;
   it = bars->item[sl];
   __syncwarp();
   if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
@@ -558,8 +571,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (n == 0) continue;
         for (int j = it.jm; j < n; ++j) {
           const int vi = kv + 2 * j + 1;
-          if (!__all_sync(0xffffffffu, at_wait<TEST>(&bars->look, looked++ & 1, a) &&
-                                           at_wait<TEST>(&bars->full[vi % NS], (vi / NS) & 1, a))) {
+          if (!at_wait_warp<TEST>(&bars->look, looked++ & 1, a) ||
+              !at_wait_warp<TEST>(&bars->full[vi % NS], (vi / NS) & 1, a)) {
             dead = true;
             break;
           }
@@ -596,7 +609,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       unsigned long long* bad = bars->bad[item & 3];
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < nt; ++j) {
-        if (!__all_sync(0xffffffffu, at_wait<TEST>(&bars->s_full[t], (ns + j) & 1, a))) {
+        if (!at_wait_warp<TEST>(&bars->s_full[t], (ns + j) & 1, a)) {
           dead = true;
           break;
         }
@@ -632,7 +645,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const float f = grow ? ex2((m - mn) * c) : 1.0f;
             if (grow) m = mn;
             l *= f;
-#pragma unroll
+            // rolled: unrolled next to 128 scores, it spilled registers of the block loop (16 packed prompts 38 us
+            // instead of 33)
+#pragma unroll 1
             for (int i = 0; i < D; i += 16) {
               float o[16];
               uint32_t u[16];
@@ -651,10 +666,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 z = ffma2(c2, make_float2(s[i + 2 * k], s[i + 2 * k + 1]), b2);
-            const float2 e = make_float2(ex2(z.x), ex2(z.y));
-            sum[k & 1] = fadd2(sum[k & 1], e);
-            p[k] = pack_bf16x2(e.x, e.y);
+            s[i + 2 * k] = ex2(z.x);
+            s[i + 2 * k + 1] = ex2(z.y);
+            p[k] = pack_bf16x2(s[i + 2 * k], s[i + 2 * k + 1]);
           }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sum[k & 1] = fadd2(sum[k & 1], make_float2(s[i + 2 * k], s[i + 2 * k + 1]));
           tmem_st16(ts + i / 2, p);
         };
         auto half_done = [&](int h) {
@@ -678,12 +695,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       // The next item is taken now: behind the stores, the slot's release would wait for them.
       AtItem next;
       more = at_next<TEST>(a, bars, pick + 1, lane, next);
-      if (nt > 0 && !__all_sync(0xffffffffu, at_wait<TEST>(&bars->o_done[t], no & 1, a))) {
+      if (nt > 0 && !at_wait_warp<TEST>(&bars->o_done[t], no & 1, a)) {
         dead = true;
         break;
       }
       tc_fence_after();
       if (nt > 0 && bars->marked[item & 3] == item) {  // add the values that were kept out of the products, where they are seen
+#pragma unroll 1
         for (int i = 0; i < D; i += 16) {
           float o[16];
           uint32_t u[16];
@@ -710,7 +728,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         tmem_st_wait();
       }
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < D; i += 32) {
         float o[32];
         if (nt > 0) {
