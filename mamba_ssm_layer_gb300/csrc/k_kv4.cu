@@ -16,9 +16,9 @@ namespace m2 {
 // time.  The angles of the row are worked out once, by the warp's lanes, into
 // shared memory: p * step mod 2^64 is the angle in turns, exactly, and only its
 // top 32 bits (a signed fraction of a half turn) enter the fp32 functions.
-// Bound: HBM, one read and one write of every row; the kernel for the usual
-// rotation of all channels is also close to the issue rate.  Measured at 8192 rows
-// of 32 + 8 heads of 128: 31 us, 5.4 TB/s.
+// Bound: HBM, one read and one write of every row, and as close the issue rate.
+// Measured at 8192 rows of 32 + 8 heads of 128: 31 to 33 us for every form of the
+// rotation, 5.1 to 5.5 TB/s.
 constexpr int kRopeWarps = 8, kRopeBatch = 4;
 
 // Cosines and sines of the row's angles.
@@ -53,12 +53,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return r;
 }
 
-// Rotation of all channels, pair i = (i, i + D/2): a lane's 8 channels are 4 l .. 4 l + 3
-// and those D/2 on, so that nothing but the sum of squares crosses lanes.  Weights
-// and angles meet once a row: with w' = w cos, w" = w sin of the pair,
+// A lane's 8 channels are 4 pairs (a, b) of the rotation, so that nothing but the
+// sum of squares crosses lanes: channels 4 l .. 4 l + 3 and those rot/2 on (pair i =
+// (i, i + rot/2)) or 8 l .. 8 l + 7 (NEXT: pair i = (2 i, 2 i + 1)), as are those of
+// the lanes past the rotated channels (PART).  Weights and angles meet once a row:
+// with w' = w cos, w" = w sin of the pair,
 //   y_a = r (a w'_a - b w"_b),  y_b = r (b w'_b + a w"_a),  r = 1 / sqrt(mean + eps).
-template <int D>
-__global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(const RopeArgs a, int parts) {
+template <int D, bool NEXT, bool PART>
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_kernel(const RopeArgs a, int parts) {
   constexpr int LH = D / 8, HW = 32 / LH;  // lanes a head, heads a group
   __shared__ float2 turn[kRopeWarps][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LH, sub = lane / LH;
@@ -66,12 +68,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(co
   pdl_wait();
   pdl_trigger();
   if (row >= a.T) return;
-  rope_angles(a, row, lane, turn[warp]);
+  const bool turns = !PART || 8 * l < a.rot;
+  const int ac = NEXT || !turns ? 8 * l : 4 * l;                       // the lane's first channel
+  const int bd = NEXT || !turns ? 4 : (PART ? a.rot : D) / 2;  // and its second four's distance
+  if (!PART || a.rot) rope_angles(a, row, lane, turn[warp]);
   float2 cs[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) cs[i] = turn[warp][4 * l + i];
+  for (int i = 0; i < 4; ++i) cs[i] = turns ? turn[warp][4 * l + i] : make_float2(1.0f, 0.0f);
   const int gq = (a.H + HW - 1) / HW, groups = gq + (a.Hkv + HW - 1) / HW;
   const int per = (groups + parts - 1) / parts, g0 = (int)(id - row * parts) * per, g1 = min(groups, g0 + per);
+  // two words of a lane's channels -> the a and b of two pairs
+  auto pairs = [](uint32_t u, uint32_t v, float2& x, float2& y) {
+    x = NEXT ? make_float2(bf16lo(u), bf16lo(v)) : make_float2(bf16lo(u), bf16hi(u));
+    y = NEXT ? make_float2(bf16hi(u), bf16hi(v)) : make_float2(bf16lo(v), bf16hi(v));
+  };
   // the groups from `from` to `to` of n heads at in -> out
   auto run = [&](const uint16_t* in, uint16_t* out, const uint16_t* w, int n, int from, int to) {
     if (from >= to) return;
@@ -80,14 +90,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(co
     for (int i = 0; i < 2; ++i) {
       float2 wa = make_float2(1.0f, 1.0f), wb = wa;
       if (w) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(w + 4 * l + 2 * i);
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(w + D / 2 + 4 * l + 2 * i);
-        wa = make_float2(bf16lo(u), bf16hi(u)), wb = make_float2(bf16lo(v), bf16hi(v));
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(w + ac + (NEXT ? 4 * i : 2 * i));
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(w + ac + (NEXT ? 4 * i + 2 : bd + 2 * i));
+        pairs(u, v, wa, wb);
       }
       const float2 c = make_float2(cs[2 * i].x, cs[2 * i + 1].x), s = make_float2(cs[2 * i].y, cs[2 * i + 1].y);
       ca[i] = mul2(wa, c), cb[i] = mul2(wb, c), sa[i] = mul2(wa, s), sb[i] = mul2(wb, make_float2(-s.x, -s.y));
     }
-    const int64_t lane_at = (int64_t)sub * D + 4 * l;
+    const int64_t lane_at = (int64_t)sub * D + ac;
     in += lane_at, out += lane_at;
     for (int gb = from; gb < to; gb += kRopeBatch) {
       uint2 u[kRopeBatch], v[kRopeBatch];
@@ -95,14 +105,21 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(co
       for (int k = 0; k < kRopeBatch; ++k) {
         u[k] = v[k] = make_uint2(0u, 0u);
         if (gb + k < to && (gb + k) * HW + sub < n) {
-          u[k] = *reinterpret_cast<const uint2*>(in + (gb + k) * (HW * D));
-          v[k] = *reinterpret_cast<const uint2*>(in + (gb + k) * (HW * D) + D / 2);
+          const uint16_t* x = in + (gb + k) * (HW * D);
+          if (NEXT) {
+            const uint4 z = *reinterpret_cast<const uint4*>(x);
+            u[k] = make_uint2(z.x, z.z), v[k] = make_uint2(z.y, z.w);
+          } else {
+            u[k] = *reinterpret_cast<const uint2*>(x);
+            v[k] = *reinterpret_cast<const uint2*>(x + bd);
+          }
         }
       }
 #pragma unroll
       for (int k = 0; k < kRopeBatch; ++k) {
-        float2 xa[2] = {make_float2(bf16lo(u[k].x), bf16hi(u[k].x)), make_float2(bf16lo(u[k].y), bf16hi(u[k].y))};
-        float2 xb[2] = {make_float2(bf16lo(v[k].x), bf16hi(v[k].x)), make_float2(bf16lo(v[k].y), bf16hi(v[k].y))};
+        float2 xa[2], xb[2];
+        pairs(u[k].x, v[k].x, xa[0], xb[0]);
+        pairs(u[k].y, v[k].y, xa[1], xb[1]);
         float r = 1.0f;
         if (w) {
           const float2 q = fma2(xa[0], xa[0], fma2(xa[1], xa[1], fma2(xb[0], xb[0], mul2(xb[1], xb[1]))));
@@ -115,13 +132,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(co
         float2 ya[2], yb[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          ya[i] = mul2(fma2(xa[i], ca[i], mul2(xb[i], sb[i])), r2);
-          yb[i] = mul2(fma2(xb[i], cb[i], mul2(xa[i], sa[i])), r2);
+          // (0 * Inf must not come from one channel into another that it does not turn with)
+          const float2 pa = turns ? xa[i] : make_float2(0.0f, 0.0f), pb = turns ? xb[i] : make_float2(0.0f, 0.0f);
+          ya[i] = mul2(fma2(xa[i], ca[i], mul2(pb, sb[i])), r2);
+          yb[i] = mul2(fma2(xb[i], cb[i], mul2(pa, sa[i])), r2);
         }
         if (gb + k < to && (gb + k) * HW + sub < n) {
           uint16_t* d = out + (gb + k) * (HW * D);
-          *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(ya[0].x, ya[0].y), pack_bf16x2(ya[1].x, ya[1].y));
-          *reinterpret_cast<uint2*>(d + D / 2) = make_uint2(pack_bf16x2(yb[0].x, yb[0].y), pack_bf16x2(yb[1].x, yb[1].y));
+          if (NEXT) {
+            *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16x2(ya[0].x, yb[0].x), pack_bf16x2(ya[0].y, yb[0].y),
+                                                      pack_bf16x2(ya[1].x, yb[1].x), pack_bf16x2(ya[1].y, yb[1].y));
+          } else {
+            *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(ya[0].x, ya[0].y), pack_bf16x2(ya[1].x, ya[1].y));
+            *reinterpret_cast<uint2*>(d + bd) = make_uint2(pack_bf16x2(yb[0].x, yb[0].y), pack_bf16x2(yb[1].x, yb[1].y));
+          }
         }
       }
     }
@@ -130,93 +154,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_all_kernel(co
   run(a.k + row * a.ld_k, a.k_out + row * a.ld_ko, a.k_w, a.Hkv, max(g0, gq) - gq, max(g1, gq) - gq);
 }
 
-// Every other form: part of the channels rotated, neighbouring pairs, none.  A
-// lane's 8 channels lie together.
-template <int D>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const RopeArgs a, int parts) {
-  constexpr int LH = D / 8, HW = 32 / LH;
-  __shared__ float2 turn[kRopeWarps][D / 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LH, half = a.rot / 2, c0 = 8 * l;
-  const int64_t id = (int64_t)blockIdx.x * kRopeWarps + warp, row = id / parts;
-  pdl_wait();
-  pdl_trigger();
-  if (row >= a.T) return;
-  const float2* cs = turn[warp];
-  if (half) rope_angles(a, row, lane, turn[warp]);
-  const int heads = a.H + a.Hkv, groups = (heads + HW - 1) / HW;
-  const int per = (groups + parts - 1) / parts, g0 = (int)(id - row * parts) * per, g1 = min(groups, g0 + per);
-  for (int gb = g0; gb < g1; gb += kRopeBatch) {
-    uint4 in[kRopeBatch];
-#pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
-      const int h = (gb + k) * HW + lane / LH;
-      in[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (gb + k < g1 && h < heads)
-        in[k] = *reinterpret_cast<const uint4*>((h < a.H ? a.q + row * a.ld_q + h * D : a.k + row * a.ld_k + (h - a.H) * D) + c0);
-    }
-#pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
-      if (gb + k >= g1) break;
-      const int h = (gb + k) * HW + lane / LH;
-      const bool isq = h < a.H;
-      const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
-      float x[8], ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-      for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const uint16_t* nw = isq ? a.q_w : a.k_w;
-      if (nw) {
-        const float rr = rsqrtf(ss * (1.0f / D) + a.eps);
-        const uint4 v = *reinterpret_cast<const uint4*>(nw + c0);
-        const uint32_t n[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] *= rr * bf16lo(n[i]), x[2 * i + 1] *= rr * bf16hi(n[i]);
-      }
-      if (half && a.interleaved) {
-        if (c0 < a.rot) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 t = cs[c0 / 2 + i];
-            const float u = x[2 * i], v = x[2 * i + 1];
-            x[2 * i] = u * t.x - v * t.y;
-            x[2 * i + 1] = v * t.x + u * t.y;
-          }
-        }
-      } else if (half) {
-        // the partner channel is rot/2 away: rot/16 lanes
-        __syncwarp();
-        const int dl = a.rot / 16;
-        const bool first = l < dl, in_rot = l < 2 * dl;
-        const int src = in_rot ? (first ? lane + dl : lane - dl) : lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xffffffffu, x[i], src);
-          if (in_rot) {
-            const float2 t = cs[(first ? c0 : c0 - half) + i];
-            x[i] = x[i] * t.x + (first ? -o : o) * t.y;
-          }
-        }
-      }
-      if (h < heads)
-        *reinterpret_cast<uint4*>((isq ? a.q_out + row * a.ld_qo + h * D : a.k_out + row * a.ld_ko + (h - a.H) * D) + c0) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
-    }
-  }
-}
-
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t s) {
-  const bool all = a.rot == a.D && !a.interleaved;
+  const bool part = a.rot < a.D, next = a.interleaved && a.rot;
   // Few rows: a row's heads are dealt out over several warps, until every SM has
   // 16 (64 rows of 32 + 8 heads of 128: one batch of loads a warp).
   int parts = 1;
   while (parts < 8 && (int64_t)a.T * parts < 16ll * num_sms()) parts *= 2;
   const dim3 grid((unsigned)(((int64_t)a.T * parts + kRopeWarps - 1) / kRopeWarps)), block(kRopeWarps * 32);
-  auto k = a.D == 128 ? (all ? qk_norm_rope_all_kernel<128> : qk_norm_rope_kernel<128>)
-                      : (all ? qk_norm_rope_all_kernel<64> : qk_norm_rope_kernel<64>);
+  void (*const kernels[2][2][2])(RopeArgs, int) = {
+      {{qk_norm_rope_kernel<64, false, false>, qk_norm_rope_kernel<64, false, true>},
+       {qk_norm_rope_kernel<64, true, false>, qk_norm_rope_kernel<64, true, true>}},
+      {{qk_norm_rope_kernel<128, false, false>, qk_norm_rope_kernel<128, false, true>},
+       {qk_norm_rope_kernel<128, true, false>, qk_norm_rope_kernel<128, true, true>}}};
+  auto k = kernels[a.D == 128][next][part];
   trace_pre(K_QK_NORM_ROPE, s);
   const cudaError_t e = launch_k(k, grid, block, 0, s, true, a, parts);
   trace_post(K_QK_NORM_ROPE, s);
