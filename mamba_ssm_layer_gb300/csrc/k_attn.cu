@@ -10,7 +10,10 @@
 // m is the row's reference maximum.  It follows the running maximum only when
 // that has grown by more than 2^8 in the exponential: until then P stays below
 // 2^8, which bf16 and fp32 hold as well, and O needs no rescaling.
-// CTAs are persistent: the copies and the first scores of a CTA's next item (a
+// Few items over many keys are cut along the keys (SPLIT): a cluster takes an item,
+// each of its CTAs a run of the blocks, and they join their maxima, sums and outputs
+// through each other's shared memory.
+// Otherwise CTAs are persistent: the copies and the first scores of a CTA's next item (a
 // tile pair of one head group) run under the last softmax and the output of the
 // current one.
 // Bound: the tensor cores (4 * 128 * 128 * D operations a tile pair) and the
@@ -111,6 +114,7 @@ struct AtArgs {
   int32_t items;    // tile pairs * groups
   int32_t wide;     // output rows start on 32 bytes
   int32_t sorted;   // order[] holds the pairs, most key blocks first
+  int32_t split;    // CTAs of an item
   int64_t limit;    // of the pipeline's waits, SM clock cycles
   int32_t cu_q[kSeqs + 1], cu_k[kSeqs + 1];
   int32_t tile[kSeqs + 1];  // first tile pair of each sequence
@@ -269,11 +273,15 @@ __device__ __forceinline__ bool at_drain(uint64_t* bar, uint32_t parity) {
 
 // A CTA's k-th item: every other round backwards, so that each CTA gets late
 // (long) and early (short) tiles alike.
-__device__ __forceinline__ int at_pick(int k, int items) {
+template <bool SPLIT>
+__device__ __forceinline__ int at_pick(int k, const AtArgs& a) {
+  if (SPLIT) return k == 0 ? (int)blockIdx.x / a.split : -1;
+  const int items = a.items;
   const int g = gridDim.x, id = k * g + (k & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
   return id < items ? id : -1;
 }
 
+template <bool SPLIT>
 __device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
   AtItem it;
   const int tokens = kAtRows >> a.pk_log;  // of one tile
@@ -299,6 +307,13 @@ __device__ __forceinline__ AtItem at_item(const AtArgs& a, int id) {
   };
   it.n0 = blocks(0);
   it.n1 = blocks(tokens);
+  if (SPLIT) {  // this CTA's run of the blocks, as if the sequence began there
+    const int run = (max(it.n0, it.n1) + a.split - 1) / a.split, from = (int)blockIdx.x % a.split * run;
+    it.n0 = min(max(it.n0 - from, 0), run);
+    it.n1 = min(max(it.n1 - from, 0), run);
+    it.see -= from * kAtRows;
+    it.row_k += from * kAtRows;
+  }
   it.jm = max(0, (it.see + 1) >> 7);
   return it;
 }
@@ -357,7 +372,22 @@ __device__ __forceinline__ bool at_next(const AtArgs& a, AtBars* bars, int pick,
   return it.hg >= 0;
 }
 
-template <int D, bool TEST>
+// The shared memory of the cluster's CTA `rank`, at this CTA's address.
+__device__ __forceinline__ float cluster_ld(const float* p, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(smem_addr(p)), "r"(rank)
+               : "memory");
+  return v;
+}
+// Every thread of every CTA of the cluster (each comes here: all waits before it are bounded).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int D, bool TEST, bool SPLIT>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AtArgs a) {
@@ -399,6 +429,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const int tokens = kAtRows >> a.pk_log;
   pdl_wait();
   pdl_trigger();
+  // SPLIT: the row's maximum, sum, key blocks and output here
+  float part_m = -INFINITY, part_l = 0.0f;
+  int part_n = 0;
+  uint16_t* part_dst = nullptr;
 
   // Every role walks the same items, which the copies' thread picks; a key block j of an item is copies kv + 2j
   // (K) and kv + 2j + 1 (V) of the CTA, and barrier phases are counted through.
@@ -410,10 +444,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       int kv = 0, nq0 = 0, nq1 = 0;  // copies and Q tiles issued
       bool dead = false;
       for (int pick = 0; !dead; ++pick) {
-        const int id = at_pick(pick, a.items), sl = pick % kAtItems;
+        const int id = at_pick<SPLIT>(pick, a), sl = pick % kAtItems;
         AtItem it;
         it.hg = -1;
-        if (id >= 0) it = at_item(a, id);
+        if (id >= 0) it = at_item<SPLIT>(a, id);
         if (pick >= kAtItems && !at_wait<TEST>(&bars->item_empty[sl], ((pick / kAtItems) - 1) & 1, a)) break;
         bars->item[sl] = it;
         mbar_arrive(&bars->item_full[sl]);
@@ -689,7 +723,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (dead) break;
-      const float inv = limit >= 0 ? 1.0f / l : 0.0f;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
       uint16_t* dst = a.out + (size_t)(it.row_q + min(tok, it.left - 1)) * a.ld_o +
                       (size_t)((it.hg << a.pk_log) + (r & ((1 << a.pk_log) - 1))) * D;
       // The next item is taken now: behind the stores, the slot's release would wait for them.
@@ -728,24 +762,29 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         tmem_st_wait();
       }
+      if constexpr (SPLIT) {
+        part_m = m, part_l = l, part_n = nt;
+        part_dst = tok < it.left ? dst : nullptr;
+      } else {
 #pragma unroll 1
-      for (int i = 0; i < D; i += 32) {
-        float o[32];
-        if (nt > 0) {
-          tmem_ld32_async(to + i, o);
-          tmem_ld_wait<32>(o);
-        }
-        uint32_t w[16];
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          if (nt > 0) {
+            tmem_ld32_async(to + i, o);
+            tmem_ld_wait<32>(o);
+          }
+          uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = limit >= 0 ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
-        if (tok < it.left) {
-          if (a.wide) {
-            store32(dst + i, w);
-            store32(dst + i + 16, w + 8);
-          } else {
+          for (int k = 0; k < 16; ++k) w[k] = l != 0.0f ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+          if (tok < it.left) {
+            if (a.wide) {
+              store32(dst + i, w);
+              store32(dst + i + 16, w + 8);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<uint4*>(dst + i + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+              for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<uint4*>(dst + i + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+            }
           }
         }
       }
@@ -758,6 +797,64 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (SPLIT) {
+    // The tiles' memory is free now: O goes there, [tile][channel][row], then maxima and sums.
+    tc_fence_after();
+    const int t = warp >> 2, r = 32 * (warp & 3) + lane, n = a.split, d0 = (int)blockIdx.x % n * (D / n);
+    float* o_part = reinterpret_cast<float*>(smem) + t * D * kAtRows + r;
+    float* m_part = reinterpret_cast<float*>(smem) + 2 * D * kAtRows + t * kAtRows + r;
+    float* l_part = m_part + 2 * kAtRows;
+    static_assert((2 * D + 4) * kAtRows * 4 <= C::kBars, "shared memory");
+    if (warp < 8) {
+      *m_part = part_m;
+      *l_part = part_l;
+      if (part_n > 0) {
+        const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::kTmO + t * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          tmem_ld32_async(to + i, o);
+          tmem_ld_wait<32>(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o_part[(i + k) * kAtRows] = o[k];
+        }
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp < 8 && part_dst) {
+      const float c = a.scale_log2 > 0.0f ? a.scale_log2 : 1.0f;
+      float top = -INFINITY, l = 0.0f, w[8];
+      for (int y = 0; y < n; ++y) top = fmaxf(top, cluster_ld(m_part, y));
+      uint32_t some = 0;  // parts that saw something
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        w[y] = 0.0f;
+        if (y >= n) continue;
+        const float m1 = cluster_ld(m_part, y), l1 = cluster_ld(l_part, y);
+        if (m1 == -INFINITY && l1 == 0.0f) continue;
+        some |= 1u << y;
+        w[y] = m1 == -INFINITY ? 1.0f : ex2((m1 - top) * c);  // (a sum of NaN is passed on)
+        l = fmaf(l1, w[y], l);
+      }
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      for (int d = d0; d < d0 + D / n; d += 8) {
+        float o[8] = {};
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          if (!(some >> y & 1u)) continue;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = fmaf(cluster_ld(o_part + (d + k) * kAtRows, y), w[y], o[k]);
+        }
+        *reinterpret_cast<uint4*>(part_dst + d) =
+            make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                       pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // a CTA's memory stays until all have read it
+  }
   if (warp == 8) {
     tc_fence_after();
     tmem_free(tmem, 512);
@@ -784,9 +881,53 @@ static bool encode_heads(CUtensorMap* map, const uint16_t* base, int D, int head
 // Limit of the pipeline's waits of each device (0: the default), for later launches.
 static std::atomic<long long> g_limit[64];
 
-template <int D, bool TEST>
-static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s) {
+// CTAs of an item: a cut costs a join of about 4 key blocks, and its cluster's CTAs
+// have to find room together (in 4 of 5 SMs).  Measured at 32 heads on 8 of 128, one
+// sequence, cut and uncut: 16 tokens on 500 keys 10.3 and 8.0 us, 700 10.4 and 10.1,
+// 1000 11.3 and 12.4, 4000 15 and 38; 64 tokens on 60000 keys 87 and 581.
+static int at_split(int items, int64_t blocks) {
+  int best = 1;
+  int64_t cost = blocks;
+  for (int n = 2; n <= 8 && items * n <= num_sms() * 4 / 5; n *= 2) {
+    const int64_t c = (blocks + n - 1) / n + 4;
+    if (c < cost) best = n, cost = c;
+  }
+  return best;
+}
+
+template <int D, bool TEST, bool SPLIT>
+static cudaError_t launch_attn_kernel(const AtArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                      cudaStream_t s) {
   static int done_mask[64] = {0};
+  auto kern = attn_prefill_kernel<D, TEST, SPLIT>;
+  constexpr int smem = at_smem_bytes<D>();
+  cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
+  if (e != cudaSuccess) return e;
+  trace_pre(K_ATTN_PREFILL, s);
+  if (SPLIT) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.items * a.split);
+    cfg.blockDim = dim3(kAtThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, q, k, v, a);
+  } else {
+    e = launch_k(kern, dim3(a.items < num_sms() ? a.items : num_sms()), dim3(kAtThreads), smem, s, true, q, k, v, a);
+  }
+  trace_post(K_ATTN_PREFILL, s);
+  return e;
+}
+
+template <int D>
+static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s) {
   AtArgs a;
   a.limit = limit;
   a.out = g.out;
@@ -814,12 +955,16 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
       !encode_heads(&k, keys ? g.k : g.q, D, keys ? g.Hkv : 1, keys ? g.Tk : 1, keys ? g.ld_k : g.ld_q, 1, kAtRows) ||
       !encode_heads(&v, keys ? g.v : g.q, D, keys ? g.Hkv : 1, keys ? g.Tk : 1, keys ? g.ld_v : g.ld_q, 1, kAtRows))
     return cudaErrorInvalidValue;
-  auto kern = attn_prefill_kernel<D, TEST>;
-  constexpr int smem = at_smem_bytes<D>();
-  cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
-  if (e != cudaSuccess) return e;
   a.items = a.tile[g.nseq] * a.groups;
   a.sorted = a.tile[g.nseq] <= kAtSorted ? 1 : 0;
+  int64_t longest = 0;  // key blocks of a pair
+  for (int i = 0; i < g.nseq; ++i) {
+    const int nq = a.cu_q[i + 1] - a.cu_q[i], nk = a.cu_k[i + 1] - a.cu_k[i];
+    const int64_t n = nq > 0 ? ((int64_t)nk + kAtRows - 1) / kAtRows : 0;
+    longest = n > longest ? n : longest;
+  }
+  const bool test = limit < 1000000;
+  a.split = test ? 1 : at_split(a.items, longest);
   if (a.sorted) {  // counting sort by key blocks (longer than the last bucket: any order)
     constexpr int kBuckets = 256;
     uint16_t first[kBuckets + 1] = {0}, len[kAtSorted];
@@ -835,10 +980,8 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
     for (int b = 0; b < kBuckets; ++b) first[b + 1] += first[b];
     for (int t = 0; t < a.tile[g.nseq]; ++t) a.order[first[len[t]]++] = (uint16_t)t;
   }
-  trace_pre(K_ATTN_PREFILL, s);
-  e = launch_k(kern, dim3(a.items < num_sms() ? a.items : num_sms()), dim3(kAtThreads), smem, s, true, q, k, v, a);
-  trace_post(K_ATTN_PREFILL, s);
-  return e;
+  if (test) return launch_attn_kernel<D, true, false>(a, q, k, v, s);
+  return a.split > 1 ? launch_attn_kernel<D, false, true>(a, q, k, v, s) : launch_attn_kernel<D, false, false>(a, q, k, v, s);
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
@@ -846,8 +989,7 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
   cudaGetDevice(&dev);
   int64_t limit = dev >= 0 && dev < 64 ? g_limit[dev].load(std::memory_order_relaxed) : 0;
   if (limit <= 0) limit = kWaitCycles;
-  if (limit < 1000000) return a.D == 128 ? launch_attn<128, true>(a, limit, s) : launch_attn<64, true>(a, limit, s);
-  return a.D == 128 ? launch_attn<128, false>(a, limit, s) : launch_attn<64, false>(a, limit, s);
+  return a.D == 128 ? launch_attn<128>(a, limit, s) : launch_attn<64>(a, limit, s);
 }
 
 int status_attn(int clear) { return tu_status(clear); }

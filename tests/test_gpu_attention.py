@@ -331,6 +331,27 @@ def test_prefill_bad_values_stay_where_they_are_seen(bad, D, H, Hkv):
     assert bool(got[533:623].isfinite().all()) and bool(got[623:].isnan().all())
 
 
+@pytest.mark.parametrize("D,H,Hkv", [(128, 8, 2), (64, 4, 4), (128, 5, 1), (64, 16, 1)])
+@pytest.mark.parametrize("lens_q,lens_k", [
+    ([1], [9000]), ([1], [1409]), ([70], [3333]), ([300], [2500]), ([1, 40, 0, 9], [1500, 4000, 17, 3]),
+    ([600], [600]), ([1500], [1500]), ([2000, 30], [1100, 30])])
+def test_prefill_few_rows_over_many_keys(lens_q, lens_k, D, H, Hkv):
+    """Few items, cut along the keys: parts of one block, parts that some row or tile does not reach."""
+    run_prefill(lens_q, lens_k, H, Hkv, D, extra=8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_few_rows_values_of_far_parts(D):
+    """Scores that grow from part to part, values that are not finite in the first and the last one."""
+    def plant(q, k, v, cu_q, cu_k):
+        k.mul_(torch.linspace(0.01, 4.0, len(k), device="cuda")[:, None])
+        v[1990, 3] = math.inf   # seen from row 30 of sequence 0 on
+        v[cu_k[1] + 5, 7] = math.nan
+    got, _ = run_prefill([40, 20], [2000, 1800], 4, 1, D, fix=plant)
+    assert bool(got[:30].isfinite().all()) and not bool(got[30:40, :, 3].isfinite().any())
+    assert bool(got[40:, :, :7].isfinite().all()) and not bool(got[40:, :, 7].isfinite().any())
+
+
 def test_prefill_unused_rows_may_hold_anything():
     """Rows around the sequences' own: q rows past a tile's end, k and v of the neighbours."""
     def plant(q, k, v, cu_q, cu_k):
