@@ -14,12 +14,12 @@
 // outputs are fp32.  Rows that a warp, then a CTA, holds only in part are
 // joined: warps through shared memory, CTAs by attn_decode_combine.
 // Bound: HBM (4.5 bits a value) and, as close, the issue rate: a unit is about
-// 1160 instructions of a warp (256 conversions of two codes, 256 multiplications by
-// scales, 64 MMAs at HN = 8), 82% of the issue slots while a span is streamed.
-// Measured at 32 + 8 heads of 128: 131000 tokens of one sequence 37 us (4.1 TB/s),
-// 64 sequences of 64..4096 tokens 43 us (4.0 TB/s); 6 to 7 us of that are the way to
-// the first data, 4 to 5 the joining.  8 warps with 3 stages took 48 us instead of 37
-// in the kernel itself, 12 warps with 128 registers the same.
+// 1060 instructions of a warp with all around it (256 conversions of two codes, 256
+// multiplications by scales, 64 MMAs at HN = 8), 80% of the issue slots while a span
+// is streamed.  Measured at 32 + 8 heads of 128: 131000 tokens of one sequence 35.5 us
+// (4.2 TB/s), 64 sequences of 64..4096 tokens 41 us (4.1 TB/s); 6 to 7 us of that are
+// the way to the first data, 4 to 5 the joining.  8 warps with 3 stages took 48 us
+// instead of 37 in the kernel itself, 12 warps with 128 registers the same.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
