@@ -1,8 +1,9 @@
 // k_attn.cu -- causal attention of packed sequences on the tensor cores.
 //
 // A tile is 128 query rows: 128 / PK consecutive tokens x PK query heads that
-// share a kv head (PK: the largest power of two that divides H / Hkv), so that
-// short prompts fill it and one K/V tile serves all of them.  A CTA takes two
+// share a kv head (PK: the largest power of two that divides H / Hkv, or the
+// smallest that covers it, with slots left empty, where that takes fewer tiles), so
+// that short prompts fill it and one K/V tile serves all of them.  A CTA takes two
 // neighbouring tiles of one sequence through the keys, 128 at a time:
 //   S = Q K^T   (tcgen05, 128 x 128 fp32 in tensor memory)
 //   P = exp2(c S - c m) as bf16, written over S; l += sum P   (one thread a row)
@@ -106,7 +107,8 @@ struct AtArgs {
   uint16_t* out;
   const uint16_t* v;
   int32_t ld_o, ld_v;
-  int32_t groups;   // H / PK
+  int32_t groups;   // H / slots
+  int32_t slots;    // heads of a tile: PK or, if that covers H / Hkv, H / Hkv
   int32_t pk_log;
   int32_t gqa;      // H / Hkv
   float scale_log2; // scale * log2(e)
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         bars->item[sl] = it;
         mbar_arrive(&bars->item_full[sl]);
         if (id < 0) break;
-        const int n = max(it.n0, it.n1), h0 = it.hg << a.pk_log, hk = h0 / a.gqa;
+        const int n = max(it.n0, it.n1), h0 = it.hg * a.slots, hk = h0 / a.gqa;
         auto load_q = [&](int t) {
           if (!(t ? it.n1 : it.n0) || dead) return;
           int& nq = t ? nq1 : nq0;
@@ -724,8 +726,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
       if (dead) break;
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
-      uint16_t* dst = a.out + (size_t)(it.row_q + min(tok, it.left - 1)) * a.ld_o +
-                      (size_t)((it.hg << a.pk_log) + (r & ((1 << a.pk_log) - 1))) * D;
+      const int slot = r & ((1 << a.pk_log) - 1);
+      const bool own = tok < it.left && slot < a.slots;  // a row of the output
+      uint16_t* dst = a.out + (size_t)(it.row_q + min(tok, it.left - 1)) * a.ld_o + (size_t)(it.hg * a.slots + slot) * D;
       // The next item is taken now: behind the stores, the slot's release would wait for them.
       AtItem next;
       more = at_next<TEST>(a, bars, pick + 1, lane, next);
@@ -745,9 +748,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const unsigned long long e = bad[w];
             for (uint32_t bits = j < nt && (uint32_t)(e >> 32) == item ? (uint32_t)e : 0; bits; bits &= bits - 1) {
               const int key = j * kAtRows + (w & 3) * 32 + __ffs(bits) - 1;
-              if (key > limit || tok >= it.left) continue;
+              if (key > limit || !own) continue;
               const uint16_t* vr = a.v + (size_t)(it.row_k + key) * a.ld_v +
-                                   (size_t)((it.hg << a.pk_log) / a.gqa) * D + i;
+                                   (size_t)(it.hg * a.slots / a.gqa) * D + i;
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float x = bf16_to_f32(vr[k]);
@@ -764,7 +767,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
       if constexpr (SPLIT) {
         part_m = m, part_l = l, part_n = nt;
-        part_dst = tok < it.left ? dst : nullptr;
+        part_dst = own ? dst : nullptr;
       } else {
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) w[k] = l != 0.0f ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
-          if (tok < it.left) {
+          if (own) {
             if (a.wide) {
               store32(dst + i, w);
               store32(dst + i + 16, w + 8);
@@ -935,10 +938,27 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
   a.ld_o = g.ld_o;
   a.ld_v = g.ld_v;
   a.gqa = g.H / g.Hkv;
-  a.pk_log = 0;
-  while (a.pk_log < 7 && a.gqa % (2 << a.pk_log) == 0) ++a.pk_log;
+  // Heads of a tile: the covering power of two if the dividing one makes more items
+  // than there are SMs and the covering one fewer.  Measured, dividing and covering:
+  // 59 sequences of 1..2 tokens, 14 heads on 2 (826 and 118 items) 20 and 6.4 us; 16 of
+  // 64..512 20.2 and 19.1; but 8 of 20..60 after 500..900, 12 heads on 4 (96 and 32
+  // items) 11.8 and 13.4.
+  int64_t least = 0;
+  for (int cover = 0; cover < 2; ++cover) {
+    int log = 0;
+    while (log < 7 && (cover ? (1 << log) < a.gqa : a.gqa % (2 << log) == 0)) ++log;
+    const int slots = cover ? a.gqa : 1 << log, pair = 2 * (kAtRows >> log);
+    if ((1 << log) < slots) continue;  // more heads than rows
+    int64_t n = 0;
+    for (int i = 0; i < g.nseq; ++i) n += (g.cu_q[i + 1] - g.cu_q[i] + pair - 1) / pair;
+    n *= g.H / slots;
+    if (cover && (least <= num_sms() || n >= least)) break;
+    least = n;
+    a.pk_log = log;
+    a.slots = slots;
+  }
   const int pk = 1 << a.pk_log, tokens = kAtRows / pk;
-  a.groups = g.H / pk;
+  a.groups = g.H / a.slots;
   a.scale_log2 = g.scale * 1.4426950408889634f;
   a.nseq = g.nseq;
   a.wide = (reinterpret_cast<uintptr_t>(g.out) & 31) == 0 && g.ld_o % 16 == 0;

@@ -341,6 +341,13 @@ def test_prefill_few_rows_over_many_keys(lens_q, lens_k, D, H, Hkv):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(7, 1), (14, 2), (3, 1), (12, 1), (33, 3), (100, 1), (130, 1)])
+@pytest.mark.parametrize("lens_q,lens_k", [([1, 2, 0, 1], [6, 7, 3, 1]), ([5] * 40, [9] * 40), ([3], [3000]), ([35, 150], [35, 170])])
+def test_prefill_heads_that_leave_slots_empty(lens_q, lens_k, H, Hkv, D):
+    run_prefill(lens_q, lens_k, H, Hkv, D, extra=8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_prefill_few_rows_values_of_far_parts(D):
     """Scores that grow from part to part, values that are not finite in the first and the last one."""
     def plant(q, k, v, cu_q, cu_k):
