@@ -59,6 +59,11 @@ constexpr int kAtRows = 128;      // query rows of a tile, keys of a block
 // (128 pairs) 237 to 232 both ways.
 constexpr int kAtSorted = 512;
 constexpr int kAtItems = 4;       // items handed on ahead of their use
+// Items whose marks of values are kept apart.  A softmax warp reads item i's marks
+// before it takes item i + 2, so that the last item handed on by then is i + 1 +
+// kAtItems; a tile that the next items leave empty holds nothing back earlier.
+constexpr int kAtMarks = 8;
+static_assert(kAtMarks >= kAtItems + 2, "marks are written again only after they have been read");
 constexpr int kAtMaskBlocks = 4;  // key blocks that some row of the two tiles sees only in part: at most 3
 
 template <int D>
@@ -91,10 +96,9 @@ struct AtBars {
   uint64_t item_full[kAtItems], item_empty[kAtItems];
   AtItem item[kAtItems];
   // Keys of a masked block whose values are not finite: (item << 32) | bits, by the
-  // CTA's item.  A block is looked through after its first scores were issued, when
-  // the tiles have at most the output of the item before last ahead of them.
-  unsigned long long bad[4][kAtMaskBlocks * 4];
-  uint32_t marked[4];  // the last item with such keys
+  // CTA's item with keys (items without lie between at most); then the last item
+  // that has such keys.
+  unsigned long long bad[kAtMarks][kAtMaskBlocks * 4 + 1];
   uint32_t tmem;
 };
 template <int D>
@@ -330,8 +334,8 @@ __device__ __forceinline__ void max_abs(uint32_t& a, uint32_t b) {
 // zero in shared memory and their key is marked; rows that do see the key add
 // them at the end.
 template <int D>
-__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long long* bad, volatile uint32_t* marked,
-                                             uint32_t item) {
+__device__ __forceinline__ void at_clean_row(uint8_t* tile, int r, unsigned long long* bad,
+                                             volatile unsigned long long* marked, uint32_t item) {
   uint32_t top[2] = {0u, 0u};  // largest magnitudes, NaN above all
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
@@ -419,8 +423,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
-    for (int i = 0; i < 4 * kAtMaskBlocks * 4; ++i) (&bars->bad[0][0])[i] = ~0ull;
-    for (int i = 0; i < 4; ++i) bars->marked[i] = ~0u;
+    for (int i = 0; i < kAtMarks * (kAtMaskBlocks * 4 + 1); ++i) (&bars->bad[0][0])[i] = ~0ull;
     fence_mbar_init();
   }
   if (warp == 8) tmem_alloc(&bars->tmem, 512);
@@ -613,8 +616,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             break;
           }
           for (int r = (warp - 10) * 32 + lane; r < kAtRows; r += 64)
-            at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[item & 3] + 4 * (j - it.jm),
-                            &bars->marked[item & 3], item);
+            at_clean_row<D>(smem + C::kKV + (vi % NS) * C::kTile, r, bars->bad[item % kAtMarks] + 4 * (j - it.jm),
+                            &bars->bad[item % kAtMarks][kAtMaskBlocks * 4], item);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->clean);
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int tok = t * tokens + (r >> a.pk_log);
       const int limit = it.see + tok;  // the last key this row sees
       const int warp_limit = it.see + t * tokens + ((r & ~31) >> a.pk_log);  // the warp's first row
-      unsigned long long* bad = bars->bad[item & 3];
+      unsigned long long* bad = bars->bad[item % kAtMarks];
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < nt; ++j) {
         if (!at_wait_warp<TEST>(&bars->s_full[t], (ns + j) & 1, a)) {
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         break;
       }
       tc_fence_after();
-      if (nt > 0 && bars->marked[item & 3] == item) {  // add the values that were kept out of the products, where they are seen
+      if (nt > 0 && bad[kAtMaskBlocks * 4] == item) {  // add the values that were kept out of the products, where they are seen
 #pragma unroll 1
         for (int i = 0; i < D; i += 16) {
           float o[16];
