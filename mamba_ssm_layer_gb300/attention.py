@@ -91,13 +91,27 @@ class DeviceAttention:
 
     def buffers(self, max_rows: int, max_keys: int = 0, nseq: int = 1) -> dict:
         """Scratch for calls of up to max_rows token rows (prompts over cached tokens: max_keys cached and new
-        tokens of all sequences).  Layers run one after the other can share it."""
+        tokens of all sequences; calls that need more are refused).  Layers run one after the other can share it."""
         bf, dev = torch.bfloat16, self.device
         return dict(qkv=_empty((max_rows, self.n_qkv), bf, dev), q=_empty((max_rows, self.H * self.D), bf, dev),
                     k=_empty((max_rows, self.Hkv * self.D), bf, dev),
                     attn=_empty((max_rows, self.H * self.D), bf, dev),
                     keys=_empty((max(max_keys, 1), 2 * self.Hkv * self.D), bf, dev),
                     ws=_empty((abi.m2_attn_decode_kv4_workspace_bytes(nseq, self.H, self.Hkv, self.D),), torch.uint8, dev))
+
+    def _check(self, fn, T, x, out, row_pos, cache, b, keys=0) -> None:
+        """T rows of x, out and row_pos, and scratch and cache of this mixer's heads that hold them: the kernels
+        see pointers only."""
+        def dense(t, rows, width):
+            return t.shape == (rows, width) and t.element_size() == 2 and t.is_contiguous()
+        if not (dense(x, T, self.hidden) and dense(out, T, self.hidden) and row_pos.dtype == torch.int32
+                and row_pos.numel() == T and row_pos.is_contiguous()
+                and (cache.n_kv_heads, cache.head_dim) == (self.Hkv, self.D)):
+            raise abi.M2Error(fn, abi.M2_ERR_ARG)
+        widths = dict(qkv=self.n_qkv, q=self.H * self.D, k=self.Hkv * self.D, attn=self.H * self.D,
+                      keys=2 * self.Hkv * self.D)
+        if any(b[k].shape[1] != w or b[k].shape[0] < (keys if k == "keys" else T) for k, w in widths.items()):
+            raise abi.M2Error(fn, abi.M2_ERR_WORKSPACE)
 
     def _project(self, x, b, row_pos, stream):
         T, H, Hkv, D, n = x.shape[0], self.H, self.Hkv, self.D, self.n_qkv
@@ -113,13 +127,16 @@ class DeviceAttention:
     def prefill(self, x, new, row_pos, cache: Kv4Cache, layer: int, b: dict, out, stream=None) -> None:
         """x, out [sum(new)][hidden] bf16: new[i] tokens of each sequence, after those that the cache holds.
         row_pos: device int32, each row's position.  Appends to the cache (reserved before); the caller advances."""
-        s = stream if stream is not None else torch.cuda.current_stream()
-        H, Hkv, D = self.H, self.Hkv, self.D
-        q, k, v = self._project(x, b, row_pos, s)
+        if len(new) != cache.nseq or min(new) < 0:
+            raise abi.M2Error("DeviceAttention.prefill", abi.M2_ERR_ARG)
         cu, all_ = [0], [0]
         for n, t in zip(new, cache.tokens):
             cu.append(cu[-1] + n)
             all_.append(all_[-1] + n + t)
+        self._check("DeviceAttention.prefill", cu[-1], x, out, row_pos, cache, b, all_[-1] if all_[-1] > cu[-1] else 0)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        H, Hkv, D = self.H, self.Hkv, self.D
+        q, k, v = self._project(x, b, row_pos, s)
         abi.m2_kv4_append(cache.struct[layer], k, Hkv * D, v, self.n_qkv, cu, cache.pos, s)
         ld_k, ld_v = Hkv * D, self.n_qkv
         if all_[-1] > cu[-1]:
@@ -132,6 +149,7 @@ class DeviceAttention:
     def decode(self, x, cache: Kv4Cache, layer: int, b: dict, kv_len, out, stream=None) -> None:
         """x, out [nseq][hidden] bf16: one token of every sequence; kv_len = cache.pos + 1 (device int32).
         Appends and attends; the caller advances.  Can be captured."""
+        self._check("DeviceAttention.decode", cache.nseq, x, out, kv_len, cache, b)
         s = stream if stream is not None else torch.cuda.current_stream()
         H, Hkv, D = self.H, self.Hkv, self.D
         q, k, v = self._project(x, b, cache.pos, s)

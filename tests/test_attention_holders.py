@@ -1,0 +1,117 @@
+"""The attention mixer's and the cache's holders on the host: what they refuse and count.  No GPU needed: the
+holders live on the CPU and no kernel is launched."""
+import pytest
+import torch
+
+from mamba_ssm_layer_gb300 import abi, synth
+from mamba_ssm_layer_gb300.attention import DeviceAttention, Kv4Cache
+
+bf = torch.bfloat16
+DIMS = synth.TINY_ATTENTION
+CALLS = ("w8a16_gemv", "m2_qk_norm_rope", "m2_kv4_append", "m2_kv4_gather", "m2_attn_prefill_varlen",
+         "m2_attn_decode_kv4")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from __graft_entry__ import build
+    build()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names and arguments of the entry points that a holder calls, in place of the calls."""
+    seen = []
+    for name in CALLS:
+        monkeypatch.setattr(abi, name, lambda *a, _n=name, **k: seen.append((_n, a)))
+    return seen
+
+
+@pytest.fixture(scope="module")
+def mixer():
+    return DeviceAttention(synth.make_attention(DIMS, 9), device="cpu")
+
+
+class Stream:
+    cuda_stream = 0
+
+
+def prefill(m, cache, b, new, **over):
+    a = dict(x=torch.zeros(sum(new), m.hidden, dtype=bf), row_pos=torch.zeros(sum(new), dtype=torch.int32),
+             out=torch.zeros(sum(new), m.hidden, dtype=bf))
+    a.update(over)
+    m.prefill(a["x"], new, a["row_pos"], cache, 0, b, a["out"], Stream())
+
+
+def decode(m, cache, b, **over):
+    a = dict(x=torch.zeros(cache.nseq, m.hidden, dtype=bf), kv_len=cache.pos + 1,
+             out=torch.zeros(cache.nseq, m.hidden, dtype=bf))
+    a.update(over)
+    m.decode(a["x"], cache, 0, b, a["kv_len"], a["out"], Stream())
+
+
+def cache_of(m, nseq=2, **over):
+    a = dict(n_layers=1, nseq=nseq, n_pages=12, max_tokens=256, n_kv_heads=m.Hkv, head_dim=m.D, device="cpu")
+    a.update(over)
+    return Kv4Cache(**a)
+
+
+@pytest.mark.parametrize("new,over", [
+    ([5, 8], {}),                                         # more rows than max_rows
+    ([5], {}), ([1, 2, 3], {}), ([-1, 4], {}),            # not a count for every sequence
+    ([3, 4], dict(x=torch.zeros(6, DIMS["hidden"], dtype=bf))),
+    ([3, 4], dict(x=torch.zeros(8, DIMS["hidden"], dtype=bf))),
+    ([3, 4], dict(x=torch.zeros(7, DIMS["hidden"] - 8, dtype=bf))),
+    ([3, 4], dict(x=torch.zeros(7, DIMS["hidden"] + 8, dtype=bf)[:, 8:])),  # the rows are not dense
+    ([3, 4], dict(x=torch.zeros(7, DIMS["hidden"]))),
+    ([3, 4], dict(out=torch.zeros(6, DIMS["hidden"], dtype=bf))),
+    ([3, 4], dict(row_pos=torch.zeros(6, dtype=torch.int32))),
+    ([3, 4], dict(row_pos=torch.zeros(7, dtype=torch.int64)))])
+def test_prefill_refuses_rows_that_do_not_fit(mixer, calls, new, over):
+    cache, b = cache_of(mixer), mixer.buffers(12, 64, 2)
+    prefill(mixer, cache, b, [3, 4])  # the call itself is fine
+    assert len(calls) == 5
+    with pytest.raises(abi.M2Error):
+        prefill(mixer, cache, b, new, **over)
+    assert len(calls) == 5  # refused before any launch
+
+
+@pytest.mark.parametrize("max_keys,held,ok", [(0, [0, 0], True), (0, [1, 0], False), (27, [20, 0], True),
+                                              (26, [20, 0], False), (26, [0, 20], False)])
+def test_prefill_refuses_more_keys_than_its_buffer_holds(mixer, calls, max_keys, held, ok):
+    cache, b = cache_of(mixer), mixer.buffers(12, max_keys, 2)
+    cache.tokens[:] = held
+    if ok:
+        prefill(mixer, cache, b, [3, 4])
+        assert [n for n, _ in calls].count("m2_kv4_gather") == (1 if any(held) else 0)
+    else:
+        with pytest.raises(abi.M2Error) as e:
+            prefill(mixer, cache, b, [3, 4])
+        assert e.value.status == abi.M2_ERR_WORKSPACE and not calls
+
+
+@pytest.mark.parametrize("over", [
+    dict(x=torch.zeros(3, DIMS["hidden"], dtype=bf)), dict(x=torch.zeros(1, DIMS["hidden"], dtype=bf)),
+    dict(out=torch.zeros(1, DIMS["hidden"], dtype=bf)), dict(kv_len=torch.zeros(1, dtype=torch.int32)),
+    dict(kv_len=torch.zeros(2, dtype=torch.int64))])
+def test_decode_refuses_rows_that_do_not_fit(mixer, calls, over):
+    cache, b = cache_of(mixer), mixer.buffers(12, 64, 2)
+    decode(mixer, cache, b)
+    assert len(calls) == 5
+    with pytest.raises(abi.M2Error):
+        decode(mixer, cache, b, **over)
+    with pytest.raises(abi.M2Error):
+        decode(mixer, cache, mixer.buffers(1, 64, 2))
+    assert len(calls) == 5
+
+
+def test_buffers_and_caches_of_other_heads_are_refused(mixer, calls):
+    other = DeviceAttention(synth.make_attention(dict(DIMS, kv_heads=1), 9), device="cpu")
+    with pytest.raises(abi.M2Error):
+        prefill(mixer, cache_of(mixer), other.buffers(12, 64, 2), [3, 4])
+    for heads in (dict(n_kv_heads=1), dict(head_dim=128)):
+        with pytest.raises(abi.M2Error):
+            prefill(mixer, cache_of(mixer, **heads), mixer.buffers(12, 64, 2), [3, 4])
+        with pytest.raises(abi.M2Error):
+            decode(mixer, cache_of(mixer, **heads), mixer.buffers(12, 64, 2))
+    assert not calls
