@@ -72,6 +72,7 @@ static int kv4_rows(const m2_kv4_cache* c, uint16_t* k, int32_t ld_k, uint16_t* 
   if ((st = check_offsets(cu, c->nseq))) return st;
   if (cu[c->nseq] == 0) return M2_OK;  // no rows: their pointers may be null
   if ((st = check_rows(k, ld_k, w)) || (st = check_rows(v, ld_v, w))) return st;
+  if (reinterpret_cast<uintptr_t>(pos) & 3u) return M2_ERR_ALIGN;
   for (int32_t i0 = 0; i0 < c->nseq; i0 += kSeqs) {
     const int32_t n = c->nseq - i0 < kSeqs ? c->nseq - i0 : kSeqs;
     if (cu[i0 + n] == cu[i0]) continue;
