@@ -1,9 +1,10 @@
 """A small hybrid stack: a Mamba-2 layer, an attention mixer, a Mamba-2 layer.
 
 Prompts of different lengths go through the stack in one call per layer, a second
-chunk of each follows over the cached tokens, and then single tokens, replayed
-from a captured graph.  The attention mixer runs between an RMS norm and a
-residual add (plain torch here); everything else is the library's kernels.
+chunk of each follows over the cached tokens, then single tokens, replayed from a
+captured graph, and one more chunk over all of them.  The attention mixer runs
+between an RMS norm and a residual add (plain torch here); everything else is the
+library's kernels.
 
     python examples/hybrid_stack.py            # small shapes
     python examples/hybrid_stack.py --wide     # hidden 4096, 32 query and 8 kv heads of 128
@@ -53,7 +54,8 @@ class HybridStack:
         self.cache.advance(new)
 
     def decode(self, x):
-        """x [nseq][hidden] bf16 bits, in place: one token of each sequence (pages reserved before)."""
+        """x [nseq][hidden] bf16 bits, in place: one token of each sequence (pages reserved before).  Can be
+        captured: the device counts it, ``decoded`` tells the host."""
         self.first.decode(x, self.states[0], self.ws)
         torch.add(self.cache.pos, 1, out=self.kv_len)
         out = self.mixed[:self.nseq]
@@ -61,6 +63,10 @@ class HybridStack:
         x.view(torch.bfloat16).add_(out)
         self.last.decode(x, self.states[1], self.ws)
         self.cache.pos.add_(1)
+
+    def decoded(self, steps):
+        """The decode steps that have run since the last prompt or call of this."""
+        self.cache.advance([steps] * self.nseq, on_device=False)
 
 
 def main(wide=False, steps=32):
@@ -87,10 +93,13 @@ def main(wide=False, steps=32):
         graph.replay()
     torch.cuda.synchronize()
     t = time.perf_counter() - t
-    finite = bool(torch.isfinite(rows.view(torch.bfloat16)).all())
-    print(f"{nseq} sequences, prompts {min(lens)}..{max(lens)} + 64, {steps} tokens each: "
+    stack.decoded(steps + 1)
+    chunk = to_dev(synth.make_hidden(64 * nseq, stack.hidden, 7, 3))
+    stack.prefill(chunk, [64] * nseq)
+    finite = all(bool(torch.isfinite(x.view(torch.bfloat16)).all()) for x in (rows, chunk))
+    print(f"{nseq} sequences, prompts {min(lens)}..{max(lens)} + 64, {steps} tokens each, + 64: "
           f"{t / steps * 1e6:.1f} us a step, finite {finite}")
-    return finite and stack.cache.pos.tolist() == [n + 64 + 1 + steps for n in lens]
+    return finite and stack.cache.pos.tolist() == stack.cache.tokens == [n + 64 + 1 + steps + 64 for n in lens]
 
 
 if __name__ == "__main__":

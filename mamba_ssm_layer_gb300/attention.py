@@ -22,7 +22,9 @@ class Kv4Cache:
     every layer's pool belongs to the same tokens).  ``reserve`` hands out pages
     on the host; appending, reading and attending are the layers' calls; then
     ``advance`` counts the new tokens.  A captured decode loop reserves ahead and
-    advances with ``pos.add_(1)`` inside the capture.
+    advances with ``pos.add_(1)`` inside the capture; the host's count follows after
+    the replays, before the next ``reserve`` or prompt, with
+    ``advance(steps, on_device=False)``.
     """
 
     def __init__(self, n_layers: int, nseq: int, n_pages: int, max_tokens: int, n_kv_heads: int, head_dim: int,
@@ -57,9 +59,11 @@ class Kv4Cache:
             self._owned[i] += got
             self.table[i, have:have + n].copy_(torch.tensor(got, dtype=torch.int32))
 
-    def advance(self, new) -> None:
-        """Counts new[i] appended tokens of each sequence (on the device unless the capture did it)."""
-        self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
+    def advance(self, new, on_device: bool = True) -> None:
+        """Counts new[i] appended tokens of each sequence.  on_device False: on the host only, where ``pos`` has
+        counted them already (a captured loop)."""
+        if on_device:
+            self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
         self.tokens = [t + n for t, n in zip(self.tokens, new)]
 
     def release(self, seq: int) -> None:

@@ -115,3 +115,17 @@ def test_buffers_and_caches_of_other_heads_are_refused(mixer, calls):
         with pytest.raises(abi.M2Error):
             decode(mixer, cache_of(mixer, **heads), mixer.buffers(12, 64, 2))
     assert not calls
+
+
+def test_cache_counts_what_a_captured_loop_advanced():
+    c = Kv4Cache(1, 2, 20, 640, 2, 64, device="cpu")
+    c.reserve([100, 70])
+    c.advance([100, 70])
+    for _ in range(40):  # as in a capture: the device counts, the host does not see it
+        c.pos.add_(1)
+    c.advance([40, 40], on_device=False)
+    assert c.pos.tolist() == c.tokens == [140, 110]
+    c.reserve([64, 64])
+    assert (c.table >= 0).sum(1).tolist() == [4, 3]  # 204 and 174 tokens
+    c.advance([64, 64])
+    assert c.pos.tolist() == c.tokens == [204, 174]

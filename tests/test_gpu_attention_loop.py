@@ -1,0 +1,106 @@
+"""The attention mixer in a conversation: a prompt, tokens from a captured loop, the next chunk.
+
+Attention is held to the 64-bit form on the rows that the stages before it left in
+their buffers, with the tolerances of test_gpu_attention.py."""
+import pytest
+import torch
+
+from mamba_ssm_layer_gb300 import abi, synth
+from mamba_ssm_layer_gb300.attention import DeviceAttention, Kv4Cache
+from mamba_ssm_layer_gb300.layer import to_dev
+from tests import attention_ref as ref
+from tests.test_gpu_attention import BF16, EVAL, F16, close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from __graft_entry__ import build
+    build()
+    abi.m2_device_status(clear=True)
+    yield
+    assert abi.m2_device_status() == abi.M2_OK
+
+
+class Talk:
+    """A mixer, its cache, and the keys and values that every sequence's cache holds, in 64 bits."""
+
+    def __init__(self, dims, nseq, max_tokens=512):
+        self.m, self.n = DeviceAttention(synth.make_attention(dims, 9)), nseq
+        self.cache = Kv4Cache(1, nseq, nseq * 8, max_tokens, self.m.Hkv, self.m.D)
+        self.b = self.m.buffers(600, 2000, nseq)
+        self.held = [[] for _ in range(nseq)], [[] for _ in range(nseq)]
+        self.call = 0
+
+    def hidden(self, T):
+        self.call += 1
+        return to_dev(synth.make_hidden(T, self.m.hidden, 9, self.call)).view(torch.bfloat16)
+
+    def rows(self, T):
+        """Queries, keys and values that the last call of T rows computed."""
+        m, b = self.m, self.b
+        v = b["qkv"][:T, (m.H + m.Hkv) * m.D:].reshape(T, m.Hkv, m.D)
+        return b["q"][:T].reshape(T, m.H, m.D), b["k"][:T].reshape(T, m.Hkv, m.D), v
+
+    def hold(self, new):
+        _, k, v = self.rows(sum(new))
+        at = 0
+        for i, n in enumerate(new):
+            self.held[0][i].append(ref.rounded_rows(k[at:at + n]))
+            self.held[1][i].append(ref.rounded_rows(v[at:at + n]))
+            at += n
+
+    def check(self, new, prec, own=()):
+        """The last call's attention; sequences in `own` attend to their own rows, the others to the cache's."""
+        q, k, v = self.rows(sum(new))
+        at = 0
+        for i, n in enumerate(new):
+            r = slice(at, at + n)
+            at += n
+            kk, vv = (k[r], v[r]) if i in own else (torch.cat(h[i]) for h in self.held)
+            want, size = ref.attend(q[r], kk, vv, self.m.scale)
+            close(self.b["attn"][r].reshape(n, self.m.H, self.m.D), want, BF16 * want.abs() + (prec + EVAL) * size + 1e-30)
+
+    def prefill(self, new, **how):
+        x = self.hidden(sum(new))
+        pos = torch.cat([torch.arange(t, t + k) for t, k in zip(self.cache.tokens, new)]).to(torch.int32).cuda()
+        self.cache.reserve(new)
+        out = torch.empty_like(x)
+        self.m.prefill(x, new, pos, self.cache, 0, self.b, out, **how)
+        self.hold(new)
+        self.cache.advance(new)
+        return out
+
+
+@pytest.mark.parametrize("dims", [synth.TINY_ATTENTION, dict(synth.ATTENTION_4096, hidden=512)])
+def test_chunk_after_a_captured_loop(dims):
+    t = Talk(dims, 2)
+    t.prefill([60, 5])
+    t.check([60, 5], BF16, own=(0, 1))
+    steps = 9  # over the first page's end
+    t.cache.reserve([steps + 1] * 2)
+    x = torch.zeros(2, t.m.hidden, dtype=torch.bfloat16, device="cuda")
+    out, n = torch.empty_like(x), torch.empty_like(t.cache.pos)
+
+    def step():
+        torch.add(t.cache.pos, 1, out=n)
+        t.m.decode(x, t.cache, 0, t.b, n, out)
+        t.cache.pos.add_(1)
+    x.copy_(t.hidden(2))
+    step()  # the first launches load the kernels
+    t.hold([1, 1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(steps):
+        x.copy_(t.hidden(2))
+        graph.replay()
+        t.hold([1, 1])
+        t.check([1, 1], F16)
+    t.cache.advance([steps + 1] * 2, on_device=False)
+    assert t.cache.pos.tolist() == t.cache.tokens == [70, 15]
+    for new in ([70, 40], [1, 90]):
+        t.prefill(new)
+        t.check(new, BF16)
+    assert t.cache.pos.tolist() == t.cache.tokens == [141, 145]
