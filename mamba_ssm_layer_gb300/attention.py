@@ -44,17 +44,23 @@ class Kv4Cache:
         self.struct = [abi.kv4_cache(p, n_pages, n_kv_heads, head_dim, self.table, nseq, self.max_pages)
                        for p in self.pages]
 
+    def _counts(self, fn: str, new) -> None:
+        if len(new) != self.nseq or min(new) < 0:
+            raise abi.M2Error(fn, abi.M2_ERR_ARG)
+
     def reserve(self, new) -> None:
-        """Pages for new[i] more tokens of each sequence."""
+        """Pages for new[i] more tokens of each sequence; all of them or, with an error, none."""
+        self._counts("Kv4Cache.reserve", new)
         need = [-(-(t + n) // PAGE) - len(o) for t, n, o in zip(self.tokens, new, self._owned)]
         if sum(max(0, n) for n in need) > len(self._free):
             raise RuntimeError("Kv4Cache: out of pages")
+        for i, (n, o) in enumerate(zip(need, self._owned)):
+            if len(o) + n > self.max_pages:
+                raise RuntimeError(f"Kv4Cache: sequence {i} would pass max_tokens")
         for i, n in enumerate(need):
             if n <= 0:
                 continue
             have = len(self._owned[i])
-            if have + n > self.max_pages:
-                raise RuntimeError(f"Kv4Cache: sequence {i} would pass max_tokens")
             got = [self._free.pop() for _ in range(n)]
             self._owned[i] += got
             self.table[i, have:have + n].copy_(torch.tensor(got, dtype=torch.int32))
@@ -62,6 +68,7 @@ class Kv4Cache:
     def advance(self, new, on_device: bool = True) -> None:
         """Counts new[i] appended tokens of each sequence.  on_device False: on the host only, where ``pos`` has
         counted them already (a captured loop)."""
+        self._counts("Kv4Cache.advance", new)
         if on_device:
             self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
         self.tokens = [t + n for t, n in zip(self.tokens, new)]
@@ -131,8 +138,7 @@ class DeviceAttention:
     def prefill(self, x, new, row_pos, cache: Kv4Cache, layer: int, b: dict, out, stream=None) -> None:
         """x, out [sum(new)][hidden] bf16: new[i] tokens of each sequence, after those that the cache holds.
         row_pos: device int32, each row's position.  Appends to the cache (reserved before); the caller advances."""
-        if len(new) != cache.nseq or min(new) < 0:
-            raise abi.M2Error("DeviceAttention.prefill", abi.M2_ERR_ARG)
+        cache._counts("DeviceAttention.prefill", new)
         cu, all_ = [0], [0]
         for n, t in zip(new, cache.tokens):
             cu.append(cu[-1] + n)

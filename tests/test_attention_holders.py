@@ -129,3 +129,18 @@ def test_cache_counts_what_a_captured_loop_advanced():
     assert (c.table >= 0).sum(1).tolist() == [4, 3]  # 204 and 174 tokens
     c.advance([64, 64])
     assert c.pos.tolist() == c.tokens == [204, 174]
+
+
+@pytest.mark.parametrize("new,error", [([100, 193], RuntimeError), ([193, 10], RuntimeError), ([10], abi.M2Error),
+                                       ([10, 10, 10], abi.M2Error), ([10, -1], abi.M2Error),
+                                       ([190, 190], RuntimeError)])
+def test_a_refused_reserve_hands_out_nothing(new, error):
+    c = Kv4Cache(1, 2, 5, 192, 2, 64, device="cpu")
+    c.reserve([5, 0])
+    table = c.table.clone()
+    with pytest.raises(error):
+        c.reserve(new)
+    assert torch.equal(c.table, table) and len(c._free) == 4
+    with pytest.raises(abi.M2Error):
+        c.advance([1])
+    assert c.pos.tolist() == c.tokens == [0, 0]
