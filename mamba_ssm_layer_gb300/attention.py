@@ -7,12 +7,21 @@ over the cache.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import abi
 from .layer import _empty, _zeros, to_dev
 
 PAGE = abi.M2_KV4_PAGE
+
+
+def _on(stream):
+    """Torch's own work under the stream of the layers' calls (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class Kv4Cache:
@@ -24,7 +33,9 @@ class Kv4Cache:
     ``advance`` counts the new tokens.  A captured decode loop reserves ahead and
     advances with ``pos.add_(1)`` inside the capture; the host's count follows after
     the replays, before the next ``reserve`` or prompt, with
-    ``advance(steps, on_device=False)``.
+    ``advance(steps, on_device=False)``.  These calls write the table and the counts
+    that the layers' kernels read: they take the same ``stream`` (None: the current
+    one), which orders them.
     """
 
     def __init__(self, n_layers: int, nseq: int, n_pages: int, max_tokens: int, n_kv_heads: int, head_dim: int,
@@ -48,7 +59,7 @@ class Kv4Cache:
         if len(new) != self.nseq or min(new) < 0:
             raise abi.M2Error(fn, abi.M2_ERR_ARG)
 
-    def reserve(self, new) -> None:
+    def reserve(self, new, stream=None) -> None:
         """Pages for new[i] more tokens of each sequence; all of them or, with an error, none."""
         self._counts("Kv4Cache.reserve", new)
         need = [-(-(t + n) // PAGE) - len(o) for t, n, o in zip(self.tokens, new, self._owned)]
@@ -63,23 +74,26 @@ class Kv4Cache:
             have = len(self._owned[i])
             got = [self._free.pop() for _ in range(n)]
             self._owned[i] += got
-            self.table[i, have:have + n].copy_(torch.tensor(got, dtype=torch.int32))
+            with _on(stream):
+                self.table[i, have:have + n].copy_(torch.tensor(got, dtype=torch.int32))
 
-    def advance(self, new, on_device: bool = True) -> None:
+    def advance(self, new, on_device: bool = True, stream=None) -> None:
         """Counts new[i] appended tokens of each sequence.  on_device False: on the host only, where ``pos`` has
         counted them already (a captured loop)."""
         self._counts("Kv4Cache.advance", new)
         if on_device:
-            self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
+            with _on(stream):
+                self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
         self.tokens = [t + n for t, n in zip(self.tokens, new)]
 
-    def release(self, seq: int) -> None:
+    def release(self, seq: int, stream=None) -> None:
         """Gives a finished sequence's pages back."""
         self._free += reversed(self._owned[seq])
         self._owned[seq] = []
         self.tokens[seq] = 0
-        self.pos[seq] = 0
-        self.table[seq].fill_(-1)
+        with _on(stream):
+            self.pos[seq] = 0
+            self.table[seq].fill_(-1)
 
 
 class DeviceAttention:

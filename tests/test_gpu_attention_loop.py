@@ -104,3 +104,37 @@ def test_chunk_after_a_captured_loop(dims):
         t.prefill(new)
         t.check(new, BF16)
     assert t.cache.pos.tolist() == t.cache.tokens == [141, 145]
+
+
+def test_cache_changes_are_ordered_with_the_calls_on_their_stream():
+    """Appends and counts queued behind a long kernel on a side stream: each append sees the count that the calls
+    before it left, and a slot is released only after its last call."""
+    K, D = 2, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(50, K * D, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    c = Kv4Cache(1, 1, 2, 64, K, D)
+    out = [torch.zeros(50, K * D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    s = torch.cuda.Stream()
+    # the first launches load the kernels, which may wait for everything
+    c.reserve([1])
+    abi.m2_kv4_append(c.struct[0], k, K * D, v, K * D, [0, 1], c.pos)
+    c.advance([1])
+    abi.m2_kv4_gather(c.struct[0], out[0], K * D, out[1], K * D, [0, 1])
+    c.release(0)
+    torch.cuda._sleep(1)
+    c.reserve([50])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    for rows, n in ((slice(0, 30), 30), (slice(30, 50), 20)):
+        abi.m2_kv4_append(c.struct[0], k[rows], K * D, v[rows], K * D, [0, n], c.pos, s)
+        c.advance([n], stream=s)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    abi.m2_kv4_gather(c.struct[0], out[0], K * D, out[1], K * D, [0, 50], s)
+    c.release(0, stream=s)
+    c.reserve([1], stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for got, x in zip(out, (k, v)):
+        assert torch.equal(got.to(ref.F).view(50, K, D), ref.rounded_rows(x.view(50, K, D)))
+    assert c.pos.tolist() == [0] and int((c.table >= 0).sum()) == 1
