@@ -48,7 +48,7 @@ class HybridStack:
                                .astype(np.int32)).cuda()
         self.first.prefill_varlen(x, cu, self.states[0], self.ws)
         out = self.mixed[:x.shape[0]]
-        self.mixer.prefill(self.norm(x), new, pos, self.cache, 0, self.b, out)
+        self.mixer.prefill(self.norm(x), new, pos, self.cache, 0, self.b, out, first_over_cache=False)
         x.view(torch.bfloat16).add_(out)
         self.last.prefill_varlen(x, cu, self.states[1], self.ws)
         self.cache.advance(new)

@@ -149,25 +149,42 @@ class DeviceAttention:
     def _output(self, b, out, stream):
         abi.w8a16_gemv(b["attn"], self.t["o_w"], self.t["o_s"], out, out.shape[0], self.hidden, self.H * self.D, stream)
 
-    def prefill(self, x, new, row_pos, cache: Kv4Cache, layer: int, b: dict, out, stream=None) -> None:
+    def prefill(self, x, new, row_pos, cache: Kv4Cache, layer: int, b: dict, out, stream=None,
+                first_over_cache: bool | None = None) -> None:
         """x, out [sum(new)][hidden] bf16: new[i] tokens of each sequence, after those that the cache holds.
-        row_pos: device int32, each row's position.  Appends to the cache (reserved before); the caller advances."""
+        row_pos: device int32, each row's position.  Appends to the cache (reserved before); the caller advances.
+
+        A sequence that the cache holds tokens of attends to the cache's rows, as the single tokens after this will.
+        first_over_cache says what the others attend to: True, to the cache's 4-bit rows too; False, to their own
+        bf16 rows (one call for each run of sequences of a kind).  Either way a sequence's result does not depend on
+        the rest of the batch.  None, in one call: their own rows if the cache holds no token of any sequence, else
+        the cache's, so that a first prompt's result then differs by the 4-bit rounding of its keys and values."""
         cache._counts("DeviceAttention.prefill", new)
-        cu, all_ = [0], [0]
+        if first_over_cache is None:
+            first_over_cache = any(cache.tokens)
+        cu, held, runs = [0], [0], []  # row offsets, those of the rows read back; a run: [over the cache, q, k offsets]
         for n, t in zip(new, cache.tokens):
+            over = t > 0 or first_over_cache
+            held.append(held[-1] + (n + t if n and over else 0))
             cu.append(cu[-1] + n)
-            all_.append(all_[-1] + n + t)
-        self._check("DeviceAttention.prefill", cu[-1], x, out, row_pos, cache, b, all_[-1] if all_[-1] > cu[-1] else 0)
+            if n:
+                at = held if over else cu
+                if not runs or runs[-1][0] != over:
+                    runs.append([over, [cu[-2]], [at[-2]]])
+                runs[-1][1].append(cu[-1])
+                runs[-1][2].append(at[-1])
+        self._check("DeviceAttention.prefill", cu[-1], x, out, row_pos, cache, b, held[-1])
         s = stream if stream is not None else torch.cuda.current_stream()
         H, Hkv, D = self.H, self.Hkv, self.D
         q, k, v = self._project(x, b, row_pos, s)
         abi.m2_kv4_append(cache.struct[layer], k, Hkv * D, v, self.n_qkv, cu, cache.pos, s)
-        ld_k, ld_v = Hkv * D, self.n_qkv
-        if all_[-1] > cu[-1]:
-            # earlier tokens: attend to the cache's rows, as the single tokens after this will
-            k, v, ld_k, ld_v = b["keys"], b["keys"][:, Hkv * D:], 2 * Hkv * D, 2 * Hkv * D
-            abi.m2_kv4_gather(cache.struct[layer], k, ld_k, v, ld_v, all_, s)
-        abi.m2_attn_prefill_varlen(q, H * D, k, ld_k, v, ld_v, b["attn"], H * D, H, Hkv, D, cu, all_, self.scale, s)
+        fresh, read = (k, Hkv * D, v, self.n_qkv), (b["keys"], 2 * Hkv * D, b["keys"][:, Hkv * D:], 2 * Hkv * D)
+        if held[-1]:
+            abi.m2_kv4_gather(cache.struct[layer], *read, held, s)
+        for over, cq, ck in runs:
+            rk, ld_k, rv, ld_v = read if over else fresh
+            abi.m2_attn_prefill_varlen(q[cq[0]:], H * D, rk[ck[0]:], ld_k, rv[ck[0]:], ld_v, b["attn"][cq[0]:], H * D,
+                                       H, Hkv, D, [c - cq[0] for c in cq], [c - ck[0] for c in ck], self.scale, s)
         self._output(b, out, s)
 
     def decode(self, x, cache: Kv4Cache, layer: int, b: dict, kv_len, out, stream=None) -> None:

@@ -144,3 +144,45 @@ def test_a_refused_reserve_hands_out_nothing(new, error):
     with pytest.raises(abi.M2Error):
         c.advance([1])
     assert c.pos.tolist() == c.tokens == [0, 0]
+
+
+@pytest.mark.parametrize("new,held,runs", [
+    # runs: (first row, first key row, sequences, over the cache) of each call to attention
+    ([3, 4], [0, 0], [(0, 0, 2, False)]),
+    ([3, 4], [5, 6], [(0, 0, 2, True)]),
+    ([3, 4], [0, 6], [(0, 0, 1, False), (3, 0, 1, True)]),
+    ([3, 4, 2, 1], [5, 0, 0, 9], [(0, 0, 1, True), (3, 3, 2, False), (9, 8, 1, True)]),
+    # sequences without new rows take part in neither
+    ([0, 4, 0, 2], [50, 0, 7, 9], [(0, 0, 1, False), (4, 0, 1, True)]),
+    ([0, 0], [4, 0], [])])
+def test_a_first_prompt_attends_to_its_own_rows_whatever_the_batch(mixer, calls, new, held, runs):
+    n = len(new)
+    cache, b = cache_of(mixer, n), mixer.buffers(12, 24, n)
+    cache.tokens[:] = held
+    a = dict(x=torch.zeros(sum(new), mixer.hidden, dtype=bf), row_pos=torch.zeros(sum(new), dtype=torch.int32),
+             out=torch.zeros(sum(new), mixer.hidden, dtype=bf))
+    mixer.prefill(a["x"], new, a["row_pos"], cache, 0, b, a["out"], Stream(), first_over_cache=False)
+    got = [x for name, x in calls if name == "m2_attn_prefill_varlen"]
+    assert len(got) == len(runs)
+    row = lambda t, base: (t.data_ptr() - base.data_ptr()) // (base.stride(0) * 2)  # noqa: E731
+    for (q, _, k, ld_k, v, ld_v, out, _, *_, cu_q, cu_k, _, _), (q0, k0, count, over) in zip(got, runs):
+        assert row(q, b["q"]) == row(out, b["attn"]) == q0 and len(cu_q) == count + 1
+        assert row(k, b["keys"] if over else b["k"]) == k0
+        assert row(v, b["keys"] if over else b["qkv"]) == k0
+        assert (ld_k, ld_v) == ((2 * mixer.Hkv * mixer.D,) * 2 if over else (mixer.Hkv * mixer.D, mixer.n_qkv))
+    gathers = [x for name, x in calls if name == "m2_kv4_gather"]
+    want = [0]
+    for m, t in zip(new, held):
+        want.append(want[-1] + (m + t if m and t else 0))
+    assert [list(x[5]) for x in gathers] == ([want] if want[-1] else [])
+
+
+@pytest.mark.parametrize("held", [[0, 0], [0, 6], [3, 6]])
+def test_every_prompt_over_the_cache(mixer, calls, held):
+    cache, b = cache_of(mixer), mixer.buffers(12, 24, 2)
+    cache.tokens[:] = held
+    a = [torch.zeros(7, mixer.hidden, dtype=bf) for _ in range(2)]
+    mixer.prefill(a[0], [3, 4], torch.zeros(7, dtype=torch.int32), cache, 0, b, a[1], Stream(), first_over_cache=True)
+    names = [name for name, _ in calls]
+    assert names.count("m2_attn_prefill_varlen") == names.count("m2_kv4_gather") == 1
+    assert dict(calls)["m2_attn_prefill_varlen"][2].data_ptr() == b["keys"].data_ptr()

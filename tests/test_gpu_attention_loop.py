@@ -138,3 +138,18 @@ def test_cache_changes_are_ordered_with_the_calls_on_their_stream():
     for got, x in zip(out, (k, v)):
         assert torch.equal(got.to(ref.F).view(50, K, D), ref.rounded_rows(x.view(50, K, D)))
     assert c.pos.tolist() == [0] and int((c.table >= 0).sum()) == 1
+
+
+@pytest.mark.parametrize("dims", [synth.TINY_ATTENTION, dict(synth.ATTENTION_4096, hidden=512)])
+@pytest.mark.parametrize("over", [False, True])
+def test_a_first_prompt_is_the_same_alone_and_beside_a_conversation(dims, over):
+    t = Talk(dims, 4)
+    t.prefill([40, 0, 0, 17], first_over_cache=over)
+    t.check([40, 0, 0, 17], BF16, own=() if over else (0, 3))
+    new = [5, 90, 64, 3]
+    out = t.prefill(new, first_over_cache=over)
+    t.check(new, BF16, own=() if over else (1, 2))
+    alone = Talk(dims, 2)
+    x = synth.make_hidden(sum(new), t.m.hidden, 9, t.call)[5:159]  # the rows of sequences 1 and 2
+    alone.hidden = lambda T: to_dev(x).view(torch.bfloat16)
+    assert torch.equal(alone.prefill([90, 64], first_over_cache=over), out[5:159])
