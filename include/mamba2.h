@@ -361,6 +361,7 @@ int m2_rope_steps(double theta, int32_t rot_dim, uint64_t* steps);
  * are held (larger ones and infinities saturate), groups below about 2^-16
  * become zero, and a NaN makes its group NaN.  4.5 bits a value. */
 #define M2_KV4_PAGE 64
+#define M2_KV4_IDLE INT32_MIN /* kv_pos of a slot without a sequence (m2_kv4_append) */
 typedef struct m2_kv4_cache {
   void* pages;                 /* [n_pages][n_kv_heads][72 * head_dim] bytes, 16-byte aligned        */
   int32_t n_pages;
@@ -376,10 +377,13 @@ size_t m2_kv4_page_bytes(int32_t n_kv_heads, int32_t head_dim);
  * sequence i.
  *   cu_rows  HOST array of nseq + 1 offsets, cu_rows[0] = 0, non-decreasing.
  *   kv_pos   device [nseq] int32: tokens each sequence holds before the call.
- *            Not advanced: every layer of a stack can share one array.
+ *            Not advanced: every layer of a stack can share one array.  Below
+ *            -2^30 (M2_KV4_IDLE, and what a captured loop that counts every slot
+ *            makes of it) the slot takes no part: its rows are not stored, and
+ *            nothing is reported.
  * Rows of a sequence must be appended in order; a page belongs to one
  * sequence.  A row whose page index lies outside [0, n_pages), or whose
- * position is negative or past the block table, is not stored, and
+ * position is negative (but not idle) or past the block table, is not stored, and
  * m2_device_status reports M2_ERR_ARG. */
 int m2_kv4_append(const m2_kv4_cache* cache, const uint16_t* k, int32_t ld_k, const uint16_t* v, int32_t ld_v,
                   const int32_t* cu_rows, const int32_t* kv_pos, cudaStream_t stream);
@@ -408,7 +412,7 @@ int m2_attn_prefill_varlen(const uint16_t* q, int32_t ld_q, const uint16_t* k, i
 /* Attention of one query token a sequence over the cache: q and out
  * [cache->nseq][H*head_dim] bf16.
  *   kv_len  device [nseq] int32: tokens each sequence sees (its own, appended
- *           before the call, included).  A length of 0 gives a row of zeros;
+ *           before the call, included).  A length of 0 or less gives a row of zeros;
  *           one past the block table is cut to it and reported by
  *           m2_device_status as M2_ERR_ARG, as is a page outside the pool,
  *           whose tokens are left out.

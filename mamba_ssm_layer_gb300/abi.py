@@ -288,6 +288,7 @@ def m2_copy(dst, src, nbytes: int, stream=None, check=True) -> int:
 # ------------------------------------------------------------------ attention of hybrid stacks
 
 M2_KV4_PAGE = 64
+M2_KV4_IDLE = -2 ** 31  # kv_pos of a slot without a sequence
 
 
 def _offsets(fn: str, cu, nseq: int):

@@ -51,6 +51,7 @@ class Kv4Cache:
         self.pos = _zeros((nseq,), torch.int32, device)  # tokens held, for the kernels
         self.tokens = [0] * nseq                         # the same, on the host
         self._owned = [[] for _ in range(nseq)]
+        self._idle = set()
         self._free = list(range(n_pages - 1, -1, -1))
         self.struct = [abi.kv4_cache(p, n_pages, n_kv_heads, head_dim, self.table, nseq, self.max_pages)
                        for p in self.pages]
@@ -71,6 +72,10 @@ class Kv4Cache:
         for i, n in enumerate(need):
             if n <= 0:
                 continue
+            if i in self._idle:
+                self._idle.remove(i)
+                with _on(stream):
+                    self.pos[i] = 0
             have = len(self._owned[i])
             got = [self._free.pop() for _ in range(n)]
             self._owned[i] += got
@@ -86,13 +91,16 @@ class Kv4Cache:
                 self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
         self.tokens = [t + n for t, n in zip(self.tokens, new)]
 
-    def release(self, seq: int, stream=None) -> None:
-        """Gives a finished sequence's pages back."""
+    def release(self, seq: int, stream=None, idle: bool = False) -> None:
+        """Gives a finished sequence's pages back.  idle: the slot may stay in decode steps without a sequence (its
+        rows are not stored, its output is zeros) until pages are reserved for it; without it such a step reports
+        M2_ERR_ARG."""
         self._free += reversed(self._owned[seq])
         self._owned[seq] = []
         self.tokens[seq] = 0
+        (self._idle.add if idle else self._idle.discard)(seq)
         with _on(stream):
-            self.pos[seq] = 0
+            self.pos[seq] = abi.M2_KV4_IDLE if idle else 0
             self.table[seq].fill_(-1)
 
 

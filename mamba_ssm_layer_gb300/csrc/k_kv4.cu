@@ -217,7 +217,7 @@ __device__ __forceinline__ RowTask row_task(const Kv4RowsArgs& a, int64_t tasks)
   t.end = t.first + a.cu[lo + 1] - a.cu[lo];
   const int64_t blk = (t.first >> 3) + (p - block_base(a, lo));  // from the block of `first` (also below zero) on
   t.tok = 8 * blk;
-  if (t.tok >= t.end || t.end == t.first) return t;
+  if (t.tok >= t.end || t.end == t.first || t.first < -(1 << 30)) return t;  // (the last: an idle slot)
   t.any = true;
   const int64_t pg = blk >= 0 ? blk / (kPage / 8) : a.c.ld_table;
   t.page = pg < a.c.ld_table ? a.c.table[(size_t)lo * a.c.ld_table + pg] : -1;

@@ -186,3 +186,18 @@ def test_every_prompt_over_the_cache(mixer, calls, held):
     names = [name for name, _ in calls]
     assert names.count("m2_attn_prefill_varlen") == names.count("m2_kv4_gather") == 1
     assert dict(calls)["m2_attn_prefill_varlen"][2].data_ptr() == b["keys"].data_ptr()
+
+
+def test_cache_slot_without_a_sequence():
+    c = Kv4Cache(1, 3, 9, 192, 2, 64, device="cpu")
+    c.reserve([10, 70, 5])
+    c.advance([10, 70, 5])
+    c.release(1, idle=True)
+    assert c.pos.tolist() == [10, abi.M2_KV4_IDLE, 5] and c.tokens == [10, 0, 5]
+    c.pos.add_(1)  # a captured loop counts every slot
+    c.advance([1, 0, 1], on_device=False)
+    c.reserve([1, 0, 1])
+    assert c.pos.tolist() == [11, abi.M2_KV4_IDLE + 1, 6]
+    c.reserve([0, 100, 0])  # the slot's next sequence
+    c.advance([0, 100, 0])
+    assert c.pos.tolist() == c.tokens == [11, 100, 6]

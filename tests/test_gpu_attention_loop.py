@@ -153,3 +153,38 @@ def test_a_first_prompt_is_the_same_alone_and_beside_a_conversation(dims, over):
     x = synth.make_hidden(sum(new), t.m.hidden, 9, t.call)[5:159]  # the rows of sequences 1 and 2
     alone.hidden = lambda T: to_dev(x).view(torch.bfloat16)
     assert torch.equal(alone.prefill([90, 64], first_over_cache=over), out[5:159])
+
+
+def test_slots_without_a_sequence_report_nothing():
+    t = Talk(synth.TINY_ATTENTION, 3)
+    t.prefill([60, 5, 20], first_over_cache=False)
+    t.cache.release(1, idle=True)
+    t.cache.reserve([6, 0, 6])
+    pages = t.cache.pages[0].clone()
+    for _ in range(6):
+        x = t.hidden(3)
+        out = torch.empty_like(x)
+        t.m.decode(x, t.cache, 0, t.b, t.cache.pos + 1, out)
+        q, k, v = t.rows(3)
+        for i in (0, 2):
+            t.held[0][i].append(ref.rounded_rows(k[i:i + 1]))
+            t.held[1][i].append(ref.rounded_rows(v[i:i + 1]))
+            want, size = ref.attend(q[i:i + 1], *(torch.cat(h[i]) for h in t.held), t.m.scale)
+            close(t.b["attn"][i].reshape(1, t.m.H, t.m.D), want, BF16 * want.abs() + (F16 + EVAL) * size + 1e-30)
+        assert bool((t.b["attn"][1] == 0).all())
+        t.cache.pos.add_(1)  # every slot, as a captured loop does
+    t.cache.advance([6, 0, 6], on_device=False)
+    assert abi.m2_device_status() == abi.M2_OK
+    owned = torch.zeros(len(pages), dtype=torch.bool, device="cuda")
+    owned[t.cache.table[t.cache.table >= 0].long()] = True
+    assert torch.equal(t.cache.pages[0][~owned], pages[~owned])
+    t.held[0][1], t.held[1][1] = [], []
+    t.prefill([3, 80, 0], first_over_cache=False)  # the slot's next sequence
+    t.check([3, 80, 0], BF16, own=(1,))
+    assert t.cache.pos.tolist() == t.cache.tokens == [69, 80, 26]
+    # a slot that was not marked still reports
+    t.cache.release(2)
+    x = t.hidden(3)
+    t.cache.reserve([1, 1, 0])
+    t.m.decode(x, t.cache, 0, t.b, t.cache.pos + 1, torch.empty_like(x))
+    assert abi.m2_device_status(clear=True) == abi.M2_ERR_ARG
