@@ -987,7 +987,7 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
     longest = n > longest ? n : longest;
   }
   const bool test = limit < 1000000;
-  a.split = test ? 1 : at_split(a.items, longest);
+  a.split = at_split(a.items, longest);
   if (a.sorted) {  // counting sort by key blocks (longer than the last bucket: any order)
     constexpr int kBuckets = 256;
     uint16_t first[kBuckets + 1] = {0}, len[kAtSorted];
@@ -1003,7 +1003,8 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
     for (int b = 0; b < kBuckets; ++b) first[b + 1] += first[b];
     for (int t = 0; t < a.tile[g.nseq]; ++t) a.order[first[len[t]]++] = (uint16_t)t;
   }
-  if (test) return launch_attn_kernel<D, true, false>(a, q, k, v, s);
+  if (test)
+    return a.split > 1 ? launch_attn_kernel<D, true, true>(a, q, k, v, s) : launch_attn_kernel<D, true, false>(a, q, k, v, s);
   return a.split > 1 ? launch_attn_kernel<D, false, true>(a, q, k, v, s) : launch_attn_kernel<D, false, false>(a, q, k, v, s);
 }
 
