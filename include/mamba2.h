@@ -398,7 +398,8 @@ int m2_kv4_gather(const m2_kv4_cache* cache, uint16_t* k, int32_t ld_k, uint16_t
  * .. cu_q[i+1]-1 and key/value rows cu_k[i] .. cu_k[i+1]-1; its queries are the
  * LAST tokens of its keys: with nq queries and nk keys, query j sees keys 0 ..
  * j + nk - nq (the whole prompt when nq = nk, a chunk after cached tokens when
- * nq < nk).  A query that sees no key (nq > nk) gives a row of zeros.
+ * nq < nk).  A query that sees no key (nq > nk) gives a row of zeros, as does one
+ * whose scores are all -Inf (an infinite query or key: its softmax is 0 / 0).
  *   out[j] = sum_t softmax_t(scale * q[j] . k[t]) v[t]
  * per head; scores and sums in fp32, probabilities rounded to bf16 for the
  * second product.  Keys and values that a query does not see do not reach it,
@@ -412,7 +413,8 @@ int m2_attn_prefill_varlen(const uint16_t* q, int32_t ld_q, const uint16_t* k, i
 /* Attention of one query token a sequence over the cache: q and out
  * [cache->nseq][H*head_dim] bf16.
  *   kv_len  device [nseq] int32: tokens each sequence sees (its own, appended
- *           before the call, included).  A length of 0 or less gives a row of zeros;
+ *           before the call, included).  A length of 0 or less gives a row of zeros
+ *           (as do scores that are all -Inf, see above);
  *           one past the block table is cut to it and reported by
  *           m2_device_status as M2_ERR_ARG, as is a page outside the pool,
  *           whose tokens are left out.

@@ -10,25 +10,30 @@
 //   O += P V    (P read from tensor memory, V as an MN-major operand)
 // m is the row's reference maximum.  It follows the running maximum only when
 // that has grown by more than 2^8 in the exponential: until then P stays below
-// 2^8, which bf16 and fp32 hold as well, and O needs no rescaling.
+// 2^8, which bf16 and fp32 hold as well, and O needs no rescaling.  (This and two
+// query tiles a CTA are known from the literature.)
+// P takes V's type, since both operands of a product have one: a probability is off
+// by at most 2^-8 of itself, the sum l is taken before that rounding.  It shows: rms
+// error against 64 bits 0.0019 to 0.0023 of the output on the measured prompts, 0.0015
+// to 0.0017 with fp32 probabilities, most of which is the output's own rounding.
 // Few items over many keys are cut along the keys (SPLIT): a cluster takes an item,
 // each of its CTAs a run of the blocks, and they join their maxima, sums and outputs
 // through each other's shared memory.
 // Otherwise CTAs are persistent: the copies and the first scores of a CTA's next item (a
 // tile pair of one head group) run under the last softmax and the output of the
 // current one.
-// Bound: the tensor cores (4 * 128 * 128 * D operations a tile pair) and the
-// exponentials (one a score); while one tile's scores are in the softmax
+// Bound: the tensor cores (8 * 128 * 128 * D operations a tile pair and key block)
+// and the exponentials (one a score); while one tile's scores are in the softmax
 // warps, the other tile's products run.
-// Measured at 32 + 8 heads: one prompt of 8192 tokens, D = 128, 330 us (1.7
-// PFLOP/s; a step of both tiles is 2800 cycles for 2048 of products: 1800 of
-// softmax, 950 of them exponentials, which a warp alone on its quarter of the SM
-// issues at half the rate of two, then the products that the next scores wait
-// for); four chunks of 200..1000 tokens over up to 6000, D = 64, 107 us (0.8
-// PFLOP/s); 16 prompts of 64..512 tokens 32 us, of which an item's first block
-// and output take as long as its products.  Two threads a row (16 softmax warps of
-// 104 registers) took 418 us where one took 371: what a warp does once a block
-// (waits, votes, the exchange of maxima) counts twice.
+// Measured at 32 + 8 heads, as graph replays: one prompt of 8192 tokens, D = 128, 312
+// to 356 us by run (1.76 to 1.54 PFLOP/s; the power limit sets the clock; a step of
+// both tiles is 2800 cycles for 2048 of products: 1800 of softmax, 950 of them
+// exponentials, which a warp alone on its quarter of the SM issues at half the rate of
+// two, then the products that the next scores wait for); four chunks of 200..1000
+// tokens over up to 6000, D = 64, 107 us (0.8 PFLOP/s); 16 prompts of 64..512 tokens
+// 32 us, of which an item's first block and output take as long as its products.  Two
+// threads a row (16 softmax warps of 104 registers) took 418 us where one took 371:
+// what a warp does once a block (waits, votes, the exchange of maxima) counts twice.
 //
 // Roles: warps 0-3 softmax and output of tile 0, warps 4-7 of tile 1, warp 8
 // issues the products, warp 9 the TMA copies, warps 10 and 11 look through the
@@ -53,10 +58,13 @@ constexpr int kAtThreads = 384;
 constexpr int kAtRegsSoftmax = 216, kAtRegsOther = 72;
 constexpr int kAtRows = 128;      // query rows of a tile, keys of a block
 // Up to so many tile pairs are handed out longest first; with more of them, later
-// ones first (a sequence's longest) spreads the work as well.  Measured by the
+// ones first (a sequence's longest) spreads the work as well.  Few pairs, by the
 // blocks of the busiest CTA against the mean: four chunks over up to 6000 tokens
 // (33 pairs x 8 groups) 95 to 79 sorted, 113 to 79 unsorted; one prompt of 8192
-// (128 pairs) 237 to 232 both ways.
+// (128 pairs) 237 to 232 both ways.  Many, sorted and unsorted, us: one prompt of
+// 40000 (625 pairs) 7680 and 7670, 128 of 64..512 (666) 188 and 187, 128 of 1..1000
+// (1101) 395 and 391, 100 chunks of 200..700 over up to 8000 (751) 1540 and 1540, 128
+// of 30, 60 or 3000 (2014) 2200 and 1980.
 constexpr int kAtSorted = 512;
 constexpr int kAtItems = 4;       // items handed on ahead of their use
 // Items whose marks of values are kept apart.  A softmax warp reads item i's marks
@@ -76,7 +84,7 @@ struct AtCfg {
   // Tensor-memory columns: S 2 x 128 (P over it), O 2 x D.  (With D = 64 there is
   // room for P of its own, so that the next scores run under the softmax; scores are
   // then read while products run, which takes twice as long, and four chunks over
-  // cached tokens took 123 us instead of 115.)
+  // cached tokens took 119 us instead of 107.)
   static constexpr uint32_t kTmS = 0, kTmO = 256;
 };
 // What a CTA works on: the copies' thread works it out and hands it on through
@@ -890,7 +898,8 @@ static std::atomic<long long> g_limit[64];
 // CTAs of an item: a cut costs a join of about 4 key blocks, and its cluster's CTAs
 // have to find room together (in 4 of 5 SMs).  Measured at 32 heads on 8 of 128, one
 // sequence, cut and uncut: 16 tokens on 500 keys 10.3 and 8.0 us, 700 10.4 and 10.1,
-// 1000 11.3 and 12.4, 4000 15 and 38; 64 tokens on 60000 keys 87 and 581.
+// 1000 11.3 and 12.4, 4000 15 and 38; 64 tokens on 60000 keys 87 and 581.  (The cut
+// kernel spills 124 bytes of stores and 56 of loads a thread, the others none.)
 static int at_split(int items, int64_t blocks) {
   int best = 1;
   int64_t cost = blocks;

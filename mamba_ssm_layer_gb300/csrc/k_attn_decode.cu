@@ -10,15 +10,19 @@
 //   S^T [64 tokens x HN] = K Q^T    K codes become f16 and take their scale,
 //                                   exactly (6 significant bits)
 //   O^T [D x HN] += V^T P^T         likewise V; P rounded to f16 (2^-11)
-// Queries enter as f16 rows prescaled by an exact power of two.  Scores, sums and
-// outputs are fp32.  Rows that a warp, then a CTA, holds only in part are
+// Queries enter as f16 rows prescaled by an exact power of two (exact but for
+// channels more than 2^17 below the head's largest).  f16 is what the codes convert to;
+// the rms error against 64 bits is 0.00169 of the output, with fp32 queries and
+// probabilities 0.00168.  Scores, sums and outputs are fp32.  Rows that a warp, then a CTA, holds only in part are
 // joined: warps through shared memory, CTAs by attn_decode_combine.
-// Bound: HBM (4.5 bits a value) and, as close, the issue rate: a unit is about
-// 1060 instructions of a warp with all around it (256 conversions of two codes, 256
-// multiplications by scales, 64 MMAs at HN = 8), 80% of the issue slots while a span
-// is streamed.  Measured at 32 + 8 heads of 128: 131000 tokens of one sequence 35.5 us
-// (4.2 TB/s), 64 sequences of 64..4096 tokens 41 us (4.1 TB/s); 6 to 7 us of that are
-// the way to the first data, 4 to 5 the joining.  8 warps with 3 stages took 48 us
+// Bound: HBM (4.5 bits a value) once data streams, and the start and the joining of
+// rows cut between CTAs.  Measured at 32 + 8 heads of 128, as graph replays: 131000
+// tokens of one sequence 35.5 us (4.2 TB/s), 64 sequences of 64..4096 tokens 41 us (4.1
+// TB/s); 6 to 7 us of that are the way to the first data, 4 to 5 the joining, and what
+// is between runs at 5.6 to 6 TB/s.  A unit is about 1060 instructions of a warp with
+// all around it (256 conversions of two codes, 256 multiplications by scales, 64 MMAs
+// at HN = 8): 47% of the issue slots over the whole launch.  168 registers a
+// thread at D = 128, which spills 24 bytes of stores at HN = 8 and 348 at HN = 16.  8 warps with 3 stages took 48 us
 // instead of 37 in the kernel itself, 12 warps with 128 registers the same.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -746,7 +750,12 @@ static cudaError_t launch_ad(const AttnDecodeArgs& g, cudaStream_t s) {
   a.G = g.H / g.c.Hkv;
   a.chunks = (a.G + 8 * NT - 1) / (8 * NT);
   a.rows = g.c.Hkv * a.chunks;
-  // Few rows of few pages: a CTA takes a whole row, and nothing is left to combine.
+  // Few rows in a narrow table: a CTA takes a whole row, and nothing is left to combine.
+  // The table's width is what the host knows: lengths are read on the device, and a
+  // captured step has to serve while they grow.  Measured, whole rows and spans, us
+  // by tokens: 8 rows of 128 (32 query heads) 64: 5.9 and 8.2, 700: 9.3 and 10.7, 1500: 11.9
+  // and 11.6, 2048 (32 pages): 13.7 and 11.4; 152 rows 700: 10.0 and 12.7, 2048: 17.2 and
+  // 18.5; 16 rows of 64 700: 8.0 and 9.7, 2048: 10.7 and 9.7.
   a.by_row = (int64_t)g.B * a.rows <= num_sms() && g.c.ld_table <= 32;
   a.nc = a.by_row ? g.B * a.rows : num_sms();
   const size_t rec = ad_record<D, 8 * NT>(), n = num_sms();

@@ -181,10 +181,13 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t s) {
 // between the layout's order and that of the rows, so that rows and runs are
 // both read and written 16 bytes a lane.  Sequence i's tasks start at
 // block_base(i): a closed form that leaves room for blocks cut at both ends.
-// Bound: HBM (2 bytes a value of the rows, 0.56 of the cache); with few rows the
-// two launches and the quantizing, 20 instructions a value.  Measured at 8 heads
-// of 128: 16 sequences of 64..512 new tokens written and read back in 15 us, four
-// of 500..2048 after 1000..12000 in 43 us (5.3 TB/s), of it 33 the reading.
+// Bound: HBM (2 bytes a value of the rows, 0.56 of the cache) for the reading.  The
+// writing fills no unit (ALU 59%, issue 55%, DRAM 25% at four chunks): its chain of
+// loads, quantizing (20 instructions a value) and stores is what it waits for, and
+// with few rows both are two launches.  Measured at 8 heads of 128, as graph replays:
+// 16 sequences of 64..512 new tokens written and read back in 15 us (21 a call from
+// Python), four of 500..2048 after 1000..12000 in 43 us (5.3 TB/s), of it 33 the
+// reading; one new token of 1, 16, 64, 256 sequences written in 3.5, 3.8, 4.2, 9.4 us.
 __device__ __forceinline__ int64_t block_base(const Kv4RowsArgs& a, int i) { return a.cu[i] / 8 + 2ll * i; }
 static int64_t block_count(const Kv4RowsArgs& a) { return a.cu[a.nseq] / 8 + 2ll * a.nseq; }
 

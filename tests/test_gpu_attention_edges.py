@@ -145,3 +145,35 @@ def test_operators_run_on_their_stream():
     out, size = ref.attend(q.view(n, H, D), rk, rv, 0.1)
     close(got[0].view(n, H, D), out, 2.0 ** -8 * out.abs() + (2.0 ** -8 + 2.0 ** -15) * size + 1e-30)
     close(got[1].view(1, H, D), out[-1:], 2.0 ** -8 * out[-1:].abs() + (2.0 ** -11 + 2.0 ** -15) * size[-1:] + 1e-30)
+
+
+# ------------------------------------------------------------------ scores that are all -Inf
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_q,n_k", [(300, 300), (40, 3000)])
+def test_rows_whose_scores_are_all_minus_infinity_are_zeros(n_q, n_k, D):
+    H, K = 4, 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v = (torch.randn(r, w * D, device="cuda", generator=g).to(torch.bfloat16)
+               for r, w in ((n_q, H), (n_k, K), (n_k, K)))
+    first = n_k - n_q + 10  # rows 0 .. 9 see only such keys
+    q.view(n_q, H, D)[..., 0] = 1.0
+    k.view(n_k, K, D)[:first, :, 0] = -math.inf
+    out = torch.full((n_q, H * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    abi.m2_attn_prefill_varlen(q, H * D, k, K * D, v, K * D, out, H * D, H, K, D, [0, n_q], [0, n_k], 0.1)
+    assert bool((out[:10] == 0).all())
+    want, size = ref.attend(q[10:].view(-1, H, D), k[first:].view(-1, K, D), v[first:].view(-1, K, D), 0.1)
+    close(out[10:].view(-1, H, D), want, 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -15) * size + 1e-30)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_single_tokens_of_an_infinite_query(D):
+    """Its scores are all -Inf (zeros) or hold a NaN or +Inf (NaN)."""
+    def plant(k, v, cu):
+        k.view(-1, 2, D)[:, 0, 3] = -2.0
+        k.view(-1, 2, D)[:, 1, 3] = torch.where(torch.arange(len(k), device="cuda") % 3 > 0, 1.0, -1.0).to(k.dtype)
+    r = run_decode([500], 4, 2, D, fix=plant)
+    r["q"][0, 3::D] = math.inf
+    r["call"]()
+    out = r["out"].view(4, D)
+    assert bool((out[:2] == 0).all()) and bool(out[2:].isnan().all())
