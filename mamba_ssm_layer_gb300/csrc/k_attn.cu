@@ -748,7 +748,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         break;
       }
       tc_fence_after();
-      if (nt > 0 && bad[kAtMaskBlocks * 4] == item) {  // add the values that were kept out of the products, where they are seen
+      if (nt > 0 && bad[kAtMaskBlocks * 4] == item) {
+        // add the values that were kept out of the products, where they are seen
 #pragma unroll 1
         for (int i = 0; i < D; i += 16) {
           float o[16];
@@ -1013,7 +1014,8 @@ static cudaError_t launch_attn(const AttnArgs& g, int64_t limit, cudaStream_t s)
     for (int t = 0; t < a.tile[g.nseq]; ++t) a.order[first[len[t]]++] = (uint16_t)t;
   }
   if (test)
-    return a.split > 1 ? launch_attn_kernel<D, true, true>(a, q, k, v, s) : launch_attn_kernel<D, true, false>(a, q, k, v, s);
+    return a.split > 1 ? launch_attn_kernel<D, true, true>(a, q, k, v, s)
+                       : launch_attn_kernel<D, true, false>(a, q, k, v, s);
   return a.split > 1 ? launch_attn_kernel<D, false, true>(a, q, k, v, s) : launch_attn_kernel<D, false, false>(a, q, k, v, s);
 }
 
