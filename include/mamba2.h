@@ -428,13 +428,148 @@ size_t m2_attn_decode_kv4_workspace_bytes(int32_t nseq, int32_t H, int32_t Hkv, 
 int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q, uint16_t* out, int32_t ld_o,
                        int32_t H, const int32_t* kv_len, float scale, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* -------------------------------------------------- trees of drafted tokens
+ *
+ * A draft proposes a tree of tokens for every sequence, one pass of the stack runs all
+ * of them without changing any state, the target's probabilities decide which path
+ * holds, and then every layer keeps that path:
+ *   mamba2_layer_tree         a Mamba-2 layer over the trees' rows (its parts:
+ *   mamba2_tree_conv, mamba2_tree_ssm)
+ *   m2_kv4_append             the nodes' key and value rows behind the context: node r of
+ *                             a sequence that holds L tokens is token L + r
+ *   m2_attn_tree_kv4          attention of the nodes over context and ancestors
+ *   m2_verify_tree            the accepted path, and one token more
+ *   mamba2_layer_tree_commit  state, conv ring and position along the path (its part:
+ *   mamba2_tree_commit)
+ *   m2_kv4_keep               the path's cache rows moved together
+ * Results of a node are those of its path fed as single tokens.  A node's position (for
+ * the rotation) is L + its depth.
+ *   cu_nodes  HOST array of nseq + 1 offsets, cu_nodes[0] = 0, non-decreasing, at most
+ *             M2_TREE_NODES nodes a sequence (M2_ERR_UNSUPPORTED otherwise); read during
+ *             the call only.  Rows, parents and paths of sequence i start there.
+ *   parent    device int32 [cu_nodes[nseq]]: index within the sequence's nodes of each
+ *             node's parent, below the node's own; -1: the node follows the context.  A
+ *             node with any other value (a padded place), or below one, is not part of
+ *             the tree: its outputs are zeros, and no other node sees it.
+ *   path      device int32 [cu_nodes[nseq]], count device int32 [nseq]: count[i] nodes,
+ *             from the first on, each an entry below its sequence's number of nodes.
+ *             Entries that are not, and counts outside 0 .. nodes, are left out and
+ *             reported by m2_device_status (M2_ERR_ARG).
+ * Topology, paths and counts are read on the device: a captured pass serves for every
+ * tree of its size.  What nodes beside a node's path hold does not reach it, NaN and
+ * infinities included.  A call without nodes launches nothing and succeeds. */
+#define M2_TREE_NODES 64
+
+/* Causal depthwise conv over the trees, with bias (or NULL) and optional SiLU: a node's
+ * window is its own row, its ancestors', then the ring from the newest token back
+ * (conv1d_update's arithmetic).  Ring and position are only read.
+ *   x [T][C] rows ld_x apart, out [T][C] rows ld_o apart, w [C][d_conv], 2 <= d_conv <= 8.
+ * Any alignment serves; 16-byte aligned pointers and strides with C % 8 == 0 are faster. */
+int mamba2_tree_conv(const uint16_t* conv_state, const int32_t* conv_pos, const uint16_t* x, int32_t ld_x,
+                     const uint16_t* w, const uint16_t* bias, uint16_t* out, int32_t ld_o, int32_t nseq,
+                     const int32_t* cu_nodes, const int32_t* parent, int32_t C, int32_t d_conv, int32_t silu,
+                     cudaStream_t stream);
+
+/* SSM outputs of every node; the state h [nseq][H][P][N] (finite values) is only read.  With dt_j and
+ * dA_j as in mamba2_ssm_step, path(r) a node and its ancestors, s_r = sum over path(r) of
+ * log dA_j:
+ *   y_r = e^{s_r} C_r h^T + sum_{j in path(r)} e^{s_r - s_j} dt_j (C_r . B_j) x_j + D x_r
+ * which is what the steps along the path give, in fp32 (every fp32 operand enters the
+ * products with all its bits).  x [T][H*P], Bm and Cm [T][G*N] rows ld_in apart, dt_raw
+ * [T][H] rows ld_dt apart, bf16; y [T][H*P] fp32, 8-byte aligned.  Other rules as
+ * mamba2_ssm_step. */
+int mamba2_tree_ssm(const float* h, const uint16_t* x, const uint16_t* Bm, const uint16_t* Cm, int32_t ld_in,
+                    const uint16_t* dt_raw, int32_t ld_dt, const float* A_log, const float* D, const float* dt_bias,
+                    float* y, int32_t nseq, const int32_t* cu_nodes, const int32_t* parent, int32_t H, int32_t P,
+                    int32_t N, int32_t G, cudaStream_t stream);
+
+/* State, ring and position of every sequence moved along its accepted path: the steps of
+ * mamba2_ssm_step on the state (the same bits), the path's raw rows into the ring, the
+ * position advanced by count.  Each output may be its input itself (the same pointer);
+ * otherwise it is written whole.
+ *   xbc     [T][H*P + 2*G*N] raw projection rows, ld_xbc apart (what the ring holds)
+ *   u       [T][H*P + 2*G*N] conv outputs x | B | C, ld_u apart (ld_u % 4 == 0)
+ *   dt_raw  [T][H], ld_dt apart
+ * Sequences without nodes, or with a count of 0, keep what they have. */
+int mamba2_tree_commit(const float* h, const uint16_t* conv_state, const int32_t* conv_pos, float* h_out,
+                       uint16_t* conv_state_out, int32_t* conv_pos_out, const uint16_t* xbc, int32_t ld_xbc,
+                       const uint16_t* u, int32_t ld_u, const uint16_t* dt_raw, int32_t ld_dt, const float* A_log,
+                       const float* dt_bias, int32_t nseq, const int32_t* cu_nodes, const int32_t* path,
+                       const int32_t* count, int32_t H, int32_t P, int32_t N, int32_t G, int32_t d_conv,
+                       cudaStream_t stream);
+
+/* A layer over the trees' rows: hidden [T][hidden] bf16 in place, as mamba2_layer_prefill_varlen,
+ * but every node continues its parent and the sequences' state is only read.  The workspace
+ * (m2_workspace_bytes_tree bytes, 256-byte aligned) holds what the commit needs: each
+ * layer of a stack keeps its own from mamba2_layer_tree to mamba2_layer_tree_commit,
+ * which takes the same layer, trees and sequences. */
+size_t m2_workspace_bytes_tree(const m2_dims* dims, int32_t max_seqs, int32_t max_total_nodes);
+int mamba2_layer_tree(const m2_dims* dims, const m2_layer* layer, uint16_t* hidden, int32_t nseq,
+                      const int32_t* cu_nodes, const int32_t* parent, const float* ssm_state,
+                      const uint16_t* conv_state, const int32_t* conv_pos, void* ws, size_t ws_bytes,
+                      cudaStream_t stream);
+int mamba2_layer_tree_commit(const m2_dims* dims, const m2_layer* layer, int32_t nseq, const int32_t* cu_nodes,
+                             const int32_t* path, const int32_t* count, float* ssm_state, uint16_t* conv_state,
+                             int32_t* conv_pos, const void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of the nodes over the 4-bit cache.  Node r of sequence i sees the tokens 0 ..
+ * kv_pos[i] - 1 and those of its path, token kv_pos[i] + a for node a (appended before the
+ * call); each query head reads its kv head as in m2_attn_decode_kv4, with its rounding.
+ *   q, out    [T][H*head_dim] bf16.
+ *   kv_pos    device [nseq] int32: the context's tokens, as m2_kv4_append took it.  Below
+ *             -2^30 (M2_KV4_IDLE) the sequence takes no part: its rows are zeros.  So they
+ *             are for another negative value, which m2_device_status reports as
+ *             M2_ERR_ARG, as it does tokens past the block table and pages outside the
+ *             pool, which are left out.
+ *   ws        m2_attn_tree_kv4_workspace_bytes(H, Hkv, head_dim) bytes, 256-byte aligned.
+ * A row that sees nothing, or whose scores are all -Inf, is zeros.  The number of
+ * sequences (at most 128 of them counted) times ld_table times 4 (H + Hkv) stays below
+ * 2^31 (M2_ERR_UNSUPPORTED). */
+size_t m2_attn_tree_kv4_workspace_bytes(int32_t H, int32_t Hkv, int32_t head_dim);
+int m2_attn_tree_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q, uint16_t* out, int32_t ld_o,
+                     int32_t H, const int32_t* cu_nodes, const int32_t* parent, const int32_t* kv_pos, float scale,
+                     void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Verification of the drafted tokens.  Node 0 of a sequence is the last certain token.  The
+ * walk starts there; at node c with target row p = p[c] and draft row q = q[c], its
+ * children r (drawn from q) are asked in order, k of them refused so far:
+ *   r is accepted, and the walk goes on there, if u[r] * q(x_r) * S_k < R_k(x_r)
+ *   R_k = max(p - c_k q, 0);  c_0 = 0, S_0 = 1;  c_{k+1} = c_k + S_k, S_k = sum R_k
+ * (x_r = token[r]), which is sampling from p whatever the draft.  With no child left, the
+ * next token is drawn from the last R: the first t with R(0) + .. + R(t) > u_next * sum R;
+ * from p itself if R holds nothing; -1 if p holds nothing either.
+ *   p, q       [T][V] fp32 or bf16 (fmt), rows ld_p / ld_q apart, rows by node: the
+ *              distributions of the token after it.  q NULL: children were chosen without
+ *              chance and differ from one another; r is accepted if u[r] * S_k < p(x_r), a
+ *              refused token is removed from p, and S_k is what is left of it.
+ *   token      device int32 [T]; outside [0, V): the node is refused and changes nothing.
+ *   u          device fp32 [T], u_next device fp32 [nseq]: numbers in [0, 1).
+ *   path, count, next_token  device int32 [T], [nseq], [nseq]: the accepted nodes, node 0
+ *              first, then -1; their number; the token drawn.  A sequence without nodes,
+ *              or whose node 0 has a parent: count 0, token -1.
+ * Values of p and q that are not positive and finite count as 0.  Sums are accurate to
+ * about 2^-45, comparisons are made in 64 bits. */
+enum { M2_PROB_F32 = 1, M2_PROB_BF16 = 2 };
+int m2_verify_tree(const void* p, int64_t ld_p, const void* q, int64_t ld_q, int32_t fmt, int32_t V, int32_t nseq,
+                   const int32_t* cu_nodes, const int32_t* parent, const int32_t* token, const float* u,
+                   const float* u_next, int32_t* path, int32_t* count, int32_t* next_token, cudaStream_t stream);
+
+/* The accepted nodes' rows of one layer's cache moved to the tokens that follow the
+ * context: token kv_pos[i] + path[j] becomes kv_pos[i] + j for j < count[i], as if all were
+ * read before any is written (codes and scales as they are).  kv_pos is not advanced; idle
+ * slots (below -2^30) take no part.  Rows whose page lies outside the pool or past the
+ * table are not moved, and reported. */
+int m2_kv4_keep(const m2_kv4_cache* cache, const int32_t* cu_nodes, const int32_t* path, const int32_t* count,
+                const int32_t* kv_pos, cudaStream_t stream);
+
 /* ------------------------------------------------------------ diagnostics */
 
 /* Where a call keeps its intermediate values in the workspace, for reading
  * them back (tests, debugging).  kind: M2_WS_KIND_DECODE (n = batch rows,
  * cu_seqlens unused), M2_WS_KIND_PREFILL or M2_WS_KIND_PREFILL_W8A8 (n =
  * sequences, cu_seqlens their host offsets as for the varlen prefill; the
- * one-sequence prefill is n = 1, {0, T}).  offsets[n_offsets >= M2_WS_COUNT]
+ * one-sequence prefill is n = 1, {0, T}), or M2_WS_KIND_TREE (mamba2_layer_tree; as the
+ * prefill).  offsets[n_offsets >= M2_WS_COUNT]
  * receives byte offsets from ws, SIZE_MAX for a region the call does not use:
  *   M2_WS_XN  input RMSNorm output [rows][hidden] (tensor-core paths)
  *   M2_WS_ZX  in_proj output [rows][rup8(n_in)] bf16: z | xBC | dt (decode:
@@ -452,14 +587,14 @@ int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_
  *             [d_inner/128][rup128(T)].
  * Contents are valid after the call completes and until the next call on the
  * same workspace.  Host only; returns M2_OK or M2_ERR_ARG. */
-enum { M2_WS_KIND_DECODE = 0, M2_WS_KIND_PREFILL = 1, M2_WS_KIND_PREFILL_W8A8 = 2 };
+enum { M2_WS_KIND_DECODE = 0, M2_WS_KIND_PREFILL = 1, M2_WS_KIND_PREFILL_W8A8 = 2, M2_WS_KIND_TREE = 3 };
 enum { M2_WS_XN = 0, M2_WS_ZX, M2_WS_U, M2_WS_Y, M2_WS_G, M2_WS_Q8, M2_WS_SQ, M2_WS_UNSCALE, M2_WS_COUNT };
 int m2_workspace_map(const m2_dims* dims, int32_t kind, int32_t n, const int32_t* cu_seqlens, size_t* offsets,
                      int32_t n_offsets);
 
 /* Device status word: M2_OK, or the first failure a kernel recorded on the
  * current device (M2_ERR_TIMEOUT; M2_ERR_ARG for a page index or length that the
- * 4-bit cache's kernels left out).  Synchronises the device.  clear != 0 resets it. */
+ * 4-bit cache's kernels, or a path's entry or count that the tree kernels, left out).  Synchronises the device.  clear != 0 resets it. */
 int m2_device_status(int clear);
 
 /* Limit of the library's in-kernel pipeline waits on the current device, in

@@ -40,7 +40,10 @@ EXPORTS = ("m2_strerror", "m2_validate", "m2_workspace_bytes", "mamba2_layer_dec
            "m2_trace_begin", "m2_trace_end", "m2_kernel_name", "m2_kernel_count", "m2_set_fused_decode", "m2_copy",
            "m2_set_wait_limit", "m2_wait_check", "m2_workspace_map",
            "m2_qk_norm_rope", "m2_rope_steps", "m2_kv4_page_bytes", "m2_kv4_append", "m2_kv4_gather",
-           "m2_attn_prefill_varlen", "m2_attn_decode_kv4_workspace_bytes", "m2_attn_decode_kv4")
+           "m2_attn_prefill_varlen", "m2_attn_decode_kv4_workspace_bytes", "m2_attn_decode_kv4",
+           "mamba2_tree_conv", "mamba2_tree_ssm", "mamba2_tree_commit", "m2_workspace_bytes_tree", "mamba2_layer_tree",
+           "mamba2_layer_tree_commit", "m2_attn_tree_kv4_workspace_bytes", "m2_attn_tree_kv4", "m2_verify_tree",
+           "m2_kv4_keep")
 
 
 class M2Dims(C.Structure):
@@ -139,6 +142,26 @@ def lib():
             l.m2_attn_decode_kv4_workspace_bytes.restype = SZ
             l.m2_attn_decode_kv4.argtypes = [CACHE, P, I32, P, I32, I32, P, F, P, SZ, P]
             l.m2_attn_decode_kv4.restype = C.c_int
+            DIMS, LAYER, I64 = C.POINTER(M2Dims), C.POINTER(M2Layer), C.c_int64
+            l.mamba2_tree_conv.argtypes = [P, P, P, I32, P, P, P, I32, I32, CU, P, I32, I32, I32, P]
+            l.mamba2_tree_conv.restype = C.c_int
+            l.mamba2_tree_ssm.argtypes = [P, P, P, P, I32, P, I32, P, P, P, P, I32, CU, P, I32, I32, I32, I32, P]
+            l.mamba2_tree_ssm.restype = C.c_int
+            l.mamba2_tree_commit.argtypes = [P, P, P, P, P, P, P, I32, P, I32, P, I32, P, P, I32, CU, P, P, I32, I32, I32,
+                                             I32, I32, P]
+            l.mamba2_tree_commit.restype = C.c_int
+            l.m2_workspace_bytes_tree.argtypes = [DIMS, I32, I32]; l.m2_workspace_bytes_tree.restype = SZ
+            l.mamba2_layer_tree.argtypes = [DIMS, LAYER, P, I32, CU, P, P, P, P, P, SZ, P]
+            l.mamba2_layer_tree.restype = C.c_int
+            l.mamba2_layer_tree_commit.argtypes = [DIMS, LAYER, I32, CU, P, P, P, P, P, P, SZ, P]
+            l.mamba2_layer_tree_commit.restype = C.c_int
+            l.m2_attn_tree_kv4_workspace_bytes.argtypes = [I32, I32, I32]
+            l.m2_attn_tree_kv4_workspace_bytes.restype = SZ
+            l.m2_attn_tree_kv4.argtypes = [CACHE, P, I32, P, I32, I32, CU, P, P, F, P, SZ, P]
+            l.m2_attn_tree_kv4.restype = C.c_int
+            l.m2_verify_tree.argtypes = [P, I64, P, I64, I32, I32, I32, CU, P, P, P, P, P, P, P, P]
+            l.m2_verify_tree.restype = C.c_int
+            l.m2_kv4_keep.argtypes = [CACHE, CU, P, P, P, P]; l.m2_kv4_keep.restype = C.c_int
             _lib = l
     return _lib
 
@@ -360,6 +383,98 @@ def m2_attn_decode_kv4(cache, q, ld_q, out, ld_o, H, kv_len, scale, ws, ws_bytes
     return _check("m2_attn_decode_kv4", st) if check else st
 
 
+# ------------------------------------------------------------------ trees of drafted tokens
+
+M2_TREE_NODES = 64
+M2_PROB_F32, M2_PROB_BF16 = 1, 2
+
+
+def mamba2_tree_conv(conv_state, conv_pos, x, ld_x, w, bias, out, ld_o, cu_nodes, parent, Cc, d_conv, silu=1,
+                     stream=None, check=True) -> int:
+    """cu_nodes: host sequence of nseq + 1 node offsets (here and below)."""
+    n = len(cu_nodes) - 1
+    cu = _offsets("mamba2_tree_conv", cu_nodes, n)
+    st = (_lib or lib()).mamba2_tree_conv(_ptr(conv_state), _ptr(conv_pos), _ptr(x), ld_x, _ptr(w), _ptr(bias),
+                                          _ptr(out), ld_o, n, cu.buffer_info()[0], _ptr(parent), Cc, d_conv, silu,
+                                          _stream(stream))
+    return _check("mamba2_tree_conv", st) if check else st
+
+
+def mamba2_tree_ssm(h, x, Bm, Cm, ld_in, dt_raw, ld_dt, A_log, D, dt_bias, y, cu_nodes, parent, H, P, N, G, stream=None,
+                    check=True) -> int:
+    n = len(cu_nodes) - 1
+    cu = _offsets("mamba2_tree_ssm", cu_nodes, n)
+    st = (_lib or lib()).mamba2_tree_ssm(_ptr(h), _ptr(x), _ptr(Bm), _ptr(Cm), ld_in, _ptr(dt_raw), ld_dt, _ptr(A_log),
+                                         _ptr(D), _ptr(dt_bias), _ptr(y), n, cu.buffer_info()[0], _ptr(parent), H, P, N,
+                                         G, _stream(stream))
+    return _check("mamba2_tree_ssm", st) if check else st
+
+
+def mamba2_tree_commit(h, conv_state, conv_pos, h_out, conv_state_out, conv_pos_out, xbc, ld_xbc, u, ld_u, dt_raw,
+                       ld_dt, A_log, dt_bias, cu_nodes, path, count, H, P, N, G, d_conv, stream=None, check=True) -> int:
+    """Each output may be its input itself."""
+    n = len(cu_nodes) - 1
+    cu = _offsets("mamba2_tree_commit", cu_nodes, n)
+    st = (_lib or lib()).mamba2_tree_commit(_ptr(h), _ptr(conv_state), _ptr(conv_pos), _ptr(h_out),
+                                            _ptr(conv_state_out), _ptr(conv_pos_out), _ptr(xbc), ld_xbc, _ptr(u), ld_u,
+                                            _ptr(dt_raw), ld_dt, _ptr(A_log), _ptr(dt_bias), n, cu.buffer_info()[0],
+                                            _ptr(path), _ptr(count), H, P, N, G, d_conv, _stream(stream))
+    return _check("mamba2_tree_commit", st) if check else st
+
+
+def m2_workspace_bytes_tree(dims: M2Dims, max_seqs: int, max_total_nodes: int) -> int:
+    return lib().m2_workspace_bytes_tree(C.byref(dims), max_seqs, max_total_nodes)
+
+
+def mamba2_layer_tree(dims, layer, hidden, cu_nodes, parent, ssm_state, conv_state, conv_pos, ws, ws_bytes, stream=None,
+                      check=True) -> int:
+    n = len(cu_nodes) - 1
+    cu = _offsets("mamba2_layer_tree", cu_nodes, n)
+    st = lib().mamba2_layer_tree(C.byref(dims), C.byref(layer), _ptr(hidden), n, cu.buffer_info()[0], _ptr(parent),
+                                 _ptr(ssm_state), _ptr(conv_state), _ptr(conv_pos), _ptr(ws), ws_bytes, _stream(stream))
+    return _check("mamba2_layer_tree", st) if check else st
+
+
+def mamba2_layer_tree_commit(dims, layer, cu_nodes, path, count, ssm_state, conv_state, conv_pos, ws, ws_bytes,
+                             stream=None, check=True) -> int:
+    n = len(cu_nodes) - 1
+    cu = _offsets("mamba2_layer_tree_commit", cu_nodes, n)
+    st = lib().mamba2_layer_tree_commit(C.byref(dims), C.byref(layer), n, cu.buffer_info()[0], _ptr(path), _ptr(count),
+                                        _ptr(ssm_state), _ptr(conv_state), _ptr(conv_pos), _ptr(ws), ws_bytes,
+                                        _stream(stream))
+    return _check("mamba2_layer_tree_commit", st) if check else st
+
+
+def m2_attn_tree_kv4_workspace_bytes(H: int, Hkv: int, head_dim: int) -> int:
+    return lib().m2_attn_tree_kv4_workspace_bytes(H, Hkv, head_dim)
+
+
+def m2_attn_tree_kv4(cache, q, ld_q, out, ld_o, H, cu_nodes, parent, kv_pos, scale, ws, ws_bytes, stream=None,
+                     check=True) -> int:
+    cu = _offsets("m2_attn_tree_kv4", cu_nodes, cache.nseq)
+    st = (_lib or lib()).m2_attn_tree_kv4(C.byref(cache), _ptr(q), ld_q, _ptr(out), ld_o, H, cu.buffer_info()[0],
+                                          _ptr(parent), _ptr(kv_pos), scale, _ptr(ws), ws_bytes, _stream(stream))
+    return _check("m2_attn_tree_kv4", st) if check else st
+
+
+def m2_verify_tree(p, ld_p, q, ld_q, fmt, V, cu_nodes, parent, token, u, u_next, path, count, next_token, stream=None,
+                   check=True) -> int:
+    """q None: the drafted tokens were chosen without chance."""
+    n = len(cu_nodes) - 1
+    cu = _offsets("m2_verify_tree", cu_nodes, n)
+    st = (_lib or lib()).m2_verify_tree(_ptr(p), ld_p, _ptr(q), ld_q, fmt, V, n, cu.buffer_info()[0], _ptr(parent),
+                                        _ptr(token), _ptr(u), _ptr(u_next), _ptr(path), _ptr(count), _ptr(next_token),
+                                        _stream(stream))
+    return _check("m2_verify_tree", st) if check else st
+
+
+def m2_kv4_keep(cache, cu_nodes, path, count, kv_pos, stream=None, check=True) -> int:
+    cu = _offsets("m2_kv4_keep", cu_nodes, cache.nseq)
+    st = (_lib or lib()).m2_kv4_keep(C.byref(cache), cu.buffer_info()[0], _ptr(path), _ptr(count), _ptr(kv_pos),
+                                     _stream(stream))
+    return _check("m2_kv4_keep", st) if check else st
+
+
 def m2_device_status(clear: bool = False) -> int:
     return lib().m2_device_status(1 if clear else 0)
 
@@ -385,7 +500,7 @@ def m2_wait_check(probe, out, stream=None, check=True) -> int:
     return _check("m2_wait_check", st) if check else st
 
 
-M2_WS_KIND_DECODE, M2_WS_KIND_PREFILL, M2_WS_KIND_PREFILL_W8A8 = 0, 1, 2
+M2_WS_KIND_DECODE, M2_WS_KIND_PREFILL, M2_WS_KIND_PREFILL_W8A8, M2_WS_KIND_TREE = 0, 1, 2, 3
 WS_REGIONS = ("xn", "zx", "u", "y", "g", "q8", "sq", "unscale")
 
 

@@ -1,0 +1,719 @@
+// k_attn_tree.cu -- attention of a tree of drafted tokens over the paged 4-bit cache
+// (include/mamba2.h has the rule of what a node sees).
+//
+// A unit is one page (64 tokens) of one kv head for one tile of rows: 16 R rows, row m
+// = node m / G with query head m % G of the group.  The units of all sequences, in the
+// order (sequence, kv head, tile, page), are cut into equal spans, one a CTA, and each
+// span into equal runs, one a stream.  A stream is R warps of 16 rows each, which read
+// the same ring of bulk copies; 12 / R streams a CTA.  In a warp, on warp MMA:
+//   S [16 x 64 tokens] = Q K^T    K codes become f16 and take their scale, exactly
+//   O [16 x D] += P V             likewise V; P rounded to f16 (2^-11)
+// The pages' orders of codes are those of both products' B operands, P goes from the
+// first to the second in registers.  Queries are f16 rows prescaled by an exact power of
+// two.  Scores, sums and outputs are fp32.  A row's node is a 64-bit mask of its path;
+// shifted to a page's tokens it says what the row sees there.  Rows that a stream, then
+// a CTA, holds only in part are joined: streams through shared memory, CTAs by
+// attn_tree_combine.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "m2_common.cuh"
+#include "m2_kernels.h"
+#include "m2_kv4.cuh"
+#include "m2_kv4_mma.cuh"
+#include "m2_tc.cuh"
+#include "m2_tree.cuh"
+
+namespace m2 {
+
+constexpr int kAtWarps = 12, kAtrThreads = kAtWarps * 32;
+
+template <int D, int R>
+struct AtrCfg {
+  static constexpr int kUnit = Kv4Block<D>::kBytes;
+  static constexpr int kStreams = kAtWarps / R, kRows = 16 * R;
+  static constexpr int kStages = (D == 128 ? 2 : 4) * R;  // 12 warps' worth of 18 KB
+  static constexpr int kRing = kStages * kUnit;           // of one stream
+  static constexpr int kStride = D + 8;                   // floats between the rows of a record: no bank conflicts
+  static constexpr int kRecord = 2 * kRows + kRows * kStride;  // maxima, sums, outputs
+  static constexpr int kParts = 2 * kStreams;             // a stream leaves a first and a last part at most
+};
+// Which row tile a partial belongs to, and whether it starts before / ends after the CTA's span.
+struct AtrMeta {
+  int32_t seg, before, after;
+};
+struct AtrShared {
+  uint64_t full[kAtWarps * 4], empty[kAtWarps * 4];
+  int32_t ok[kAtWarps * 4];
+  AtrMeta meta[2 * kAtWarps];
+  float part_m[kAtrThreads], part_l[kAtrThreads];  // [part][row]: maxima (then weights) and sums
+  float row_l[kAtrThreads];                        // [cut tile][row]
+  uint32_t row_parts[2 * kAtWarps];
+  int32_t cta_seg[2];
+  int32_t scan[kAtWarps];
+  int32_t run0[kAtWarps + 1], run_b[kAtWarps], run_base[kAtWarps];
+};
+
+struct AtrArgs {
+  AttnTreeArgs g;
+  int32_t G, most_tiles;    // query heads a kv head; tiles of the launch's largest tree
+  int32_t nc, by_row;       // CTAs; one CTA a tile: none is cut
+  float* part;              // [nc][kStreams] records
+  float* cta_part;          // [nc][2] records: a tile that began earlier, one that goes on
+  int32_t* cta_seg;         // [nc][2] their tiles, -1 where there is none
+};
+
+__device__ __forceinline__ int atr_nodes(const AttnTreeArgs& g, int b) { return g.t.cu[b + 1] - g.t.cu[b]; }
+// Tokens that the tree's last node could see; 0 for a slot that takes no part.
+__device__ __forceinline__ int atr_len(const AttnTreeArgs& g, int b) {
+  const int n = atr_nodes(g, b), pos = g.pos[b];
+  if (n == 0 || pos < 0) {
+    if (n && pos >= -(1 << 30)) M2_RECORD_ARG(g_status);
+    return 0;
+  }
+  const int most = g.c.ld_table * kPage;
+  if (pos > most - n) M2_RECORD_ARG(g_status);
+  return pos > most - n ? most : pos + n;
+}
+__device__ __forceinline__ int atr_tiles(const AtrArgs& a, int b, int rows) {
+  return (atr_nodes(a.g, b) * a.G + rows - 1) / rows;
+}
+__device__ __forceinline__ int atr_units(const AtrArgs& a, int b, int rows) {
+  const int n = atr_len(a.g, b);
+  return (n + kPage - 1) / kPage * a.g.c.Hkv * atr_tiles(a, b, rows);
+}
+
+// The running softmax of 16 rows in a warp: lane (r, c) = (lane / 4, lane % 4) owns rows r and r + 8.
+template <int D>
+struct AtrRows {
+  uint32_t q[D / 16][4];  // A operand: rows r, r + 8; channels 16g + 4c .. + 3
+  float qs[2];            // score factor (log2 units)
+  float m[2], l[2];       // reference maximum; this lane's share of the sum
+  uint64_t seen[2];       // the rows' paths; 0: no such row
+  float o[D / 8][4];      // channels 8i + 2c, + 1 of rows r, r + 8
+
+  // Rows m0 .. m0 + 15 of sequence b, kv head hk; tree: the sequence's masks.
+  __device__ __forceinline__ void start(const AtrArgs& a, int b, int hk, int m0, const uint64_t (&tree)[2], int lane) {
+    const int r = lane >> 2, c = lane & 3, first = a.g.t.cu[b], rows = atr_nodes(a.g, b) * a.G;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int x = m0 + r + 8 * k, node = min(x, rows - 1) / a.G, h = x - node * a.G;
+      const uint64_t path = tree_mask_of(tree, node);
+      seen[k] = x < rows ? path : 0ull;
+      uint2 w[D / 16];
+      float top = 0.0f;
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) {
+        w[g] = make_uint2(0u, 0u);
+        if (seen[k])
+          w[g] = *reinterpret_cast<const uint2*>(a.g.q + (size_t)(first + node) * a.g.ld_q + (size_t)(hk * a.G + h) * D +
+                                                 16 * g + 4 * c);
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w[g].x)), fabsf(bf16hi(w[g].x))),
+                               fmaxf(fabsf(bf16lo(w[g].y)), fabsf(bf16hi(w[g].y)))));
+      }
+      float f;
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      kv4_query_scale(top, a.g.scale, f, qs[k]);
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) {
+        q[g][k] = pack_f16x2(bf16lo(w[g].x) * f, bf16hi(w[g].x) * f);
+        q[g][2 + k] = pack_f16x2(bf16lo(w[g].y) * f, bf16hi(w[g].y) * f);
+      }
+      m[k] = -INFINITY, l[k] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+  }
+
+  // One unit in shared memory.  base: its first token less the context's length (0 or
+  // more: only nodes; -64 or less: only context); left: tokens of the sequence from its first on.
+  __device__ __forceinline__ void unit(const uint8_t* u, int base, int left, int lane) {
+    using L = Kv4Block<D>;
+    constexpr int GW = D / 32;  // words of a lane's codes: 2 groups each
+    const int r = lane >> 2, c = lane & 3;
+    float s[8][4];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      uint32_t k[GW], sc[GW / 2];
+      const int t = 8 * nt + r;
+      lds_words<GW>(u + L::kK + t * (D / 2) + c * (D / 8), k);
+      lds_words<GW / 2>(u + L::kKs + t * (D / 16), sc);
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        const uint32_t e = scales02(sc[w / 2], kScaleBits), f = scales13(sc[w / 2], kScaleBits);
+        uint32_t x[4];
+        codes4(k[w], x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = w & 1 ? hmul2_hi(x[i], i < 2 ? e : f) : hmul2_lo(x[i], i < 2 ? e : f);
+        if (w == 0)
+          mma_f16_first(s[nt], q[0][0], q[0][1], q[0][2], q[0][3], x[0], x[1]);
+        else
+          mma_f16(s[nt], q[2 * w][0], q[2 * w][1], q[2 * w][2], q[2 * w][3], x[0], x[1]);
+        mma_f16(s[nt], q[2 * w + 1][0], q[2 * w + 1][1], q[2 * w + 1][2], q[2 * w + 1][3], x[2], x[3]);
+      }
+    }
+    // what the rows see of the page, by token
+    const bool part = base > -kPage;
+    uint64_t see[2] = {~0ull, ~0ull};
+    uint64_t bad = 0;  // tokens with values that are not finite, some group of them
+    if (part) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        see[k] = base >= 0 ? seen[k] >> base : seen[k] << -base | ((1ull << -base) - 1);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (!(see[k] >> (8 * nt + 2 * c + j) & 1)) s[nt][2 * k + j] = -INFINITY;
+      }
+      uint32_t vs[GW];  // of token pair `lane`: bytes (even, even, odd, odd)
+      lds_words<GW>(u + L::kVs + lane * (D / 8), vs);
+      uint32_t even = 0, odd = 0;
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        const uint32_t x = vs[w] & 0xF8F8F8F8u;  // exponents
+        even |= (x & 0xFFu) == 0xF8u || (x & 0xFF00u) == 0xF800u;
+        odd |= (x & 0xFF0000u) == 0xF80000u || (x & 0xFF000000u) == 0xF8000000u;
+      }
+      const uint32_t be = __ballot_sync(0xffffffffu, even && 2 * lane < left), bo = __ballot_sync(0xffffffffu, odd && 2 * lane + 1 < left);
+      if (be | bo)
+        for (int t = 0; t < 32; ++t) bad |= (uint64_t)((be >> t & 1) | (bo >> t & 1) << 1) << (2 * t);
+    }
+    // softmax: P becomes the second product's A operand.  qs > 0: maxima are taken before it is applied.
+    bool grow = false;
+    float mx[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mx[k] = fmaxf(s[0][2 * k], s[0][2 * k + 1]);
+#pragma unroll
+      for (int nt = 1; nt < 8; ++nt) mx[k] = fmaxf(mx[k], fmaxf(s[nt][2 * k], s[nt][2 * k + 1]));
+      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+      mx[k] *= qs[k];
+      grow |= mx[k] - m[k] > 8.0f;
+    }
+    // the reference follows the maximum once it has grown 2^8: until then P (with its
+    // factor 2^7, which keeps small ones out of f16's subnormals) stays below 2^15
+    if (__any_sync(0xffffffffu, grow)) {
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool up = mx[k] - m[k] > 8.0f;
+        f[k] = up ? ad_ex2(m[k] - mx[k]) : 1.0f;
+        if (up) m[k] = mx[k];
+        l[k] *= f[k];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
+    }
+    uint32_t p[4][4];
+    const float b0 = m[0] == -INFINITY ? 0.0f : 7.0f - m[0], b1 = m[1] == -INFINITY ? 0.0f : 7.0f - m[1];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float x0 = ad_ex2(fmaf(s[nt][0], qs[0], b0)), x1 = ad_ex2(fmaf(s[nt][1], qs[0], b0));
+      const float x2 = ad_ex2(fmaf(s[nt][2], qs[1], b1)), x3 = ad_ex2(fmaf(s[nt][3], qs[1], b1));
+      l[0] += x0 + x1;
+      l[1] += x2 + x3;
+      p[nt / 2][nt % 2 * 2] = pack_f16x2(x0, x1);
+      p[nt / 2][nt % 2 * 2 + 1] = pack_f16x2(x2, x3);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint32_t v0[GW], v1[GW], s0[GW], s1[GW];
+      lds_words<GW>(u + L::kV + (2 * ks) * (4 * D) + r * (D / 2) + c * (D / 8), v0);
+      lds_words<GW>(u + L::kV + (2 * ks + 1) * (4 * D) + r * (D / 2) + c * (D / 8), v1);
+      lds_words<GW>(u + L::kVs + (8 * ks + c) * (D / 8), s0);
+      lds_words<GW>(u + L::kVs + (8 * ks + 4 + c) * (D / 8), s1);
+      uint32_t k0 = kScaleBits, k1 = kScaleBits;  // slots past the last token may hold any scale: theirs become 0
+      if (part) {
+        const int t0 = 16 * ks + 2 * c, t1 = t0 + 8;
+        k0 = (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
+        k1 = (t1 < left ? 0x7F80u : 0u) | (t1 + 1 < left ? 0x7F800000u : 0u);
+      }
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        uint32_t e0 = scales02(s0[w], k0), f0 = scales13(s0[w], k0), e1 = scales02(s1[w], k1), f1 = scales13(s1[w], k1);
+        if (bad) e0 = kv4_finite(e0), f0 = kv4_finite(f0), e1 = kv4_finite(e1), f1 = kv4_finite(f1);
+        uint32_t x[4], y[4];
+        codes4(v0[w], x);
+        codes4(v1[w], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = hmul2(x[i], i < 2 ? e0 : f0);
+          y[i] = hmul2(y[i], i < 2 ? e1 : f1);
+          mma_f16(o[4 * w + i], p[ks][0], p[ks][1], p[ks][2], p[ks][3], x[i], y[i]);
+        }
+      }
+    }
+    // values that are not finite, kept out of the product: they are NaN to the rows that see them
+    for (; bad; bad &= bad - 1) {
+      const int t = __ffsll((long long)bad) - 1;
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g)
+        if ((u[L::vs(t, g)] & 0xF8u) == 0xF8u) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (see[j >> 1] >> t & 1) o[2 * g][j] = o[2 * g + 1][j] = __int_as_float(0x7FFFFFFF);
+        }
+    }
+  }
+
+  // The sums over the lanes of a row; rows that are none hold nothing.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+      if (seen[k] == 0) {
+        m[k] = -INFINITY, l[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][2 * k] = o[i][2 * k + 1] = 0.0f;
+      }
+    }
+  }
+  // pm, pl, out: of the warp's first row
+  __device__ __forceinline__ void store_part(float* out, float* pm, float* pl, int stride, int lane) const {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (c == 0) pm[r + 8 * k] = m[k], pl[r + 8 * k] = l[k];
+      float* d = out + (r + 8 * k) * stride + 2 * c;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(o[i][2 * k], o[i][2 * k + 1]);
+    }
+  }
+  __device__ __forceinline__ void store_out(const AtrArgs& a, int b, int hk, int m0, int lane) const {
+    const int r = lane >> 2, c = lane & 3, rows = atr_nodes(a.g, b) * a.G;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int x = m0 + r + 8 * k, node = x / a.G;
+      if (x >= rows) continue;
+      const float inv = l[k] != 0.0f ? 1.0f / l[k] : 0.0f;  // nothing seen: zeros
+      uint16_t* d = a.g.out + (size_t)(a.g.t.cu[b] + node) * a.g.ld_o + (size_t)(hk * a.G + x - node * a.G) * D + 2 * c;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<uint32_t*>(d + 8 * i) = pack_bf16x2(o[i][2 * k] * inv, o[i][2 * k + 1] * inv);
+    }
+  }
+};
+
+// A position in the order of units.
+struct AtrCursor {
+  int b, hk, tile, page, pages, tiles, len;
+  __device__ __forceinline__ void load(const AtrArgs& a, int rows) {
+    len = atr_len(a.g, b);
+    pages = (len + kPage - 1) / kPage;
+    tiles = atr_tiles(a, b, rows);
+  }
+  // to the next unit; b == nseq past the last one
+  __device__ __forceinline__ void next(const AtrArgs& a, int rows) {
+    if (++page < pages) return;
+    page = 0;
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++hk < a.g.c.Hkv) return;
+    hk = 0;
+    do {
+      if (++b >= a.g.t.nseq) return;
+      load(a, rows);
+    } while (pages == 0);
+  }
+  __device__ __forceinline__ int seg(const AtrArgs& a) const { return (b * a.g.c.Hkv + hk) * a.most_tiles + tile; }
+};
+
+// Row `row` of tile `seg`: where its output goes; null if there is no such row.
+__device__ __forceinline__ uint16_t* atr_out(const AtrArgs& a, int seg, int row, int rows, int D) {
+  const int tile = seg % a.most_tiles, bh = seg / a.most_tiles, b = bh / a.g.c.Hkv, hk = bh - b * a.g.c.Hkv;
+  const int x = tile * rows + row, node = x / a.G;
+  if (node >= atr_nodes(a.g, b)) return nullptr;
+  return a.g.out + (size_t)(a.g.t.cu[b] + node) * a.g.ld_o + (size_t)(hk * a.G + x - node * a.G) * D;
+}
+__device__ __forceinline__ void atr_store4(uint16_t* d, float4 o, float l) {
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
+  *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_constant__ AtrArgs a) {
+  using C = AtrCfg<D, R>;
+  constexpr int S = C::kStages, ST = C::kStreams, ROWS = C::kRows, PARTS = C::kParts;
+  static_assert(PARTS * ROWS == kAtrThreads && PARTS <= 32 && ST * S <= kAtWarps * 4, "a thread per part and row");
+  static_assert(C::kRecord * 4 <= C::kRing, "a record lies in its stream's ring");
+  extern __shared__ __align__(128) uint8_t smem[];
+  AtrShared* sh = reinterpret_cast<AtrShared*>(smem + ST * C::kRing);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int stream = warp / R, rw = warp % R;  // rows 16 rw .. of the stream's tile
+  uint64_t* full = sh->full + stream * S;
+  uint64_t* empty = sh->empty + stream * S;
+  int32_t* ok = sh->ok + stream * S;
+  if (rw == 0 && lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], R);
+    sh->meta[2 * stream].seg = sh->meta[2 * stream + 1].seg = -1;
+    fence_mbar_init();
+  }
+  if (tid < 2) sh->cta_seg[tid] = -1;
+  pdl_wait();
+  pdl_trigger();
+  const int B = a.g.t.nseq;
+  // ---- the span and its runs: prefix sums of the sequences' units (one a thread: kSeqs <= 384)
+  static_assert(kSeqs <= kAtrThreads, "a sequence a thread");
+  const int mine = tid < B ? atr_units(a, tid, ROWS) : 0;
+  int pre = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) sh->scan[warp] = pre;
+  __syncthreads();
+  int total = 0;
+  pre -= mine;
+#pragma unroll
+  for (int w = 0; w < kAtWarps; ++w) {
+    if (w < warp) pre += sh->scan[w];
+    total += sh->scan[w];
+  }
+  int s0, s1;
+  if (a.by_row) {  // tile cta % rows of sequence cta / rows
+    const int rows = a.g.c.Hkv * a.most_tiles, b = cta / rows, row = cta - b * rows;
+    if (tid == b) {
+      const int tiles = atr_tiles(a, b, ROWS), n = tiles ? mine / (a.g.c.Hkv * tiles) : 0;
+      const bool in = row < a.g.c.Hkv * tiles;
+      sh->run0[0] = pre + (in ? row * n : 0);
+      sh->run0[1] = sh->run0[0] + (in ? n : 0);
+    }
+    __syncthreads();
+    s0 = sh->run0[0];
+    s1 = sh->run0[1];
+    __syncthreads();
+  } else {
+    // at least a unit for every stream: the CTAs without work are the last ones
+    const int nc = min(a.nc, (total + ST - 1) / ST), q = nc ? total / nc : 0, extra = total - q * nc;
+    s0 = cta < nc ? q * cta + min(cta, extra) : total;
+    s1 = cta < nc ? s0 + q + (cta < extra ? 1 : 0) : total;
+  }
+  {
+    // run w: its share of the span, the first ones a unit longer
+    const int q = (s1 - s0) / ST, extra = s1 - s0 - q * ST;
+    if (tid <= ST) sh->run0[tid] = s0 + q * tid + min(tid, extra);
+    if (mine && pre < s1 && pre + mine > s0)
+      for (int w = 0; w < ST; ++w) {
+        const int u = s0 + q * w + min(w, extra);
+        if (u >= pre && u < pre + mine) {
+          sh->run_b[w] = tid;
+          sh->run_base[w] = pre;
+        }
+      }
+  }
+  // rows of sequences that take no part
+  for (int b = cta; b < B; b += gridDim.x)
+    if (atr_len(a.g, b) == 0)
+      for (int i = tid; i < atr_nodes(a.g, b) * (a.g.H * D / 8); i += kAtrThreads) {
+        const int j = i / (a.g.H * D / 8), e = i - j * (a.g.H * D / 8);
+        *reinterpret_cast<uint4*>(a.g.out + (size_t)(a.g.t.cu[b] + j) * a.g.ld_o + 8 * e) = make_uint4(0u, 0u, 0u, 0u);
+      }
+  __syncthreads();
+
+  // ---- this stream's run
+  uint8_t* ring = smem + stream * C::kRing;
+  const int u0 = sh->run0[stream], u1 = sh->run0[stream + 1], n = u1 - u0;
+  bool last = false;  // a part is left at the run's end
+  AtrCursor cur;
+  AtrRows<D> rows;
+  int row_at = 0;     // the tile's first unit
+  if (n > 0) {
+    cur.b = sh->run_b[stream];
+    cur.load(a, ROWS);
+    {
+      int in = u0 - sh->run_base[stream];
+      cur.hk = in / (cur.tiles * cur.pages);
+      in -= cur.hk * (cur.tiles * cur.pages);
+      cur.tile = in / cur.pages;
+      cur.page = in - cur.tile * cur.pages;
+    }
+    AtrCursor ahead = cur;
+    const uint64_t pol = a.most_tiles > 1 ? policy_evict_normal() : policy_evict_first();
+    auto fetch = [&](int i) {  // unit i of the run into its stage (the first warp of the stream)
+      const int st = i % S;
+      if (lane == 0) {
+        const int page = a.g.c.table[(size_t)ahead.b * a.g.c.ld_table + ahead.page];
+        const bool in = page >= 0 && page < a.g.c.n_pages;
+        ok[st] = in;
+        if (in) {
+          mbar_arrive_expect_tx(&full[st], C::kUnit);
+          bulk_g2s(ring + st * C::kUnit, a.g.c.pages + ((size_t)page * a.g.c.Hkv + ahead.hk) * C::kUnit, C::kUnit,
+                   &full[st], pol);
+        } else {
+          M2_RECORD_ARG(g_status);
+          mbar_arrive(&full[st]);
+        }
+      }
+      ahead.next(a, ROWS);
+    };
+    int fetched = 0;
+    if (rw == 0)
+      for (; fetched < S && fetched < n; ++fetched) fetch(fetched);
+    uint64_t tree[2];
+    int tree_b = cur.b;
+    tree_masks(a.g.t.parent + a.g.t.cu[cur.b], atr_nodes(a.g, cur.b), lane, tree);
+    rows.start(a, cur.b, cur.hk, cur.tile * ROWS + 16 * rw, tree, lane);
+    int first_page = cur.page;  // of the tile's part in this run
+    row_at = u0 - cur.page;
+    int pos = a.g.pos[cur.b];
+    bool dead = false;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % S;
+      // the stage before the last one is free once the stream's other warps have read it too
+      constexpr int LAG = R > 1 ? 1 : 0;
+      if (rw == 0 && fetched < n && i > LAG && fetched == i - 1 - LAG + S) {
+        const int e = fetched % S;
+        if (R > 1 && !__all_sync(0xffffffffu, mbar_wait(&empty[e], (fetched / S - 1) & 1))) {
+          dead = true;
+          break;
+        }
+        fetch(fetched++);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / S) & 1))) {
+        dead = true;
+        break;
+      }
+      if (ok[st]) rows.unit(ring + st * C::kUnit, cur.page * kPage - pos, cur.len - cur.page * kPage, lane);
+      __syncwarp();  // the stage is read
+      if (R > 1 && lane == 0) mbar_arrive(&empty[st]);
+      const bool ends = cur.page + 1 == cur.pages;
+      if (ends || i + 1 == n) {  // the tile leaves this stream
+        rows.finish();
+        if (ends && first_page == 0) {
+          rows.store_out(a, cur.b, cur.hk, cur.tile * ROWS + 16 * rw, lane);
+        } else {
+          // an earlier part goes through L2, the last one into the ring once the stream has read it
+          const int slot = i + 1 == n ? 1 : 0;
+          last = slot;
+          if (!slot) {
+            const int e = 2 * stream * ROWS + 16 * rw;
+            rows.store_part(a.part + (size_t)(cta * ST + stream) * C::kRecord + 16 * rw * C::kStride, sh->part_m + e,
+                            sh->part_l + e, C::kStride, lane);
+          }
+          if (rw == 0 && lane == 0) {
+            AtrMeta& mt = sh->meta[2 * stream + slot];
+            mt.seg = cur.seg(a);
+            mt.before = row_at < s0;
+            mt.after = row_at + cur.pages > s1;
+          }
+        }
+        if (i + 1 < n) {
+          cur.next(a, ROWS);
+          first_page = 0;
+          row_at = u0 + i + 1;
+          if (cur.b != tree_b) {
+            tree_b = cur.b;
+            pos = a.g.pos[cur.b];
+            tree_masks(a.g.t.parent + a.g.t.cu[cur.b], atr_nodes(a.g, cur.b), lane, tree);
+          }
+          rows.start(a, cur.b, cur.hk, cur.tile * ROWS + 16 * rw, tree, lane);
+        }
+      } else {
+        ++cur.page;
+      }
+    }
+    if (dead && rw == 0)  // every copy of this stream has landed before the CTA goes on
+      for (int i = max(0, fetched - S); i < fetched; ++i)
+        if (!mbar_drain(&full[i % S], (i / S) & 1)) break;
+  }
+  __syncthreads();  // every ring is read
+  if (last) {
+    const int e = (2 * stream + 1) * ROWS + 16 * rw;
+    rows.store_part(reinterpret_cast<float*>(ring) + 16 * rw * C::kStride, sh->part_m + e, sh->part_l + e, C::kStride, lane);
+  }
+  __syncthreads();
+
+  // ---- tiles cut between streams
+  const int seg_e = lane < PARTS ? sh->meta[lane].seg : -1;
+  const uint32_t same = __match_any_sync(0xffffffffu, seg_e);  // entry `lane`: all parts of its tile
+  const uint32_t lead = __ballot_sync(0xffffffffu, seg_e >= 0 && (same & ((1u << lane) - 1)) == 0);
+  const int ntiles = __popc(lead);
+  {
+    // a thread per (part, row): those of a tile's first part weigh its parts
+    const int e = tid / ROWS, x = tid - e * ROWS;
+    const uint32_t parts = __shfl_sync(0xffffffffu, same, e & 31);
+    if (lead >> e & 1) {
+      float top = -INFINITY, l = 0.0f;
+      for (uint32_t y = parts; y; y &= y - 1) top = fmaxf(top, sh->part_m[(__ffs(y) - 1) * ROWS + x]);
+      for (uint32_t y = parts; y; y &= y - 1) {
+        const int k = (__ffs(y) - 1) * ROWS + x;
+        const float w = ad_weight(sh->part_m[k], sh->part_l[k], top);
+        l += sh->part_l[k] * w;
+        sh->part_m[k] = w;
+      }
+      const int k = __popc(lead & ((1u << e) - 1));
+      sh->row_l[k * ROWS + x] = l;
+      sh->row_parts[k] = parts;
+      const AtrMeta& mt = sh->meta[e];
+      if (mt.before || mt.after) {  // cut between CTAs too
+        float* rec = a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * C::kRecord;
+        rec[x] = top;
+        rec[ROWS + x] = l;
+        if (x == 0) sh->cta_seg[mt.before ? 0 : 1] = mt.seg;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < ntiles * (ROWS * D / 4); i += kAtrThreads) {
+    const int k = i / (ROWS * D / 4), x = i / (D / 4) % ROWS, d = i % (D / 4) * 4;
+    uint32_t parts = sh->row_parts[k];
+    const AtrMeta& mt = sh->meta[__ffs(parts) - 1];
+    uint16_t* out = atr_out(a, mt.seg, x, ROWS, D);
+    if (!out) continue;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    while (parts) {
+      // four parts at a time, their loads together
+      float4 v[4];
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int y = parts ? __ffs(parts) - 1 : -1;
+        parts &= parts - 1;
+        w[j] = 0.0f;
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (y >= 0) {
+          w[j] = sh->part_m[y * ROWS + x];
+          v[j] = y & 1 ? *reinterpret_cast<const float4*>(smem + (y >> 1) * C::kRing + (x * C::kStride + d) * 4)
+                       : *reinterpret_cast<const float4*>(a.part + (size_t)(cta * ST + (y >> 1)) * C::kRecord +
+                                                          x * C::kStride + d);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o.x = fmaf(v[j].x, w[j], o.x), o.y = fmaf(v[j].y, w[j], o.y), o.z = fmaf(v[j].z, w[j], o.z),
+        o.w = fmaf(v[j].w, w[j], o.w);
+    }
+    if (mt.before || mt.after)
+      *reinterpret_cast<float4*>(a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * C::kRecord + 2 * ROWS +
+                                 x * C::kStride + d) = o;
+    else
+      atr_store4(out + d, o, sh->row_l[k * ROWS + x]);
+  }
+  if (tid < 2 && !a.by_row) a.cta_seg[2 * cta + tid] = sh->cta_seg[tid];
+}
+
+// Tiles cut between CTAs: block (c, x) joins row x of the tile that began in span c and
+// goes on.  D/4 threads hold four channels each; the parts are dealt out over groups of
+// them and joined through shared memory.
+constexpr int kAtrcThreads = 128;
+template <int D, int R>
+__global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(const __grid_constant__ AtrArgs a) {
+  using C = AtrCfg<D, R>;
+  constexpr int P = D / 4, GR = kAtrcThreads / P;
+  __shared__ float pm[GR], pl[GR];
+  __shared__ float4 po[kAtrcThreads];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, x = blockIdx.y, tid = threadIdx.x, g = tid / P, d = tid % P * 4;
+  const int seg = a.cta_seg[2 * c + 1];
+  auto load = [&](int y, float& m, float& l, float4& o) {
+    const float* r = a.cta_part + (size_t)(y == 0 ? 2 * c + 1 : 2 * min(c + y, a.nc - 1)) * C::kRecord;
+    m = r[x], l = r[C::kRows + x];
+    o = *reinterpret_cast<const float4*>(r + 2 * C::kRows + x * C::kStride + d);
+  };
+  float m, l;
+  float4 o;
+  load(g, m, l, o);  // (any span's record may be read; how many there are is known next)
+  int k = 1;         // parts: this span's, then those of the spans that the tile goes on through
+  for (int y = c + 1; y < a.nc; y += kAtrcThreads) {
+    const int n = __syncthreads_count(y + tid < a.nc && a.cta_seg[2 * (y + tid)] == seg);
+    k += n;
+    if (n < kAtrcThreads) break;
+  }
+  uint16_t* out = seg < 0 ? nullptr : atr_out(a, seg, x, C::kRows, D);
+  if (!out) return;
+  if (g >= k) m = -INFINITY, l = 0.0f, o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int y = g + GR; y < k; y += GR) {
+    float m1, l1;
+    float4 v;
+    load(y, m1, l1, v);
+    const float top = fmaxf(m, m1), f = ad_weight(m, l, top), w = ad_weight(m1, l1, top);
+    m = top;
+    l = l * f + l1 * w;
+    o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+  }
+  po[tid] = o;
+  if (d == 0) pm[g] = m, pl[g] = l;
+  __syncthreads();
+  if (g == 0) {
+    float top = m, sum = 0.0f;
+#pragma unroll
+    for (int y = 1; y < GR; ++y) top = fmaxf(top, pm[y]);
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int y = 0; y < GR; ++y) {
+      const float w = ad_weight(pm[y], pl[y], top);
+      const float4 v = po[y * P + tid];
+      sum = fmaf(pl[y], w, sum);
+      t = make_float4(fmaf(v.x, w, t.x), fmaf(v.y, w, t.y), fmaf(v.z, w, t.z), fmaf(v.w, w, t.w));
+    }
+    atr_store4(out + d, t, sum);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+template <int D, int R>
+static size_t atr_ws_bytes() {
+  using C = AtrCfg<D, R>;
+  const size_t n = num_sms();
+  return n * (C::kStreams + 2) * C::kRecord * 4 + (n * 2 * 4 + 255) / 256 * 256;
+}
+size_t attn_tree_ws_bytes(int32_t H, int32_t Hkv, int32_t D) {
+  (void)H, (void)Hkv;  // whatever the tile: the largest records
+  return D == 128 ? atr_ws_bytes<128, 4>() : atr_ws_bytes<64, 4>();
+}
+
+template <int D, int R>
+static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
+  using C = AtrCfg<D, R>;
+  static int done_mask[64] = {0};
+  constexpr int smem = C::kStreams * C::kRing + (int)sizeof(AtrShared);
+  static_assert(smem <= 232448, "shared memory");
+  static_assert((C::kStreams + 2) * C::kRecord <= (AtrCfg<D, 4>::kStreams + 2) * AtrCfg<D, 4>::kRecord, "workspace");
+  AtrArgs a;
+  a.g = g;
+  a.G = g.H / g.c.Hkv;
+  a.most_tiles = (g.most * a.G + C::kRows - 1) / C::kRows;
+  const int64_t tiles = (int64_t)g.t.nseq * g.c.Hkv * a.most_tiles;
+  // Few tiles in a narrow table: a CTA takes a whole tile, and nothing is left to
+  // combine.  (The table's width is what the host knows of the lengths.)
+  a.by_row = tiles <= num_sms() && g.c.ld_table <= 32;
+  a.nc = a.by_row ? (int)tiles : num_sms();
+  const size_t n = num_sms();
+  a.cta_seg = static_cast<int32_t*>(g.ws);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.ws) + (n * 2 * 4 + 255) / 256 * 256);
+  a.cta_part = a.part + n * C::kStreams * C::kRecord;
+  auto kern = attn_tree_kernel<D, R>;
+  cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
+  if (e != cudaSuccess) return e;
+  trace_pre(K_ATTN_TREE, s);
+  e = launch_k(kern, dim3(a.nc), dim3(kAtrThreads), smem, s, true, a);
+  trace_post(K_ATTN_TREE, s);
+  if (e != cudaSuccess || a.by_row) return e;
+  trace_pre(K_ATTN_TREE_COMBINE, s);
+  e = launch_k(attn_tree_combine_kernel<D, R>, dim3(a.nc, g.most * a.G < C::kRows ? g.most * a.G : C::kRows),
+               dim3(kAtrcThreads), 0, s, true, a);
+  trace_post(K_ATTN_TREE_COMBINE, s);
+  return e;
+}
+
+cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s) {
+  const int rows = a.most * (a.H / a.c.Hkv);
+  if (a.c.D == 128) return rows <= 16 ? launch_atr<128, 1>(a, s) : rows <= 32 ? launch_atr<128, 2>(a, s) : launch_atr<128, 4>(a, s);
+  return rows <= 16 ? launch_atr<64, 1>(a, s) : rows <= 32 ? launch_atr<64, 2>(a, s) : launch_atr<64, 4>(a, s);
+}
+
+int status_attn_tree(int clear) { return tu_status(clear); }
+cudaError_t wait_limit_attn_tree(long long cycles) { return tu_set_wait_limit(cycles); }
+
+}  // namespace m2

@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "m2_common.cuh"
 #include "m2_kernels.h"
 #include "m2_kv4.cuh"
@@ -432,6 +434,131 @@ cudaError_t launch_kv4_append(const Kv4RowsArgs& a, cudaStream_t s) {
 }
 cudaError_t launch_kv4_gather(const Kv4RowsArgs& a, cudaStream_t s) {
   return launch_rows(kv4_gather_kernel<128>, kv4_gather_kernel<64>, K_KV4_GATHER, a, s);
+}
+
+// ------------------------------------------------------------------ accepted rows moved together
+//
+// A CTA takes one kv head of one sequence: it reads what the accepted nodes' tokens
+// hold into shared memory, then writes it to the tokens that follow the context.  All
+// is read before anything is written, and a page belongs to one sequence, so that no
+// order has to be kept.  Codes and scales are moved as they are.  Entries of the path
+// that stand where they belong (most of them) are not touched.
+// Bound: latency, a launch and two dependent trips to memory.
+constexpr int kKeepThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kKeepThreads) kv4_keep_kernel(const Kv4KeepArgs a) {
+  using L = Kv4Block<D>;
+  constexpr int RUN = D / 8;  // bytes of one r of a token pair's V codes
+  __shared__ __align__(16) uint8_t kc[kTreeNodes][D / 2], vc[kTreeNodes][8][RUN], ks[kTreeNodes][D / 16];
+  __shared__ __align__(16) uint16_t vs[kTreeNodes][D / 32];
+  __shared__ uint8_t* from[kTreeNodes];  // the source's page, null: not moved
+  __shared__ uint8_t* to[kTreeNodes];
+  __shared__ int at[kTreeNodes];
+  __shared__ int lo, hi;
+  const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int first = a.t.cu[i], n = a.t.cu[i + 1] - first, pos = a.pos[i];
+  if (pos < -(1 << 30)) return;  // an idle slot
+  int count = a.count[i];
+  if (count < 0 || count > n) {
+    M2_RECORD_ARG(g_status);
+    count = max(0, min(count, n));
+  }
+  if (tid == 0) lo = kTreeNodes, hi = 0;
+  __syncthreads();
+  if (tid < count) {
+    const int s = a.t.parent[first + tid];
+    auto page = [&](int64_t t) -> uint8_t* {
+      const int64_t pg = t >= 0 ? t / kPage : a.c.ld_table;
+      const int id = pg < a.c.ld_table ? a.c.table[(size_t)i * a.c.ld_table + pg] : -1;
+      return id >= 0 && id < a.c.n_pages ? a.c.pages + ((size_t)id * a.c.Hkv + h) * L::kBytes : nullptr;
+    };
+    from[tid] = nullptr;
+    if (s != tid) {
+      uint8_t* f = s >= 0 && s < n ? page((int64_t)pos + s) : nullptr;
+      uint8_t* d = page((int64_t)pos + tid);
+      if (f && d) {
+        from[tid] = f, to[tid] = d, at[tid] = s;
+        atomicMin(&lo, tid);
+        atomicMax(&hi, tid + 1);
+      } else {
+        M2_RECORD_ARG(g_status);
+      }
+    }
+  }
+  __syncthreads();
+  const int j0 = lo, moved = hi - lo;
+  if (moved <= 0) return;
+  using Run = typename std::conditional<D == 128, uint4, uint2>::type;
+  auto nibbles = [](Run v, int odd) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int k = 0; k < RUN / 4; ++k) w[k] = (w[k] >> (4 * odd)) & 0x0F0F0F0Fu;
+    return v;
+  };
+  // V codes: 8 runs a token; K codes: D / 32 pieces of 16 bytes; scales: one piece
+  constexpr int PIECES = 8 + D / 32 + 1;
+  for (int k = tid; k < moved * PIECES; k += kKeepThreads) {
+    const int j = j0 + k / PIECES, e = k % PIECES;
+    const uint8_t* f = from[j];
+    if (!f) continue;
+    const int t = (int)(((int64_t)pos + at[j]) % kPage);
+    if (e < 8) {
+      *reinterpret_cast<Run*>(vc[j][e]) = nibbles(*reinterpret_cast<const Run*>(f + L::v(t, 0, e)), t & 1);
+    } else if (e < PIECES - 1) {
+      reinterpret_cast<uint4*>(kc[j])[e - 8] = reinterpret_cast<const uint4*>(f + L::k(t, 0, 0))[e - 8];
+    } else {
+#pragma unroll
+      for (int g = 0; g < D / 16; g += 4)
+        *reinterpret_cast<uint32_t*>(ks[j] + g) = *reinterpret_cast<const uint32_t*>(f + L::ks(t, g));
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) vs[j][g] = *reinterpret_cast<const uint16_t*>(f + L::vs(t, 2 * g));
+    }
+  }
+  __syncthreads();
+  // the tokens written come in pairs that share V bytes: pair k holds tokens 2k and 2k + 1
+  const int64_t pair0 = ((int64_t)pos + j0) >> 1;
+  const int pairs = (int)((((int64_t)pos + j0 + moved - 1) >> 1) - pair0) + 1;
+  for (int k = tid; k < pairs * 8; k += kKeepThreads) {
+    const int e = k % 8, je = (int)(2 * (pair0 + k / 8) - pos);  // path entries of the even token, and the odd one
+    const bool even = je >= j0 && je < j0 + moved && from[je], odd = je + 1 >= j0 && je + 1 < j0 + moved && from[je + 1];
+    if (!even && !odd) continue;
+    uint8_t* d = (even ? to[je] : to[je + 1]) + L::v((int)((2 * (pair0 + k / 8)) % kPage), 0, e);
+    Run v = *reinterpret_cast<const Run*>(d);
+    Run x = even ? *reinterpret_cast<const Run*>(vc[je][e]) : nibbles(v, 0);
+    Run y = odd ? *reinterpret_cast<const Run*>(vc[je + 1][e]) : nibbles(v, 1);
+    uint32_t *w = reinterpret_cast<uint32_t*>(&v), *wx = reinterpret_cast<uint32_t*>(&x), *wy = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+    for (int q = 0; q < RUN / 4; ++q) w[q] = wx[q] | wy[q] << 4;
+    *reinterpret_cast<Run*>(d) = v;
+  }
+  constexpr int ROWS = D / 32 + 1;
+  for (int k = tid; k < moved * ROWS; k += kKeepThreads) {
+    const int j = j0 + k / ROWS, e = k % ROWS;
+    if (!from[j]) continue;
+    uint8_t* d = to[j];
+    const int t = (int)(((int64_t)pos + j) % kPage);
+    if (e < ROWS - 1) {
+      reinterpret_cast<uint4*>(d + L::k(t, 0, 0))[e] = reinterpret_cast<const uint4*>(kc[j])[e];
+    } else {
+#pragma unroll
+      for (int g = 0; g < D / 16; g += 4)
+        *reinterpret_cast<uint32_t*>(d + L::ks(t, g)) = *reinterpret_cast<const uint32_t*>(ks[j] + g);
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) *reinterpret_cast<uint16_t*>(d + L::vs(t, 2 * g)) = vs[j][g];
+    }
+  }
+}
+
+cudaError_t launch_kv4_keep(const Kv4KeepArgs& a, cudaStream_t s) {
+  const dim3 grid(a.c.Hkv, a.t.nseq), block(kKeepThreads);
+  trace_pre(K_KV4_KEEP, s);
+  const cudaError_t e = a.c.D == 128 ? launch_k(kv4_keep_kernel<128>, grid, block, 0, s, true, a)
+                                     : launch_k(kv4_keep_kernel<64>, grid, block, 0, s, true, a);
+  trace_post(K_KV4_KEEP, s);
+  return e;
 }
 
 int status_kv4(int clear) { return tu_status(clear); }

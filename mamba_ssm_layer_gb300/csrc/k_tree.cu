@@ -1,0 +1,597 @@
+// k_tree.cu -- the Mamba-2 mixer over trees of drafted tokens: the causal conv, the
+// SSM outputs of every node without touching the state, and the move of state, conv
+// ring and position along the accepted path (include/mamba2.h has the formulas).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "m2_common.cuh"
+#include "m2_kernels.h"
+#include "m2_tree.cuh"
+
+namespace m2 {
+
+// ------------------------------------------------------------------ conv
+//
+// A thread takes VEC channels of one node.  The node's window is the last rows of
+// its path (the set bits of its mask, from the top), then the ring from the newest
+// token back.  Sums run as the single-token conv's, oldest tap first; products of
+// two bf16 values are exact, so the results are the same bits.
+constexpr int kTcThreads = 128;
+
+template <int K, int VEC>
+__global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const TreeConvArgs a) {
+  constexpr int L = K - 1;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, row = blockIdx.y;
+  const int i = tree_seq(a.t, row), first = a.t.cu[i], n = a.t.cu[i + 1] - first;
+  uint64_t m[2];
+  tree_masks(a.t.parent + first, n, lane, m);
+  uint64_t path = tree_mask_of(m, row - first);
+  const int c = (blockIdx.x * kTcThreads + threadIdx.x) * VEC;
+  if (c >= a.C) return;
+  uint16_t* out = a.out + (size_t)row * a.ld_o + c;
+  if (path == 0) {  // not part of the tree
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = 0;
+    return;
+  }
+  const uint16_t* tap[K];  // oldest first
+  int back = 0;
+  const int pos = a.pos[i];
+#pragma unroll
+  for (int j = L; j >= 0; --j) {
+    if (path) {
+      const int at = 63 - __clzll((long long)path);
+      path &= ~(1ull << at);
+      tap[j] = a.x + (size_t)(first + at) * a.ld_x + c;
+    } else {
+      ++back;
+      const int slot = ((pos - back) % L + L) % L;
+      tap[j] = a.ring + ((size_t)i * L + slot) * a.C + c;
+    }
+  }
+  float s[VEC];
+  if constexpr (VEC == 8) {
+    uint4 v[K], w[K];
+    uint4 b = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      v[j] = *reinterpret_cast<const uint4*>(tap[j]);
+      w[j] = *reinterpret_cast<const uint4*>(a.w + (size_t)c * K + 8 * j);  // 16 * K bytes: 8 channels' taps
+    }
+    if (a.bias) b = *reinterpret_cast<const uint4*>(a.bias + c);
+    auto half = [](const uint4& x, int e) {
+      const uint32_t u = e < 4 ? (e < 2 ? x.x : x.y) : (e < 6 ? x.z : x.w);
+      return e & 1 ? bf16hi(u) : bf16lo(u);
+    };
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[e] = half(b, e);
+#pragma unroll
+      for (int j = 0; j < K; ++j) s[e] = fmaf(half(w[(e * K + j) / 8], (e * K + j) % 8), half(v[j], e), s[e]);
+      if (a.silu) s[e] = silu_f(s[e]);
+    }
+    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
+                                                pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+  } else {
+    s[0] = a.bias ? bf16_to_f32(a.bias[c]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) s[0] = fmaf(bf16_to_f32(a.w[(size_t)c * K + j]), bf16_to_f32(*tap[j]), s[0]);
+    *out = f32_to_bf16(a.silu ? silu_f(s[0]) : s[0]);
+  }
+}
+
+template <int VEC>
+static cudaError_t launch_tree_conv_v(const TreeConvArgs& a, cudaStream_t s) {
+  const dim3 grid((a.C + kTcThreads * VEC - 1) / (kTcThreads * VEC), a.t.cu[a.t.nseq]), block(kTcThreads);
+  switch (a.dconv) {
+    case 2: return launch_k(tree_conv_kernel<2, VEC>, grid, block, 0, s, true, a);
+    case 3: return launch_k(tree_conv_kernel<3, VEC>, grid, block, 0, s, true, a);
+    case 4: return launch_k(tree_conv_kernel<4, VEC>, grid, block, 0, s, true, a);
+    case 5: return launch_k(tree_conv_kernel<5, VEC>, grid, block, 0, s, true, a);
+    case 6: return launch_k(tree_conv_kernel<6, VEC>, grid, block, 0, s, true, a);
+    case 7: return launch_k(tree_conv_kernel<7, VEC>, grid, block, 0, s, true, a);
+    default: return launch_k(tree_conv_kernel<8, VEC>, grid, block, 0, s, true, a);
+  }
+}
+
+cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
+  trace_pre(K_TREE_CONV, s);
+  const cudaError_t e = a.wide ? launch_tree_conv_v<8>(a, s) : launch_tree_conv_v<1>(a, s);
+  trace_post(K_TREE_CONV, s);
+  return e;
+}
+
+// ------------------------------------------------------------------ SSM outputs
+//
+// With la_j = dt_j A, s_i = the sum of la over node i's path and h the sequence's
+// state (which is only read),
+//   y_i = e^{s_i} C_i h^T + sum_{j on i's path} e^{s_i - s_j} dt_j (C_i . B_j) x_j + D x_i,
+// three products on warp MMA (m16n8k16, bf16, fp32 sums): nodes are the rows,
+//   C h^T    k = states, columns = channels p; a warp takes 8 channels, whose state
+//            rows it loads straight into the operand's layout (a lane's four
+//            consecutive states stand at k = 2c, 2c+1, 2c+8, 2c+9; C is read in the
+//            same order)
+//   C B^T    once for the heads of a group
+//   L x      L the masked, decayed C B^T times dt
+// h and L are fp32 and enter as three bf16 terms each, which hold all 24 bits; the
+// smaller two have sums of their own.  s is a pair of floats (64 nodes of a chain
+// would cost its differences their last bits).
+// Values of x that are not finite would reach nodes beside their path as 0 * Inf: they
+// are 0 in the product, and the nodes below them add them when they store.
+// Bound: HBM, the state read once (32 KB a head of 64 x 128), up to 16 nodes; with 64
+// nodes the tensor cores' legacy rate is as near.
+constexpr int kTsThreads = 256, kTsWarps = kTsThreads / 32;
+
+template <int N, int MT>
+struct TsCfg {
+  static constexpr int kNodes = 16 * MT;
+  static constexpr int kRow = N + 16;        // bf16 elements between rows of the C and B tiles: no bank conflicts
+  static constexpr int kCb = kNodes + 4;     // floats between rows of C B^T
+  static constexpr int kL = kNodes + 8;      // bf16 elements between rows of L
+};
+// Shared memory of a CTA: masks, C and B tiles, C B^T, the heads' dt and s, then for
+// one head at a time L's three terms and x.
+template <int N, int MT>
+__host__ __device__ constexpr int ts_x_stride(int P) {
+  return (P + 7) / 8 * 8 + 8;
+}
+template <int N, int MT>
+__host__ __device__ inline int ts_smem_bytes(int P, int heads) {
+  using C = TsCfg<N, MT>;
+  return C::kNodes * 8 + 16 + 2 * C::kNodes * C::kRow * 2 + C::kNodes * C::kCb * 4 + heads * C::kNodes * 12 +
+         3 * C::kNodes * C::kL * 2 + C::kNodes * ts_x_stride<N, MT>(P) * 2;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_addr(p))
+               : "memory");
+}
+__device__ __forceinline__ void ldsm2_trans(uint32_t& r0, uint32_t& r1, const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(smem_addr(p))
+               : "memory");
+}
+// Two floats as three pairs of bf16 whose sum they are (all 24 bits).
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16x2(a, b);
+  const float a1 = a - bf16lo(hi), b1 = b - bf16hi(hi);
+  mid = pack_bf16x2(a1, b1);
+  lo = pack_bf16x2(a1 - bf16lo(mid), b1 - bf16hi(mid));
+}
+
+template <int N, int MT>
+__global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(const TreeSsmArgs a, int heads, int chunks) {
+  using Cf = TsCfg<N, MT>;
+  constexpr int KS = N / 16, NODES = Cf::kNodes;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int xs = ts_x_stride<N, MT>(a.P);
+  uint64_t* mask = reinterpret_cast<uint64_t*>(smem);
+  unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);  // nodes with such x, heads in turn
+  uint16_t* ct = reinterpret_cast<uint16_t*>(bad + 2);
+  uint16_t* bt = ct + NODES * Cf::kRow;
+  uint16_t* lt = bt + NODES * Cf::kRow;  // L's terms
+  uint16_t* xt = lt + 3 * NODES * Cf::kL;
+  float* cb = reinterpret_cast<float*>(xt + NODES * xs);
+  float* sdt = cb + NODES * Cf::kCb;     // [heads][NODES]
+  float* shi = sdt + heads * NODES;
+  float* slo = shi + heads * NODES;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  const int i = blockIdx.y, g = blockIdx.x / chunks, per = a.H / a.G;
+  const int h0 = g * per + (blockIdx.x - g * chunks) * heads, nh = min(heads, (g + 1) * per - h0);
+  const int first = a.t.cu[i], n = a.t.cu[i + 1] - first;
+  pdl_wait();
+  pdl_trigger();
+  if (n == 0) return;
+  // this warp's tiles of 8 channels, heads one after the other: the state of the next one is on its way
+  const int pt = (a.P + 7) / 8, mine = warp < pt ? (pt - warp + kTsWarps - 1) / kTsWarps : 0;
+  const float* hb = a.h + ((size_t)i * a.H + h0) * a.P * N;
+  float4 hv[KS];
+  auto load = [&](int head, int k) {
+    const int p = (warp + k * kTsWarps) * 8 + r;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      hv[ks] = p < a.P ? *reinterpret_cast<const float4*>(hb + ((size_t)head * a.P + p) * N + 16 * ks + 4 * c)
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  if (mine) load(0, 0);
+  // ---- masks, C and B rows, dt and the decays' sums
+  if (warp == 0) {
+    uint64_t m[2];
+    tree_masks(a.t.parent + first, n, lane, m);
+    if (lane < NODES) mask[lane] = m[0];
+    if (MT == 4) mask[lane + 32] = m[1];
+    if (lane < 2) bad[lane] = 0ull;
+  }
+  for (int k = tid; k < NODES * (N / 4); k += kTsThreads) {
+    const int j = k / (N / 4), e = k % (N / 4) * 4;
+    uint2 vc = make_uint2(0u, 0u), vb = vc;
+    if (j < n) {
+      vc = *reinterpret_cast<const uint2*>(a.Cm + (size_t)(first + j) * a.ld_in + (size_t)g * N + e);
+      vb = *reinterpret_cast<const uint2*>(a.Bm + (size_t)(first + j) * a.ld_in + (size_t)g * N + e);
+    }
+    *reinterpret_cast<uint2*>(ct + j * Cf::kRow + e) = vc;
+    *reinterpret_cast<uint2*>(bt + j * Cf::kRow + e) = vb;
+  }
+  for (int k = tid; k < nh * NODES; k += kTsThreads) {
+    const int head = k / NODES, j = k % NODES;
+    float dt = 0.0f, la = 0.0f;
+    if (j < n) {
+      const float A = -expf(a.A_log[h0 + head]);
+      dt = softplus_f(bf16_to_f32(a.dt[(size_t)(first + j) * a.ld_dt + h0 + head]) + a.dt_bias[h0 + head]);
+      dt = fminf(fmaxf(dt, 1e-9f), 1e9f);
+      la = dt * A;
+    }
+    sdt[k] = dt;
+    shi[k] = la;
+  }
+  __syncthreads();
+  // sums along the paths; all of them read before any is written
+  constexpr int ROUNDS = 4;  // of 256 (head, node) pairs: the host keeps heads * NODES within 1024
+  float th[ROUNDS], tl[ROUNDS];
+#pragma unroll
+  for (int q = 0; q < ROUNDS; ++q) {
+    const int k = tid + q * kTsThreads;
+    th[q] = tl[q] = 0.0f;
+    if (k < nh * NODES)
+      for (uint64_t m = mask[k % NODES]; m; m &= m - 1)
+        two_sum_acc(th[q], tl[q], shi[k / NODES * NODES + __ffsll((long long)m) - 1]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < ROUNDS; ++q) {
+    const int k = tid + q * kTsThreads;
+    if (k < nh * NODES) shi[k] = th[q], slo[k] = tl[q];
+  }
+  // ---- C B^T
+  for (int k = warp; k < MT * 2 * MT; k += kTsWarps) {
+    const int mt = k / (2 * MT), nt = k % (2 * MT);
+    if (nt > 2 * mt + 1) continue;  // above the diagonal: no node stands above one before it
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint2 a0 = *reinterpret_cast<const uint2*>(ct + (16 * mt + r) * Cf::kRow + 16 * ks + 4 * c);
+      const uint2 a1 = *reinterpret_cast<const uint2*>(ct + (16 * mt + 8 + r) * Cf::kRow + 16 * ks + 4 * c);
+      const uint2 b = *reinterpret_cast<const uint2*>(bt + (8 * nt + r) * Cf::kRow + 16 * ks + 4 * c);
+      mma_bf16(acc, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+    }
+    float* d = cb + (16 * mt + r) * Cf::kCb + 8 * nt + 2 * c;
+    *reinterpret_cast<float2*>(d) = make_float2(acc[0], acc[1]);
+    *reinterpret_cast<float2*>(d + 8 * Cf::kCb) = make_float2(acc[2], acc[3]);
+  }
+  __syncthreads();
+  for (int head = 0; head < nh; ++head) {
+    const int h = h0 + head;
+    const float* dt_h = sdt + head * NODES;
+    const float* hi_h = shi + head * NODES;
+    const float* lo_h = slo + head * NODES;
+    // ---- L and x of the head (pairs of columns: a bf16x2 word)
+    for (int k = tid; k < NODES * (NODES / 2); k += kTsThreads) {
+      const int row = k / (NODES / 2), col = k % (NODES / 2) * 2;
+      const uint64_t m = mask[row];
+      float v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v[e] = 0.0f;
+        if (m >> (col + e) & 1) {
+          const float d = (hi_h[row] - hi_h[col + e]) + (lo_h[row] - lo_h[col + e]);
+          v[e] = expf(d) * dt_h[col + e] * cb[row * Cf::kCb + col + e];
+        }
+      }
+      uint32_t w0, w1, w2;
+      split3(v[0], v[1], w0, w1, w2);
+      uint32_t* d = reinterpret_cast<uint32_t*>(lt + row * Cf::kL + col);
+      constexpr int T = NODES * Cf::kL / 2;  // words of a term
+      d[0] = w0, d[T] = w1, d[2 * T] = w2;
+    }
+    // (halves with all exponent bits set are infinities and NaN)
+    auto finite = [](uint32_t w) {
+      if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+      if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+      return w;
+    };
+    const int q2 = xs / (a.wide_x ? 4 : 1);
+    for (int k = tid; k < NODES * q2; k += kTsThreads) {
+      const int j = k / q2, q = k - j * q2;
+      const bool in = mask[j] != 0;  // (0 for nodes past the last one too)
+      if (a.wide_x) {
+        uint2 v = make_uint2(0u, 0u);
+        if (in && 4 * q < a.P)
+          v = *reinterpret_cast<const uint2*>(a.x + (size_t)(first + j) * a.ld_in + (size_t)h * a.P + 4 * q);
+        const uint2 f = make_uint2(finite(v.x), finite(v.y));
+        if (f.x != v.x || f.y != v.y) atomicOr(&bad[head & 1], 1ull << j);
+        *reinterpret_cast<uint2*>(xt + j * xs + 4 * q) = f;
+      } else {
+        const uint32_t v = in && q < a.P ? a.x[(size_t)(first + j) * a.ld_in + (size_t)h * a.P + q] : 0u;
+        const uint32_t f = finite(v);
+        if (f != v) atomicOr(&bad[head & 1], 1ull << j);
+        xt[j * xs + q] = (uint16_t)f;
+      }
+    }
+    __syncthreads();
+    const float Dh = a.D[h];
+    const uint64_t odd = bad[head & 1];
+    if (tid == 0) bad[(head + 1) & 1] = 0ull;
+    for (int k = 0; k < mine; ++k) {
+      const int p0 = (warp + k * kTsWarps) * 8;
+      float acc[MT][4], low[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] = low[mt][e] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t b0[3], b1[3];
+        split3(hv[ks].x, hv[ks].y, b0[0], b0[1], b0[2]);
+        split3(hv[ks].z, hv[ks].w, b1[0], b1[1], b1[2]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint2 a0 = *reinterpret_cast<const uint2*>(ct + (16 * mt + r) * Cf::kRow + 16 * ks + 4 * c);
+          const uint2 a1 = *reinterpret_cast<const uint2*>(ct + (16 * mt + 8 + r) * Cf::kRow + 16 * ks + 4 * c);
+          mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[2], b1[2]);
+          mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[1], b1[1]);
+          mma_bf16(acc[mt], a0.x, a1.x, a0.y, a1.y, b0[0], b1[0]);
+        }
+      }
+      // the next tile's state
+      if (k + 1 < mine)
+        load(head, k + 1);
+      else if (head + 1 < nh)
+        load(head + 1, 0);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r0 = 16 * mt + r;
+        const float e0 = expf(hi_h[r0] + lo_h[r0]), e1 = expf(hi_h[r0 + 8] + lo_h[r0 + 8]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[mt][e] = (acc[mt][e] + low[mt][e]) * (e < 2 ? e0 : e1);
+          low[mt][e] = 0.0f;
+        }
+        float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks <= mt; ++ks) {
+          uint32_t b0, b1;
+          ldsm2_trans(b0, b1, xt + (16 * ks + (lane & 15)) * xs + p0);
+#pragma unroll
+          for (int t = 2; t >= 0; --t) {
+            uint32_t l[4];
+            ldsm4(l, lt + t * NODES * Cf::kL + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8);
+            if (t)
+              mma_bf16(low[mt], l[0], l[1], l[2], l[3], b0, b1);
+            else
+              mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = r0 + 8 * e, p = p0 + 2 * c;
+          if (j >= n || p >= a.P) continue;
+          const uint64_t m = mask[j];
+          const uint32_t xw = *reinterpret_cast<const uint32_t*>(xt + j * xs + p);
+          float y[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            y[f] = m ? (acc[mt][2 * e + f] + (top[2 * e + f] + low[mt][2 * e + f])) + Dh * (f ? bf16hi(xw) : bf16lo(xw)) : 0.0f;
+            for (uint64_t o = m & odd; o; o &= o - 1) {
+              const int at = __ffsll((long long)o) - 1;
+              if (p + f >= a.P) continue;
+              const float v = bf16_to_f32(a.x[(size_t)(first + at) * a.ld_in + (size_t)h * a.P + p + f]);
+              if (isfinite(v)) continue;
+              float l = 0.0f;
+              for (int t = 2; t >= 0; --t) l += bf16_to_f32(lt[t * NODES * Cf::kL + j * Cf::kL + at]);
+              y[f] += (at == j ? l + Dh : l) * v;
+            }
+          }
+          const float y0 = y[0], y1 = y[1];
+          float* d = a.y + (size_t)(first + j) * a.H * a.P + (size_t)h * a.P + p;
+          if (a.P % 2 == 0) {
+            *reinterpret_cast<float2*>(d) = make_float2(y0, y1);
+          } else {
+            d[0] = y0;
+            if (p + 1 < a.P) d[1] = y1;
+          }
+        }
+      }
+    }
+    __syncthreads();  // L and x are written anew
+  }
+}
+
+template <int N, int MT>
+static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
+  static int done_mask[64] = {0};
+  const int per = a.H / a.G;
+  // Heads of a CTA: C, B and their product serve all of them; halved until the
+  // CTAs fill the SMs twice.  heads * nodes stays within the path sums' 1024 pairs.
+  int heads = per < 16 ? per : 16;
+  while (heads > 1 && (heads * 16 * MT > 1024 ||
+                       (int64_t)a.t.nseq * a.G * ((per + heads - 1) / heads) < 4ll * num_sms()))
+    heads = (heads + 1) / 2;
+  const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
+  auto k = tree_ssm_kernel<N, MT>;
+  cudaError_t e = set_smem_once((const void*)k, smem, done_mask);
+  if (e != cudaSuccess) return e;
+  return launch_k(k, dim3(a.G * chunks, a.t.nseq), dim3(kTsThreads), smem, s, true, a, heads, chunks);
+}
+template <int N>
+static cudaError_t launch_tree_ssm_m(const TreeSsmArgs& a, int most, cudaStream_t s) {
+  return most <= 16 ? launch_tree_ssm_n<N, 1>(a, s) : most <= 32 ? launch_tree_ssm_n<N, 2>(a, s) : launch_tree_ssm_n<N, 4>(a, s);
+}
+
+cudaError_t launch_tree_ssm(const TreeSsmArgs& a, cudaStream_t s) {
+  int most = 0;
+  for (int i = 0; i < a.t.nseq; ++i) most = a.t.cu[i + 1] - a.t.cu[i] > most ? a.t.cu[i + 1] - a.t.cu[i] : most;
+  cudaError_t e;
+  trace_pre(K_TREE_SSM, s);
+  switch (a.N) {
+    case 16: e = launch_tree_ssm_m<16>(a, most, s); break;
+    case 32: e = launch_tree_ssm_m<32>(a, most, s); break;
+    case 64: e = launch_tree_ssm_m<64>(a, most, s); break;
+    default: e = launch_tree_ssm_m<128>(a, most, s); break;
+  }
+  trace_post(K_TREE_SSM, s);
+  return e;
+}
+
+// ------------------------------------------------------------------ commit
+//
+// Two launches.  The ring's kernel comes first: the conv of a decode step reads ring
+// and position while the launch before it may still run, and that launch is then the
+// state's kernel, which starts its successor only after the ring's has ended.
+// A sequence's ring is moved by a cluster, so that the position is stored (perhaps in
+// place) after every CTA has read it.
+
+// Accepted nodes of sequence i, within its tree.
+__device__ __forceinline__ int tree_count(const TreeArgs& t, const int32_t* count, int i) {
+  const int n = t.cu[i + 1] - t.cu[i], k = count[i];
+  if (k < 0 || k > n) atomicCAS(&g_status, 0, -1);
+  return max(0, min(k, n));
+}
+// Row of the path's entry j, or -1 (reported) if it names no node.
+__device__ __forceinline__ int tree_path_row(const TreeArgs& t, int i, int j) {
+  const int first = t.cu[i], at = t.parent[first + j];
+  if (at >= 0 && at < t.cu[i + 1] - first) return first + at;
+  atomicCAS(&g_status, 0, -1);
+  return -1;
+}
+
+constexpr int kTrThreads = 256, kTrCtas = 8;
+
+template <int VEC>
+__global__ void __launch_bounds__(kTrThreads) __cluster_dims__(kTrCtas, 1, 1) tree_ring_kernel(const TreeCommitArgs a) {
+  using T = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.y, L = a.dconv - 1, C = a.H * a.P + 2 * a.G * a.N;
+  const int n = tree_count(a.t, a.count, i), pos = a.pos[i];
+  const uint16_t* in = a.ring + (size_t)i * L * C;
+  uint16_t* out = a.ring_out + (size_t)i * L * C;
+  for (int c = (blockIdx.x * kTrThreads + threadIdx.x) * VEC; c < C; c += kTrCtas * kTrThreads * VEC) {
+    for (int slot = 0; slot < L; ++slot) {
+      // the newest token of the path in this slot: the last j < n with (pos + j) % L == slot
+      const int p = ((pos + n - 1 - slot) % L + L) % L, j = n - 1 - p;
+      const int row = j >= 0 ? tree_path_row(a.t, i, j) : -1;
+      if (row >= 0)
+        *reinterpret_cast<T*>(out + (size_t)slot * C + c) = *reinterpret_cast<const T*>(a.xbc + (size_t)row * a.ld_xbc + c);
+      else if (in != out)
+        *reinterpret_cast<T*>(out + (size_t)slot * C + c) = *reinterpret_cast<const T*>(in + (size_t)slot * C + c);
+    }
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.pos_out[i] = pos + n;
+}
+
+__device__ __forceinline__ float4 tc_bf4(const uint16_t* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
+}
+
+// The steps of the single-token kernel, in its order and arithmetic, with the state
+// in registers: LPR = N/4 lanes a row, ROWS rows a thread.
+// Bound: HBM, the state read and written once.
+template <int LPR, int ROWS>
+__global__ void __launch_bounds__(256) tree_state_kernel(const TreeCommitArgs a, int psplit) {
+  constexpr int RPW = 32 / LPR, CTA_ROWS = 8 * RPW * ROWS;
+  __shared__ float sdt[kTreeNodes], sda[kTreeNodes];
+  __shared__ int srow[kTreeNodes];
+  const int i = blockIdx.y, h = blockIdx.x / psplit, pc = blockIdx.x % psplit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n4 = (lane % LPR) * 4, g = h / (a.H / a.G);
+  const size_t base = ((size_t)i * a.H + h) * a.P * a.N;
+  const int p0 = pc * CTA_ROWS + warp * RPW + lane / LPR;
+  pdl_wait();
+  pdl_trigger();
+  float4 hv[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int p = p0 + k * 8 * RPW;
+    if (p < a.P) hv[k] = *reinterpret_cast<const float4*>(a.h + base + (size_t)p * a.N + n4);
+  }
+  const int n = tree_count(a.t, a.count, i);
+  if (threadIdx.x < n) {
+    const int row = tree_path_row(a.t, i, threadIdx.x);
+    float dt = 0.0f, da = 1.0f;
+    if (row >= 0) ssm_dt_dA(bf16_to_f32(a.dt[(size_t)row * a.ld_dt + h]), a.dt_bias[h], a.A_log[h], dt, da);
+    srow[threadIdx.x] = row;
+    sdt[threadIdx.x] = dt;
+    sda[threadIdx.x] = da;
+  }
+  __syncthreads();
+  const uint16_t* ub = a.u + (size_t)a.H * a.P + (size_t)g * a.N + n4;
+  const uint16_t* ux = a.u + (size_t)h * a.P;
+  for (int j = 0; j < n; ++j) {
+    const int row = srow[j];
+    if (row < 0) continue;
+    const float dt = sdt[j], dA = sda[j];
+    const float4 Bv = tc_bf4(ub + (size_t)row * a.ld_u);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int p = p0 + k * 8 * RPW;
+      if (p < a.P) {
+        const float dtx = dt * bf16_to_f32(ux[(size_t)row * a.ld_u + p]);
+        hv[k].x = fmaf(dA, hv[k].x, dtx * Bv.x);
+        hv[k].y = fmaf(dA, hv[k].y, dtx * Bv.y);
+        hv[k].z = fmaf(dA, hv[k].z, dtx * Bv.z);
+        hv[k].w = fmaf(dA, hv[k].w, dtx * Bv.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int p = p0 + k * 8 * RPW;
+    if (p < a.P) *reinterpret_cast<float4*>(a.h_out + base + (size_t)p * a.N + n4) = hv[k];
+  }
+}
+
+template <int LPR>
+static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
+  constexpr int RPW = 32 / LPR;
+  const int64_t heads = (int64_t)a.t.nseq * a.H;
+  const int max_rows = (a.P + 8 * RPW - 1) / (8 * RPW);
+  // rows a thread: doubled while the grid has more CTAs than four an SM
+  int rows = 1;
+  while (rows < 8 && rows < max_rows && heads * ((a.P + 8 * RPW * rows - 1) / (8 * RPW * rows)) > 4ll * num_sms()) rows *= 2;
+  const int psplit = (a.P + 8 * RPW * rows - 1) / (8 * RPW * rows);
+  const dim3 grid(a.H * psplit, a.t.nseq), block(256);
+  switch (rows) {
+    case 1: return launch_k(tree_state_kernel<LPR, 1>, grid, block, 0, s, true, a, psplit);
+    case 2: return launch_k(tree_state_kernel<LPR, 2>, grid, block, 0, s, true, a, psplit);
+    case 4: return launch_k(tree_state_kernel<LPR, 4>, grid, block, 0, s, true, a, psplit);
+    default: return launch_k(tree_state_kernel<LPR, 8>, grid, block, 0, s, true, a, psplit);
+  }
+}
+
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
+  const dim3 grid(kTrCtas, a.t.nseq), block(kTrThreads);
+  trace_pre(K_TREE_RING, s);
+  cudaError_t e = a.wide ? launch_k(tree_ring_kernel<8>, grid, block, 0, s, true, a)
+                         : launch_k(tree_ring_kernel<1>, grid, block, 0, s, true, a);
+  trace_post(K_TREE_RING, s);
+  if (e != cudaSuccess) return e;
+  trace_pre(K_TREE_STATE, s);
+  switch (a.N / 4) {
+    case 4: e = launch_tree_state<4>(a, s); break;
+    case 8: e = launch_tree_state<8>(a, s); break;
+    case 16: e = launch_tree_state<16>(a, s); break;
+    default: e = launch_tree_state<32>(a, s); break;
+  }
+  trace_post(K_TREE_STATE, s);
+  return e;
+}
+
+int status_tree(int clear) { return tu_status(clear); }
+
+}  // namespace m2

@@ -1,0 +1,343 @@
+// k_verify.cu -- verification of drafted tokens (include/mamba2.h has the rule).
+//
+// The walk itself is a few comparisons; what takes time is a row of the target (and of
+// the draft): one for the token that the walk ends on, one for every sibling that is
+// asked after a refusal.  A cluster of 8 CTAs takes a sequence, its CTAs and their warps
+// consecutive runs of the vocabulary.  The probabilities that the walk asks for are
+// gathered at the start; the first CTA walks until it needs a sum
+//   S = sum_t R(t),  R = max(p - c q, 0)
+// and tells the others the row and c.  The last sum's parts, by CTA and warp, say which
+// warp's run the random number falls into; that warp reads it again, from L2.
+// A refusal takes S q from what remains, so that c grows by S: R never has to be
+// stored, whatever the number of refusals.
+// R and its sums are pairs of floats (about 2^-46 of the sum; fp64 adds are slow here),
+// comparisons fp64: a sum in fp32 would move one drawn token in some thousand.
+// Bound: HBM, the rows once.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "m2_common.cuh"
+#include "m2_kernels.h"
+#include "m2_tree.cuh"
+
+namespace m2 {
+
+constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32, kVfCtas = 8;
+
+enum { VF_SUM = 0, VF_DRAW = 1 };
+struct VfCmd {
+  int32_t what, cur;
+  float c_hi, c_lo;
+  int32_t gone;      // refused tokens, where there is no draft row: their number
+};
+struct VfShared {
+  float tot_hi[2][kVfCtas], tot_lo[2][kVfCtas];  // the CTAs' sums, passes in turn
+  VfCmd cmd;
+  int32_t gone_tok[kTreeNodes];
+  float hi[kVfWarps], lo[kVfWarps];
+  int32_t parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
+  float u[kTreeNodes], p[kTreeNodes], q[kTreeNodes];
+  int32_t count;     // accepted nodes so far (first CTA)
+  int32_t warp;      // drawing: the run, and what lies before it
+  double before;
+};
+
+// Probabilities that are not positive numbers count as 0.
+__device__ __forceinline__ float vf_clean(float x) { return x > 0.0f && x < INFINITY ? x : 0.0f; }
+template <bool BF>
+__device__ __forceinline__ float vf_one(const void* row, int64_t at) {
+  return vf_clean(BF ? bf16_to_f32(static_cast<const uint16_t*>(row)[at]) : static_cast<const float*>(row)[at]);
+}
+// Four of a row from element `at` on; past the end 0.  wide: they can be read at once.
+template <bool BF>
+__device__ __forceinline__ float4 vf_four(const void* row, int at, int V, bool wide) {
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (wide && at + 4 <= V) {
+    if (BF) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + at);
+      v = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+    } else {
+      v = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + at);
+    }
+    return make_float4(vf_clean(v.x), vf_clean(v.y), vf_clean(v.z), vf_clean(v.w));
+  }
+  if (at < V) v.x = vf_one<BF>(row, at);
+  if (at + 1 < V) v.y = vf_one<BF>(row, at + 1);
+  if (at + 2 < V) v.z = vf_one<BF>(row, at + 2);
+  if (at + 3 < V) v.w = vf_one<BF>(row, at + 3);
+  return v;
+}
+// (hi, lo) += R of one token.
+__device__ __forceinline__ void vf_add(float& hi, float& lo, float p, float q, float c_hi, float c_lo) {
+  const float t = c_hi * q, e = fmaf(c_hi, q, -t) + c_lo * q;  // c q = t + e
+  const float s = p - t, b = s - p;
+  const float d = ((p - (s - b)) - (t + b)) - e;               // p - c q = s + d
+  if (s + d > 0.0f) {
+    two_sum_acc(hi, lo, s);
+    lo += d;
+  }
+}
+
+__device__ __forceinline__ void vf_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of this CTA's shared memory at the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ void vf_put(void* at, int rank, uint32_t v) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(
+                   smem_addr(at)),
+               "r"(rank), "r"(v)
+               : "memory");
+}
+
+// The walk up to the next sum.  One thread of the cluster holds this.
+struct VfWalk {
+  int cur, r, count, gone;
+  bool known, last;  // S is; the draw was from the untouched row already
+  double c, S;
+};
+
+template <bool BF>
+__global__ void __launch_bounds__(kVfThreads, 2) __cluster_dims__(kVfCtas, 1, 1) verify_tree_kernel(const VerifyArgs a) {
+  __shared__ VfShared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x, i = blockIdx.y;
+  const int first = a.t.cu[i], n = a.t.cu[i + 1] - first, V = a.V;
+  constexpr int ES = BF ? 2 : 4;
+  pdl_wait();
+  pdl_trigger();
+  auto row_of = [&](const void* m, int64_t ld, int node) {
+    return static_cast<const void*>(static_cast<const char*>(m) + (int64_t)(first + node) * ld * ES);
+  };
+  if (rank == 0 && tid < n) {
+    const int par = a.t.parent[first + tid], x = a.token[first + tid];
+    const bool in = tid > 0 && par >= 0 && par < tid, tok = x >= 0 && x < V;
+    sh.parent[tid] = tid == 0 ? par : in ? par : -1;
+    sh.token[tid] = tok ? x : -1;
+    sh.u[tid] = a.u[first + tid];
+    sh.p[tid] = in && tok ? vf_one<BF>(row_of(a.p, a.ld_p, par), x) : 0.0f;
+    sh.q[tid] = in && tok && a.q ? vf_one<BF>(row_of(a.q, a.ld_q, par), x) : 0.0f;
+  }
+  __syncthreads();
+  if (n == 0 || a.t.parent[first] != -1) {  // nothing to start from (the same for the whole cluster)
+    if (rank == 0) {
+      if (tid < n) a.path[first + tid] = -1;
+      if (tid == 0) a.count[i] = 0, a.next[i] = -1;
+    }
+    return;
+  }
+  vf_cluster_sync();  // every CTA runs: its shared memory may be written
+  VfWalk w;
+  w.cur = 0, w.r = 1, w.count = 1, w.gone = 0, w.known = true, w.last = false, w.c = 0.0, w.S = 1.0;
+  if (rank == 0 && tid == 0) sh.path[0] = 0;
+  // runs of the vocabulary, whole rounds of a warp
+  const int per = (V + kVfCtas * kVfWarps * 128 - 1) / (kVfCtas * kVfWarps * 128) * 128;
+  const int64_t from64 = (int64_t)(rank * kVfWarps + warp) * per;
+  const int from = (int)min(from64, (int64_t)V), to = (int)min(from64 + per, (int64_t)V);
+  for (int pass = 0;; ++pass) {
+    if (rank == 0 && warp == 0) {
+      VfCmd cmd;
+      if (lane == 0) {
+        bool ask = false;  // a sum is needed before the next comparison
+        for (; w.r < n && !ask; ) {
+          const int r = w.r;
+          if (sh.parent[r] != w.cur || sh.token[r] < 0) {
+            ++w.r;
+            continue;
+          }
+          if (!w.known) {
+            ask = true;
+            break;
+          }
+          bool ok;
+          if (a.q) {
+            const double q = sh.q[r], left = (double)sh.p[r] - w.c * q;
+            ok = (double)sh.u[r] * q * w.S < (left > 0.0 ? left : 0.0);
+          } else {
+            bool was = false;
+            for (int k = 0; k < w.gone; ++k) was |= sh.gone_tok[k] == sh.token[r];
+            ok = !was && (double)sh.u[r] * w.S < (double)sh.p[r];
+          }
+          ++w.r;
+          if (ok) {
+            sh.path[w.count++] = r;
+            w.cur = r, w.c = 0.0, w.S = 1.0, w.known = true, w.gone = 0;
+          } else {
+            w.c += w.S;
+            w.known = false;
+            if (!a.q) sh.gone_tok[w.gone++] = sh.token[r];
+          }
+        }
+        cmd.what = ask ? VF_SUM : VF_DRAW;
+        cmd.cur = w.cur;
+        cmd.c_hi = a.q ? (float)w.c : 0.0f;
+        cmd.c_lo = a.q ? (float)(w.c - (double)cmd.c_hi) : 0.0f;
+        cmd.gone = w.gone;
+        sh.count = w.count;
+      }
+      // to all CTAs, lane d to CTA d
+      __syncwarp();
+      cmd.what = __shfl_sync(0xffffffffu, cmd.what, 0);
+      cmd.cur = __shfl_sync(0xffffffffu, cmd.cur, 0);
+      cmd.c_hi = __shfl_sync(0xffffffffu, cmd.c_hi, 0);
+      cmd.c_lo = __shfl_sync(0xffffffffu, cmd.c_lo, 0);
+      cmd.gone = __shfl_sync(0xffffffffu, cmd.gone, 0);
+      if (lane < kVfCtas) {
+        vf_put(&sh.cmd.what, lane, (uint32_t)cmd.what);
+        vf_put(&sh.cmd.cur, lane, (uint32_t)cmd.cur);
+        vf_put(&sh.cmd.c_hi, lane, __float_as_uint(cmd.c_hi));
+        vf_put(&sh.cmd.c_lo, lane, __float_as_uint(cmd.c_lo));
+        vf_put(&sh.cmd.gone, lane, (uint32_t)cmd.gone);
+        if (lane > 0)
+          for (int k = 0; k < cmd.gone; ++k) vf_put(&sh.gone_tok[k], lane, (uint32_t)sh.gone_tok[k]);
+      }
+    }
+    vf_cluster_sync();
+    const VfCmd cmd = sh.cmd;
+    const void* p = row_of(a.p, a.ld_p, cmd.cur);
+    const bool minus = a.q && cmd.c_hi > 0.0f;  // nothing refused: the draft's row is not read
+    const void* q = minus ? row_of(a.q, a.ld_q, cmd.cur) : nullptr;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (4 * ES - 1)) == 0;
+    float hi = 0.0f, lo = 0.0f;
+    constexpr int UN = 4;
+    for (int at = from + 4 * lane; at < to; at += 128 * UN) {
+      float4 v[UN], m[UN];
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        v[k] = vf_four<BF>(p, at + 128 * k, to, wide);
+        m[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (minus) m[k] = vf_four<BF>(q, at + 128 * k, to, wide);
+      }
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        vf_add(hi, lo, v[k].x, m[k].x, cmd.c_hi, cmd.c_lo);
+        vf_add(hi, lo, v[k].y, m[k].y, cmd.c_hi, cmd.c_lo);
+        vf_add(hi, lo, v[k].z, m[k].z, cmd.c_hi, cmd.c_lo);
+        vf_add(hi, lo, v[k].w, m[k].w, cmd.c_hi, cmd.c_lo);
+      }
+    }
+    two_sum_warp(hi, lo);
+    if (lane == 0) {
+      // refused tokens of a draft without rows: each once
+      for (int k = 0; k < cmd.gone; ++k) {
+        const int x = sh.gone_tok[k];
+        bool again = false;
+        for (int e = 0; e < k; ++e) again |= sh.gone_tok[e] == x;
+        if (!again && x >= from && x < to) two_sum_acc(hi, lo, -vf_one<BF>(p, x));
+      }
+      sh.hi[warp] = hi, sh.lo[warp] = lo;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      hi = lane < kVfWarps ? sh.hi[lane] : 0.0f, lo = lane < kVfWarps ? sh.lo[lane] : 0.0f;
+      two_sum_warp(hi, lo);
+      if (lane < kVfCtas) {
+        vf_put(&sh.tot_hi[pass & 1][rank], lane, __float_as_uint(hi));
+        vf_put(&sh.tot_lo[pass & 1][rank], lane, __float_as_uint(lo));
+      }
+    }
+    vf_cluster_sync();
+    if (cmd.what == VF_SUM) {
+      if (rank == 0 && tid == 0) {
+        w.S = 0.0;
+        for (int k = 0; k < kVfCtas; ++k) w.S += (double)sh.tot_hi[pass & 1][k] + (double)sh.tot_lo[pass & 1][k];
+        w.known = true;
+      }
+      continue;
+    }
+    // ---- draw: which CTA, which warp
+    if (tid == 0) {
+      double total = 0.0, at[kVfCtas];
+      for (int k = 0; k < kVfCtas; ++k) {
+        at[k] = (double)sh.tot_hi[pass & 1][k] + (double)sh.tot_lo[pass & 1][k];
+        total += at[k];
+      }
+      double want = (double)a.u_next[i] * total, run = 0.0, before = 0.0;
+      if (!(want > 0.0)) want = 0.0;
+      int cta = -1;  // the first whose end lies past `want`; else the last with anything in it
+      for (int k = 0; k < kVfCtas; ++k) {
+        if (at[k] > 0.0) {
+          cta = k, before = run;
+          if (run + at[k] > want) break;
+        }
+        run += at[k];
+      }
+      sh.warp = total > 0.0 ? -1 : -2;
+      if (cta == rank && total > 0.0) {
+        run = before;
+        for (int k = 0; k < kVfWarps; ++k) {
+          const double s = (double)sh.hi[k] + (double)sh.lo[k];
+          if (s > 0.0) {
+            sh.warp = k, sh.before = want - run;
+            if (run + s > want) break;
+          }
+          run += s;
+        }
+      }
+    }
+    __syncthreads();
+    if (sh.warp == -2 && (cmd.c_hi > 0.0f || cmd.gone > 0)) {
+      // nothing is left of the row: from the row itself
+      if (rank == 0 && tid == 0) w.c = 0.0, w.gone = 0, w.r = n;
+      __syncthreads();  // sh.warp has been read
+      continue;
+    }
+    if (rank == 0) {
+      if (tid < n) a.path[first + tid] = tid < sh.count ? sh.path[tid] : -1;
+      if (tid == 0) {
+        a.count[i] = sh.count;
+        if (sh.warp == -2) a.next[i] = -1;  // an empty row
+      }
+    }
+    if (sh.warp == warp) {
+      // a lane takes consecutive tokens of the run; then the lane that holds the place looks for it
+      const int len = (to - from + 31) / 32, l0 = min(to, from + lane * len), l1 = min(to, l0 + len);
+      float vh = 0.0f, vl = 0.0f;
+      auto value = [&](int x, float& h, float& l) {
+        for (int k = 0; k < cmd.gone; ++k)
+          if (sh.gone_tok[k] == x) return;
+        vf_add(h, l, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, cmd.c_hi, cmd.c_lo);
+      };
+#pragma unroll 8
+      for (int x = l0; x < l1; ++x) value(x, vh, vl);
+      float sh_hi = vh, sh_lo = vl;  // inclusive sums over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float oh = __shfl_up_sync(0xffffffffu, sh_hi, o), ol = __shfl_up_sync(0xffffffffu, sh_lo, o);
+        if (lane >= o) {
+          two_sum_acc(sh_hi, sh_lo, oh);
+          sh_lo += ol;
+        }
+      }
+      const double want = sh.before, end = (double)sh_hi + (double)sh_lo;
+      const bool some = vh > 0.0f;
+      const uint32_t past = __ballot_sync(0xffffffffu, some && end > want), any = __ballot_sync(0xffffffffu, some);
+      const int owner = past ? __ffs(past) - 1 : 31 - __clz((int)any);
+      const float ph = __shfl_up_sync(0xffffffffu, sh_hi, 1), pl = __shfl_up_sync(0xffffffffu, sh_lo, 1);
+      if (lane == owner) {
+        float h = lane ? ph : 0.0f, l = lane ? pl : 0.0f;
+        int found = -1;
+        for (int x = l0; x < l1; ++x) {
+          float eh = 0.0f, el = 0.0f;
+          value(x, eh, el);
+          if (!(eh > 0.0f)) continue;
+          found = x;
+          two_sum_acc(h, l, eh);
+          l += el;
+          if ((double)h + (double)l > want) break;
+        }
+        a.next[i] = found;
+      }
+    }
+    break;
+  }
+}
+
+cudaError_t launch_verify_tree(const VerifyArgs& a, cudaStream_t s) {
+  const dim3 grid(kVfCtas, a.t.nseq), block(kVfThreads);
+  trace_pre(K_VERIFY_TREE, s);
+  const cudaError_t e = a.bf16 ? launch_k(verify_tree_kernel<true>, grid, block, 0, s, true, a)
+                               : launch_k(verify_tree_kernel<false>, grid, block, 0, s, true, a);
+  trace_post(K_VERIFY_TREE, s);
+  return e;
+}
+
+}  // namespace m2

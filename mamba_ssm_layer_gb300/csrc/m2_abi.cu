@@ -79,7 +79,8 @@ static const char* kNames[K_COUNT] = {
     "conv_pos",      "ssm_step",        "conv_prefill",    "ssm_scan_seq",
     "gemm_tc",       "ssd_chunk_state", "ssd_state_pass",  "ssd_chunk_out",   "gemm_tc_reduce",
     "conv_ring_store", "decode_step_fused", "copy", "wait_check", "qk_norm_rope", "kv4_append", "kv4_gather",
-    "attn_prefill",  "attn_decode_kv4", "attn_decode_combine"};
+    "attn_prefill",  "attn_decode_kv4", "attn_decode_combine", "tree_conv", "tree_ssm", "tree_ring", "tree_state",
+    "verify_tree", "kv4_keep", "attn_tree_kv4", "attn_tree_combine"};
 
 // ------------------------------------------------------------------ helpers
 
@@ -655,9 +656,119 @@ static int prefill_impl(const m2_dims* dims, const m2_layer* L, uint16_t* hidden
   return M2_OK;
 }
 
+// ------------------------------------------------------------------ trees of drafted tokens
+
+// A tree call's workspace: the prefill's regions without the SSD scan's.
+static size_t tree_ws(const m2_dims& d, int T, int nseq) { return prefill_map(d, T, nseq, 0).part + proj_part_bytes(d, T); }
+
+// Checks that the layer's two tree calls share; *T receives the node rows.
+static int tree_check(const m2_dims* dims, const m2_layer* L, int32_t nseq, const int32_t* cu, const float* ssm_state,
+                      const uint16_t* conv_state, const int32_t* conv_pos, const void* ws, size_t ws_bytes, int* T) {
+  const int st = m2_validate(dims, L);
+  if (st) return st;
+  if (nseq <= 0 || !cu || !ssm_state || !conv_state || !conv_pos || cu[0] != 0) return M2_ERR_ARG;
+  for (int i = 0; i < nseq; ++i)
+    if (cu[i + 1] < cu[i]) return M2_ERR_ARG;
+  for (int i = 0; i < nseq; ++i)
+    if (cu[i + 1] - cu[i] > kTreeNodes) return M2_ERR_UNSUPPORTED;
+  *T = cu[nseq];
+  if (*T == 0) return M2_OK;
+  if (!al16(ssm_state) || !al8(conv_state)) return M2_ERR_ALIGN;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < tree_ws(*dims, *T, nseq)) return M2_ERR_WORKSPACE;
+  return M2_OK;
+}
+
 }  // namespace m2
 
 extern "C" {
+
+size_t m2_workspace_bytes_tree(const m2_dims* dims, int32_t max_seqs, int32_t max_total_nodes) {
+  if (check_dims(dims) || max_seqs <= 0 || max_total_nodes < 0) return 0;
+  return tree_ws(*dims, max_total_nodes, max_seqs);
+}
+
+int mamba2_layer_tree(const m2_dims* dims, const m2_layer* L, uint16_t* hidden, int32_t nseq, const int32_t* cu_nodes,
+                      const int32_t* parent, const float* ssm_state, const uint16_t* conv_state,
+                      const int32_t* conv_pos, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int T = 0;
+  int st = tree_check(dims, L, nseq, cu_nodes, ssm_state, conv_state, conv_pos, ws, ws_bytes, &T);
+  if (st || T == 0) return st;
+  if (!hidden || !parent) return M2_ERR_ARG;
+  if (!al16(hidden) || (reinterpret_cast<uintptr_t>(parent) & 3u)) return M2_ERR_ALIGN;
+  const m2_dims& d = *dims;
+  const Derived r = derive(d);
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  const PrefillMap wm = prefill_map(d, T, nseq, 0);
+  uint16_t* xn = reinterpret_cast<uint16_t*>(w8 + wm.xn);
+  uint16_t* zx = reinterpret_cast<uint16_t*>(w8 + wm.zx);
+  uint16_t* u = reinterpret_cast<uint16_t*>(w8 + wm.u);
+  float* y = reinterpret_cast<float*>(w8 + wm.y);
+  uint16_t* g = reinterpret_cast<uint16_t*>(w8 + wm.g);
+  float* us_in = reinterpret_cast<float*>(w8 + wm.unscale);
+  float* us_out = us_in + T;
+  float* part = reinterpret_cast<float*>(w8 + wm.part);
+  const size_t part_bytes = proj_part_bytes(d, T);
+  cudaError_t e;
+  PrepArgs pa;
+  memset(&pa, 0, sizeof(pa));
+  pa.mode = PREP_RMSNORM;
+  pa.x = hidden;
+  pa.ldx = d.hidden;
+  pa.w = L->norm_w;
+  pa.eps = d.eps_in;
+  pa.M = T;
+  pa.K = d.hidden;
+  pa.out = xn;
+  pa.ldo = d.hidden;
+  pa.f16 = proj_f16(L->in_proj, T) ? 1 : 0;
+  pa.unscale = us_in;
+  if ((e = launch_prep(pa, stream))) return launch_status(e);
+  if ((e = proj(L->in_proj, xn, d.hidden, T, zx, r.ldz, EPI_STORE, nullptr, 0, stream, nullptr, us_in, 0, part,
+                part_bytes)))
+    return launch_status(e);
+  if ((st = mamba2_tree_conv(conv_state, conv_pos, zx + r.d_inner, r.ldz, L->conv_w, L->conv_b, u, r.d_xbc, nseq,
+                             cu_nodes, parent, r.d_xbc, d.d_conv, 1, stream)))
+    return st;
+  if ((st = mamba2_tree_ssm(ssm_state, u, u + r.d_inner, u + r.d_inner + d.n_groups * d.d_state, r.d_xbc,
+                            zx + r.d_inner + r.d_xbc, r.ldz, L->A_log, L->D, L->dt_bias, y, nseq, cu_nodes, parent,
+                            d.nheads, d.head_dim, d.d_state, d.n_groups, stream)))
+    return st;
+  memset(&pa, 0, sizeof(pa));
+  pa.mode = PREP_GATED;
+  pa.y = y;
+  pa.ldy = r.d_inner;
+  pa.z = zx;
+  pa.ldz = r.ldz;
+  pa.w = L->gnorm_w;
+  pa.eps = d.eps_gated;
+  pa.group = d.gnorm_group;
+  pa.M = T;
+  pa.K = r.d_inner;
+  pa.out = g;
+  pa.ldo = r.d_inner;
+  pa.f16 = proj_f16(L->out_proj, T) ? 1 : 0;
+  pa.unscale = us_out;
+  if ((e = launch_prep(pa, stream))) return launch_status(e);
+  return launch_status(proj(L->out_proj, g, r.d_inner, T, hidden, d.hidden, EPI_RESID, hidden, d.hidden, stream, nullptr,
+                            us_out, 0, part, part_bytes));
+}
+
+int mamba2_layer_tree_commit(const m2_dims* dims, const m2_layer* L, int32_t nseq, const int32_t* cu_nodes,
+                             const int32_t* path, const int32_t* count, float* ssm_state, uint16_t* conv_state,
+                             int32_t* conv_pos, const void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int T = 0;
+  const int st = tree_check(dims, L, nseq, cu_nodes, ssm_state, conv_state, conv_pos, ws, ws_bytes, &T);
+  if (st || T == 0) return st;
+  const m2_dims& d = *dims;
+  const Derived r = derive(d);
+  const uint8_t* w8 = static_cast<const uint8_t*>(ws);
+  const PrefillMap wm = prefill_map(d, T, nseq, 0);
+  const uint16_t* zx = reinterpret_cast<const uint16_t*>(w8 + wm.zx);
+  const uint16_t* u = reinterpret_cast<const uint16_t*>(w8 + wm.u);
+  return mamba2_tree_commit(ssm_state, conv_state, conv_pos, ssm_state, conv_state, conv_pos, zx + r.d_inner, r.ldz, u,
+                            r.d_xbc, zx + r.d_inner + r.d_xbc, r.ldz, L->A_log, L->dt_bias, nseq, cu_nodes, path, count,
+                            d.nheads, d.head_dim, d.d_state, d.n_groups, d.d_conv, stream);
+}
 
 int mamba2_layer_prefill(const m2_dims* dims, const m2_layer* L, uint16_t* hidden, int32_t T, float* ssm_state,
                          uint16_t* conv_state, int32_t* conv_pos, void* ws, size_t ws_bytes, cudaStream_t stream) {
@@ -895,7 +1006,8 @@ int mamba2_layer_decode_noalloc(const m2_dims* dims, const m2_layer* layer, uint
 int m2_device_status(int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return M2_ERR_LAUNCH;
   const int parts[] = {status_gemv(clear), status_gemv_mma(clear), status_gemm_tc(clear), status_mixer(clear),
-                       status_kv4(clear), status_attn(clear), status_attn_decode(clear)};
+                       status_kv4(clear), status_attn(clear), status_attn_decode(clear), status_tree(clear),
+                       status_attn_tree(clear)};
   for (int v : parts)
     if (v != 0) return v;
   return M2_OK;
@@ -914,14 +1026,14 @@ int m2_workspace_map(const m2_dims* dims, int32_t kind, int32_t n, const int32_t
     offsets[M2_WS_UNSCALE] = m.unscale;
     return M2_OK;
   }
-  if (kind != M2_WS_KIND_PREFILL && kind != M2_WS_KIND_PREFILL_W8A8) return M2_ERR_ARG;
+  if (kind != M2_WS_KIND_PREFILL && kind != M2_WS_KIND_PREFILL_W8A8 && kind != M2_WS_KIND_TREE) return M2_ERR_ARG;
   if (!cu_seqlens || cu_seqlens[0] != 0) return M2_ERR_ARG;
   for (int i = 0; i < n; ++i)
     if (cu_seqlens[i + 1] < cu_seqlens[i]) return M2_ERR_ARG;
   const int T = cu_seqlens[n];
   if (T <= 0) return M2_ERR_ARG;
   std::vector<int32_t> tab(2 * (size_t)(n + 1));
-  const int nchunks = ssd_chunk_table(cu_seqlens, n, tab.data());
+  const int nchunks = kind == M2_WS_KIND_TREE ? 0 : ssd_chunk_table(cu_seqlens, n, tab.data());
   const PrefillMap m = prefill_map(*dims, T, n, nchunks);
   offsets[M2_WS_XN] = m.xn;
   offsets[M2_WS_ZX] = m.zx;
@@ -940,7 +1052,8 @@ int m2_set_wait_limit(int64_t cycles) {
   const long long v = cycles > 0 ? (long long)cycles : 4000000000LL;
   if (wait_limit_gemv(v) != cudaSuccess || wait_limit_gemv_mma(v) != cudaSuccess ||
       wait_limit_gemm_tc(v) != cudaSuccess || wait_limit_mixer(v) != cudaSuccess ||
-      wait_limit_attn(v) != cudaSuccess || wait_limit_attn_decode(v) != cudaSuccess) {
+      wait_limit_attn(v) != cudaSuccess || wait_limit_attn_decode(v) != cudaSuccess ||
+      wait_limit_attn_tree(v) != cudaSuccess) {
     cudaGetLastError();
     return M2_ERR_DEVICE;
   }

@@ -6,62 +6,10 @@
 #include <string.h>
 
 #include "../../include/mamba2.h"
+#include "m2_attn_checks.h"
 #include "m2_kernels.h"
 
 namespace m2 {
-
-static inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static int status_of(cudaError_t e) {
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return M2_ERR_LAUNCH;
-  }
-  return M2_OK;
-}
-
-static bool head_dim_ok(int32_t D) { return D == 64 || D == 128; }
-
-// Head counts of an attention layer.
-static int check_heads(int32_t H, int32_t Hkv, int32_t D) {
-  if (H <= 0 || Hkv <= 0 || D <= 0 || H % Hkv) return M2_ERR_ARG;
-  if (!head_dim_ok(D) || H > 4096) return M2_ERR_UNSUPPORTED;
-  return M2_OK;
-}
-
-// Rows of `width` elements, `ld` apart, that are read or written 16 bytes at a time.
-static int check_rows(const void* p, int32_t ld, int32_t width) {
-  if (!p || ld < width) return M2_ERR_ARG;
-  if (!al16(p) || ld % 8) return M2_ERR_ALIGN;
-  return M2_OK;
-}
-
-static int check_offsets(const int32_t* cu, int32_t nseq) {
-  if (!cu || nseq <= 0 || cu[0] != 0) return M2_ERR_ARG;
-  for (int i = 0; i < nseq; ++i)
-    if (cu[i + 1] < cu[i]) return M2_ERR_ARG;
-  return M2_OK;
-}
-
-static int check_cache(const m2_kv4_cache* c) {
-  if (!c || !c->pages || !c->block_table || c->n_pages <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 ||
-      c->nseq <= 0 || c->ld_table <= 0 || c->ld_table > INT32_MAX / M2_KV4_PAGE)
-    return M2_ERR_ARG;
-  if (!head_dim_ok(c->head_dim) || c->n_kv_heads > 4096) return M2_ERR_UNSUPPORTED;
-  if (!al16(c->pages) || (reinterpret_cast<uintptr_t>(c->block_table) & 3u)) return M2_ERR_ALIGN;
-  return M2_OK;
-}
-
-static Kv4 kv4_of(const m2_kv4_cache* c) {
-  Kv4 k;
-  k.pages = static_cast<uint8_t*>(c->pages);
-  k.table = c->block_table;
-  k.n_pages = c->n_pages;
-  k.Hkv = c->n_kv_heads;
-  k.D = c->head_dim;
-  k.ld_table = c->ld_table;
-  return k;
-}
 
 // Append (pos set) and gather: checks, then one launch per kSeqs sequences.
 static int kv4_rows(const m2_kv4_cache* c, uint16_t* k, int32_t ld_k, uint16_t* v, int32_t ld_v, const int32_t* cu,

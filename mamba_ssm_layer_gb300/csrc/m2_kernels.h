@@ -39,6 +39,14 @@ enum KernelId : int32_t {
   K_ATTN_PREFILL,
   K_ATTN_DECODE,
   K_ATTN_COMBINE,
+  K_TREE_CONV,
+  K_TREE_SSM,
+  K_TREE_RING,
+  K_TREE_STATE,
+  K_VERIFY_TREE,
+  K_KV4_KEEP,
+  K_ATTN_TREE,
+  K_ATTN_TREE_COMBINE,
   K_COUNT
 };
 
@@ -55,6 +63,8 @@ int status_mixer(int clear);
 int status_kv4(int clear);
 int status_attn(int clear);
 int status_attn_decode(int clear);
+int status_tree(int clear);
+int status_attn_tree(int clear);
 // Setters of each translation unit's pipeline wait limit (SM clock cycles).
 cudaError_t wait_limit_gemv(long long cycles);
 cudaError_t wait_limit_gemv_mma(long long cycles);
@@ -62,6 +72,7 @@ cudaError_t wait_limit_gemm_tc(long long cycles);
 cudaError_t wait_limit_mixer(long long cycles);
 cudaError_t wait_limit_attn(long long cycles);
 cudaError_t wait_limit_attn_decode(long long cycles);
+cudaError_t wait_limit_attn_tree(long long cycles);
 
 // Number of SMs of the current device (cached).
 int num_sms();
@@ -394,5 +405,107 @@ struct AttnDecodeArgs {
 };
 size_t attn_decode_ws_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t D);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ trees of drafted tokens
+
+// The nodes of a launch's sequences (up to kSeqs): sequence i has nodes cu[i] ..
+// cu[i + 1] - 1 of the launch, at most kTreeNodes.
+constexpr int kTreeNodes = 64;
+struct TreeArgs {
+  const int32_t* parent;  // of the launch's first node
+  int32_t nseq;
+  int32_t cu[kSeqs + 1];  // cu[0] = 0
+};
+
+// Causal conv over the tree (k_tree.cu).
+struct TreeConvArgs {
+  TreeArgs t;
+  const uint16_t* ring;   // [nseq][d_conv-1][C]
+  const int32_t* pos;
+  const uint16_t* x;      // rows ld_x apart
+  const uint16_t* w;      // [C][d_conv]
+  const uint16_t* bias;   // [C] or null
+  uint16_t* out;          // rows ld_o apart
+  int32_t ld_x, ld_o, C, dconv, silu;
+  int32_t wide;           // 16-byte loads fit
+};
+cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s);
+
+// SSM outputs over the tree (k_tree.cu); the state is only read.
+struct TreeSsmArgs {
+  TreeArgs t;
+  const float* h;         // [nseq][H][P][N]
+  const uint16_t* x;      // rows ld_in apart
+  const uint16_t* Bm;
+  const uint16_t* Cm;
+  const uint16_t* dt;     // rows ld_dt apart
+  const float* A_log;
+  const float* D;
+  const float* dt_bias;
+  float* y;               // [T][H*P]
+  int32_t ld_in, ld_dt, H, P, N, G;
+  int32_t wide_x;         // x rows of a head can be read 8 bytes at a time
+};
+cudaError_t launch_tree_ssm(const TreeSsmArgs& a, cudaStream_t s);
+
+// The state, ring and position moved along the accepted path (k_tree.cu).
+struct TreeCommitArgs {
+  TreeArgs t;             // parent: the paths
+  const int32_t* count;
+  const float* h;
+  const uint16_t* ring;
+  const int32_t* pos;
+  float* h_out;           // each may be the input itself
+  uint16_t* ring_out;
+  int32_t* pos_out;
+  const uint16_t* xbc;    // raw rows, ld_xbc apart
+  const uint16_t* u;      // conv output x | B | C, ld_u apart
+  const uint16_t* dt;     // ld_dt apart
+  const float* A_log;
+  const float* dt_bias;
+  int32_t ld_xbc, ld_u, ld_dt, H, P, N, G, dconv;
+  int32_t wide;           // the ring's and rows' channels can be read 16 bytes at a time
+};
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s);
+
+// Verification of drafted tokens (k_verify.cu).
+struct VerifyArgs {
+  TreeArgs t;
+  const void* p;          // [T] rows ld_p apart, fp32 or bf16
+  const void* q;          // or null
+  int64_t ld_p, ld_q;
+  int32_t bf16, V;
+  const int32_t* token;
+  const float* u;
+  const float* u_next;
+  int32_t* path;
+  int32_t* count;
+  int32_t* next;
+};
+cudaError_t launch_verify_tree(const VerifyArgs& a, cudaStream_t s);
+
+// Accepted rows of the 4-bit cache moved together (k_kv4.cu).
+struct Kv4KeepArgs {
+  Kv4 c;
+  TreeArgs t;             // parent: the paths
+  const int32_t* count;
+  const int32_t* pos;
+};
+cudaError_t launch_kv4_keep(const Kv4KeepArgs& a, cudaStream_t s);
+
+// Attention of the tree's nodes over the 4-bit cache (k_attn_tree.cu).
+struct AttnTreeArgs {
+  Kv4 c;
+  TreeArgs t;
+  const uint16_t* q;
+  uint16_t* out;
+  int32_t ld_q, ld_o, H;
+  int32_t most;           // nodes of the launch's largest tree
+  const int32_t* pos;
+  float scale;
+  void* ws;
+};
+size_t attn_tree_ws_bytes(int32_t H, int32_t Hkv, int32_t D);
+cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s);
 
 }  // namespace m2
