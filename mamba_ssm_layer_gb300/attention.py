@@ -12,7 +12,7 @@ import contextlib
 import torch
 
 from . import abi
-from .layer import _empty, _zeros, to_dev
+from .layer import _check_nodes, _empty, _zeros, to_dev
 
 PAGE = abi.M2_KV4_PAGE
 
@@ -91,6 +91,20 @@ class Kv4Cache:
                 self.pos.add_(torch.tensor(list(new), dtype=torch.int32).to(self.pos.device))
         self.tokens = [t + n for t, n in zip(self.tokens, new)]
 
+    def keep(self, cu_nodes, path: torch.Tensor, count: torch.Tensor, stream=None) -> None:
+        """After a tree of drafted tokens (``DeviceAttention.tree`` of every layer): the accepted nodes' rows moved
+        behind the context in all layers, and ``pos`` advanced by ``count`` (both device int32, of
+        ``abi.m2_verify_tree``).  Can be captured; the host's count follows with
+        ``advance(count, on_device=False)``."""
+        _check_nodes("Kv4Cache.keep", cu_nodes, self.nseq, path)
+        if count.dtype != torch.int32 or count.numel() != self.nseq:
+            raise abi.M2Error("Kv4Cache.keep", abi.M2_ERR_ARG)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        for c in self.struct:
+            abi.m2_kv4_keep(c, cu_nodes, path, count, self.pos, s)
+        with _on(stream):
+            self.pos.add_(count)
+
     def release(self, seq: int, stream=None, idle: bool = False) -> None:
         """Gives a finished sequence's pages back.  idle: the slot may stay in decode steps without a sequence (its
         rows are not stored, its output is zeros) until pages are reserved for it; without it such a step reports
@@ -122,11 +136,15 @@ class DeviceAttention:
             self.steps = torch.tensor(abi.m2_rope_steps(d["theta"], self.rot), dtype=torch.int64).to(device)
         self.device = device
 
-    def buffers(self, max_rows: int, max_keys: int = 0, nseq: int = 1) -> dict:
+    def buffers(self, max_rows: int, max_keys: int = 0, nseq: int = 1, trees: bool = False) -> dict:
         """Scratch for calls of up to max_rows token rows (prompts over cached tokens: max_keys cached and new
-        tokens of all sequences; calls that need more are refused).  Layers run one after the other can share it."""
+        tokens of all sequences; trees: for ``tree`` too; calls that need more are refused).  Layers run one after
+        the other can share it."""
         bf, dev = torch.bfloat16, self.device
-        return dict(qkv=_empty((max_rows, self.n_qkv), bf, dev), q=_empty((max_rows, self.H * self.D), bf, dev),
+        more = {}
+        if trees:
+            more["tree_ws"] = _empty((abi.m2_attn_tree_kv4_workspace_bytes(self.H, self.Hkv, self.D),), torch.uint8, dev)
+        return dict(more, qkv=_empty((max_rows, self.n_qkv), bf, dev), q=_empty((max_rows, self.H * self.D), bf, dev),
                     k=_empty((max_rows, self.Hkv * self.D), bf, dev),
                     attn=_empty((max_rows, self.H * self.D), bf, dev),
                     keys=_empty((max(max_keys, 1), 2 * self.Hkv * self.D), bf, dev),
@@ -205,4 +223,22 @@ class DeviceAttention:
         abi.m2_kv4_append(cache.struct[layer], k, Hkv * D, v, self.n_qkv, range(cache.nseq + 1), cache.pos, s)
         abi.m2_attn_decode_kv4(cache.struct[layer], q, H * D, b["attn"], H * D, H, kv_len, self.scale, b["ws"],
                                b["ws"].numel(), s)
+        self._output(b, out, s)
+
+    def tree(self, x, cu_nodes, parent, row_pos, cache: Kv4Cache, layer: int, b: dict, out, stream=None) -> None:
+        """x, out [T][hidden] bf16: the nodes of every sequence's tree of drafted tokens, rows cu_nodes[i] ..
+        cu_nodes[i+1]-1 of sequence i; parent and row_pos device int32 [T]: each node's parent, and its position (the
+        context's tokens + its depth).  The nodes' keys and values go behind the context (pages for them reserved
+        before) and are attended to there; ``Kv4Cache.keep`` then keeps the accepted ones.  Can be captured."""
+        _check_nodes("DeviceAttention.tree", cu_nodes, cache.nseq, parent)
+        T = cu_nodes[-1]
+        self._check("DeviceAttention.tree", T, x, out, row_pos, cache, b)
+        if "tree_ws" not in b:
+            raise abi.M2Error("DeviceAttention.tree", abi.M2_ERR_WORKSPACE)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        H, Hkv, D = self.H, self.Hkv, self.D
+        q, k, v = self._project(x, b, row_pos, s)
+        abi.m2_kv4_append(cache.struct[layer], k, Hkv * D, v, self.n_qkv, cu_nodes, cache.pos, s)
+        abi.m2_attn_tree_kv4(cache.struct[layer], q, H * D, b["attn"], H * D, H, cu_nodes, parent, cache.pos, self.scale,
+                             b["tree_ws"], b["tree_ws"].numel(), s)
         self._output(b, out, s)

@@ -56,6 +56,13 @@ def bits_u16(t: torch.Tensor) -> np.ndarray:
     return t.detach().cpu().numpy().view(np.uint16)
 
 
+def _check_nodes(fn: str, cu_nodes, nseq: int, by_node: torch.Tensor) -> None:
+    """Offsets of every sequence's nodes, and an int32 array of an entry for each: the kernels see pointers only."""
+    if len(cu_nodes) != nseq + 1 or by_node.dtype != torch.int32 or by_node.numel() < cu_nodes[-1] \
+            or not by_node.is_contiguous():
+        raise abi.M2Error(fn, abi.M2_ERR_ARG)
+
+
 class DeviceLayer:
     """One layer's parameters on the device plus the ctypes structs that point at them."""
 
@@ -131,3 +138,29 @@ class DeviceLayer:
         T = hidden.shape[0]
         abi.mamba2_layer_prefill(self.dims, self.struct, hidden, T, h, ring, pos, ws, ws.numel(),
                                  stream if stream is not None else torch.cuda.current_stream())
+
+    def workspace_tree(self, max_seqs: int, max_total_nodes: int, device="cuda") -> torch.Tensor:
+        """Workspace of ``tree``: it holds what ``tree_commit`` needs, so that every layer keeps its own between the
+        two calls."""
+        n = abi.m2_workspace_bytes_tree(self.dims, max_seqs, max_total_nodes)
+        return _empty((max(n, 256),), torch.uint8, device)
+
+    def tree(self, hidden: torch.Tensor, cu_nodes, parent: torch.Tensor, state, ws: torch.Tensor, stream=None) -> None:
+        """hidden [T][hidden], in place: rows cu_nodes[i] .. cu_nodes[i+1]-1 are the nodes of sequence i's tree of
+        drafted tokens, parent (device int32 [T]) their parents; the state is only read."""
+        h, ring, pos = state
+        _check_nodes("DeviceLayer.tree", cu_nodes, pos.numel(), parent)
+        if hidden.shape != (cu_nodes[-1], self.dims_dict["hidden"]) or hidden.element_size() != 2 or not hidden.is_contiguous():
+            raise abi.M2Error("DeviceLayer.tree", abi.M2_ERR_ARG)
+        abi.mamba2_layer_tree(self.dims, self.struct, hidden, cu_nodes, parent, h, ring, pos, ws, ws.numel(),
+                              stream if stream is not None else torch.cuda.current_stream())
+
+    def tree_commit(self, cu_nodes, path: torch.Tensor, count: torch.Tensor, state, ws: torch.Tensor,
+                    stream=None) -> None:
+        """The state moved along the accepted path of the last ``tree`` call with this workspace."""
+        h, ring, pos = state
+        _check_nodes("DeviceLayer.tree_commit", cu_nodes, pos.numel(), path)
+        if count.dtype != torch.int32 or count.numel() != pos.numel():
+            raise abi.M2Error("DeviceLayer.tree_commit", abi.M2_ERR_ARG)
+        abi.mamba2_layer_tree_commit(self.dims, self.struct, cu_nodes, path, count, h, ring, pos, ws, ws.numel(),
+                                     stream if stream is not None else torch.cuda.current_stream())

@@ -187,3 +187,71 @@ def test_reference_verification_keeps_the_target_distribution():
         hits[token[path[1]] if len(path) > 1 else last] += 1
     # binomial spread: five standard deviations
     assert bool(((hits / N - p[0]).abs() < 5 * (p[0] * (1 - p[0]) / N).sqrt()).all())
+
+
+# ------------------------------------------------------------------ holders (on the CPU: no kernel is launched)
+
+class Stream:
+    cuda_stream = 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+    for name in ("w8a16_gemv", "m2_qk_norm_rope", "m2_kv4_append", "m2_attn_tree_kv4", "m2_kv4_keep", "mamba2_layer_tree",
+                 "mamba2_layer_tree_commit"):
+        monkeypatch.setattr(abi, name, lambda *a, _n=name, **k: seen.append((_n, a)))
+    return seen
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def test_attention_holder_checks_its_trees(calls):
+    from mamba_ssm_layer_gb300.attention import DeviceAttention, Kv4Cache
+    m = DeviceAttention(synth.make_attention(synth.TINY_ATTENTION, 9), device="cpu")
+    cache = Kv4Cache(2, 2, 12, 256, m.Hkv, m.D, device="cpu")
+    bf = torch.bfloat16
+    good = dict(x=torch.zeros(5, m.hidden, dtype=bf), cu=[0, 3, 5], parent=ints(-1, 0, 0, -1, 0), row_pos=ints(0, 1, 1, 0, 1),
+                b=m.buffers(8, 0, 2, trees=True), out=torch.zeros(5, m.hidden, dtype=bf))
+
+    def tree(**over):
+        a = dict(good, **over)
+        m.tree(a["x"], a["cu"], a["parent"], a["row_pos"], cache, 1, a["b"], a["out"], Stream())
+    tree()
+    assert [n for n, _ in calls] == ["w8a16_gemv", "m2_qk_norm_rope", "m2_kv4_append", "m2_attn_tree_kv4", "w8a16_gemv"]
+    for over in (dict(cu=[0, 5]), dict(parent=ints(-1, 0, 0, -1)), dict(parent=torch.zeros(5, dtype=torch.int64)),
+                 dict(x=torch.zeros(4, m.hidden, dtype=bf)), dict(out=torch.zeros(6, m.hidden, dtype=bf)),
+                 dict(row_pos=ints(0, 1, 1, 0)), dict(b=m.buffers(4, 0, 2, trees=True)), dict(b=m.buffers(8, 0, 2)),
+                 dict(parent=torch.zeros(10, dtype=torch.int32)[::2])):
+        with pytest.raises(abi.M2Error):
+            tree(**over)
+    assert len(calls) == 5
+    path, count = ints(0, 2, -1, 0, -1), ints(2, 1)
+    with pytest.raises(abi.M2Error):
+        cache.keep([0, 5], path, count, 0)
+    with pytest.raises(abi.M2Error):
+        cache.keep([0, 3, 5], path, ints(2), 0)
+    with pytest.raises(abi.M2Error):
+        cache.keep([0, 3, 5], ints(0, 2), count, 0)
+    assert len(calls) == 5
+
+
+def test_layer_holder_checks_its_trees(calls):
+    from mamba_ssm_layer_gb300.layer import DeviceLayer
+    dl = DeviceLayer(synth.make_layer(synth.TINY, synth.WL_TINY_DECODE), device="cpu")
+    st, ws = dl.new_state(2, device="cpu"), dl.workspace_tree(2, 5, device="cpu")
+    x = torch.zeros(5, 256, dtype=torch.int16)
+    dl.tree(x, [0, 3, 5], ints(-1, 0, 0, -1, 0), st, ws, Stream())
+    dl.tree_commit([0, 3, 5], ints(0, 1, -1, 0, -1), ints(2, 1), st, ws, Stream())
+    assert [n for n, _ in calls] == ["mamba2_layer_tree", "mamba2_layer_tree_commit"]
+    for bad in (lambda: dl.tree(x, [0, 5], ints(-1, 0, 0, -1, 0), st, ws, Stream()),
+                lambda: dl.tree(x[:4], [0, 3, 5], ints(-1, 0, 0, -1, 0), st, ws, Stream()),
+                lambda: dl.tree(x.float(), [0, 3, 5], ints(-1, 0, 0, -1, 0), st, ws, Stream()),
+                lambda: dl.tree(x, [0, 3, 5], ints(-1, 0, 0), st, ws, Stream()),
+                lambda: dl.tree_commit([0, 3, 5], ints(0, 1), ints(2, 1), st, ws, Stream()),
+                lambda: dl.tree_commit([0, 3, 5], ints(0, 1, -1, 0, -1), ints(2), st, ws, Stream())):
+        with pytest.raises(abi.M2Error):
+            bad()
+    assert len(calls) == 2
