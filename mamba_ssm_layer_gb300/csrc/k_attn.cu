@@ -49,6 +49,7 @@
 #include "m2_common.cuh"
 #include "m2_kernels.h"
 #include "m2_tc.cuh"
+#include "m2_tc_attn.cuh"
 
 namespace m2 {
 
@@ -135,51 +136,6 @@ struct AtArgs {
   uint16_t order[kAtSorted];
 };
 
-// 32 columns of this warp's 32 lanes, without waiting.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-// The loads above have arrived; n values may be used after this.
-template <int N>
-__device__ __forceinline__ void tmem_ld_wait(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // no use moves above the wait
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  uint64_t d;
-  asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%1, %2};\n\tmov.b64 rb, {%3, %4};\n\tadd.rn.f32x2 %0, ra, rb;\n\t}"
-      : "=l"(d)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
-  return r;
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // Operands are 128-byte swizzled: Q and K K-major (leading offset unused: 1), V
 // MN-major (64 channels a row, rows along the keys; the next 64 channels at the
 // leading offset); 8-row atoms 1024 bytes apart (stride offset).
@@ -188,27 +144,6 @@ __device__ __forceinline__ bool elect_one() {
 // Every lane comes here and only the leader's product takes place: with a branch
 // around them operands pass through vector registers, and a prompt of 8192 tokens
 // took 370 us instead of 349.
-constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint64_t at_desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
-__device__ __forceinline__ void at_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc, int leader) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader));
-}
-__device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc, int leader) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader));
-}
-__device__ __forceinline__ void at_commit(uint64_t* bar, int leader) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
-      "r"(leader)
-      : "memory");
-}
 template <int D>
 __device__ __forceinline__ void at_issue_scores(uint32_t d, uint32_t q, uint32_t k, int leader) {
 #pragma unroll
@@ -225,13 +160,6 @@ __device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t
   for (int i = 0; i < 4; ++i)
     at_mma_ts(d, p + 8 * i, at_desc((v + i * (2048 >> 4)) | ((kAtRows * 128 >> 4) << 16)),
               tc_idesc(kAtRows, D) | (1u << 16), acc || i > 0, leader);
-}
-
-// 32 bytes, aligned: a whole sector.
-__device__ __forceinline__ void store32(uint16_t* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
 }
 
 // A potentially blocking test, for as long as the hardware likes.  (A time asked for

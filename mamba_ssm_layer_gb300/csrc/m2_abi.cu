@@ -1007,7 +1007,7 @@ int m2_device_status(int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return M2_ERR_LAUNCH;
   const int parts[] = {status_gemv(clear), status_gemv_mma(clear), status_gemm_tc(clear), status_mixer(clear),
                        status_kv4(clear), status_attn(clear), status_attn_decode(clear), status_tree(clear),
-                       status_attn_tree(clear)};
+                       status_attn_tree(clear), status_attn_tree_tc(clear)};
   for (int v : parts)
     if (v != 0) return v;
   return M2_OK;
@@ -1053,7 +1053,7 @@ int m2_set_wait_limit(int64_t cycles) {
   if (wait_limit_gemv(v) != cudaSuccess || wait_limit_gemv_mma(v) != cudaSuccess ||
       wait_limit_gemm_tc(v) != cudaSuccess || wait_limit_mixer(v) != cudaSuccess ||
       wait_limit_attn(v) != cudaSuccess || wait_limit_attn_decode(v) != cudaSuccess ||
-      wait_limit_attn_tree(v) != cudaSuccess) {
+      wait_limit_attn_tree(v) != cudaSuccess || wait_limit_attn_tree_tc(v) != cudaSuccess) {
     cudaGetLastError();
     return M2_ERR_DEVICE;
   }

@@ -65,6 +65,7 @@ int status_attn(int clear);
 int status_attn_decode(int clear);
 int status_tree(int clear);
 int status_attn_tree(int clear);
+int status_attn_tree_tc(int clear);
 // Setters of each translation unit's pipeline wait limit (SM clock cycles).
 cudaError_t wait_limit_gemv(long long cycles);
 cudaError_t wait_limit_gemv_mma(long long cycles);
@@ -73,6 +74,7 @@ cudaError_t wait_limit_mixer(long long cycles);
 cudaError_t wait_limit_attn(long long cycles);
 cudaError_t wait_limit_attn_decode(long long cycles);
 cudaError_t wait_limit_attn_tree(long long cycles);
+cudaError_t wait_limit_attn_tree_tc(long long cycles);
 
 // Number of SMs of the current device (cached).
 int num_sms();
@@ -507,5 +509,8 @@ struct AttnTreeArgs {
 };
 size_t attn_tree_ws_bytes(int32_t H, int32_t Hkv, int32_t D);
 cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s);
+// The same on the tensor cores, for many rows (k_attn_tree_tc.cu).
+size_t attn_tree_tc_ws_bytes(int32_t D);
+cudaError_t launch_attn_tree_tc(const AttnTreeArgs& a, cudaStream_t s);
 
 }  // namespace m2
