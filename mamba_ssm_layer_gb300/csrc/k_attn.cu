@@ -162,19 +162,6 @@ __device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t
               tc_idesc(kAtRows, D) | (1u << 16), acc || i > 0, leader);
 }
 
-// A potentially blocking test, for as long as the hardware likes.  (A time asked for
-// becomes sleeping in steps, which took 1 to 2% longer.)
-__device__ __forceinline__ bool at_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // mbar_wait without a call (a kernel that hands registers between its warps has to
 // be one function), its limit from the launch's parameters.  The hardware may hold a
 // suspended wait longer than asked, so that a short limit takes waits that only test

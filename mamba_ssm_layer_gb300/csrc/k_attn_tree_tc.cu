@@ -12,8 +12,10 @@
 //   softmax    a thread a row: S from tensor memory, P as f16 over it, maxima and sums
 //              in fp32; the reference follows the maximum once it has grown 2^8 (as in
 //              the other attention kernels), so that O is rarely rescaled
-// With T = 2 the two tiles' products and softmax alternate and a page is converted once
-// for both; with T = 1 two units' scores do.
+// Two chains of S, softmax, P V run side by side, so that one's products run under the
+// other's softmax: with T = 2 the chains are the two tiles, for which a page is converted
+// once; with T = 1 they are the even and the odd pages of one tile, each with sums and
+// outputs of its own, which are joined at the end.  A job is a chain's work on a page.
 // A row's node is a 64-bit mask of its path; shifted to a page's tokens it says what the
 // row sees there.  Values that are not finite among the nodes' own tokens are kept out of
 // the products (0 * Inf) and make NaN of the rows that see them at the end.
@@ -32,31 +34,40 @@
 
 namespace m2 {
 
-constexpr int kTtWarps = 14, kTtThreads = kTtWarps * 32, kTtProducts = 12;
+constexpr int kTtSoft = 8, kTtDeq = 8, kTtProducts = kTtSoft + kTtDeq, kTtCopies = kTtProducts + 1;  // warps
+constexpr int kTtWarps = 20, kTtThreads = kTtWarps * 32;
+// Registers a thread after the hand-over; launched with 96 (65536 / 640, in steps of 8):
+// 256 * 144 + 384 * 64 = 640 * 96.
+constexpr int kTtRegsSoftmax = 144, kTtRegsOther = 64;
+// What a tile costs beside its pages, in pages (loading queries, storing outputs): the spans
+// are cut by the sum.
+constexpr int kTtSetup = 5;
 
 template <int D, int T>
 struct TtCfg {
   static constexpr int kRows = 128 * T;
-  static constexpr int kSoft = 4 * T, kDeq = 12 - kSoft;  // warps
   static constexpr int kUnit = Kv4Block<D>::kBytes;
   static constexpr int kTile = 64 * D * 2;                // a K or V tile
   static constexpr int kTiles = 3;                        // of each
   static constexpr int kStages = D == 128 ? 12 : 16;      // raw pages
   static constexpr int kK = 0, kV = kTiles * kTile, kRing = 2 * kTiles * kTile;
   static constexpr int kShared = kRing + kStages * kUnit;
-  // Tensor-memory columns: S 2 x 64 (P over it), O T x D, Q T x D / 2
-  static constexpr uint32_t kTmO = 128, kTmQ = 128 + T * D;
+  // Tensor-memory columns: S 2 x 64 (P over it), O 2 x D, Q T x D / 2
+  static constexpr uint32_t kTmO = 128, kTmQ = 128 + 2 * D;
   static_assert(kTmQ + T * D / 2 <= 512, "tensor memory");
   static constexpr int kRecord = 2 * kRows + kRows * D;   // floats: maxima, sums, outputs
 };
 struct TtShared {
-  uint64_t raw_full[16], raw_empty[16], k_full[3], k_empty[3], v_full[3], v_empty[3];
-  uint64_t s_full[2], p_full[2], o_done[2];  // by slot: jobs (unit, tile) alternate
+  uint64_t raw_full[16], raw_empty[16], full[3], empty[3];  // raw pages; K and V tiles of a page
+  uint64_t s_full[2], p_full[2];  // by chain
   uint64_t q_full, fin;
+  uint64_t merge_full, merge_empty;  // T = 1: the second chain's maxima and sums
   uint64_t bad[8];        // by unit: tokens with values that are not finite
   uint8_t group[8][64];   // and their groups of 16 channels
   int32_t ok[16];         // by raw page: it is one
   int32_t seen[8];        // by unit: likewise
+  float m1[128], l1[128];  // T = 1: the second chain's maxima and sums,
+  uint32_t odd1[128];      // and its rows' groups that are NaN
   int32_t cta_seg[2], scan[kTtWarps], span[2], run_b, run_base;
   uint32_t tmem;
 };
@@ -66,8 +77,19 @@ constexpr int tt_smem_bytes() {
   return TtCfg<D, T>::kShared + (int)sizeof(TtShared) + 1024;
 }
 
-__device__ __forceinline__ bool tt_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+// A bounded wait of a whole warp, which stays together.  Inline and without an asked-for
+// time: mbar_wait's suspended waits ended some 900 cycles late, and a unit takes 1500.
+__device__ __forceinline__ bool tt_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  const bool suspend = limit >= 1000000;  // a shorter limit than a suspended wait may take: only test
+  while (!__all_sync(0xffffffffu, suspend ? at_try(bar, parity) : mbar_test_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+      record_timeout();
+      return false;
+    }
+  }
+  return true;
 }
 // Four 8 x 8 matrices of 16-bit elements from fragments to rows of 16 bytes: lane l gives row l % 8 of matrix l / 8.
 __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&x)[4]) {
@@ -76,23 +98,38 @@ __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&x)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t tt_max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // A run of consecutive pages of one tile: what a CTA's span consists of.
 struct TtRun {
   AtrCursor cur;
-  int pages, pos, left;  // of the run; the context's length; units left after it
-  __device__ __forceinline__ void set(const AtrArgs& a, int units) {
-    pages = min(units, cur.pages - cur.page);
-    left = units - pages;
+  int pages, pos, left;  // of the run; the context's length; the span's units after it
+  // from the tile's unit `off` on, the first kTtSetup of which are no pages
+  __device__ __forceinline__ void set(const AtrArgs& a, int off, int units) {
+    const int take = min(units, cur.pages + kTtSetup - off);
+    left = units - take;
+    cur.page = max(0, off - kTtSetup);
+    pages = max(0, off + take - kTtSetup) - cur.page;
     pos = a.g.pos[cur.b];
   }
   __device__ __forceinline__ bool next(const AtrArgs& a, int rows) {
-    if (left == 0) return false;
-    cur.page = cur.pages - 1;
-    cur.next(a, rows);
-    set(a, left);
+    do {
+      if (left == 0) return false;
+      cur.page = cur.pages - 1;
+      cur.next(a, rows);
+      set(a, 0, left);
+    } while (pages == 0);
     return true;
   }
 };
+__device__ __forceinline__ int tt_units(const AtrArgs& a, int b, int rows) {
+  const int n = atr_len(a.g, b);
+  return n ? ((n + kPage - 1) / kPage + kTtSetup) * a.g.c.Hkv * atr_tiles(a, b, rows) : 0;
+}
 
 template <int D, int T>
 __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __grid_constant__ AtrArgs a) {
@@ -103,15 +140,15 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
   uint8_t* smem = raw_smem + (1024 - (smem_addr(raw_smem) & 1023)) % 1024;
   TtShared* sh = reinterpret_cast<TtShared*>(smem + C::kShared);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const long long limit = *reinterpret_cast<volatile long long*>(&g_wait_limit);
+  auto tt_wait = [&](uint64_t* bar, uint32_t parity) { return tt_wait_until(bar, parity, limit); };
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(&sh->raw_full[i], 1), mbar_init(&sh->raw_empty[i], C::kDeq);
-    for (int i = 0; i < NT; ++i) {
-      mbar_init(&sh->k_full[i], C::kDeq), mbar_init(&sh->v_full[i], C::kDeq);
-      mbar_init(&sh->k_empty[i], 1), mbar_init(&sh->v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) mbar_init(&sh->s_full[i], 1), mbar_init(&sh->p_full[i], 4), mbar_init(&sh->o_done[i], 1);
-    mbar_init(&sh->q_full, C::kSoft);
+    for (int i = 0; i < S; ++i) mbar_init(&sh->raw_full[i], 1), mbar_init(&sh->raw_empty[i], kTtDeq);
+    for (int i = 0; i < NT; ++i) mbar_init(&sh->full[i], kTtDeq), mbar_init(&sh->empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh->s_full[i], 1), mbar_init(&sh->p_full[i], 4);
+    mbar_init(&sh->q_full, kTtSoft);
     mbar_init(&sh->fin, 1);
+    mbar_init(&sh->merge_full, 4), mbar_init(&sh->merge_empty, 4);
     sh->cta_seg[0] = sh->cta_seg[1] = -1;
     fence_mbar_init();
   }
@@ -121,7 +158,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
   const int B = a.g.t.nseq;
   // ---- the span: prefix sums of the sequences' units (one a thread)
   static_assert(kSeqs <= kTtThreads, "a sequence a thread");
-  const int mine = tid < B ? atr_units(a, tid, C::kRows) : 0;
+  const int mine = tid < B ? tt_units(a, tid, C::kRows) : 0;
   int pre = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -171,71 +208,88 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
   const uint32_t tmem = sh->tmem;
   const int units = s1 - s0;
   TtRun run;
+  bool work = false;
   if (units > 0) {
     run.cur.b = sh->run_b;
     run.cur.load(a, C::kRows);
+    const int all = run.cur.pages + kTtSetup;
     int in = s0 - sh->run_base;
-    run.cur.hk = in / (run.cur.tiles * run.cur.pages);
-    in -= run.cur.hk * (run.cur.tiles * run.cur.pages);
-    run.cur.tile = in / run.cur.pages;
-    run.cur.page = in - run.cur.tile * run.cur.pages;
-    run.set(a, units);
-    if (warp < C::kSoft) {
+    run.cur.hk = in / (run.cur.tiles * all);
+    in -= run.cur.hk * (run.cur.tiles * all);
+    run.cur.tile = in / all;
+    run.set(a, in - run.cur.tile * all, units);
+    work = run.pages > 0 || run.next(a, C::kRows);
+  }
+  if (work) {
+    if (warp < kTtSoft) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTtRegsSoftmax));
       // ------------------------------------------------ softmax and output
-      const int t = warp >> 2, x = 32 * warp + lane;  // the tile of 128, the row
+      // ch: the chain; x: the row of the CTA's 128 * T
+      const int ch = warp >> 2, x = T == 2 ? 32 * warp + lane : 32 * (warp & 3) + lane;
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t to = tmem + lanes + C::kTmO + t * D, tq = tmem + lanes + C::kTmQ + t * (D / 2);
+      const uint32_t ts = tmem + lanes + 64 * ch, to = tmem + lanes + C::kTmO + ch * D;
+      const uint32_t tq = tmem + lanes + C::kTmQ + (T == 2 ? ch * (D / 2) : 0);
       uint64_t tree[2];
-      int tree_b = -1, u = 0;  // units before the run
+      int tree_b = -1, u = 0, done = 0;  // units and runs before this one
       bool dead = false;
       do {
         const int b = run.cur.b, rows = atr_nodes(a.g, b) * a.G, first = a.g.t.cu[b];
+        const int xr = run.cur.tile * C::kRows + x, node = min(xr, rows - 1) / a.G, h = min(xr, rows - 1) - node * a.G;
+        const bool alive = xr < rows;
+        const uint4* q = reinterpret_cast<const uint4*>(a.g.q + (size_t)(first + node) * a.g.ld_q +
+                                                        (size_t)(run.cur.hk * a.G + h) * D);
+        uint4 v[D / 8];  // the row, on its way while the tree is looked through
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = alive ? q[i] : make_uint4(0u, 0u, 0u, 0u);
         if (b != tree_b) {
           tree_b = b;
           tree_masks(a.g.t.parent + first, atr_nodes(a.g, b), lane, tree);
         }
-        const int xr = run.cur.tile * C::kRows + x, node = min(xr, rows - 1) / a.G, h = min(xr, rows - 1) - node * a.G;
         const uint64_t path = tree_mask_of(tree, node);
-        const bool alive = xr < rows;
         const uint64_t mask = alive ? path : 0ull;
-        float qs;
-        {
-          uint32_t w[D / 2];
+        const bool some = __any_sync(0xffffffffu, mask != 0);  // else nothing of this warp is read
+        float qs = 1.0f;
+        if (some) {
+          // magnitudes of bf16 compare as integers (of a NaN too, which makes all of the row NaN either way)
+          uint32_t top2 = 0;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (mask)
-              v = *reinterpret_cast<const uint4*>(a.g.q + (size_t)(first + node) * a.g.ld_q +
-                                                  (size_t)(run.cur.hk * a.G + h) * D + 8 * i);
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            top2 = tt_max2(tt_max2(top2, tt_max2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu)),
+                           tt_max2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
           }
-          float top = 0.0f, f;
+          float f;
+          kv4_query_scale(__uint_as_float(max(top2 << 16, top2 & 0xFFFF0000u)), a.g.scale, f, qs);
+          if (T == 2 || ch == 0) {
+            // column 8g + 4h + c holds channels 16g + 4c + 2h and the next.  (Rolled, the row from L1: this code runs
+            // once a tile, and fetching its instructions took longer than running it.)
+#pragma unroll 1
+            for (int g = 0; g < D / 32; ++g) {
+              uint32_t w[16], y[16];
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
-          kv4_query_scale(top, a.g.scale, f, qs);
-          // column 8g + 4h + c holds channels 16g + 4c + 2h and the next
+              for (int i = 0; i < 4; ++i) {
+                const uint4 z = mask ? q[4 * g + i] : make_uint4(0u, 0u, 0u, 0u);
+                w[4 * i] = z.x, w[4 * i + 1] = z.y, w[4 * i + 2] = z.z, w[4 * i + 3] = z.w;
+              }
 #pragma unroll
-          for (int g = 0; g < D / 32; ++g) {
-            uint32_t y[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t z = w[16 * g + (i & 8) + 2 * (i & 3) + (i >> 2 & 1)];
-              y[i] = pack_f16x2(bf16lo(z) * f, bf16hi(z) * f);
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t z = w[(i & 8) + 2 * (i & 3) + (i >> 2 & 1)];
+                y[i] = pack_f16x2(bf16lo(z) * f, bf16hi(z) * f);
+              }
+              tmem_st16(tq + 16 * g, y);
             }
-            tmem_st16(tq + 16 * g, y);
+            tmem_st_wait();
           }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->q_full);
         }
-        const bool some = __any_sync(0xffffffffu, mask != 0);  // else nothing of this warp is read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_full);
         float m = -INFINITY, l = 0.0f;
         uint32_t odd = 0;  // groups of channels that are NaN
-        for (int k = 0; k < run.pages; ++k) {
-          const int un = u + k, j = T * un + t, slot = j & 1, base = (run.cur.page + k) * kPage - run.pos;
-          const uint32_t ts = tmem + lanes + 64 * slot;
-          if (!tt_wait(&sh->s_full[slot], (j >> 1) & 1)) {
+        const int k0 = T == 2 ? 0 : (u ^ ch) & 1;  // T = 1: the chain's first page of the run
+        int last = -1;                             // and its last unit
+        for (int k = k0; k < run.pages; k += T == 2 ? 1 : 2) {
+          const int un = u + k, nth = T == 2 ? un : un >> 1, base = (run.cur.page + k) * kPage - run.pos;
+          if (!tt_wait(&sh->s_full[ch], nth & 1)) {
             dead = true;
             break;
           }
@@ -244,8 +298,8 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
             float s[64];
             tmem_ld32_async(ts, s);
             tmem_ld32_async(ts + 32, s + 32);
-            tmem_ld_wait<64>(s);
             const bool there = sh->seen[un & 7] != 0;
+            tmem_ld_wait<64>(s);
             if (base > -kPage || !there) {
               uint64_t see = base >= 0 ? mask >> base : base > -kPage ? mask << -base | ((1ull << -base) - 1) : ~0ull;
               if (!there) see = 0;
@@ -261,13 +315,12 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
 #pragma unroll
             for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
             const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;  // qs > 0
-            if (k == 0) {
+            if (last < 0) {
               m = mn;
             } else {
               const bool grow = mn - m > 8.0f;
               if (__any_sync(0xffffffffu, grow)) {  // rescale what was summed so far, its products complete
-                const int p = j - T;
-                if (!tt_wait(&sh->o_done[p & 1], (p >> 1) & 1)) {
+                if (!tt_wait(&sh->empty[last % NT], (last / NT) & 1)) {
                   dead = true;
                   break;
                 }
@@ -305,67 +358,106 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
             l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
             tmem_st_wait();
           }
+          last = un;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+          if (lane == 0) mbar_arrive(&sh->p_full[ch]);
         }
         if (dead) break;
         // ---- the tile leaves this CTA, whole or in part
         u += run.pages;
-        const int last = T * (u - 1) + t, seg = run.cur.seg(a);
-        const bool before = run.cur.page > 0, after = run.cur.page + run.pages < run.cur.pages;
-        if (!tt_wait(&sh->o_done[last & 1], (last >> 1) & 1)) {
+        const int seg = run.cur.seg(a);
+        const bool before = run.cur.page > 0, part = before || run.cur.page + run.pages < run.cur.pages;
+        if (last >= 0 && !tt_wait(&sh->empty[last % NT], (last / NT) & 1)) {
           dead = true;
           break;
         }
         tc_fence_after();
-        if (mask == 0) l = 0.0f, m = -INFINITY;
-        if (some) {
-          const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
-          float* rec = a.cta_part + (size_t)(2 * cta + (before ? 0 : 1)) * C::kRecord;
-          uint16_t* out = a.g.out + (size_t)(first + node) * a.g.ld_o + (size_t)(run.cur.hk * a.G + h) * D;
-          if (before || after) rec[x] = m, rec[C::kRows + x] = l;
-#pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            float o[32];
-            tmem_ld32_async(to + i, o);
-            tmem_ld_wait<32>(o);
-            if (mask == 0) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-            } else if (odd) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (odd >> (i / 16 + e / 16) & 1u) o[e] = __int_as_float(0x7FFFFFFF);
+        float f0 = 1.0f, f1 = 0.0f;  // the chains' weights
+        if (T == 1) {
+          if (ch == 1) {
+            sh->m1[x] = m, sh->l1[x] = l, sh->odd1[x] = odd;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->merge_full);
+            // (not ahead into the next run, whose arrivals would count for this one's)
+            if (!tt_wait(&sh->merge_empty, done++ & 1)) {
+              dead = true;
+              break;
             }
-            if (!alive) continue;
-            if (before || after) {
-              float* d = rec + 2 * C::kRows + (size_t)x * D + i;
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            continue;
+          }
+          if (!tt_wait(&sh->merge_full, done++ & 1)) {
+            dead = true;
+            break;
+          }
+          tc_fence_after();
+          if (run.pages > 1 || last < 0) {
+            const float m1 = sh->m1[x], l1 = sh->l1[x], top = fmaxf(m, m1);
+            // (a chain without a page has outputs of an earlier run: they are not looked at)
+            f0 = last >= 0 ? ad_weight(m, l, top) : 0.0f, f1 = ad_weight(m1, l1, top);
+            l = l * f0 + l1 * f1;
+            m = top;
+            odd |= sh->odd1[x];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->merge_empty);
+        }
+        const bool first_chain = T == 2 || last >= 0, second_chain = T == 1 && (run.pages > 1 || last < 0);
+        if (mask == 0) l = 0.0f, m = -INFINITY;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
+        float* rec = a.cta_part + (size_t)(2 * cta + (before ? 0 : 1)) * C::kRecord;
+        uint16_t* out = a.g.out + (size_t)(first + node) * a.g.ld_o + (size_t)(run.cur.hk * a.G + h) * D;
+        if (part && alive) rec[x] = m, rec[C::kRows + x] = l;
+        if (__any_sync(0xffffffffu, alive)) {
+#pragma unroll 1
+          for (int i = 0; i < D; i += 16) {
+            float o[16];
+            if (first_chain) {
+              tmem_ld16(to + i, o);
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
+              for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+            }
+            if (second_chain) {
+              float p[16];
+              tmem_ld16(to + D + i, p);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = first_chain ? o[e] * f0 + p[e] * f1 : p[e] * f1;
+            }
+            if (mask == 0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+            } else if (odd >> (i / 16) & 1u) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __int_as_float(0x7FFFFFFF);
+            }
+            if (!alive) {
+            } else if (part) {
+              float* d = rec + 2 * C::kRows + (size_t)x * D + i;
+#pragma unroll
+              for (int e = 0; e < 16; e += 8) {
+                uint32_t y[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) y[c] = __float_as_uint(o[e + c]);
+                store32(reinterpret_cast<uint16_t*>(d + e), y);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 8)
                 *reinterpret_cast<uint4*>(out + i + e) =
                     make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
             }
+            __syncwarp();  // the next load is the whole warp's
           }
-        } else if (alive && !(before || after)) {  // places without a node, a whole warp of them
-          uint16_t* out = a.g.out + (size_t)(first + node) * a.g.ld_o + (size_t)(run.cur.hk * a.G + h) * D;
-          for (int i = 0; i < D; i += 8) *reinterpret_cast<uint4*>(out + i) = make_uint4(0u, 0u, 0u, 0u);
-        } else if (alive) {
-          float* rec = a.cta_part + (size_t)(2 * cta + (before ? 0 : 1)) * C::kRecord;
-          rec[x] = m, rec[C::kRows + x] = l;
-          for (int i = 0; i < D; i += 4)
-            *reinterpret_cast<float4*>(rec + 2 * C::kRows + (size_t)x * D + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        if ((before || after) && tid == 0) sh->cta_seg[before ? 0 : 1] = seg;
+        if (part && tid == 0) sh->cta_seg[before ? 0 : 1] = seg;
       } while (run.next(a, C::kRows));
-    } else if (warp < 12) {
-      // ------------------------------------------------ dequant
-      const int w0 = warp - C::kSoft, r = lane >> 2, c = lane & 3, mr = lane & 7, mq = lane >> 3;
+    } else if (warp < kTtProducts) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtRegsOther));
+      // ------------------------------------------------ dequant: 8 tokens of K and of V a warp
+      const int blk = warp - kTtSoft, r = lane >> 2, c = lane & 3, mr = lane & 7, mq = lane >> 3;
       int u = 0;
       bool dead = false;
       do {
@@ -373,145 +465,126 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
           const int st = u % S, kb = u % NT, page = run.cur.page + k;
           const int base = page * kPage - run.pos, left = run.cur.len - page * kPage;
           const uint8_t* raw = smem + C::kRing + st * C::kUnit;
-          if (!tt_wait(&sh->raw_full[st], (u / S) & 1) ||
-              (u >= NT && !tt_wait(&sh->k_empty[kb], (u / NT - 1) & 1))) {
+          if (!tt_wait(&sh->raw_full[st], (u / S) & 1)) {
             dead = true;
             break;
           }
           const bool ok = sh->ok[st] != 0;
-          if (w0 == 0 && lane == 0) sh->seen[u & 7] = ok;
-          const uint32_t ktile = smem_addr(smem + C::kK + kb * C::kTile), vtile = smem_addr(smem + C::kV + kb * C::kTile);
-#pragma unroll
-          for (int blk = w0; blk < 8; blk += C::kDeq) {  // 8 tokens
-            uint32_t code[GW], sc[GW / 2];
-            const int tok = 8 * blk + r;
-            lds_words<GW>(raw + L::kK + tok * (D / 2) + c * (D / 8), code);
-            lds_words<GW / 2>(raw + L::kKs + tok * (D / 16), sc);
-#pragma unroll
-            for (int w = 0; w < GW; ++w) {
-              const uint32_t e = scales02(sc[w / 2], kScaleBits), f = scales13(sc[w / 2], kScaleBits);
-              uint32_t x[4];
-              codes4(code[w], x);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                x[i] = w & 1 ? hmul2_hi(x[i], i < 2 ? e : f) : hmul2_lo(x[i], i < 2 ? e : f);
-                if (!ok) x[i] = 0u;
-              }
-              stsm4(ktile + sw128_chunk(64, 8 * blk + mr, 4 * w + mq), x);
-            }
-            if (base > -kPage) {
-              // tokens with values that are not finite, of those that hold any
-              uint32_t vs[GW], g0 = 0, g1 = 0;
-              lds_words<GW>(raw + L::kVs + (4 * blk + c) * (D / 8), vs);
-#pragma unroll
-              for (int w = 0; w < GW; ++w) {
-                const uint32_t z = vs[w] & 0xF8F8F8F8u;
-                g0 |= ((z & 0xFFu) == 0xF8u ? 1u : 0u) << (2 * w) | ((z & 0xFF00u) == 0xF800u ? 2u : 0u) << (2 * w);
-                g1 |= ((z & 0xFF0000u) == 0xF80000u ? 1u : 0u) << (2 * w) | ((z & 0xFF000000u) == 0xF8000000u ? 2u : 0u) << (2 * w);
-              }
-              const int t0 = 8 * blk + 2 * c;
-              if (!ok || t0 >= left) g0 = 0;
-              if (!ok || t0 + 1 >= left) g1 = 0;
-              const uint32_t b0 = __ballot_sync(0xffffffffu, g0 != 0) & 15u, b1 = __ballot_sync(0xffffffffu, g1 != 0) & 15u;
-              if (r == 0) sh->group[u & 7][t0] = (uint8_t)g0, sh->group[u & 7][t0 + 1] = (uint8_t)g1;
-              uint32_t bits = 0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) bits |= (b0 >> i & 1u) << (2 * i) | (b1 >> i & 1u) << (2 * i + 1);
-              if (lane == 0) reinterpret_cast<uint8_t*>(&sh->bad[u & 7])[blk] = (uint8_t)bits;
-            }
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->k_full[kb]);
-          if (u >= NT && !tt_wait(&sh->v_empty[kb], (u / NT - 1) & 1)) {
+          const uint32_t there = ok ? kScaleBits : 0u;  // scales of a page that is none are 0
+          uint32_t kc[GW], ks[GW / 2], vc[GW], vs[GW];
+          const int tok = 8 * blk + r, t0 = 8 * blk + 2 * c;
+          lds_words<GW>(raw + L::kK + tok * (D / 2) + c * (D / 8), kc);
+          lds_words<GW / 2>(raw + L::kKs + tok * (D / 16), ks);
+          lds_words<GW>(raw + L::kV + blk * (4 * D) + r * (D / 2) + c * (D / 8), vc);
+          lds_words<GW>(raw + L::kVs + (4 * blk + c) * (D / 8), vs);
+          if (u >= NT && !tt_wait(&sh->empty[kb], (u / NT - 1) & 1)) {
             dead = true;
             break;
           }
+          const uint32_t vtile = smem_addr(smem + C::kV + kb * C::kTile) + mr * 128 + ((blk ^ mr) << 4);
 #pragma unroll
-          for (int blk = w0; blk < 8; blk += C::kDeq) {
-            uint32_t code[GW], vs[GW];
-            lds_words<GW>(raw + L::kV + blk * (4 * D) + r * (D / 2) + c * (D / 8), code);
-            lds_words<GW>(raw + L::kVs + (4 * blk + c) * (D / 8), vs);
-            uint32_t bits = kScaleBits;  // slots past the last token may hold any scale: theirs become 0
-            if (left < kPage) {
-              const int t0 = 8 * blk + 2 * c;
-              bits = (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
-            }
-            if (!ok) bits = 0u;
+          for (int w = 0; w < GW; ++w) {
+            const uint32_t e = scales02(ks[w / 2], there), f = scales13(ks[w / 2], there);
+            uint32_t x[4];
+            codes4(kc[w], x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = w & 1 ? hmul2_hi(x[i], i < 2 ? e : f) : hmul2_lo(x[i], i < 2 ? e : f);
+            // chunk 4w + mq of the row (its low three bits are swizzled by the row's)
+            stsm4(smem_addr(smem + C::kK + kb * C::kTile) + sw128_chunk(64, 8 * blk + mr, 4 * w + mq), x);
+          }
+          uint32_t bits = there;  // slots past the last token may hold any scale: theirs become 0
+          if (left < kPage) bits &= (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
+          const bool nodes = base > -kPage;
+#pragma unroll
+          for (int w = 0; w < GW; ++w) {
+            uint32_t e = scales02(vs[w], bits), f = scales13(vs[w], bits);
+            if (nodes) e = kv4_finite(e), f = kv4_finite(f);
+            uint32_t x[4];
+            codes4(vc[w], x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], i < 2 ? e : f);
+            stsm4(vtile + (4 * w + mq) * 1024, x);  // channels 8 (4w + mq) + mr
+          }
+          if (nodes) {
+            // tokens with values that are not finite, of those that hold any
+            uint32_t g0 = 0, g1 = 0;
 #pragma unroll
             for (int w = 0; w < GW; ++w) {
-              uint32_t e = scales02(vs[w], bits), f = scales13(vs[w], bits);
-              if (base > -kPage) e = kv4_finite(e), f = kv4_finite(f);
-              uint32_t x[4];
-              codes4(code[w], x);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], i < 2 ? e : f);
-              stsm4(vtile + sw128_chunk(D, 8 * (4 * w + mq) + mr, blk), x);
+              const uint32_t z = vs[w] & 0xF8F8F8F8u;
+              g0 |= ((z & 0xFFu) == 0xF8u ? 1u : 0u) << (2 * w) | ((z & 0xFF00u) == 0xF800u ? 2u : 0u) << (2 * w);
+              g1 |= ((z & 0xFF0000u) == 0xF80000u ? 1u : 0u) << (2 * w) | ((z & 0xFF000000u) == 0xF8000000u ? 2u : 0u) << (2 * w);
             }
+            if (!ok || t0 >= left) g0 = 0;
+            if (!ok || t0 + 1 >= left) g1 = 0;
+            const uint32_t b0 = __ballot_sync(0xffffffffu, g0 != 0) & 15u, b1 = __ballot_sync(0xffffffffu, g1 != 0) & 15u;
+            if (r == 0) sh->group[u & 7][t0] = (uint8_t)g0, sh->group[u & 7][t0 + 1] = (uint8_t)g1;
+            uint32_t marks = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) marks |= (b0 >> i & 1u) << (2 * i) | (b1 >> i & 1u) << (2 * i + 1);
+            if (lane == 0) reinterpret_cast<uint8_t*>(&sh->bad[u & 7])[blk] = (uint8_t)marks;
           }
+          if (blk == 0 && lane == 0) sh->seen[u & 7] = ok;
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&sh->v_full[kb]);
+            mbar_arrive(&sh->full[kb]);
             mbar_arrive(&sh->raw_empty[st]);
           }
         }
       } while (!dead && run.next(a, C::kRows));
-    } else if (warp == kTtProducts) {
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtRegsOther));
+    if (warp == kTtProducts) {
       // ------------------------------------------------ products
+      // Operand addresses reach the products through uniform registers: what they are made of is
+      // broadcast from a lane, which the compiler takes as uniform.
       const int leader = elect_one();
-      const uint32_t k0 = smem_addr(smem + C::kK) >> 4, v0 = smem_addr(smem + C::kV) >> 4;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t k0 = __shfl_sync(0xffffffffu, smem_addr(smem + C::kK) >> 4, 0), v0 = k0 + ((C::kV - C::kK) >> 4);
       int u = 0, runs = 0;
       bool dead = false;
-      // scores of job j = (unit, tile)
+      // scores of job j = (unit, tile); the unit's K is there
       auto scores = [&](int j) {
-        const int un = j / T, t = j % T, kb = un % NT;
-        if (t == 0 && !tt_wait(&sh->k_full[kb], (un / NT) & 1)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + 64 * (j & 1), q = tmem + C::kTmQ + t * (D / 2), k = k0 + kb * (C::kTile >> 4);
+        const int t = j % T, kb = j / T % NT;
+        const uint32_t d = tm + 64 * (j & 1), q = tm + C::kTmQ + t * (D / 2), k = k0 + kb * (C::kTile >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
           at_mma_ts(d, q + 8 * i, at_desc((k + (i >> 2) * (64 * 128 >> 4) + (i & 3) * 2) | (1u << 16)), tc_idesc_f16(128, 64),
                     i > 0, leader);
         at_commit(&sh->s_full[j & 1], leader);
-        if (t == T - 1) at_commit(&sh->k_empty[kb], leader);
-        return true;
       };
+      auto there = [&](int un) { return tt_wait(&sh->full[un % NT], (un / NT) & 1); };
       do {
-        const int j0 = T * u, j1 = T * (u + run.pages);
-        if (!tt_wait(&sh->q_full, runs++ & 1)) {
+        const int pages = __shfl_sync(0xffffffffu, run.pages, 0), j0 = T * u, j1 = T * (u + pages);
+        if (!tt_wait(&sh->q_full, runs++ & 1) || !there(u) || (T == 1 && pages > 1 && !there(u + 1))) {
           dead = true;
           break;
         }
         tc_fence_after();
-        if (!scores(j0) || (j0 + 1 < j1 && !scores(j0 + 1))) {
-          dead = true;
-          break;
-        }
+        scores(j0);
+        if (j0 + 1 < j1) scores(j0 + 1);
         for (int j = j0; j < j1; ++j) {
-          const int un = j / T, t = j % T, kb = un % NT;
-          if (!tt_wait(&sh->p_full[j & 1], (j >> 1) & 1) || (t == 0 && !tt_wait(&sh->v_full[kb], (un / NT) & 1))) {
+          // P V of this job, then the chain's next scores, whose operands are waited for ahead of P
+          const int un = j / T, t = j % T, vb = un % NT, chain = j & 1;
+          const bool more = j + 2 < j1;
+          if ((t == 0 && more && !there((j + 2) / T)) || !tt_wait(&sh->p_full[chain], (T == 2 ? un : un >> 1) & 1)) {
             dead = true;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + C::kTmO + t * D, p = tmem + 64 * (j & 1), v = v0 + kb * (C::kTile >> 4);
+          const uint32_t d = tm + C::kTmO + chain * D, p = tm + 64 * chain, v = v0 + vb * (C::kTile >> 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            at_mma_ts(d, p + 8 * i, at_desc((v + 2 * i) | (1u << 16)), tc_idesc_f16(128, D), un > u || i > 0, leader);
-          at_commit(&sh->o_done[j & 1], leader);
-          if (t == T - 1) at_commit(&sh->v_empty[kb], leader);
-          if (j + 2 < j1 && !scores(j + 2)) {
-            dead = true;
-            break;
-          }
+            at_mma_ts(d, p + 8 * i, at_desc((v + 2 * i) | (1u << 16)), tc_idesc_f16(128, D), j >= j0 + 2 || i > 0, leader);
+          if (t == T - 1) at_commit(&sh->empty[vb], leader);
+          if (more) scores(j + 2);
         }
-        u += run.pages;
+        u += pages;
       } while (!dead && run.next(a, C::kRows));
       at_commit(&sh->fin, leader);  // everything issued here is done before tensor memory is freed
       __syncwarp();
-      mbar_drain(&sh->fin, 0);
-    } else {
+      tt_wait_until(&sh->fin, 0, kWaitCycles);
+    } else if (warp == kTtCopies) {
       // ------------------------------------------------ copies
       const uint64_t pol = a.most_tiles > 1 ? policy_evict_normal() : policy_evict_first();
       int u = 0;
@@ -544,7 +617,8 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
       } while (!dead && run.next(a, C::kRows));
       // every copy has landed before the CTA ends
       for (int i = max(0, u - S); i < u; ++i)
-        if (!mbar_drain(&sh->raw_full[i % S], (i / S) & 1)) break;
+        if (!tt_wait_until(&sh->raw_full[i % S], (i / S) & 1, kWaitCycles)) break;
+    }
     }
   }
   tc_fence_before();

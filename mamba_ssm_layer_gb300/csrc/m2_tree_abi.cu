@@ -227,8 +227,8 @@ int m2_attn_tree_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q,
   a.H = H;
   a.scale = scale;
   a.ws = ws;
-  // units (pages x tiles of at least 16 rows x kv heads) are counted in 32 bits
-  if ((int64_t)(cache->nseq < kSeqs ? cache->nseq : kSeqs) * cache->ld_table > INT32_MAX / (4ll * H + 4 * cache->n_kv_heads))
+  // units (pages and what a tile costs beside them, x tiles of at least 16 rows x kv heads) are counted in 32 bits
+  if ((cache->nseq < kSeqs ? cache->nseq : kSeqs) * (cache->ld_table + 8ll) > INT32_MAX / (4ll * H + 4 * cache->n_kv_heads))
     return M2_ERR_UNSUPPORTED;
   for (int32_t i0 = 0; i0 < cache->nseq; i0 += kSeqs) {
     a.t = tree_of(cu_nodes, cache->nseq, i0, parent);
