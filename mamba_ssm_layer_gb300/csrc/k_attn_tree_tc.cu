@@ -34,11 +34,8 @@
 
 namespace m2 {
 
-constexpr int kTtSoft = 8, kTtDeq = 8, kTtProducts = kTtSoft + kTtDeq, kTtCopies = kTtProducts + 1;  // warps
-constexpr int kTtWarps = 20, kTtThreads = kTtWarps * 32;
-// Registers a thread after the hand-over; launched with 96 (65536 / 640, in steps of 8):
-// 256 * 144 + 384 * 64 = 640 * 96.
-constexpr int kTtRegsSoftmax = 144, kTtRegsOther = 64;
+constexpr int kTtSoft = 8, kTtDeq = 4, kTtProducts = kTtSoft + kTtDeq, kTtCopies = kTtProducts + 1;  // warps
+constexpr int kTtWarps = 14, kTtThreads = kTtWarps * 32;
 // What a tile costs beside its pages, in pages (loading queries, storing outputs): the spans
 // are cut by the sum.
 constexpr int kTtSetup = 5;
@@ -48,8 +45,8 @@ struct TtCfg {
   static constexpr int kRows = 128 * T;
   static constexpr int kUnit = Kv4Block<D>::kBytes;
   static constexpr int kTile = 64 * D * 2;                // a K or V tile
-  static constexpr int kTiles = 3;                        // of each
-  static constexpr int kStages = D == 128 ? 12 : 16;      // raw pages
+  static constexpr int kTiles = 4;                        // of each
+  static constexpr int kStages = D == 128 ? 9 : 16;       // raw pages
   static constexpr int kK = 0, kV = kTiles * kTile, kRing = 2 * kTiles * kTile;
   static constexpr int kShared = kRing + kStages * kUnit;
   // Tensor-memory columns: S 2 x 64 (P over it), O 2 x D, Q T x D / 2
@@ -58,7 +55,7 @@ struct TtCfg {
   static constexpr int kRecord = 2 * kRows + kRows * D;   // floats: maxima, sums, outputs
 };
 struct TtShared {
-  uint64_t raw_full[16], raw_empty[16], full[3], empty[3];  // raw pages; K and V tiles of a page
+  uint64_t raw_full[16], raw_empty[16], full[4], empty[4];  // raw pages; K and V tiles of a page
   uint64_t s_full[2], p_full[2];  // by chain
   uint64_t q_full, fin;
   uint64_t merge_full, merge_empty;  // T = 1: the second chain's maxima and sums
@@ -222,7 +219,6 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
   }
   if (work) {
     if (warp < kTtSoft) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTtRegsSoftmax));
       // ------------------------------------------------ softmax and output
       // ch: the chain; x: the row of the CTA's 128 * T
       const int ch = warp >> 2, x = T == 2 ? 32 * warp + lane : 32 * (warp & 3) + lane;
@@ -455,9 +451,8 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
         if (part && tid == 0) sh->cta_seg[before ? 0 : 1] = seg;
       } while (run.next(a, C::kRows));
     } else if (warp < kTtProducts) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtRegsOther));
-      // ------------------------------------------------ dequant: 8 tokens of K and of V a warp
-      const int blk = warp - kTtSoft, r = lane >> 2, c = lane & 3, mr = lane & 7, mq = lane >> 3;
+      // ------------------------------------------------ dequant: 16 tokens of K and of V a warp
+      const int w0 = warp - kTtSoft, r = lane >> 2, c = lane & 3, mr = lane & 7, mq = lane >> 3;
       int u = 0;
       bool dead = false;
       do {
@@ -471,59 +466,69 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
           }
           const bool ok = sh->ok[st] != 0;
           const uint32_t there = ok ? kScaleBits : 0u;  // scales of a page that is none are 0
-          uint32_t kc[GW], ks[GW / 2], vc[GW], vs[GW];
-          const int tok = 8 * blk + r, t0 = 8 * blk + 2 * c;
-          lds_words<GW>(raw + L::kK + tok * (D / 2) + c * (D / 8), kc);
-          lds_words<GW / 2>(raw + L::kKs + tok * (D / 16), ks);
-          lds_words<GW>(raw + L::kV + blk * (4 * D) + r * (D / 2) + c * (D / 8), vc);
-          lds_words<GW>(raw + L::kVs + (4 * blk + c) * (D / 8), vs);
+          uint32_t kc[2][GW], ks[2][GW / 2], vc[2][GW], vs[2][GW];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int blk = w0 + kTtDeq * n;
+            lds_words<GW>(raw + L::kK + (8 * blk + r) * (D / 2) + c * (D / 8), kc[n]);
+            lds_words<GW / 2>(raw + L::kKs + (8 * blk + r) * (D / 16), ks[n]);
+            lds_words<GW>(raw + L::kV + blk * (4 * D) + r * (D / 2) + c * (D / 8), vc[n]);
+            lds_words<GW>(raw + L::kVs + (4 * blk + c) * (D / 8), vs[n]);
+          }
           if (u >= NT && !tt_wait(&sh->empty[kb], (u / NT - 1) & 1)) {
             dead = true;
             break;
           }
-          const uint32_t vtile = smem_addr(smem + C::kV + kb * C::kTile) + mr * 128 + ((blk ^ mr) << 4);
-#pragma unroll
-          for (int w = 0; w < GW; ++w) {
-            const uint32_t e = scales02(ks[w / 2], there), f = scales13(ks[w / 2], there);
-            uint32_t x[4];
-            codes4(kc[w], x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = w & 1 ? hmul2_hi(x[i], i < 2 ? e : f) : hmul2_lo(x[i], i < 2 ? e : f);
-            // chunk 4w + mq of the row (its low three bits are swizzled by the row's)
-            stsm4(smem_addr(smem + C::kK + kb * C::kTile) + sw128_chunk(64, 8 * blk + mr, 4 * w + mq), x);
-          }
-          uint32_t bits = there;  // slots past the last token may hold any scale: theirs become 0
-          if (left < kPage) bits &= (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
           const bool nodes = base > -kPage;
+          const uint32_t ktile = smem_addr(smem + C::kK + kb * C::kTile), vtile = smem_addr(smem + C::kV + kb * C::kTile);
 #pragma unroll
-          for (int w = 0; w < GW; ++w) {
-            uint32_t e = scales02(vs[w], bits), f = scales13(vs[w], bits);
-            if (nodes) e = kv4_finite(e), f = kv4_finite(f);
-            uint32_t x[4];
-            codes4(vc[w], x);
+          for (int n = 0; n < 2; ++n) {
+            const int blk = w0 + kTtDeq * n, t0 = 8 * blk + 2 * c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], i < 2 ? e : f);
-            stsm4(vtile + (4 * w + mq) * 1024, x);  // channels 8 (4w + mq) + mr
+            for (int w = 0; w < GW; ++w) {
+              const uint32_t e = scales02(ks[n][w / 2], there), f = scales13(ks[n][w / 2], there);
+              uint32_t x[4];
+              codes4(kc[n][w], x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = w & 1 ? hmul2_hi(x[i], i < 2 ? e : f) : hmul2_lo(x[i], i < 2 ? e : f);
+              stsm4(ktile + sw128_chunk(64, 8 * blk + mr, 4 * w + mq), x);
+            }
+            uint32_t bits = there;  // slots past the last token may hold any scale: theirs become 0
+            if (left < kPage) bits &= (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
+#pragma unroll
+            for (int w = 0; w < GW; ++w) {
+              uint32_t e = scales02(vs[n][w], bits), f = scales13(vs[n][w], bits);
+              if (nodes) e = kv4_finite(e), f = kv4_finite(f);
+              uint32_t x[4];
+              codes4(vc[n][w], x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], i < 2 ? e : f);
+              stsm4(vtile + mr * 128 + ((blk ^ mr) << 4) + (4 * w + mq) * 1024, x);  // channels 8 (4w + mq) + mr
+            }
           }
           if (nodes) {
             // tokens with values that are not finite, of those that hold any
-            uint32_t g0 = 0, g1 = 0;
 #pragma unroll
-            for (int w = 0; w < GW; ++w) {
-              const uint32_t z = vs[w] & 0xF8F8F8F8u;
-              g0 |= ((z & 0xFFu) == 0xF8u ? 1u : 0u) << (2 * w) | ((z & 0xFF00u) == 0xF800u ? 2u : 0u) << (2 * w);
-              g1 |= ((z & 0xFF0000u) == 0xF80000u ? 1u : 0u) << (2 * w) | ((z & 0xFF000000u) == 0xF8000000u ? 2u : 0u) << (2 * w);
+            for (int n = 0; n < 2; ++n) {
+              const int blk = w0 + kTtDeq * n, t0 = 8 * blk + 2 * c;
+              uint32_t g0 = 0, g1 = 0;
+#pragma unroll
+              for (int w = 0; w < GW; ++w) {
+                const uint32_t z = vs[n][w] & 0xF8F8F8F8u;
+                g0 |= ((z & 0xFFu) == 0xF8u ? 1u : 0u) << (2 * w) | ((z & 0xFF00u) == 0xF800u ? 2u : 0u) << (2 * w);
+                g1 |= ((z & 0xFF0000u) == 0xF80000u ? 1u : 0u) << (2 * w) | ((z & 0xFF000000u) == 0xF8000000u ? 2u : 0u) << (2 * w);
+              }
+              if (!ok || t0 >= left) g0 = 0;
+              if (!ok || t0 + 1 >= left) g1 = 0;
+              const uint32_t b0 = __ballot_sync(0xffffffffu, g0 != 0) & 15u, b1 = __ballot_sync(0xffffffffu, g1 != 0) & 15u;
+              if (r == 0) sh->group[u & 7][t0] = (uint8_t)g0, sh->group[u & 7][t0 + 1] = (uint8_t)g1;
+              uint32_t marks = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) marks |= (b0 >> i & 1u) << (2 * i) | (b1 >> i & 1u) << (2 * i + 1);
+              if (lane == 0) reinterpret_cast<uint8_t*>(&sh->bad[u & 7])[blk] = (uint8_t)marks;
             }
-            if (!ok || t0 >= left) g0 = 0;
-            if (!ok || t0 + 1 >= left) g1 = 0;
-            const uint32_t b0 = __ballot_sync(0xffffffffu, g0 != 0) & 15u, b1 = __ballot_sync(0xffffffffu, g1 != 0) & 15u;
-            if (r == 0) sh->group[u & 7][t0] = (uint8_t)g0, sh->group[u & 7][t0 + 1] = (uint8_t)g1;
-            uint32_t marks = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) marks |= (b0 >> i & 1u) << (2 * i) | (b1 >> i & 1u) << (2 * i + 1);
-            if (lane == 0) reinterpret_cast<uint8_t*>(&sh->bad[u & 7])[blk] = (uint8_t)marks;
           }
-          if (blk == 0 && lane == 0) sh->seen[u & 7] = ok;
+          if (w0 == 0 && lane == 0) sh->seen[u & 7] = ok;
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
@@ -532,9 +537,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
           }
         }
       } while (!dead && run.next(a, C::kRows));
-    } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtRegsOther));
-    if (warp == kTtProducts) {
+    } else if (warp == kTtProducts) {
       // ------------------------------------------------ products
       // Operand addresses reach the products through uniform registers: what they are made of is
       // broadcast from a lane, which the compiler takes as uniform.
@@ -564,10 +567,10 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
         scores(j0);
         if (j0 + 1 < j1) scores(j0 + 1);
         for (int j = j0; j < j1; ++j) {
-          // P V of this job, then the chain's next scores, whose operands are waited for ahead of P
+          // P V of this job, then the chain's next scores
           const int un = j / T, t = j % T, vb = un % NT, chain = j & 1;
           const bool more = j + 2 < j1;
-          if ((t == 0 && more && !there((j + 2) / T)) || !tt_wait(&sh->p_full[chain], (T == 2 ? un : un >> 1) & 1)) {
+          if (!tt_wait(&sh->p_full[chain], (T == 2 ? un : un >> 1) & 1)) {
             dead = true;
             break;
           }
@@ -577,7 +580,15 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
           for (int i = 0; i < 4; ++i)
             at_mma_ts(d, p + 8 * i, at_desc((v + 2 * i) | (1u << 16)), tc_idesc_f16(128, D), j >= j0 + 2 || i > 0, leader);
           if (t == T - 1) at_commit(&sh->empty[vb], leader);
-          if (more) scores(j + 2);
+          if (!more) continue;
+          if (t == 0) {
+            if (!there((j + 2) / T)) {
+              dead = true;
+              break;
+            }
+            tc_fence_after();
+          }
+          scores(j + 2);
         }
         u += pages;
       } while (!dead && run.next(a, C::kRows));
@@ -618,7 +629,6 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
       // every copy has landed before the CTA ends
       for (int i = max(0, u - S); i < u; ++i)
         if (!tt_wait_until(&sh->raw_full[i % S], (i / S) & 1, kWaitCycles)) break;
-    }
     }
   }
   tc_fence_before();
