@@ -1,18 +1,18 @@
 // k_attn_tree.cu -- attention of a tree of drafted tokens over the paged 4-bit cache
-// (include/mamba2.h has the rule of what a node sees).
+// (include/mamba2.h has the rule of what a node sees), for few rows: nodes x query heads
+// of a kv head at most 16.  k_attn_tree_tc.cu serves more.
 //
-// A unit is one page (64 tokens) of one kv head for one tile of rows: 16 R rows, row m
-// = node m / G with query head m % G of the group.  The units of all sequences, in the
-// order (sequence, kv head, tile, page), are cut into equal spans, one a CTA, and each
-// span into equal runs, one a stream.  A stream is R warps of 16 rows each, which read
-// the same ring of bulk copies; 12 / R streams a CTA.  In a warp, on warp MMA:
-//   S [16 x 64 tokens] = Q K^T    K codes become f16 and take their scale, exactly
+// A unit is one page (64 tokens) of one kv head; row m is node m / G with query head m % G
+// of the group.  The units of all sequences, in the order (sequence, kv head, page), are
+// cut into equal spans, one a CTA, and each span into equal runs, one a warp, which streams
+// them through its own ring of bulk copies.  On warp MMA, half a page at a time:
+//   S [16 x 32 tokens] = Q K^T    K codes become f16 and take their scale, exactly
 //   O [16 x D] += P V             likewise V; P rounded to f16 (2^-11)
 // The pages' orders of codes are those of both products' B operands, P goes from the
 // first to the second in registers.  Queries are f16 rows prescaled by an exact power of
 // two.  Scores, sums and outputs are fp32.  A row's node is a 64-bit mask of its path;
-// shifted to a page's tokens it says what the row sees there.  Rows that a stream, then
-// a CTA, holds only in part are joined: streams through shared memory, CTAs by
+// shifted to a page's tokens it says what the row sees there.  Rows that a warp, then a
+// CTA, holds only in part are joined: warps through shared memory, CTAs by
 // attn_tree_combine.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -29,27 +29,27 @@ namespace m2 {
 
 constexpr int kAtWarps = 12, kAtrThreads = kAtWarps * 32;
 
-template <int D, int R>
+constexpr int kAtrRows = 16, kAtrParts = 2 * kAtWarps;  // a warp leaves a first and a last part at most
+
+template <int D>
 struct AtrCfg {
   static constexpr int kUnit = Kv4Block<D>::kBytes;
-  static constexpr int kStreams = kAtWarps / R, kRows = 16 * R;
-  static constexpr int kStages = (D == 128 ? 2 : 4) * R;  // 12 warps' worth of 18 KB
-  static constexpr int kRing = kStages * kUnit;           // of one stream
-  static constexpr int kStride = D + 8;                   // floats between the rows of a record: no bank conflicts
-  static constexpr int kRecord = 2 * kRows + kRows * kStride;  // maxima, sums, outputs
-  static constexpr int kParts = 2 * kStreams;             // a stream leaves a first and a last part at most
+  static constexpr int kStages = D == 128 ? 2 : 4;  // 12 warps * stages * unit = 216 KB
+  static constexpr int kRing = kStages * kUnit;     // of one warp
+  static constexpr int kStride = D + 8;             // floats between the rows of a record: no bank conflicts
+  static constexpr int kRecord = 2 * kAtrRows + kAtrRows * kStride;  // maxima, sums, outputs
 };
 // Which row tile a partial belongs to, and whether it starts before / ends after the CTA's span.
 struct AtrMeta {
   int32_t seg, before, after;
 };
 struct AtrShared {
-  uint64_t full[kAtWarps * 4], empty[kAtWarps * 4];
-  int32_t ok[kAtWarps * 4];
-  AtrMeta meta[2 * kAtWarps];
-  float part_m[kAtrThreads], part_l[kAtrThreads];  // [part][row]: maxima (then weights) and sums
-  float row_l[kAtrThreads];                        // [cut tile][row]
-  uint32_t row_parts[2 * kAtWarps];
+  uint64_t full[kAtWarps][4];
+  int32_t ok[kAtWarps][4];
+  AtrMeta meta[kAtrParts];
+  float part_m[kAtrParts][kAtrRows], part_l[kAtrParts][kAtrRows];  // maxima (then weights) and sums
+  float row_l[kAtrParts][kAtrRows];                                // sums of the cut tiles
+  uint32_t row_parts[kAtrParts];
   int32_t cta_seg[2];
   int32_t scan[kAtWarps];
   int32_t run0[kAtWarps + 1], run_b[kAtWarps], run_base[kAtWarps];
@@ -64,33 +64,39 @@ struct AtrRows {
   uint64_t seen[2];       // the rows' paths; 0: no such row
   float o[D / 8][4];      // channels 8i + 2c, + 1 of rows r, r + 8
 
-  // Rows m0 .. m0 + 15 of sequence b, kv head hk; tree: the sequence's masks.
-  __device__ __forceinline__ void start(const AtrArgs& a, int b, int hk, int m0, const uint64_t (&tree)[2], int lane) {
-    const int r = lane >> 2, c = lane & 3, first = a.g.t.cu[b], rows = atr_nodes(a.g, b) * a.G;
+  // The rows of sequence b for kv head hk.  tree: the sequence's masks, worked out here while the queries are on
+  // their way (again: they are another sequence's).
+  __device__ __forceinline__ void start(const AtrArgs& a, int b, int hk, uint64_t (&tree)[2], bool again, int lane) {
+    const int r = lane >> 2, c = lane & 3, first = a.g.t.cu[b], n = atr_nodes(a.g, b), rows = n * a.G;
+    uint2 w[2][D / 16];
+    int node[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int x = m0 + r + 8 * k, node = min(x, rows - 1) / a.G, h = x - node * a.G;
-      const uint64_t path = tree_mask_of(tree, node);
-      seen[k] = x < rows ? path : 0ull;
-      uint2 w[D / 16];
+      const int x = r + 8 * k;
+      node[k] = min(x, rows - 1) / a.G;
+      const uint2* q0 = reinterpret_cast<const uint2*>(a.g.q + (size_t)(first + node[k]) * a.g.ld_q +
+                                                       (size_t)(hk * a.G + min(x, rows - 1) - node[k] * a.G) * D + 4 * c);
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) w[k][g] = x < rows ? q0[4 * g] : make_uint2(0u, 0u);
+    }
+    if (again) tree_masks(a.g.t.parent + first, n, lane, tree);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint64_t path = tree_mask_of(tree, node[k]);
+      seen[k] = r + 8 * k < rows ? path : 0ull;
       float top = 0.0f;
 #pragma unroll
-      for (int g = 0; g < D / 16; ++g) {
-        w[g] = make_uint2(0u, 0u);
-        if (seen[k])
-          w[g] = *reinterpret_cast<const uint2*>(a.g.q + (size_t)(first + node) * a.g.ld_q + (size_t)(hk * a.G + h) * D +
-                                                 16 * g + 4 * c);
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w[g].x)), fabsf(bf16hi(w[g].x))),
-                               fmaxf(fabsf(bf16lo(w[g].y)), fabsf(bf16hi(w[g].y)))));
-      }
+      for (int g = 0; g < D / 16; ++g)
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w[k][g].x)), fabsf(bf16hi(w[k][g].x))),
+                               fmaxf(fabsf(bf16lo(w[k][g].y)), fabsf(bf16hi(w[k][g].y)))));
       float f;
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       kv4_query_scale(top, a.g.scale, f, qs[k]);
 #pragma unroll
       for (int g = 0; g < D / 16; ++g) {
-        q[g][k] = pack_f16x2(bf16lo(w[g].x) * f, bf16hi(w[g].x) * f);
-        q[g][2 + k] = pack_f16x2(bf16lo(w[g].y) * f, bf16hi(w[g].y) * f);
+        q[g][k] = pack_f16x2(bf16lo(w[k][g].x) * f, bf16hi(w[k][g].x) * f);
+        q[g][2 + k] = pack_f16x2(bf16lo(w[k][g].y) * f, bf16hi(w[k][g].y) * f);
       }
       m[k] = -INFINITY, l[k] = 0.0f;
     }
@@ -101,46 +107,15 @@ struct AtrRows {
   }
 
   // One unit in shared memory.  base: its first token less the context's length (0 or
-  // more: only nodes; -64 or less: only context); left: tokens of the sequence from its first on.
+  // more: only nodes; -64 or less: only context); left: tokens of the sequence from its
+  // first on.  Half a page at a time: with a whole one's scores registers were spilled.
   __device__ __forceinline__ void unit(const uint8_t* u, int base, int left, int lane) {
     using L = Kv4Block<D>;
     constexpr int GW = D / 32;  // words of a lane's codes: 2 groups each
     const int r = lane >> 2, c = lane & 3;
-    float s[8][4];
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      uint32_t k[GW], sc[GW / 2];
-      const int t = 8 * nt + r;
-      lds_words<GW>(u + L::kK + t * (D / 2) + c * (D / 8), k);
-      lds_words<GW / 2>(u + L::kKs + t * (D / 16), sc);
-#pragma unroll
-      for (int w = 0; w < GW; ++w) {
-        const uint32_t e = scales02(sc[w / 2], kScaleBits), f = scales13(sc[w / 2], kScaleBits);
-        uint32_t x[4];
-        codes4(k[w], x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = w & 1 ? hmul2_hi(x[i], i < 2 ? e : f) : hmul2_lo(x[i], i < 2 ? e : f);
-        if (w == 0)
-          mma_f16_first(s[nt], q[0][0], q[0][1], q[0][2], q[0][3], x[0], x[1]);
-        else
-          mma_f16(s[nt], q[2 * w][0], q[2 * w][1], q[2 * w][2], q[2 * w][3], x[0], x[1]);
-        mma_f16(s[nt], q[2 * w + 1][0], q[2 * w + 1][1], q[2 * w + 1][2], q[2 * w + 1][3], x[2], x[3]);
-      }
-    }
-    // what the rows see of the page, by token
     const bool part = base > -kPage;
-    uint64_t see[2] = {~0ull, ~0ull};
     uint64_t bad = 0;  // tokens with values that are not finite, some group of them
     if (part) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        see[k] = base >= 0 ? seen[k] >> base : seen[k] << -base | ((1ull << -base) - 1);
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (!(see[k] >> (8 * nt + 2 * c + j) & 1)) s[nt][2 * k + j] = -INFINITY;
-      }
       uint32_t vs[GW];  // of token pair `lane`: bytes (even, even, odd, odd)
       lds_words<GW>(u + L::kVs + lane * (D / 8), vs);
       uint32_t even = 0, odd = 0;
@@ -154,71 +129,119 @@ struct AtrRows {
       if (be | bo)
         for (int t = 0; t < 32; ++t) bad |= (uint64_t)((be >> t & 1) | (bo >> t & 1) << 1) << (2 * t);
     }
-    // softmax: P becomes the second product's A operand.  qs > 0: maxima are taken before it is applied.
-    bool grow = false;
-    float mx[2];
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      float s[4][4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      mx[k] = fmaxf(s[0][2 * k], s[0][2 * k + 1]);
+      for (int nt = 0; nt < 4; nt += 2) {  // two tiles of 8 tokens in turn: a product waits for the one before it on its sums
+        uint32_t k[2][GW], sc[2][GW / 2];
 #pragma unroll
-      for (int nt = 1; nt < 8; ++nt) mx[k] = fmaxf(mx[k], fmaxf(s[nt][2 * k], s[nt][2 * k + 1]));
-      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-      mx[k] *= qs[k];
-      grow |= mx[k] - m[k] > 8.0f;
-    }
-    // the reference follows the maximum once it has grown 2^8: until then P (with its
-    // factor 2^7, which keeps small ones out of f16's subnormals) stays below 2^15
-    if (__any_sync(0xffffffffu, grow)) {
-      float f[2];
+        for (int h = 0; h < 2; ++h) {
+          const int t = 32 * half + 8 * (nt + h) + r;
+          lds_words<GW>(u + L::kK + t * (D / 2) + c * (D / 8), k[h]);
+          lds_words<GW / 2>(u + L::kKs + t * (D / 16), sc[h]);
+        }
+#pragma unroll
+        for (int w = 0; w < GW; ++w) {
+          uint32_t x[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t e = scales02(sc[h][w / 2], kScaleBits), f = scales13(sc[h][w / 2], kScaleBits);
+            codes4(k[h][w], x[h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[h][i] = w & 1 ? hmul2_hi(x[h][i], i < 2 ? e : f) : hmul2_lo(x[h][i], i < 2 ? e : f);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (w == 0)
+              mma_f16_first(s[nt + h], q[0][0], q[0][1], q[0][2], q[0][3], x[h][0], x[h][1]);
+            else
+              mma_f16(s[nt + h], q[2 * w][0], q[2 * w][1], q[2 * w][2], q[2 * w][3], x[h][0], x[h][1]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma_f16(s[nt + h], q[2 * w + 1][0], q[2 * w + 1][1], q[2 * w + 1][2], q[2 * w + 1][3], x[h][2], x[h][3]);
+        }
+      }
+      if (part) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint64_t see = base >= 0 ? seen[k] >> base : seen[k] << -base | ((1ull << -base) - 1);
+          const uint32_t bits = (uint32_t)(see >> (32 * half)) >> (2 * c);
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (!(bits >> (8 * nt + j) & 1u)) s[nt][2 * k + j] = -INFINITY;
+        }
+      }
+      // softmax: P becomes the second product's A operand.  qs > 0: maxima are taken before it is applied.
+      bool grow = false;
+      float mx[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const bool up = mx[k] - m[k] > 8.0f;
-        f[k] = up ? ad_ex2(m[k] - mx[k]) : 1.0f;
-        if (up) m[k] = mx[k];
-        l[k] *= f[k];
+        mx[k] = fmaxf(s[0][2 * k], s[0][2 * k + 1]);
+#pragma unroll
+        for (int nt = 1; nt < 4; ++nt) mx[k] = fmaxf(mx[k], fmaxf(s[nt][2 * k], s[nt][2 * k + 1]));
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+        mx[k] *= qs[k];
+        grow |= mx[k] - m[k] > 8.0f;
+      }
+      // the reference follows the maximum once it has grown 2^8: until then P (with its
+      // factor 2^7, which keeps small ones out of f16's subnormals) stays below 2^15
+      if (__any_sync(0xffffffffu, grow)) {
+        float f[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool up = mx[k] - m[k] > 8.0f;
+          f[k] = up ? ad_ex2(m[k] - mx[k]) : 1.0f;
+          if (up) m[k] = mx[k];
+          l[k] *= f[k];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
+      }
+      uint32_t p[2][4];
+      const float b0 = m[0] == -INFINITY ? 0.0f : 7.0f - m[0], b1 = m[1] == -INFINITY ? 0.0f : 7.0f - m[1];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const float x0 = ad_ex2(fmaf(s[nt][0], qs[0], b0)), x1 = ad_ex2(fmaf(s[nt][1], qs[0], b0));
+        const float x2 = ad_ex2(fmaf(s[nt][2], qs[1], b1)), x3 = ad_ex2(fmaf(s[nt][3], qs[1], b1));
+        l[0] += x0 + x1;
+        l[1] += x2 + x3;
+        p[nt / 2][nt % 2 * 2] = pack_f16x2(x0, x1);
+        p[nt / 2][nt % 2 * 2 + 1] = pack_f16x2(x2, x3);
       }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int ks = 0; ks < 2; ++ks) {
+        const int blk = 4 * half + 2 * ks;  // 8 tokens; and the next 8
+        uint32_t v0[GW], v1[GW], s0[GW], s1[GW];
+        lds_words<GW>(u + L::kV + blk * (4 * D) + r * (D / 2) + c * (D / 8), v0);
+        lds_words<GW>(u + L::kV + (blk + 1) * (4 * D) + r * (D / 2) + c * (D / 8), v1);
+        lds_words<GW>(u + L::kVs + (4 * blk + c) * (D / 8), s0);
+        lds_words<GW>(u + L::kVs + (4 * blk + 4 + c) * (D / 8), s1);
+        uint32_t k0 = kScaleBits, k1 = kScaleBits;  // slots past the last token may hold any scale: theirs become 0
+        if (part) {
+          const int t0 = 8 * blk + 2 * c, t1 = t0 + 8;
+          k0 = (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
+          k1 = (t1 < left ? 0x7F80u : 0u) | (t1 + 1 < left ? 0x7F800000u : 0u);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
-    }
-    uint32_t p[4][4];
-    const float b0 = m[0] == -INFINITY ? 0.0f : 7.0f - m[0], b1 = m[1] == -INFINITY ? 0.0f : 7.0f - m[1];
+        for (int w = 0; w < GW; ++w) {
+          uint32_t e0 = scales02(s0[w], k0), f0 = scales13(s0[w], k0), e1 = scales02(s1[w], k1), f1 = scales13(s1[w], k1);
+          if (bad) e0 = kv4_finite(e0), f0 = kv4_finite(f0), e1 = kv4_finite(e1), f1 = kv4_finite(f1);
+          uint32_t x[4], y[4];
+          codes4(v0[w], x);
+          codes4(v1[w], y);
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float x0 = ad_ex2(fmaf(s[nt][0], qs[0], b0)), x1 = ad_ex2(fmaf(s[nt][1], qs[0], b0));
-      const float x2 = ad_ex2(fmaf(s[nt][2], qs[1], b1)), x3 = ad_ex2(fmaf(s[nt][3], qs[1], b1));
-      l[0] += x0 + x1;
-      l[1] += x2 + x3;
-      p[nt / 2][nt % 2 * 2] = pack_f16x2(x0, x1);
-      p[nt / 2][nt % 2 * 2 + 1] = pack_f16x2(x2, x3);
-    }
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t v0[GW], v1[GW], s0[GW], s1[GW];
-      lds_words<GW>(u + L::kV + (2 * ks) * (4 * D) + r * (D / 2) + c * (D / 8), v0);
-      lds_words<GW>(u + L::kV + (2 * ks + 1) * (4 * D) + r * (D / 2) + c * (D / 8), v1);
-      lds_words<GW>(u + L::kVs + (8 * ks + c) * (D / 8), s0);
-      lds_words<GW>(u + L::kVs + (8 * ks + 4 + c) * (D / 8), s1);
-      uint32_t k0 = kScaleBits, k1 = kScaleBits;  // slots past the last token may hold any scale: theirs become 0
-      if (part) {
-        const int t0 = 16 * ks + 2 * c, t1 = t0 + 8;
-        k0 = (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
-        k1 = (t1 < left ? 0x7F80u : 0u) | (t1 + 1 < left ? 0x7F800000u : 0u);
-      }
-#pragma unroll
-      for (int w = 0; w < GW; ++w) {
-        uint32_t e0 = scales02(s0[w], k0), f0 = scales13(s0[w], k0), e1 = scales02(s1[w], k1), f1 = scales13(s1[w], k1);
-        if (bad) e0 = kv4_finite(e0), f0 = kv4_finite(f0), e1 = kv4_finite(e1), f1 = kv4_finite(f1);
-        uint32_t x[4], y[4];
-        codes4(v0[w], x);
-        codes4(v1[w], y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = hmul2(x[i], i < 2 ? e0 : f0);
-          y[i] = hmul2(y[i], i < 2 ? e1 : f1);
-          mma_f16(o[4 * w + i], p[ks][0], p[ks][1], p[ks][2], p[ks][3], x[i], y[i]);
+          for (int i = 0; i < 4; ++i) {
+            x[i] = hmul2(x[i], i < 2 ? e0 : f0);
+            y[i] = hmul2(y[i], i < 2 ? e1 : f1);
+            mma_f16(o[4 * w + i], p[ks][0], p[ks][1], p[ks][2], p[ks][3], x[i], y[i]);
+          }
         }
       }
     }
@@ -229,8 +252,11 @@ struct AtrRows {
       for (int g = 0; g < D / 16; ++g)
         if ((u[L::vs(t, g)] & 0xF8u) == 0xF8u) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (see[j >> 1] >> t & 1) o[2 * g][j] = o[2 * g + 1][j] = __int_as_float(0x7FFFFFFF);
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t path = seen[j >> 1];
+            const bool see = base + t < 0 || path >> (base + t) & 1;
+            if (see) o[2 * g][j] = o[2 * g + 1][j] = __int_as_float(0x7FFFFFFF);
+          }
         }
     }
   }
@@ -248,22 +274,21 @@ struct AtrRows {
       }
     }
   }
-  // pm, pl, out: of the warp's first row
-  __device__ __forceinline__ void store_part(float* out, float* pm, float* pl, int stride, int lane) const {
+  __device__ __forceinline__ void store_part(float* out, float* pm, float* pl, int lane) const {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (c == 0) pm[r + 8 * k] = m[k], pl[r + 8 * k] = l[k];
-      float* d = out + (r + 8 * k) * stride + 2 * c;
+      float* d = out + (r + 8 * k) * AtrCfg<D>::kStride + 2 * c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(o[i][2 * k], o[i][2 * k + 1]);
     }
   }
-  __device__ __forceinline__ void store_out(const AtrArgs& a, int b, int hk, int m0, int lane) const {
+  __device__ __forceinline__ void store_out(const AtrArgs& a, int b, int hk, int lane) const {
     const int r = lane >> 2, c = lane & 3, rows = atr_nodes(a.g, b) * a.G;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int x = m0 + r + 8 * k, node = x / a.G;
+      const int x = r + 8 * k, node = x / a.G;
       if (x >= rows) continue;
       const float inv = l[k] != 0.0f ? 1.0f / l[k] : 0.0f;  // nothing seen: zeros
       uint16_t* d = a.g.out + (size_t)(a.g.t.cu[b] + node) * a.g.ld_o + (size_t)(hk * a.G + x - node * a.G) * D + 2 * c;
@@ -274,29 +299,25 @@ struct AtrRows {
   }
 };
 
-template <int D, int R>
+template <int D>
 __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_constant__ AtrArgs a) {
-  using C = AtrCfg<D, R>;
-  constexpr int S = C::kStages, ST = C::kStreams, ROWS = C::kRows, PARTS = C::kParts;
-  static_assert(PARTS * ROWS == kAtrThreads && PARTS <= 32 && ST * S <= kAtWarps * 4, "a thread per part and row");
-  static_assert(C::kRecord * 4 <= C::kRing, "a record lies in its stream's ring");
+  using C = AtrCfg<D>;
+  constexpr int S = C::kStages, ROWS = kAtrRows, PARTS = kAtrParts;
+  static_assert(PARTS * ROWS == kAtrThreads && PARTS <= 32 && S <= 4, "a thread per part and row");
+  static_assert(C::kRecord * 4 <= C::kRing, "a record lies in its warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
-  AtrShared* sh = reinterpret_cast<AtrShared*>(smem + ST * C::kRing);
+  AtrShared* sh = reinterpret_cast<AtrShared*>(smem + kAtWarps * C::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-  const int stream = warp / R, rw = warp % R;  // rows 16 rw .. of the stream's tile
-  uint64_t* full = sh->full + stream * S;
-  uint64_t* empty = sh->empty + stream * S;
-  int32_t* ok = sh->ok + stream * S;
-  if (rw == 0 && lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], R);
-    sh->meta[2 * stream].seg = sh->meta[2 * stream + 1].seg = -1;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&sh->full[warp][s], 1);
+    sh->meta[2 * warp].seg = sh->meta[2 * warp + 1].seg = -1;
     fence_mbar_init();
   }
   if (tid < 2) sh->cta_seg[tid] = -1;
   pdl_wait();
   pdl_trigger();
   const int B = a.g.t.nseq;
-  // ---- the span and its runs: prefix sums of the sequences' units (one a thread: kSeqs <= 384)
+  // ---- the span and its runs: prefix sums of the sequences' units (one a thread)
   static_assert(kSeqs <= kAtrThreads, "a sequence a thread");
   const int mine = tid < B ? atr_units(a, tid, ROWS) : 0;
   int pre = mine;
@@ -315,30 +336,29 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
     total += sh->scan[w];
   }
   int s0, s1;
-  if (a.by_row) {  // tile cta % rows of sequence cta / rows
-    const int rows = a.g.c.Hkv * a.most_tiles, b = cta / rows, row = cta - b * rows;
+  if (a.by_row) {  // kv head cta % Hkv of sequence cta / Hkv
+    const int b = cta / a.g.c.Hkv;
     if (tid == b) {
-      const int tiles = atr_tiles(a, b, ROWS), n = tiles ? mine / (a.g.c.Hkv * tiles) : 0;
-      const bool in = row < a.g.c.Hkv * tiles;
-      sh->run0[0] = pre + (in ? row * n : 0);
-      sh->run0[1] = sh->run0[0] + (in ? n : 0);
+      const int n = mine / a.g.c.Hkv;
+      sh->run0[0] = pre + (cta - b * a.g.c.Hkv) * n;
+      sh->run0[1] = sh->run0[0] + n;
     }
     __syncthreads();
     s0 = sh->run0[0];
     s1 = sh->run0[1];
     __syncthreads();
   } else {
-    // at least a unit for every stream: the CTAs without work are the last ones
-    const int nc = min(a.nc, (total + ST - 1) / ST), q = nc ? total / nc : 0, extra = total - q * nc;
+    // at least a unit for every warp: the CTAs without work are the last ones
+    const int nc = min(a.nc, (total + kAtWarps - 1) / kAtWarps), q = nc ? total / nc : 0, extra = total - q * nc;
     s0 = cta < nc ? q * cta + min(cta, extra) : total;
     s1 = cta < nc ? s0 + q + (cta < extra ? 1 : 0) : total;
   }
   {
     // run w: its share of the span, the first ones a unit longer
-    const int q = (s1 - s0) / ST, extra = s1 - s0 - q * ST;
-    if (tid <= ST) sh->run0[tid] = s0 + q * tid + min(tid, extra);
+    const int q = (s1 - s0) / kAtWarps, extra = s1 - s0 - q * kAtWarps;
+    if (tid <= kAtWarps) sh->run0[tid] = s0 + q * tid + min(tid, extra);
     if (mine && pre < s1 && pre + mine > s0)
-      for (int w = 0; w < ST; ++w) {
+      for (int w = 0; w < kAtWarps; ++w) {
         const int u = s0 + q * w + min(w, extra);
         if (u >= pre && u < pre + mine) {
           sh->run_b[w] = tid;
@@ -355,120 +375,98 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
       }
   __syncthreads();
 
-  // ---- this stream's run
-  uint8_t* ring = smem + stream * C::kRing;
-  const int u0 = sh->run0[stream], u1 = sh->run0[stream + 1], n = u1 - u0;
-  bool last = false;  // a part is left at the run's end
-  AtrCursor cur;
-  AtrRows<D> rows;
-  int row_at = 0;     // the tile's first unit
+  // ---- this warp's run
+  uint8_t* ring = smem + warp * C::kRing;
+  const int u0 = sh->run0[warp], u1 = sh->run0[warp + 1], n = u1 - u0;
   if (n > 0) {
-    cur.b = sh->run_b[stream];
+    AtrCursor cur;
+    cur.b = sh->run_b[warp];
     cur.load(a, ROWS);
     {
-      int in = u0 - sh->run_base[stream];
-      cur.hk = in / (cur.tiles * cur.pages);
-      in -= cur.hk * (cur.tiles * cur.pages);
-      cur.tile = in / cur.pages;
-      cur.page = in - cur.tile * cur.pages;
+      const int in = u0 - sh->run_base[warp];
+      cur.tile = 0;
+      cur.hk = in / cur.pages;
+      cur.page = in - cur.hk * cur.pages;
     }
     AtrCursor ahead = cur;
-    const uint64_t pol = a.most_tiles > 1 ? policy_evict_normal() : policy_evict_first();
-    auto fetch = [&](int i) {  // unit i of the run into its stage (the first warp of the stream)
-      const int st = i % S;
+    const uint64_t pol = policy_evict_first();
+    // The page of the next copy, loaded a unit before it is asked for.
+    auto entry = [&]() { return a.g.c.table[(size_t)ahead.b * a.g.c.ld_table + ahead.page]; };
+    int page = entry();
+    int fetched = 0;
+    auto fetch = [&]() {  // unit `fetched` of the run into its stage
+      const int st = fetched % S, hk = ahead.hk, id = page;
+      if (++fetched < n) {
+        ahead.next(a, ROWS);
+        page = entry();
+      }
       if (lane == 0) {
-        const int page = a.g.c.table[(size_t)ahead.b * a.g.c.ld_table + ahead.page];
-        const bool in = page >= 0 && page < a.g.c.n_pages;
-        ok[st] = in;
-        if (in) {
-          mbar_arrive_expect_tx(&full[st], C::kUnit);
-          bulk_g2s(ring + st * C::kUnit, a.g.c.pages + ((size_t)page * a.g.c.Hkv + ahead.hk) * C::kUnit, C::kUnit,
-                   &full[st], pol);
+        const bool ok = id >= 0 && id < a.g.c.n_pages;
+        sh->ok[warp][st] = ok;
+        if (ok) {
+          mbar_arrive_expect_tx(&sh->full[warp][st], C::kUnit);
+          bulk_g2s(ring + st * C::kUnit, a.g.c.pages + ((size_t)id * a.g.c.Hkv + hk) * C::kUnit, C::kUnit,
+                   &sh->full[warp][st], pol);
         } else {
           M2_RECORD_ARG(g_status);
-          mbar_arrive(&full[st]);
+          mbar_arrive(&sh->full[warp][st]);
         }
       }
-      ahead.next(a, ROWS);
     };
-    int fetched = 0;
-    if (rw == 0)
-      for (; fetched < S && fetched < n; ++fetched) fetch(fetched);
-    uint64_t tree[2];
-    int tree_b = cur.b;
-    tree_masks(a.g.t.parent + a.g.t.cu[cur.b], atr_nodes(a.g, cur.b), lane, tree);
-    rows.start(a, cur.b, cur.hk, cur.tile * ROWS + 16 * rw, tree, lane);
-    int first_page = cur.page;  // of the tile's part in this run
-    row_at = u0 - cur.page;
+    while (fetched < S && fetched < n) fetch();
+    uint64_t tree[2] = {0, 0};
+    AtrRows<D> rows;
+    rows.start(a, cur.b, cur.hk, tree, true, lane);
+    int first_page = cur.page;   // of the tile's part in this run
+    int row_at = u0 - cur.page;  // the tile's first unit
     int pos = a.g.pos[cur.b];
     bool dead = false;
     for (int i = 0; i < n; ++i) {
       const int st = i % S;
-      // the stage before the last one is free once the stream's other warps have read it too
-      constexpr int LAG = R > 1 ? 1 : 0;
-      if (rw == 0 && fetched < n && i > LAG && fetched == i - 1 - LAG + S) {
-        const int e = fetched % S;
-        if (R > 1 && !__all_sync(0xffffffffu, mbar_wait(&empty[e], (fetched / S - 1) & 1))) {
-          dead = true;
-          break;
-        }
-        fetch(fetched++);
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / S) & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[warp][st], (i / S) & 1))) {
         dead = true;
         break;
       }
-      if (ok[st]) rows.unit(ring + st * C::kUnit, cur.page * kPage - pos, cur.len - cur.page * kPage, lane);
+      if (sh->ok[warp][st]) rows.unit(ring + st * C::kUnit, cur.page * kPage - pos, cur.len - cur.page * kPage, lane);
       __syncwarp();  // the stage is read
-      if (R > 1 && lane == 0) mbar_arrive(&empty[st]);
+      if (fetched < n) fetch();
       const bool ends = cur.page + 1 == cur.pages;
-      if (ends || i + 1 == n) {  // the tile leaves this stream
+      if (ends || i + 1 == n) {  // the tile leaves this warp
         rows.finish();
         if (ends && first_page == 0) {
-          rows.store_out(a, cur.b, cur.hk, cur.tile * ROWS + 16 * rw, lane);
+          rows.store_out(a, cur.b, cur.hk, lane);
         } else {
-          // an earlier part goes through L2, the last one into the ring once the stream has read it
           const int slot = i + 1 == n ? 1 : 0;
-          last = slot;
-          if (!slot) {
-            const int e = 2 * stream * ROWS + 16 * rw;
-            rows.store_part(a.part + (size_t)(cta * ST + stream) * C::kRecord + 16 * rw * C::kStride, sh->part_m + e,
-                            sh->part_l + e, C::kStride, lane);
-          }
-          if (rw == 0 && lane == 0) {
-            AtrMeta& mt = sh->meta[2 * stream + slot];
+          // the last part goes into the ring (free by now), an earlier one through L2
+          rows.store_part(slot ? reinterpret_cast<float*>(ring) : a.part + (size_t)(cta * kAtWarps + warp) * C::kRecord,
+                          sh->part_m[2 * warp + slot], sh->part_l[2 * warp + slot], lane);
+          if (lane == 0) {
+            AtrMeta& mt = sh->meta[2 * warp + slot];
             mt.seg = cur.seg(a);
             mt.before = row_at < s0;
             mt.after = row_at + cur.pages > s1;
           }
         }
         if (i + 1 < n) {
+          const int b = cur.b;
           cur.next(a, ROWS);
           first_page = 0;
           row_at = u0 + i + 1;
-          if (cur.b != tree_b) {
-            tree_b = cur.b;
-            pos = a.g.pos[cur.b];
-            tree_masks(a.g.t.parent + a.g.t.cu[cur.b], atr_nodes(a.g, cur.b), lane, tree);
-          }
-          rows.start(a, cur.b, cur.hk, cur.tile * ROWS + 16 * rw, tree, lane);
+          pos = a.g.pos[cur.b];
+          rows.start(a, cur.b, cur.hk, tree, cur.b != b, lane);
         }
       } else {
         ++cur.page;
       }
     }
-    if (dead && rw == 0)  // every copy of this stream has landed before the CTA goes on
+    if (dead) {  // every copy of this warp has landed before the CTA goes on
       for (int i = max(0, fetched - S); i < fetched; ++i)
-        if (!mbar_drain(&full[i % S], (i / S) & 1)) break;
-  }
-  __syncthreads();  // every ring is read
-  if (last) {
-    const int e = (2 * stream + 1) * ROWS + 16 * rw;
-    rows.store_part(reinterpret_cast<float*>(ring) + 16 * rw * C::kStride, sh->part_m + e, sh->part_l + e, C::kStride, lane);
+        if (!mbar_drain(&sh->full[warp][i % S], (i / S) & 1)) break;
+    }
   }
   __syncthreads();
 
-  // ---- tiles cut between streams
+  // ---- tiles cut between warps
   const int seg_e = lane < PARTS ? sh->meta[lane].seg : -1;
   const uint32_t same = __match_any_sync(0xffffffffu, seg_e);  // entry `lane`: all parts of its tile
   const uint32_t lead = __ballot_sync(0xffffffffu, seg_e >= 0 && (same & ((1u << lane) - 1)) == 0);
@@ -479,15 +477,15 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
     const uint32_t parts = __shfl_sync(0xffffffffu, same, e & 31);
     if (lead >> e & 1) {
       float top = -INFINITY, l = 0.0f;
-      for (uint32_t y = parts; y; y &= y - 1) top = fmaxf(top, sh->part_m[(__ffs(y) - 1) * ROWS + x]);
+      for (uint32_t y = parts; y; y &= y - 1) top = fmaxf(top, sh->part_m[__ffs(y) - 1][x]);
       for (uint32_t y = parts; y; y &= y - 1) {
-        const int k = (__ffs(y) - 1) * ROWS + x;
-        const float w = ad_weight(sh->part_m[k], sh->part_l[k], top);
-        l += sh->part_l[k] * w;
-        sh->part_m[k] = w;
+        const int k = __ffs(y) - 1;
+        const float w = ad_weight(sh->part_m[k][x], sh->part_l[k][x], top);
+        l += sh->part_l[k][x] * w;
+        sh->part_m[k][x] = w;
       }
       const int k = __popc(lead & ((1u << e) - 1));
-      sh->row_l[k * ROWS + x] = l;
+      sh->row_l[k][x] = l;
       sh->row_parts[k] = parts;
       const AtrMeta& mt = sh->meta[e];
       if (mt.before || mt.after) {  // cut between CTAs too
@@ -517,9 +515,9 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
         w[j] = 0.0f;
         v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (y >= 0) {
-          w[j] = sh->part_m[y * ROWS + x];
+          w[j] = sh->part_m[y][x];
           v[j] = y & 1 ? *reinterpret_cast<const float4*>(smem + (y >> 1) * C::kRing + (x * C::kStride + d) * 4)
-                       : *reinterpret_cast<const float4*>(a.part + (size_t)(cta * ST + (y >> 1)) * C::kRecord +
+                       : *reinterpret_cast<const float4*>(a.part + (size_t)(cta * kAtWarps + (y >> 1)) * C::kRecord +
                                                           x * C::kStride + d);
         }
       }
@@ -532,7 +530,7 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
       *reinterpret_cast<float4*>(a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * C::kRecord + 2 * ROWS +
                                  x * C::kStride + d) = o;
     else
-      atr_store4(out + d, o, sh->row_l[k * ROWS + x]);
+      atr_store4(out + d, o, sh->row_l[k][x]);
   }
   if (tid < 2 && !a.by_row) a.cta_seg[2 * cta + tid] = sh->cta_seg[tid];
 }
@@ -541,9 +539,9 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
 // goes on.  D/4 threads hold four channels each; the parts are dealt out over groups of
 // them and joined through shared memory.
 constexpr int kAtrcThreads = 128;
-template <int D, int R>
+template <int D>
 __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(const __grid_constant__ AtrArgs a) {
-  using C = AtrCfg<D, R>;
+  using C = AtrCfg<D>;
   constexpr int P = D / 4, GR = kAtrcThreads / P;
   __shared__ float pm[GR], pl[GR];
   __shared__ float4 po[kAtrcThreads];
@@ -553,8 +551,8 @@ __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(con
   const int seg = a.cta_seg[2 * c + 1];
   auto load = [&](int y, float& m, float& l, float4& o) {
     const float* r = a.cta_part + (size_t)(y == 0 ? 2 * c + 1 : 2 * min(c + y, a.nc - 1)) * C::kRecord;
-    m = r[x], l = r[C::kRows + x];
-    o = *reinterpret_cast<const float4*>(r + 2 * C::kRows + x * C::kStride + d);
+    m = r[x], l = r[kAtrRows + x];
+    o = *reinterpret_cast<const float4*>(r + 2 * kAtrRows + x * C::kStride + d);
   };
   float m, l;
   float4 o;
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(con
     k += n;
     if (n < kAtrcThreads) break;
   }
-  uint16_t* out = seg < 0 ? nullptr : atr_out(a, seg, x, C::kRows, D);
+  uint16_t* out = seg < 0 ? nullptr : atr_out(a, seg, x, kAtrRows, D);
   if (!out) return;
   if (g >= k) m = -INFINITY, l = 0.0f, o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int y = g + GR; y < k; y += GR) {
@@ -598,30 +596,27 @@ __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(con
 
 // ------------------------------------------------------------------ host
 
-template <int D, int R>
+template <int D>
 static size_t atr_ws_bytes() {
-  using C = AtrCfg<D, R>;
   const size_t n = num_sms();
-  return n * (C::kStreams + 2) * C::kRecord * 4 + (n * 2 * 4 + 255) / 256 * 256;
+  return n * (kAtWarps + 2) * AtrCfg<D>::kRecord * 4 + (n * 2 * 4 + 255) / 256 * 256;
 }
-size_t attn_tree_ws_bytes(int32_t H, int32_t Hkv, int32_t D) {
-  (void)H, (void)Hkv;  // whatever the tile: the largest records
-  const size_t x = D == 128 ? atr_ws_bytes<128, 4>() : atr_ws_bytes<64, 4>(), y = attn_tree_tc_ws_bytes(D);
-  return x > y ? x : y;
+size_t attn_tree_ws_bytes(int32_t D) {
+  const size_t x = D == 128 ? atr_ws_bytes<128>() : atr_ws_bytes<64>(), y = attn_tree_tc_ws_bytes(D);
+  return x > y ? x : y;  // whatever the trees
 }
 
-template <int D, int R>
+template <int D>
 static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
-  using C = AtrCfg<D, R>;
+  using C = AtrCfg<D>;
   static int done_mask[64] = {0};
-  constexpr int smem = C::kStreams * C::kRing + (int)sizeof(AtrShared);
+  constexpr int smem = kAtWarps * C::kRing + (int)sizeof(AtrShared);
   static_assert(smem <= 232448, "shared memory");
-  static_assert((C::kStreams + 2) * C::kRecord <= (AtrCfg<D, 4>::kStreams + 2) * AtrCfg<D, 4>::kRecord, "workspace");
   AtrArgs a;
   a.g = g;
   a.G = g.H / g.c.Hkv;
-  a.most_tiles = (g.most * a.G + C::kRows - 1) / C::kRows;
-  const int64_t tiles = (int64_t)g.t.nseq * g.c.Hkv * a.most_tiles;
+  a.most_tiles = 1;
+  const int64_t tiles = (int64_t)g.t.nseq * g.c.Hkv;
   // Few tiles in a narrow table: a CTA takes a whole tile, and nothing is left to
   // combine.  (The table's width is what the host knows of the lengths.)
   a.by_row = tiles <= num_sms() && g.c.ld_table <= 32;
@@ -629,8 +624,8 @@ static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
   const size_t n = num_sms();
   a.cta_seg = static_cast<int32_t*>(g.ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.ws) + (n * 2 * 4 + 255) / 256 * 256);
-  a.cta_part = a.part + n * C::kStreams * C::kRecord;
-  auto kern = attn_tree_kernel<D, R>;
+  a.cta_part = a.part + n * kAtWarps * C::kRecord;
+  auto kern = attn_tree_kernel<D>;
   cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
   if (e != cudaSuccess) return e;
   trace_pre(K_ATTN_TREE, s);
@@ -638,17 +633,14 @@ static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
   trace_post(K_ATTN_TREE, s);
   if (e != cudaSuccess || a.by_row) return e;
   trace_pre(K_ATTN_TREE_COMBINE, s);
-  e = launch_k(attn_tree_combine_kernel<D, R>, dim3(a.nc, g.most * a.G < C::kRows ? g.most * a.G : C::kRows),
-               dim3(kAtrcThreads), 0, s, true, a);
+  e = launch_k(attn_tree_combine_kernel<D>, dim3(a.nc, g.most * a.G), dim3(kAtrcThreads), 0, s, true, a);
   trace_post(K_ATTN_TREE_COMBINE, s);
   return e;
 }
 
 cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s) {
-  const int rows = a.most * (a.H / a.c.Hkv);
-  if (rows > 16) return launch_attn_tree_tc(a, s);
-  if (a.c.D == 128) return rows <= 16 ? launch_atr<128, 1>(a, s) : rows <= 32 ? launch_atr<128, 2>(a, s) : launch_atr<128, 4>(a, s);
-  return rows <= 16 ? launch_atr<64, 1>(a, s) : rows <= 32 ? launch_atr<64, 2>(a, s) : launch_atr<64, 4>(a, s);
+  if (a.most * (a.H / a.c.Hkv) > kAtrRows) return launch_attn_tree_tc(a, s);
+  return a.c.D == 128 ? launch_atr<128>(a, s) : launch_atr<64>(a, s);
 }
 
 int status_attn_tree(int clear) { return tu_status(clear); }

@@ -507,7 +507,7 @@ struct AttnTreeArgs {
   float scale;
   void* ws;
 };
-size_t attn_tree_ws_bytes(int32_t H, int32_t Hkv, int32_t D);
+size_t attn_tree_ws_bytes(int32_t D);
 cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s);
 // The same on the tensor cores, for many rows (k_attn_tree_tc.cu).
 size_t attn_tree_tc_ws_bytes(int32_t D);

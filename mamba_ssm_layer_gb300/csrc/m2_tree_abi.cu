@@ -201,7 +201,7 @@ int m2_kv4_keep(const m2_kv4_cache* cache, const int32_t* cu_nodes, const int32_
 }
 
 size_t m2_attn_tree_kv4_workspace_bytes(int32_t H, int32_t Hkv, int32_t head_dim) {
-  return check_heads(H, Hkv, head_dim) ? 0 : attn_tree_ws_bytes(H, Hkv, head_dim);
+  return check_heads(H, Hkv, head_dim) ? 0 : attn_tree_ws_bytes(head_dim);
 }
 
 int m2_attn_tree_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q, uint16_t* out, int32_t ld_o,
@@ -218,7 +218,7 @@ int m2_attn_tree_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q,
   if ((st = check_rows(q, ld_q, w)) || (st = check_rows(out, ld_o, w))) return st;
   if (!al4(parent) || !al4(kv_pos)) return M2_ERR_ALIGN;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) ||
-      ws_bytes < attn_tree_ws_bytes(H, cache->n_kv_heads, cache->head_dim))
+      ws_bytes < attn_tree_ws_bytes(cache->head_dim))
     return M2_ERR_WORKSPACE;
   AttnTreeArgs a;
   a.c = kv4_of(cache);
