@@ -415,11 +415,12 @@ template <int N, int MT>
 static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
   static int done_mask[64] = {0};
   const int per = a.H / a.G;
-  // Heads of a CTA: C, B and their product serve all of them; halved until the
-  // CTAs fill the SMs twice.  heads * nodes stays within the path sums' 1024 pairs.
+  // Heads of a CTA: C, B and their product serve all of them, and the loads of the next
+  // one's state run under the current one's products; halved until there are CTAs for
+  // most of the places on the SMs.  heads * nodes stays within the path sums' 1024 pairs.
   int heads = per < 16 ? per : 16;
   while (heads > 1 && (heads * 16 * MT > 1024 ||
-                       (int64_t)a.t.nseq * a.G * ((per + heads - 1) / heads) < 4ll * num_sms()))
+                       2 * (int64_t)a.t.nseq * a.G * ((per + heads - 1) / heads) < (MT == 4 ? 1 : 3) * (int64_t)num_sms()))
     heads = (heads + 1) / 2;
   const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
   auto k = tree_ssm_kernel<N, MT>;
@@ -501,17 +502,20 @@ __device__ __forceinline__ float4 tc_bf4(const uint16_t* p) {
 }
 
 // The steps of the single-token kernel, in its order and arithmetic, with the state
-// in registers: LPR = N/4 lanes a row, ROWS rows a thread.
+// in registers: LPR = N/4 lanes a row, ROWS rows a thread.  What the path's nodes bring
+// (dt and decay, B, this CTA's channels of x) comes into shared memory in one trip, under
+// the state's loads: a CTA's stay is what limits the bytes in flight.
 // Bound: HBM, the state read and written once.
 template <int LPR, int ROWS>
 __global__ void __launch_bounds__(256) tree_state_kernel(const TreeCommitArgs a, int psplit) {
   constexpr int RPW = 32 / LPR, CTA_ROWS = 8 * RPW * ROWS;
+  extern __shared__ __align__(16) uint8_t smem[];  // [nodes] of B (N bf16), of x (CTA_ROWS fp32)
   __shared__ float sdt[kTreeNodes], sda[kTreeNodes];
   __shared__ int srow[kTreeNodes];
-  const int i = blockIdx.y, h = blockIdx.x / psplit, pc = blockIdx.x % psplit;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n4 = (lane % LPR) * 4, g = h / (a.H / a.G);
+  const int i = blockIdx.y, h = blockIdx.x / psplit, pc = blockIdx.x % psplit, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31, n4 = (lane % LPR) * 4, g = h / (a.H / a.G);
   const size_t base = ((size_t)i * a.H + h) * a.P * a.N;
-  const int p0 = pc * CTA_ROWS + warp * RPW + lane / LPR;
+  const int r0 = warp * RPW + lane / LPR, p0 = pc * CTA_ROWS + r0;
   pdl_wait();
   pdl_trigger();
   float4 hv[ROWS];
@@ -521,32 +525,39 @@ __global__ void __launch_bounds__(256) tree_state_kernel(const TreeCommitArgs a,
     if (p < a.P) hv[k] = *reinterpret_cast<const float4*>(a.h + base + (size_t)p * a.N + n4);
   }
   const int n = tree_count(a.t, a.count, i);
-  if (threadIdx.x < n) {
-    const int row = tree_path_row(a.t, i, threadIdx.x);
+  float* sx = reinterpret_cast<float*>(smem);
+  uint16_t* sb = reinterpret_cast<uint16_t*>(sx + n * CTA_ROWS);
+  if (tid < n) {
+    const int row = tree_path_row(a.t, i, tid);
     float dt = 0.0f, da = 1.0f;
     if (row >= 0) ssm_dt_dA(bf16_to_f32(a.dt[(size_t)row * a.ld_dt + h]), a.dt_bias[h], a.A_log[h], dt, da);
-    srow[threadIdx.x] = row;
-    sdt[threadIdx.x] = dt;
-    sda[threadIdx.x] = da;
+    srow[tid] = row;
+    sdt[tid] = dt;
+    sda[tid] = da;
   }
   __syncthreads();
-  const uint16_t* ub = a.u + (size_t)a.H * a.P + (size_t)g * a.N + n4;
-  const uint16_t* ux = a.u + (size_t)h * a.P;
-  for (int j = 0; j < n; ++j) {
-    const int row = srow[j];
+  for (int k = tid; k < n * (LPR + CTA_ROWS); k += 256) {
+    const int j = k / (LPR + CTA_ROWS), e = k - j * (LPR + CTA_ROWS), row = srow[j];
     if (row < 0) continue;
-    const float dt = sdt[j], dA = sda[j];
-    const float4 Bv = tc_bf4(ub + (size_t)row * a.ld_u);
+    const uint16_t* u = a.u + (size_t)row * a.ld_u;
+    if (e < LPR)
+      *reinterpret_cast<uint2*>(sb + j * a.N + 4 * e) =
+          *reinterpret_cast<const uint2*>(u + (size_t)a.H * a.P + (size_t)g * a.N + 4 * e);
+    else if (pc * CTA_ROWS + e - LPR < a.P)
+      sx[j * CTA_ROWS + e - LPR] = sdt[j] * bf16_to_f32(u[(size_t)h * a.P + pc * CTA_ROWS + e - LPR]);
+  }
+  __syncthreads();
+  for (int j = 0; j < n; ++j) {
+    if (srow[j] < 0) continue;
+    const float dA = sda[j];
+    const float4 Bv = tc_bf4(sb + j * a.N + n4);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      const int p = p0 + k * 8 * RPW;
-      if (p < a.P) {
-        const float dtx = dt * bf16_to_f32(ux[(size_t)row * a.ld_u + p]);
-        hv[k].x = fmaf(dA, hv[k].x, dtx * Bv.x);
-        hv[k].y = fmaf(dA, hv[k].y, dtx * Bv.y);
-        hv[k].z = fmaf(dA, hv[k].z, dtx * Bv.z);
-        hv[k].w = fmaf(dA, hv[k].w, dtx * Bv.w);
-      }
+      const float dtx = sx[j * CTA_ROWS + r0 + k * 8 * RPW];  // (of no use past the last channel)
+      hv[k].x = fmaf(dA, hv[k].x, dtx * Bv.x);
+      hv[k].y = fmaf(dA, hv[k].y, dtx * Bv.y);
+      hv[k].z = fmaf(dA, hv[k].z, dtx * Bv.z);
+      hv[k].w = fmaf(dA, hv[k].w, dtx * Bv.w);
     }
   }
 #pragma unroll
@@ -566,11 +577,19 @@ static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
   while (rows < 8 && rows < max_rows && heads * ((a.P + 8 * RPW * rows - 1) / (8 * RPW * rows)) > 4ll * num_sms()) rows *= 2;
   const int psplit = (a.P + 8 * RPW * rows - 1) / (8 * RPW * rows);
   const dim3 grid(a.H * psplit, a.t.nseq), block(256);
+  int most = 0;
+  for (int i = 0; i < a.t.nseq; ++i) most = a.t.cu[i + 1] - a.t.cu[i] > most ? a.t.cu[i + 1] - a.t.cu[i] : most;
+  const int smem = most * (a.N * 2 + 8 * RPW * rows * 4);  // at most 64 * (32 + 2048) bytes: N = 16
+  auto go = [&](void (*k)(TreeCommitArgs, int), int* done_mask) {
+    const cudaError_t e = smem > 48 * 1024 ? set_smem_once((const void*)k, smem, done_mask) : cudaSuccess;
+    return e != cudaSuccess ? e : launch_k(k, grid, block, smem, s, true, a, psplit);
+  };
+  static int done[4][64] = {{0}};
   switch (rows) {
-    case 1: return launch_k(tree_state_kernel<LPR, 1>, grid, block, 0, s, true, a, psplit);
-    case 2: return launch_k(tree_state_kernel<LPR, 2>, grid, block, 0, s, true, a, psplit);
-    case 4: return launch_k(tree_state_kernel<LPR, 4>, grid, block, 0, s, true, a, psplit);
-    default: return launch_k(tree_state_kernel<LPR, 8>, grid, block, 0, s, true, a, psplit);
+    case 1: return go(tree_state_kernel<LPR, 1>, done[0]);
+    case 2: return go(tree_state_kernel<LPR, 2>, done[1]);
+    case 4: return go(tree_state_kernel<LPR, 4>, done[2]);
+    default: return go(tree_state_kernel<LPR, 8>, done[3]);
   }
 }
 

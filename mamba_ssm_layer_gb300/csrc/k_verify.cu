@@ -22,7 +22,7 @@
 
 namespace m2 {
 
-constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32, kVfCtas = 8;
+constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32, kVfCtas = 8;
 
 enum { VF_SUM = 0, VF_DRAW = 1 };
 struct VfCmd {
@@ -43,7 +43,9 @@ struct VfShared {
 };
 
 // Probabilities that are not positive numbers count as 0.
-__device__ __forceinline__ float vf_clean(float x) { return x > 0.0f && x < INFINITY ? x : 0.0f; }
+__device__ __forceinline__ float vf_clean(float x) {  // as integers: 1 .. the largest finite value
+  return __float_as_uint(x) - 1u < 0x7F7FFFFFu ? x : 0.0f;
+}
 template <bool BF>
 __device__ __forceinline__ float vf_one(const void* row, int64_t at) {
   return vf_clean(BF ? bf16_to_f32(static_cast<const uint16_t*>(row)[at]) : static_cast<const float*>(row)[at]);
@@ -97,7 +99,7 @@ struct VfWalk {
 };
 
 template <bool BF>
-__global__ void __launch_bounds__(kVfThreads, 2) __cluster_dims__(kVfCtas, 1, 1) verify_tree_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1) verify_tree_kernel(const VerifyArgs a) {
   __shared__ VfShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x, i = blockIdx.y;
   const int first = a.t.cu[i], n = a.t.cu[i + 1] - first, V = a.V;
@@ -196,23 +198,45 @@ __global__ void __launch_bounds__(kVfThreads, 2) __cluster_dims__(kVfCtas, 1, 1)
     const bool minus = a.q && cmd.c_hi > 0.0f;  // nothing refused: the draft's row is not read
     const void* q = minus ? row_of(a.q, a.ld_q, cmd.cur) : nullptr;
     const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (4 * ES - 1)) == 0;
-    float hi = 0.0f, lo = 0.0f;
+    // four sums a lane: additions that wait for one another are what a pass of few warps would take
+    float hi4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lo4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     constexpr int UN = 4;
-    for (int at = from + 4 * lane; at < to; at += 128 * UN) {
-      float4 v[UN], m[UN];
+    auto add = [&](const float4& v, const float4& m) {
+      vf_add(hi4[0], lo4[0], v.x, m.x, cmd.c_hi, cmd.c_lo);
+      vf_add(hi4[1], lo4[1], v.y, m.y, cmd.c_hi, cmd.c_lo);
+      vf_add(hi4[2], lo4[2], v.z, m.z, cmd.c_hi, cmd.c_lo);
+      vf_add(hi4[3], lo4[3], v.w, m.w, cmd.c_hi, cmd.c_lo);
+    };
+    if (minus) {
+      for (int at = from + 4 * lane; at < to; at += 128 * UN) {
+        float4 v[UN], m[UN];
 #pragma unroll
-      for (int k = 0; k < UN; ++k) {
-        v[k] = vf_four<BF>(p, at + 128 * k, to, wide);
-        m[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (minus) m[k] = vf_four<BF>(q, at + 128 * k, to, wide);
-      }
+        for (int k = 0; k < UN; ++k) {
+          v[k] = vf_four<BF>(p, at + 128 * k, to, wide);
+          m[k] = vf_four<BF>(q, at + 128 * k, to, wide);
+        }
 #pragma unroll
-      for (int k = 0; k < UN; ++k) {
-        vf_add(hi, lo, v[k].x, m[k].x, cmd.c_hi, cmd.c_lo);
-        vf_add(hi, lo, v[k].y, m[k].y, cmd.c_hi, cmd.c_lo);
-        vf_add(hi, lo, v[k].z, m[k].z, cmd.c_hi, cmd.c_lo);
-        vf_add(hi, lo, v[k].w, m[k].w, cmd.c_hi, cmd.c_lo);
+        for (int k = 0; k < UN; ++k) add(v[k], m[k]);
       }
+    } else {
+      for (int at = from + 4 * lane; at < to; at += 128 * UN) {
+        float4 v[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) v[k] = vf_four<BF>(p, at + 128 * k, to, wide);
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+          two_sum_acc(hi4[0], lo4[0], v[k].x);
+          two_sum_acc(hi4[1], lo4[1], v[k].y);
+          two_sum_acc(hi4[2], lo4[2], v[k].z);
+          two_sum_acc(hi4[3], lo4[3], v[k].w);
+        }
+      }
+    }
+    float hi = hi4[0], lo = lo4[0];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      two_sum_acc(hi, lo, hi4[k]);
+      lo += lo4[k];
     }
     two_sum_warp(hi, lo);
     if (lane == 0) {
