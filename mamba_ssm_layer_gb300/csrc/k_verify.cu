@@ -38,8 +38,10 @@ struct VfShared {
   int32_t parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
   float u[kTreeNodes], p[kTreeNodes], q[kTreeNodes];
   int32_t count;     // accepted nodes so far (first CTA)
-  int32_t warp;      // drawing: the run, and what lies before it
-  double before;
+  int32_t run;       // drawing: the run that the random number falls into (-1: another CTA's, -2: the row is empty)
+  double want;       // and what is left of the number there
+  float scan_hi[kVfWarps], scan_lo[kVfWarps];
+  int32_t owner, last;
 };
 
 // Probabilities that are not positive numbers count as 0.
@@ -89,6 +91,15 @@ __device__ __forceinline__ void vf_put(void* at, int rank, uint32_t v) {
                    smem_addr(at)),
                "r"(rank), "r"(v)
                : "memory");
+}
+
+// u q S < p - c q (a < b, where b is 0 at least), in fp32 where that decides it: its error is
+// below 2^-21 of the three products.  Else in 64 bits, whose latency here is that of a sum.
+__device__ __forceinline__ bool vf_less(float u, float q, double S, float p, double c) {
+  const float a = u * q * (float)S, t = (float)c * q, b = fmaxf(p - t, 0.0f);
+  if (fabsf(a - b) > 9.5367431640625e-7f * (fabsf(a) + p + t)) return a < b;  // 2^-20
+  const double left = (double)p - c * q;
+  return (double)u * q * S < (left > 0.0 ? left : 0.0);
 }
 
 // The walk up to the next sum.  One thread of the cluster holds this.
@@ -151,12 +162,11 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
           }
           bool ok;
           if (a.q) {
-            const double q = sh.q[r], left = (double)sh.p[r] - w.c * q;
-            ok = (double)sh.u[r] * q * w.S < (left > 0.0 ? left : 0.0);
+            ok = vf_less(sh.u[r], sh.q[r], w.S, sh.p[r], w.c);
           } else {
             bool was = false;
             for (int k = 0; k < w.gone; ++k) was |= sh.gone_tok[k] == sh.token[r];
-            ok = !was && (double)sh.u[r] * w.S < (double)sh.p[r];
+            ok = !was && vf_less(sh.u[r], 1.0f, w.S, sh.p[r], 0.0);
           }
           ++w.r;
           if (ok) {
@@ -267,81 +277,110 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
       }
       continue;
     }
-    // ---- draw: which CTA, which warp
-    if (tid == 0) {
-      double total = 0.0, at[kVfCtas];
-      for (int k = 0; k < kVfCtas; ++k) {
-        at[k] = (double)sh.tot_hi[pass & 1][k] + (double)sh.tot_lo[pass & 1][k];
-        total += at[k];
-      }
-      double want = (double)a.u_next[i] * total, run = 0.0, before = 0.0;
-      if (!(want > 0.0)) want = 0.0;
-      int cta = -1;  // the first whose end lies past `want`; else the last with anything in it
-      for (int k = 0; k < kVfCtas; ++k) {
-        if (at[k] > 0.0) {
-          cta = k, before = run;
-          if (run + at[k] > want) break;
-        }
-        run += at[k];
-      }
-      sh.warp = total > 0.0 ? -1 : -2;
-      if (cta == rank && total > 0.0) {
-        run = before;
-        for (int k = 0; k < kVfWarps; ++k) {
-          const double s = (double)sh.hi[k] + (double)sh.lo[k];
-          if (s > 0.0) {
-            sh.warp = k, sh.before = want - run;
-            if (run + s > want) break;
+    // ---- draw: which CTA, which of its warps' runs.  Lane k holds the k-th CTA's sum, then the k-th run's.
+    if (warp == 0) {
+      auto scan = [&](float& h, float& l) {  // over 8 lanes, inclusive
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          const float oh = __shfl_up_sync(0xffffffffu, h, o), ol = __shfl_up_sync(0xffffffffu, l, o);
+          if (lane >= o) {
+            two_sum_acc(h, l, oh);
+            l += ol;
           }
-          run += s;
         }
+      };
+      static_assert(kVfCtas == 8 && kVfWarps == 8, "eight lanes");
+      // the first whose end lies past `want`, else the last with anything in it; -1: there is nothing
+      auto pick = [&](bool some, double end, double want) {
+        const uint32_t any = __ballot_sync(0xffffffffu, some && lane < 8), past = __ballot_sync(0xffffffffu, some && lane < 8 && end > want);
+        return past ? __ffs((int)past) - 1 : 31 - __clz((int)any);
+      };
+      float h = lane < 8 ? sh.tot_hi[pass & 1][lane] : 0.0f, l = lane < 8 ? sh.tot_lo[pass & 1][lane] : 0.0f;
+      const bool some = h > 0.0f;
+      scan(h, l);
+      const double end = (double)h + (double)l, total = __shfl_sync(0xffffffffu, end, 7);
+      double want = (double)a.u_next[i] * total;
+      if (!(want > 0.0)) want = 0.0;
+      const int cta = pick(some, end, want);
+      int run = cta < 0 ? -2 : -1;
+      if (cta == rank) {
+        const double before = __shfl_sync(0xffffffffu, end, max(cta - 1, 0));
+        if (cta > 0) want -= before;
+        h = lane < 8 ? sh.hi[lane] : 0.0f, l = lane < 8 ? sh.lo[lane] : 0.0f;
+        const bool part = h > 0.0f;
+        scan(h, l);
+        const double stop = (double)h + (double)l;
+        run = pick(part, stop, want);
+        const double skip = __shfl_sync(0xffffffffu, stop, max(run - 1, 0));
+        if (run > 0) want -= skip;
       }
+      if (lane == 0) sh.run = run, sh.want = want, sh.owner = kVfThreads, sh.last = -1;
     }
     __syncthreads();
-    if (sh.warp == -2 && (cmd.c_hi > 0.0f || cmd.gone > 0)) {
+    const int run = sh.run;
+    if (run == -2 && (cmd.c_hi > 0.0f || cmd.gone > 0)) {
       // nothing is left of the row: from the row itself
       if (rank == 0 && tid == 0) w.c = 0.0, w.gone = 0, w.r = n;
-      __syncthreads();  // sh.warp has been read
+      __syncthreads();  // sh.run has been read
       continue;
     }
     if (rank == 0) {
       if (tid < n) a.path[first + tid] = tid < sh.count ? sh.path[tid] : -1;
       if (tid == 0) {
         a.count[i] = sh.count;
-        if (sh.warp == -2) a.next[i] = -1;  // an empty row
+        if (run == -2) a.next[i] = -1;  // an empty row
       }
     }
-    if (sh.warp == warp) {
-      // a lane takes consecutive tokens of the run; then the lane that holds the place looks for it
-      const int len = (to - from + 31) / 32, l0 = min(to, from + lane * len), l1 = min(to, l0 + len);
-      float vh = 0.0f, vl = 0.0f;
-      auto value = [&](int x, float& h, float& l) {
+    if (run >= 0) {
+      // The run again, by the whole CTA: a thread takes consecutive tokens of it.
+      const int64_t r0 = min((int64_t)(rank * kVfWarps + run) * per, (int64_t)V);
+      const int r1 = (int)min(r0 + per, (int64_t)V), each = (per / kVfThreads + 3) / 4 * 4 + (per % kVfThreads ? 4 : 0);
+      const int x0 = (int)min(r0 + (int64_t)tid * each, (int64_t)r1), x1 = (int)min((int64_t)x0 + each, (int64_t)r1);
+      auto value = [&](int x, float vp, float vq, float& h, float& l) {
         for (int k = 0; k < cmd.gone; ++k)
           if (sh.gone_tok[k] == x) return;
-        vf_add(h, l, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, cmd.c_hi, cmd.c_lo);
+        vf_add(h, l, vp, vq, cmd.c_hi, cmd.c_lo);
       };
-#pragma unroll 8
-      for (int x = l0; x < l1; ++x) value(x, vh, vl);
-      float sh_hi = vh, sh_lo = vl;  // inclusive sums over the lanes
+      float vh = 0.0f, vl = 0.0f;
+#pragma unroll 2
+      for (int x = x0; x < x1; x += 4) {
+        const float4 v = vf_four<BF>(p, x, x1, wide), m = minus ? vf_four<BF>(q, x, x1, wide) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        value(x, v.x, m.x, vh, vl);
+        value(x + 1, v.y, m.y, vh, vl);
+        value(x + 2, v.z, m.z, vh, vl);
+        value(x + 3, v.w, m.w, vh, vl);
+      }
+      const bool some = vh > 0.0f;
+      float h = vh, l = vl;  // inclusive sums over the threads
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float oh = __shfl_up_sync(0xffffffffu, sh_hi, o), ol = __shfl_up_sync(0xffffffffu, sh_lo, o);
+        const float oh = __shfl_up_sync(0xffffffffu, h, o), ol = __shfl_up_sync(0xffffffffu, l, o);
         if (lane >= o) {
-          two_sum_acc(sh_hi, sh_lo, oh);
-          sh_lo += ol;
+          two_sum_acc(h, l, oh);
+          l += ol;
         }
       }
-      const double want = sh.before, end = (double)sh_hi + (double)sh_lo;
-      const bool some = vh > 0.0f;
-      const uint32_t past = __ballot_sync(0xffffffffu, some && end > want), any = __ballot_sync(0xffffffffu, some);
-      const int owner = past ? __ffs(past) - 1 : 31 - __clz((int)any);
-      const float ph = __shfl_up_sync(0xffffffffu, sh_hi, 1), pl = __shfl_up_sync(0xffffffffu, sh_lo, 1);
-      if (lane == owner) {
-        float h = lane ? ph : 0.0f, l = lane ? pl : 0.0f;
+      if (lane == 31) sh.scan_hi[warp] = h, sh.scan_lo[warp] = l;
+      __syncthreads();
+      float bh = 0.0f, bl = 0.0f;  // the warps before
+      for (int k = 0; k < warp; ++k) {
+        two_sum_acc(bh, bl, sh.scan_hi[k]);
+        bl += sh.scan_lo[k];
+      }
+      two_sum_acc(h, l, bh);
+      l += bl;
+      const double want = sh.want;
+      if (some && (double)h + (double)l > want) atomicMin(&sh.owner, tid);
+      if (some) atomicMax(&sh.last, tid);
+      // what lies before this thread
+      const float ph = __shfl_up_sync(0xffffffffu, h, 1), pl = __shfl_up_sync(0xffffffffu, l, 1);
+      __syncthreads();
+      if (tid == (sh.owner < kVfThreads ? sh.owner : sh.last)) {
+        h = lane ? ph : bh, l = lane ? pl : bl;
         int found = -1;
-        for (int x = l0; x < l1; ++x) {
+        for (int x = x0; x < x1; ++x) {
           float eh = 0.0f, el = 0.0f;
-          value(x, eh, el);
+          value(x, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, eh, el);
           if (!(eh > 0.0f)) continue;
           found = x;
           two_sum_acc(h, l, eh);
