@@ -18,6 +18,7 @@
 
 #include "m2_common.cuh"
 #include "m2_kernels.h"
+#include "m2_tc_attn.cuh"
 #include "m2_tree.cuh"
 
 namespace m2 {
@@ -52,34 +53,60 @@ template <bool BF>
 __device__ __forceinline__ float vf_one(const void* row, int64_t at) {
   return vf_clean(BF ? bf16_to_f32(static_cast<const uint16_t*>(row)[at]) : static_cast<const float*>(row)[at]);
 }
-// Four of a row from element `at` on; past the end 0.  wide: they can be read at once.
+// Four of a row from element `at` on as they are; past the end 0.  wide: they can be read at once.
 template <bool BF>
-__device__ __forceinline__ float4 vf_four(const void* row, int at, int V, bool wide) {
+__device__ __forceinline__ float4 vf_raw(const void* row, int at, int V, bool wide) {
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (wide && at + 4 <= V) {
     if (BF) {
       const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + at);
-      v = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-    } else {
-      v = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + at);
+      return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
     }
-    return make_float4(vf_clean(v.x), vf_clean(v.y), vf_clean(v.z), vf_clean(v.w));
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(row) + at);
   }
-  if (at < V) v.x = vf_one<BF>(row, at);
-  if (at + 1 < V) v.y = vf_one<BF>(row, at + 1);
-  if (at + 2 < V) v.z = vf_one<BF>(row, at + 2);
-  if (at + 3 < V) v.w = vf_one<BF>(row, at + 3);
+  auto one = [&](int x) { return BF ? bf16_to_f32(static_cast<const uint16_t*>(row)[x]) : static_cast<const float*>(row)[x]; };
+  if (at < V) v.x = one(at);
+  if (at + 1 < V) v.y = one(at + 1);
+  if (at + 2 < V) v.z = one(at + 2);
+  if (at + 3 < V) v.w = one(at + 3);
   return v;
 }
-// (hi, lo) += R of one token.
+template <bool BF>
+__device__ __forceinline__ float4 vf_four(const void* row, int at, int V, bool wide) {
+  const float4 v = vf_raw<BF>(row, at, V, wide);
+  return make_float4(vf_clean(v.x), vf_clean(v.y), vf_clean(v.z), vf_clean(v.w));
+}
+// (hi, lo) += R of one token.  Where R is positive p is the larger of the two, so that three
+// additions give p - c q and its rounding.
 __device__ __forceinline__ void vf_add(float& hi, float& lo, float p, float q, float c_hi, float c_lo) {
-  const float t = c_hi * q, e = fmaf(c_hi, q, -t) + c_lo * q;  // c q = t + e
-  const float s = p - t, b = s - p;
-  const float d = ((p - (s - b)) - (t + b)) - e;               // p - c q = s + d
-  if (s + d > 0.0f) {
+  const float t = fminf(c_hi * q, p), s = p - t;
+  if (s > 0.0f) {
     two_sum_acc(hi, lo, s);
-    lo += d;
+    lo += ((p - s) - t) - fmaf(c_lo, q, fmaf(c_hi, q, -t));
   }
+}
+// Two tokens a lane at once.  What is not positive, NaN among it, counts as 0 here;
+// infinities are found afterwards (`most` of the draft, the sum of the target).
+__device__ __forceinline__ float2 vf_sub2(float2 a, float2 b) { return ffma2(b, make_float2(-1.0f, -1.0f), a); }
+__device__ __forceinline__ void vf_sum2(float2& hi, float2& lo, float2 s) {
+  const float2 t = fadd2(hi, s), z = vf_sub2(t, hi);
+  lo = fadd2(lo, fadd2(vf_sub2(hi, vf_sub2(t, z)), vf_sub2(s, z)));
+  hi = t;
+}
+template <bool ONE>  // c is 1
+__device__ __forceinline__ void vf_add2(float2& hi, float2& lo, float2 p, float2 q, float c_hi, float c_lo, float& most) {
+  p = make_float2(fmaxf(p.x, 0.0f), fmaxf(p.y, 0.0f));
+  q = make_float2(fmaxf(q.x, 0.0f), fmaxf(q.y, 0.0f));
+  most = max3(most, q.x, q.y);
+  const float2 cq = ONE ? q : make_float2(c_hi * q.x, c_hi * q.y);
+  const float2 t = make_float2(fminf(cq.x, p.x), fminf(cq.y, p.y)), s = vf_sub2(p, t);
+  float2 d = vf_sub2(vf_sub2(p, s), t);
+  if (!ONE) {  // the product's own rounding, where something is left
+    const float2 e = make_float2(fmaf(c_lo, q.x, fmaf(c_hi, q.x, -t.x)), fmaf(c_lo, q.y, fmaf(c_hi, q.y, -t.y)));
+    d = vf_sub2(d, make_float2(s.x > 0.0f ? e.x : 0.0f, s.y > 0.0f ? e.y : 0.0f));
+  }
+  vf_sum2(hi, lo, s);
+  lo = fadd2(lo, d);
 }
 
 __device__ __forceinline__ void vf_cluster_sync() {
@@ -208,45 +235,58 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
     const bool minus = a.q && cmd.c_hi > 0.0f;  // nothing refused: the draft's row is not read
     const void* q = minus ? row_of(a.q, a.ld_q, cmd.cur) : nullptr;
     const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (4 * ES - 1)) == 0;
-    // four sums a lane: additions that wait for one another are what a pass of few warps would take
-    float hi4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lo4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float2 hi2[2], lo2[2];
+    hi2[0] = hi2[1] = lo2[0] = lo2[1] = make_float2(0.0f, 0.0f);
+    float most = 0.0f;
     constexpr int UN = 4;
-    auto add = [&](const float4& v, const float4& m) {
-      vf_add(hi4[0], lo4[0], v.x, m.x, cmd.c_hi, cmd.c_lo);
-      vf_add(hi4[1], lo4[1], v.y, m.y, cmd.c_hi, cmd.c_lo);
-      vf_add(hi4[2], lo4[2], v.z, m.z, cmd.c_hi, cmd.c_lo);
-      vf_add(hi4[3], lo4[3], v.w, m.w, cmd.c_hi, cmd.c_lo);
-    };
+    const bool once = cmd.c_hi == 1.0f && cmd.c_lo == 0.0f;  // one refusal: c is 1
     if (minus) {
       for (int at = from + 4 * lane; at < to; at += 128 * UN) {
         float4 v[UN], m[UN];
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
-          v[k] = vf_four<BF>(p, at + 128 * k, to, wide);
-          m[k] = vf_four<BF>(q, at + 128 * k, to, wide);
+          v[k] = vf_raw<BF>(p, at + 128 * k, to, wide);
+          m[k] = vf_raw<BF>(q, at + 128 * k, to, wide);
         }
+        if (once) {
 #pragma unroll
-        for (int k = 0; k < UN; ++k) add(v[k], m[k]);
+          for (int k = 0; k < UN; ++k) {
+            vf_add2<true>(hi2[0], lo2[0], make_float2(v[k].x, v[k].y), make_float2(m[k].x, m[k].y), 1.0f, 0.0f, most);
+            vf_add2<true>(hi2[1], lo2[1], make_float2(v[k].z, v[k].w), make_float2(m[k].z, m[k].w), 1.0f, 0.0f, most);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < UN; ++k) {
+            vf_add2<false>(hi2[0], lo2[0], make_float2(v[k].x, v[k].y), make_float2(m[k].x, m[k].y), cmd.c_hi, cmd.c_lo, most);
+            vf_add2<false>(hi2[1], lo2[1], make_float2(v[k].z, v[k].w), make_float2(m[k].z, m[k].w), cmd.c_hi, cmd.c_lo, most);
+          }
+        }
       }
     } else {
       for (int at = from + 4 * lane; at < to; at += 128 * UN) {
         float4 v[UN];
 #pragma unroll
-        for (int k = 0; k < UN; ++k) v[k] = vf_four<BF>(p, at + 128 * k, to, wide);
+        for (int k = 0; k < UN; ++k) v[k] = vf_raw<BF>(p, at + 128 * k, to, wide);
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
-          two_sum_acc(hi4[0], lo4[0], v[k].x);
-          two_sum_acc(hi4[1], lo4[1], v[k].y);
-          two_sum_acc(hi4[2], lo4[2], v[k].z);
-          two_sum_acc(hi4[3], lo4[3], v[k].w);
+          vf_sum2(hi2[0], lo2[0], make_float2(fmaxf(v[k].x, 0.0f), fmaxf(v[k].y, 0.0f)));
+          vf_sum2(hi2[1], lo2[1], make_float2(fmaxf(v[k].z, 0.0f), fmaxf(v[k].w, 0.0f)));
         }
       }
     }
-    float hi = hi4[0], lo = lo4[0];
-#pragma unroll
-    for (int k = 1; k < 4; ++k) {
-      two_sum_acc(hi, lo, hi4[k]);
-      lo += lo4[k];
+    float hi = hi2[0].x, lo = lo2[0].x;
+    auto more = [&](float h, float l) {
+      two_sum_acc(hi, lo, h);
+      lo += l;
+    };
+    more(hi2[0].y, lo2[0].y);
+    more(hi2[1].x, lo2[1].x);
+    more(hi2[1].y, lo2[1].y);
+    if (__any_sync(0xffffffffu, !(hi < INFINITY) || !(lo < INFINITY) || most == INFINITY)) {
+      // an infinity among them, which counts as 0: the run once more, value by value
+      hi = lo = 0.0f;
+      for (int x = from + lane; x < to; x += 32)
+        vf_add(hi, lo, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, cmd.c_hi, cmd.c_lo);
     }
     two_sum_warp(hi, lo);
     if (lane == 0) {
