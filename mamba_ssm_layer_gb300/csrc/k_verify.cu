@@ -238,25 +238,25 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
     float2 hi2[2], lo2[2];
     hi2[0] = hi2[1] = lo2[0] = lo2[1] = make_float2(0.0f, 0.0f);
     float most = 0.0f;
-    constexpr int UN = 4;
+    constexpr int UN = 4, UM = 2;  // loads together (64 registers: four of each were spilled)
     const bool once = cmd.c_hi == 1.0f && cmd.c_lo == 0.0f;  // one refusal: c is 1
     if (minus) {
-      for (int at = from + 4 * lane; at < to; at += 128 * UN) {
-        float4 v[UN], m[UN];
+      for (int at = from + 4 * lane; at < to; at += 128 * UM) {
+        float4 v[UM], m[UM];
 #pragma unroll
-        for (int k = 0; k < UN; ++k) {
+        for (int k = 0; k < UM; ++k) {
           v[k] = vf_raw<BF>(p, at + 128 * k, to, wide);
           m[k] = vf_raw<BF>(q, at + 128 * k, to, wide);
         }
         if (once) {
 #pragma unroll
-          for (int k = 0; k < UN; ++k) {
+          for (int k = 0; k < UM; ++k) {
             vf_add2<true>(hi2[0], lo2[0], make_float2(v[k].x, v[k].y), make_float2(m[k].x, m[k].y), 1.0f, 0.0f, most);
             vf_add2<true>(hi2[1], lo2[1], make_float2(v[k].z, v[k].w), make_float2(m[k].z, m[k].w), 1.0f, 0.0f, most);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < UN; ++k) {
+          for (int k = 0; k < UM; ++k) {
             vf_add2<false>(hi2[0], lo2[0], make_float2(v[k].x, v[k].y), make_float2(m[k].x, m[k].y), cmd.c_hi, cmd.c_lo, most);
             vf_add2<false>(hi2[1], lo2[1], make_float2(v[k].z, v[k].w), make_float2(m[k].z, m[k].w), cmd.c_hi, cmd.c_lo, most);
           }
