@@ -171,7 +171,7 @@ __device__ __forceinline__ void at_issue_values(uint32_t d, uint32_t p, uint32_t
 template <bool TEST>
 __device__ __forceinline__ bool at_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
   const long long t0 = clock64();
-  while (!(TEST ? mbar_test_wait(bar, parity) : at_try(bar, parity))) {
+  while (!(TEST ? mbar_test_wait(bar, parity) : mbar_try(bar, parity))) {
     if (clock64() - t0 > limit) {
       record_timeout();
       return false;
@@ -188,7 +188,7 @@ template <bool TEST>
 __device__ __forceinline__ bool at_wait_warp(uint64_t* bar, uint32_t parity, const AtArgs& a) {
   if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, TEST ? mbar_test_wait(bar, parity) : at_try(bar, parity))) {
+  while (!__all_sync(0xffffffffu, TEST ? mbar_test_wait(bar, parity) : mbar_try(bar, parity))) {
     if (__any_sync(0xffffffffu, clock64() - t0 > a.limit)) {
       record_timeout();
       return false;

@@ -74,20 +74,6 @@ constexpr int tt_smem_bytes() {
   return TtCfg<D, T>::kShared + (int)sizeof(TtShared) + 1024;
 }
 
-// A bounded wait of a whole warp, which stays together.  Inline and without an asked-for
-// time: mbar_wait's suspended waits ended some 900 cycles late, and a unit takes 1500.
-__device__ __forceinline__ bool tt_wait_until(uint64_t* bar, uint32_t parity, long long limit) {
-  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-  const long long t0 = clock64();
-  const bool suspend = limit >= 1000000;  // a shorter limit than a suspended wait may take: only test
-  while (!__all_sync(0xffffffffu, suspend ? at_try(bar, parity) : mbar_test_wait(bar, parity))) {
-    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
-      record_timeout();
-      return false;
-    }
-  }
-  return true;
-}
 // Four 8 x 8 matrices of 16-bit elements from fragments to rows of 16 bytes: lane l gives row l % 8 of matrix l / 8.
 __device__ __forceinline__ void stsm4(uint32_t addr, const uint32_t (&x)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]),
@@ -138,7 +124,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
   TtShared* sh = reinterpret_cast<TtShared*>(smem + C::kShared);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const long long limit = *reinterpret_cast<volatile long long*>(&g_wait_limit);
-  auto tt_wait = [&](uint64_t* bar, uint32_t parity) { return tt_wait_until(bar, parity, limit); };
+  auto tt_wait = [&](uint64_t* bar, uint32_t parity) { return mbar_warp_wait(bar, parity, limit); };
   if (tid == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&sh->raw_full[i], 1), mbar_init(&sh->raw_empty[i], kTtDeq);
     for (int i = 0; i < NT; ++i) mbar_init(&sh->full[i], kTtDeq), mbar_init(&sh->empty[i], 1);
@@ -594,7 +580,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
       } while (!dead && run.next(a, C::kRows));
       at_commit(&sh->fin, leader);  // everything issued here is done before tensor memory is freed
       __syncwarp();
-      tt_wait_until(&sh->fin, 0, kWaitCycles);
+      mbar_warp_wait(&sh->fin, 0, kWaitCycles);
     } else if (warp == kTtCopies) {
       // ------------------------------------------------ copies
       const uint64_t pol = a.most_tiles > 1 ? policy_evict_normal() : policy_evict_first();
@@ -628,7 +614,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
       } while (!dead && run.next(a, C::kRows));
       // every copy has landed before the CTA ends
       for (int i = max(0, u - S); i < u; ++i)
-        if (!tt_wait_until(&sh->raw_full[i % S], (i / S) & 1, kWaitCycles)) break;
+        if (!mbar_warp_wait(&sh->raw_full[i % S], (i / S) & 1, kWaitCycles)) break;
     }
   }
   tc_fence_before();

@@ -14,87 +14,115 @@ namespace m2 {
 
 // ------------------------------------------------------------------ conv
 //
-// A thread takes VEC channels of one node.  The node's window is the last rows of
-// its path (the set bits of its mask, from the top), then the ring from the newest
-// token back.  Sums run as the single-token conv's, oldest tap first; products of
-// two bf16 values are exact, so the results are the same bits.
-constexpr int kTcThreads = 128;
+// A thread takes VEC channels of `piece` consecutive nodes of a sequence, the next node's
+// taps on their way under the current one's sums.  A node's window is the last rows of its
+// path (the set bits of its mask, from the top), then the ring from the newest token back.
+// Sums run as the single-token conv's, oldest tap first; products of two bf16 values are
+// exact, so the results are the same bits.
+constexpr int kTcThreads = 128, kTcMost = 8, kTcCtas = 8;
 
 template <int K, int VEC>
-__global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const TreeConvArgs a) {
+__global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_constant__ TreeConvArgs a, int piece) {
   constexpr int L = K - 1;
+  using T = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, row = blockIdx.y;
-  const int i = tree_seq(a.t, row), first = a.t.cu[i], n = a.t.cu[i + 1] - first;
+  const int lane = threadIdx.x & 31, at_piece = blockIdx.y;
+  // sequence i's pieces start at cu[i] / piece + i, which leaves room for a cut last one
+  // (pieces of one node need none)
+  const int cut = piece > 1;
+  int i = 0;
+  for (int hi = a.t.nseq; hi - i > 1;) {
+    const int m = (i + hi) / 2;
+    if (a.t.cu[m] / piece + m * cut <= at_piece)
+      i = m;
+    else
+      hi = m;
+  }
+  const int first = a.t.cu[i], n = a.t.cu[i + 1] - first, r0 = (at_piece - first / piece - i * cut) * piece;
+  if (r0 >= n) return;
+  const int c = (blockIdx.x * kTcThreads + threadIdx.x) * VEC;
+  const bool in = c < a.C;
+  T w[K * VEC / (VEC == 8 ? 8 : 1)], b{};
+  if (in) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j] = reinterpret_cast<const T*>(a.w + (size_t)c * K)[j];
+    if (a.bias) b = *reinterpret_cast<const T*>(a.bias + c);
+  }
+  const int pos = a.pos[i];
   uint64_t m[2];
   tree_masks(a.t.parent + first, n, lane, m);
-  uint64_t path = tree_mask_of(m, row - first);
-  const int c = (blockIdx.x * kTcThreads + threadIdx.x) * VEC;
-  if (c >= a.C) return;
-  uint16_t* out = a.out + (size_t)row * a.ld_o + c;
-  if (path == 0) {  // not part of the tree
+  auto load = [&](int r, T (&v)[K]) {  // a node's taps, oldest first; false: not part of the tree
+    uint64_t path = tree_mask_of(m, r);
+    if (path == 0) return false;
+    int slot = (pos % L + L) % L;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) out[e] = 0;
-    return;
-  }
-  const uint16_t* tap[K];  // oldest first
-  int back = 0;
-  const int pos = a.pos[i];
-#pragma unroll
-  for (int j = L; j >= 0; --j) {
-    if (path) {
-      const int at = 63 - __clzll((long long)path);
-      path &= ~(1ull << at);
-      tap[j] = a.x + (size_t)(first + at) * a.ld_x + c;
-    } else {
-      ++back;
-      const int slot = ((pos - back) % L + L) % L;
-      tap[j] = a.ring + ((size_t)i * L + slot) * a.C + c;
+    for (int j = L; j >= 0; --j) {
+      const uint16_t* p;
+      if (path) {
+        const int at = 63 - __clzll((long long)path);
+        path &= ~(1ull << at);
+        p = a.x + (size_t)(first + at) * a.ld_x + c;
+      } else {
+        slot = slot ? slot - 1 : L - 1;
+        p = a.ring + ((size_t)i * L + slot) * a.C + c;
+      }
+      if (in) v[j] = *reinterpret_cast<const T*>(p);
     }
-  }
-  float s[VEC];
-  if constexpr (VEC == 8) {
-    uint4 v[K], w[K];
-    uint4 b = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      v[j] = *reinterpret_cast<const uint4*>(tap[j]);
-      w[j] = *reinterpret_cast<const uint4*>(a.w + (size_t)c * K + 8 * j);  // 16 * K bytes: 8 channels' taps
-    }
-    if (a.bias) b = *reinterpret_cast<const uint4*>(a.bias + c);
-    auto half = [](const uint4& x, int e) {
+    return true;
+  };
+  auto pick = [](const T& x, int e) {
+    if constexpr (VEC == 8) {
       const uint32_t u = e < 4 ? (e < 2 ? x.x : x.y) : (e < 6 ? x.z : x.w);
       return e & 1 ? bf16hi(u) : bf16lo(u);
-    };
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s[e] = half(b, e);
-#pragma unroll
-      for (int j = 0; j < K; ++j) s[e] = fmaf(half(w[(e * K + j) / 8], (e * K + j) % 8), half(v[j], e), s[e]);
-      if (a.silu) s[e] = silu_f(s[e]);
+    } else {
+      return bf16_to_f32(x);
     }
-    *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
-                                                pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
-  } else {
-    s[0] = a.bias ? bf16_to_f32(a.bias[c]) : 0.0f;
+  };
+  const int end = min(n, r0 + piece);
+  T next[K] = {};
+  bool there = load(r0, next);
+#pragma unroll 1
+  for (int r = r0; r < end; ++r) {
+    const bool now = there;
+    T v[K];
 #pragma unroll
-    for (int j = 0; j < K; ++j) s[0] = fmaf(bf16_to_f32(a.w[(size_t)c * K + j]), bf16_to_f32(*tap[j]), s[0]);
-    *out = f32_to_bf16(a.silu ? silu_f(s[0]) : s[0]);
+    for (int j = 0; j < K; ++j) v[j] = next[j];
+    if (r + 1 < end) there = load(r + 1, next);
+    if (!in) continue;
+    float s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      s[e] = pick(b, e);
+#pragma unroll
+      for (int j = 0; j < K; ++j) s[e] = fmaf(pick(w[(e * K + j) / VEC], (e * K + j) % VEC), pick(v[j], e), s[e]);
+      if (a.silu) s[e] = silu_f(s[e]);
+      if (!now) s[e] = 0.0f;
+    }
+    T o;
+    if constexpr (VEC == 8)
+      o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+    else
+      o = f32_to_bf16(s[0]);
+    *reinterpret_cast<T*>(a.out + (size_t)(first + r) * a.ld_o + c) = o;
   }
 }
 
 template <int VEC>
 static cudaError_t launch_tree_conv_v(const TreeConvArgs& a, cudaStream_t s) {
-  const dim3 grid((a.C + kTcThreads * VEC - 1) / (kTcThreads * VEC), a.t.cu[a.t.nseq]), block(kTcThreads);
+  // One node a CTA while all of them run at once; then so many that they do.
+  const int blocks = (a.C + kTcThreads * VEC - 1) / (kTcThreads * VEC), nodes = a.t.cu[a.t.nseq];
+  int piece = 1;
+  while (piece < kTcMost && (int64_t)blocks * nodes / piece > (int64_t)kTcCtas * num_sms()) piece *= 2;
+  const dim3 grid(blocks, nodes / piece + (piece > 1 ? a.t.nseq : 0)), block(kTcThreads);
   switch (a.dconv) {
-    case 2: return launch_k(tree_conv_kernel<2, VEC>, grid, block, 0, s, true, a);
-    case 3: return launch_k(tree_conv_kernel<3, VEC>, grid, block, 0, s, true, a);
-    case 4: return launch_k(tree_conv_kernel<4, VEC>, grid, block, 0, s, true, a);
-    case 5: return launch_k(tree_conv_kernel<5, VEC>, grid, block, 0, s, true, a);
-    case 6: return launch_k(tree_conv_kernel<6, VEC>, grid, block, 0, s, true, a);
-    case 7: return launch_k(tree_conv_kernel<7, VEC>, grid, block, 0, s, true, a);
-    default: return launch_k(tree_conv_kernel<8, VEC>, grid, block, 0, s, true, a);
+    case 2: return launch_k(tree_conv_kernel<2, VEC>, grid, block, 0, s, true, a, piece);
+    case 3: return launch_k(tree_conv_kernel<3, VEC>, grid, block, 0, s, true, a, piece);
+    case 4: return launch_k(tree_conv_kernel<4, VEC>, grid, block, 0, s, true, a, piece);
+    case 5: return launch_k(tree_conv_kernel<5, VEC>, grid, block, 0, s, true, a, piece);
+    case 6: return launch_k(tree_conv_kernel<6, VEC>, grid, block, 0, s, true, a, piece);
+    case 7: return launch_k(tree_conv_kernel<7, VEC>, grid, block, 0, s, true, a, piece);
+    default: return launch_k(tree_conv_kernel<8, VEC>, grid, block, 0, s, true, a, piece);
   }
 }
 
@@ -124,7 +152,12 @@ cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
 // are 0 in the product, and the nodes below them add them when they store.
 // Bound: HBM, the state read once (32 KB a head of 64 x 128), up to 16 nodes; with 64
 // nodes the tensor cores' legacy rate is as near.
-constexpr int kTsThreads = 256, kTsWarps = kTsThreads / 32;
+//
+// A CTA takes some heads of one group of a sequence.  Their states come by bulk copies of
+// 64 rows, one ahead; L and x of the next head are made ready under the current head's
+// products, behind one barrier a piece.
+constexpr int kTsWarps = 8, kTsThreads = kTsWarps * 32, kTsBlock = 64, kTsStages = 2;
+constexpr int kTsSmemMax = 227 * 1024;
 
 template <int N, int MT>
 struct TsCfg {
@@ -132,18 +165,19 @@ struct TsCfg {
   static constexpr int kRow = N + 16;        // bf16 elements between rows of the C and B tiles: no bank conflicts
   static constexpr int kCb = kNodes + 4;     // floats between rows of C B^T
   static constexpr int kL = kNodes + 8;      // bf16 elements between rows of L
+  static constexpr int kTerms = 3 * kNodes * kL;  // elements of a head's L
+  static constexpr int kStage = kTsBlock * N * 4; // bytes of a piece of the state
+  // B's tile is read once, before the first L is written
+  static constexpr int kLs = 2 * kTerms > kNodes * kRow ? 2 * kTerms : kNodes * kRow;
 };
-// Shared memory of a CTA: masks, C and B tiles, C B^T, the heads' dt and s, then for
-// one head at a time L's three terms and x.
-template <int N, int MT>
-__host__ __device__ constexpr int ts_x_stride(int P) {
-  return (P + 7) / 8 * 8 + 8;
-}
+// Shared memory of a CTA: the ring, barriers, masks, C's tile, L's terms twice (and first
+// B's tile), x twice, C B^T, the heads' dt and s.
+__host__ __device__ constexpr int ts_x_stride(int P) { return (P + 7) / 8 * 8 + 8; }
 template <int N, int MT>
 __host__ __device__ inline int ts_smem_bytes(int P, int heads) {
   using C = TsCfg<N, MT>;
-  return C::kNodes * 8 + 16 + 2 * C::kNodes * C::kRow * 2 + C::kNodes * C::kCb * 4 + heads * C::kNodes * 12 +
-         3 * C::kNodes * C::kL * 2 + C::kNodes * ts_x_stride<N, MT>(P) * 2;
+  return kTsStages * C::kStage + 64 + C::kNodes * 8 + 32 + C::kNodes * C::kRow * 2 + C::kLs * 2 +
+         2 * C::kNodes * ts_x_stride(P) * 2 + C::kNodes * C::kCb * 4 + heads * C::kNodes * 12;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -166,6 +200,9 @@ __device__ __forceinline__ void ldsm2_trans(uint32_t& r0, uint32_t& r1, const vo
                : "r"(smem_addr(p))
                : "memory");
 }
+__device__ __forceinline__ void ts_copy8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
 // Two floats as three pairs of bf16 whose sum they are (all 24 bits).
 __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16x2(a, b);
@@ -175,18 +212,20 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
 }
 
 template <int N, int MT>
-__global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(const TreeSsmArgs a, int heads, int chunks) {
+__global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2)
+    tree_ssm_kernel(const __grid_constant__ TreeSsmArgs a, int heads, int chunks) {
   using Cf = TsCfg<N, MT>;
   constexpr int KS = N / 16, NODES = Cf::kNodes;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int xs = ts_x_stride<N, MT>(a.P);
-  uint64_t* mask = reinterpret_cast<uint64_t*>(smem);
-  unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);  // nodes with such x, heads in turn
-  uint16_t* ct = reinterpret_cast<uint16_t*>(bad + 2);
-  uint16_t* bt = ct + NODES * Cf::kRow;
-  uint16_t* lt = bt + NODES * Cf::kRow;  // L's terms
-  uint16_t* xt = lt + 3 * NODES * Cf::kL;
-  float* cb = reinterpret_cast<float*>(xt + NODES * xs);
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int xs = ts_x_stride(a.P);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTsStages * Cf::kStage);
+  uint64_t* mask = full + 8;
+  unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);  // nodes with x that is not finite, three heads in turn
+  uint16_t* ct = reinterpret_cast<uint16_t*>(bad + 4);
+  uint16_t* lt = ct + NODES * Cf::kRow;  // L's terms, heads in turn
+  uint16_t* bt = lt;
+  uint16_t* xt = lt + Cf::kLs;           // x, heads in turn
+  float* cb = reinterpret_cast<float*>(xt + 2 * NODES * xs);
   float* sdt = cb + NODES * Cf::kCb;     // [heads][NODES]
   float* shi = sdt + heads * NODES;
   float* slo = shi + heads * NODES;
@@ -194,28 +233,36 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(c
   const int i = blockIdx.y, g = blockIdx.x / chunks, per = a.H / a.G;
   const int h0 = g * per + (blockIdx.x - g * chunks) * heads, nh = min(heads, (g + 1) * per - h0);
   const int first = a.t.cu[i], n = a.t.cu[i + 1] - first;
+  const int blocks = (a.P + kTsBlock - 1) / kTsBlock;  // pieces of a head's state
+  if (tid == 0) {
+    for (int k = 0; k < kTsStages; ++k) mbar_init(&full[k], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
   if (n == 0) return;
-  // this warp's tiles of 8 channels, heads one after the other: the state of the next one is on its way
-  const int pt = (a.P + 7) / 8, mine = warp < pt ? (pt - warp + kTsWarps - 1) / kTsWarps : 0;
-  const float* hb = a.h + ((size_t)i * a.H + h0) * a.P * N;
-  float4 hv[KS];
-  auto load = [&](int head, int k) {
-    const int p = (warp + k * kTsWarps) * 8 + r;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-      hv[ks] = p < a.P ? *reinterpret_cast<const float4*>(hb + ((size_t)head * a.P + p) * N + 16 * ks + 4 * c)
-                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // ---- the states: thread 0 asks for piece `asked`
+  const uint64_t pol = policy_evict_first();
+  int asked = 0, ask_p = 0;
+  const float* ask_h = a.h + ((size_t)i * a.H + h0) * a.P * N;
+  auto ask_state = [&] {
+    if (asked == nh * blocks) return;
+    const int st = asked % kTsStages, rows = min(kTsBlock, a.P - ask_p);
+    mbar_arrive_expect_tx(&full[st], (uint32_t)rows * N * 4);
+    bulk_g2s(smem + st * Cf::kStage, ask_h, (uint32_t)rows * N * 4, &full[st], pol);
+    ask_h += rows * N;
+    ask_p = ask_p + rows == a.P ? 0 : ask_p + rows;
+    ++asked;
   };
-  if (mine) load(0, 0);
+  if (tid == 0) ask_state();
   // ---- masks, C and B rows, dt and the decays' sums
   if (warp == 0) {
     uint64_t m[2];
     tree_masks(a.t.parent + first, n, lane, m);
     if (lane < NODES) mask[lane] = m[0];
     if (MT == 4) mask[lane + 32] = m[1];
-    if (lane < 2) bad[lane] = 0ull;
+    if (lane < 3) bad[lane] = 0ull;
   }
   for (int k = tid; k < NODES * (N / 4); k += kTsThreads) {
     const int j = k / (N / 4), e = k % (N / 4) * 4;
@@ -251,12 +298,6 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(c
       for (uint64_t m = mask[k % NODES]; m; m &= m - 1)
         two_sum_acc(th[q], tl[q], shi[k / NODES * NODES + __ffsll((long long)m) - 1]);
   }
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < ROUNDS; ++q) {
-    const int k = tid + q * kTsThreads;
-    if (k < nh * NODES) shi[k] = th[q], slo[k] = tl[q];
-  }
   // ---- C B^T
   for (int k = warp; k < MT * 2 * MT; k += kTsWarps) {
     const int mt = k / (2 * MT), nt = k % (2 * MT);
@@ -274,84 +315,148 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(c
     *reinterpret_cast<float2*>(d + 8 * Cf::kCb) = make_float2(acc[2], acc[3]);
   }
   __syncthreads();
-  for (int head = 0; head < nh; ++head) {
-    const int h = h0 + head;
-    const float* dt_h = sdt + head * NODES;
-    const float* hi_h = shi + head * NODES;
-    const float* lo_h = slo + head * NODES;
-    // ---- L and x of the head (pairs of columns: a bf16x2 word)
-    for (int k = tid; k < NODES * (NODES / 2); k += kTsThreads) {
-      const int row = k / (NODES / 2), col = k % (NODES / 2) * 2;
-      const uint64_t m = mask[row];
-      float v[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        v[e] = 0.0f;
-        if (m >> (col + e) & 1) {
-          const float d = (hi_h[row] - hi_h[col + e]) + (lo_h[row] - lo_h[col + e]);
-          v[e] = expf(d) * dt_h[col + e] * cb[row * Cf::kCb + col + e];
+  for (int q = 0; q < ROUNDS; ++q) {
+    const int k = tid + q * kTsThreads;
+    if (k < nh * NODES) shi[k] = th[q], slo[k] = tl[q];
+  }
+  __syncthreads();
+  // (halves with all exponent bits set are infinities and NaN)
+  auto finite = [](uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+    return w;
+  };
+  // x of a head: asked for, then looked through by the threads that asked (wide), or both
+  // at once; 16 threads a row.  Columns past P hold anything: they only reach themselves.
+  const int xq = tid & 15, xj = tid >> 4;
+  auto ask_x = [&](int head) {
+    uint16_t* d = xt + (head & 1) * NODES * xs;
+#pragma unroll 1
+    for (int j = xj; j < NODES; j += kTsThreads / 16) {
+      const bool in = mask[j] != 0;  // (0 for nodes past the last one too)
+      const uint16_t* src = a.x + (size_t)(first + j) * a.ld_in + (size_t)(h0 + head) * a.P;
+#pragma unroll 1
+      for (int q = xq; q < (a.wide_x ? a.P / 4 : a.P); q += 16) {
+        if (!a.wide_x) {
+          const uint32_t v = in ? src[q] : 0u;
+          const uint32_t f = finite(v);
+          if (f != v) atomicOr(&bad[head % 3], 1ull << j);
+          d[j * xs + q] = (uint16_t)f;
+        } else if (in) {
+          ts_copy8(d + j * xs + 4 * q, src + 4 * q);
+        } else {
+          *reinterpret_cast<uint2*>(d + j * xs + 4 * q) = make_uint2(0u, 0u);
         }
       }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto look_x = [&](int head) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!a.wide_x) return;
+    uint16_t* d = xt + (head & 1) * NODES * xs;
+#pragma unroll 1
+    for (int j = xj; j < NODES; j += kTsThreads / 16)
+#pragma unroll 1
+      for (int q = xq; q < a.P / 4; q += 16) {
+        uint2* p = reinterpret_cast<uint2*>(d + j * xs + 4 * q);
+        const uint2 v = *p, f = make_uint2(finite(v.x), finite(v.y));
+        if (f.x != v.x || f.y != v.y) {
+          atomicOr(&bad[head % 3], 1ull << j);
+          *p = f;
+        }
+      }
+  };
+  // L of a head: a lane keeps two columns (a bf16x2 word), a warp takes rows in turn.
+  // Blocks above the diagonal are never read.
+  auto make_l = [&](int head) {
+    constexpr int LPR = NODES / 2, RPW = 32 / LPR;
+    const int col = lane % LPR * 2;
+    const float2 dc = *reinterpret_cast<const float2*>(sdt + head * NODES + col);
+    const float2 hc = *reinterpret_cast<const float2*>(shi + head * NODES + col);
+    const float2 lc = *reinterpret_cast<const float2*>(slo + head * NODES + col);
+    uint16_t* lh = lt + (head & 1) * Cf::kTerms + col;
+#pragma unroll 1
+    for (int row = warp * RPW + lane / LPR; row < NODES; row += kTsWarps * RPW) {
+      if (col > (row | 15)) continue;
+      const uint64_t m = mask[row] >> col;
+      const float hr = shi[head * NODES + row], lr = slo[head * NODES + row];
+      const float2 cv = *reinterpret_cast<const float2*>(cb + row * Cf::kCb + col);
+      // a node above has the larger s: the others' differences may overflow, and are not taken
+      float v0 = expf((hr - hc.x) + (lr - lc.x)) * dc.x * cv.x, v1 = expf((hr - hc.y) + (lr - lc.y)) * dc.y * cv.y;
+      v0 = m & 1 ? v0 : 0.0f;
+      v1 = m & 2 ? v1 : 0.0f;
       uint32_t w0, w1, w2;
-      split3(v[0], v[1], w0, w1, w2);
-      uint32_t* d = reinterpret_cast<uint32_t*>(lt + row * Cf::kL + col);
+      split3(v0, v1, w0, w1, w2);
+      uint32_t* d = reinterpret_cast<uint32_t*>(lh + row * Cf::kL);
       constexpr int T = NODES * Cf::kL / 2;  // words of a term
       d[0] = w0, d[T] = w1, d[2 * T] = w2;
     }
-    // (halves with all exponent bits set are infinities and NaN)
-    auto finite = [](uint32_t w) {
-      if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-      if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
-      return w;
-    };
-    const int q2 = xs / (a.wide_x ? 4 : 1);
-    for (int k = tid; k < NODES * q2; k += kTsThreads) {
-      const int j = k / q2, q = k - j * q2;
-      const bool in = mask[j] != 0;  // (0 for nodes past the last one too)
-      if (a.wide_x) {
-        uint2 v = make_uint2(0u, 0u);
-        if (in && 4 * q < a.P)
-          v = *reinterpret_cast<const uint2*>(a.x + (size_t)(first + j) * a.ld_in + (size_t)h * a.P + 4 * q);
-        const uint2 f = make_uint2(finite(v.x), finite(v.y));
-        if (f.x != v.x || f.y != v.y) atomicOr(&bad[head & 1], 1ull << j);
-        *reinterpret_cast<uint2*>(xt + j * xs + 4 * q) = f;
-      } else {
-        const uint32_t v = in && q < a.P ? a.x[(size_t)(first + j) * a.ld_in + (size_t)h * a.P + q] : 0u;
-        const uint32_t f = finite(v);
-        if (f != v) atomicOr(&bad[head & 1], 1ull << j);
-        xt[j * xs + q] = (uint16_t)f;
-      }
-    }
-    __syncthreads();
+  };
+  const long long limit = *reinterpret_cast<volatile long long*>(&g_wait_limit);
+  ask_x(0);
+  make_l(0);
+  look_x(0);
+  uint2 cf[MT == 1 ? KS : 1][2];  // 16 nodes' C stays in registers
+  if (MT == 1) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) cf[ks % (MT == 1 ? KS : 1)][e] = *reinterpret_cast<const uint2*>(ct + (8 * e + r) * Cf::kRow + 16 * ks + 4 * c);
+  }
+  bool dead = false;
+  int item = 0;
+  for (int head = 0; head < nh; ++head) {
+    const int h = h0 + head;
+    const float* hi_h = shi + head * NODES;
+    const float* lo_h = slo + head * NODES;
+    const uint16_t* lh = lt + (head & 1) * Cf::kTerms;
+    const uint16_t* xh = xt + (head & 1) * NODES * xs;
     const float Dh = a.D[h];
-    const uint64_t odd = bad[head & 1];
-    if (tid == 0) bad[(head + 1) & 1] = 0ull;
-    for (int k = 0; k < mine; ++k) {
-      const int p0 = (warp + k * kTsWarps) * 8;
+    uint64_t odd = 0;
+    for (int b = 0; b < blocks; ++b, ++item) {
+      const int st = item % kTsStages, p0 = b * kTsBlock + warp * 8;
+      // every warp has read the piece before; L and x of this head are there, those of the one before are read
+      __syncthreads();
+      if (tid == 0) {
+        if (!dead) ask_state();
+        if (b == 0) bad[(head + 2) % 3] = 0ull;  // read by all before, next written behind the next barrier
+      }
+      if (b == 0) odd = bad[head % 3];
+      if (!dead && !mbar_warp_wait(&full[st], (item / kTsStages) & 1, limit)) dead = true;
       float acc[MT][4], low[MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][e] = low[mt][e] = 0.0f;
+      const float* hs = reinterpret_cast<const float*>(smem + st * Cf::kStage) + (warp * 8 + r) * N + 4 * c;
+      float4 hv[2];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
+        if (KS == 1) {
+          hv[0] = *reinterpret_cast<const float4*>(hs);
+        } else if (ks % 2 == 0) {
+          // rows lie a multiple of the banks apart: odd ones read their halves in the other order
+          const float4 v0 = *reinterpret_cast<const float4*>(hs + 16 * (ks + (r & 1)));
+          const float4 v1 = *reinterpret_cast<const float4*>(hs + 16 * (ks + 1 - (r & 1)));
+          hv[0] = r & 1 ? v1 : v0;
+          hv[1] = r & 1 ? v0 : v1;
+        }
+        const float4 hk = hv[ks & 1];
         uint32_t b0[3], b1[3];
-        split3(hv[ks].x, hv[ks].y, b0[0], b0[1], b0[2]);
-        split3(hv[ks].z, hv[ks].w, b1[0], b1[1], b1[2]);
+        split3(hk.x, hk.y, b0[0], b0[1], b0[2]);
+        split3(hk.z, hk.w, b1[0], b1[1], b1[2]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const uint2 a0 = *reinterpret_cast<const uint2*>(ct + (16 * mt + r) * Cf::kRow + 16 * ks + 4 * c);
-          const uint2 a1 = *reinterpret_cast<const uint2*>(ct + (16 * mt + 8 + r) * Cf::kRow + 16 * ks + 4 * c);
+          const uint2 a0 = MT == 1 ? cf[ks % (MT == 1 ? KS : 1)][0] : *reinterpret_cast<const uint2*>(ct + (16 * mt + r) * Cf::kRow + 16 * ks + 4 * c);
+          const uint2 a1 = MT == 1 ? cf[ks % (MT == 1 ? KS : 1)][1] : *reinterpret_cast<const uint2*>(ct + (16 * mt + 8 + r) * Cf::kRow + 16 * ks + 4 * c);
           mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[2], b1[2]);
-          mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[1], b1[1]);
           mma_bf16(acc[mt], a0.x, a1.x, a0.y, a1.y, b0[0], b1[0]);
+          mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[1], b1[1]);
         }
       }
-      // the next tile's state
-      if (k + 1 < mine)
-        load(head, k + 1);
-      else if (head + 1 < nh)
-        load(head + 1, 0);
+      if (b == 0 && head + 1 < nh) ask_x(head + 1);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int r0 = 16 * mt + r;
@@ -362,18 +467,20 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(c
           low[mt][e] = 0.0f;
         }
         float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p0 < a.P) {
 #pragma unroll
-        for (int ks = 0; ks <= mt; ++ks) {
-          uint32_t b0, b1;
-          ldsm2_trans(b0, b1, xt + (16 * ks + (lane & 15)) * xs + p0);
+          for (int ks = 0; ks <= mt; ++ks) {
+            uint32_t b0, b1;
+            ldsm2_trans(b0, b1, xh + (16 * ks + (lane & 15)) * xs + p0);
 #pragma unroll
-          for (int t = 2; t >= 0; --t) {
-            uint32_t l[4];
-            ldsm4(l, lt + t * NODES * Cf::kL + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8);
-            if (t)
-              mma_bf16(low[mt], l[0], l[1], l[2], l[3], b0, b1);
-            else
-              mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
+            for (int t = 2; t >= 0; --t) {
+              uint32_t l[4];
+              ldsm4(l, lh + t * NODES * Cf::kL + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8);
+              if (t)
+                mma_bf16(low[mt], l[0], l[1], l[2], l[3], b0, b1);
+              else
+                mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
+            }
           }
         }
 #pragma unroll
@@ -381,7 +488,7 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(c
           const int j = r0 + 8 * e, p = p0 + 2 * c;
           if (j >= n || p >= a.P) continue;
           const uint64_t m = mask[j];
-          const uint32_t xw = *reinterpret_cast<const uint32_t*>(xt + j * xs + p);
+          const uint32_t xw = *reinterpret_cast<const uint32_t*>(xh + j * xs + p);
           float y[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
@@ -392,23 +499,27 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2) tree_ssm_kernel(c
               const float v = bf16_to_f32(a.x[(size_t)(first + at) * a.ld_in + (size_t)h * a.P + p + f]);
               if (isfinite(v)) continue;
               float l = 0.0f;
-              for (int t = 2; t >= 0; --t) l += bf16_to_f32(lt[t * NODES * Cf::kL + j * Cf::kL + at]);
+              for (int t = 2; t >= 0; --t) l += bf16_to_f32(lh[t * NODES * Cf::kL + j * Cf::kL + at]);
               y[f] += (at == j ? l + Dh : l) * v;
             }
           }
-          const float y0 = y[0], y1 = y[1];
           float* d = a.y + (size_t)(first + j) * a.H * a.P + (size_t)h * a.P + p;
           if (a.P % 2 == 0) {
-            *reinterpret_cast<float2*>(d) = make_float2(y0, y1);
+            *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
           } else {
-            d[0] = y0;
-            if (p + 1 < a.P) d[1] = y1;
+            d[0] = y[0];
+            if (p + 1 < a.P) d[1] = y[1];
           }
         }
       }
     }
-    __syncthreads();  // L and x are written anew
+    if (head + 1 < nh) {
+      make_l(head + 1);
+      look_x(head + 1);
+    }
   }
+  if (tid == 0 && dead)  // gave up on a piece: what was asked for still lands here
+    for (int k = max(0, asked - kTsStages); k < asked; ++k) mbar_drain(&full[k % kTsStages], (k / kTsStages) & 1);
 }
 
 template <int N, int MT>
@@ -419,7 +530,7 @@ static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
   // one's state run under the current one's products; halved until there are CTAs for
   // most of the places on the SMs.  heads * nodes stays within the path sums' 1024 pairs.
   int heads = per < 16 ? per : 16;
-  while (heads > 1 && (heads * 16 * MT > 1024 ||
+  while (heads > 1 && (heads * 16 * MT > 1024 || ts_smem_bytes<N, MT>(a.P, heads) > kTsSmemMax ||
                        2 * (int64_t)a.t.nseq * a.G * ((per + heads - 1) / heads) < (MT == 4 ? 1 : 3) * (int64_t)num_sms()))
     heads = (heads + 1) / 2;
   const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
@@ -612,5 +723,6 @@ cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
 }
 
 int status_tree(int clear) { return tu_status(clear); }
+cudaError_t wait_limit_tree(long long cycles) { return tu_set_wait_limit(cycles); }
 
 }  // namespace m2

@@ -235,6 +235,34 @@ __device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity) {
   if (mbar_test_wait(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, kWaitCycles);
 }
+// A potentially blocking test, for as long as the hardware likes.  (A time asked for
+// becomes sleeping in steps, which took 1 to 2% longer.)
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A bounded wait of a whole warp, which stays together.  Inline and without an asked-for
+// time: mbar_wait's suspended waits ended some 900 cycles late, which counts where a
+// stage of the pipeline takes one or two thousand.
+__device__ __forceinline__ bool mbar_warp_wait(uint64_t* bar, uint32_t parity, long long limit) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  const bool suspend = limit >= 1000000;  // a shorter limit than a suspended wait may take: only test
+  while (!__all_sync(0xffffffffu, suspend ? mbar_try(bar, parity) : mbar_test_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+      record_timeout();
+      return false;
+    }
+  }
+  return true;
+}
 
 // ------------------------------------------------------------------ bulk copy
 

@@ -84,18 +84,4 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* w) {
                : "memory");
 }
 
-// A potentially blocking test, for as long as the hardware likes.  (A time asked for
-// becomes sleeping in steps, which took 1 to 2% longer.)
-__device__ __forceinline__ bool at_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 }  // namespace m2
