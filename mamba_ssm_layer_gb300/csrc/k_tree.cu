@@ -16,15 +16,31 @@ namespace m2 {
 //
 // A thread takes VEC channels of `piece` consecutive nodes of a sequence, the next node's
 // taps on their way under the current one's sums.  A node's window is the last rows of its
-// path (the set bits of its mask, from the top), then the ring from the newest token back.
+// path (the set bits of its mask, from the top), then the ring from the newest token back:
+// a lane of the first warp looks up a node's rows for the CTA.
 // Sums run as the single-token conv's, oldest tap first; products of two bf16 values are
 // exact, so the results are the same bits.
-constexpr int kTcThreads = 128, kTcMost = 8, kTcCtas = 8;
+constexpr int kTcThreads = 128, kTcMost = 16, kTcCtas = 5;
+
+// Two fused multiply-adds, each rounded as one.
+__device__ __forceinline__ float2 tc_fma2(float2 x, float2 y, float2 z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<const uint64_t&>(x)), "l"(reinterpret_cast<const uint64_t&>(y)),
+        "l"(reinterpret_cast<const uint64_t&>(z)));
+  return reinterpret_cast<const float2&>(r);
+}
+__device__ __forceinline__ float2 tc_pair(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+__device__ __forceinline__ uint32_t tc_word(const uint4& v, int e) {
+  return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+}
 
 template <int K, int VEC>
 __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_constant__ TreeConvArgs a, int piece) {
-  constexpr int L = K - 1;
+  constexpr int L = K - 1, PAIRS = VEC == 8 ? 4 : 1;
   using T = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
+  __shared__ const uint16_t* tap[kTcMost][K];  // channel 0 of a node's taps, oldest first; null: not part of the tree
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, at_piece = blockIdx.y;
@@ -41,70 +57,96 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
   }
   const int first = a.t.cu[i], n = a.t.cu[i + 1] - first, r0 = (at_piece - first / piece - i * cut) * piece;
   if (r0 >= n) return;
+  if (threadIdx.x < 32) {
+    const int pos = a.pos[i];
+    uint64_t m[2];
+    tree_masks(a.t.parent + first, n, lane, m);
+    uint64_t path = tree_mask_of(m, min(r0 + lane, n - 1));
+    if (lane < piece) {
+      const bool in = path != 0;
+      int slot = (pos % L + L) % L;
+#pragma unroll
+      for (int j = L; j >= 0; --j) {
+        const uint16_t* p;
+        if (path) {
+          const int at = 63 - __clzll((long long)path);
+          path &= ~(1ull << at);
+          p = a.x + (size_t)(first + at) * a.ld_x;
+        } else {
+          slot = slot ? slot - 1 : L - 1;
+          p = a.ring + ((size_t)i * L + slot) * a.C;
+        }
+        tap[lane][j] = in ? p : nullptr;
+      }
+    }
+  }
   const int c = (blockIdx.x * kTcThreads + threadIdx.x) * VEC;
   const bool in = c < a.C;
-  T w[K * VEC / (VEC == 8 ? 8 : 1)], b{};
-  if (in) {
+  float2 w[K][PAIRS], b[PAIRS];  // of two channels
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j] = reinterpret_cast<const T*>(a.w + (size_t)c * K)[j];
-    if (a.bias) b = *reinterpret_cast<const T*>(a.bias + c);
-  }
-  const int pos = a.pos[i];
-  uint64_t m[2];
-  tree_masks(a.t.parent + first, n, lane, m);
-  auto load = [&](int r, T (&v)[K]) {  // a node's taps, oldest first; false: not part of the tree
-    uint64_t path = tree_mask_of(m, r);
-    if (path == 0) return false;
-    int slot = (pos % L + L) % L;
-#pragma unroll
-    for (int j = L; j >= 0; --j) {
-      const uint16_t* p;
-      if (path) {
-        const int at = 63 - __clzll((long long)path);
-        path &= ~(1ull << at);
-        p = a.x + (size_t)(first + at) * a.ld_x + c;
-      } else {
-        slot = slot ? slot - 1 : L - 1;
-        p = a.ring + ((size_t)i * L + slot) * a.C + c;
-      }
-      if (in) v[j] = *reinterpret_cast<const T*>(p);
-    }
-    return true;
-  };
-  auto pick = [](const T& x, int e) {
-    if constexpr (VEC == 8) {
-      const uint32_t u = e < 4 ? (e < 2 ? x.x : x.y) : (e < 6 ? x.z : x.w);
-      return e & 1 ? bf16hi(u) : bf16lo(u);
-    } else {
-      return bf16_to_f32(x);
-    }
-  };
-  const int end = min(n, r0 + piece);
-  T next[K] = {};
-  bool there = load(r0, next);
-#pragma unroll 1
-  for (int r = r0; r < end; ++r) {
-    const bool now = there;
-    T v[K];
-#pragma unroll
-    for (int j = 0; j < K; ++j) v[j] = next[j];
-    if (r + 1 < end) there = load(r + 1, next);
+  for (int e = 0; e < PAIRS; ++e) {
+    b[e] = make_float2(0.0f, 0.0f);
     if (!in) continue;
-    float s[VEC];
+    auto weight = [&](int at) { return bf16_to_f32(a.w[(size_t)c * K + at]); };
+    if constexpr (VEC == 8) {
+      uint4 pack[K];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      s[e] = pick(b, e);
+      for (int j = 0; j < K; ++j) pack[j] = reinterpret_cast<const uint4*>(a.w + (size_t)c * K)[j];
+      auto part = [&](int at) {
+        const uint32_t u = tc_word(pack[at / 8], at % 8 / 2);
+        return at & 1 ? bf16hi(u) : bf16lo(u);
+      };
 #pragma unroll
-      for (int j = 0; j < K; ++j) s[e] = fmaf(pick(w[(e * K + j) / VEC], (e * K + j) % VEC), pick(v[j], e), s[e]);
-      if (a.silu) s[e] = silu_f(s[e]);
-      if (!now) s[e] = 0.0f;
+      for (int j = 0; j < K; ++j) w[j][e] = make_float2(part(2 * e * K + j), part((2 * e + 1) * K + j));
+      if (a.bias) b[e] = tc_pair(tc_word(*reinterpret_cast<const uint4*>(a.bias + c), e));
+    } else {
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][e] = make_float2(weight(j), 0.0f);
+      if (a.bias) b[e] = make_float2(bf16_to_f32(a.bias[c]), 0.0f);
     }
-    T o;
+  }
+  __syncthreads();
+  if (!in) return;
+  const int count = min(n - r0, piece);
+  T next[K] = {};
+  auto load = [&](int r) {
+    if (!tap[r][0]) return;
+#pragma unroll
+    for (int j = 0; j < K; ++j) next[j] = *reinterpret_cast<const T*>(tap[r][j] + c);
+  };
+  load(0);
+  uint16_t* out = a.out + (size_t)(first + r0) * a.ld_o + c;
+#pragma unroll 1
+  for (int r = 0; r < count; ++r, out += a.ld_o) {
+    float2 s[PAIRS];
+#pragma unroll
+    for (int e = 0; e < PAIRS; ++e) {
+      s[e] = b[e];
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        float2 v;
+        if constexpr (VEC == 8)
+          v = tc_pair(tc_word(next[j], e));
+        else
+          v = make_float2(bf16_to_f32(next[j]), 0.0f);
+        s[e] = tc_fma2(w[j][e], v, s[e]);
+      }
+    }
+    if (r + 1 < count) load(r + 1);
+    if (a.silu) {
+#pragma unroll
+      for (int e = 0; e < PAIRS; ++e) {
+        s[e].x = silu_f(s[e].x);
+        if (VEC == 8) s[e].y = silu_f(s[e].y);
+      }
+    }
+    const bool there = tap[r][0] != nullptr;
     if constexpr (VEC == 8)
-      o = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+      *reinterpret_cast<uint4*>(out) = there ? make_uint4(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y),
+                                                          pack_bf16x2(s[2].x, s[2].y), pack_bf16x2(s[3].x, s[3].y))
+                                             : make_uint4(0u, 0u, 0u, 0u);
     else
-      o = f32_to_bf16(s[0]);
-    *reinterpret_cast<T*>(a.out + (size_t)(first + r) * a.ld_o + c) = o;
+      *out = there ? f32_to_bf16(s[0].x) : (uint16_t)0;
   }
 }
 
@@ -153,10 +195,11 @@ cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
 // Bound: HBM, the state read once (32 KB a head of 64 x 128), up to 16 nodes; with 64
 // nodes the tensor cores' legacy rate is as near.
 //
-// A CTA takes some heads of one group of a sequence.  Their states come by bulk copies of
-// 64 rows, one ahead; L and x of the next head are made ready under the current head's
-// products, behind one barrier a piece.
-constexpr int kTsWarps = 8, kTsThreads = kTsWarps * 32, kTsBlock = 64, kTsStages = 2;
+// A CTA takes some heads of one group of a sequence.  Warps of two kinds: products (8 for
+// the channels; 16 with 64 nodes, halves of the rows) and helpers, which ask for the states
+// (bulk copies of 64 rows, one or two ahead) and make L and x of the next head under the
+// current head's products.  One barrier a piece of the state.
+constexpr int kTsBlock = 64, kTsStages = 2;
 constexpr int kTsSmemMax = 227 * 1024;
 
 template <int N, int MT>
@@ -167,17 +210,19 @@ struct TsCfg {
   static constexpr int kL = kNodes + 8;      // bf16 elements between rows of L
   static constexpr int kTerms = 3 * kNodes * kL;  // elements of a head's L
   static constexpr int kStage = kTsBlock * N * 4; // bytes of a piece of the state
+  static constexpr int kGroups = MT == 4 ? 2 : 1, kTiles = MT / kGroups;  // product warps for a column, tiles of rows each
+  static constexpr int kProd = 8 * kGroups, kHelp = 4 * kGroups, kWarps = kProd + kHelp;
   // B's tile is read once, before the first L is written
   static constexpr int kLs = 2 * kTerms > kNodes * kRow ? 2 * kTerms : kNodes * kRow;
 };
 // Shared memory of a CTA: the ring, barriers, masks, C's tile, L's terms twice (and first
-// B's tile), x twice, C B^T, the heads' dt and s.
+// B's tile), x twice, C B^T, the heads' dt, s and e^s.
 __host__ __device__ constexpr int ts_x_stride(int P) { return (P + 7) / 8 * 8 + 8; }
 template <int N, int MT>
 __host__ __device__ inline int ts_smem_bytes(int P, int heads) {
   using C = TsCfg<N, MT>;
   return kTsStages * C::kStage + 64 + C::kNodes * 8 + 32 + C::kNodes * C::kRow * 2 + C::kLs * 2 +
-         2 * C::kNodes * ts_x_stride(P) * 2 + C::kNodes * C::kCb * 4 + heads * C::kNodes * 12;
+         2 * C::kNodes * ts_x_stride(P) * 2 + C::kNodes * C::kCb * 4 + heads * C::kNodes * 16;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -212,13 +257,14 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
 }
 
 template <int N, int MT>
-__global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2)
+__global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
     tree_ssm_kernel(const __grid_constant__ TreeSsmArgs a, int heads, int chunks) {
   using Cf = TsCfg<N, MT>;
-  constexpr int KS = N / 16, NODES = Cf::kNodes;
+  constexpr int KS = N / 16, NODES = Cf::kNodes, MG = Cf::kTiles, SLOTS = MT == 4 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   const int xs = ts_x_stride(a.P);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTsStages * Cf::kStage);
+  int* gave_up = reinterpret_cast<int*>(full + kTsStages);
   uint64_t* mask = full + 8;
   unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);  // nodes with x that is not finite, three heads in turn
   uint16_t* ct = reinterpret_cast<uint16_t*>(bad + 4);
@@ -229,77 +275,186 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2)
   float* sdt = cb + NODES * Cf::kCb;     // [heads][NODES]
   float* shi = sdt + heads * NODES;
   float* slo = shi + heads * NODES;
+  float* ses = slo + heads * NODES;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  const int help = tid - Cf::kProd * 32;  // below 0: a product warp
   const int i = blockIdx.y, g = blockIdx.x / chunks, per = a.H / a.G;
   const int h0 = g * per + (blockIdx.x - g * chunks) * heads, nh = min(heads, (g + 1) * per - h0);
   const int first = a.t.cu[i], n = a.t.cu[i + 1] - first;
   const int blocks = (a.P + kTsBlock - 1) / kTsBlock;  // pieces of a head's state
   if (tid == 0) {
     for (int k = 0; k < kTsStages; ++k) mbar_init(&full[k], 1);
+    *gave_up = 0;
     fence_mbar_init();
   }
+  if (tid < 3) bad[tid] = 0ull;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   if (n == 0) return;
-  // ---- the states: thread 0 asks for piece `asked`
-  const uint64_t pol = policy_evict_first();
+
+  // ---- the first helper asks for the states
   int asked = 0, ask_p = 0;
   const float* ask_h = a.h + ((size_t)i * a.H + h0) * a.P * N;
   auto ask_state = [&] {
     if (asked == nh * blocks) return;
     const int st = asked % kTsStages, rows = min(kTsBlock, a.P - ask_p);
     mbar_arrive_expect_tx(&full[st], (uint32_t)rows * N * 4);
-    bulk_g2s(smem + st * Cf::kStage, ask_h, (uint32_t)rows * N * 4, &full[st], pol);
+    bulk_g2s(smem + st * Cf::kStage, ask_h, (uint32_t)rows * N * 4, &full[st], policy_evict_first());
     ask_h += rows * N;
     ask_p = ask_p + rows == a.P ? 0 : ask_p + rows;
     ++asked;
   };
-  if (tid == 0) ask_state();
-  // ---- masks, C and B rows, dt and the decays' sums
-  if (warp == 0) {
+  // x of a head, 16 helpers a row: asked for, then looked through by the threads that asked
+  // (wide), or both at once.  Columns past P hold anything: they only reach themselves.
+  // (halves with all exponent bits set are infinities and NaN)
+  auto finite = [](uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+    return w;
+  };
+  const int xq = help & 15, xj = help >> 4;
+  auto ask_x = [&](int head) {
+    uint16_t* d = xt + (head & 1) * NODES * xs;
+#pragma unroll 1
+    for (int j = xj; j < NODES; j += Cf::kHelp * 2) {
+      const uint16_t* src = a.x + (size_t)(first + j) * a.ld_in + (size_t)(h0 + head) * a.P;
+#pragma unroll 1
+      for (int q = xq; q < (a.wide_x ? a.P / 4 : a.P); q += 16) {
+        if (!a.wide_x) {
+          const uint32_t v = j < n ? src[q] : 0u;
+          const uint32_t f = finite(v);
+          if (f != v) atomicOr(&bad[head % 3], 1ull << j);
+          d[j * xs + q] = (uint16_t)f;
+        } else if (j < n) {
+          ts_copy8(d + j * xs + 4 * q, src + 4 * q);
+        } else {
+          *reinterpret_cast<uint2*>(d + j * xs + 4 * q) = make_uint2(0u, 0u);
+        }
+      }
+    }
+  };
+  auto look_x = [&](int head) {  // (the copies have landed)
+    if (!a.wide_x) return;
+    uint16_t* d = xt + (head & 1) * NODES * xs;
+#pragma unroll 1
+    for (int j = xj; j < NODES; j += Cf::kHelp * 2)
+#pragma unroll 1
+      for (int q = xq; q < a.P / 4; q += 16) {
+        uint2* p = reinterpret_cast<uint2*>(d + j * xs + 4 * q);
+        const uint2 v = *p, f = make_uint2(finite(v.x), finite(v.y));
+        if (f.x != v.x || f.y != v.y) {
+          atomicOr(&bad[head % 3], 1ull << j);
+          *p = f;
+        }
+      }
+  };
+  // L of a head: a lane keeps two columns (a bf16x2 word), `count` warps take rows in turn.
+  // Blocks above the diagonal are never read.
+  auto make_l = [&](int head, int w, int count) {
+    constexpr int LPR = NODES / 2, RPW = 32 / LPR;
+    const int col = lane % LPR * 2;
+    const float2 dc = *reinterpret_cast<const float2*>(sdt + head * NODES + col);
+    const float2 hc = *reinterpret_cast<const float2*>(shi + head * NODES + col);
+    const float2 lc = *reinterpret_cast<const float2*>(slo + head * NODES + col);
+    uint16_t* lh = lt + (head & 1) * Cf::kTerms + col;
+#pragma unroll(MT == 4 ? 2 : 1)
+    for (int row = w * RPW + lane / LPR; row < NODES; row += count * RPW) {
+      if (col > (row | 15)) continue;
+      const uint64_t m = mask[row] >> col;
+      const float hr = shi[head * NODES + row], lr = slo[head * NODES + row];
+      const float2 cv = *reinterpret_cast<const float2*>(cb + row * Cf::kCb + col);
+      float v0 = expf((hr - hc.x) + (lr - lc.x)) * dc.x * cv.x, v1 = expf((hr - hc.y) + (lr - lc.y)) * dc.y * cv.y;
+      v0 = m & 1 ? v0 : 0.0f;
+      v1 = m & 2 ? v1 : 0.0f;
+      uint32_t w0, w1, w2;
+      split3(v0, v1, w0, w1, w2);
+      uint32_t* d = reinterpret_cast<uint32_t*>(lh + row * Cf::kL);
+      constexpr int T = NODES * Cf::kL / 2;  // words of a term
+      d[0] = w0, d[T] = w1, d[2 * T] = w2;
+    }
+  };
+
+  // ---- the start: C and B, masks, dt, the decays' sums
+  if (help == 0) {
+    ask_state();
+    ask_state();
+  }
+  if (help >= 0) ask_x(0);
+  for (int k = tid; k < NODES * (N / 4); k += Cf::kWarps * 32) {
+    const int j = k / (N / 4), e = k % (N / 4) * 4;
+    if (j < n) {
+      ts_copy8(ct + j * Cf::kRow + e, a.Cm + (size_t)(first + j) * a.ld_in + (size_t)g * N + e);
+      ts_copy8(bt + j * Cf::kRow + e, a.Bm + (size_t)(first + j) * a.ld_in + (size_t)g * N + e);
+    } else {
+      *reinterpret_cast<uint2*>(ct + j * Cf::kRow + e) = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(bt + j * Cf::kRow + e) = make_uint2(0u, 0u);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  // A warp takes heads in turn, a lane nodes l and l + 32: the sums double their reach as
+  // the masks do.  (Sums of nodes outside the tree are never used.)
+  for (int head = warp; head < nh; head += Cf::kWarps) {
+    const float A = -expf(a.A_log[h0 + head]), bias = a.dt_bias[h0 + head];
+    float hi[SLOTS], lo[SLOTS];
+    int up[SLOTS];
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int j = lane + 32 * k;
+      float dt = 0.0f;
+      up[k] = -1;
+      if (j < n) {
+        const int q = a.t.parent[first + j];
+        up[k] = q < j ? q : -1;
+        dt = softplus_f(bf16_to_f32(a.dt[(size_t)(first + j) * a.ld_dt + h0 + head]) + bias);
+        dt = fminf(fmaxf(dt, 1e-9f), 1e9f);
+      }
+      if (j < NODES) sdt[head * NODES + j] = dt;
+      hi[k] = dt * A;
+      lo[k] = 0.0f;
+    }
+#pragma unroll 1
+    for (int d = 1; d < n; d *= 2) {
+      float nh_[SLOTS], nl[SLOTS];
+      int nu[SLOTS];
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) {
+        float x = __shfl_sync(0xffffffffu, hi[0], up[k] & 31), y = __shfl_sync(0xffffffffu, lo[0], up[k] & 31);
+        int u = __shfl_sync(0xffffffffu, up[0], up[k] & 31);
+        if (SLOTS == 2) {
+          const float x1 = __shfl_sync(0xffffffffu, hi[SLOTS - 1], up[k] & 31);
+          const float y1 = __shfl_sync(0xffffffffu, lo[SLOTS - 1], up[k] & 31);
+          const int u1 = __shfl_sync(0xffffffffu, up[SLOTS - 1], up[k] & 31);
+          if (up[k] & 32) x = x1, y = y1, u = u1;
+        }
+        nh_[k] = hi[k], nl[k] = lo[k], nu[k] = up[k];
+        if (up[k] >= 0) {
+          two_sum_acc(nh_[k], nl[k], x);
+          nl[k] += y;
+          nu[k] = u < 0 ? -1 : u;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) hi[k] = nh_[k], lo[k] = nl[k], up[k] = nu[k];
+    }
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int j = head * NODES + lane + 32 * k;
+      if (lane + 32 * k >= NODES) continue;
+      shi[j] = hi[k], slo[j] = lo[k];
+      ses[j] = expf(hi[k] + lo[k]);
+    }
+  }
+  if (warp == Cf::kWarps - 1) {
     uint64_t m[2];
     tree_masks(a.t.parent + first, n, lane, m);
     if (lane < NODES) mask[lane] = m[0];
     if (MT == 4) mask[lane + 32] = m[1];
-    if (lane < 3) bad[lane] = 0ull;
   }
-  for (int k = tid; k < NODES * (N / 4); k += kTsThreads) {
-    const int j = k / (N / 4), e = k % (N / 4) * 4;
-    uint2 vc = make_uint2(0u, 0u), vb = vc;
-    if (j < n) {
-      vc = *reinterpret_cast<const uint2*>(a.Cm + (size_t)(first + j) * a.ld_in + (size_t)g * N + e);
-      vb = *reinterpret_cast<const uint2*>(a.Bm + (size_t)(first + j) * a.ld_in + (size_t)g * N + e);
-    }
-    *reinterpret_cast<uint2*>(ct + j * Cf::kRow + e) = vc;
-    *reinterpret_cast<uint2*>(bt + j * Cf::kRow + e) = vb;
-  }
-  for (int k = tid; k < nh * NODES; k += kTsThreads) {
-    const int head = k / NODES, j = k % NODES;
-    float dt = 0.0f, la = 0.0f;
-    if (j < n) {
-      const float A = -expf(a.A_log[h0 + head]);
-      dt = softplus_f(bf16_to_f32(a.dt[(size_t)(first + j) * a.ld_dt + h0 + head]) + a.dt_bias[h0 + head]);
-      dt = fminf(fmaxf(dt, 1e-9f), 1e9f);
-      la = dt * A;
-    }
-    sdt[k] = dt;
-    shi[k] = la;
-  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  // sums along the paths; all of them read before any is written
-  constexpr int ROUNDS = 4;  // of 256 (head, node) pairs: the host keeps heads * NODES within 1024
-  float th[ROUNDS], tl[ROUNDS];
-#pragma unroll
-  for (int q = 0; q < ROUNDS; ++q) {
-    const int k = tid + q * kTsThreads;
-    th[q] = tl[q] = 0.0f;
-    if (k < nh * NODES)
-      for (uint64_t m = mask[k % NODES]; m; m &= m - 1)
-        two_sum_acc(th[q], tl[q], shi[k / NODES * NODES + __ffsll((long long)m) - 1]);
-  }
   // ---- C B^T
-  for (int k = warp; k < MT * 2 * MT; k += kTsWarps) {
+  for (int k = warp; k < MT * 2 * MT; k += Cf::kWarps) {
     const int mt = k / (2 * MT), nt = k % (2 * MT);
     if (nt > 2 * mt + 1) continue;  // above the diagonal: no node stands above one before it
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -314,123 +469,89 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2)
     *reinterpret_cast<float2*>(d) = make_float2(acc[0], acc[1]);
     *reinterpret_cast<float2*>(d + 8 * Cf::kCb) = make_float2(acc[2], acc[3]);
   }
+  if (help >= 0) look_x(0);
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < ROUNDS; ++q) {
-    const int k = tid + q * kTsThreads;
-    if (k < nh * NODES) shi[k] = th[q], slo[k] = tl[q];
+  make_l(0, warp, Cf::kWarps);
+
+  if (help >= 0) {
+    int item = 0;
+    for (int head = 0; head < nh; ++head)
+      for (int b = 0; b < blocks; ++b, ++item) {
+        __syncthreads();
+        if (help == 0) {
+          // (where a wait ran out, the stage may still be written)
+          if (item > 0 && !*reinterpret_cast<volatile int*>(gave_up)) ask_state();
+          if (b == 0) bad[(head + 2) % 3] = 0ull;  // read by all before, next written behind the next barrier
+        }
+        if (b > 0 || head + 1 == nh) continue;
+        ask_x(head + 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        make_l(head + 1, warp - Cf::kProd, Cf::kHelp);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        look_x(head + 1);
+      }
+    if (help == 0)  // nothing is in flight behind the CTA
+      for (int k = max(0, asked - kTsStages); k < asked; ++k) mbar_drain(&full[k % kTsStages], (k / kTsStages) & 1);
+    return;
   }
-  __syncthreads();
-  // (halves with all exponent bits set are infinities and NaN)
-  auto finite = [](uint32_t w) {
-    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
-    return w;
-  };
-  // x of a head: asked for, then looked through by the threads that asked (wide), or both
-  // at once; 16 threads a row.  Columns past P hold anything: they only reach themselves.
-  const int xq = tid & 15, xj = tid >> 4;
-  auto ask_x = [&](int head) {
-    uint16_t* d = xt + (head & 1) * NODES * xs;
-#pragma unroll 1
-    for (int j = xj; j < NODES; j += kTsThreads / 16) {
-      const bool in = mask[j] != 0;  // (0 for nodes past the last one too)
-      const uint16_t* src = a.x + (size_t)(first + j) * a.ld_in + (size_t)(h0 + head) * a.P;
-#pragma unroll 1
-      for (int q = xq; q < (a.wide_x ? a.P / 4 : a.P); q += 16) {
-        if (!a.wide_x) {
-          const uint32_t v = in ? src[q] : 0u;
-          const uint32_t f = finite(v);
-          if (f != v) atomicOr(&bad[head % 3], 1ull << j);
-          d[j * xs + q] = (uint16_t)f;
-        } else if (in) {
-          ts_copy8(d + j * xs + 4 * q, src + 4 * q);
-        } else {
-          *reinterpret_cast<uint2*>(d + j * xs + 4 * q) = make_uint2(0u, 0u);
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto look_x = [&](int head) {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (!a.wide_x) return;
-    uint16_t* d = xt + (head & 1) * NODES * xs;
-#pragma unroll 1
-    for (int j = xj; j < NODES; j += kTsThreads / 16)
-#pragma unroll 1
-      for (int q = xq; q < a.P / 4; q += 16) {
-        uint2* p = reinterpret_cast<uint2*>(d + j * xs + 4 * q);
-        const uint2 v = *p, f = make_uint2(finite(v.x), finite(v.y));
-        if (f.x != v.x || f.y != v.y) {
-          atomicOr(&bad[head % 3], 1ull << j);
-          *p = f;
-        }
-      }
-  };
-  // L of a head: a lane keeps two columns (a bf16x2 word), a warp takes rows in turn.
-  // Blocks above the diagonal are never read.
-  auto make_l = [&](int head) {
-    constexpr int LPR = NODES / 2, RPW = 32 / LPR;
-    const int col = lane % LPR * 2;
-    const float2 dc = *reinterpret_cast<const float2*>(sdt + head * NODES + col);
-    const float2 hc = *reinterpret_cast<const float2*>(shi + head * NODES + col);
-    const float2 lc = *reinterpret_cast<const float2*>(slo + head * NODES + col);
-    uint16_t* lh = lt + (head & 1) * Cf::kTerms + col;
-#pragma unroll 1
-    for (int row = warp * RPW + lane / LPR; row < NODES; row += kTsWarps * RPW) {
-      if (col > (row | 15)) continue;
-      const uint64_t m = mask[row] >> col;
-      const float hr = shi[head * NODES + row], lr = slo[head * NODES + row];
-      const float2 cv = *reinterpret_cast<const float2*>(cb + row * Cf::kCb + col);
-      // a node above has the larger s: the others' differences may overflow, and are not taken
-      float v0 = expf((hr - hc.x) + (lr - lc.x)) * dc.x * cv.x, v1 = expf((hr - hc.y) + (lr - lc.y)) * dc.y * cv.y;
-      v0 = m & 1 ? v0 : 0.0f;
-      v1 = m & 2 ? v1 : 0.0f;
-      uint32_t w0, w1, w2;
-      split3(v0, v1, w0, w1, w2);
-      uint32_t* d = reinterpret_cast<uint32_t*>(lh + row * Cf::kL);
-      constexpr int T = NODES * Cf::kL / 2;  // words of a term
-      d[0] = w0, d[T] = w1, d[2 * T] = w2;
-    }
-  };
+
+  // ---- the products
   const long long limit = *reinterpret_cast<volatile long long*>(&g_wait_limit);
-  ask_x(0);
-  make_l(0);
-  look_x(0);
-  uint2 cf[MT == 1 ? KS : 1][2];  // 16 nodes' C stays in registers
-  if (MT == 1) {
+  const int grp = warp / 8, pw = warp % 8 * 8;
+  auto tile = [&](int q) { return MT == 4 ? (q ? 3 - grp : grp) : q; };  // (L's blocks: 1 + 4 and 2 + 3)
+  unsigned live = 0;  // the thread's rows that are part of the tree
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+  for (int q = 0; q < MG; ++q)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) cf[ks % (MT == 1 ? KS : 1)][e] = *reinterpret_cast<const uint2*>(ct + (8 * e + r) * Cf::kRow + 16 * ks + 4 * c);
-  }
+    for (int e = 0; e < 2; ++e) live |= (mask[16 * tile(q) + r + 8 * e] != 0 ? 1u : 0u) << (2 * q + e);
   bool dead = false;
   int item = 0;
   for (int head = 0; head < nh; ++head) {
     const int h = h0 + head;
-    const float* hi_h = shi + head * NODES;
-    const float* lo_h = slo + head * NODES;
+    const float Dh = a.D[h];
     const uint16_t* lh = lt + (head & 1) * Cf::kTerms;
     const uint16_t* xh = xt + (head & 1) * NODES * xs;
-    const float Dh = a.D[h];
-    uint64_t odd = 0;
     for (int b = 0; b < blocks; ++b, ++item) {
-      const int st = item % kTsStages, p0 = b * kTsBlock + warp * 8;
+      const int st = item % kTsStages, p0 = b * kTsBlock + pw, p = p0 + 2 * c;
       // every warp has read the piece before; L and x of this head are there, those of the one before are read
       __syncthreads();
-      if (tid == 0) {
-        if (!dead) ask_state();
-        if (b == 0) bad[(head + 2) % 3] = 0ull;  // read by all before, next written behind the next barrier
+      const uint64_t odd = bad[head % 3];
+      const bool on = p0 < a.P;
+      // L x
+      float t[MG][4];
+      if (on) {
+#pragma unroll
+        for (int q = 0; q < MG; ++q) {
+          const int mt = tile(q);
+          float top[4] = {0.0f, 0.0f, 0.0f, 0.0f}, low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll(MT == 4 ? 1 : 2)
+          for (int ks = 0; ks <= mt; ++ks) {
+            uint32_t b0, b1, l[4];
+            ldsm2_trans(b0, b1, xh + (16 * ks + (lane & 15)) * xs + p0);
+            const uint16_t* ls = lh + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8;
+            ldsm4(l, ls);
+            mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
+            ldsm4(l, ls + NODES * Cf::kL);
+            mma_bf16(low, l[0], l[1], l[2], l[3], b0, b1);
+            ldsm4(l, ls + 2 * NODES * Cf::kL);
+            mma_bf16(low, l[0], l[1], l[2], l[3], b0, b1);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[q][e] = top[e] + low[e];
+        }
       }
-      if (b == 0) odd = bad[head % 3];
-      if (!dead && !mbar_warp_wait(&full[st], (item / kTsStages) & 1, limit)) dead = true;
-      float acc[MT][4], low[MT][4];
+      if (!dead && !mbar_warp_wait(&full[st], (item / kTsStages) & 1, limit)) {
+        dead = true;
+        *reinterpret_cast<volatile int*>(gave_up) = 1;
+      }
+      if (!on) continue;
+      // C h^T; the terms' sums apart (16 nodes: all three, for shorter chains)
+      float acc[MG][4], mid[MG][4], low[MG][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int q = 0; q < MG; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mt][e] = low[mt][e] = 0.0f;
-      const float* hs = reinterpret_cast<const float*>(smem + st * Cf::kStage) + (warp * 8 + r) * N + 4 * c;
+        for (int e = 0; e < 4; ++e) acc[q][e] = mid[q][e] = low[q][e] = 0.0f;
+      const float* hs = reinterpret_cast<const float*>(smem + st * Cf::kStage) + (pw + r) * N + 4 * c;
       float4 hv[2];
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -448,62 +569,42 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2)
         split3(hk.x, hk.y, b0[0], b0[1], b0[2]);
         split3(hk.z, hk.w, b1[0], b1[1], b1[2]);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint2 a0 = MT == 1 ? cf[ks % (MT == 1 ? KS : 1)][0] : *reinterpret_cast<const uint2*>(ct + (16 * mt + r) * Cf::kRow + 16 * ks + 4 * c);
-          const uint2 a1 = MT == 1 ? cf[ks % (MT == 1 ? KS : 1)][1] : *reinterpret_cast<const uint2*>(ct + (16 * mt + 8 + r) * Cf::kRow + 16 * ks + 4 * c);
-          mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[2], b1[2]);
-          mma_bf16(acc[mt], a0.x, a1.x, a0.y, a1.y, b0[0], b1[0]);
-          mma_bf16(low[mt], a0.x, a1.x, a0.y, a1.y, b0[1], b1[1]);
+        for (int q = 0; q < MG; ++q) {
+          const uint16_t* cs = ct + (16 * tile(q) + r) * Cf::kRow + 16 * ks + 4 * c;
+          const uint2 a0 = *reinterpret_cast<const uint2*>(cs);
+          const uint2 a1 = *reinterpret_cast<const uint2*>(cs + 8 * Cf::kRow);
+          mma_bf16(low[q], a0.x, a1.x, a0.y, a1.y, b0[2], b1[2]);
+          mma_bf16(acc[q], a0.x, a1.x, a0.y, a1.y, b0[0], b1[0]);
+          mma_bf16(MG == 1 ? mid[q] : low[q], a0.x, a1.x, a0.y, a1.y, b0[1], b1[1]);
         }
       }
-      if (b == 0 && head + 1 < nh) ask_x(head + 1);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int r0 = 16 * mt + r;
-        const float e0 = expf(hi_h[r0] + lo_h[r0]), e1 = expf(hi_h[r0 + 8] + lo_h[r0 + 8]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[mt][e] = (acc[mt][e] + low[mt][e]) * (e < 2 ? e0 : e1);
-          low[mt][e] = 0.0f;
-        }
-        float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p0 < a.P) {
-#pragma unroll
-          for (int ks = 0; ks <= mt; ++ks) {
-            uint32_t b0, b1;
-            ldsm2_trans(b0, b1, xh + (16 * ks + (lane & 15)) * xs + p0);
-#pragma unroll
-            for (int t = 2; t >= 0; --t) {
-              uint32_t l[4];
-              ldsm4(l, lh + t * NODES * Cf::kL + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8);
-              if (t)
-                mma_bf16(low[mt], l[0], l[1], l[2], l[3], b0, b1);
-              else
-                mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
-            }
-          }
-        }
+      for (int q = 0; q < MG; ++q)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = r0 + 8 * e, p = p0 + 2 * c;
+          const int j = 16 * tile(q) + r + 8 * e;
           if (j >= n || p >= a.P) continue;
-          const uint64_t m = mask[j];
           const uint32_t xw = *reinterpret_cast<const uint32_t*>(xh + j * xs + p);
+          const float es = ses[head * NODES + j];
           float y[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            y[f] = m ? (acc[mt][2 * e + f] + (top[2 * e + f] + low[mt][2 * e + f])) + Dh * (f ? bf16hi(xw) : bf16lo(xw)) : 0.0f;
-            for (uint64_t o = m & odd; o; o &= o - 1) {
+            const int at = 2 * e + f;
+            const float ch = acc[q][at] + (MG == 1 ? mid[q][at] + low[q][at] : low[q][at]);
+            y[f] = live >> (2 * q + e) & 1 ? fmaf(Dh, f ? bf16hi(xw) : bf16lo(xw), fmaf(ch, es, t[q][at])) : 0.0f;
+          }
+          if (odd) {
+            for (uint64_t o = mask[j] & odd; o; o &= o - 1) {
               const int at = __ffsll((long long)o) - 1;
-              if (p + f >= a.P) continue;
-              const float v = bf16_to_f32(a.x[(size_t)(first + at) * a.ld_in + (size_t)h * a.P + p + f]);
-              if (isfinite(v)) continue;
               float l = 0.0f;
-              for (int t = 2; t >= 0; --t) l += bf16_to_f32(lh[t * NODES * Cf::kL + j * Cf::kL + at]);
-              y[f] += (at == j ? l + Dh : l) * v;
+              for (int k = 2; k >= 0; --k) l += bf16_to_f32(lh[k * NODES * Cf::kL + j * Cf::kL + at]);
+              for (int f = 0; f < 2 && p + f < a.P; ++f) {
+                const float v = bf16_to_f32(a.x[(size_t)(first + at) * a.ld_in + (size_t)h * a.P + p + f]);
+                if (!isfinite(v)) y[f] += (at == j ? l + Dh : l) * v;
+              }
             }
           }
-          float* d = a.y + (size_t)(first + j) * a.H * a.P + (size_t)h * a.P + p;
+          float* d = a.y + ((size_t)(first + j) * a.H + h) * a.P + p;
           if (a.P % 2 == 0) {
             *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
           } else {
@@ -511,15 +612,8 @@ __global__ void __launch_bounds__(kTsThreads, MT == 4 ? 1 : 2)
             if (p + 1 < a.P) d[1] = y[1];
           }
         }
-      }
-    }
-    if (head + 1 < nh) {
-      make_l(head + 1);
-      look_x(head + 1);
     }
   }
-  if (tid == 0 && dead)  // gave up on a piece: what was asked for still lands here
-    for (int k = max(0, asked - kTsStages); k < asked; ++k) mbar_drain(&full[k % kTsStages], (k / kTsStages) & 1);
 }
 
 template <int N, int MT>
@@ -530,14 +624,14 @@ static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
   // one's state run under the current one's products; halved until there are CTAs for
   // most of the places on the SMs.  heads * nodes stays within the path sums' 1024 pairs.
   int heads = per < 16 ? per : 16;
-  while (heads > 1 && (heads * 16 * MT > 1024 || ts_smem_bytes<N, MT>(a.P, heads) > kTsSmemMax ||
+  while (heads > 1 && (ts_smem_bytes<N, MT>(a.P, heads) > kTsSmemMax ||
                        2 * (int64_t)a.t.nseq * a.G * ((per + heads - 1) / heads) < (MT == 4 ? 1 : 3) * (int64_t)num_sms()))
     heads = (heads + 1) / 2;
   const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
   auto k = tree_ssm_kernel<N, MT>;
   cudaError_t e = set_smem_once((const void*)k, smem, done_mask);
   if (e != cudaSuccess) return e;
-  return launch_k(k, dim3(a.G * chunks, a.t.nseq), dim3(kTsThreads), smem, s, true, a, heads, chunks);
+  return launch_k(k, dim3(a.G * chunks, a.t.nseq), dim3(TsCfg<N, MT>::kWarps * 32), smem, s, true, a, heads, chunks);
 }
 template <int N>
 static cudaError_t launch_tree_ssm_m(const TreeSsmArgs& a, int most, cudaStream_t s) {
