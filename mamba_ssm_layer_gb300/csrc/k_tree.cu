@@ -196,10 +196,13 @@ cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
 // nodes the tensor cores' legacy rate is as near.
 //
 // A CTA takes some heads of one group of a sequence.  Warps of two kinds: products (8 for
-// the channels; 16 with 64 nodes, halves of the rows) and helpers, which ask for the states
-// (bulk copies of 64 rows, one or two ahead) and make L and x of the next head under the
-// current head's products.  One barrier a piece of the state.
-constexpr int kTsBlock = 64, kTsStages = 2;
+// the channels; 16 with 64 nodes, halves of the rows) and helpers, which make L and x of
+// the next head under the current head's products; one barrier a head.  A product warp (a
+// pair of them with 64 nodes) streams the 8 channels' states it reads through a ring of
+// its own, three slots ahead, so that no barrier stands between a slot read and the next
+// one asked for.
+constexpr int kTsBlock = 64;   // channels of a head at once
+constexpr int kTsSlots = 4;
 constexpr int kTsSmemMax = 227 * 1024;
 
 template <int N, int MT>
@@ -209,19 +212,20 @@ struct TsCfg {
   static constexpr int kCb = kNodes + 4;     // floats between rows of C B^T
   static constexpr int kL = kNodes + 8;      // bf16 elements between rows of L
   static constexpr int kTerms = 3 * kNodes * kL;  // elements of a head's L
-  static constexpr int kStage = kTsBlock * N * 4; // bytes of a piece of the state
+  static constexpr int kK = N < 64 ? N : 64, kHalves = N / kK;  // states of a channel in a slot
+  static constexpr int kSlot = 8 * kK;            // floats
   static constexpr int kGroups = MT == 4 ? 2 : 1, kTiles = MT / kGroups;  // product warps for a column, tiles of rows each
   static constexpr int kProd = 8 * kGroups, kHelp = 4 * kGroups, kWarps = kProd + kHelp;
-  // B's tile is read once, before the first L is written
-  static constexpr int kLs = 2 * kTerms > kNodes * kRow ? 2 * kTerms : kNodes * kRow;
+  // the rows of C and B are read once, before the first L is written
+  static constexpr int kLs = 2 * kTerms > 2 * kNodes * kRow ? 2 * kTerms : 2 * kNodes * kRow;
 };
-// Shared memory of a CTA: the ring, barriers, masks, C's tile, L's terms twice (and first
-// B's tile), x twice, C B^T, the heads' dt, s and e^s.
+// Shared memory of a CTA: the rings, masks, C as operands, L's terms twice (and first the
+// rows of C and B), x twice, C B^T, the heads' dt, s and e^s.
 __host__ __device__ constexpr int ts_x_stride(int P) { return (P + 7) / 8 * 8 + 8; }
 template <int N, int MT>
 __host__ __device__ inline int ts_smem_bytes(int P, int heads) {
   using C = TsCfg<N, MT>;
-  return kTsStages * C::kStage + 64 + C::kNodes * 8 + 32 + C::kNodes * C::kRow * 2 + C::kLs * 2 +
+  return 8 * kTsSlots * C::kSlot * 4 + C::kNodes * 8 + 32 + C::kNodes * N * 2 + C::kLs * 2 +
          2 * C::kNodes * ts_x_stride(P) * 2 + C::kNodes * C::kCb * 4 + heads * C::kNodes * 16;
 }
 
@@ -245,15 +249,26 @@ __device__ __forceinline__ void ldsm2_trans(uint32_t& r0, uint32_t& r1, const vo
                : "r"(smem_addr(p))
                : "memory");
 }
+__device__ __forceinline__ void ts_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void ts_copy8(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
-// Two floats as three pairs of bf16 whose sum they are (all 24 bits).
+// Two floats as three pairs of bf16 whose sums they are: each takes the upper 8 bits of
+// what is left, which is all 24 (truncation costs fewer instructions than rounding).
 __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  hi = pack_bf16x2(a, b);
-  const float a1 = a - bf16lo(hi), b1 = b - bf16hi(hi);
-  mid = pack_bf16x2(a1, b1);
-  lo = pack_bf16x2(a1 - bf16lo(mid), b1 - bf16hi(mid));
+  const float2 minus = make_float2(-1.0f, -1.0f);
+  float2 v = make_float2(a, b);
+  auto rest = [&] {
+    const float2 u = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u), __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
+    v = tc_fma2(u, minus, v);
+  };
+  hi = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+  rest();
+  mid = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+  rest();
+  lo = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
 }
 
 template <int N, int MT>
@@ -263,13 +278,11 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
   constexpr int KS = N / 16, NODES = Cf::kNodes, MG = Cf::kTiles, SLOTS = MT == 4 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   const int xs = ts_x_stride(a.P);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTsStages * Cf::kStage);
-  int* gave_up = reinterpret_cast<int*>(full + kTsStages);
-  uint64_t* mask = full + 8;
+  uint64_t* mask = reinterpret_cast<uint64_t*>(smem + 8 * kTsSlots * Cf::kSlot * 4);
   unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);  // nodes with x that is not finite, three heads in turn
-  uint16_t* ct = reinterpret_cast<uint16_t*>(bad + 4);
-  uint16_t* lt = ct + NODES * Cf::kRow;  // L's terms, heads in turn
-  uint16_t* bt = lt;
+  uint4* cfrag = reinterpret_cast<uint4*>(bad + 4);  // C as a lane's operands of a tile and 16 states
+  uint16_t* lt = reinterpret_cast<uint16_t*>(cfrag + MT * KS * 32);  // L's terms, heads in turn
+  uint16_t *ct = lt, *bt = lt + NODES * Cf::kRow;
   uint16_t* xt = lt + Cf::kLs;           // x, heads in turn
   float* cb = reinterpret_cast<float*>(xt + 2 * NODES * xs);
   float* sdt = cb + NODES * Cf::kCb;     // [heads][NODES]
@@ -281,29 +294,44 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
   const int i = blockIdx.y, g = blockIdx.x / chunks, per = a.H / a.G;
   const int h0 = g * per + (blockIdx.x - g * chunks) * heads, nh = min(heads, (g + 1) * per - h0);
   const int first = a.t.cu[i], n = a.t.cu[i + 1] - first;
-  const int blocks = (a.P + kTsBlock - 1) / kTsBlock;  // pieces of a head's state
-  if (tid == 0) {
-    for (int k = 0; k < kTsStages; ++k) mbar_init(&full[k], 1);
-    *gave_up = 0;
-    fence_mbar_init();
-  }
   if (tid < 3) bad[tid] = 0ull;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   if (n == 0) return;
 
-  // ---- the first helper asks for the states
-  int asked = 0, ask_p = 0;
-  const float* ask_h = a.h + ((size_t)i * a.H + h0) * a.P * N;
-  auto ask_state = [&] {
-    if (asked == nh * blocks) return;
-    const int st = asked % kTsStages, rows = min(kTsBlock, a.P - ask_p);
-    mbar_arrive_expect_tx(&full[st], (uint32_t)rows * N * 4);
-    bulk_g2s(smem + st * Cf::kStage, ask_h, (uint32_t)rows * N * 4, &full[st], policy_evict_first());
-    ask_h += rows * N;
-    ask_p = ask_p + rows == a.P ? 0 : ask_p + rows;
-    ++asked;
+  // ---- the states.  A slot holds kK states of 8 channels, 16-byte pieces of odd rows
+  // with their 64-byte halves exchanged (no bank conflicts).  Every slot has a copy group.
+  const int grp = warp / 8 % Cf::kGroups, pw = warp % 8 * 8;
+  float* ring = reinterpret_cast<float*>(smem) + (warp & 7) * kTsSlots * Cf::kSlot;
+  constexpr int Q = Cf::kK / 4, COPIES = (8 * Q + 31) / 32;  // pieces of a row; copies of a lane
+  const int my_row = lane / Q, my_q = Q >= 8 ? lane % Q ^ (my_row & 1) * 4 : lane % Q;  // (rows a copy apart: an even number)
+  const uint32_t ring_to = smem_addr(ring) + (my_row * Cf::kK + my_q * 4) * 4;
+  const float* ask = a.h + (((size_t)i * a.H + h0) * a.P + pw + my_row) * N + lane % Q * 4;
+  int ask_slot = 0, ask_p = pw, ask_head = pw < a.P ? 0 : nh;
+  auto ask_state = [&](int half) {
+    if (ask_head < nh) {
+      const uint32_t to = ring_to + ask_slot * Cf::kSlot * 4;
+      const float* from = ask + half * Cf::kK;
+#pragma unroll
+      for (int k = 0; k < COPIES; ++k) {
+        // (with 64 nodes each warp of the pair asks for half)
+        if (Cf::kGroups == 2 && (COPIES > 1 ? k % 2 != grp : grp)) continue;
+        if (ask_p + my_row + k * (32 / Q) < a.P)
+          ts_copy16(to + k * (32 / Q) * Cf::kK * 4, from + (size_t)k * (32 / Q) * N);
+      }
+      if (half == Cf::kHalves - 1) {
+        ask += (size_t)kTsBlock * N;
+        ask_p += kTsBlock;
+        if (ask_p >= a.P) {
+          ask -= (size_t)(ask_p - pw - a.P) * N;
+          ask_p = pw;
+          ++ask_head;
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ask_slot = (ask_slot + 1) % kTsSlots;
   };
   // x of a head, 16 helpers a row: asked for, then looked through by the threads that asked
   // (wide), or both at once.  Columns past P hold anything: they only reach themselves.
@@ -375,11 +403,26 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
     }
   };
 
-  // ---- the start: C and B, masks, dt, the decays' sums
-  if (help == 0) {
-    ask_state();
-    ask_state();
+  // ---- the start: dt and the decays' sums, C and B, masks.  What is small is asked for
+  // before the states, whose pieces would fill the queues ahead of it.
+  int32_t par[SLOTS];
+  uint16_t raw[SLOTS];
+  float A = 0.0f, bias = 0.0f;
+  auto load_head = [&](int head) {  // a lane takes nodes l and l + 32
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) {
+      const int j = lane + 32 * k;
+      if (j < n) raw[k] = a.dt[(size_t)(first + j) * a.ld_dt + h0 + head];
+    }
+    A = a.A_log[h0 + head];
+    bias = a.dt_bias[h0 + head];
+  };
+#pragma unroll
+  for (int k = 0; k < SLOTS; ++k) {
+    par[k] = lane + 32 * k < n ? a.t.parent[first + lane + 32 * k] : -1;
+    raw[k] = 0;
   }
+  if (warp < nh) load_head(warp);
   if (help >= 0) ask_x(0);
   for (int k = tid; k < NODES * (N / 4); k += Cf::kWarps * 32) {
     const int j = k / (N / 4), e = k % (N / 4) * 4;
@@ -392,23 +435,20 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
-  // A warp takes heads in turn, a lane nodes l and l + 32: the sums double their reach as
-  // the masks do.  (Sums of nodes outside the tree are never used.)
+  if (help < 0)
+    for (int k = 0; k < kTsSlots - 1; ++k) ask_state(k % Cf::kHalves);
+  // A warp takes heads in turn: the sums double their reach as the masks do.  (Sums of
+  // nodes outside the tree are never used.)
   for (int head = warp; head < nh; head += Cf::kWarps) {
-    const float A = -expf(a.A_log[h0 + head]), bias = a.dt_bias[h0 + head];
+    A = -expf(A);
     float hi[SLOTS], lo[SLOTS];
     int up[SLOTS];
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
       const int j = lane + 32 * k;
-      float dt = 0.0f;
-      up[k] = -1;
-      if (j < n) {
-        const int q = a.t.parent[first + j];
-        up[k] = q < j ? q : -1;
-        dt = softplus_f(bf16_to_f32(a.dt[(size_t)(first + j) * a.ld_dt + h0 + head]) + bias);
-        dt = fminf(fmaxf(dt, 1e-9f), 1e9f);
-      }
+      up[k] = par[k] < j ? par[k] : -1;
+      float dt = softplus_f(bf16_to_f32(raw[k]) + bias);
+      dt = j < n ? fminf(fmaxf(dt, 1e-9f), 1e9f) : 0.0f;
       if (j < NODES) sdt[head * NODES + j] = dt;
       hi[k] = dt * A;
       lo[k] = 0.0f;
@@ -444,6 +484,7 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
       shi[j] = hi[k], slo[j] = lo[k];
       ses[j] = expf(hi[k] + lo[k]);
     }
+    if (head + Cf::kWarps < nh) load_head(head + Cf::kWarps);
   }
   if (warp == Cf::kWarps - 1) {
     uint64_t m[2];
@@ -451,8 +492,16 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
     if (lane < NODES) mask[lane] = m[0];
     if (MT == 4) mask[lane + 32] = m[1];
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (help < 0)
+    asm volatile("cp.async.wait_group %0;" ::"n"(kTsSlots - 1) : "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
+  for (int k = warp; k < MT * KS; k += Cf::kWarps) {
+    const uint16_t* cs = ct + (k / KS * 16 + r) * Cf::kRow + k % KS * 16 + 4 * c;
+    const uint2 a0 = *reinterpret_cast<const uint2*>(cs), a1 = *reinterpret_cast<const uint2*>(cs + 8 * Cf::kRow);
+    cfrag[k * 32 + lane] = make_uint4(a0.x, a1.x, a0.y, a1.y);
+  }
   // ---- C B^T
   for (int k = warp; k < MT * 2 * MT; k += Cf::kWarps) {
     const int mt = k / (2 * MT), nt = k % (2 * MT);
@@ -474,108 +523,89 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
   make_l(0, warp, Cf::kWarps);
 
   if (help >= 0) {
-    int item = 0;
-    for (int head = 0; head < nh; ++head)
-      for (int b = 0; b < blocks; ++b, ++item) {
-        __syncthreads();
-        if (help == 0) {
-          // (where a wait ran out, the stage may still be written)
-          if (item > 0 && !*reinterpret_cast<volatile int*>(gave_up)) ask_state();
-          if (b == 0) bad[(head + 2) % 3] = 0ull;  // read by all before, next written behind the next barrier
-        }
-        if (b > 0 || head + 1 == nh) continue;
-        ask_x(head + 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        make_l(head + 1, warp - Cf::kProd, Cf::kHelp);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        look_x(head + 1);
-      }
-    if (help == 0)  // nothing is in flight behind the CTA
-      for (int k = max(0, asked - kTsStages); k < asked; ++k) mbar_drain(&full[k % kTsStages], (k / kTsStages) & 1);
+    for (int head = 0; head < nh; ++head) {
+      __syncthreads();
+      if (help == 0) bad[(head + 2) % 3] = 0ull;  // read by all before, next written behind the next barrier
+      if (head + 1 == nh) break;
+      ask_x(head + 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      make_l(head + 1, warp - Cf::kProd, Cf::kHelp);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      look_x(head + 1);
+    }
     return;
   }
 
   // ---- the products
-  const long long limit = *reinterpret_cast<volatile long long*>(&g_wait_limit);
-  const int grp = warp / 8, pw = warp % 8 * 8;
   auto tile = [&](int q) { return MT == 4 ? (q ? 3 - grp : grp) : q; };  // (L's blocks: 1 + 4 and 2 + 3)
   unsigned live = 0;  // the thread's rows that are part of the tree
 #pragma unroll
   for (int q = 0; q < MG; ++q)
 #pragma unroll
     for (int e = 0; e < 2; ++e) live |= (mask[16 * tile(q) + r + 8 * e] != 0 ? 1u : 0u) << (2 * q + e);
-  bool dead = false;
-  int item = 0;
-  for (int head = 0; head < nh; ++head) {
+  const int HP = a.H * a.P;
+  float* yr = a.y + (size_t)(first + r) * HP + h0 * a.P + pw + 2 * c;
+  int slot = 0;
+  for (int head = 0; head < nh; ++head, yr += a.P) {
     const int h = h0 + head;
     const float Dh = a.D[h];
     const uint16_t* lh = lt + (head & 1) * Cf::kTerms;
     const uint16_t* xh = xt + (head & 1) * NODES * xs;
-    for (int b = 0; b < blocks; ++b, ++item) {
-      const int st = item % kTsStages, p0 = b * kTsBlock + pw, p = p0 + 2 * c;
-      // every warp has read the piece before; L and x of this head are there, those of the one before are read
-      __syncthreads();
-      const uint64_t odd = bad[head % 3];
-      const bool on = p0 < a.P;
+    __syncthreads();  // L and x of this head are there, those of the one before are read
+    const uint64_t odd = bad[head % 3];
+    for (int p0 = pw; p0 < a.P; p0 += kTsBlock) {
+      const int p = p0 + 2 * c;
       // L x
       float t[MG][4];
-      if (on) {
 #pragma unroll
-        for (int q = 0; q < MG; ++q) {
-          const int mt = tile(q);
-          float top[4] = {0.0f, 0.0f, 0.0f, 0.0f}, low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < MG; ++q) {
+        const int mt = tile(q);
+        float top[4] = {0.0f, 0.0f, 0.0f, 0.0f}, low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll(MT == 4 ? 1 : 2)
-          for (int ks = 0; ks <= mt; ++ks) {
-            uint32_t b0, b1, l[4];
-            ldsm2_trans(b0, b1, xh + (16 * ks + (lane & 15)) * xs + p0);
-            const uint16_t* ls = lh + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8;
-            ldsm4(l, ls);
-            mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
-            ldsm4(l, ls + NODES * Cf::kL);
-            mma_bf16(low, l[0], l[1], l[2], l[3], b0, b1);
-            ldsm4(l, ls + 2 * NODES * Cf::kL);
-            mma_bf16(low, l[0], l[1], l[2], l[3], b0, b1);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t[q][e] = top[e] + low[e];
+        for (int ks = 0; ks <= mt; ++ks) {
+          uint32_t b0, b1, l[4];
+          ldsm2_trans(b0, b1, xh + (16 * ks + (lane & 15)) * xs + p0);
+          const uint16_t* ls = lh + (16 * mt + (lane & 15)) * Cf::kL + 16 * ks + (lane >> 4) * 8;
+          ldsm4(l, ls);
+          mma_bf16(top, l[0], l[1], l[2], l[3], b0, b1);
+          ldsm4(l, ls + NODES * Cf::kL);
+          mma_bf16(low, l[0], l[1], l[2], l[3], b0, b1);
+          ldsm4(l, ls + 2 * NODES * Cf::kL);
+          mma_bf16(low, l[0], l[1], l[2], l[3], b0, b1);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[q][e] = top[e] + low[e];
       }
-      if (!dead && !mbar_warp_wait(&full[st], (item / kTsStages) & 1, limit)) {
-        dead = true;
-        *reinterpret_cast<volatile int*>(gave_up) = 1;
-      }
-      if (!on) continue;
-      // C h^T; the terms' sums apart (16 nodes: all three, for shorter chains)
-      float acc[MG][4], mid[MG][4], low[MG][4];
+      // C h^T, the smaller terms' sums apart
+      float acc[MG][4], low[MG][4];
 #pragma unroll
       for (int q = 0; q < MG; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[q][e] = mid[q][e] = low[q][e] = 0.0f;
-      const float* hs = reinterpret_cast<const float*>(smem + st * Cf::kStage) + (pw + r) * N + 4 * c;
-      float4 hv[2];
+        for (int e = 0; e < 4; ++e) acc[q][e] = low[q][e] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (KS == 1) {
-          hv[0] = *reinterpret_cast<const float4*>(hs);
-        } else if (ks % 2 == 0) {
-          // rows lie a multiple of the banks apart: odd ones read their halves in the other order
-          const float4 v0 = *reinterpret_cast<const float4*>(hs + 16 * (ks + (r & 1)));
-          const float4 v1 = *reinterpret_cast<const float4*>(hs + 16 * (ks + 1 - (r & 1)));
-          hv[0] = r & 1 ? v1 : v0;
-          hv[1] = r & 1 ? v0 : v1;
-        }
-        const float4 hk = hv[ks & 1];
-        uint32_t b0[3], b1[3];
-        split3(hk.x, hk.y, b0[0], b0[1], b0[2]);
-        split3(hk.z, hk.w, b1[0], b1[1], b1[2]);
+      for (int half = 0; half < Cf::kHalves; ++half) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kTsSlots - 2) : "memory");
+        if (Cf::kGroups == 2)
+          named_bar(1 + warp % 8, 64);  // the other warp's part has landed too, and both have read the slot before
+        else
+          __syncwarp();
+        ask_state((half + kTsSlots - 1) % Cf::kHalves);
+        const float* hs = ring + slot * Cf::kSlot + r * Cf::kK;
+        slot = (slot + 1) % kTsSlots;
 #pragma unroll
-        for (int q = 0; q < MG; ++q) {
-          const uint16_t* cs = ct + (16 * tile(q) + r) * Cf::kRow + 16 * ks + 4 * c;
-          const uint2 a0 = *reinterpret_cast<const uint2*>(cs);
-          const uint2 a1 = *reinterpret_cast<const uint2*>(cs + 8 * Cf::kRow);
-          mma_bf16(low[q], a0.x, a1.x, a0.y, a1.y, b0[2], b1[2]);
-          mma_bf16(acc[q], a0.x, a1.x, a0.y, a1.y, b0[0], b1[0]);
-          mma_bf16(MG == 1 ? mid[q] : low[q], a0.x, a1.x, a0.y, a1.y, b0[1], b1[1]);
+        for (int kk = 0; kk < Cf::kK / 16; ++kk) {
+          const int ks = half * (Cf::kK / 16) + kk;
+          const float4 hk = *reinterpret_cast<const float4*>(hs + (Cf::kK >= 32 ? (4 * kk + c) ^ (r & 1) * 4 : c) * 4);
+          uint32_t b0[3], b1[3];
+          split3(hk.x, hk.y, b0[0], b0[1], b0[2]);
+          split3(hk.z, hk.w, b1[0], b1[1], b1[2]);
+#pragma unroll
+          for (int q = 0; q < MG; ++q) {
+            const uint4 f = cfrag[(tile(q) * KS + ks) * 32 + lane];
+            mma_bf16(low[q], f.x, f.y, f.z, f.w, b0[2], b1[2]);
+            mma_bf16(acc[q], f.x, f.y, f.z, f.w, b0[0], b1[0]);
+            mma_bf16(low[q], f.x, f.y, f.z, f.w, b0[1], b1[1]);
+          }
         }
       }
 #pragma unroll
@@ -590,8 +620,8 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int at = 2 * e + f;
-            const float ch = acc[q][at] + (MG == 1 ? mid[q][at] + low[q][at] : low[q][at]);
-            y[f] = live >> (2 * q + e) & 1 ? fmaf(Dh, f ? bf16hi(xw) : bf16lo(xw), fmaf(ch, es, t[q][at])) : 0.0f;
+            y[f] = fmaf(Dh, f ? bf16hi(xw) : bf16lo(xw), fmaf(acc[q][at] + low[q][at], es, t[q][at]));
+            if (!(live >> (2 * q + e) & 1)) y[f] = 0.0f;
           }
           if (odd) {
             for (uint64_t o = mask[j] & odd; o; o &= o - 1) {
@@ -604,7 +634,7 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
               }
             }
           }
-          float* d = a.y + ((size_t)(first + j) * a.H + h) * a.P + p;
+          float* d = yr + (j - r) * HP + (p0 - pw);
           if (a.P % 2 == 0) {
             *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
           } else {
@@ -817,6 +847,5 @@ cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
 }
 
 int status_tree(int clear) { return tu_status(clear); }
-cudaError_t wait_limit_tree(long long cycles) { return tu_set_wait_limit(cycles); }
 
 }  // namespace m2
