@@ -650,13 +650,23 @@ template <int N, int MT>
 static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
   static int done_mask[64] = {0};
   const int per = a.H / a.G;
-  // Heads of a CTA: C, B and their product serve all of them, and the loads of the next
-  // one's state run under the current one's products; halved until there are CTAs for
-  // most of the places on the SMs.  heads * nodes stays within the path sums' 1024 pairs.
-  int heads = per < 16 ? per : 16;
-  while (heads > 1 && (ts_smem_bytes<N, MT>(a.P, heads) > kTsSmemMax ||
-                       2 * (int64_t)a.t.nseq * a.G * ((per + heads - 1) / heads) < (MT == 4 ? 1 : 3) * (int64_t)num_sms()))
-    heads = (heads + 1) / 2;
+  // Heads of a CTA.  Its start (masks, C B^T, the sums) takes as long as 1.5 heads and
+  // serves all of them; an SM works through its CTAs, of which two side by side take 0.7
+  // of what they take one after the other (64 nodes: one at a time).  Of 16, 8, 4, 2 and 1
+  // the one that comes out least; us for 128 heads of 64 x 128 in 8 groups:
+  //                          16     8      4      2      1
+  //   4 sequences x 16              -      7.4    6.6    8.2
+  //   16 x 16                24.2   19.2   20.9   22.8
+  //   64 x 5                 61.6   56.8
+  //   16 x 64                65.1   69.0   77.1
+  int heads = 1;
+  double least = 0.0;
+  for (int h = per < 16 ? per : 16;; h = (h + 1) / 2) {
+    const int64_t ctas = (int64_t)a.t.nseq * a.G * ((per + h - 1) / h), turns = (ctas + num_sms() - 1) / num_sms();
+    const double one = h + 1.5, all = MT == 4 || turns == 1 ? turns * one : 0.7 * turns * one;
+    if (ts_smem_bytes<N, MT>(a.P, h) <= kTsSmemMax && (least == 0.0 || all < least)) heads = h, least = all;
+    if (h == 1) break;
+  }
   const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
   auto k = tree_ssm_kernel<N, MT>;
   cudaError_t e = set_smem_once((const void*)k, smem, done_mask);
