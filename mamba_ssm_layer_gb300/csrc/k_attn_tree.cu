@@ -2,10 +2,11 @@
 // (include/mamba2.h has the rule of what a node sees), for few rows: nodes x query heads
 // of a kv head at most 16.  k_attn_tree_tc.cu serves more.
 //
-// A unit is one page (64 tokens) of one kv head; row m is node m / G with query head m % G
-// of the group.  The units of all sequences, in the order (sequence, kv head, page), are
-// cut into equal spans, one a CTA, and each span into equal runs, one a warp, which streams
-// them through its own ring of bulk copies.  On warp MMA, half a page at a time:
+// A unit is half a page (32 tokens) of one kv head; row m is node m / G with query head
+// m % G of the group.  The units of all sequences, in the order (sequence, kv head, page),
+// are cut into equal spans, one a CTA, and each span into equal runs, one a warp, which
+// streams their pages through its own ring.  What a tile costs a warp before its first page
+// counts as kAtrSetup units ahead of its own.  On warp MMA:
 //   S [16 x 32 tokens] = Q K^T    K codes become f16 and take their scale, exactly
 //   O [16 x D] += P V             likewise V; P rounded to f16 (2^-11)
 // The pages' orders of codes are those of both products' B operands, P goes from the
@@ -29,13 +30,14 @@ namespace m2 {
 
 constexpr int kAtWarps = 12, kAtrThreads = kAtWarps * 32;
 
+constexpr int kAtrSetup = 2;  // units (even: a page's units stay together)
 constexpr int kAtrRows = 16, kAtrParts = 2 * kAtWarps;  // a warp leaves a first and a last part at most
 
 template <int D>
 struct AtrCfg {
-  static constexpr int kUnit = Kv4Block<D>::kBytes;
-  static constexpr int kStages = D == 128 ? 2 : 4;  // 12 warps * stages * unit = 216 KB
-  static constexpr int kRing = kStages * kUnit;     // of one warp
+  static constexpr int kBytes = Kv4Block<D>::kBytes;
+  static constexpr int kStages = D == 128 ? 2 : 4;  // 12 warps * stages * bytes = 216 KB
+  static constexpr int kRing = kStages * kBytes;    // of one warp
   static constexpr int kStride = D + 8;             // floats between the rows of a record: no bank conflicts
   static constexpr int kRecord = 2 * kAtrRows + kAtrRows * kStride;  // maxima, sums, outputs
 };
@@ -44,11 +46,10 @@ struct AtrMeta {
   int32_t seg, before, after;
 };
 struct AtrShared {
-  uint64_t full[kAtWarps][4];
-  int32_t ok[kAtWarps][4];
+  uint16_t* out[kAtrParts][kAtrRows];  // where a joined row goes: the output, or the CTA's record; null: nowhere
   AtrMeta meta[kAtrParts];
   float part_m[kAtrParts][kAtrRows], part_l[kAtrParts][kAtrRows];  // maxima (then weights) and sums
-  float row_l[kAtrParts][kAtrRows];                                // sums of the cut tiles
+  float row_l[kAtrParts][kAtrRows];                                // sums of the cut tiles; -1: into a record
   uint32_t row_parts[kAtrParts];
   int32_t cta_seg[2];
   int32_t scan[kAtWarps];
@@ -106,10 +107,10 @@ struct AtrRows {
       for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
   }
 
-  // One unit in shared memory.  base: its first token less the context's length (0 or
-  // more: only nodes; -64 or less: only context); left: tokens of the sequence from its
-  // first on.  Half a page at a time: with a whole one's scores registers were spilled.
-  __device__ __forceinline__ void unit(const uint8_t* u, int base, int left, int lane) {
+  // A page in shared memory, its units h0 to h1 - 1.  base: its first token less the
+  // context's length (0 or more: only nodes; -64 or less: only context); left: tokens of
+  // the sequence from its first on.  (With a whole page's scores registers were spilled.)
+  __device__ __forceinline__ void units(const uint8_t* u, int base, int left, int h0, int h1, int lane) {
     using L = Kv4Block<D>;
     constexpr int GW = D / 32;  // words of a lane's codes: 2 groups each
     const int r = lane >> 2, c = lane & 3;
@@ -127,10 +128,10 @@ struct AtrRows {
       }
       const uint32_t be = __ballot_sync(0xffffffffu, even && 2 * lane < left), bo = __ballot_sync(0xffffffffu, odd && 2 * lane + 1 < left);
       if (be | bo)
-        for (int t = 0; t < 32; ++t) bad |= (uint64_t)((be >> t & 1) | (bo >> t & 1) << 1) << (2 * t);
+        for (int t = 16 * h0; t < 16 * h1; ++t) bad |= (uint64_t)((be >> t & 1) | (bo >> t & 1) << 1) << (2 * t);
     }
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
+    for (int half = h0; half < h1; ++half) {
       float s[4][4];
 #pragma unroll
       for (int nt = 0; nt < 4; nt += 2) {  // two tiles of 8 tokens in turn: a product waits for the one before it on its sums
@@ -245,7 +246,7 @@ struct AtrRows {
         }
       }
     }
-    // values that are not finite, kept out of the product: they are NaN to the rows that see them
+    // values that are not finite, kept out of the products: they are NaN to the rows that see them
     for (; bad; bad &= bad - 1) {
       const int t = __ffsll((long long)bad) - 1;
 #pragma unroll
@@ -299,27 +300,28 @@ struct AtrRows {
   }
 };
 
+__device__ __forceinline__ void atr_copy16(uint32_t dst, const void* src, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(pol) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_constant__ AtrArgs a) {
   using C = AtrCfg<D>;
   constexpr int S = C::kStages, ROWS = kAtrRows, PARTS = kAtrParts;
-  static_assert(PARTS * ROWS == kAtrThreads && PARTS <= 32 && S <= 4, "a thread per part and row");
+  static_assert(PARTS * ROWS == kAtrThreads && PARTS <= 32, "a thread per part and row");
   static_assert(C::kRecord * 4 <= C::kRing, "a record lies in its warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
   AtrShared* sh = reinterpret_cast<AtrShared*>(smem + kAtWarps * C::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&sh->full[warp][s], 1);
-    sh->meta[2 * warp].seg = sh->meta[2 * warp + 1].seg = -1;
-    fence_mbar_init();
-  }
+  if (lane == 0) sh->meta[2 * warp].seg = sh->meta[2 * warp + 1].seg = -1;
   if (tid < 2) sh->cta_seg[tid] = -1;
   pdl_wait();
   pdl_trigger();
   const int B = a.g.t.nseq;
   // ---- the span and its runs: prefix sums of the sequences' units (one a thread)
   static_assert(kSeqs <= kAtrThreads, "a sequence a thread");
-  const int mine = tid < B ? atr_units(a, tid, ROWS) : 0;
+  const int their = tid < B ? (atr_len(a.g, tid) + kPage - 1) / kPage : 0;
+  const int mine = their ? (2 * their + kAtrSetup) * a.g.c.Hkv : 0;
   int pre = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -377,91 +379,99 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
 
   // ---- this warp's run
   uint8_t* ring = smem + warp * C::kRing;
-  const int u0 = sh->run0[warp], u1 = sh->run0[warp + 1], n = u1 - u0;
-  if (n > 0) {
+  const int u0 = sh->run0[warp], u1 = sh->run0[warp + 1];
+  if (u1 > u0) {
     AtrCursor cur;
     cur.b = sh->run_b[warp];
     cur.load(a, ROWS);
+    int at;  // the tile's first unit behind its set-up
     {
-      const int in = u0 - sh->run_base[warp];
+      const int each = 2 * cur.pages + kAtrSetup, in = u0 - sh->run_base[warp];
       cur.tile = 0;
-      cur.hk = in / cur.pages;
-      cur.page = in - cur.hk * cur.pages;
+      cur.hk = in / each;
+      at = u0 - (in - cur.hk * each) + kAtrSetup;
+      cur.page = max(u0 - at, 0) / 2;
     }
-    AtrCursor ahead = cur;
+    // Pages are asked for by all lanes (a bulk copy by one of them held its warp up for
+    // 1000 cycles, a page's products take 6500).  Their numbers are loaded ahead, the first two together.
     const uint64_t pol = policy_evict_first();
-    // The page of the next copy, loaded a unit before it is asked for.
-    auto entry = [&]() { return a.g.c.table[(size_t)ahead.b * a.g.c.ld_table + ahead.page]; };
-    int page = entry();
-    int fetched = 0;
-    auto fetch = [&]() {  // unit `fetched` of the run into its stage
-      const int st = fetched % S, hk = ahead.hk, id = page;
-      if (++fetched < n) {
+    AtrCursor ahead = cur;
+    int ahead_at = at, id = 0, id_hk = 0, id1 = 0, id1_hk = 0;
+    bool more = true, more1 = true;  // id and id1 are pages of the run
+    auto look = [&](bool first) {    // id = id1; id1 = the run's next page
+      id = id1, id_hk = id1_hk, more = more1;
+      if (!more1) return;
+      if (!first) {
+        if (ahead.page + 1 == ahead.pages) ahead_at += 2 * ahead.pages + kAtrSetup;
         ahead.next(a, ROWS);
-        page = entry();
       }
-      if (lane == 0) {
-        const bool ok = id >= 0 && id < a.g.c.n_pages;
-        sh->ok[warp][st] = ok;
-        if (ok) {
-          mbar_arrive_expect_tx(&sh->full[warp][st], C::kUnit);
-          bulk_g2s(ring + st * C::kUnit, a.g.c.pages + ((size_t)id * a.g.c.Hkv + hk) * C::kUnit, C::kUnit,
-                   &sh->full[warp][st], pol);
-        } else {
-          M2_RECORD_ARG(g_status);
-          mbar_arrive(&sh->full[warp][st]);
-        }
-      }
+      more1 = ahead_at + 2 * ahead.page < u1;
+      if (more1) id1 = a.g.c.table[(size_t)ahead.b * a.g.c.ld_table + ahead.page], id1_hk = ahead.hk;
     };
-    while (fetched < S && fetched < n) fetch();
+    look(true);
+    look(false);
+    int fetched = 0;
+    uint32_t ok = 0;  // stages that hold a page
+    const uint32_t to = smem_addr(ring) + 16 * lane;
     uint64_t tree[2] = {0, 0};
     AtrRows<D> rows;
-    rows.start(a, cur.b, cur.hk, tree, true, lane);
-    int first_page = cur.page;   // of the tile's part in this run
-    int row_at = u0 - cur.page;  // the tile's first unit
-    int pos = a.g.pos[cur.b];
-    bool dead = false;
-    for (int i = 0; i < n; ++i) {
-      const int st = i % S;
-      if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[warp][st], (i / S) & 1))) {
-        dead = true;
-        break;
+    int pos = 0, masks_of = -1;
+    // Everything stands in this loop once: code that is not in the SM's cache costs some 50 cycles an instruction.
+#pragma unroll 1
+    for (int i = 0; at + 2 * cur.page < u1; ++i) {
+      // the pages up to S - 1 after this one; always a copy group
+#pragma unroll 1
+      for (; fetched < i + S; ++fetched) {
+        if (more) {
+          const int st = fetched % S;
+          const bool good = id >= 0 && id < a.g.c.n_pages;
+          ok = good ? ok | 1u << st : ok & ~(1u << st);
+          if (good) {
+            const uint8_t* src = a.g.c.pages + ((size_t)id * a.g.c.Hkv + id_hk) * C::kBytes + 16 * lane;
+#pragma unroll
+            for (int k = 0; k < C::kBytes / 512; ++k) atr_copy16(to + st * C::kBytes + 512 * k, src + 512 * k, pol);
+          } else if (lane == 0) {
+            M2_RECORD_ARG(g_status);
+          }
+          look(false);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      if (sh->ok[warp][st]) rows.unit(ring + st * C::kUnit, cur.page * kPage - pos, cur.len - cur.page * kPage, lane);
+      if (i == 0 || cur.page == 0) {
+        pos = a.g.pos[cur.b];
+        rows.start(a, cur.b, cur.hk, tree, cur.b != masks_of, lane);
+        masks_of = cur.b;
+      }
+      const int st = i % S, left = u1 - at - 2 * cur.page;  // units of the run from this page on
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      __syncwarp();
+      if (ok >> st & 1)
+        rows.units(ring + st * C::kBytes, cur.page * kPage - pos, cur.len - cur.page * kPage,
+                   max(u0 - at - 2 * cur.page, 0), min(left, 2), lane);
       __syncwarp();  // the stage is read
-      if (fetched < n) fetch();
       const bool ends = cur.page + 1 == cur.pages;
-      if (ends || i + 1 == n) {  // the tile leaves this warp
+      if (ends || left <= 2) {  // the tile leaves this warp
         rows.finish();
-        if (ends && first_page == 0) {
+        const int end = at + 2 * cur.pages;
+        if (at >= u0 && end <= u1) {
           rows.store_out(a, cur.b, cur.hk, lane);
         } else {
-          const int slot = i + 1 == n ? 1 : 0;
+          const int slot = end + kAtrSetup >= u1 ? 1 : 0;
           // the last part goes into the ring (free by now), an earlier one through L2
           rows.store_part(slot ? reinterpret_cast<float*>(ring) : a.part + (size_t)(cta * kAtWarps + warp) * C::kRecord,
                           sh->part_m[2 * warp + slot], sh->part_l[2 * warp + slot], lane);
           if (lane == 0) {
             AtrMeta& mt = sh->meta[2 * warp + slot];
             mt.seg = cur.seg(a);
-            mt.before = row_at < s0;
-            mt.after = row_at + cur.pages > s1;
+            mt.before = at < s0;
+            mt.after = end > s1;
           }
         }
-        if (i + 1 < n) {
-          const int b = cur.b;
-          cur.next(a, ROWS);
-          first_page = 0;
-          row_at = u0 + i + 1;
-          pos = a.g.pos[cur.b];
-          rows.start(a, cur.b, cur.hk, tree, cur.b != b, lane);
-        }
-      } else {
-        ++cur.page;
+        if (!ends) break;
+        at = end + kAtrSetup;
       }
-    }
-    if (dead) {  // every copy of this warp has landed before the CTA goes on
-      for (int i = max(0, fetched - S); i < fetched; ++i)
-        if (!mbar_drain(&sh->full[warp][i % S], (i / S) & 1)) break;
+      cur.next(a, ROWS);
+      if (cur.b >= B) break;
     }
   }
   __syncthreads();
@@ -485,31 +495,36 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
         sh->part_m[k][x] = w;
       }
       const int k = __popc(lead & ((1u << e) - 1));
-      sh->row_l[k][x] = l;
-      sh->row_parts[k] = parts;
       const AtrMeta& mt = sh->meta[e];
-      if (mt.before || mt.after) {  // cut between CTAs too
+      uint16_t* out = atr_out(a, mt.seg, x, ROWS, D);
+      if (out && (mt.before || mt.after)) {  // cut between CTAs too
         float* rec = a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * C::kRecord;
         rec[x] = top;
         rec[ROWS + x] = l;
-        if (x == 0) sh->cta_seg[mt.before ? 0 : 1] = mt.seg;
+        out = reinterpret_cast<uint16_t*>(rec + 2 * ROWS + x * C::kStride);
+        l = -1.0f;
       }
+      if (x == 0) {
+        sh->row_parts[k] = parts;
+        if (mt.before || mt.after) sh->cta_seg[mt.before ? 0 : 1] = mt.seg;
+      }
+      sh->row_l[k][x] = l;
+      sh->out[k][x] = out;
     }
   }
   __syncthreads();
   for (int i = tid; i < ntiles * (ROWS * D / 4); i += kAtrThreads) {
     const int k = i / (ROWS * D / 4), x = i / (D / 4) % ROWS, d = i % (D / 4) * 4;
     uint32_t parts = sh->row_parts[k];
-    const AtrMeta& mt = sh->meta[__ffs(parts) - 1];
-    uint16_t* out = atr_out(a, mt.seg, x, ROWS, D);
+    uint16_t* out = sh->out[k][x];
     if (!out) continue;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     while (parts) {
-      // four parts at a time, their loads together
-      float4 v[4];
-      float w[4];
+      // six parts at a time, their loads together
+      float4 v[6];
+      float w[6];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 6; ++j) {
         const int y = parts ? __ffs(parts) - 1 : -1;
         parts &= parts - 1;
         w[j] = 0.0f;
@@ -522,15 +537,15 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 6; ++j)
         o.x = fmaf(v[j].x, w[j], o.x), o.y = fmaf(v[j].y, w[j], o.y), o.z = fmaf(v[j].z, w[j], o.z),
         o.w = fmaf(v[j].w, w[j], o.w);
     }
-    if (mt.before || mt.after)
-      *reinterpret_cast<float4*>(a.cta_part + (size_t)(2 * cta + (mt.before ? 0 : 1)) * C::kRecord + 2 * ROWS +
-                                 x * C::kStride + d) = o;
+    const float l = sh->row_l[k][x];
+    if (l < 0.0f)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + d) = o;
     else
-      atr_store4(out + d, o, sh->row_l[k][x]);
+      atr_store4(out + d, o, l);
   }
   if (tid < 2 && !a.by_row) a.cta_seg[2 * cta + tid] = sh->cta_seg[tid];
 }
@@ -644,6 +659,5 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s) {
 }
 
 int status_attn_tree(int clear) { return tu_status(clear); }
-cudaError_t wait_limit_attn_tree(long long cycles) { return tu_set_wait_limit(cycles); }
 
 }  // namespace m2

@@ -1053,7 +1053,7 @@ int m2_set_wait_limit(int64_t cycles) {
   if (wait_limit_gemv(v) != cudaSuccess || wait_limit_gemv_mma(v) != cudaSuccess ||
       wait_limit_gemm_tc(v) != cudaSuccess || wait_limit_mixer(v) != cudaSuccess ||
       wait_limit_attn(v) != cudaSuccess || wait_limit_attn_decode(v) != cudaSuccess ||
-      wait_limit_attn_tree(v) != cudaSuccess || wait_limit_attn_tree_tc(v) != cudaSuccess) {
+      wait_limit_attn_tree_tc(v) != cudaSuccess) {
     cudaGetLastError();
     return M2_ERR_DEVICE;
   }

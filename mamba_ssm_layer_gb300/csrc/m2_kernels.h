@@ -73,7 +73,6 @@ cudaError_t wait_limit_gemm_tc(long long cycles);
 cudaError_t wait_limit_mixer(long long cycles);
 cudaError_t wait_limit_attn(long long cycles);
 cudaError_t wait_limit_attn_decode(long long cycles);
-cudaError_t wait_limit_attn_tree(long long cycles);
 cudaError_t wait_limit_attn_tree_tc(long long cycles);
 
 // Number of SMs of the current device (cached).
