@@ -698,8 +698,7 @@ static cudaError_t launch_tt(const AttnTreeArgs& g, cudaStream_t s) {
   a.G = g.H / g.c.Hkv;
   a.most_tiles = (g.most * a.G + C::kRows - 1) / C::kRows;
   const int64_t tiles = (int64_t)g.t.nseq * g.c.Hkv * a.most_tiles;
-  // Few tiles in a narrow table: a CTA takes a whole tile, and nothing is left to combine.
-  a.by_row = tiles <= num_sms() && g.c.ld_table <= 32;
+  a.by_row = atr_by_row(tiles, g.c.ld_table);
   a.nc = a.by_row ? (int)tiles : num_sms();
   a.cta_seg = static_cast<int32_t*>(g.ws);
   a.part = nullptr;

@@ -71,6 +71,18 @@ __device__ __forceinline__ uint16_t* atr_out(const AtrArgs& a, int seg, int row,
   if (node >= atr_nodes(a.g, b)) return nullptr;
   return a.g.out + (size_t)(a.g.t.cu[b] + node) * a.g.ld_o + (size_t)(hk * a.G + x - node * a.G) * D;
 }
+// A CTA a tile, none cut, and nothing to combine, where the tiles are short or enough of
+// them to fill the SMs.  (The table's width is what the host knows of the lengths.)  us,
+// split / whole, 32 heads over 8 of 128 channels, as many pages as the table is wide:
+//                    4 nodes (16 rows)       5 nodes (20 rows)
+//   1 x 8 pages      14.3 / 12.0             12.0 / 12.3
+//   1 x 16           14.3 / 14.9             15.0 / 17.7
+//   1 x 32           14.5 / 20.1             15.9 / 28.1
+//   8 x 32           18.6 / 20.5             22.5 / 28.9
+//   16 x 32                                  34.0 / 29.4
+inline bool atr_by_row(int64_t tiles, int ld_table) {
+  return tiles <= num_sms() && ld_table <= (2 * tiles > num_sms() ? 32 : 8);
+}
 __device__ __forceinline__ void atr_store4(uint16_t* d, float4 o, float l) {
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros
   *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
