@@ -37,8 +37,9 @@ namespace m2 {
 constexpr int kTtSoft = 8, kTtDeq = 4, kTtProducts = kTtSoft + kTtDeq, kTtCopies = kTtProducts + 1;  // warps
 constexpr int kTtWarps = 14, kTtThreads = kTtWarps * 32;
 // What a tile costs beside its pages, in pages (loading queries, storing outputs): the spans
-// are cut by the sum.
-constexpr int kTtSetup = 5;
+// are cut by the sum.  0, 2, 5, 8: 58.7, 44.6, 37.7, 36.4 us for 16 trees of 9 to 16 nodes,
+// 83, 82, 76, 76 for two of 64.
+constexpr int kTtSetup = 8;
 
 template <int D, int T>
 struct TtCfg {
@@ -720,6 +721,9 @@ static cudaError_t launch_tt(const AttnTreeArgs& g, cudaStream_t s) {
 
 cudaError_t launch_attn_tree_tc(const AttnTreeArgs& a, cudaStream_t s) {
   const int rows = a.most * (a.H / a.c.Hkv);
+  // Up to 128 rows as one tile whose pages go to two chains in turn; more as two tiles that
+  // share each page.  The other way round: 36 / 42 us (16 trees of up to 64 rows), 91 / 76
+  // (two of 256).
   if (a.c.D == 128) return rows <= 128 ? launch_tt<128, 1>(a, s) : launch_tt<128, 2>(a, s);
   return rows <= 128 ? launch_tt<64, 1>(a, s) : launch_tt<64, 2>(a, s);
 }
