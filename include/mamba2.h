@@ -523,7 +523,7 @@ int mamba2_layer_tree_commit(const m2_dims* dims, const m2_layer* layer, int32_t
  *             pool, which are left out.
  *   ws        m2_attn_tree_kv4_workspace_bytes(H, Hkv, head_dim) bytes, 256-byte aligned.
  * A row that sees nothing, or whose scores are all -Inf, is zeros.  The number of
- * sequences (at most 128 of them counted) times ld_table times 4 (H + Hkv) stays below
+ * sequences (at most 128 of them counted) times ld_table + 8 times 4 (H + Hkv) stays below
  * 2^31 (M2_ERR_UNSUPPORTED). */
 size_t m2_attn_tree_kv4_workspace_bytes(int32_t H, int32_t Hkv, int32_t head_dim);
 int m2_attn_tree_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_q, uint16_t* out, int32_t ld_o,

@@ -15,6 +15,9 @@
 // shifted to a page's tokens it says what the row sees there.  Rows that a warp, then a
 // CTA, holds only in part are joined: warps through shared memory, CTAs by
 // attn_tree_combine.
+// Bound: issue slots (a page takes a warp 6400 cycles, 12 warps an SM; 1000 more pass between
+// pages), the start until the first page (5 us) and the joining (5 us): 64 chains of 4 over
+// 64 to 4096 tokens 62 us (155 MB, 2.5 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

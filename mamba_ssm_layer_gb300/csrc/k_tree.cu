@@ -20,6 +20,8 @@ namespace m2 {
 // a lane of the first warp looks up a node's rows for the CTA.
 // Sums run as the single-token conv's, oldest tap first; products of two bf16 values are
 // exact, so the results are the same bits.
+// Bound: latency (masks, rows: 3.0 us for a chain of 5, 10240 channels), then issue slots:
+// 16 trees of 16 nodes 7.1 us, of 64 nodes 20 us (42 MB).
 constexpr int kTcThreads = 128, kTcMost = 16, kTcCtas = 5;
 
 // Two fused multiply-adds, each rounded as one.
@@ -152,7 +154,9 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
 
 template <int VEC>
 static cudaError_t launch_tree_conv_v(const TreeConvArgs& a, cudaStream_t s) {
-  // One node a CTA while all of them run at once; then so many that they do.
+  // One node a CTA while all of them run at once; then so many that they do.  For 2, 4, 8,
+  // 16 CTAs an SM: 16 x 4 nodes 5.4, 4.9, 4.1, 4.1 us, 16 x 16 10.0, 7.1, 8.6, 10.3, 64 x 5
+  // 8.9, 8.9, 11.7, 12.5.
   const int blocks = (a.C + kTcThreads * VEC - 1) / (kTcThreads * VEC), nodes = a.t.cu[a.t.nseq];
   int piece = 1;
   while (piece < kTcMost && (int64_t)blocks * nodes / piece > (int64_t)kTcCtas * num_sms()) piece *= 2;
@@ -192,8 +196,11 @@ cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
 // would cost its differences their last bits).
 // Values of x that are not finite would reach nodes beside their path as 0 * Inf: they
 // are 0 in the product, and the nodes below them add them when they store.
-// Bound: HBM, the state read once (32 KB a head of 64 x 128), up to 16 nodes; with 64
-// nodes the tensor cores' legacy rate is as near.
+// Bound: HBM, the state read once (32 KB a head of 64 x 128), up to 16 nodes: 64 chains of
+// 5 take 57 us (4.9 TB/s), 16 trees of 16 19 us (of which 3 us pass until the first
+// product), one chain 3.5 us; the split and the products fill three quarters of the issue
+// slots meanwhile.  More nodes: issue slots and the legacy tensor rate (16 x 32 nodes 29 us,
+// 16 x 64 65 us).
 //
 // A CTA takes some heads of one group of a sequence.  Warps of two kinds: products (8 for
 // the channels; 16 with 64 nodes, halves of the rows) and helpers, which make L and x of
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
         ask += (size_t)kTsBlock * N;
         ask_p += kTsBlock;
         if (ask_p >= a.P) {
-          ask -= (size_t)(ask_p - pw - a.P) * N;
+          ask -= (int64_t)(ask_p - pw - a.P) * N;
           ask_p = pw;
           ++ask_head;
         }
@@ -669,7 +676,7 @@ static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
   }
   const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
   auto k = tree_ssm_kernel<N, MT>;
-  cudaError_t e = set_smem_once((const void*)k, smem, done_mask);
+  cudaError_t e = set_smem_once((const void*)k, kTsSmemMax, done_mask);  // (one limit whatever the call: no call lowers another's)
   if (e != cudaSuccess) return e;
   return launch_k(k, dim3(a.G * chunks, a.t.nseq), dim3(TsCfg<N, MT>::kWarps * 32), smem, s, true, a, heads, chunks);
 }
@@ -824,9 +831,9 @@ static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
   const dim3 grid(a.H * psplit, a.t.nseq), block(256);
   int most = 0;
   for (int i = 0; i < a.t.nseq; ++i) most = a.t.cu[i + 1] - a.t.cu[i] > most ? a.t.cu[i + 1] - a.t.cu[i] : most;
-  const int smem = most * (a.N * 2 + 8 * RPW * rows * 4);  // at most 64 * (32 + 2048) bytes: N = 16
+  const int each = a.N * 2 + 8 * RPW * rows * 4, smem = most * each;  // at most 64 * (32 + 2048) bytes: N = 16
   auto go = [&](void (*k)(TreeCommitArgs, int), int* done_mask) {
-    const cudaError_t e = smem > 48 * 1024 ? set_smem_once((const void*)k, smem, done_mask) : cudaSuccess;
+    const cudaError_t e = smem > 48 * 1024 ? set_smem_once((const void*)k, kTreeNodes * each, done_mask) : cudaSuccess;
     return e != cudaSuccess ? e : launch_k(k, grid, block, smem, s, true, a, psplit);
   };
   static int done[4][64] = {{0}};
