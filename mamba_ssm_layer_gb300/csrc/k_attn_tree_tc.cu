@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
     for (int i = 0; i < S; ++i) mbar_init(&sh->raw_full[i], 1), mbar_init(&sh->raw_empty[i], kTtDeq);
     for (int i = 0; i < NT; ++i) mbar_init(&sh->full[i], kTtDeq), mbar_init(&sh->empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh->s_full[i], 1), mbar_init(&sh->p_full[i], 4);
-    mbar_init(&sh->q_full, kTtSoft);
+    mbar_init(&sh->q_full, T == 2 ? kTtSoft : 4);
     mbar_init(&sh->fin, 1);
     mbar_init(&sh->merge_full, 4), mbar_init(&sh->merge_empty, 4);
     sh->cta_seg[0] = sh->cta_seg[1] = -1;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
       const uint32_t tq = tmem + lanes + C::kTmQ + (T == 2 ? ch * (D / 2) : 0);
       uint64_t tree[2];
       int tree_b = -1, u = 0, done = 0;  // units and runs before this one
-      bool dead = false;
+      bool dead = false, owed = false;  // owed: a hand-over of the second chain that the first may not have taken
       do {
         const int b = run.cur.b, rows = atr_nodes(a.g, b) * a.G, first = a.g.t.cu[b];
         const int xr = run.cur.tile * C::kRows + x, node = min(xr, rows - 1) / a.G, h = min(xr, rows - 1) - node * a.G;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
           }
           float f;
           kv4_query_scale(__uint_as_float(max(top2 << 16, top2 & 0xFFFF0000u)), a.g.scale, f, qs);
-          if (T == 2 || ch == 0) {
+          if (T == 2 || ch == 1) {
             // column 8g + 4h + c holds channels 16g + 4c + 2h and the next.  (Rolled, the row from L1: this code runs
             // once a tile, and fetching its instructions took longer than running it.)
 #pragma unroll 1
@@ -267,9 +267,11 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
             tmem_st_wait();
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->q_full);
+        if (T == 2 || ch == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->q_full);
+        }
         float m = -INFINITY, l = 0.0f;
         uint32_t odd = 0;  // groups of channels that are NaN
         const int k0 = T == 2 ? 0 : (u ^ ch) & 1;  // T = 1: the chain's first page of the run
@@ -347,6 +349,14 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
           }
           last = un;
           tc_fence_before();
+          // (the first chain has read the second's outputs of the run before, which products write over now)
+          if (owed) {
+            if (!tt_wait(&sh->merge_empty, (done - 1) & 1)) {
+              dead = true;
+              break;
+            }
+            owed = false;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->p_full[ch]);
         }
@@ -355,7 +365,9 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
         u += run.pages;
         const int seg = run.cur.seg(a);
         const bool before = run.cur.page > 0, part = before || run.cur.page + run.pages < run.cur.pages;
-        if (last >= 0 && !tt_wait(&sh->empty[last % NT], (last / NT) & 1)) {
+        // the last products; of the second chain: the run's last, behind which nothing reads the queries
+        const int wait_for = T == 1 && ch == 1 ? u - 1 : last;
+        if (wait_for >= 0 && !tt_wait(&sh->empty[wait_for % NT], (wait_for / NT) & 1)) {
           dead = true;
           break;
         }
@@ -363,15 +375,17 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
         float f0 = 1.0f, f1 = 0.0f;  // the chains' weights
         if (T == 1) {
           if (ch == 1) {
+            // The chain goes on to the next run's queries while the first one joins and stores this run.
+            if (owed && !tt_wait(&sh->merge_empty, (done - 1) & 1)) {
+              dead = true;
+              break;
+            }
             sh->m1[x] = m, sh->l1[x] = l, sh->odd1[x] = odd;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->merge_full);
-            // (not ahead into the next run, whose arrivals would count for this one's)
-            if (!tt_wait(&sh->merge_empty, done++ & 1)) {
-              dead = true;
-              break;
-            }
+            ++done;
+            owed = true;
             continue;
           }
           if (!tt_wait(&sh->merge_full, done++ & 1)) {
@@ -387,8 +401,6 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
             m = top;
             odd |= sh->odd1[x];
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->merge_empty);
         }
         const bool first_chain = T == 2 || last >= 0, second_chain = T == 1 && (run.pages > 1 || last < 0);
         if (mask == 0) l = 0.0f, m = -INFINITY;
@@ -438,6 +450,11 @@ __global__ void __launch_bounds__(kTtThreads, 1) attn_tree_tc_kernel(const __gri
             }
             __syncwarp();  // the next load is the whole warp's
           }
+        }
+        if (T == 1) {  // the second chain's maxima, sums and outputs are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->merge_empty);
         }
         if (part && tid == 0) sh->cta_seg[before ? 0 : 1] = seg;
       } while (run.next(a, C::kRows));
