@@ -3,18 +3,19 @@
 // The walk itself is a few comparisons; what takes time is a row of the target (and of
 // the draft): one for the token that the walk ends on, one for every sibling that is
 // asked after a refusal.  A cluster of 8 CTAs takes a sequence, its CTAs and their warps
-// consecutive runs of the vocabulary.  The probabilities that the walk asks for are
-// gathered at the start; the first CTA walks until it needs a sum
+// consecutive runs of the vocabulary.  Every CTA gathers the probabilities that the walk
+// asks for and walks by itself, the same way, until it needs a sum
 //   S = sum_t R(t),  R = max(p - c q, 0)
-// and tells the others the row and c.  The last sum's parts, by CTA and warp, say which
-// warp's run the random number falls into; that warp reads it again, from L2.
+// whose parts all CTAs give each other: one hand-over a pass.  The last sum's parts, by
+// CTA and warp, say which warp's run the random number falls into; that CTA reads it
+// again, from L2.
 // A refusal takes S q from what remains, so that c grows by S: R never has to be
 // stored, whatever the number of refusals.
 // R and its sums are pairs of floats (about 2^-46 of the sum; fp64 adds are slow here),
 // comparisons fp64: a sum in fp32 would move one drawn token in some thousand.
 // Bound: HBM, the rows once, and the passes' hand-overs through the cluster: 64 sequences of
-// 5 to 8 nodes over 131072 words 31 us (67 MB, 2.1 TB/s; a pass over a row 4 to 6 us), a
-// chain of 5 over 32000 words 7 us.
+// 5 to 8 nodes over 131072 words 29 us (67 MB, 2.3 TB/s; a pass over a row 4 to 6 us), a
+// chain of 5 over 32000 words 6.5 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -40,7 +41,7 @@ struct VfShared {
   float hi[kVfWarps], lo[kVfWarps];
   int32_t parent[kTreeNodes], token[kTreeNodes], path[kTreeNodes];
   float u[kTreeNodes], p[kTreeNodes], q[kTreeNodes];
-  int32_t count;     // accepted nodes so far (first CTA)
+  int32_t count;     // accepted nodes so far
   int32_t run;       // drawing: the run that the random number falls into (-1: another CTA's, -2: the row is empty)
   double want;       // and what is left of the number there
   float scan_hi[kVfWarps], scan_lo[kVfWarps];
@@ -114,6 +115,8 @@ __device__ __forceinline__ void vf_add2(float2& hi, float2& lo, float2 p, float2
 __device__ __forceinline__ void vf_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void vf_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void vf_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // A word of this CTA's shared memory at the same place in CTA `rank` of the cluster.
 __device__ __forceinline__ void vf_put(void* at, int rank, uint32_t v) {
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(
@@ -131,7 +134,7 @@ __device__ __forceinline__ bool vf_less(float u, float q, double S, float p, dou
   return (double)u * q * S < (left > 0.0 ? left : 0.0);
 }
 
-// The walk up to the next sum.  One thread of the cluster holds this.
+// The walk up to the next sum.  One thread of every CTA holds this.
 struct VfWalk {
   int cur, r, count, gone;
   bool known, last;  // S is; the draw was from the untouched row already
@@ -146,10 +149,11 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
   constexpr int ES = BF ? 2 : 4;
   pdl_wait();
   pdl_trigger();
+  vf_cluster_arrive();  // waited for before the first word goes to another CTA, which has to run by then
   auto row_of = [&](const void* m, int64_t ld, int node) {
     return static_cast<const void*>(static_cast<const char*>(m) + (int64_t)(first + node) * ld * ES);
   };
-  if (rank == 0 && tid < n) {
+  if (tid < n) {
     const int par = a.t.parent[first + tid], x = a.token[first + tid];
     const bool in = tid > 0 && par >= 0 && par < tid, tok = x >= 0 && x < V;
     sh.parent[tid] = tid == 0 ? par : in ? par : -1;
@@ -164,74 +168,57 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
       if (tid < n) a.path[first + tid] = -1;
       if (tid == 0) a.count[i] = 0, a.next[i] = -1;
     }
+    vf_cluster_wait();
     return;
   }
-  vf_cluster_sync();  // every CTA runs: its shared memory may be written
   VfWalk w;
   w.cur = 0, w.r = 1, w.count = 1, w.gone = 0, w.known = true, w.last = false, w.c = 0.0, w.S = 1.0;
-  if (rank == 0 && tid == 0) sh.path[0] = 0;
+  if (tid == 0) sh.path[0] = 0;
   // runs of the vocabulary, whole rounds of a warp
   const int per = (V + kVfCtas * kVfWarps * 128 - 1) / (kVfCtas * kVfWarps * 128) * 128;
   const int64_t from64 = (int64_t)(rank * kVfWarps + warp) * per;
   const int from = (int)min(from64, (int64_t)V), to = (int)min(from64 + per, (int64_t)V);
   for (int pass = 0;; ++pass) {
-    if (rank == 0 && warp == 0) {
+    if (tid == 0) {
       VfCmd cmd;
-      if (lane == 0) {
-        bool ask = false;  // a sum is needed before the next comparison
-        for (; w.r < n && !ask; ) {
-          const int r = w.r;
-          if (sh.parent[r] != w.cur || sh.token[r] < 0) {
-            ++w.r;
-            continue;
-          }
-          if (!w.known) {
-            ask = true;
-            break;
-          }
-          bool ok;
-          if (a.q) {
-            ok = vf_less(sh.u[r], sh.q[r], w.S, sh.p[r], w.c);
-          } else {
-            bool was = false;
-            for (int k = 0; k < w.gone; ++k) was |= sh.gone_tok[k] == sh.token[r];
-            ok = !was && vf_less(sh.u[r], 1.0f, w.S, sh.p[r], 0.0);
-          }
+      bool ask = false;  // a sum is needed before the next comparison
+      for (; w.r < n && !ask; ) {
+        const int r = w.r;
+        if (sh.parent[r] != w.cur || sh.token[r] < 0) {
           ++w.r;
-          if (ok) {
-            sh.path[w.count++] = r;
-            w.cur = r, w.c = 0.0, w.S = 1.0, w.known = true, w.gone = 0;
-          } else {
-            w.c += w.S;
-            w.known = false;
-            if (!a.q) sh.gone_tok[w.gone++] = sh.token[r];
-          }
+          continue;
         }
-        cmd.what = ask ? VF_SUM : VF_DRAW;
-        cmd.cur = w.cur;
-        cmd.c_hi = a.q ? (float)w.c : 0.0f;
-        cmd.c_lo = a.q ? (float)(w.c - (double)cmd.c_hi) : 0.0f;
-        cmd.gone = w.gone;
-        sh.count = w.count;
+        if (!w.known) {
+          ask = true;
+          break;
+        }
+        bool ok;
+        if (a.q) {
+          ok = vf_less(sh.u[r], sh.q[r], w.S, sh.p[r], w.c);
+        } else {
+          bool was = false;
+          for (int k = 0; k < w.gone; ++k) was |= sh.gone_tok[k] == sh.token[r];
+          ok = !was && vf_less(sh.u[r], 1.0f, w.S, sh.p[r], 0.0);
+        }
+        ++w.r;
+        if (ok) {
+          sh.path[w.count++] = r;
+          w.cur = r, w.c = 0.0, w.S = 1.0, w.known = true, w.gone = 0;
+        } else {
+          w.c += w.S;
+          w.known = false;
+          if (!a.q) sh.gone_tok[w.gone++] = sh.token[r];
+        }
       }
-      // to all CTAs, lane d to CTA d
-      __syncwarp();
-      cmd.what = __shfl_sync(0xffffffffu, cmd.what, 0);
-      cmd.cur = __shfl_sync(0xffffffffu, cmd.cur, 0);
-      cmd.c_hi = __shfl_sync(0xffffffffu, cmd.c_hi, 0);
-      cmd.c_lo = __shfl_sync(0xffffffffu, cmd.c_lo, 0);
-      cmd.gone = __shfl_sync(0xffffffffu, cmd.gone, 0);
-      if (lane < kVfCtas) {
-        vf_put(&sh.cmd.what, lane, (uint32_t)cmd.what);
-        vf_put(&sh.cmd.cur, lane, (uint32_t)cmd.cur);
-        vf_put(&sh.cmd.c_hi, lane, __float_as_uint(cmd.c_hi));
-        vf_put(&sh.cmd.c_lo, lane, __float_as_uint(cmd.c_lo));
-        vf_put(&sh.cmd.gone, lane, (uint32_t)cmd.gone);
-        if (lane > 0)
-          for (int k = 0; k < cmd.gone; ++k) vf_put(&sh.gone_tok[k], lane, (uint32_t)sh.gone_tok[k]);
-      }
+      cmd.what = ask ? VF_SUM : VF_DRAW;
+      cmd.cur = w.cur;
+      cmd.c_hi = a.q ? (float)w.c : 0.0f;
+      cmd.c_lo = a.q ? (float)(w.c - (double)cmd.c_hi) : 0.0f;
+      cmd.gone = w.gone;
+      sh.count = w.count;
+      sh.cmd = cmd;
     }
-    vf_cluster_sync();
+    __syncthreads();
     const VfCmd cmd = sh.cmd;
     const void* p = row_of(a.p, a.ld_p, cmd.cur);
     const bool minus = a.q && cmd.c_hi > 0.0f;  // nothing refused: the draft's row is not read
@@ -301,6 +288,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
       }
       sh.hi[warp] = hi, sh.lo[warp] = lo;
     }
+    if (pass == 0) vf_cluster_wait();
     __syncthreads();
     if (warp == 0) {
       hi = lane < kVfWarps ? sh.hi[lane] : 0.0f, lo = lane < kVfWarps ? sh.lo[lane] : 0.0f;
@@ -312,9 +300,12 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
     }
     vf_cluster_sync();
     if (cmd.what == VF_SUM) {
-      if (rank == 0 && tid == 0) {
-        w.S = 0.0;
-        for (int k = 0; k < kVfCtas; ++k) w.S += (double)sh.tot_hi[pass & 1][k] + (double)sh.tot_lo[pass & 1][k];
+      if (warp == 0) {  // (64-bit additions are slow: three of them, one after the other)
+        const int k = lane % kVfCtas;
+        double S = (double)sh.tot_hi[pass & 1][k] + (double)sh.tot_lo[pass & 1][k];
+#pragma unroll
+        for (int o = 1; o < kVfCtas; o <<= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+        w.S = S;
         w.known = true;
       }
       continue;
@@ -362,7 +353,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
     const int run = sh.run;
     if (run == -2 && (cmd.c_hi > 0.0f || cmd.gone > 0)) {
       // nothing is left of the row: from the row itself
-      if (rank == 0 && tid == 0) w.c = 0.0, w.gone = 0, w.r = n;
+      if (tid == 0) w.c = 0.0, w.gone = 0, w.r = n;
       __syncthreads();  // sh.run has been read
       continue;
     }
