@@ -154,9 +154,9 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
 
 template <int VEC>
 static cudaError_t launch_tree_conv_v(const TreeConvArgs& a, cudaStream_t s) {
-  // One node a CTA while all of them run at once; then so many that they do.  For 2, 4, 8,
-  // 16 CTAs an SM: 16 x 4 nodes 5.4, 4.9, 4.1, 4.1 us, 16 x 16 10.0, 7.1, 8.6, 10.3, 64 x 5
-  // 8.9, 8.9, 11.7, 12.5.
+  // One node a CTA while all of them run at once; then so many that they do.  For 2, 4, 5, 8,
+  // 16 CTAs an SM: 16 x 4 nodes 5.4, 4.9, 4.1, 4.1, 4.1 us, 16 x 16 10.0, 7.1, 7.1, 8.6, 10.3,
+  // 64 x 5 8.9, 8.9, 8.9, 11.7, 12.5.
   const int blocks = (a.C + kTcThreads * VEC - 1) / (kTcThreads * VEC), nodes = a.t.cu[a.t.nseq];
   int piece = 1;
   while (piece < kTcMost && (int64_t)blocks * nodes / piece > (int64_t)kTcCtas * num_sms()) piece *= 2;
@@ -185,9 +185,8 @@ cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
 // state (which is only read),
 //   y_i = e^{s_i} C_i h^T + sum_{j on i's path} e^{s_i - s_j} dt_j (C_i . B_j) x_j + D x_i,
 // three products on warp MMA (m16n8k16, bf16, fp32 sums): nodes are the rows,
-//   C h^T    k = states, columns = channels p; a warp takes 8 channels, whose state
-//            rows it loads straight into the operand's layout (a lane's four
-//            consecutive states stand at k = 2c, 2c+1, 2c+8, 2c+9; C is read in the
+//   C h^T    k = states, columns = channels p; a warp takes 8 channels (a lane's four
+//            consecutive states stand at k = 2c, 2c+1, 2c+8, 2c+9; C is kept in the
 //            same order)
 //   C B^T    once for the heads of a group
 //   L x      L the masked, decayed C B^T times dt
@@ -268,7 +267,8 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
   const float2 minus = make_float2(-1.0f, -1.0f);
   float2 v = make_float2(a, b);
   auto rest = [&] {
-    const float2 u = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u), __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
+    const float2 u = make_float2(__uint_as_float(__float_as_uint(v.x) & 0xFFFF0000u),
+                                 __uint_as_float(__float_as_uint(v.y) & 0xFFFF0000u));
     v = tc_fma2(u, minus, v);
   };
   hi = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
   extern __shared__ __align__(128) uint8_t smem[];
   const int xs = ts_x_stride(a.P);
   uint64_t* mask = reinterpret_cast<uint64_t*>(smem + 8 * kTsSlots * Cf::kSlot * 4);
-  unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);  // nodes with x that is not finite, three heads in turn
+  // nodes with x that is not finite, three heads in turn
+  unsigned long long* bad = reinterpret_cast<unsigned long long*>(mask + NODES);
   uint4* cfrag = reinterpret_cast<uint4*>(bad + 4);  // C as a lane's operands of a tile and 16 states
   uint16_t* lt = reinterpret_cast<uint16_t*>(cfrag + MT * KS * 32);  // L's terms, heads in turn
   uint16_t *ct = lt, *bt = lt + NODES * Cf::kRow;
@@ -676,13 +677,18 @@ static cudaError_t launch_tree_ssm_n(const TreeSsmArgs& a, cudaStream_t s) {
   }
   const int chunks = (per + heads - 1) / heads, smem = ts_smem_bytes<N, MT>(a.P, heads);
   auto k = tree_ssm_kernel<N, MT>;
-  cudaError_t e = set_smem_once((const void*)k, kTsSmemMax, done_mask);  // (one limit whatever the call: no call lowers another's)
+  // (one limit whatever the call: no call lowers another's)
+  cudaError_t e = set_smem_once((const void*)k, kTsSmemMax, done_mask);
   if (e != cudaSuccess) return e;
   return launch_k(k, dim3(a.G * chunks, a.t.nseq), dim3(TsCfg<N, MT>::kWarps * 32), smem, s, true, a, heads, chunks);
 }
 template <int N>
 static cudaError_t launch_tree_ssm_m(const TreeSsmArgs& a, int most, cudaStream_t s) {
-  return most <= 16 ? launch_tree_ssm_n<N, 1>(a, s) : most <= 32 ? launch_tree_ssm_n<N, 2>(a, s) : launch_tree_ssm_n<N, 4>(a, s);
+  // Rows for 16, 32 or 64 nodes.  us with 16 / 32 / 64, 128 heads as above: 16 sequences x 16
+  // nodes 19.2 / 27.5 / 60, 64 x 5 56.8 / 85.5 / 215, one x 5 3.5 / 4.5 / 7.4; 16 x 32 - / 29.4 / 61.4.
+  return most <= 16   ? launch_tree_ssm_n<N, 1>(a, s)
+         : most <= 32 ? launch_tree_ssm_n<N, 2>(a, s)
+                      : launch_tree_ssm_n<N, 4>(a, s);
 }
 
 cudaError_t launch_tree_ssm(const TreeSsmArgs& a, cudaStream_t s) {
@@ -702,11 +708,13 @@ cudaError_t launch_tree_ssm(const TreeSsmArgs& a, cudaStream_t s) {
 
 // ------------------------------------------------------------------ commit
 //
-// Two launches.  The ring's kernel comes first: the conv of a decode step reads ring
-// and position while the launch before it may still run, and that launch is then the
-// state's kernel, which starts its successor only after the ring's has ended.
-// A sequence's ring is moved by a cluster, so that the position is stored (perhaps in
-// place) after every CTA has read it.
+// One launch: the state's blocks, and a block a sequence for ring and position, which it
+// stores (perhaps in place) once all of it has read the old one.  It never starts its
+// successor early: the conv of a decode step reads ring and position while the launch
+// before it may still run.  (With the ring in a launch of its own: one sequence 5.9 us
+// instead of 5.5, two 7.0 instead of 5.9, no difference from four on.)
+// Channels that cannot be moved 16 bytes at a time take two launches: first the ring's, a
+// cluster a sequence, then the state's, which may start its successor early.
 
 // Accepted nodes of sequence i, within its tree.
 __device__ __forceinline__ int tree_count(const TreeArgs& t, const int32_t* count, int i) {
@@ -724,26 +732,30 @@ __device__ __forceinline__ int tree_path_row(const TreeArgs& t, int i, int j) {
 
 constexpr int kTrThreads = 256, kTrCtas = 8;
 
+// The ring of sequence i, channels from VEC * at on, VEC * step apart; the path's n nodes, position pos.
 template <int VEC>
-__global__ void __launch_bounds__(kTrThreads) __cluster_dims__(kTrCtas, 1, 1) tree_ring_kernel(const TreeCommitArgs a) {
+__device__ __forceinline__ void tree_ring(const TreeCommitArgs& a, int i, int n, int pos, int at, int step) {
   using T = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
-  pdl_wait();
-  pdl_trigger();
-  const int i = blockIdx.y, L = a.dconv - 1, C = a.H * a.P + 2 * a.G * a.N;
-  const int n = tree_count(a.t, a.count, i), pos = a.pos[i];
+  const int L = a.dconv - 1, C = a.H * a.P + 2 * a.G * a.N;
   const uint16_t* in = a.ring + (size_t)i * L * C;
   uint16_t* out = a.ring_out + (size_t)i * L * C;
-  for (int c = (blockIdx.x * kTrThreads + threadIdx.x) * VEC; c < C; c += kTrCtas * kTrThreads * VEC) {
-    for (int slot = 0; slot < L; ++slot) {
-      // the newest token of the path in this slot: the last j < n with (pos + j) % L == slot
-      const int p = ((pos + n - 1 - slot) % L + L) % L, j = n - 1 - p;
-      const int row = j >= 0 ? tree_path_row(a.t, i, j) : -1;
-      if (row >= 0)
-        *reinterpret_cast<T*>(out + (size_t)slot * C + c) = *reinterpret_cast<const T*>(a.xbc + (size_t)row * a.ld_xbc + c);
-      else if (in != out)
-        *reinterpret_cast<T*>(out + (size_t)slot * C + c) = *reinterpret_cast<const T*>(in + (size_t)slot * C + c);
-    }
+  for (int slot = 0; slot < L; ++slot) {
+    // the newest token of the path in this slot: the last j < n with (pos + j) % L == slot
+    const int p = ((pos + n - 1 - slot) % L + L) % L, j = n - 1 - p;
+    const int row = j >= 0 ? tree_path_row(a.t, i, j) : -1;
+    if (row < 0 && in == out) continue;
+    const uint16_t* from = row >= 0 ? a.xbc + (size_t)row * a.ld_xbc : in + (size_t)slot * C;
+#pragma unroll 4
+    for (int c = at * VEC; c < C; c += step * VEC)
+      *reinterpret_cast<T*>(out + (size_t)slot * C + c) = *reinterpret_cast<const T*>(from + c);
   }
+}
+
+__global__ void __launch_bounds__(kTrThreads) __cluster_dims__(kTrCtas, 1, 1) tree_ring_kernel(const TreeCommitArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.y, n = tree_count(a.t, a.count, i), pos = a.pos[i];
+  tree_ring<1>(a, i, n, pos, blockIdx.x * kTrThreads + threadIdx.x, kTrCtas * kTrThreads);
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (blockIdx.x == 0 && threadIdx.x == 0) a.pos_out[i] = pos + n;
 }
@@ -764,12 +776,20 @@ __global__ void __launch_bounds__(256) tree_state_kernel(const TreeCommitArgs a,
   extern __shared__ __align__(16) uint8_t smem[];  // [nodes] of B (N bf16), of x (CTA_ROWS fp32)
   __shared__ float sdt[kTreeNodes], sda[kTreeNodes];
   __shared__ int srow[kTreeNodes];
-  const int i = blockIdx.y, h = blockIdx.x / psplit, pc = blockIdx.x % psplit, tid = threadIdx.x;
+  const int i = blockIdx.y, block = (int)blockIdx.x - (a.wide ? 1 : 0), tid = threadIdx.x;
+  const int h = block / psplit, pc = block % psplit;
   const int warp = tid >> 5, lane = tid & 31, n4 = (lane % LPR) * 4, g = h / (a.H / a.G);
   const size_t base = ((size_t)i * a.H + h) * a.P * a.N;
   const int r0 = warp * RPW + lane / LPR, p0 = pc * CTA_ROWS + r0;
   pdl_wait();
-  pdl_trigger();
+  if (!a.wide) pdl_trigger();
+  if (block < 0) {  // the ring's
+    const int n = tree_count(a.t, a.count, i), pos = a.pos[i];
+    tree_ring<8>(a, i, n, pos, tid, 256);
+    __syncthreads();
+    if (tid == 0) a.pos_out[i] = pos + n;
+    return;
+  }
   float4 hv[ROWS];
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
@@ -824,11 +844,13 @@ static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
   constexpr int RPW = 32 / LPR;
   const int64_t heads = (int64_t)a.t.nseq * a.H;
   const int max_rows = (a.P + 8 * RPW - 1) / (8 * RPW);
-  // rows a thread: doubled while the grid has more CTAs than four an SM
+  // rows a thread: doubled while the grid has more CTAs than four an SM.  us for 1, 2, 4, 8 rows,
+  // 128 heads of 64 x 128: one sequence 6.6, 6.1, 5.9, 6.2, 16 sequences 49.7, 39.1, 33.5, 32.3, 64
+  // 174, 132, 106, 98
   int rows = 1;
   while (rows < 8 && rows < max_rows && heads * ((a.P + 8 * RPW * rows - 1) / (8 * RPW * rows)) > 4ll * num_sms()) rows *= 2;
   const int psplit = (a.P + 8 * RPW * rows - 1) / (8 * RPW * rows);
-  const dim3 grid(a.H * psplit, a.t.nseq), block(256);
+  const dim3 grid(a.H * psplit + (a.wide ? 1 : 0), a.t.nseq), block(256);
   int most = 0;
   for (int i = 0; i < a.t.nseq; ++i) most = a.t.cu[i + 1] - a.t.cu[i] > most ? a.t.cu[i + 1] - a.t.cu[i] : most;
   const int each = a.N * 2 + 8 * RPW * rows * 4, smem = most * each;  // at most 64 * (32 + 2048) bytes: N = 16
@@ -846,12 +868,13 @@ static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
-  const dim3 grid(kTrCtas, a.t.nseq), block(kTrThreads);
-  trace_pre(K_TREE_RING, s);
-  cudaError_t e = a.wide ? launch_k(tree_ring_kernel<8>, grid, block, 0, s, true, a)
-                         : launch_k(tree_ring_kernel<1>, grid, block, 0, s, true, a);
-  trace_post(K_TREE_RING, s);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (!a.wide) {
+    trace_pre(K_TREE_RING, s);
+    e = launch_k(tree_ring_kernel, dim3(kTrCtas, a.t.nseq), dim3(kTrThreads), 0, s, true, a);
+    trace_post(K_TREE_RING, s);
+    if (e != cudaSuccess) return e;
+  }
   trace_pre(K_TREE_STATE, s);
   switch (a.N / 4) {
     case 4: e = launch_tree_state<4>(a, s); break;
