@@ -20,7 +20,7 @@ namespace m2 {
 // a lane of the first warp looks up a node's rows for the CTA.
 // Sums run as the single-token conv's, oldest tap first; products of two bf16 values are
 // exact, so the results are the same bits.
-// Bound: latency (masks, rows: 3.0 us for a chain of 5, 10240 channels), then issue slots:
+// Bound: latency (masks, rows: 2.6 us for a chain of 5, 10240 channels), then issue slots:
 // 16 trees of 16 nodes 7.1 us, of 64 nodes 20 us (42 MB).
 constexpr int kTcThreads = 128, kTcMost = 16, kTcCtas = 5;
 
@@ -37,11 +37,12 @@ __device__ __forceinline__ float2 tc_pair(uint32_t w) { return make_float2(bf16l
 __device__ __forceinline__ uint32_t tc_word(const uint4& v, int e) {
   return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
 }
+__device__ __forceinline__ uint32_t tc_word(const uint2& v, int e) { return e == 0 ? v.x : v.y; }
 
 template <int K, int VEC>
 __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_constant__ TreeConvArgs a, int piece) {
-  constexpr int L = K - 1, PAIRS = VEC == 8 ? 4 : 1;
-  using T = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
+  constexpr int L = K - 1, PAIRS = VEC > 1 ? VEC / 2 : 1;
+  using T = typename std::conditional<VEC == 8, uint4, typename std::conditional<VEC == 4, uint2, uint16_t>::type>::type;
   __shared__ const uint16_t* tap[kTcMost][K];  // channel 0 of a node's taps, oldest first; null: not part of the tree
   pdl_wait();
   pdl_trigger();
@@ -89,21 +90,20 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
   for (int e = 0; e < PAIRS; ++e) {
     b[e] = make_float2(0.0f, 0.0f);
     if (!in) continue;
-    auto weight = [&](int at) { return bf16_to_f32(a.w[(size_t)c * K + at]); };
-    if constexpr (VEC == 8) {
-      uint4 pack[K];
+    if constexpr (VEC > 1) {
+      T pack[K];
 #pragma unroll
-      for (int j = 0; j < K; ++j) pack[j] = reinterpret_cast<const uint4*>(a.w + (size_t)c * K)[j];
+      for (int j = 0; j < K; ++j) pack[j] = reinterpret_cast<const T*>(a.w + (size_t)c * K)[j];
       auto part = [&](int at) {
-        const uint32_t u = tc_word(pack[at / 8], at % 8 / 2);
+        const uint32_t u = tc_word(pack[at / VEC], at % VEC / 2);
         return at & 1 ? bf16hi(u) : bf16lo(u);
       };
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j][e] = make_float2(part(2 * e * K + j), part((2 * e + 1) * K + j));
-      if (a.bias) b[e] = tc_pair(tc_word(*reinterpret_cast<const uint4*>(a.bias + c), e));
+      if (a.bias) b[e] = tc_pair(tc_word(*reinterpret_cast<const T*>(a.bias + c), e));
     } else {
 #pragma unroll
-      for (int j = 0; j < K; ++j) w[j][e] = make_float2(weight(j), 0.0f);
+      for (int j = 0; j < K; ++j) w[j][e] = make_float2(bf16_to_f32(a.w[(size_t)c * K + j]), 0.0f);
       if (a.bias) b[e] = make_float2(bf16_to_f32(a.bias[c]), 0.0f);
     }
   }
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         float2 v;
-        if constexpr (VEC == 8)
+        if constexpr (VEC > 1)
           v = tc_pair(tc_word(next[j], e));
         else
           v = make_float2(bf16_to_f32(next[j]), 0.0f);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
 #pragma unroll
       for (int e = 0; e < PAIRS; ++e) {
         s[e].x = silu_f(s[e].x);
-        if (VEC == 8) s[e].y = silu_f(s[e].y);
+        if (VEC > 1) s[e].y = silu_f(s[e].y);
       }
     }
     const bool there = tap[r][0] != nullptr;
@@ -147,6 +147,9 @@ __global__ void __launch_bounds__(kTcThreads) tree_conv_kernel(const __grid_cons
       *reinterpret_cast<uint4*>(out) = there ? make_uint4(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y),
                                                           pack_bf16x2(s[2].x, s[2].y), pack_bf16x2(s[3].x, s[3].y))
                                              : make_uint4(0u, 0u, 0u, 0u);
+    else if constexpr (VEC == 4)
+      *reinterpret_cast<uint2*>(out) =
+          there ? make_uint2(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y)) : make_uint2(0u, 0u);
     else
       *out = there ? f32_to_bf16(s[0].x) : (uint16_t)0;
   }
@@ -174,7 +177,14 @@ static cudaError_t launch_tree_conv_v(const TreeConvArgs& a, cudaStream_t s) {
 
 cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
   trace_pre(K_TREE_CONV, s);
-  const cudaError_t e = a.wide ? launch_tree_conv_v<8>(a, s) : launch_tree_conv_v<1>(a, s);
+  // Eight channels a thread, or four where eight leave SMs without a block: one chain of 5 nodes
+  // and 10240 channels 3.0 / 2.5 us, 16 x 4 nodes 4.1 / 4.4, 16 x 64 20.3 / 22.0.
+  const int blocks = (a.C + kTcThreads * 8 - 1) / (kTcThreads * 8);
+  cudaError_t e;
+  if (!a.wide)
+    e = launch_tree_conv_v<1>(a, s);
+  else
+    e = blocks * a.t.cu[a.t.nseq] < num_sms() ? launch_tree_conv_v<4>(a, s) : launch_tree_conv_v<8>(a, s);
   trace_post(K_TREE_CONV, s);
   return e;
 }
