@@ -783,7 +783,7 @@ __device__ __forceinline__ float4 tc_bf4(const uint16_t* p) {
 template <int LPR, int ROWS>
 __global__ void __launch_bounds__(256) tree_state_kernel(const TreeCommitArgs a, int psplit) {
   constexpr int RPW = 32 / LPR, CTA_ROWS = 8 * RPW * ROWS;
-  extern __shared__ __align__(16) uint8_t smem[];  // [nodes] of B (N bf16), of x (CTA_ROWS fp32)
+  extern __shared__ __align__(128) uint8_t smem[];  // [nodes] of B (N bf16), of x (CTA_ROWS fp32)
   __shared__ float sdt[kTreeNodes], sda[kTreeNodes];
   __shared__ int srow[kTreeNodes];
   const int i = blockIdx.y, block = (int)blockIdx.x - (a.wide ? 1 : 0), tid = threadIdx.x;
