@@ -1,6 +1,6 @@
 // k_attn_tree.cu -- attention of a tree of drafted tokens over the paged 4-bit cache
 // (include/mamba2.h has the rule of what a node sees), for few rows: nodes x query heads
-// of a kv head at most 16.  k_attn_tree_tc.cu serves more.
+// of a kv head at most 16 (8 have a form of their own).  k_attn_tree_tc.cu serves more.
 //
 // A unit is half a page (32 tokens) of one kv head; row m is node m / G with query head
 // m % G of the group.  The units of all sequences, in the order (sequence, kv head, page),
@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "m2_attn_tree.cuh"
 #include "m2_common.cuh"
 #include "m2_kernels.h"
@@ -34,30 +36,53 @@ namespace m2 {
 constexpr int kAtWarps = 12, kAtrThreads = kAtWarps * 32;
 
 constexpr int kAtrSetup = 2;  // units (even: a page's units stay together); 0, 2, 4: 64.3, 61.7, 61.4 us for 64 sequences
-constexpr int kAtrRows = 16, kAtrParts = 2 * kAtWarps;  // a warp leaves a first and a last part at most
+constexpr int kAtrParts = 2 * kAtWarps;  // a warp leaves a first and a last part at most
 
-template <int D>
+// ROWS: 8 or 16 a warp.
+template <int D, int ROWS>
 struct AtrCfg {
   static constexpr int kBytes = Kv4Block<D>::kBytes;
   static constexpr int kStages = D == 128 ? 2 : 4;  // 12 warps * stages * bytes = 216 KB
   static constexpr int kRing = kStages * kBytes;    // of one warp
   static constexpr int kStride = D + 8;             // floats between the rows of a record: no bank conflicts
-  static constexpr int kRecord = 2 * kAtrRows + kAtrRows * kStride;  // maxima, sums, outputs
+  static constexpr int kRecord = 2 * ROWS + ROWS * kStride;  // maxima, sums, outputs
 };
 // Which row tile a partial belongs to, and whether it starts before / ends after the CTA's span.
 struct AtrMeta {
   int32_t seg, before, after;
 };
+template <int ROWS>
 struct AtrShared {
-  uint16_t* out[kAtrParts][kAtrRows];  // where a joined row goes: the output, or the CTA's record; null: nowhere
+  uint16_t* out[kAtrParts][ROWS];  // where a joined row goes: the output, or the CTA's record; null: nowhere
   AtrMeta meta[kAtrParts];
-  float part_m[kAtrParts][kAtrRows], part_l[kAtrParts][kAtrRows];  // maxima (then weights) and sums
-  float row_l[kAtrParts][kAtrRows];                                // sums of the cut tiles; -1: into a record
+  float part_m[kAtrParts][ROWS], part_l[kAtrParts][ROWS];  // maxima (then weights) and sums
+  float row_l[kAtrParts][ROWS];                                // sums of the cut tiles; -1: into a record
   uint32_t row_parts[kAtrParts];
   int32_t cta_seg[2];
   int32_t scan[kAtWarps];
   int32_t run0[kAtWarps + 1], run_b[kAtWarps], run_base[kAtWarps];
 };
+
+// Tokens of a page's units h0 to h1 - 1 (of the first `left`) that hold values that are not finite, some group of them.
+template <int D>
+__device__ __forceinline__ uint64_t atr_bad(const uint8_t* u, int left, int h0, int h1, int lane) {
+  constexpr int GW = D / 32;
+  uint64_t bad = 0;
+  uint32_t vs[GW];  // of token pair `lane`: bytes (even, even, odd, odd)
+  lds_words<GW>(u + Kv4Block<D>::kVs + lane * (D / 8), vs);
+  uint32_t even = 0, odd = 0;
+#pragma unroll
+  for (int w = 0; w < GW; ++w) {
+    const uint32_t x = vs[w] & 0xF8F8F8F8u;  // exponents
+    even |= (x & 0xFFu) == 0xF8u || (x & 0xFF00u) == 0xF800u;
+    odd |= (x & 0xFF0000u) == 0xF80000u || (x & 0xFF000000u) == 0xF8000000u;
+  }
+  const uint32_t be = __ballot_sync(0xffffffffu, even && 2 * lane < left);
+  const uint32_t bo = __ballot_sync(0xffffffffu, odd && 2 * lane + 1 < left);
+  if (be | bo)
+    for (int t = 16 * h0; t < 16 * h1; ++t) bad |= (uint64_t)((be >> t & 1) | (bo >> t & 1) << 1) << (2 * t);
+  return bad;
+}
 
 // The running softmax of 16 rows in a warp: lane (r, c) = (lane / 4, lane % 4) owns rows r and r + 8.
 template <int D>
@@ -118,21 +143,7 @@ struct AtrRows {
     constexpr int GW = D / 32;  // words of a lane's codes: 2 groups each
     const int r = lane >> 2, c = lane & 3;
     const bool part = base > -kPage;
-    uint64_t bad = 0;  // tokens with values that are not finite, some group of them
-    if (part) {
-      uint32_t vs[GW];  // of token pair `lane`: bytes (even, even, odd, odd)
-      lds_words<GW>(u + L::kVs + lane * (D / 8), vs);
-      uint32_t even = 0, odd = 0;
-#pragma unroll
-      for (int w = 0; w < GW; ++w) {
-        const uint32_t x = vs[w] & 0xF8F8F8F8u;  // exponents
-        even |= (x & 0xFFu) == 0xF8u || (x & 0xFF00u) == 0xF800u;
-        odd |= (x & 0xFF0000u) == 0xF80000u || (x & 0xFF000000u) == 0xF8000000u;
-      }
-      const uint32_t be = __ballot_sync(0xffffffffu, even && 2 * lane < left), bo = __ballot_sync(0xffffffffu, odd && 2 * lane + 1 < left);
-      if (be | bo)
-        for (int t = 16 * h0; t < 16 * h1; ++t) bad |= (uint64_t)((be >> t & 1) | (bo >> t & 1) << 1) << (2 * t);
-    }
+    uint64_t bad = part ? atr_bad<D>(u, left, h0, h1, lane) : 0ull;
 #pragma unroll 1
     for (int half = h0; half < h1; ++half) {
       float s[4][4];
@@ -283,7 +294,7 @@ struct AtrRows {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (c == 0) pm[r + 8 * k] = m[k], pl[r + 8 * k] = l[k];
-      float* d = out + (r + 8 * k) * AtrCfg<D>::kStride + 2 * c;
+      float* d = out + (r + 8 * k) * AtrCfg<D, 16>::kStride + 2 * c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(o[i][2 * k], o[i][2 * k + 1]);
     }
@@ -303,18 +314,226 @@ struct AtrRows {
   }
 };
 
+// The same for 8 rows, the other way round: tokens (then channels) are the products' rows
+// and the queries' rows their 8 columns, so that nothing of a product is empty.  Lane (r, c)
+// owns rows 2c and 2c + 1.
+template <int D>
+struct AtrFewRows {
+  uint32_t q[D / 16][2];  // B operand: row r; channels 16g + 4c .. + 3
+  float qs[2], m[2], l[2];
+  uint64_t seen[2];
+  float o[D / 16][4];     // channels 16i + r and 16i + 8 + r of rows 2c, 2c + 1
+
+  __device__ __forceinline__ void start(const AtrArgs& a, int b, int hk, uint64_t (&tree)[2], bool again, int lane) {
+    const int r = lane >> 2, c = lane & 3, first = a.g.t.cu[b], n = atr_nodes(a.g, b), rows = n * a.G;
+    const int x = min(r, rows - 1), node = x / a.G;
+    const uint2* q0 = reinterpret_cast<const uint2*>(a.g.q + (size_t)(first + node) * a.g.ld_q +
+                                                     (size_t)(hk * a.G + x - node * a.G) * D + 4 * c);
+    uint2 w[D / 16];
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g) w[g] = r < rows ? q0[4 * g] : make_uint2(0u, 0u);
+    if (again) tree_masks(a.g.t.parent + first, n, lane, tree);
+    float top = 0.0f;
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g)
+      top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16lo(w[g].x)), fabsf(bf16hi(w[g].x))),
+                             fmaxf(fabsf(bf16lo(w[g].y)), fabsf(bf16hi(w[g].y)))));
+    float f, scale;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    kv4_query_scale(top, a.g.scale, f, scale);
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g) {
+      q[g][0] = pack_f16x2(bf16lo(w[g].x) * f, bf16hi(w[g].x) * f);
+      q[g][1] = pack_f16x2(bf16lo(w[g].y) * f, bf16hi(w[g].y) * f);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      qs[k] = __shfl_sync(0xffffffffu, scale, 8 * c + 4 * k);
+      const uint64_t path = tree_mask_of(tree, min(2 * c + k, rows - 1) / a.G);
+      seen[k] = 2 * c + k < rows ? path : 0ull;
+      m[k] = -INFINITY, l[k] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+  }
+
+  __device__ __forceinline__ void units(const uint8_t* u, int base, int left, int h0, int h1, int lane) {
+    using L = Kv4Block<D>;
+    constexpr int GW = D / 32;
+    const int r = lane >> 2, c = lane & 3;
+    const bool part = base > -kPage;
+    const uint64_t bad = part ? atr_bad<D>(u, left, h0, h1, lane) : 0ull;
+#pragma unroll 1
+    for (int half = h0; half < h1; ++half) {
+      float s[2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t k0[GW], k1[GW], c0[GW / 2], c1[GW / 2];
+        const int t0 = 32 * half + 16 * mt + r;
+        lds_words<GW>(u + L::kK + t0 * (D / 2) + c * (D / 8), k0);
+        lds_words<GW>(u + L::kK + (t0 + 8) * (D / 2) + c * (D / 8), k1);
+        lds_words<GW / 2>(u + L::kKs + t0 * (D / 16), c0);
+        lds_words<GW / 2>(u + L::kKs + (t0 + 8) * (D / 16), c1);
+#pragma unroll
+        for (int w = 0; w < GW; ++w) {
+          const uint32_t e0 = scales02(c0[w / 2], kScaleBits), f0 = scales13(c0[w / 2], kScaleBits);
+          const uint32_t e1 = scales02(c1[w / 2], kScaleBits), f1 = scales13(c1[w / 2], kScaleBits);
+          uint32_t x[4], y[4];
+          codes4(k0[w], x);
+          codes4(k1[w], y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t sx = i < 2 ? e0 : f0, sy = i < 2 ? e1 : f1;
+            x[i] = w & 1 ? hmul2_hi(x[i], sx) : hmul2_lo(x[i], sx);
+            y[i] = w & 1 ? hmul2_hi(y[i], sy) : hmul2_lo(y[i], sy);
+          }
+          if (w == 0)
+            mma_f16_first(s[mt], x[0], y[0], x[1], y[1], q[0][0], q[0][1]);
+          else
+            mma_f16(s[mt], x[0], y[0], x[1], y[1], q[2 * w][0], q[2 * w][1]);
+          mma_f16(s[mt], x[2], y[2], x[3], y[3], q[2 * w + 1][0], q[2 * w + 1][1]);
+        }
+      }
+      bool grow = false;
+      float mx[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (part) {
+          const uint64_t see = base >= 0 ? seen[k] >> base : seen[k] << -base | ((1ull << -base) - 1);
+          const uint32_t bits = (uint32_t)(see >> (32 * half)) >> r;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (!(bits >> (16 * mt + 8 * j) & 1u)) s[mt][2 * j + k] = -INFINITY;
+        }
+        mx[k] = fmaxf(fmaxf(s[0][k], s[0][2 + k]), fmaxf(s[1][k], s[1][2 + k]));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], x));
+        mx[k] *= qs[k];
+        grow |= mx[k] - m[k] > 8.0f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {  // (as for 16 rows)
+        float f[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool up = mx[k] - m[k] > 8.0f;
+          f[k] = up ? ad_ex2(m[k] - mx[k]) : 1.0f;
+          if (up) m[k] = mx[k];
+          l[k] *= f[k];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] *= f[j & 1];
+      }
+      uint32_t p[2][2];
+      const float b0 = m[0] == -INFINITY ? 0.0f : 7.0f - m[0], b1 = m[1] == -INFINITY ? 0.0f : 7.0f - m[1];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float x0 = ad_ex2(fmaf(s[mt][0], qs[0], b0)), x1 = ad_ex2(fmaf(s[mt][1], qs[1], b1));
+        const float x2 = ad_ex2(fmaf(s[mt][2], qs[0], b0)), x3 = ad_ex2(fmaf(s[mt][3], qs[1], b1));
+        l[0] += x0 + x2;
+        l[1] += x1 + x3;
+        p[mt][0] = trans8x8(pack_f16x2(x0, x1));
+        p[mt][1] = trans8x8(pack_f16x2(x2, x3));
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int blk = 4 * half + 2 * ks;
+        uint32_t v0[GW], v1[GW], s0[GW], s1[GW];
+        lds_words<GW>(u + L::kV + blk * (4 * D) + r * (D / 2) + c * (D / 8), v0);
+        lds_words<GW>(u + L::kV + (blk + 1) * (4 * D) + r * (D / 2) + c * (D / 8), v1);
+        lds_words<GW>(u + L::kVs + (4 * blk + c) * (D / 8), s0);
+        lds_words<GW>(u + L::kVs + (4 * blk + 4 + c) * (D / 8), s1);
+        uint32_t k0 = kScaleBits, k1 = kScaleBits;  // slots past the last token may hold any scale: theirs become 0
+        if (part) {
+          const int t0 = 8 * blk + 2 * c, t1 = t0 + 8;
+          k0 = (t0 < left ? 0x7F80u : 0u) | (t0 + 1 < left ? 0x7F800000u : 0u);
+          k1 = (t1 < left ? 0x7F80u : 0u) | (t1 + 1 < left ? 0x7F800000u : 0u);
+        }
+#pragma unroll
+        for (int w = 0; w < GW; ++w) {
+          uint32_t e0 = scales02(s0[w], k0), f0 = scales13(s0[w], k0), e1 = scales02(s1[w], k1), f1 = scales13(s1[w], k1);
+          if (bad) e0 = kv4_finite(e0), f0 = kv4_finite(f0), e1 = kv4_finite(e1), f1 = kv4_finite(f1);
+          uint32_t x[4], y[4];
+          codes4(v0[w], x);
+          codes4(v1[w], y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], i < 2 ? e0 : f0), y[i] = hmul2(y[i], i < 2 ? e1 : f1);
+          mma_f16(o[2 * w], x[0], x[1], y[0], y[1], p[ks][0], p[ks][1]);
+          mma_f16(o[2 * w + 1], x[2], x[3], y[2], y[3], p[ks][0], p[ks][1]);
+        }
+      }
+    }
+    for (uint64_t e = bad; e; e &= e - 1) {
+      const int t = __ffsll((long long)e) - 1;
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g)
+        if ((u[L::vs(t, g)] & 0xF8u) == 0xF8u) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool see = base + t < 0 || seen[j & 1] >> (base + t) & 1;
+            if (see) o[g][j] = __int_as_float(0x7FFFFFFF);
+          }
+        }
+    }
+  }
+
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
+      if (seen[k] == 0) {
+        m[k] = -INFINITY, l[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i][k] = o[i][2 + k] = 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void store_part(float* out, float* pm, float* pl, int lane) const {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (r == 0) pm[2 * c + k] = m[k], pl[2 * c + k] = l[k];
+      float* d = out + (2 * c + k) * AtrCfg<D, 8>::kStride + r;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) d[16 * i] = o[i][k], d[16 * i + 8] = o[i][2 + k];
+    }
+  }
+  __device__ __forceinline__ void store_out(const AtrArgs& a, int b, int hk, int lane) const {
+    const int r = lane >> 2, c = lane & 3, rows = atr_nodes(a.g, b) * a.G;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int x = 2 * c + k, node = x / a.G;
+      if (x >= rows) continue;
+      const float inv = l[k] != 0.0f ? 1.0f / l[k] : 0.0f;  // nothing seen: zeros
+      uint16_t* d = a.g.out + (size_t)(a.g.t.cu[b] + node) * a.g.ld_o + (size_t)(hk * a.G + x - node * a.G) * D + r;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        d[16 * i] = f32_to_bf16(o[i][k] * inv);
+        d[16 * i + 8] = f32_to_bf16(o[i][2 + k] * inv);
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ void atr_copy16(uint32_t dst, const void* src, uint64_t pol) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(pol) : "memory");
 }
 
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_constant__ AtrArgs a) {
-  using C = AtrCfg<D>;
-  constexpr int S = C::kStages, ROWS = kAtrRows, PARTS = kAtrParts;
-  static_assert(PARTS * ROWS == kAtrThreads && PARTS <= 32, "a thread per part and row");
+  using C = AtrCfg<D, ROWS>;
+  constexpr int S = C::kStages, PARTS = kAtrParts;
+  static_assert(PARTS * ROWS <= kAtrThreads && PARTS <= 32, "a thread per part and row");
   static_assert(C::kRecord * 4 <= C::kRing, "a record lies in its warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
-  AtrShared* sh = reinterpret_cast<AtrShared*>(smem + kAtWarps * C::kRing);
+  AtrShared<ROWS>* sh = reinterpret_cast<AtrShared<ROWS>*>(smem + kAtWarps * C::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   if (lane == 0) sh->meta[2 * warp].seg = sh->meta[2 * warp + 1].seg = -1;
   if (tid < 2) sh->cta_seg[tid] = -1;
@@ -417,7 +636,7 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
     uint32_t ok = 0;  // stages that hold a page
     const uint32_t to = smem_addr(ring) + 16 * lane;
     uint64_t tree[2] = {0, 0};
-    AtrRows<D> rows;
+    typename std::conditional<ROWS == 8, AtrFewRows<D>, AtrRows<D>>::type rows;
     int pos = 0, masks_of = -1;
     // Everything stands in this loop once: code that is not in the SM's cache costs some 50 cycles an instruction.
 #pragma unroll 1
@@ -488,7 +707,7 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
     // a thread per (part, row): those of a tile's first part weigh its parts
     const int e = tid / ROWS, x = tid - e * ROWS;
     const uint32_t parts = __shfl_sync(0xffffffffu, same, e & 31);
-    if (lead >> e & 1) {
+    if (e < PARTS && (lead >> e & 1)) {
       float top = -INFINITY, l = 0.0f;
       for (uint32_t y = parts; y; y &= y - 1) top = fmaxf(top, sh->part_m[__ffs(y) - 1][x]);
       for (uint32_t y = parts; y; y &= y - 1) {
@@ -557,9 +776,9 @@ __global__ void __launch_bounds__(kAtrThreads, 1) attn_tree_kernel(const __grid_
 // goes on.  D/4 threads hold four channels each; the parts are dealt out over groups of
 // them and joined through shared memory.
 constexpr int kAtrcThreads = 128;
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(const __grid_constant__ AtrArgs a) {
-  using C = AtrCfg<D>;
+  using C = AtrCfg<D, ROWS>;
   constexpr int P = D / 4, GR = kAtrcThreads / P;
   __shared__ float pm[GR], pl[GR];
   __shared__ float4 po[kAtrcThreads];
@@ -569,8 +788,8 @@ __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(con
   const int seg = a.cta_seg[2 * c + 1];
   auto load = [&](int y, float& m, float& l, float4& o) {
     const float* r = a.cta_part + (size_t)(y == 0 ? 2 * c + 1 : 2 * min(c + y, a.nc - 1)) * C::kRecord;
-    m = r[x], l = r[kAtrRows + x];
-    o = *reinterpret_cast<const float4*>(r + 2 * kAtrRows + x * C::kStride + d);
+    m = r[x], l = r[ROWS + x];
+    o = *reinterpret_cast<const float4*>(r + 2 * ROWS + x * C::kStride + d);
   };
   float m, l;
   float4 o;
@@ -581,7 +800,7 @@ __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(con
     k += n;
     if (n < kAtrcThreads) break;
   }
-  uint16_t* out = seg < 0 ? nullptr : atr_out(a, seg, x, kAtrRows, D);
+  uint16_t* out = seg < 0 ? nullptr : atr_out(a, seg, x, ROWS, D);
   if (!out) return;
   if (g >= k) m = -INFINITY, l = 0.0f, o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int y = g + GR; y < k; y += GR) {
@@ -617,18 +836,18 @@ __global__ void __launch_bounds__(kAtrcThreads, 16) attn_tree_combine_kernel(con
 template <int D>
 static size_t atr_ws_bytes() {
   const size_t n = num_sms();
-  return n * (kAtWarps + 2) * AtrCfg<D>::kRecord * 4 + (n * 2 * 4 + 255) / 256 * 256;
+  return n * (kAtWarps + 2) * AtrCfg<D, 16>::kRecord * 4 + (n * 2 * 4 + 255) / 256 * 256;
 }
 size_t attn_tree_ws_bytes(int32_t D) {
   const size_t x = D == 128 ? atr_ws_bytes<128>() : atr_ws_bytes<64>(), y = attn_tree_tc_ws_bytes(D);
   return x > y ? x : y;  // whatever the trees
 }
 
-template <int D>
+template <int D, int ROWS>
 static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
-  using C = AtrCfg<D>;
+  using C = AtrCfg<D, ROWS>;
   static int done_mask[64] = {0};
-  constexpr int smem = kAtWarps * C::kRing + (int)sizeof(AtrShared);
+  constexpr int smem = kAtWarps * C::kRing + (int)sizeof(AtrShared<ROWS>);
   static_assert(smem <= 232448, "shared memory");
   AtrArgs a;
   a.g = g;
@@ -641,7 +860,7 @@ static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
   a.cta_seg = static_cast<int32_t*>(g.ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(g.ws) + (n * 2 * 4 + 255) / 256 * 256);
   a.cta_part = a.part + n * kAtWarps * C::kRecord;
-  auto kern = attn_tree_kernel<D>;
+  auto kern = attn_tree_kernel<D, ROWS>;
   cudaError_t e = set_smem_once((const void*)kern, smem, done_mask);
   if (e != cudaSuccess) return e;
   trace_pre(K_ATTN_TREE, s);
@@ -649,7 +868,7 @@ static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
   trace_post(K_ATTN_TREE, s);
   if (e != cudaSuccess || a.by_row) return e;
   trace_pre(K_ATTN_TREE_COMBINE, s);
-  e = launch_k(attn_tree_combine_kernel<D>, dim3(a.nc, g.most * a.G), dim3(kAtrcThreads), 0, s, true, a);
+  e = launch_k(attn_tree_combine_kernel<D, ROWS>, dim3(a.nc, g.most * a.G), dim3(kAtrcThreads), 0, s, true, a);
   trace_post(K_ATTN_TREE_COMBINE, s);
   return e;
 }
@@ -657,9 +876,12 @@ static cudaError_t launch_atr(const AttnTreeArgs& g, cudaStream_t s) {
 cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s) {
   // 16 rows here / by the tensor-core kernel: 61.9 / 102.9 us for 64 sequences of 64 to
   // 4096 tokens, 14.4 / 15.8 for one of 2000; a second tile of 16 rows would work through
-  // every page again.
-  if (a.most * (a.H / a.c.Hkv) > kAtrRows) return launch_attn_tree_tc(a, s);
-  return a.c.D == 128 ? launch_atr<128>(a, s) : launch_atr<64>(a, s);
+  // every page again.  8 rows by the kernel for 8 / for 16: 46.8 / 56.5 us for the 64, 21.7 /
+  // 24.2 for one of 30000; 5 rows of 16 kv heads of 64: 55.4 / 61.8.
+  const int rows = a.most * (a.H / a.c.Hkv);
+  if (rows > 16) return launch_attn_tree_tc(a, s);
+  if (rows > 8) return a.c.D == 128 ? launch_atr<128, 16>(a, s) : launch_atr<64, 16>(a, s);
+  return a.c.D == 128 ? launch_atr<128, 8>(a, s) : launch_atr<64, 8>(a, s);
 }
 
 int status_attn_tree(int clear) { return tu_status(clear); }

@@ -160,6 +160,17 @@ def test_attention_of_short_and_long_together(H, Hkv, D, n):
     run_tree(lens, pasts, H, Hkv, D, seed=n)
 
 
+@pytest.mark.parametrize("H,Hkv,D,n", [(4, 4, 128, 8), (4, 2, 128, 4), (32, 8, 128, 2), (8, 8, 64, 7), (6, 2, 64, 2), (8, 1, 64, 1),
+                                       (3, 3, 128, 5), (16, 16, 64, 8)])
+def test_attention_of_few_rows(H, Hkv, D, n):
+    """At most 8 rows a kv head, at every kind of length and cut."""
+    rng = random.Random(H + n)
+    for seed, pasts in enumerate(([0, 1, 31, 32, 33, 63, 64, 65, 127, 128, 500], [3000], [700, 0, 40, 9] * 35)):
+        lens = [n if i % 3 < 2 else rng.randrange(n + 1) for i in range(len(pasts))]
+        run_tree(lens, pasts, H, Hkv, D, seed=seed)
+    run_tree([n, n], [20, 9000], H, Hkv, D, kind="chain", spread=30.0, seed=5, width=400)
+
+
 # ------------------------------------------------------------------ waits, streams, graphs
 
 @pytest.mark.parametrize("D", [64, 128])
