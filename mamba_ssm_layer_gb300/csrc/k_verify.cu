@@ -228,6 +228,15 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
     hi2[0] = hi2[1] = lo2[0] = lo2[1] = make_float2(0.0f, 0.0f);
     float most = 0.0f;
     constexpr int UN = 4, UM = 2;  // loads together (64 registers: four of each were spilled)
+    // Refused tokens of a draft without rows are left out of the sums, as out of the search below:
+    // taken from them again they would leave roundings where nothing is left.
+    auto refused = [&](int x) {
+      for (int k = 0; k < cmd.gone; ++k)
+        if (sh.gone_tok[k] == x) return true;
+      return false;
+    };
+    bool some_gone = false;  // in this warp's run
+    for (int k = 0; k < cmd.gone; ++k) some_gone |= sh.gone_tok[k] >= from && sh.gone_tok[k] < to;
     const bool once = cmd.c_hi == 1.0f && cmd.c_lo == 0.0f;  // one refusal: c is 1
     if (minus) {
       for (int at = from + 4 * lane; at < to; at += 128 * UM) {
@@ -256,6 +265,18 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
         float4 v[UN];
 #pragma unroll
         for (int k = 0; k < UN; ++k) v[k] = vf_raw<BF>(p, at + 128 * k, to, wide);
+        if (some_gone) {
+          for (int g = 0; g < cmd.gone; ++g) {
+            const int x = sh.gone_tok[g] - at;
+#pragma unroll
+            for (int k = 0; k < UN; ++k) {
+              if (x == 128 * k) v[k].x = 0.0f;
+              if (x == 128 * k + 1) v[k].y = 0.0f;
+              if (x == 128 * k + 2) v[k].z = 0.0f;
+              if (x == 128 * k + 3) v[k].w = 0.0f;
+            }
+          }
+        }
 #pragma unroll
         for (int k = 0; k < UN; ++k) {
           vf_sum2(hi2[0], lo2[0], make_float2(fmaxf(v[k].x, 0.0f), fmaxf(v[k].y, 0.0f)));
@@ -275,19 +296,10 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
       // an infinity among them, which counts as 0: the run once more, value by value
       hi = lo = 0.0f;
       for (int x = from + lane; x < to; x += 32)
-        vf_add(hi, lo, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, cmd.c_hi, cmd.c_lo);
+        if (!(some_gone && refused(x))) vf_add(hi, lo, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, cmd.c_hi, cmd.c_lo);
     }
     two_sum_warp(hi, lo);
-    if (lane == 0) {
-      // refused tokens of a draft without rows: each once
-      for (int k = 0; k < cmd.gone; ++k) {
-        const int x = sh.gone_tok[k];
-        bool again = false;
-        for (int e = 0; e < k; ++e) again |= sh.gone_tok[e] == x;
-        if (!again && x >= from && x < to) two_sum_acc(hi, lo, -vf_one<BF>(p, x));
-      }
-      sh.hi[warp] = hi, sh.lo[warp] = lo;
-    }
+    if (lane == 0) sh.hi[warp] = hi, sh.lo[warp] = lo;
     if (pass == 0) vf_cluster_wait();
     __syncthreads();
     if (warp == 0) {
@@ -370,9 +382,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
       const int r1 = (int)min(r0 + per, (int64_t)V), each = (per / kVfThreads + 3) / 4 * 4 + (per % kVfThreads ? 4 : 0);
       const int x0 = (int)min(r0 + (int64_t)tid * each, (int64_t)r1), x1 = (int)min((int64_t)x0 + each, (int64_t)r1);
       auto value = [&](int x, float vp, float vq, float& h, float& l) {
-        for (int k = 0; k < cmd.gone; ++k)
-          if (sh.gone_tok[k] == x) return;
-        vf_add(h, l, vp, vq, cmd.c_hi, cmd.c_lo);
+        if (!refused(x)) vf_add(h, l, vp, vq, cmd.c_hi, cmd.c_lo);
       };
       float vh = 0.0f, vl = 0.0f;
 #pragma unroll 2

@@ -1,0 +1,71 @@
+"""Faults that were found in the operators for trees of drafted tokens, each held by what it
+answered wrongly.  Plain forms in tree_ref.py."""
+import random
+
+import pytest
+import torch
+
+from mamba_ssm_layer_gb300 import abi
+from tests.test_gpu_tree import same_as_reference, verify
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from __graft_entry__ import build
+    build()
+    abi.m2_device_status(clear=True)
+    yield
+    assert abi.m2_device_status() == abi.M2_OK
+
+
+# ------------------------------------------------------------------ verification: what refused tokens leave
+
+def row(V, values):
+    p = torch.zeros(1, V, device="cuda")
+    for x, v in values.items():
+        p[0, x] = v
+    return p
+
+
+def floats(*v):
+    return torch.tensor(v, dtype=torch.float32, device="cuda")
+
+
+BELOW_ONE = 1.0 - 2.0 ** -24
+
+
+def test_verify_draws_the_little_that_refused_tokens_leave():
+    """Two tokens hold all but 5e-8 of the row: they are refused, and the third is drawn."""
+    for at in ([0, 1, 2], [0, 1, 999], [999, 0, 1], [5, 400, 700]):
+        p = row(1000, dict(zip(at, (0.4566476, 0.54335237, 4.7786124e-8))))
+        p = p.expand(3, -1).contiguous()
+        got = verify(p, None, [0, 3], [[-1, 0, 0]], [0, at[0], at[1]], floats(0.0, 0.9, BELOW_ONE), floats(0.5))
+        assert got == ([0, -1, -1], [1], [at[2]])
+
+
+@pytest.mark.parametrize("V", [3, 40, 1000, 70000])
+@pytest.mark.parametrize("u_next", [0.0, 0.5, BELOW_ONE, 1.0])
+def test_verify_never_draws_a_refused_token(V, u_next):
+    """Runs that hold refused tokens alone, beside one with a token that is left; a random number of 1 takes the last."""
+    rng = random.Random(V)
+    for n in (2, 5, 40):
+        n = min(n, V - 1)
+        far = sorted(rng.sample(range(V), n + 1))
+        left = far.pop(rng.randrange(n + 1))
+        weight = (torch.rand(n, generator=torch.Generator().manual_seed(n)) + 0.1).tolist()
+        p = row(V, {x: w / sum(weight) for x, w in zip(far, weight)})
+        p[0, left] = 2.0 ** -40
+        p = p.expand(n + 1, -1).contiguous()
+        u = torch.full((n + 1,), 2.0, device="cuda")  # (refused whatever is left)
+        got = verify(p, None, [0, n + 1], [[-1] + [0] * n], [0] + far, u, floats(u_next))
+        assert got == ([0] + [-1] * n, [1], [left]), n
+
+
+@pytest.mark.parametrize("V", [64, 5000])
+def test_verify_refused_tokens_beside_values_that_are_none(V):
+    """Infinities and NaN in the same run as refused tokens."""
+    p = row(V, {3: 0.25, 9: 0.25, 11: 0.5, 20: float("inf"), 21: float("nan"), 22: -1.0}).expand(4, -1).contiguous()
+    for un in (0.0, 0.4, BELOW_ONE):
+        same_as_reference(p, None, [0, 4], [[-1, 0, 0, 0]], [0, 11, 3, 20], floats(0.0, 0.9, BELOW_ONE, 0.0), floats(un))
