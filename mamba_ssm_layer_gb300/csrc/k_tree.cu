@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
               }
             }
           }
-          float* d = yr + (j - r) * HP + (p0 - pw);
+          float* d = yr + (size_t)(j - r) * HP + (p0 - pw);  // (past 2^31 elements where H * P is large)
           if (a.P % 2 == 0) {
             *reinterpret_cast<float2*>(d) = make_float2(y[0], y[1]);
           } else {

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 from mamba_ssm_layer_gb300 import abi
-from tests.test_gpu_tree import same_as_reference, verify
+from tests.test_gpu_attention import gen, rows
+from tests.test_gpu_tree import ints, same_as_reference, verify
+from tests.tree_ref import random_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,29 @@ def test_verify_refused_tokens_beside_values_that_are_none(V):
     p = row(V, {3: 0.25, 9: 0.25, 11: 0.5, 20: float("inf"), 21: float("nan"), 22: -1.0}).expand(4, -1).contiguous()
     for un in (0.0, 0.4, BELOW_ONE):
         same_as_reference(p, None, [0, 4], [[-1, 0, 0, 0]], [0, 11, 3, 20], floats(0.0, 0.9, BELOW_ONE, 0.0), floats(un))
+
+
+# ------------------------------------------------------------------ SSM outputs: rows far apart
+
+def test_ssm_rows_of_many_channels():
+    """56 rows of H * P outputs pass 2^31 elements: what the first, middle and last heads give alone."""
+    H, P, N, G, n = 150016, 256, 16, 1, 64
+    assert 56 * H * P > 2 ** 31
+    g = gen(1)
+    h = torch.empty(1, H, P, N, device="cuda").normal_(generator=g)
+    x = torch.empty(n, H * P, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    bc, dt = rows(n, 2 * N, g), rows(n, H, g)
+    A_log, D, bias = (torch.rand(H, device="cuda", generator=g) for _ in range(3))
+    parent = ints(random_parents(n, random.Random(1)))
+    wide = torch.empty(n, 2, H * P, dtype=torch.bfloat16, device="cuda")  # B and C at x's stride
+    wide[:, 0, :2 * N].copy_(bc)
+    B, C, ld = wide[:, 0], wide[:, 0, N:], 2 * H * P
+    wide[:, 1].copy_(x)
+    del x
+    x, y = wide[:, 1], torch.full((n, H * P), 7.0, device="cuda")
+    abi.mamba2_tree_ssm(h, x, B, C, ld, dt, H, A_log, D, bias, y, [0, n], parent, H, P, N, G)
+    for h0 in (0, H // 2, H - 8):
+        one, to = torch.empty(n, 8 * P, device="cuda"), slice(h0, h0 + 8)
+        abi.mamba2_tree_ssm(h[0, to], x[:, h0 * P:], B, C, ld, dt[:, h0:], H, A_log[to].clone(), D[to].clone(), bias[to].clone(),
+                            one, [0, n], parent, 8, P, N, G)
+        assert torch.equal(y[:, h0 * P:(h0 + 8) * P], one)
