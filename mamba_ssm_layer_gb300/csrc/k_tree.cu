@@ -849,6 +849,13 @@ __global__ void __launch_bounds__(256) tree_state_kernel(const TreeCommitArgs a,
   }
 }
 
+static cudaError_t launch_tree_ring(const TreeCommitArgs& a, cudaStream_t s) {
+  trace_pre(K_TREE_RING, s);
+  const cudaError_t e = launch_k(tree_ring_kernel, dim3(kTrCtas, a.t.nseq), dim3(kTrThreads), 0, s, true, a);
+  trace_post(K_TREE_RING, s);
+  return e;
+}
+
 template <int LPR>
 static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
   constexpr int RPW = 32 / LPR;
@@ -865,8 +872,15 @@ static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
   for (int i = 0; i < a.t.nseq; ++i) most = a.t.cu[i + 1] - a.t.cu[i] > most ? a.t.cu[i + 1] - a.t.cu[i] : most;
   const int each = a.N * 2 + 8 * RPW * rows * 4, smem = most * each;  // at most 64 * (32 + 2048) bytes: N = 16
   auto go = [&](void (*k)(TreeCommitArgs, int), int* done_mask) {
-    const cudaError_t e = smem > 48 * 1024 ? set_smem_once((const void*)k, kTreeNodes * each, done_mask) : cudaSuccess;
-    return e != cudaSuccess ? e : launch_k(k, grid, block, smem, s, true, a, psplit);
+    // One limit whatever the call's trees (beside it a block has 768 bytes of its own), and asked for before anything
+    // is launched: a refusal leaves ring and position as they were.
+    cudaError_t e = set_smem_once((const void*)k, kTreeNodes * each, done_mask);
+    if (e == cudaSuccess && !a.wide) e = launch_tree_ring(a, s);
+    if (e != cudaSuccess) return e;
+    trace_pre(K_TREE_STATE, s);
+    e = launch_k(k, grid, block, smem, s, true, a, psplit);
+    trace_post(K_TREE_STATE, s);
+    return e;
   };
   static int done[4][64] = {{0}};
   switch (rows) {
@@ -878,22 +892,12 @@ static cudaError_t launch_tree_state(const TreeCommitArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
-  cudaError_t e;
-  if (!a.wide) {
-    trace_pre(K_TREE_RING, s);
-    e = launch_k(tree_ring_kernel, dim3(kTrCtas, a.t.nseq), dim3(kTrThreads), 0, s, true, a);
-    trace_post(K_TREE_RING, s);
-    if (e != cudaSuccess) return e;
-  }
-  trace_pre(K_TREE_STATE, s);
   switch (a.N / 4) {
-    case 4: e = launch_tree_state<4>(a, s); break;
-    case 8: e = launch_tree_state<8>(a, s); break;
-    case 16: e = launch_tree_state<16>(a, s); break;
-    default: e = launch_tree_state<32>(a, s); break;
+    case 4: return launch_tree_state<4>(a, s);
+    case 8: return launch_tree_state<8>(a, s);
+    case 16: return launch_tree_state<16>(a, s);
+    default: return launch_tree_state<32>(a, s);
   }
-  trace_post(K_TREE_STATE, s);
-  return e;
 }
 
 int status_tree(int clear) { return tu_status(clear); }

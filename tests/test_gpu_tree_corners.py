@@ -7,7 +7,7 @@ import torch
 
 from mamba_ssm_layer_gb300 import abi
 from tests.test_gpu_attention import gen, rows
-from tests.test_gpu_tree import ints, same_as_reference, verify
+from tests.test_gpu_tree import Ssm, ints, same_as_reference, verify
 from tests.tree_ref import random_parents
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +97,28 @@ def test_ssm_rows_of_many_channels():
         abi.mamba2_tree_ssm(h[0, to], x[:, h0 * P:], B, C, ld, dt[:, h0:], H, A_log[to].clone(), D[to].clone(), bias[to].clone(),
                             one, [0, n], parent, 8, P, N, G)
         assert torch.equal(y[:, h0 * P:(h0 + 8) * P], one)
+
+
+# ------------------------------------------------------------------ commit: shared memory next to what needs no asking
+
+@pytest.mark.parametrize("N,n", [(16, 46), (16, 45), (16, 47), (32, 45), (32, 44), (32, 46)])
+@pytest.mark.parametrize("G", [1, 2])
+def test_commit_of_wide_heads(N, n, G):
+    """Heads of 256 channels, enough of them for the longest blocks, and paths whose inputs just fill the shared memory
+    that a kernel has without asking for more (of which a block's own arrays take 768 bytes)."""
+    H, P, K, B = 40, 256, 4, 8
+    s = Ssm(B, B * n, H, P, N, G, n, extra=4)
+    W, xbc = s.W, s.u.contiguous() if G == 1 else s.u  # (in one launch; with the ring in a launch of its own)
+    ring, pos = rows(B * (K - 1), W, gen(2)).view(B, K - 1, W), ints([7 * i for i in range(B)])
+    h1, ring1, pos1 = s.h.clone(), ring.clone(), pos.clone()
+    for j in range(n):
+        u, dt = s.u[j::n].contiguous(), s.dt[j::n].contiguous()
+        dt = torch.cat([dt, dt.new_zeros(B, W - H)], 1)
+        y = torch.empty(B, H * P, device="cuda")
+        abi.mamba2_ssm_step(h1, u, u[:, H * P:], u[:, H * P + G * N:], dt, W, s.A_log, s.D, s.dt_bias, y, B, H, P, N, G)
+        ring1[torch.arange(B, device="cuda"), (pos1 % (K - 1)).long()] = s.u[j::n]
+        pos1 += 1
+    abi.mamba2_tree_commit(s.h, ring, pos, s.h, ring, pos, xbc, xbc.stride(0), s.u, s.u.stride(0), s.dt, s.dt.stride(0),
+                           s.A_log, s.dt_bias, [n * i for i in range(B + 1)], ints(list(range(n)) * B), ints([n] * B), H, P,
+                           N, G, K)
+    assert torch.equal(s.h, h1) and torch.equal(ring, ring1) and torch.equal(pos, pos1)
