@@ -79,14 +79,22 @@ __device__ __forceinline__ float4 vf_four(const void* row, int at, int V, bool w
   const float4 v = vf_raw<BF>(row, at, V, wide);
   return make_float4(vf_clean(v.x), vf_clean(v.y), vf_clean(v.z), vf_clean(v.w));
 }
-// (hi, lo) += R of one token.  Where R is positive p is the larger of the two, so that three
-// additions give p - c q and its rounding.
-__device__ __forceinline__ void vf_add(float& hi, float& lo, float p, float q, float c_hi, float c_lo) {
-  const float t = fminf(c_hi * q, p), s = p - t;
-  if (s > 0.0f) {
-    two_sum_acc(hi, lo, s);
-    lo += ((p - s) - t) - fmaf(c_lo, q, fmaf(c_hi, q, -t));
-  }
+// (hi, lo) += R of one token; whether there is any.  p - c q in fp32, s, and what its additions and
+// the product lost, d: their sum's sign is R's, also where c q is p but for its rounding (s is then 0
+// or one place off either way).
+__device__ __forceinline__ bool vf_add(float& hi, float& lo, float p, float q, float c_hi, float c_lo) {
+  const float t = __fmul_rn(c_hi, q), s = p - t;  // (never one fused step: d needs the product as it was rounded)
+  const float d = ((p - s) - t) - fmaf(c_lo, q, fmaf(c_hi, q, -t));
+  if (!(s + d > 0.0f)) return false;
+  two_sum_acc(hi, lo, s);
+  lo += d;
+  return true;
+}
+// The pair with its sum in hi: hi is positive where the sum is.
+__device__ __forceinline__ void vf_norm(float& hi, float& lo) {
+  const float s = hi + lo;
+  lo -= s - hi;
+  hi = s;
 }
 // Two tokens a lane at once.  What is not positive, NaN among it, counts as 0 here;
 // infinities are found afterwards (`most` of the draft, the sum of the target).
@@ -102,11 +110,15 @@ __device__ __forceinline__ void vf_add2(float2& hi, float2& lo, float2 p, float2
   q = make_float2(fmaxf(q.x, 0.0f), fmaxf(q.y, 0.0f));
   most = max3(most, q.x, q.y);
   const float2 cq = ONE ? q : make_float2(c_hi * q.x, c_hi * q.y);
-  const float2 t = make_float2(fminf(cq.x, p.x), fminf(cq.y, p.y)), s = vf_sub2(p, t);
-  float2 d = vf_sub2(vf_sub2(p, s), t);
-  if (!ONE) {  // the product's own rounding, where something is left
+  // (c = 1: the product is exact, so that s alone says what is left)
+  const float2 t = ONE ? make_float2(fminf(cq.x, p.x), fminf(cq.y, p.y)) : cq;
+  float2 s = vf_sub2(p, t), d = vf_sub2(vf_sub2(p, s), t);
+  if (!ONE) {
     const float2 e = make_float2(fmaf(c_lo, q.x, fmaf(c_hi, q.x, -t.x)), fmaf(c_lo, q.y, fmaf(c_hi, q.y, -t.y)));
-    d = vf_sub2(d, make_float2(s.x > 0.0f ? e.x : 0.0f, s.y > 0.0f ? e.y : 0.0f));
+    d = vf_sub2(d, e);
+    const bool x = s.x + d.x > 0.0f, y = s.y + d.y > 0.0f;
+    s = make_float2(x ? s.x : 0.0f, y ? s.y : 0.0f);
+    d = make_float2(x ? d.x : 0.0f, y ? d.y : 0.0f);
   }
   vf_sum2(hi, lo, s);
   lo = fadd2(lo, d);
@@ -299,12 +311,14 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
         if (!(some_gone && refused(x))) vf_add(hi, lo, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, cmd.c_hi, cmd.c_lo);
     }
     two_sum_warp(hi, lo);
+    vf_norm(hi, lo);
     if (lane == 0) sh.hi[warp] = hi, sh.lo[warp] = lo;
     if (pass == 0) vf_cluster_wait();
     __syncthreads();
     if (warp == 0) {
       hi = lane < kVfWarps ? sh.hi[lane] : 0.0f, lo = lane < kVfWarps ? sh.lo[lane] : 0.0f;
       two_sum_warp(hi, lo);
+      vf_norm(hi, lo);
       if (lane < kVfCtas) {
         vf_put(&sh.tot_hi[pass & 1][rank], lane, __float_as_uint(hi));
         vf_put(&sh.tot_lo[pass & 1][rank], lane, __float_as_uint(lo));
@@ -382,18 +396,18 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
       const int r1 = (int)min(r0 + per, (int64_t)V), each = (per / kVfThreads + 3) / 4 * 4 + (per % kVfThreads ? 4 : 0);
       const int x0 = (int)min(r0 + (int64_t)tid * each, (int64_t)r1), x1 = (int)min((int64_t)x0 + each, (int64_t)r1);
       auto value = [&](int x, float vp, float vq, float& h, float& l) {
-        if (!refused(x)) vf_add(h, l, vp, vq, cmd.c_hi, cmd.c_lo);
+        return !refused(x) && vf_add(h, l, vp, vq, cmd.c_hi, cmd.c_lo);
       };
       float vh = 0.0f, vl = 0.0f;
+      bool some = false;
 #pragma unroll 2
       for (int x = x0; x < x1; x += 4) {
         const float4 v = vf_four<BF>(p, x, x1, wide), m = minus ? vf_four<BF>(q, x, x1, wide) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        value(x, v.x, m.x, vh, vl);
-        value(x + 1, v.y, m.y, vh, vl);
-        value(x + 2, v.z, m.z, vh, vl);
-        value(x + 3, v.w, m.w, vh, vl);
+        some |= value(x, v.x, m.x, vh, vl);
+        some |= value(x + 1, v.y, m.y, vh, vl);
+        some |= value(x + 2, v.z, m.z, vh, vl);
+        some |= value(x + 3, v.w, m.w, vh, vl);
       }
-      const bool some = vh > 0.0f;
       float h = vh, l = vl;  // inclusive sums over the threads
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -423,8 +437,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) __cluster_dims__(kVfCtas, 1, 1)
         int found = -1;
         for (int x = x0; x < x1; ++x) {
           float eh = 0.0f, el = 0.0f;
-          value(x, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, eh, el);
-          if (!(eh > 0.0f)) continue;
+          if (!value(x, vf_one<BF>(p, x), minus ? vf_one<BF>(q, x) : 0.0f, eh, el)) continue;
           found = x;
           two_sum_acc(h, l, eh);
           l += el;

@@ -6,9 +6,9 @@ import pytest
 import torch
 
 from mamba_ssm_layer_gb300 import abi
+from tests import tree_ref as ref
 from tests.test_gpu_attention import gen, rows
 from tests.test_gpu_tree import Ssm, ints, same_as_reference, verify
-from tests.tree_ref import random_parents
 
 pytestmark = pytest.mark.gpu
 
@@ -84,7 +84,7 @@ def test_ssm_rows_of_many_channels():
     x = torch.empty(n, H * P, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
     bc, dt = rows(n, 2 * N, g), rows(n, H, g)
     A_log, D, bias = (torch.rand(H, device="cuda", generator=g) for _ in range(3))
-    parent = ints(random_parents(n, random.Random(1)))
+    parent = ints(ref.random_parents(n, random.Random(1)))
     wide = torch.empty(n, 2, H * P, dtype=torch.bfloat16, device="cuda")  # B and C at x's stride
     wide[:, 0, :2 * N].copy_(bc)
     B, C, ld = wide[:, 0], wide[:, 0, N:], 2 * H * P
@@ -122,3 +122,29 @@ def test_commit_of_wide_heads(N, n, G):
                            s.A_log, s.dt_bias, [n * i for i in range(B + 1)], ints(list(range(n)) * B), ints([n] * B), H, P,
                            N, G, K)
     assert torch.equal(s.h, h1) and torch.equal(ring, ring1) and torch.equal(pos, pos1)
+
+
+# ------------------------------------------------------------------ verification: tokens whose remainder is next to 0
+
+def bits(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda").view(torch.float32)
+
+
+def test_verify_remainders_next_to_zero():
+    """After two refusals c q of token 0 is its p but for half a rounding, which is 2^-16 of what all leave together and
+    moves the third child's comparison."""
+    q = bits(0x3f000000, 0x3e999998, 0x3d4ccccd, 0x3e19999a)
+    p = bits(0x3f066668, 0x3ea18937, 0, 0x3e2353f8)
+    P, Q = p.to(ref.F), q.to(ref.F)
+    c = 1 + (P - Q).clamp(min=0).sum()
+    left = (P - c * Q).clamp(min=0)
+    border = float(left[1] / (Q[1] * left.sum()))
+    assert 0 < float(left[0]) < 2.0 ** -24 * float(P[0]) and 0 < border < 1
+    for V in (4, 3000):
+        pr, qr = torch.zeros(4, V, device="cuda"), torch.zeros(4, V, device="cuda")
+        pr[:, :4], qr[:, :4] = p, q
+        for off in (-4e-6, -1e-6, -2e-7, 2e-7, 1e-6, 4e-6):
+            u = floats(0.0, 0.9, 0.9, border + off)
+            for un in (0.0, 0.1, 0.25, 0.9):
+                got = same_as_reference(pr, qr, [0, 4], [[-1, 0, 0, 0]], [0, 2, 2, 1], u, floats(un))
+                assert (got[1] == [2]) == (off < 0)
