@@ -12,7 +12,7 @@ import contextlib
 import torch
 
 from . import abi
-from .layer import _check_nodes, _empty, _zeros, to_dev
+from .layer import _check_count, _check_nodes, _empty, _zeros, to_dev
 
 PAGE = abi.M2_KV4_PAGE
 
@@ -97,8 +97,7 @@ class Kv4Cache:
         ``abi.m2_verify_tree``).  Can be captured; the host's count follows with
         ``advance(count, on_device=False)``."""
         _check_nodes("Kv4Cache.keep", cu_nodes, self.nseq, path)
-        if count.dtype != torch.int32 or count.numel() != self.nseq:
-            raise abi.M2Error("Kv4Cache.keep", abi.M2_ERR_ARG)
+        _check_count("Kv4Cache.keep", count, self.nseq)
         s = stream if stream is not None else torch.cuda.current_stream()
         for c in self.struct:
             abi.m2_kv4_keep(c, cu_nodes, path, count, self.pos, s)

@@ -63,6 +63,12 @@ def _check_nodes(fn: str, cu_nodes, nseq: int, by_node: torch.Tensor) -> None:
         raise abi.M2Error(fn, abi.M2_ERR_ARG)
 
 
+def _check_count(fn: str, count: torch.Tensor, nseq: int) -> None:
+    """An int32 entry a sequence, one behind the other."""
+    if count.dtype != torch.int32 or count.numel() != nseq or not count.is_contiguous():
+        raise abi.M2Error(fn, abi.M2_ERR_ARG)
+
+
 class DeviceLayer:
     """One layer's parameters on the device plus the ctypes structs that point at them."""
 
@@ -160,7 +166,6 @@ class DeviceLayer:
         """The state moved along the accepted path of the last ``tree`` call with this workspace."""
         h, ring, pos = state
         _check_nodes("DeviceLayer.tree_commit", cu_nodes, pos.numel(), path)
-        if count.dtype != torch.int32 or count.numel() != pos.numel():
-            raise abi.M2Error("DeviceLayer.tree_commit", abi.M2_ERR_ARG)
+        _check_count("DeviceLayer.tree_commit", count, pos.numel())
         abi.mamba2_layer_tree_commit(self.dims, self.struct, cu_nodes, path, count, h, ring, pos, ws, ws.numel(),
                                      stream if stream is not None else torch.cuda.current_stream())

@@ -1,0 +1,40 @@
+"""Faults that were found in the holders and entry points for trees of drafted tokens, each held
+by what it accepted or refused wrongly.  No GPU needed."""
+import pytest
+import torch
+
+from mamba_ssm_layer_gb300 import abi, synth
+from tests.test_tree_host import Stream, calls, ints  # noqa: F401
+
+CU = [0, 3, 5]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from __graft_entry__ import build
+    build()
+
+
+def mixer(nseq=2):
+    from mamba_ssm_layer_gb300.attention import DeviceAttention, Kv4Cache
+    m = DeviceAttention(synth.make_attention(synth.TINY_ATTENTION, 9), device="cpu")
+    return m, Kv4Cache(2, nseq, 12, 256, m.Hkv, m.D, device="cpu")
+
+
+def layer(nseq=2):
+    from mamba_ssm_layer_gb300.layer import DeviceLayer
+    dl = DeviceLayer(synth.make_layer(synth.TINY, synth.WL_TINY_DECODE), device="cpu")
+    return dl, dl.new_state(nseq, device="cpu"), dl.workspace_tree(nseq, 5, device="cpu")
+
+
+@pytest.mark.parametrize("count", [torch.arange(4, dtype=torch.int32).view(2, 2)[:, 0], ints(1).expand(2),
+                                   torch.arange(4, dtype=torch.int32)[::2]])
+def test_counts_lie_one_behind_the_other(calls, count):  # noqa: F811
+    _, cache = mixer()
+    dl, st, ws = layer()
+    path = ints(0, 2, -1, 0, -1)
+    with pytest.raises(abi.M2Error):
+        cache.keep(CU, path, count, 0)
+    with pytest.raises(abi.M2Error):
+        dl.tree_commit(CU, path, count, st, ws, Stream())
+    assert not calls and cache.pos.tolist() == [0, 0]
