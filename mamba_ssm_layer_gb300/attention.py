@@ -102,7 +102,7 @@ class Kv4Cache:
         for c in self.struct:
             abi.m2_kv4_keep(c, cu_nodes, path, count, self.pos, s)
         with _on(stream):
-            self.pos.add_(count)
+            self.pos.add_(count.view(-1))
 
     def release(self, seq: int, stream=None, idle: bool = False) -> None:
         """Gives a finished sequence's pages back.  idle: the slot may stay in decode steps without a sequence (its

@@ -1,5 +1,7 @@
 """Faults that were found in the holders and entry points for trees of drafted tokens, each held
 by what it accepted or refused wrongly.  No GPU needed."""
+import contextlib
+
 import pytest
 import torch
 
@@ -38,3 +40,13 @@ def test_counts_lie_one_behind_the_other(calls, count):  # noqa: F811
     with pytest.raises(abi.M2Error):
         dl.tree_commit(CU, path, count, st, ws, Stream())
     assert not calls and cache.pos.tolist() == [0, 0]
+
+
+def test_a_count_of_another_shape_advances_the_cache(calls, monkeypatch):  # noqa: F811
+    """It ended with an error after the rows had been moved."""
+    from mamba_ssm_layer_gb300 import attention
+    monkeypatch.setattr(attention, "_on", lambda stream: contextlib.nullcontext())
+    _, cache = mixer()
+    cache.keep(CU, ints(0, 2, -1, 0, -1), ints(2, 1).view(2, 1), 0)
+    assert [n for n, _ in calls] == ["m2_kv4_keep"] * 2 and cache.pos.tolist() == [2, 1]
+    assert cache.pos.shape == (2,)
