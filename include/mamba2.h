@@ -500,7 +500,8 @@ int mamba2_tree_commit(const float* h, const uint16_t* conv_state, const int32_t
 
 /* A layer over the trees' rows: hidden [T][hidden] bf16 in place, as mamba2_layer_prefill_varlen,
  * but every node continues its parent and the sequences' state is only read.  The workspace
- * (m2_workspace_bytes_tree bytes, 256-byte aligned) holds what the commit needs: each
+ * (m2_workspace_bytes_tree bytes, for passes of up to so many sequences and nodes; 256-byte
+ * aligned) holds what the commit needs: each
  * layer of a stack keeps its own from mamba2_layer_tree to mamba2_layer_tree_commit,
  * which takes the same layer, trees and sequences. */
 size_t m2_workspace_bytes_tree(const m2_dims* dims, int32_t max_seqs, int32_t max_total_nodes);

@@ -217,6 +217,16 @@ static size_t prefill_ws_bound(const m2_dims& d, int T, int nseq, bool w8a8 = tr
   return prefill_ws(d, T, nseq, (T + 127) / 128 + nseq, w8a8);
 }
 
+// The most that `bytes` of 1 .. M rows comes to.  Fewer rows may need more than M: the k-split
+// partials fall where a further token tile leaves a split of fewer parts (none is left from 64 rows
+// an SM on; all else grows with the rows).
+template <typename F>
+static size_t most_ws(int M, F bytes) {
+  size_t most = bytes(M);
+  for (int t = 1; t < M && t <= 64 * num_sms(); ++t) most = bytes(t) > most ? bytes(t) : most;
+  return most;
+}
+
 // Whether a projection consumes f16 activation rows, each prescaled by an
 // exact power of two (E4M3 weights: their f16 conversion is one instruction a
 // pair, in the GEMV and in the tensor-core GEMM's f16 x f16 MMAs), or bf16 rows
@@ -316,7 +326,8 @@ int m2_validate(const m2_dims* dims, const m2_layer* L) {
 size_t m2_workspace_bytes(const m2_dims* dims, int32_t max_batch, int32_t max_tokens) {
   if (check_dims(dims) || max_batch < 0 || max_tokens < 0) return 0;
   const size_t a = max_batch > 0 ? decode_ws(*dims, max_batch) : 0;
-  const size_t b = max_tokens > 0 ? prefill_ws_bound(*dims, max_tokens, 1, false) : 0;
+  const size_t b =
+      max_tokens > 0 ? most_ws(max_tokens, [&](int t) { return prefill_ws_bound(*dims, t, 1, false); }) : 0;
   return a > b ? a : b;
 }
 
@@ -684,7 +695,7 @@ extern "C" {
 
 size_t m2_workspace_bytes_tree(const m2_dims* dims, int32_t max_seqs, int32_t max_total_nodes) {
   if (check_dims(dims) || max_seqs <= 0 || max_total_nodes < 0) return 0;
-  return tree_ws(*dims, max_total_nodes, max_seqs);
+  return most_ws(max_total_nodes, [&](int t) { return tree_ws(*dims, t, max_seqs); });
 }
 
 int mamba2_layer_tree(const m2_dims* dims, const m2_layer* L, uint16_t* hidden, int32_t nseq, const int32_t* cu_nodes,
@@ -793,7 +804,7 @@ int mamba2_layer_prefill_varlen_w8a8(const m2_dims* dims, const m2_layer* L, uin
 
 size_t m2_workspace_bytes_varlen(const m2_dims* dims, int32_t max_seqs, int32_t max_total_tokens) {
   if (check_dims(dims) || max_seqs <= 0 || max_total_tokens < 0) return 0;
-  return prefill_ws_bound(*dims, max_total_tokens, max_seqs);
+  return most_ws(max_total_tokens, [&](int t) { return prefill_ws_bound(*dims, t, max_seqs); });
 }
 
 int w8a16_gemv(const uint16_t* A, const uint8_t* W, const uint16_t* S, uint16_t* out, int32_t M, int32_t N,

@@ -50,3 +50,29 @@ def test_a_count_of_another_shape_advances_the_cache(calls, monkeypatch):  # noq
     cache.keep(CU, ints(0, 2, -1, 0, -1), ints(2, 1).view(2, 1), 0)
     assert [n for n, _ in calls] == ["m2_kv4_keep"] * 2 and cache.pos.tolist() == [2, 1]
     assert cache.pos.shape == (2,)
+
+
+WS_DIMS = [synth.NEMOTRON_H_8B, synth.TINY]
+
+
+@pytest.mark.parametrize("dims", WS_DIMS)
+def test_a_workspace_for_more_rows_holds_fewer(dims):
+    """Whatever passes of up to so many rows need; the k-split partials are not monotone in the rows."""
+    d = abi.dims_struct(dims)
+    for size in (lambda t: abi.m2_workspace_bytes_tree(d, 128, t), lambda t: abi.m2_workspace_bytes_varlen(d, 8, t),
+                 lambda t: abi.m2_workspace_bytes(d, 0, t)):
+        sizes = [size(t) for t in range(1, 700)]
+        assert sizes == sorted(sizes)
+        assert size(20000) >= sizes[-1]
+
+
+def test_a_layer_workspace_for_more_nodes_serves_fewer():
+    """The workspace is looked at before hidden, which is missing here."""
+    from tests.test_tree_host import FAKE, _layer
+    d, M = abi.dims_struct(synth.NEMOTRON_H_8B), abi.M2_ERR_ARG
+    for most in (129, 130, 156, 257, 320, 328):
+        size = abi.m2_workspace_bytes_tree(d, 128, most)
+        for n in range(most - 80, most + 1):
+            cu = [0] + [n * (i + 1) // 128 for i in range(128)]
+            st = abi.mamba2_layer_tree(d, _layer(), None, cu, FAKE, FAKE, FAKE, FAKE, FAKE, size, check=False)
+            assert st == M, (most, n)
