@@ -457,7 +457,9 @@ int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_
  *             reported by m2_device_status (M2_ERR_ARG).
  * Topology, paths and counts are read on the device: a captured pass serves for every
  * tree of its size.  What nodes beside a node's path hold does not reach it, NaN and
- * infinities included.  A call without nodes launches nothing and succeeds. */
+ * infinities included.  A call without nodes succeeds, and the arrays by node may be null then.
+ * It launches nothing, but what has an entry a sequence is written as ever: the commit's outputs
+ * that are not its inputs, the verification's counts and tokens. */
 #define M2_TREE_NODES 64
 
 /* Causal depthwise conv over the trees, with bias (or NULL) and optional SiLU: a node's

@@ -110,11 +110,15 @@ int mamba2_tree_commit(const float* h, const uint16_t* conv_state, const int32_t
   const int32_t C = H * P + 2 * G * N;
   if (!h || !conv_state || !conv_pos || !h_out || !conv_state_out || !conv_pos_out || !A_log || !dt_bias || !count)
     return M2_ERR_ARG;
-  if (cu_nodes[nseq] > 0 && (!xbc || !u || !dt_raw || !path)) return M2_ERR_ARG;
-  if (ld_xbc < C || ld_u < C || ld_u % 4 || ld_dt < H) return M2_ERR_ARG;
   if (!al16(h) || !al16(h_out) || !al2(conv_state) || !al2(conv_state_out) || !al4(conv_pos) || !al4(conv_pos_out) ||
-      !al8(u + (size_t)H * P) || !al2(xbc) || !al2(dt_raw) || !al4(A_log) || !al4(dt_bias) || !al4(count) || !al4(path))
+      !al4(A_log) || !al4(dt_bias) || !al4(count))
     return M2_ERR_ALIGN;
+  if (cu_nodes[nseq] > 0) {  // else the arrays by node may be missing
+    if (!xbc || !u || !dt_raw || !path || ld_xbc < C || ld_u < C || ld_u % 4 || ld_dt < H) return M2_ERR_ARG;
+    if (!al8(u + (size_t)H * P) || !al2(xbc) || !al2(dt_raw) || !al4(path)) return M2_ERR_ALIGN;
+  } else if (h_out == h && conv_state_out == conv_state && conv_pos_out == conv_pos) {
+    return M2_OK;
+  }
   TreeCommitArgs a;
   a.A_log = A_log;
   a.dt_bias = dt_bias;
@@ -153,12 +157,14 @@ int m2_verify_tree(const void* p, int64_t ld_p, const void* q, int64_t ld_q, int
   if (V <= 0 || V > (1 << 30)) return M2_ERR_ARG;
   if ((st = check_nodes(cu_nodes, nseq))) return st;
   if (!u_next || !count || !next_token) return M2_ERR_ARG;
-  if (cu_nodes[nseq] > 0 && (!p || !parent || !token || !u || !path)) return M2_ERR_ARG;
-  if (ld_p < V || (q && ld_q < V)) return M2_ERR_ARG;
-  const uintptr_t es = fmt == M2_PROB_BF16 ? 1 : 3;
-  if ((reinterpret_cast<uintptr_t>(p) & es) || (reinterpret_cast<uintptr_t>(q) & es) || !al4(parent) || !al4(token) ||
-      !al4(u) || !al4(u_next) || !al4(path) || !al4(count) || !al4(next_token))
-    return M2_ERR_ALIGN;
+  if (!al4(u_next) || !al4(count) || !al4(next_token)) return M2_ERR_ALIGN;
+  if (cu_nodes[nseq] > 0) {  // else the arrays by node may be missing
+    if (!p || !parent || !token || !u || !path || ld_p < V || (q && ld_q < V)) return M2_ERR_ARG;
+    const uintptr_t es = fmt == M2_PROB_BF16 ? 1 : 3;
+    if ((reinterpret_cast<uintptr_t>(p) & es) || (reinterpret_cast<uintptr_t>(q) & es) || !al4(parent) || !al4(token) ||
+        !al4(u) || !al4(path))
+      return M2_ERR_ALIGN;
+  }
   VerifyArgs a;
   a.ld_p = ld_p;
   a.ld_q = ld_q;

@@ -148,3 +148,28 @@ def test_verify_remainders_next_to_zero():
             for un in (0.0, 0.1, 0.25, 0.9):
                 got = same_as_reference(pr, qr, [0, 4], [[-1, 0, 0, 0]], [0, 2, 2, 1], u, floats(un))
                 assert (got[1] == [2]) == (off < 0)
+
+
+# ------------------------------------------------------------------ calls without nodes
+
+@pytest.mark.parametrize("P", [64, 3])
+def test_commit_without_nodes(P):
+    """No array by node: outputs apart are written whole, what is in place stays."""
+    H, N, G, K, B = 1, 16, 1, 4, 3
+    s = Ssm(B, 1, H, P, N, G, 1)
+    ring, pos = rows(B * (K - 1), s.W, gen(2)).view(B, K - 1, s.W), ints([5, 6, 7])
+    count = ints([0] * B)
+    before = s.h.clone(), ring.clone(), pos.clone()
+    out = torch.full_like(s.h, 7.0), torch.full_like(ring, 7.0), torch.full_like(pos, 7)
+    for o in (out, (s.h, ring, pos)):
+        launches = abi.m2_launch_count()
+        abi.mamba2_tree_commit(s.h, ring, pos, *o, None, 0, None, 0, None, 0, s.A_log, s.dt_bias, [0] * (B + 1), None, count,
+                               H, P, N, G, K)
+        assert all(torch.equal(a, b) for a, b in zip(o, before))
+        assert (abi.m2_launch_count() == launches) == (o[0] is s.h)
+
+
+def test_verify_without_nodes():
+    count, last = ints([7] * 3), ints([7] * 3)
+    abi.m2_verify_tree(None, 0, None, 0, abi.M2_PROB_F32, 100, [0] * 4, None, None, None, floats(0.1, 0.2, 0.3), None, count, last)
+    assert count.tolist() == [0] * 3 and last.tolist() == [-1] * 3

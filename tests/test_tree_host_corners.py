@@ -76,3 +76,17 @@ def test_a_layer_workspace_for_more_nodes_serves_fewer():
             cu = [0] + [n * (i + 1) // 128 for i in range(128)]
             st = abi.mamba2_layer_tree(d, _layer(), None, cu, FAKE, FAKE, FAKE, FAKE, FAKE, size, check=False)
             assert st == M, (most, n)
+
+
+def test_arrays_by_sequence_are_checked_without_nodes():
+    from tests.test_tree_host import COMMIT, FAKE, VERIFY
+    for fn, base, by_seq in ((abi.mamba2_tree_commit, COMMIT, ("h", "conv_state", "conv_pos", "h_out", "conv_state_out",
+                                                               "conv_pos_out", "A_log", "dt_bias", "count")),
+                             (abi.m2_verify_tree, VERIFY, ("u_next", "count", "next_token"))):
+        for name in by_seq:
+            assert fn(**dict(base, cu_nodes=[0, 0, 0], **{name: None}), check=False) == abi.M2_ERR_ARG
+            assert fn(**dict(base, cu_nodes=[0, 0, 0], **{name: FAKE + 1}), check=False) == abi.M2_ERR_ALIGN
+    n = abi.m2_launch_count()
+    none = dict(xbc=None, ld_xbc=0, u=None, ld_u=0, dt_raw=None, ld_dt=0, path=None, H=1, P=3, N=16, G=1)
+    assert abi.mamba2_tree_commit(**dict(COMMIT, cu_nodes=[0, 0, 0], **none), check=False) == abi.M2_OK  # all in place
+    assert abi.m2_launch_count() == n
