@@ -234,6 +234,8 @@ class DeviceAttention:
         self._check("DeviceAttention.tree", T, x, out, row_pos, cache, b)
         if "tree_ws" not in b:
             raise abi.M2Error("DeviceAttention.tree", abi.M2_ERR_WORKSPACE)
+        if T == 0:
+            return
         s = stream if stream is not None else torch.cuda.current_stream()
         H, Hkv, D = self.H, self.Hkv, self.D
         q, k, v = self._project(x, b, row_pos, s)

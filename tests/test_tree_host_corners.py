@@ -90,3 +90,18 @@ def test_arrays_by_sequence_are_checked_without_nodes():
     none = dict(xbc=None, ld_xbc=0, u=None, ld_u=0, dt_raw=None, ld_dt=0, path=None, H=1, P=3, N=16, G=1)
     assert abi.mamba2_tree_commit(**dict(COMMIT, cu_nodes=[0, 0, 0], **none), check=False) == abi.M2_OK  # all in place
     assert abi.m2_launch_count() == n
+
+
+def test_passes_without_nodes():
+    """No mock: nothing is launched, and nothing is refused."""
+    m, cache = mixer()
+    dl, st, ws = layer()
+    none = torch.empty(0, dtype=torch.int32)
+    x = torch.empty(0, m.hidden, dtype=torch.bfloat16)
+    n = abi.m2_launch_count()
+    m.tree(x, [0, 0, 0], none, none, cache, 1, m.buffers(8, 0, 2, trees=True), torch.empty_like(x), Stream())
+    dl.tree(torch.empty(0, 256, dtype=torch.int16), [0, 0, 0], none, st, ws, Stream())
+    dl.tree_commit([0, 0, 0], none, ints(0, 0), st, ws, Stream())
+    assert abi.m2_launch_count() == n
+    with pytest.raises(abi.M2Error):
+        m.tree(x, [0, 0], none, none, cache, 1, m.buffers(8, 0, 2, trees=True), torch.empty_like(x), Stream())
