@@ -466,6 +466,8 @@ int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_
  * window is its own row, its ancestors', then the ring from the newest token back
  * (conv1d_update's arithmetic).  Ring and position are only read.
  *   x [T][C] rows ld_x apart, out [T][C] rows ld_o apart, w [C][d_conv], 2 <= d_conv <= 8.
+ *   out shares no element with x (other columns of its rows are fine): a node reads its
+ *   ancestors' rows.
  * Any alignment serves; 16-byte aligned pointers and strides with C % 8 == 0 are faster. */
 int mamba2_tree_conv(const uint16_t* conv_state, const int32_t* conv_pos, const uint16_t* x, int32_t ld_x,
                      const uint16_t* w, const uint16_t* bias, uint16_t* out, int32_t ld_o, int32_t nseq,

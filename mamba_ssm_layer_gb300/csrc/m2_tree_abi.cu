@@ -13,6 +13,13 @@ namespace m2 {
 static inline bool al8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 static inline bool al2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
+// Whether T rows of `width` elements at a and at b share any, both `ld` apart (b may be other columns of a's buffer).
+static bool rows_overlap(const uint16_t* a, const uint16_t* b, int32_t ld, int32_t width, int32_t T) {
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) / 2;
+  const int64_t m = (d % ld + ld) % ld, far = d < 0 ? -d : d;
+  return far < (int64_t)(T - 1) * ld + width && (m < width || m > ld - width);
+}
+
 static int check_ssm(int32_t H, int32_t P, int32_t N, int32_t G) {
   if (H <= 0 || P <= 0 || N <= 0 || G <= 0 || H % G) return M2_ERR_ARG;
   if (!(N == 16 || N == 32 || N == 64 || N == 128) || P > 256) return M2_ERR_UNSUPPORTED;
@@ -38,6 +45,7 @@ int mamba2_tree_conv(const uint16_t* conv_state, const int32_t* conv_pos, const 
   if (!conv_state || !conv_pos || !x || !w || !out || !parent || ld_x < C || ld_o < C) return M2_ERR_ARG;
   if (!al4(conv_pos) || !al4(parent) || !al2(conv_state) || !al2(x) || !al2(w) || !al2(bias) || !al2(out))
     return M2_ERR_ALIGN;
+  if (ld_x == ld_o && rows_overlap(x, out, ld_x, C, cu_nodes[nseq])) return M2_ERR_ARG;  // nodes read others' rows
   TreeConvArgs a;
   a.w = w;
   a.bias = bias;

@@ -173,3 +173,19 @@ def test_verify_without_nodes():
     count, last = ints([7] * 3), ints([7] * 3)
     abi.m2_verify_tree(None, 0, None, 0, abi.M2_PROB_F32, 100, [0] * 4, None, None, None, floats(0.1, 0.2, 0.3), None, count, last)
     assert count.tolist() == [0] * 3 and last.tolist() == [-1] * 3
+
+
+# ------------------------------------------------------------------ conv: outputs beside its inputs
+
+def test_conv_into_other_columns_of_its_rows():
+    g, C, K, n = gen(4), 64, 4, 9
+    ring, w, b = rows(3, C, g).view(1, 3, C), rows(C, K, g), rows(1, C, g)[0]
+    parent = ints(ref.random_parents(n, random.Random(2)))
+    for left in (True, False):
+        both = rows(n, 2 * C, g)
+        x, out = (both[:, :C], both[:, C:]) if left else (both[:, C:], both[:, :C])
+        before = x.clone()
+        apart = torch.empty(n, C, dtype=x.dtype, device="cuda")
+        abi.mamba2_tree_conv(ring, ints([5]), x, 2 * C, w, b, apart, C, [0, n], parent, C, K)
+        abi.mamba2_tree_conv(ring, ints([5]), x, 2 * C, w, b, out, 2 * C, [0, n], parent, C, K)
+        assert torch.equal(out, apart) and torch.equal(x, before)

@@ -105,3 +105,14 @@ def test_passes_without_nodes():
     assert abi.m2_launch_count() == n
     with pytest.raises(abi.M2Error):
         m.tree(x, [0, 0], none, none, cache, 1, m.buffers(8, 0, 2, trees=True), torch.empty_like(x), Stream())
+
+
+def test_conv_refuses_outputs_over_its_inputs():
+    """Nodes read their ancestors' rows, so that in place others would read outputs."""
+    from tests.test_tree_host import CONV, FAKE
+    n = abi.m2_launch_count()
+    for ld, C, T, off in ((640, 600, 8, 0), (640, 600, 8, 599), (640, 600, 8, 640), (640, 600, 8, -600), (640, 600, 8, 45),
+                          (640, 600, 8, 7 * 640 + 599), (600, 600, 1, 599), (640, 640, 8, -7 * 640)):
+        over = dict(CONV, x=FAKE + 20000, out=FAKE + 20000 + 2 * off, ld_x=ld, ld_o=ld, Cc=C, cu_nodes=[0, T])
+        assert abi.mamba2_tree_conv(**over, check=False) == abi.M2_ERR_ARG
+    assert abi.m2_launch_count() == n
