@@ -35,10 +35,6 @@ __device__ __forceinline__ int atr_len(const AttnTreeArgs& g, int b) {
 __device__ __forceinline__ int atr_tiles(const AtrArgs& a, int b, int rows) {
   return (atr_nodes(a.g, b) * a.G + rows - 1) / rows;
 }
-__device__ __forceinline__ int atr_units(const AtrArgs& a, int b, int rows) {
-  const int n = atr_len(a.g, b);
-  return (n + kPage - 1) / kPage * a.g.c.Hkv * atr_tiles(a, b, rows);
-}
 
 // A position in the order of units.
 struct AtrCursor {

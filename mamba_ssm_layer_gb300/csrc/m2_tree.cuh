@@ -9,19 +9,6 @@
 
 namespace m2 {
 
-// Row t of the launch's nodes belongs to the last sequence i with cu[i] <= t.
-__device__ __forceinline__ int tree_seq(const TreeArgs& t, int row) {
-  int lo = 0, hi = t.nseq;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) / 2;
-    if (t.cu[m] <= row)
-      lo = m;
-    else
-      hi = m;
-  }
-  return lo;
-}
-
 // The tree of one sequence in a warp: lane l gets the masks of nodes l and l + 32,
 // bit j = node j is the node itself or stands above it; 0 for a node that is not
 // part of the tree.  A parent's index is below its child's, so the bits of a mask
