@@ -453,8 +453,8 @@ int m2_attn_decode_kv4(const m2_kv4_cache* cache, const uint16_t* q, int32_t ld_
  *             the tree: its outputs are zeros, and no other node sees it.
  *   path      device int32 [cu_nodes[nseq]], count device int32 [nseq]: count[i] nodes,
  *             from the first on, each an entry below its sequence's number of nodes.
- *             Entries that are not, and counts outside 0 .. nodes, are left out and
- *             reported by m2_device_status (M2_ERR_ARG).
+ *             Entries that are not are left out, counts outside 0 .. nodes taken as the
+ *             nearer end, and both reported by m2_device_status (M2_ERR_ARG).
  * Topology, paths and counts are read on the device: a captured pass serves for every
  * tree of its size.  What nodes beside a node's path hold does not reach it, NaN and
  * infinities included.  A call without nodes succeeds, and the arrays by node may be null then.
@@ -599,7 +599,8 @@ int m2_workspace_map(const m2_dims* dims, int32_t kind, int32_t n, const int32_t
 
 /* Device status word: M2_OK, or the first failure a kernel recorded on the
  * current device (M2_ERR_TIMEOUT; M2_ERR_ARG for a page index or length that the
- * 4-bit cache's kernels, or a path's entry or count that the tree kernels, left out).  Synchronises the device.  clear != 0 resets it. */
+ * 4-bit cache's kernels left out, or a path's entry or count that the tree kernels did).
+ * Synchronises the device.  clear != 0 resets it. */
 int m2_device_status(int clear);
 
 /* Limit of the library's in-kernel pipeline waits on the current device, in

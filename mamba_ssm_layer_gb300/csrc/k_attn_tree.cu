@@ -15,9 +15,10 @@
 // shifted to a page's tokens it says what the row sees there.  Rows that a warp, then a
 // CTA, holds only in part are joined: warps through shared memory, CTAs by
 // attn_tree_combine.
-// Bound: issue slots (a page takes a warp 6400 cycles, 12 warps an SM; 1000 more pass between
-// pages), the start until the first page (5 us) and the joining (5 us): 64 chains of 4 over
-// 64 to 4096 tokens 62 us (155 MB, 2.5 TB/s).
+// Bound: latency.  A page takes a warp 6400 cycles, its half pages' scores, softmax and products
+// one after the other, and 1000 more pass between pages; with three warps a scheduler nothing is
+// full (issue slots 44 %, DRAM 34 %, tensor 27 %).  The start until the first page takes 5 us,
+// the joining 5: 64 chains of 4 over 64 to 4096 tokens 62 us (155 MB, 2.5 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -878,6 +879,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs& a, cudaStream_t s) {
   // 4096 tokens, 14.4 / 15.8 for one of 2000; a second tile of 16 rows would work through
   // every page again.  8 rows by the kernel for 8 / for 16: 46.8 / 56.5 us for the 64, 21.7 /
   // 24.2 for one of 30000; 5 rows of 16 kv heads of 64: 55.4 / 61.8.
+  // The launch's largest tree decides for all: 63 chains of 4 and one of 5 take 100 us, 64 of 4 61.
   const int rows = a.most * (a.H / a.c.Hkv);
   if (rows > 16) return launch_attn_tree_tc(a, s);
   if (rows > 8) return a.c.D == 128 ? launch_atr<128, 16>(a, s) : launch_atr<64, 16>(a, s);

@@ -20,9 +20,10 @@
 // row sees there.  Values that are not finite among the nodes' own tokens are kept out of
 // the products (0 * Inf) and make NaN of the rows that see them at the end.
 // Tiles cut between CTAs are joined by a second kernel.
-// Bound: converting pages where rows are few (a page takes 1400 cycles of the four warps, stmatrix
-// 300 of them), the softmax where they are many (a page of 256 rows 1900); a tile's start and output
-// some 11000.  16 trees of 9 to 16 nodes over 100 to 4000 tokens 36 us, two of 64 over
+// Bound: the pipeline's pace, a page every 1400 cycles where rows are few (not the four converting
+// warps' instructions alone, as six or eight of them are slower; each chain has one page's scores,
+// softmax and P V under way, one after the other) and every 1900 for 256 rows (softmax); a tile's
+// start and output some 11000.  16 trees of 9 to 16 nodes over 100 to 4000 tokens 36 us, two of 64 over
 // 30000 76 us (0.83 PFLOP/s), a chain of 5 over 700 13.5 us.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -20,8 +20,9 @@ namespace m2 {
 // a lane of the first warp looks up a node's rows for the CTA.
 // Sums run as the single-token conv's, oldest tap first; products of two bf16 values are
 // exact, so the results are the same bits.
-// Bound: latency (masks, rows: 2.6 us for a chain of 5, 10240 channels), then issue slots:
-// 16 trees of 16 nodes 7.1 us, of 64 nodes 20 us (42 MB).
+// Bound: latency (masks, rows: 2.6 us for a chain of 5, 10240 channels), also of the loads of
+// larger batches, in which a row comes from L2 once for each of its d_conv taps: 16 trees of 16
+// nodes 7.1 us (issue slots 40 %, DRAM 7 %), of 64 nodes 20 us (42 MB).
 constexpr int kTcThreads = 128, kTcMost = 16, kTcCtas = 5;
 
 // Two fused multiply-adds, each rounded as one.
@@ -207,9 +208,9 @@ cudaError_t launch_tree_conv(const TreeConvArgs& a, cudaStream_t s) {
 // are 0 in the product, and the nodes below them add them when they store.
 // Bound: HBM, the state read once (32 KB a head of 64 x 128), up to 16 nodes: 64 chains of
 // 5 take 57 us (4.9 TB/s), 16 trees of 16 19 us (of which 3 us pass until the first
-// product), one chain 3.5 us; the split and the products fill three quarters of the issue
-// slots meanwhile.  More nodes: issue slots and the legacy tensor rate (16 x 32 nodes 29 us,
-// 16 x 64 65 us).
+// product), one chain 3.5 us; over a whole launch of 16 trees the split and the products take 56 %
+// of the issue slots, HBM 42 %.  More nodes: warp MMA and what feeds it (16 x 32 nodes 29 us, 16 x
+// 64 65 us).
 //
 // A CTA takes some heads of one group of a sequence.  Warps of two kinds: products (8 for
 // the channels; 16 with 64 nodes, halves of the rows) and helpers, which make L and x of
@@ -696,6 +697,8 @@ template <int N>
 static cudaError_t launch_tree_ssm_m(const TreeSsmArgs& a, int most, cudaStream_t s) {
   // Rows for 16, 32 or 64 nodes.  us with 16 / 32 / 64, 128 heads as above: 16 sequences x 16
   // nodes 19.2 / 27.5 / 60, 64 x 5 56.8 / 85.5 / 215, one x 5 3.5 / 4.5 / 7.4; 16 x 32 - / 29.4 / 61.4.
+  // The launch's largest tree decides for all: conv and outputs of 63 x 5 and one x 64 take 232 us,
+  // of 64 x 5 66.
   return most <= 16   ? launch_tree_ssm_n<N, 1>(a, s)
          : most <= 32 ? launch_tree_ssm_n<N, 2>(a, s)
                       : launch_tree_ssm_n<N, 4>(a, s);

@@ -13,9 +13,10 @@
 // stored, whatever the number of refusals.
 // R and its sums are pairs of floats (about 2^-46 of the sum; fp64 adds are slow here),
 // comparisons fp64: a sum in fp32 would move one drawn token in some thousand.
-// Bound: HBM, the rows once, and the passes' hand-overs through the cluster: 64 sequences of
-// 5 to 8 nodes over 131072 words 29 us (67 MB, 2.3 TB/s; a pass over a row 4 to 6 us), a
-// chain of 5 over 32000 words 6.5 us.
+// Bound: latency, of the passes one after another and of a pass's loads (DRAM 23 %, issue slots
+// 28 %): 64 sequences of 5 to 8 nodes over 131072 words 28.4 us (67 MB, 2.4 TB/s; a pass over a
+// row 4 to 6 us), from bf16 rows 38, without draft rows 18; over 50256 words 16.3, over 50257
+// (rows of fp32 that are not 16-byte aligned) 21.6.  A chain of 5 over 32000 words 6.5 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
