@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(TsCfg<N, MT>::kWarps * 32, MT == 4 ? 1 : 2)
       dt = j < n ? fminf(fmaxf(dt, 1e-9f), 1e9f) : 0.0f;
       if (j < NODES) sdt[head * NODES + j] = dt;
       hi[k] = dt * A;
+      if (hi[k] < -0x1p100f) hi[k] = -0x1p100f;  // nothing is left of either; infinities would differ by NaN
       lo[k] = 0.0f;
     }
 #pragma unroll 1

@@ -189,3 +189,23 @@ def test_conv_into_other_columns_of_its_rows():
         abi.mamba2_tree_conv(ring, ints([5]), x, 2 * C, w, b, apart, C, [0, n], parent, C, K)
         abi.mamba2_tree_conv(ring, ints([5]), x, 2 * C, w, b, out, 2 * C, [0, n], parent, C, K)
         assert torch.equal(out, apart) and torch.equal(x, before)
+
+
+# ------------------------------------------------------------------ SSM outputs: decays without bound
+
+@pytest.mark.parametrize("n", [5, 30, 64])
+def test_ssm_decays_that_overflow(n):
+    """dt A below fp32's range: a step keeps nothing of what was before it, and its own term whole."""
+    parents = [ref.random_parents(n, random.Random(n), "forest")]
+    s = Ssm(1, n, 6, 16, 32, 2, 4, extra=4)
+    s.A_log[0], s.A_log[1], s.A_log[2], s.A_log[3] = 90.0, float("inf"), 75.0, -float("inf")
+    s.dt[1::3, 2] = float("inf")  # a step of 1e9
+    y = s.run([0, n], parents).view(n, 6, 16)
+    x, B, C = s.parts()
+    want, size = ref.ssm(s.h[0], x, B, C, s.dt, s.dt_bias, s.A_log, s.D, parents[0])
+    assert bool(want.isfinite().all()) and bool(y.isfinite().all())
+    decay = torch.log(ref.steps(s.dt, s.dt_bias, s.A_log)[1])  # of the paths, as far as any of it is left
+    path = ref.ancestors_sum(parents[0], decay).abs().clamp(max=200.0)[..., None]
+    assert bool(((y - want).abs() <= (2.0 ** -17 + path * 2.0 ** -21) * size + 1e-30).all())
+    s.A_log[4] = float("nan")
+    assert bool(s.run([0, n], parents).view(n, 6, 16)[:, 4].isnan().all())
